@@ -248,6 +248,64 @@ kda_status kda_packed_fused_decode(const kda_tensor* x, const kda_tensor* conv_w
                                    int32_t has_lower_bound, float lower_bound, float norm_eps,
                                    const kda_tensor* out, void* stream);
 
+/* ---- attention layers and beams around the recurrent ones ----------------
+ *
+ * A decoder that mixes KDA layers with softmax-attention layers needs, per
+ * new token: rotary positions and a paged key-value cache
+ * (kda_rope_append), attention over it (kda_paged_attention_decode), and for
+ * beam search the selection (kda_beam_select) and the copy of each surviving
+ * beam's recurrent state, conv cache and pages (kda_pool_move).
+ *
+ * Pages follow the slot convention above: page_table [N, P] int32 (column
+ * stride 1) lists the pages of each sequence in order; an entry <= 0 or >=
+ * num_pages is a null page (page 0 is reserved): nothing is written to it and
+ * its positions are not attended to.  k_pages and v_pages are [num_pages,
+ * page_size, Hkv, D], float32 or bfloat16, unit channel stride, any other
+ * positive strides that keep 4-element alignment, so a head-major page is a
+ * transposed view, and keys and values may interleave in one allocation.
+ */
+
+/*
+ * kda_rope_append: rotary positions of new tokens' q and k, and the write of
+ * their k and v into the pages.
+ *
+ *   q           [R, Hq, D], k, v [R, Hkv, D], float32 or bfloat16 (one dtype),
+ *               views into one packed row allowed; D a multiple of 4, <= 512.
+ *   phase_steps [rot/2, 2] int32 contiguous: the rotation of pair i as turns
+ *               per position in 64 fractional bits, low word first
+ *               (kda_rope_phase_steps).  rot = twice its length, a multiple of
+ *               8, <= D; channels past rot are copied; rot = 0 rotates nothing.
+ *   cu_seqlens  [N+1] int32: sequence n owns rows cu[n] .. cu[n+1]-1 (clamped
+ *               to [0, R)); NULL: row n is the one new token of sequence n.
+ *   seq_lens    [N] int32: each sequence's length INCLUDING its new rows; its
+ *               last row is at position seq_lens[n] - 1.
+ *   k_pages, v_pages (written), page_table: as above; positions past the
+ *               table's P * page_size are not written.  Two rows must not
+ *               share a position of a live page.
+ *   q_out       [R, Hq, D] of the pages' dtype (written); may be q itself.
+ *   interleaved = 0: pair i is channels (i, i + rot/2); 1: (2i, 2i + 1).
+ *   amplitude   factor on cosine and sine (1 unless a long-context scaling
+ *               asks for more).
+ * A pair (a, b) at position p turns by t = 2 pi frac(p * step):
+ * (a cos t - b sin t, a sin t + b cos t) * amplitude.  Rows outside every
+ * sequence and rows at a negative position give zero q_out and write nothing.
+ */
+kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_tensor* v, const kda_tensor* phase_steps,
+                           const kda_tensor* cu_seqlens, const kda_tensor* seq_lens, const kda_tensor* page_table,
+                           const kda_tensor* k_pages, const kda_tensor* v_pages, const kda_tensor* q_out,
+                           int32_t interleaved, float amplitude, void* stream);
+
+/*
+ * Rotation steps for kda_rope_append, computed on the host into steps[rot/2]:
+ * f_i = base^(-2i/rot) radians per position; with turns r_i = original_len *
+ * f_i / 2 pi over the original context and keep_i = clamp((r_i - low) / (high
+ * - low), 0, 1), the step is f_i (keep_i + (1 - keep_i) / factor): fast pairs
+ * keep their frequency, slow ones are stretched by `factor`.  original_len =
+ * 0 stretches all pairs alike (low and high unused); factor = 1 changes none.
+ */
+kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, double original_len, double low,
+                                double high, uint64_t* steps);
+
 /* ---- host-only queries (no CUDA calls) ---------------------------------- */
 
 /* Operation ids for kda_plan_split. */

@@ -10,10 +10,14 @@ The decode entry points of libkda, with the C names:
     kda_packed_fused_decode fused conv + KDA + RMSNorm over ragged speculative
                            rows, with per-token conv and state checkpoints
 
+and the operators that the attention layers and beams around them need:
+
+    kda_rope_append        rotary positions, keys and values into a paged cache
+
 Build the library with ``python -m linear_attention_decode_02_gb300.build``.
 """
 
 from .binding import (SCHED_AUTO, SCHED_SPLIT, SCHED_STREAM, KdaError, kda_device_error,  # noqa: F401
                       kda_fused_decode, kda_packed_decode, kda_packed_fused_decode, kda_plan_schedule, kda_plan_split,
-                      kda_recurrent_decode, kda_set_schedule_override, kda_set_split_override,
+                      kda_recurrent_decode, kda_rope_append, kda_rope_phase_steps, kda_set_schedule_override, kda_set_split_override,
                       kda_spec_decode, kda_spec_verify_decode, kda_version, library)

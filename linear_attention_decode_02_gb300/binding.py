@@ -33,6 +33,7 @@ DEFAULT_SCALE = 1.0 / math.sqrt(128.0)
 EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda_spec_decode",
            "kda_packed_fused_decode",
            "kda_spec_verify_decode",
+           "kda_rope_append", "kda_rope_phase_steps",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -54,7 +55,7 @@ class KdaTensor(ctypes.Structure):
 
 def _declare(lib):
     T = ctypes.POINTER(KdaTensor)
-    i32, f32, vp = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
+    i32, f32, f64, vp = ctypes.c_int32, ctypes.c_float, ctypes.c_double, ctypes.c_void_p
     sigs = {
         "kda_recurrent_decode": [T, T, T, T, T, T, T, T, T, T, i32, f32, f32, vp],
         "kda_packed_decode": [T, T, T, T, T, T, T, T, vp],
@@ -62,6 +63,8 @@ def _declare(lib):
         "kda_packed_fused_decode": [T, T, T, T, T, T, T, T, T, T, T, T, T, i32, f32, f32, T, vp],
         "kda_spec_decode": [T, T, T, T, T, i32, T, i32, T, T, T, f32, vp],
         "kda_spec_verify_decode": [T, T, T, T, T, i32, T, i32, T, T, T, T, T, f32, vp],
+        "kda_rope_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
+        "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -257,6 +260,31 @@ def kda_spec_verify_decode(q, k, v, g, beta, cu_seqlens, state_indices, state, t
                                         cc, kg, float(scale), _stream(q))
     _check(lib, st)
     return out
+
+
+def kda_rope_append(q, k, v, phase_steps, seq_lens, page_table, k_pages, v_pages, cu_seqlens=None,
+                    interleaved=False, amplitude=1.0, q_out=None):
+    """Rotates q and k, writes k and v into the pages in place, returns the rotated q in the pages' dtype."""
+    lib = library()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=k_pages.dtype, device=q.device)
+    with _on(q.device):
+        st = lib.kda_rope_append(_ref(q), _ref(k), _ref(v), _ref(phase_steps),
+                                 _ref(cu_seqlens) if cu_seqlens is not None else None, _ref(seq_lens),
+                                 _ref(page_table), _ref(k_pages), _ref(v_pages), _ref(q_out),
+                                 int(bool(interleaved)), float(amplitude), _stream(q))
+    _check(lib, st)
+    return q_out
+
+
+def kda_rope_phase_steps(rot_dim, base=10000.0, factor=1.0, original_len=0.0, low=1.0, high=32.0, device="cuda"):
+    """Rotation steps of kda_rope_append as an int32 tensor [rot_dim/2, 2] on `device`."""
+    lib = library()
+    steps = torch.empty((max(int(rot_dim), 0) // 2, 2), dtype=torch.int32)
+    st = lib.kda_rope_phase_steps(int(rot_dim), float(base), float(factor), float(original_len), float(low),
+                                  float(high), steps.data_ptr() or None)
+    _check(lib, st)
+    return steps.to(device)
 
 
 def kda_plan_split(op, units, state_dtype, t_max, sm_count):

@@ -1,0 +1,37 @@
+// Internal interface between the host side of the cache and beam entry points
+// (kda_cache_api.cu) and their kernels.  Plain structs of device pointers and
+// element strides, validated on the host before any launch.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// The pages of one KV cache tensor, [num_pages, page_size, Hkv, D] by strides.
+struct PageView {
+  void* data;
+  int64_t page, token, head;  // element strides
+};
+
+// Rotary positions of R token rows and the write of their keys and values.
+struct RopeArgs {
+  const void* q; const void* k; const void* v;
+  int64_t q_rs, q_hs, k_rs, k_hs, v_rs, v_hs;
+  const uint64_t* steps;       // [rot/2] turns per position, 64-bit fixed point (8-byte aligned)
+  const int32_t* cu;           // [N+1], or null: one row per sequence
+  const int32_t* lens;         // [N]
+  const int32_t* table; int64_t table_rs; int32_t table_cols;
+  PageView kp, vp;
+  int32_t num_pages, page_size;
+  void* q_out; int64_t o_rs, o_hs;
+  int32_t R, N, Hq, Hkv, D, rot;
+  int32_t interleaved;
+  float amplitude;
+  int32_t in_dtype, page_dtype;
+  int32_t vec;                 // elements per access: 8 (bf16 -> bf16, 16-byte aligned rows) or 4
+};
+
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
+
+}  // namespace kda

@@ -1,0 +1,214 @@
+// libkda C ABI: the paged KV cache, beam selection and slot copies around the
+// recurrent layers.  Contract checks on the host, then the launch; no device
+// reads, no allocation, no synchronisation.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kda_cache.h"
+#include "kda_host.h"
+#include "kda_launch.h"
+
+using namespace kda::host;
+
+namespace {
+
+// No byte is shared although the byte ranges cross: views that interleave
+// along one axis, as keys and values of one allocation do.  For a stride s of
+// `a` with every larger stride of both views a multiple of s, addresses modulo
+// s lie in [0, ea) and [r, r + eb), ea and eb the extents below that axis and
+// r the offset modulo s, which are disjoint where ea <= r and r + eb <= s.
+bool interleaved(const View& a, const View& b) {
+  const int64_t ba = esize(a.dtype), bb = esize(b.dtype);
+  for (int i = 0; i < a.ndim; ++i) {
+    if (a.shape[i] <= 1) continue;
+    const int64_t s = a.stride[i] * ba;
+    int64_t ext[2] = {0, 0};
+    bool nested = true;
+    for (int w = 0; w < 2; ++w) {
+      const View& v = w == 0 ? a : b;
+      const int64_t es = w == 0 ? ba : bb;
+      ext[w] = es;
+      for (int j = 0; j < v.ndim; ++j) {
+        if (v.shape[j] <= 1) continue;
+        const int64_t st = v.stride[j] * es;
+        if (st < s) ext[w] += (v.shape[j] - 1) * st;
+        else if (st % s != 0) nested = false;
+      }
+    }
+    if (!nested) continue;
+    const int64_t d = b.data - a.data;
+    const int64_t r = ((d % s) + s) % s;
+    if (ext[0] <= r && r + ext[1] <= s) return true;
+  }
+  return false;
+}
+
+kda_status no_shared_bytes(const View& w, std::initializer_list<const View*> others) {
+  for (const View* o : others)
+    KDA_CHECK(!overlap(w, *o) || interleaved(w, *o) || interleaved(*o, w), KDA_ERR_ALIAS, "%s overlaps %s", w.name,
+              o->name);
+  return KDA_OK;
+}
+
+bool same_view(const View& a, const View& b) {
+  if (a.data != b.data || a.dtype != b.dtype || a.ndim != b.ndim) return false;
+  for (int i = 0; i < a.ndim; ++i)
+    if (a.shape[i] != b.shape[i] || (a.shape[i] > 1 && a.stride[i] != b.stride[i])) return false;
+  return true;
+}
+
+// Every vector of the last axis starts on a `bytes` boundary.
+bool vectors_aligned(const View& v, int64_t bytes) {
+  if (reinterpret_cast<uintptr_t>(v.data) % bytes != 0) return false;
+  for (int i = 0; i < v.ndim - 1; ++i)
+    if (v.shape[i] > 1 && (v.stride[i] * esize(v.dtype)) % bytes != 0) return false;
+  return true;
+}
+
+// Key and value pages [num_pages, page_size, Hkv, D] of one dtype and shape.
+kda_status need_pages(const View& K, const View& V, int64_t Hkv, int64_t D) {
+  KDA_TRY(need_dtype(K, KDA_F32, KDA_BF16));
+  KDA_CHECK(V.dtype == K.dtype, KDA_ERR_INVALID_ARG, "v_pages: dtype must match k_pages");
+  for (const View* p : {&K, &V}) {
+    KDA_CHECK(p->shape[0] >= 1 && p->shape[0] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: num_pages %lld out of range",
+              p->name, (long long)p->shape[0]);
+    KDA_CHECK(p->shape[1] >= 1 && p->shape[1] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: page size %lld out of range",
+              p->name, (long long)p->shape[1]);
+    KDA_TRY(need_shape(*p, 0, K.shape[0]));
+    KDA_TRY(need_shape(*p, 1, K.shape[1]));
+    KDA_TRY(need_shape(*p, 2, Hkv));
+    KDA_TRY(need_shape(*p, 3, D));
+    KDA_TRY(need_vec_layout(*p));
+  }
+  return KDA_OK;
+}
+
+kda_status need_table(const View& T, int64_t N) {
+  KDA_TRY(need_dtype(T, KDA_I32));
+  KDA_TRY(need_shape(T, 0, N));
+  KDA_CHECK(T.shape[1] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: too many pages a sequence", T.name);
+  KDA_CHECK(T.shape[1] <= 1 || T.stride[1] == 1, KDA_ERR_INVALID_ARG, "%s: column stride must be 1", T.name);
+  return KDA_OK;
+}
+
+kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, double original_len, double low,
+                                double high, uint64_t* steps) {
+  KDA_CHECK(rot_dim >= 0 && rot_dim % 2 == 0 && rot_dim <= 512, KDA_ERR_INVALID_ARG,
+            "rot_dim %d must be even and in 0..512", rot_dim);
+  KDA_CHECK(std::isfinite(base) && base > 1.0, KDA_ERR_INVALID_ARG, "base must be finite and above 1");
+  KDA_CHECK(std::isfinite(factor) && factor >= 1.0, KDA_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  KDA_CHECK(std::isfinite(original_len) && original_len >= 0.0, KDA_ERR_INVALID_ARG,
+            "original_len must be finite and not negative");
+  KDA_CHECK(original_len == 0.0 || (std::isfinite(low) && std::isfinite(high) && low < high), KDA_ERR_INVALID_ARG,
+            "low must be below high");
+  KDA_CHECK(steps != nullptr || rot_dim == 0, KDA_ERR_INVALID_ARG, "steps: null pointer");
+  const double two_pi = 6.283185307179586;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double turns = std::pow(base, -2.0 * i / rot_dim) / two_pi;  // a position
+    double keep = 0.0;
+    if (original_len > 0.0) keep = std::min(1.0, std::max(0.0, (original_len * turns - low) / (high - low)));
+    const double scaled = turns * (keep + (1.0 - keep) / factor);
+    steps[i] = static_cast<uint64_t>(std::llround(std::ldexp(scaled, 64)));  // at most 2^64 / 2 pi
+  }
+  return KDA_OK;
+}
+
+kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_tensor* v, const kda_tensor* phase_steps,
+                           const kda_tensor* cu_seqlens, const kda_tensor* seq_lens, const kda_tensor* page_table,
+                           const kda_tensor* k_pages, const kda_tensor* v_pages, const kda_tensor* q_out,
+                           int32_t is_interleaved, float amplitude, void* stream) {
+  View Q, K, V, P, CU, L, T, KP, VP, O;
+  KDA_TRY(ranked_view(q, "q", 3, -1, &Q));
+  KDA_TRY(ranked_view(k, "k", 3, -1, &K));
+  KDA_TRY(ranked_view(v, "v", 3, -1, &V));
+  KDA_TRY(ranked_view(phase_steps, "phase_steps", 2, -1, &P));
+  if (cu_seqlens != nullptr) KDA_TRY(raw_view(cu_seqlens, "cu_seqlens", &CU));
+  KDA_TRY(raw_view(seq_lens, "seq_lens", &L));
+  KDA_TRY(ranked_view(page_table, "page_table", 2, -1, &T));
+  KDA_TRY(ranked_view(k_pages, "k_pages", 4, -1, &KP));
+  KDA_TRY(ranked_view(v_pages, "v_pages", 4, -1, &VP));
+  KDA_TRY(ranked_view(q_out, "q_out", 3, -1, &O));
+
+  const int64_t R = Q.shape[0], Hq = Q.shape[1], D = Q.shape[2], Hkv = K.shape[1];
+  KDA_TRY(need_dtype(Q, KDA_F32, KDA_BF16));
+  KDA_CHECK(R <= INT32_MAX, KDA_ERR_INVALID_ARG, "q: too many token rows");
+  KDA_CHECK(Hq >= 1 && Hkv >= 1, KDA_ERR_INVALID_ARG, "q, k: need at least one head");
+  KDA_CHECK((Hq + 2 * Hkv) * D <= (1 << 24), KDA_ERR_UNSUPPORTED, "q, k: too many heads");
+  KDA_CHECK(D >= 4 && D % 4 == 0 && D <= 512, KDA_ERR_UNSUPPORTED, "q: head dimension %lld must be a multiple of 4 in 4..512",
+            (long long)D);
+  for (View* t : {&K, &V}) {
+    KDA_CHECK(t->dtype == Q.dtype, KDA_ERR_INVALID_ARG, "%s: dtype must match q", t->name);
+    KDA_TRY(need_shape(*t, 0, R));
+    KDA_TRY(need_shape(*t, 1, Hkv));
+    KDA_TRY(need_shape(*t, 2, D));
+  }
+  for (View* t : {&Q, &K, &V}) KDA_TRY(need_vec_layout(*t));
+  KDA_TRY(need_dtype(P, KDA_I32));
+  KDA_TRY(need_shape(P, 1, 2));
+  KDA_TRY(need_contiguous(P));
+  const int64_t rot = 2 * P.shape[0];
+  KDA_CHECK(rot <= D && rot % 8 == 0, KDA_ERR_INVALID_ARG,
+            "phase_steps: %lld pairs; the rotated part must be a multiple of 8 and at most the head dimension",
+            (long long)P.shape[0]);
+  KDA_CHECK(reinterpret_cast<uintptr_t>(P.data) % 8 == 0, KDA_ERR_INVALID_ARG, "phase_steps: data must be 8-byte aligned");
+  KDA_CHECK(L.ndim == 1, KDA_ERR_INVALID_ARG, "seq_lens: expected rank 1");
+  const int64_t N = L.shape[0];
+  KDA_CHECK(N <= INT32_MAX - 1, KDA_ERR_INVALID_ARG, "seq_lens: too many sequences");
+  KDA_TRY(need_indices(L, N));
+  if (cu_seqlens != nullptr) {
+    KDA_TRY(need_indices(CU, N + 1));
+  } else {
+    KDA_CHECK(R == N, KDA_ERR_INVALID_ARG, "q: without cu_seqlens each of the %lld sequences has one row, not %lld",
+              (long long)N, (long long)R);
+  }
+  KDA_TRY(need_table(T, N));
+  KDA_TRY(need_pages(KP, VP, Hkv, D));
+  KDA_CHECK(O.dtype == KP.dtype, KDA_ERR_INVALID_ARG, "q_out: dtype must match the pages");
+  KDA_TRY(need_shape(O, 0, R));
+  KDA_TRY(need_shape(O, 1, Hq));
+  KDA_TRY(need_shape(O, 2, D));
+  KDA_TRY(need_vec_layout(O));
+  KDA_CHECK(is_interleaved == 0 || is_interleaved == 1, KDA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  KDA_CHECK(std::isfinite(amplitude), KDA_ERR_INVALID_ARG, "amplitude must be finite");
+  if (!same_view(O, Q)) KDA_TRY(no_shared_bytes(O, {&Q}));
+  KDA_TRY(no_shared_bytes(O, {&K, &V, &P, &CU, &L, &T, &KP, &VP}));
+  KDA_TRY(no_shared_bytes(KP, {&Q, &K, &V, &P, &CU, &L, &T, &VP}));
+  KDA_TRY(no_shared_bytes(VP, {&Q, &K, &V, &P, &CU, &L, &T}));
+  if (R == 0) return KDA_OK;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  KDA_TRY(current_device(st, &dev));
+  kda::RopeArgs a{};
+  a.q = Q.data; a.k = K.data; a.v = V.data;
+  a.q_rs = Q.stride[0]; a.q_hs = Q.stride[1];
+  a.k_rs = K.stride[0]; a.k_hs = K.stride[1];
+  a.v_rs = V.stride[0]; a.v_hs = V.stride[1];
+  a.steps = reinterpret_cast<const uint64_t*>(P.data);
+  a.cu = cu_seqlens != nullptr ? reinterpret_cast<const int32_t*>(CU.data) : nullptr;
+  a.lens = reinterpret_cast<const int32_t*>(L.data);
+  a.table = reinterpret_cast<const int32_t*>(T.data); a.table_rs = T.stride[0]; a.table_cols = (int32_t)T.shape[1];
+  a.kp = page_view(KP); a.vp = page_view(VP);
+  a.num_pages = (int32_t)KP.shape[0]; a.page_size = (int32_t)KP.shape[1];
+  a.q_out = O.data; a.o_rs = O.stride[0]; a.o_hs = O.stride[1];
+  a.R = (int32_t)R; a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.rot = (int32_t)rot;
+  a.interleaved = is_interleaved; a.amplitude = amplitude;
+  a.in_dtype = Q.dtype; a.page_dtype = KP.dtype;
+  a.vec = 4;
+  if (Q.dtype == KDA_BF16 && KP.dtype == KDA_BF16 && D % 8 == 0 && (is_interleaved || rot % 16 == 0)) {
+    bool wide = true;
+    for (const View* t : {&Q, &K, &V, &KP, &VP, &O}) wide = wide && vectors_aligned(*t, 16);
+    if (wide) a.vec = 8;
+  }
+  return check_launch(kda::launch_rope_append(a, st));
+}
+
+}  // extern "C"

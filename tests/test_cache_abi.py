@@ -1,0 +1,133 @@
+"""Contract checks of the cache and beam entry points (CPU only: descriptors of
+host memory, and only calls that are refused before any launch)."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_decode_02_gb300 import binding, build
+from linear_attention_decode_02_gb300.binding import desc
+from oracle import cache_oracle as co
+
+INVALID, UNSUPPORTED, ALIAS, CUDA = 1, 2, 3, 4
+NO_GPU = not torch.cuda.is_available()
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.library()
+
+
+def _ptr(t):
+    return None if t is None else ctypes.byref(desc(t))
+
+
+def _msg(lib):
+    return lib.kda_last_error_message().decode()
+
+
+# ---- kda_rope_append ------------------------------------------------------------------
+
+
+def _rope(R=3, Hq=4, Hkv=2, D=64, N=3, P=5, page=8):
+    return dict(q=torch.zeros(R, Hq, D, dtype=BF16), k=torch.zeros(R, Hkv, D, dtype=BF16),
+                v=torch.zeros(R, Hkv, D, dtype=BF16), steps=torch.zeros(D // 2, 2, dtype=torch.int32), cu=None,
+                lens=torch.ones(N, dtype=torch.int32), table=torch.zeros(N, P, dtype=torch.int32),
+                k_pages=torch.zeros(4, page, Hkv, D, dtype=BF16), v_pages=torch.zeros(4, page, Hkv, D, dtype=BF16),
+                q_out=torch.zeros(R, Hq, D, dtype=BF16))
+
+
+def _call_rope(lib, t, interleaved=0, amplitude=1.0):
+    return lib.kda_rope_append(*[_ptr(t[n]) for n in ("q", "k", "v", "steps", "cu", "lens", "table", "k_pages",
+                                                      "v_pages", "q_out")], interleaved, amplitude, None)
+
+
+@pytest.mark.skipif(not NO_GPU, reason="a valid call would launch on host memory")
+def test_rope_valid_calls_reach_the_device_query(lib):
+    t = _rope()
+    assert _call_rope(lib, t) in (UNSUPPORTED, CUDA), _msg(lib)
+    t["q_out"] = t["q"]  # in place
+    assert _call_rope(lib, t) in (UNSUPPORTED, CUDA), _msg(lib)
+    t = _rope()
+    x = torch.zeros(3, 8 * 64, dtype=BF16)  # in place inside a packed row
+    t.update(q=x[:, :256].view(3, 4, 64), k=x[:, 256:384].view(3, 2, 64), v=x[:, 384:].view(3, 2, 64))
+    t["q_out"] = t["q"]
+    assert _call_rope(lib, t) in (UNSUPPORTED, CUDA), _msg(lib)
+    for axis in (0, 1, 2, 3):  # keys and values interleaved along any axis of one allocation
+        shape = [4, 8, 2, 64]
+        shape.insert(axis, 2)
+        kv = torch.zeros(*shape, dtype=BF16)
+        t.update(k_pages=kv.select(axis, 0), v_pages=kv.select(axis, 1))
+        assert _call_rope(lib, t) in (UNSUPPORTED, CUDA), (axis, _msg(lib))
+    t = _rope()
+    t.update(cu=torch.zeros(4, dtype=torch.int32), steps=torch.zeros(0, 2, dtype=torch.int32))
+    assert _call_rope(lib, t) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_rope(lib, {**_rope(R=0, N=0)}) == 0
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (lambda t: t.update(k=torch.zeros(3, 2, 64)), INVALID, "k: dtype must match q"),
+    (lambda t: t.update(v=torch.zeros(3, 1, 64, dtype=BF16)), INVALID, "v: axis 1"),
+    (lambda t: t.update(steps=torch.zeros(36, 2, dtype=torch.int32)), INVALID, "phase_steps: 36 pairs"),
+    (lambda t: t.update(steps=torch.zeros(6, 2, dtype=torch.int32)), INVALID, "multiple of 8"),
+    (lambda t: t.update(steps=torch.zeros(32, 3, dtype=torch.int32)), INVALID, "phase_steps: axis 1"),
+    (lambda t: t.update(lens=torch.ones(2, dtype=torch.int32)), INVALID, "without cu_seqlens"),
+    (lambda t: t.update(cu=torch.zeros(3, dtype=torch.int32)), INVALID, "cu_seqlens: axis 0"),
+    (lambda t: t.update(lens=torch.ones(3)), INVALID, "seq_lens: dtype"),
+    (lambda t: t.update(table=torch.zeros(2, 5, dtype=torch.int32)), INVALID, "page_table: axis 0"),
+    (lambda t: t.update(table=torch.zeros(5, 3, dtype=torch.int32).t()), INVALID, "column stride"),
+    (lambda t: t.update(v_pages=torch.zeros(4, 8, 2, 64)), INVALID, "v_pages: dtype must match"),
+    (lambda t: t.update(v_pages=torch.zeros(5, 8, 2, 64, dtype=BF16)), INVALID, "v_pages: axis 0"),
+    (lambda t: t.update(k_pages=torch.zeros(4, 8, 3, 64, dtype=BF16)), INVALID, "k_pages: axis 2"),
+    (lambda t: t.update(k_pages=torch.zeros(4, 8, 2, 66, dtype=BF16)[..., 2:]), INVALID, "multiple of 4"),
+    (lambda t: t.update(q_out=torch.zeros(3, 4, 64)), INVALID, "q_out: dtype must match the pages"),
+    (lambda t: t.update(q=torch.zeros(3, 4, 62, dtype=BF16)), UNSUPPORTED, "head dimension"),
+    (lambda t: t.update(q_out=t["k_pages"].view(-1)[:768].view(3, 4, 64)), ALIAS, "q_out overlaps"),
+    (lambda t: t.update(v_pages=t["k_pages"]), ALIAS, "k_pages overlaps v_pages"),
+    (lambda t: t.update(q_out=t["q"].transpose(0, 1)[:3].contiguous().transpose(0, 1)[:, :3]), INVALID, "q_out: axis 1"),
+    (lambda t: t.update(k=None), INVALID, "k: null"),
+])
+def test_rope_refusals(lib, change, status, text):
+    t = _rope()
+    change(t)
+    assert _call_rope(lib, t) == status, _msg(lib)
+    assert text in _msg(lib)
+
+
+def test_rope_refuses_shifted_in_place_and_bad_scalars(lib):
+    t = _rope()
+    x = torch.zeros(4 * 3 * 64 + 64, dtype=BF16)
+    t.update(q=x[:768].view(3, 4, 64), q_out=x[64:832].view(3, 4, 64))
+    assert _call_rope(lib, t) == ALIAS
+    assert _call_rope(lib, _rope(), interleaved=2) == INVALID
+    assert _call_rope(lib, _rope(), amplitude=float("nan")) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(factor=8.0, original_len=8192.0, low=1.0, high=4.0),
+                                dict(factor=4.0), dict(base=500000.0, factor=32.0, original_len=4096.0)])
+def test_phase_steps_are_the_frequencies_in_64_bit_turns(lib, kw):
+    for rot in (0, 2, 64, 128, 512):
+        steps = binding.kda_rope_phase_steps(rot, device="cpu", **kw)
+        assert steps.shape == (rot // 2, 2) and steps.dtype == torch.int32
+        got = steps.numpy().astype(np.int32).view(np.uint32).astype(np.uint64)
+        turns = (got[:, 1] * np.uint64(2 ** 32) + got[:, 0]).astype(np.float64) / 2.0 ** 64
+        ref = co.rope_frequencies(rot, **kw) / (2 * np.pi)
+        # The steps are multiples of 2^-64: off by 2^-65 for that.  In float64 on both sides, the exponent's rounding
+        # (2^-53) times ln(base) <= 13.2 and pow's own put f within 2^-49; keep moves by at most high / (high - low)
+        # of that, and the sum it enters is at least 1 / factor >= 1/32 of the whole: below 2^-49 * 2 * 32 = 2^-43.
+        assert np.all(np.abs(turns - ref) <= 2.0 ** -43 * ref + 2.0 ** -64)
+
+
+@pytest.mark.parametrize("args,text", [
+    (dict(rot_dim=7), "rot_dim"), (dict(rot_dim=-2), "rot_dim"), (dict(rot_dim=514), "rot_dim"),
+    (dict(rot_dim=8, base=1.0), "base"), (dict(rot_dim=8, base=float("inf")), "base"),
+    (dict(rot_dim=8, factor=0.5), "factor"), (dict(rot_dim=8, original_len=-1.0), "original_len"),
+    (dict(rot_dim=8, original_len=4096.0, low=4.0, high=4.0), "low"),
+])
+def test_phase_step_refusals(lib, args, text):
+    with pytest.raises(binding.KdaError, match=text):
+        binding.kda_rope_phase_steps(device="cpu", **args)
