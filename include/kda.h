@@ -38,7 +38,8 @@
  *   stream) of the calling thread's current device, which must be a
  *   compute-capability 10.3 (GB300) device.  An unsupported device returns
  *   KDA_ERR_UNSUPPORTED; there is no fallback path.
- * - Every call launches exactly one kernel.  Any contract breach (dtype,
+ * - Every call launches exactly one kernel unless its comment says otherwise.
+ *   Any contract breach (dtype,
  *   rank, shape, stride, alignment, aliasing) is detected on the host and
  *   returned as a status WITHOUT launching anything; kda_last_error_message()
  *   then describes it.  A launch failure returns KDA_ERR_CUDA.
@@ -305,6 +306,30 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
  */
 kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, double original_len, double low,
                                 double high, uint64_t* steps);
+
+/*
+ * kda_pool_move: copies whole slots inside pools, in place; forks, compacts,
+ * clears and, by parent beam, reorders recurrent states, conv caches and
+ * pages alike.
+ *
+ *   pools       n_pools (1..256) descriptors, rank 1..4, any dtype: axis 0 is
+ *               the slot (the same number of slots in every pool), the other
+ *               axes dense in any order (a conv cache's [slot_stride, 1, 3*H*128]
+ *               and a head-major page are), slot stride as large or larger.
+ *   src_slots, dst_slots  [N, K] int32, column stride 1, K <= 32.
+ *   parents     [N, K] int32, column stride 1, or NULL (parent j = j).
+ * In every pool, for every row n and all its j at once: slot dst[n, j] takes
+ * what slot src[n, parents[n, j]] held before the call.  A parent outside
+ * [0, K), or a destination outside [1, num_slots), moves nothing; a source
+ * outside [1, num_slots) clears the destination to zero bytes; a slot that is
+ * its own source is not touched.
+ * Rows are independent and unordered: a live destination may appear once in
+ * the call, and may be a source only in its own row (as the null slots, a
+ * caller contract the library does not check).  Sources may repeat.
+ * Launches one kernel per 64 pools.
+ */
+kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const kda_tensor* src_slots,
+                         const kda_tensor* dst_slots, const kda_tensor* parents, void* stream);
 
 /* ---- host-only queries (no CUDA calls) ---------------------------------- */
 

@@ -33,7 +33,7 @@ DEFAULT_SCALE = 1.0 / math.sqrt(128.0)
 EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda_spec_decode",
            "kda_packed_fused_decode",
            "kda_spec_verify_decode",
-           "kda_rope_append", "kda_rope_phase_steps",
+           "kda_rope_append", "kda_rope_phase_steps", "kda_pool_move",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -64,6 +64,7 @@ def _declare(lib):
         "kda_spec_decode": [T, T, T, T, T, i32, T, i32, T, T, T, f32, vp],
         "kda_spec_verify_decode": [T, T, T, T, T, i32, T, i32, T, T, T, T, T, f32, vp],
         "kda_rope_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
+        "kda_pool_move": [ctypes.POINTER(T), i32, T, T, T, vp],
         "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
     }
     for name, args in sigs.items():
@@ -285,6 +286,25 @@ def kda_rope_phase_steps(rot_dim, base=10000.0, factor=1.0, original_len=0.0, lo
                                   float(high), steps.data_ptr() or None)
     _check(lib, st)
     return steps.to(device)
+
+
+def kda_pool_move(pools, src_slots, dst_slots, parents=None):
+    """Copies slots of every tensor of `pools` in place; returns None."""
+    lib = library()
+    dev = src_slots.device
+    with _on(dev):
+        st = lib.kda_pool_move(_pool_array(pools), len(pools), _ref(src_slots), _ref(dst_slots),
+                               _ref(parents) if parents is not None else None, _stream(src_slots))
+    _check(lib, st)
+
+
+def _pool_array(pools):
+    """Array of descriptor pointers; the descriptors stay referenced by the array's keep list."""
+    array = (ctypes.POINTER(KdaTensor) * max(1, len(pools)))()
+    array._keep = [desc(p) for p in pools]
+    for i, d in enumerate(array._keep):
+        array[i] = ctypes.pointer(d)
+    return array
 
 
 def kda_plan_split(op, units, state_dtype, t_max, sm_count):

@@ -34,4 +34,24 @@ struct RopeArgs {
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
 
+// Copies of slots within each of up to kMovePools pools, byte by byte.
+constexpr int kMovePools = 64;
+constexpr int kMoveBeams = 32;
+struct MovePool {
+  char* base;
+  int64_t stride, bytes;     // slot stride and slot size
+  int64_t first;             // first block of this pool (set by the launcher)
+};
+struct MoveArgs {
+  const int32_t* src; const int32_t* dst; const int32_t* parents;  // [N, K]; parents may be null
+  int64_t src_rs, dst_rs, par_rs;
+  int32_t N, K, num_slots;
+  int32_t pools, align;      // align: 16, 4 or 2 bytes, of every base, stride and size
+  MovePool pool[kMovePools];
+};
+
+// Sets the pools' first blocks and launches; the block count must stay below 2^31 (false: it does not).
+bool plan_pool_move(MoveArgs& a, int64_t* blocks);
+cudaError_t launch_pool_move(const MoveArgs& a, int64_t blocks, cudaStream_t s);
+
 }  // namespace kda

@@ -93,6 +93,8 @@ kda_status need_table(const View& T, int64_t N) {
   return KDA_OK;
 }
 
+constexpr int32_t kMaxPools = 256;
+
 kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
 
 }  // namespace
@@ -209,6 +211,82 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
     if (wide) a.vec = 8;
   }
   return check_launch(kda::launch_rope_append(a, st));
+}
+
+kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const kda_tensor* src_slots,
+                         const kda_tensor* dst_slots, const kda_tensor* parents, void* stream) {
+  View S, D, P;
+  KDA_CHECK(n_pools >= 1, KDA_ERR_INVALID_ARG, "pools: need at least one pool");
+  KDA_CHECK(pools != nullptr, KDA_ERR_INVALID_ARG, "pools: null pointer");
+  KDA_TRY(ranked_view(src_slots, "src_slots", 2, -1, &S));
+  KDA_TRY(ranked_view(dst_slots, "dst_slots", 2, -1, &D));
+  const int64_t N = S.shape[0], K = S.shape[1];
+  KDA_CHECK(N <= INT32_MAX, KDA_ERR_INVALID_ARG, "src_slots: too many rows");
+  KDA_CHECK(K <= kda::kMoveBeams, KDA_ERR_UNSUPPORTED, "src_slots: %lld slots a row, at most %d", (long long)K,
+            kda::kMoveBeams);
+  KDA_TRY(need_table(S, N));
+  KDA_TRY(need_table(D, N));
+  KDA_TRY(need_shape(D, 1, K));
+  if (parents != nullptr) {
+    KDA_TRY(ranked_view(parents, "parents", 2, -1, &P));
+    KDA_TRY(need_table(P, N));
+    KDA_TRY(need_shape(P, 1, K));
+  }
+  KDA_CHECK(n_pools <= kMaxPools, KDA_ERR_UNSUPPORTED, "pools: %d pools, at most %d a call", n_pools, kMaxPools);
+  View V[kMaxPools];
+  kda::MovePool M[kMaxPools];
+  for (int32_t i = 0; i < n_pools; ++i) {
+    View& v = V[i];
+    KDA_TRY(raw_view(pools[i], "pool", &v));
+    KDA_CHECK(v.shape[0] >= 1 && v.shape[0] <= INT32_MAX, KDA_ERR_INVALID_ARG, "pool %d: num_slots %lld out of range", i,
+              (long long)v.shape[0]);
+    KDA_CHECK(v.shape[0] == V[0].shape[0], KDA_ERR_INVALID_ARG, "pool %d: %lld slots, pool 0 has %lld", i,
+              (long long)v.shape[0], (long long)V[0].shape[0]);
+    // The axes of a slot, smallest stride first, must follow one another without gaps.
+    int64_t size = 1;
+    bool used[4] = {false, false, false, false};
+    for (int step = 1; step < v.ndim; ++step) {
+      int at = -1;
+      for (int j = 1; j < v.ndim; ++j)
+        if (!used[j] && (at < 0 || v.shape[j] <= 1 || (v.shape[at] > 1 && v.stride[j] < v.stride[at]))) at = j;
+      used[at] = true;
+      KDA_CHECK(v.shape[at] <= 1 || v.stride[at] == size, KDA_ERR_INVALID_ARG, "pool %d: a slot must be dense", i);
+      size *= v.shape[at];
+    }
+    KDA_CHECK(v.shape[0] <= 1 || v.stride[0] >= size, KDA_ERR_INVALID_ARG, "pool %d: slot stride %lld overlaps slots", i,
+              (long long)v.stride[0]);
+    M[i] = {v.data, v.shape[0] <= 1 ? 0 : v.stride[0] * esize(v.dtype), size * esize(v.dtype), 0};
+    KDA_TRY(no_alias(v, {&S, &D, &P}));
+    for (int32_t j = 0; j < i; ++j)
+      KDA_CHECK(!overlap(v, V[j]) || interleaved(v, V[j]) || interleaved(V[j], v), KDA_ERR_ALIAS,
+                "pool %d overlaps pool %d", i, j);
+  }
+  if (N == 0 || K == 0) return KDA_OK;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  KDA_TRY(current_device(st, &dev));
+  kda::MoveArgs a{};
+  a.src = reinterpret_cast<const int32_t*>(S.data); a.src_rs = S.stride[0];
+  a.dst = reinterpret_cast<const int32_t*>(D.data); a.dst_rs = D.stride[0];
+  if (parents != nullptr) { a.parents = reinterpret_cast<const int32_t*>(P.data); a.par_rs = P.stride[0]; }
+  a.N = (int32_t)N; a.K = (int32_t)K; a.num_slots = (int32_t)V[0].shape[0];
+  // All launches are planned before the first, so that a refusal moves nothing.
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int32_t i = 0; i < n_pools; i += kda::kMovePools) {
+      a.pools = std::min(kda::kMovePools, n_pools - i);
+      uintptr_t bits = 0;
+      for (int j = 0; j < a.pools; ++j) {
+        a.pool[j] = M[i + j];
+        bits |= reinterpret_cast<uintptr_t>(M[i + j].base) | (uintptr_t)M[i + j].stride | (uintptr_t)M[i + j].bytes;
+      }
+      a.align = bits % 16 == 0 ? 16 : (bits % 4 == 0 ? 4 : 2);
+      int64_t blocks = 0;
+      KDA_CHECK(kda::plan_pool_move(a, &blocks), KDA_ERR_UNSUPPORTED, "pools: too much to move in one call");
+      if (pass == 1 && blocks > 0) KDA_TRY(check_launch(kda::launch_pool_move(a, blocks, st)));
+    }
+  }
+  return KDA_OK;
 }
 
 }  // extern "C"

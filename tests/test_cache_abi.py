@@ -131,3 +131,54 @@ def test_phase_steps_are_the_frequencies_in_64_bit_turns(lib, kw):
 def test_phase_step_refusals(lib, args, text):
     with pytest.raises(binding.KdaError, match=text):
         binding.kda_rope_phase_steps(device="cpu", **args)
+
+
+# ---- kda_pool_move ----------------------------------------------------------------------
+
+
+def _move(lib, pools, src, dst, parents=None, n=None):
+    array = (ctypes.POINTER(binding.KdaTensor) * max(1, len(pools)))()
+    keep = [desc(p) for p in pools]
+    for i, d in enumerate(keep):
+        array[i] = ctypes.pointer(d)
+    return lib.kda_pool_move(array, len(pools) if n is None else n, _ptr(src), _ptr(dst), _ptr(parents), None)
+
+
+def _i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+@pytest.mark.skipif(not NO_GPU, reason="a valid call would launch on host memory")
+def test_move_valid_calls_reach_the_device_query(lib):
+    kv = torch.zeros(5, 2, 8, 2, 64, dtype=BF16)
+    conv = torch.zeros(5, 3, 24, dtype=BF16).permute(0, 2, 1)
+    ok = [torch.zeros(5, 2, 128, 128), conv, kv[:, 0], kv[:, 1], torch.zeros(5, 2, 8, 64).transpose(1, 2), torch.zeros(5)]
+    assert _move(lib, ok, _i32(3, 4), _i32(3, 4), _i32(3, 4)) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _move(lib, [torch.zeros(5, 4)] , _i32(0, 4), _i32(0, 4)) == 0
+
+
+@pytest.mark.parametrize("pools,src,dst,parents,status,text", [
+    ([], _i32(1, 1), _i32(1, 1), None, INVALID, "at least one pool"),
+    ([torch.zeros(5, 4), torch.zeros(6, 4)], _i32(1, 1), _i32(1, 1), None, INVALID, "pool 1: 6 slots"),
+    ([torch.zeros(5, 8)[:, ::2]], _i32(1, 1), _i32(1, 1), None, INVALID, "must be dense"),
+    ([torch.zeros(5, 4, 8)[:, :, :4]], _i32(1, 1), _i32(1, 1), None, INVALID, "must be dense"),
+    ([torch.as_strided(torch.zeros(64), (5, 8), (4, 1))], _i32(1, 1), _i32(1, 1), None, INVALID, "overlaps slots"),
+    ([torch.zeros(5, 4)], _i32(2, 3), _i32(2, 2), None, INVALID, "dst_slots: axis 1"),
+    ([torch.zeros(5, 4)], _i32(2, 3), _i32(2, 3), _i32(3, 3), INVALID, "parents: axis 0"),
+    ([torch.zeros(5, 4)], torch.zeros(2, 3), _i32(2, 3), None, INVALID, "src_slots: dtype"),
+    ([torch.zeros(5, 4)], _i32(2, 33), _i32(2, 33), None, UNSUPPORTED, "at most 32"),
+    ([torch.zeros(5, 4)], _i32(3, 2).t(), _i32(2, 3), None, INVALID, "column stride"),
+])
+def test_move_refusals(lib, pools, src, dst, parents, status, text):
+    assert _move(lib, pools, src, dst, parents) == status, _msg(lib)
+    assert text in _msg(lib)
+
+
+def test_move_refuses_shared_memory_and_too_many_pools(lib):
+    x = torch.zeros(5, 8)
+    assert _move(lib, [x, x], _i32(1, 1), _i32(1, 1)) == ALIAS
+    assert _move(lib, [x, x[:, 4:]], _i32(1, 1), _i32(1, 1)) == ALIAS
+    idx = torch.zeros(5, 8, dtype=torch.int32)
+    assert _move(lib, [idx], idx[:1, :2], _i32(1, 2)) == ALIAS
+    assert _move(lib, [torch.zeros(5, 4)], _i32(1, 1), _i32(1, 1), n=257) == UNSUPPORTED
+    assert _move(lib, [torch.zeros(5, 4)], None, _i32(1, 1)) == INVALID
