@@ -308,6 +308,41 @@ kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, dou
                                 double high, uint64_t* steps);
 
 /*
+ * kda_paged_attention_decode: softmax attention of one new token per
+ * sequence over its pages.  Launches two kernels: one over the positions,
+ * split over every SM whatever the lengths, and one that joins the parts.
+ *
+ *   q           [N, Hq, D] float32 or bfloat16, D = 64, 128 or 256, any row and
+ *               head strides that keep 4-element alignment.
+ *   k_pages, v_pages, page_table: as above, of q's dtype; Hq a multiple of Hkv,
+ *               query head h reads key head h / (Hq / Hkv).
+ *   seq_lens    [N] int32, the new token included; clamped to the table's
+ *               P * page_size positions, at most 2^30.
+ *   workspace   float32, contiguous, at least the floats that
+ *               kda_paged_attention_workspace names for the device's SM count;
+ *               its contents matter only during the call, so calls on one
+ *               stream may share one, concurrent calls may not.
+ *   window      0: every position; w > 0: only the last w positions, t >=
+ *               seq_lens[n] - w.
+ *   scale       > 0, normally 1/sqrt(D).
+ *   out         [N, Hq, D] bfloat16 contiguous (written).
+ *   lse         [N, Hq] float32 contiguous (written), or NULL: the natural
+ *               logarithm of the sum of exp(scale q.k) over the row's positions.
+ * Positions past the length, outside the window or on null pages are never
+ * read into the result, whatever their bytes hold.  A row without positions
+ * gives zero and an lse of minus infinity.  A non-finite key or value at an
+ * attended position makes its row's result non-finite.
+ */
+kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                      const kda_tensor* page_table, const kda_tensor* seq_lens,
+                                      const kda_tensor* workspace, int32_t window, float scale, const kda_tensor* out,
+                                      const kda_tensor* lse, void* stream);
+
+/* Floats of workspace of kda_paged_attention_decode on a device of sm_count SMs (dtype: KDA_F32 / KDA_BF16). */
+kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
+                                         int32_t sm_count, int64_t* floats);
+
+/*
  * kda_pool_move: copies whole slots inside pools, in place; forks, compacts,
  * clears and, by parent beam, reorders recurrent states, conv caches and
  * pages alike.

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -34,6 +35,7 @@ EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda
            "kda_packed_fused_decode",
            "kda_spec_verify_decode",
            "kda_rope_append", "kda_rope_phase_steps", "kda_pool_move",
+           "kda_paged_attention_decode", "kda_paged_attention_workspace",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -64,6 +66,8 @@ def _declare(lib):
         "kda_spec_decode": [T, T, T, T, T, i32, T, i32, T, T, T, f32, vp],
         "kda_spec_verify_decode": [T, T, T, T, T, i32, T, i32, T, T, T, T, T, f32, vp],
         "kda_rope_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
+        "kda_paged_attention_decode": [T, T, T, T, T, T, i32, f32, T, T, vp],
+        "kda_paged_attention_workspace": [i32, i32, i32, i32, i32, vp],
         "kda_pool_move": [ctypes.POINTER(T), i32, T, T, T, vp],
         "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
     }
@@ -286,6 +290,45 @@ def kda_rope_phase_steps(rot_dim, base=10000.0, factor=1.0, original_len=0.0, lo
                                   float(high), steps.data_ptr() or None)
     _check(lib, st)
     return steps.to(device)
+
+
+def kda_paged_attention_workspace(q_heads, kv_heads, head_dim, dtype, sm_count):
+    """Floats of workspace a kda_paged_attention_decode call needs (host-only query)."""
+    lib = library()
+    floats = ctypes.c_int64(0)
+    _check(lib, lib.kda_paged_attention_workspace(int(q_heads), int(kv_heads), int(head_dim), _DTYPES.get(dtype, -1),
+                                                  int(sm_count), ctypes.addressof(floats)))
+    return floats.value
+
+
+@functools.lru_cache(maxsize=None)
+def _attention_floats(q_heads, kv_heads, head_dim, dtype, device):
+    sms = torch.cuda.get_device_properties(device).multi_processor_count
+    return kda_paged_attention_workspace(q_heads, kv_heads, head_dim, dtype, sms)
+
+
+def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window=0, scale=None, out=None, lse=None,
+                               return_lse=False, workspace=None):
+    """One new token per sequence over its pages; returns bf16 out [N, Hq, D], or (out, lse) with return_lse.
+
+    Without `workspace` each call takes one from torch's allocator, which keeps
+    concurrent streams and captured graphs apart.
+    """
+    lib = library()
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        floats = _attention_floats(q.shape[1], k_pages.shape[2], q.shape[2], q.dtype, q.device)
+        workspace = torch.empty(floats, dtype=torch.float32, device=q.device)
+    with _on(q.device):
+        st = lib.kda_paged_attention_decode(_ref(q), _ref(k_pages), _ref(v_pages), _ref(page_table), _ref(seq_lens),
+                                            _ref(workspace), int(window),
+                                            float(scale if scale is not None else q.shape[2] ** -0.5), _ref(out),
+                                            _ref(lse) if lse is not None else None, _stream(q))
+    _check(lib, st)
+    return (out, lse) if return_lse else out
 
 
 def kda_pool_move(pools, src_slots, dst_slots, parents=None):

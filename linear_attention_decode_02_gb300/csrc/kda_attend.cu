@@ -1,0 +1,354 @@
+// Attention of one new token per sequence over a paged cache: the CUDA-core
+// kernel, and the join of partial results.
+//
+// softmax_t(scale q . k_t) v_t over one pass: each warp keeps, per query head,
+// the running maximum m, the sum l of 2^(s - m) and the output o scaled alike;
+// a larger maximum rescales both.  Scores are in units of log2, q carrying
+// scale * log2(e).
+//
+// A warp takes KB positions at a time.  Its lanes hold D/32 channels each, so
+// a key or value vector is one coalesced load, reused by HG query heads from
+// registers; KB * HG partial dot products are reduced by halving exchanges
+// (NV - 1 shuffles for NV values), which leaves each lane one score to
+// exponentiate.
+#include "kda_attend.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kWarpKeys = kTile / kWarps;  // positions of a tile per warp
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_lane(const T* p, float (&x)[VEC]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (VEC == 2) {
+      const float2 r = __ldg(reinterpret_cast<const float2*>(p));
+      x[0] = r.x; x[1] = r.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4) {
+        const float4 r = __ldg(reinterpret_cast<const float4*>(p + i));
+        x[i] = r.x; x[i + 1] = r.y; x[i + 2] = r.z; x[i + 3] = r.w;
+      }
+    }
+  } else {
+    if constexpr (VEC == 2) {
+      const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(p));
+      x[0] = bf_lo(r); x[1] = bf_hi(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4) {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(p + i));
+        x[i] = bf_lo(r.x); x[i + 1] = bf_hi(r.x); x[i + 2] = bf_lo(r.y); x[i + 3] = bf_hi(r.y);
+      }
+    }
+  }
+}
+
+// Sums NV values over the warp; lane l returns value l / (32 / NV).
+template <int NV>
+__device__ __forceinline__ float reduce_scatter(float (&x)[NV], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = NV / 2; n >= 1; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? x[i] : x[i + n];
+      const float keep = upper ? x[i + n] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  float r = x[0];
+#pragma unroll
+  for (; o >= 1; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+
+template <typename T, int D, int HG, int KB>
+__global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int VEC = D / 32, NV = HG * KB, REP = 32 / NV;
+  static_assert(NV <= 32 && kWarpKeys % KB == 0, "bad shape");
+  __shared__ float s_p[kWarps][32];
+  __shared__ float s_m[kWarps][HG], s_l[kWarps][HG];
+  __shared__ float s_o[kWarps][HG * D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
+  const int C = gridDim.x, c = blockIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Place place = find_place<kThreads>(a, units, c, C);
+  const Workspace ws(a.work, C, HG, D);
+  if (place.start == place.stop) {
+    if (threadIdx.x == 0) ws.note[c].n = -1;
+    return;
+  }
+  int n = place.n;
+  Span sp = span_of(a, n);
+  int64_t unit_start = place.before + (place.start - place.before) / sp.tiles * sp.tiles;
+  int group = (int)((unit_start - place.before) / sp.tiles);
+
+  for (int64_t tile = place.start; tile < place.stop;) {
+    const int hk = group / groups, g0 = (group - hk * groups) * HG, heads = min(HG, G - g0);
+    const int64_t unit_end = unit_start + sp.tiles;
+    const int64_t stop = min(unit_end, place.stop);
+    float q[HG][VEC], o[HG][VEC];
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[h][i] = q[h][i] = 0.f;
+      if (h < heads) {
+        load_lane<T, VEC>(static_cast<const T*>(a.q) + n * a.q_rs + (hk * G + g0 + h) * a.q_hs + lane * VEC, q[h]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) q[h][i] *= a.scale_log2;
+      }
+    }
+    float m = -INFINITY, l = 0.f;  // of this lane's head (lane / REP) % HG
+    const int32_t* row = a.table + (int64_t)n * a.table_rs;
+    for (; tile < stop; ++tile) {
+      // Lanes 0 .. kWarpKeys-1 look up one position each.
+      const int t0 = (sp.tile0 + (int)(tile - unit_start)) * kTile + warp * kWarpKeys;
+      int64_t ko = -1, vo = 0;
+      if (lane < kWarpKeys) {
+        const int t = t0 + lane;
+        if (t >= sp.first && t < sp.end) {
+          const int col = t / a.page_size, at = t - col * a.page_size;
+          const int page = __ldg(row + col);
+          if (page > 0 && page < a.num_pages) {
+            ko = page * a.kp.page + at * a.kp.token + hk * a.kp.head;
+            vo = page * a.vp.page + at * a.vp.token + hk * a.vp.head;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kWarpKeys; b += KB) {
+        float k[KB][VEC], v[KB][VEC], s[NV];
+        bool live[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const int64_t kj = __shfl_sync(0xffffffffu, ko, b + j), vj = __shfl_sync(0xffffffffu, vo, b + j);
+          live[j] = kj >= 0;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) k[j][i] = v[j][i] = 0.f;
+          if (live[j]) {
+            load_lane<T, VEC>(static_cast<const T*>(a.kp.data) + kj + lane * VEC, k[j]);
+            load_lane<T, VEC>(static_cast<const T*>(a.vp.data) + vj + lane * VEC, v[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) d = fmaf(q[h][i], k[j][i], d);
+            s[j * HG + h] = d;
+          }
+        float score = reduce_scatter<NV>(s, lane);
+        const int mine = lane / REP / HG;  // this lane's position in the batch
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (mine == j && !live[j]) score = -INFINITY;
+        float top = fmaxf(m, score);
+#pragma unroll
+        for (int x = HG * REP; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float p = exp2f(score - ref);
+        if (__any_sync(0xffffffffu, top > m)) {
+          const float fall = exp2f(m - ref);
+          l *= fall;
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float f = __shfl_sync(0xffffffffu, fall, h * REP);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[h][i] *= f;
+          }
+          m = top;
+        }
+        l += p;
+        if (lane % REP == 0) s_p[warp][lane / REP] = p;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float w = s_p[warp][j * HG + h];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[h][i] = fmaf(w, v[j][i], o[h][i]);
+          }
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int x = HG * REP; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (lane % REP == 0 && lane / REP < HG) {
+      s_m[warp][lane / REP] = m;
+      s_l[warp][lane / REP] = l;
+    }
+#pragma unroll
+    for (int h = 0; h < HG; ++h)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s_o[warp][h * D + lane * VEC + i] = o[h][i];
+    __syncthreads();
+
+    const bool whole = unit_start >= place.start && unit_end <= place.stop;
+    const bool at_start = unit_start <= place.start;
+    const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int h = i / D, d = i - h * D;
+      float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(s_m[w][h] - ref);
+        L = fmaf(f, s_l[w][h], L);
+        O = fmaf(f, s_o[w][i], O);
+      }
+      const int64_t head = (int64_t)n * a.Hq + hk * G + g0 + h;
+      if (whole) {
+        static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(finished(O, L));
+        if (a.lse != nullptr && d == 0) a.lse[head] = log_sum(ref, L);
+      } else {
+        ws.o_of(slot, h)[d] = O;
+        if (d == 0) {
+          ws.ml_of(slot, h)[0] = M;
+          ws.ml_of(slot, h)[1] = L;
+        }
+      }
+    }
+    if (threadIdx.x == 0 && at_start) {
+      PieceNote note;
+      note.unit_start = unit_start; note.unit_end = unit_end; note.tiles = place.T;
+      note.n = unit_start < place.start ? n : -1;
+      note.group = group;
+      ws.note[c] = note;
+    }
+    __syncthreads();
+    if (tile == unit_end) {
+      unit_start = unit_end;
+      if (++group == units) {
+        group = 0;
+        if (++n < a.N) sp = span_of(a, n);
+      }
+    }
+  }
+}
+
+// Joins the partials of one query head of the unit that the cut before piece
+// blockIdx.x crosses, if it is the unit's first cut.  The block's warps share
+// the unit's pieces, each lane D/32 channels.
+template <int D, int HG>
+__global__ void __launch_bounds__(128) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
+  constexpr int VEC = D / 32, WARPS = 4;
+  __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS][D];
+  const int c = blockIdx.x, h = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Workspace ws(a.work, C, HG, D);
+  const PieceNote note = ws.note[c];
+  if (note.n < 0) return;
+  const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG;
+  const int hk = note.group / groups, g0 = (note.group - hk * groups) * HG;
+  if (h >= min(HG, G - g0)) return;
+  const int64_t T = note.tiles;
+  const int64_t start = piece_start(c, T, C);
+  const int64_t first = piece_of(start - 1, T, C);
+  if (piece_start(first, T, C) > note.unit_start) return;  // an earlier cut crosses this unit too
+  const int64_t last = piece_of(note.unit_end - 1, T, C);
+
+  float m = -INFINITY, l = 0.f, o[VEC] = {};
+  for (int64_t i = first + warp; i <= last; i += WARPS) {
+    const int64_t begin = piece_start(i, T, C);
+    if (begin == piece_start(i + 1, T, C)) continue;  // an empty piece
+    const int64_t slot = 2 * i + (begin < note.unit_start ? 1 : 0);  // the first piece may hold another unit before
+    const float pm = ws.ml_of(slot, h)[0], pl = ws.ml_of(slot, h)[1];
+    float po[VEC];
+    const float* src = ws.o_of(slot, h) + lane * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) po[j] = src[j];
+    const float top = fmaxf(m, pm);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = exp2f(m - ref), w = exp2f(pm - ref);
+    l = l * f + pl * w;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = o[j] * f + po[j] * w;
+    m = top;
+  }
+  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) s_o[warp][lane * VEC + j] = o[j];
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += 128) {
+    float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = exp2f(s_m[w] - ref);
+      L = fmaf(f, s_l[w], L);
+      O = fmaf(f, s_o[w][d], O);
+    }
+    const int64_t head = (int64_t)note.n * a.Hq + hk * G + g0 + h;
+    static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16_rn(finished(O, L));
+    if (a.lse != nullptr && d == 0) a.lse[head] = log_sum(ref, L);
+  }
+}
+
+// Query heads a worker carries: all of the key head's up to 8 (4 where D = 256
+// would not leave the registers for more).
+int heads_class(int G, int D) {
+  const int most = D == 256 ? 4 : 8;
+  int h = 1;
+  while (h < G && h < most) h *= 2;
+  return h;
+}
+
+template <typename T, int D, int HG>
+cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t s) {
+  constexpr int KB = 32 / HG < 8 ? 32 / HG : (D == 256 ? 4 : 8);
+  cudaError_t e = launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), 0, s, 1, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kda_attend_join_kernel<D, HG>, dim3(ctas, HG), dim3(128), 0, s, 1, a, ctas);
+}
+
+template <typename T>
+cudaError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  switch (a.D * 16 + p.heads) {
+    case 64 * 16 + 1: return launch_attend<T, 64, 1>(a, p.ctas, s);
+    case 64 * 16 + 2: return launch_attend<T, 64, 2>(a, p.ctas, s);
+    case 64 * 16 + 4: return launch_attend<T, 64, 4>(a, p.ctas, s);
+    case 64 * 16 + 8: return launch_attend<T, 64, 8>(a, p.ctas, s);
+    case 128 * 16 + 1: return launch_attend<T, 128, 1>(a, p.ctas, s);
+    case 128 * 16 + 2: return launch_attend<T, 128, 2>(a, p.ctas, s);
+    case 128 * 16 + 4: return launch_attend<T, 128, 4>(a, p.ctas, s);
+    case 128 * 16 + 8: return launch_attend<T, 128, 8>(a, p.ctas, s);
+    case 256 * 16 + 1: return launch_attend<T, 256, 1>(a, p.ctas, s);
+    case 256 * 16 + 2: return launch_attend<T, 256, 2>(a, p.ctas, s);
+    case 256 * 16 + 4: return launch_attend<T, 256, 4>(a, p.ctas, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+AttendPlan attend_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
+  (void)dtype;
+  AttendPlan p;
+  p.ctas = 2 * sms;
+  p.heads = heads_class(Hq / Hkv, D);
+  p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
+  return p;
+}
+
+cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s) {
+  const AttendPlan p = attend_plan(a.Hq, a.Hkv, a.D, a.dtype, sms);
+  return a.dtype == KDA_DT_F32 ? launch_attend_d<float>(a, p, s) : launch_attend_d<__nv_bfloat16>(a, p, s);
+}
+
+}  // namespace kda

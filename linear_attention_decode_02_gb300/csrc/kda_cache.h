@@ -54,4 +54,29 @@ struct MoveArgs {
 bool plan_pool_move(MoveArgs& a, int64_t* blocks);
 cudaError_t launch_pool_move(const MoveArgs& a, int64_t blocks, cudaStream_t s);
 
+// Attention of one new token per sequence over paged keys and values.
+struct AttendArgs {
+  const void* q; int64_t q_rs, q_hs;      // [N, Hq, D]
+  PageView kp, vp;
+  int32_t num_pages, page_size;
+  const int32_t* table; int64_t table_rs; int32_t table_cols;
+  const int32_t* lens;                    // [N]
+  void* out;                              // bf16 [N, Hq, D] contiguous
+  float* lse;                             // [N, Hq] contiguous, or null
+  float* work;                            // attend_plan().floats
+  int32_t N, Hq, Hkv, D, dtype;
+  int32_t window;                         // 0: all
+  float scale_log2;                       // scale * log2(e)
+  int32_t vec16;                          // q rows, key and value vectors start on 16-byte boundaries
+};
+
+// Grid and workspace of the attention kernels: `ctas` workers that each may
+// leave two partial results of `heads` query heads.
+struct AttendPlan {
+  int32_t ctas, heads;
+  int64_t floats;
+};
+AttendPlan attend_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
+cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
+
 }  // namespace kda

@@ -95,6 +95,15 @@ kda_status need_table(const View& T, int64_t N) {
 
 constexpr int32_t kMaxPools = 256;
 
+kda_status check_attention_heads(int64_t Hq, int64_t Hkv, int64_t D) {
+  KDA_CHECK(Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0, KDA_ERR_INVALID_ARG,
+            "%lld query heads cannot share %lld key heads evenly", (long long)Hq, (long long)Hkv);
+  KDA_CHECK(Hq <= 4096, KDA_ERR_UNSUPPORTED, "%lld query heads, at most 4096", (long long)Hq);
+  KDA_CHECK(D == 64 || D == 128 || D == 256, KDA_ERR_UNSUPPORTED, "head dimension %lld: 64, 128 and 256 are served",
+            (long long)D);
+  return KDA_OK;
+}
+
 kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
 
 }  // namespace
@@ -287,6 +296,83 @@ kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const 
     }
   }
   return KDA_OK;
+}
+
+kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
+                                         int32_t sm_count, int64_t* floats) {
+  KDA_CHECK(floats != nullptr, KDA_ERR_INVALID_ARG, "floats: null pointer");
+  KDA_TRY(check_attention_heads(q_heads, kv_heads, head_dim));
+  KDA_CHECK(dtype == KDA_F32 || dtype == KDA_BF16, KDA_ERR_INVALID_ARG, "dtype %s not accepted", dtname(dtype));
+  KDA_CHECK(sm_count >= 1 && sm_count <= 4096, KDA_ERR_INVALID_ARG, "sm_count %d out of range", sm_count);
+  *floats = kda::attend_plan(q_heads, kv_heads, head_dim, dtype, sm_count).floats;
+  return KDA_OK;
+}
+
+kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                      const kda_tensor* page_table, const kda_tensor* seq_lens,
+                                      const kda_tensor* workspace, int32_t window, float scale, const kda_tensor* out,
+                                      const kda_tensor* lse, void* stream) {
+  View Q, KP, VP, T, L, W, O, E;
+  KDA_TRY(ranked_view(q, "q", 3, -1, &Q));
+  KDA_TRY(ranked_view(k_pages, "k_pages", 4, -1, &KP));
+  KDA_TRY(ranked_view(v_pages, "v_pages", 4, -1, &VP));
+  KDA_TRY(ranked_view(page_table, "page_table", 2, -1, &T));
+  KDA_TRY(raw_view(seq_lens, "seq_lens", &L));
+  KDA_TRY(ranked_view(workspace, "workspace", 1, -1, &W));
+  KDA_TRY(ranked_view(out, "out", 3, -1, &O));
+  const int64_t N = Q.shape[0], Hq = Q.shape[1], D = Q.shape[2], Hkv = KP.shape[2];
+  KDA_TRY(need_dtype(Q, KDA_F32, KDA_BF16));
+  KDA_CHECK(N <= INT32_MAX, KDA_ERR_INVALID_ARG, "q: too many sequences");
+  KDA_TRY(check_attention_heads(Hq, Hkv, D));
+  KDA_TRY(need_vec_layout(Q));
+  KDA_TRY(need_pages(KP, VP, Hkv, D));
+  KDA_CHECK(KP.dtype == Q.dtype, KDA_ERR_INVALID_ARG, "k_pages: dtype must match q");
+  KDA_TRY(need_table(T, N));
+  KDA_CHECK(T.shape[1] <= (1 << 30) / KP.shape[1], KDA_ERR_UNSUPPORTED,
+            "page_table: %lld pages of %lld positions, more than 2^30 positions a sequence", (long long)T.shape[1],
+            (long long)KP.shape[1]);
+  KDA_TRY(need_indices(L, N));
+  KDA_TRY(need_out(O));
+  KDA_TRY(need_shape(O, 0, N));
+  KDA_TRY(need_shape(O, 1, Hq));
+  KDA_TRY(need_shape(O, 2, D));
+  if (lse != nullptr) {
+    KDA_TRY(ranked_view(lse, "lse", 2, -1, &E));
+    KDA_TRY(need_dtype(E, KDA_F32));
+    KDA_TRY(need_shape(E, 0, N));
+    KDA_TRY(need_shape(E, 1, Hq));
+    KDA_TRY(need_contiguous(E));
+  }
+  KDA_TRY(need_dtype(W, KDA_F32));
+  KDA_TRY(need_contiguous(W));
+  KDA_CHECK(reinterpret_cast<uintptr_t>(W.data) % 16 == 0, KDA_ERR_INVALID_ARG, "workspace: data must be 16-byte aligned");
+  KDA_CHECK(window >= 0, KDA_ERR_INVALID_ARG, "window must not be negative (0: all positions)");
+  KDA_CHECK(std::isfinite(scale) && scale > 0.f, KDA_ERR_INVALID_ARG, "scale must be finite and positive");
+  KDA_TRY(no_shared_bytes(O, {&Q, &KP, &VP, &T, &L, &W, &E}));
+  KDA_TRY(no_shared_bytes(W, {&Q, &KP, &VP, &T, &L, &E}));
+  KDA_TRY(no_shared_bytes(E, {&Q, &KP, &VP, &T, &L}));
+  if (N == 0) return KDA_OK;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  KDA_TRY(current_device(st, &dev));
+  const kda::AttendPlan plan = kda::attend_plan((int32_t)Hq, (int32_t)Hkv, (int32_t)D, KP.dtype, dev.sms);
+  KDA_CHECK(W.shape[0] >= plan.floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
+            (long long)W.shape[0], (long long)plan.floats);
+  kda::AttendArgs a{};
+  a.q = Q.data; a.q_rs = Q.stride[0]; a.q_hs = Q.stride[1];
+  a.kp = page_view(KP); a.vp = page_view(VP);
+  a.num_pages = (int32_t)KP.shape[0]; a.page_size = (int32_t)KP.shape[1];
+  a.table = reinterpret_cast<const int32_t*>(T.data); a.table_rs = T.stride[0]; a.table_cols = (int32_t)T.shape[1];
+  a.lens = reinterpret_cast<const int32_t*>(L.data);
+  a.out = O.data;
+  a.lse = lse != nullptr ? reinterpret_cast<float*>(E.data) : nullptr;
+  a.work = reinterpret_cast<float*>(W.data);
+  a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.dtype = KP.dtype;
+  a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.vec16 = vectors_aligned(Q, 16) && vectors_aligned(KP, 16) && vectors_aligned(VP, 16);
+  return check_launch(kda::launch_paged_attention(a, dev.sms, st));
 }
 
 }  // extern "C"

@@ -182,3 +182,79 @@ def test_move_refuses_shared_memory_and_too_many_pools(lib):
     assert _move(lib, [idx], idx[:1, :2], _i32(1, 2)) == ALIAS
     assert _move(lib, [torch.zeros(5, 4)], _i32(1, 1), _i32(1, 1), n=257) == UNSUPPORTED
     assert _move(lib, [torch.zeros(5, 4)], None, _i32(1, 1)) == INVALID
+
+
+# ---- kda_paged_attention_decode -----------------------------------------------------------
+
+
+def _attend(N=3, Hq=4, Hkv=2, D=64, P=5, page=8, dtype=BF16):
+    floats = binding.kda_paged_attention_workspace(Hq, Hkv, D, dtype, 152)
+    return dict(q=torch.zeros(N, Hq, D, dtype=dtype), k_pages=torch.zeros(4, page, Hkv, D, dtype=dtype),
+                v_pages=torch.zeros(4, page, Hkv, D, dtype=dtype), table=torch.zeros(N, P, dtype=torch.int32),
+                lens=torch.zeros(N, dtype=torch.int32), work=torch.zeros(floats), out=torch.zeros(N, Hq, D, dtype=BF16),
+                lse=torch.zeros(N, Hq))
+
+
+def _call_attend(lib, t, window=0, scale=0.125):
+    d = {n: _ptr(x) for n, x in t.items()}
+    return lib.kda_paged_attention_decode(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], d["work"], window,
+                                          scale, d["out"], d["lse"], None)
+
+
+@pytest.mark.skipif(not NO_GPU, reason="a valid call would launch on host memory")
+def test_attention_valid_calls_reach_the_device_query(lib):
+    assert _call_attend(lib, _attend()) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_attend(lib, {**_attend(), "lse": None}, window=7) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_attend(lib, _attend(dtype=torch.float32)) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_attend(lib, _attend(N=0)) == 0
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (lambda t: t.update(q=torch.zeros(3, 3, 64, dtype=BF16)), INVALID, "evenly"),
+    (lambda t: t.update(q=torch.zeros(3, 4, 96, dtype=BF16)), UNSUPPORTED, "head dimension 96"),
+    (lambda t: t.update(q=torch.zeros(3, 4, 64)), INVALID, "k_pages: dtype must match q"),
+    (lambda t: t.update(v_pages=torch.zeros(4, 8, 2, 64)), INVALID, "v_pages: dtype must match"),
+    (lambda t: t.update(v_pages=torch.zeros(4, 8, 1, 64, dtype=BF16)), INVALID, "v_pages: axis 2"),
+    (lambda t: t.update(table=torch.zeros(2, 5, dtype=torch.int32)), INVALID, "page_table: axis 0"),
+    (lambda t: t.update(lens=torch.zeros(4, dtype=torch.int32)), INVALID, "seq_lens: axis 0"),
+    (lambda t: t.update(work=torch.zeros(0)), None, None),
+    (lambda t: t.update(work=torch.zeros(99, dtype=torch.int32)), INVALID, "workspace: dtype"),
+    (lambda t: t.update(out=torch.zeros(3, 4, 64)), INVALID, "out: dtype"),
+    (lambda t: t.update(lse=torch.zeros(3, 5)), INVALID, "lse: axis 1"),
+    (lambda t: t.update(lse=torch.zeros(4, 3).t()), INVALID, "contiguous"),
+    (lambda t: t.update(out=t["q"]), ALIAS, "out overlaps q"),
+    (lambda t: t.update(lse=t["work"][:12].view(3, 4)), ALIAS, "workspace overlaps lse"),
+    (lambda t: t.update(q=torch.zeros(3, 4, 66, dtype=BF16)[..., :64]), INVALID, "multiple of 4"),
+    (lambda t: t.update(table=None), INVALID, "page_table: null"),
+])
+def test_attention_refusals(lib, change, status, text):
+    t = _attend()
+    change(t)
+    got = _call_attend(lib, t)
+    if status is None:
+        assert got != 0
+        return
+    assert got == status, _msg(lib)
+    assert text in _msg(lib)
+
+
+def test_attention_refuses_bad_scalars_and_tables(lib):
+    assert _call_attend(lib, _attend(), window=-1) == INVALID
+    for scale in (0.0, -1.0, float("inf"), float("nan")):
+        assert _call_attend(lib, _attend(), scale=scale) == INVALID
+    t = _attend()
+    d = {n: desc(x) for n, x in t.items()}
+    d["table"].shape[1], d["table"].stride[0] = (1 << 27) + 1, 1 << 28  # refused before anything is read
+    ptr = {n: ctypes.byref(x) for n, x in d.items()}
+    assert lib.kda_paged_attention_decode(ptr["q"], ptr["k_pages"], ptr["v_pages"], ptr["table"], ptr["lens"],
+                                          ptr["work"], 0, 0.125, ptr["out"], ptr["lse"], None) == UNSUPPORTED
+    assert "2^30" in _msg(lib)
+
+
+def test_attention_workspace_query(lib):
+    small = binding.kda_paged_attention_workspace(8, 8, 64, BF16, 152)
+    assert 0 < small < binding.kda_paged_attention_workspace(64, 8, 128, BF16, 152) < 1 << 24
+    for args in ((8, 3, 64, BF16, 152), (8, 0, 64, BF16, 152), (8, 8, 80, BF16, 152), (8, 8, 64, torch.int32, 152),
+                 (8, 8, 64, BF16, 0)):
+        with pytest.raises(binding.KdaError):
+            binding.kda_paged_attention_workspace(*args)
