@@ -343,6 +343,34 @@ kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int3
                                          int32_t sm_count, int64_t* floats);
 
 /*
+ * kda_beam_select: the best continuations of each request's beams.  Launches
+ * two kernels, over the logits and over the pieces' candidates.
+ *
+ *   logits      [N, B, V] float32 or bfloat16, unit stride on the vocabulary, any
+ *               other positive strides; B <= 32, V <= 2^24.
+ *   scores      [N, B] float32 contiguous: log probability of each beam so far.
+ *   finished    [N, B] int32 contiguous, or NULL: non-zero marks a beam that has
+ *               ended; its one continuation is eos_token, at its score unchanged.
+ *   workspace   float32, contiguous, the floats of kda_beam_select_workspace;
+ *               its contents matter only during the call.
+ *   out_scores float32, out_parents int32, out_tokens int32 [N, M] contiguous
+ *               (written), 1 <= M <= 64.
+ * Continuation (b, t) is worth scores[b] + logits[b, t] - log sum exp(logits[b]);
+ * the M largest of a request's B * V are returned in falling order, equal ones
+ * by rising b, then t.  The comparison is in float64, the returned score
+ * rounded to float32.  A logit of minus infinity is no continuation, and a beam
+ * whose score or log-sum is not finite (a dead beam; a NaN or +infinity among
+ * its logits) has none.  Places without one get -infinity, -1 and -1.
+ */
+kda_status kda_beam_select(const kda_tensor* logits, const kda_tensor* scores, const kda_tensor* finished,
+                           int32_t eos_token, const kda_tensor* workspace, const kda_tensor* out_scores,
+                           const kda_tensor* out_parents, const kda_tensor* out_tokens, void* stream);
+
+/* Floats of workspace of kda_beam_select on a device of sm_count SMs (dtype of the logits: KDA_F32 / KDA_BF16). */
+kda_status kda_beam_select_workspace(int64_t requests, int32_t beams, int64_t vocab, int32_t num_out, int32_t dtype,
+                                     int32_t sm_count, int64_t* floats);
+
+/*
  * kda_pool_move: copies whole slots inside pools, in place; forks, compacts,
  * clears and, by parent beam, reorders recurrent states, conv caches and
  * pages alike.

@@ -14,13 +14,15 @@ and the operators that the attention layers and beams around them need:
 
     kda_rope_append        rotary positions, keys and values into a paged cache
     kda_paged_attention_decode  attention of one new token over the paged cache
+    kda_beam_select        the best continuations of each request's beams
     kda_pool_move          copies, forks, clears and reorders slots of any pools
 
 Build the library with ``python -m linear_attention_decode_02_gb300.build``.
 """
 
-from .binding import (SCHED_AUTO, SCHED_SPLIT, SCHED_STREAM, KdaError, kda_device_error,  # noqa: F401
-                      kda_fused_decode, kda_packed_decode, kda_packed_fused_decode, kda_plan_schedule, kda_plan_split,
-                      kda_paged_attention_decode, kda_paged_attention_workspace, kda_pool_move, kda_recurrent_decode,
-                      kda_rope_append, kda_rope_phase_steps, kda_set_schedule_override, kda_set_split_override, kda_spec_decode, kda_spec_verify_decode,
-                      kda_version, library)
+from .binding import (SCHED_AUTO, SCHED_SPLIT, SCHED_STREAM, KdaError, kda_beam_select,  # noqa: F401
+                      kda_beam_select_workspace, kda_device_error, kda_fused_decode, kda_packed_decode,
+                      kda_packed_fused_decode, kda_paged_attention_decode, kda_paged_attention_workspace,
+                      kda_plan_schedule, kda_plan_split, kda_pool_move, kda_recurrent_decode, kda_rope_append,
+                      kda_rope_phase_steps, kda_set_schedule_override, kda_set_split_override, kda_spec_decode,
+                      kda_spec_verify_decode, kda_version, library)

@@ -36,6 +36,7 @@ EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda
            "kda_spec_verify_decode",
            "kda_rope_append", "kda_rope_phase_steps", "kda_pool_move",
            "kda_paged_attention_decode", "kda_paged_attention_workspace",
+           "kda_beam_select", "kda_beam_select_workspace",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -68,6 +69,8 @@ def _declare(lib):
         "kda_rope_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
         "kda_paged_attention_decode": [T, T, T, T, T, T, i32, f32, T, T, vp],
         "kda_paged_attention_workspace": [i32, i32, i32, i32, i32, vp],
+        "kda_beam_select": [T, T, T, i32, T, T, T, T, vp],
+        "kda_beam_select_workspace": [ctypes.c_int64, i32, ctypes.c_int64, i32, i32, i32, vp],
         "kda_pool_move": [ctypes.POINTER(T), i32, T, T, T, vp],
         "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
     }
@@ -329,6 +332,44 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
                                             _ref(lse) if lse is not None else None, _stream(q))
     _check(lib, st)
     return (out, lse) if return_lse else out
+
+
+def kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sm_count):
+    """Floats of workspace a kda_beam_select call needs (host-only query)."""
+    lib = library()
+    floats = ctypes.c_int64(0)
+    _check(lib, lib.kda_beam_select_workspace(int(requests), int(beams), int(vocab), int(num_out),
+                                              _DTYPES.get(dtype, -1), int(sm_count), ctypes.addressof(floats)))
+    return floats.value
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_floats(requests, beams, vocab, num_out, dtype, device):
+    sms = torch.cuda.get_device_properties(device).multi_processor_count
+    return kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sms)
+
+
+def kda_beam_select(logits, scores, num_out, finished=None, eos_token=0, out=None, workspace=None):
+    """The num_out best continuations of each request: (scores, parents, tokens), each [N, num_out].
+
+    `out` may give the three tensors; the workspace is as in
+    kda_paged_attention_decode.
+    """
+    lib = library()
+    n, dev = logits.shape[0], logits.device
+    if out is None:
+        out = (torch.empty((n, num_out), dtype=torch.float32, device=dev),
+               torch.empty((n, num_out), dtype=torch.int32, device=dev),
+               torch.empty((n, num_out), dtype=torch.int32, device=dev))
+    if workspace is None:
+        floats = _beam_floats(n, logits.shape[1], logits.shape[2], int(num_out), logits.dtype, dev)
+        workspace = torch.empty(floats, dtype=torch.float32, device=dev)
+    with _on(dev):
+        st = lib.kda_beam_select(_ref(logits), _ref(scores), _ref(finished) if finished is not None else None,
+                                 int(eos_token), _ref(workspace), _ref(out[0]), _ref(out[1]), _ref(out[2]),
+                                 _stream(logits))
+    _check(lib, st)
+    return out
 
 
 def kda_pool_move(pools, src_slots, dst_slots, parents=None):

@@ -79,4 +79,23 @@ struct AttendPlan {
 AttendPlan attend_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
 
+// Beam selection over beams x vocabulary.
+constexpr int kBeamMax = 32;      // beams of a request
+constexpr int kBeamOutMax = 64;   // candidates returned
+struct BeamArgs {
+  const void* logits; int64_t ns, bs;   // [N, B, V] element strides
+  const float* scores;                  // [N, B]
+  const int32_t* finished;              // [N, B], or null
+  float* out_scores; int32_t* out_parents; int32_t* out_tokens;  // [N, M]
+  float* work;
+  int32_t N, B, V, M, eos, dtype;
+};
+// A block scans `elements` logits of one beam; `splits` blocks a beam.
+struct BeamPlan {
+  int32_t per_thread, splits;
+  int64_t floats;
+};
+BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, int32_t sms);
+cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& p, cudaStream_t s);
+
 }  // namespace kda

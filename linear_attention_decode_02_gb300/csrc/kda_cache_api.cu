@@ -104,6 +104,16 @@ kda_status check_attention_heads(int64_t Hq, int64_t Hkv, int64_t D) {
   return KDA_OK;
 }
 
+kda_status check_beam_sizes(int64_t N, int64_t B, int64_t V, int64_t M) {
+  KDA_CHECK(N >= 0 && N < (1 << 24), KDA_ERR_UNSUPPORTED, "%lld requests, fewer than 2^24 are served", (long long)N);
+  KDA_CHECK(B >= 1 && B <= kda::kBeamMax, KDA_ERR_UNSUPPORTED, "%lld beams, 1 to %d are served", (long long)B,
+            kda::kBeamMax);
+  KDA_CHECK(V >= 1 && V <= (1 << 24), KDA_ERR_UNSUPPORTED, "vocabulary of %lld, 1 to 2^24 are served", (long long)V);
+  KDA_CHECK(M >= 1 && M <= kda::kBeamOutMax, KDA_ERR_UNSUPPORTED, "%lld candidates, 1 to %d are served", (long long)M,
+            kda::kBeamOutMax);
+  return KDA_OK;
+}
+
 kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
 
 }  // namespace
@@ -373,6 +383,78 @@ kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_p
   a.scale_log2 = scale * 1.4426950408889634f;
   a.vec16 = vectors_aligned(Q, 16) && vectors_aligned(KP, 16) && vectors_aligned(VP, 16);
   return check_launch(kda::launch_paged_attention(a, dev.sms, st));
+}
+
+kda_status kda_beam_select_workspace(int64_t requests, int32_t beams, int64_t vocab, int32_t num_out, int32_t dtype,
+                                     int32_t sm_count, int64_t* floats) {
+  KDA_CHECK(floats != nullptr, KDA_ERR_INVALID_ARG, "floats: null pointer");
+  KDA_TRY(check_beam_sizes(requests, beams, vocab, num_out));
+  KDA_CHECK(dtype == KDA_F32 || dtype == KDA_BF16, KDA_ERR_INVALID_ARG, "dtype %s not accepted", dtname(dtype));
+  KDA_CHECK(sm_count >= 1 && sm_count <= 4096, KDA_ERR_INVALID_ARG, "sm_count %d out of range", sm_count);
+  *floats = requests == 0 ? 0 : kda::beam_plan(requests, beams, (int32_t)vocab, num_out, dtype, sm_count).floats;
+  return KDA_OK;
+}
+
+kda_status kda_beam_select(const kda_tensor* logits, const kda_tensor* scores, const kda_tensor* finished,
+                           int32_t eos_token, const kda_tensor* workspace, const kda_tensor* out_scores,
+                           const kda_tensor* out_parents, const kda_tensor* out_tokens, void* stream) {
+  View X, S, F, W, OS, OP, OT;
+  KDA_TRY(ranked_view(logits, "logits", 3, -1, &X));
+  KDA_TRY(ranked_view(scores, "scores", 2, -1, &S));
+  if (finished != nullptr) KDA_TRY(ranked_view(finished, "finished", 2, -1, &F));
+  KDA_TRY(ranked_view(workspace, "workspace", 1, -1, &W));
+  KDA_TRY(ranked_view(out_scores, "out_scores", 2, -1, &OS));
+  KDA_TRY(ranked_view(out_parents, "out_parents", 2, -1, &OP));
+  KDA_TRY(ranked_view(out_tokens, "out_tokens", 2, -1, &OT));
+  const int64_t N = X.shape[0], B = X.shape[1], V = X.shape[2], M = OS.shape[1];
+  KDA_TRY(need_dtype(X, KDA_F32, KDA_BF16));
+  KDA_CHECK(V <= 1 || X.stride[2] == 1, KDA_ERR_INVALID_ARG, "logits: vocabulary axis must have stride 1");
+  KDA_CHECK(reinterpret_cast<uintptr_t>(X.data) % esize(X.dtype) == 0, KDA_ERR_INVALID_ARG, "logits: misaligned data");
+  KDA_TRY(check_beam_sizes(N, B, V, M));
+  KDA_TRY(need_dtype(S, KDA_F32));
+  KDA_TRY(need_shape(S, 0, N));
+  KDA_TRY(need_shape(S, 1, B));
+  KDA_TRY(need_contiguous(S));
+  if (finished != nullptr) {
+    KDA_TRY(need_dtype(F, KDA_I32));
+    KDA_TRY(need_shape(F, 0, N));
+    KDA_TRY(need_shape(F, 1, B));
+    KDA_TRY(need_contiguous(F));
+    KDA_CHECK(eos_token >= 0 && eos_token < V, KDA_ERR_INVALID_ARG, "eos_token %d outside the vocabulary", eos_token);
+  }
+  KDA_TRY(need_dtype(OS, KDA_F32));
+  for (const View* o : {&OP, &OT}) KDA_TRY(need_dtype(*o, KDA_I32));
+  for (const View* o : {&OS, &OP, &OT}) {
+    KDA_TRY(need_shape(*o, 0, N));
+    KDA_TRY(need_shape(*o, 1, M));
+    KDA_TRY(need_contiguous(*o));
+  }
+  KDA_TRY(need_dtype(W, KDA_F32));
+  KDA_TRY(need_contiguous(W));
+  KDA_CHECK(reinterpret_cast<uintptr_t>(W.data) % 16 == 0, KDA_ERR_INVALID_ARG, "workspace: data must be 16-byte aligned");
+  KDA_TRY(no_alias(W, {&X, &S, &F, &OS, &OP, &OT}));
+  KDA_TRY(no_alias(OS, {&X, &S, &F, &OP, &OT}));
+  KDA_TRY(no_alias(OP, {&X, &S, &F, &OT}));
+  KDA_TRY(no_alias(OT, {&X, &S, &F}));
+  if (N == 0) return KDA_OK;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  KDA_TRY(current_device(st, &dev));
+  const kda::BeamPlan plan = kda::beam_plan(N, (int32_t)B, (int32_t)V, (int32_t)M, X.dtype, dev.sms);
+  KDA_TRY(check_grid(N * B * plan.splits));
+  KDA_CHECK(W.shape[0] >= plan.floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
+            (long long)W.shape[0], (long long)plan.floats);
+  kda::BeamArgs a{};
+  a.logits = X.data; a.ns = X.stride[0]; a.bs = X.stride[1];
+  a.scores = reinterpret_cast<const float*>(S.data);
+  a.finished = finished != nullptr ? reinterpret_cast<const int32_t*>(F.data) : nullptr;
+  a.out_scores = reinterpret_cast<float*>(OS.data);
+  a.out_parents = reinterpret_cast<int32_t*>(OP.data);
+  a.out_tokens = reinterpret_cast<int32_t*>(OT.data);
+  a.work = reinterpret_cast<float*>(W.data);
+  a.N = (int32_t)N; a.B = (int32_t)B; a.V = (int32_t)V; a.M = (int32_t)M; a.eos = eos_token; a.dtype = X.dtype;
+  return check_launch(kda::launch_beam_select(a, plan, st));
 }
 
 }  // extern "C"

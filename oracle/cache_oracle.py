@@ -104,9 +104,8 @@ def beam_candidates(logits, scores, finished=None, eos_token=0):
             with np.errstate(all="ignore"):
                 m = np.max(x[n, b])
                 total = np.sum(np.exp(x[n, b] - m))
-                base = m + np.log(total)
-            if np.isfinite(base):
-                c[n, b] = x[n, b] - base + s
+                if np.isfinite(m) and np.isfinite(total):
+                    c[n, b] = (x[n, b] - m) - np.log(total) + s
     return c
 
 

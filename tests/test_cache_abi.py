@@ -258,3 +258,56 @@ def test_attention_workspace_query(lib):
                  (8, 8, 64, BF16, 0)):
         with pytest.raises(binding.KdaError):
             binding.kda_paged_attention_workspace(*args)
+
+
+# ---- kda_beam_select ------------------------------------------------------------------------
+
+
+def _beam(N=2, B=3, V=100, M=4, dtype=BF16):
+    floats = binding.kda_beam_select_workspace(N, B, V, M, dtype, 152)
+    return dict(logits=torch.zeros(N, B, V, dtype=dtype), scores=torch.zeros(N, B),
+                finished=torch.zeros(N, B, dtype=torch.int32), work=torch.zeros(floats), s=torch.zeros(N, M),
+                p=torch.zeros(N, M, dtype=torch.int32), t=torch.zeros(N, M, dtype=torch.int32))
+
+
+def _call_beam(lib, t, eos=0):
+    d = {n: _ptr(x) for n, x in t.items()}
+    return lib.kda_beam_select(d["logits"], d["scores"], d["finished"], eos, d["work"], d["s"], d["p"], d["t"], None)
+
+
+@pytest.mark.skipif(not NO_GPU, reason="a valid call would launch on host memory")
+def test_beam_valid_calls_reach_the_device_query(lib):
+    assert _call_beam(lib, _beam()) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_beam(lib, {**_beam(dtype=torch.float32), "finished": None}, eos=-1) in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_beam(lib, {**_beam(), "logits": torch.zeros(3, 2, 120, dtype=BF16).transpose(0, 1)[..., 7:107]}) \
+        in (UNSUPPORTED, CUDA), _msg(lib)
+    assert _call_beam(lib, _beam(N=0)) == 0
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (lambda t: t.update(logits=torch.zeros(2, 3, 100, dtype=torch.int32)), INVALID, "logits: dtype"),
+    (lambda t: t.update(logits=torch.zeros(2, 100, 3, dtype=BF16).transpose(1, 2)), INVALID, "stride 1"),
+    (lambda t: t.update(logits=torch.zeros(2, 33, 10, dtype=BF16)), UNSUPPORTED, "33 beams"),
+    (lambda t: t.update(logits=torch.zeros(2, 3, 0, dtype=BF16)), UNSUPPORTED, "vocabulary of 0"),
+    (lambda t: t.update(scores=torch.zeros(2, 4)), INVALID, "scores: axis 1"),
+    (lambda t: t.update(scores=torch.zeros(3, 2).t()), INVALID, "scores: must be contiguous"),
+    (lambda t: t.update(finished=torch.zeros(2, 3)), INVALID, "finished: dtype"),
+    (lambda t: t.update(s=torch.zeros(2, 65)), UNSUPPORTED, "65 candidates"),
+    (lambda t: t.update(p=torch.zeros(2, 5, dtype=torch.int32)), INVALID, "out_parents: axis 1"),
+    (lambda t: t.update(t=torch.zeros(2, 4)), INVALID, "out_tokens: dtype"),
+    (lambda t: t.update(t=t["p"]), ALIAS, "out_parents overlaps out_tokens"),
+    (lambda t: t.update(s=t["work"][:8].view(2, 4)), ALIAS, "workspace overlaps out_scores"),
+    (lambda t: t.update(work=None), INVALID, "workspace: null"),
+])
+def test_beam_refusals(lib, change, status, text):
+    t = _beam()
+    change(t)
+    assert _call_beam(lib, t) == status, _msg(lib)
+    assert text in _msg(lib)
+
+
+def test_beam_refuses_tokens_outside_the_vocabulary(lib):
+    for eos in (-1, 100):
+        assert _call_beam(lib, _beam(), eos=eos) == INVALID and "eos_token" in _msg(lib)
+    with pytest.raises(binding.KdaError):
+        binding.kda_beam_select_workspace(1, 0, 10, 1, BF16, 152)
