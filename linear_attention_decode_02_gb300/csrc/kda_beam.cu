@@ -3,17 +3,26 @@
 //
 // Within a beam the order is that of the logits alone, so one pass over them
 // finds both the log-sum and the beam's M best; only those enter the
-// comparison between beams.  A block reads one piece of one beam's logits into
-// registers, takes their maximum and the sum of exponentials, and keeps the M
-// best: the M-th largest of the threads' own maxima bounds them from below, so
-// few elements pass into the list that one warp then orders.  A second kernel
-// joins the pieces' sums and merges their sorted lists.
+// comparison between beams.  A block holds one piece of one beam's logits in
+// registers as they were loaded.  Its threads' maxima give the piece's largest
+// logit and a bound: the least maximum of at least M disjoint groups of
+// threads, above which at least M elements lie and, on unordered data, about
+// M ln M.  Those few go to a list, where each finds its place by counting the
+// larger ones.  A second kernel joins the pieces' sums and orders the pieces'
+// candidates of all beams in the same way.
 //
-// Which beam wins decides the tokens, so beams are compared in float64: the
-// pieces' sums are accumulated in it from float32 exponentials, whose random
-// errors average out, and a logit enters unrounded.
+// Which beam wins decides the tokens, so the log-sums have to be better than
+// float32 gives: a piece's exponentials are 2^((x - top) log2(e) + c), with c
+// such that top log2(e) - c is an integer, so that pieces are rescaled by exact
+// powers of two; log2(e) enters in two parts; lanes and pieces are added with
+// the rounding carried along; and logarithms and candidates are unrounded sums
+// of two float32 (float64 runs at a hundredth of float32's rate here: a
+// logarithm in it alone took 1.8 us).  What is left are the exponentials' own errors, which
+// are random and average out over the vocabulary.
 //
-// Bound by memory: every logit is read once.
+// Bound by memory: every logit is read once, 128 bytes a thread in flight.
+#include <float.h>
+
 #include "kda_cache.h"
 #include "kda_device.cuh"
 
@@ -21,14 +30,82 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kList = 1024;  // elements that may pass the bound
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatches = 8;   // batches of loads a block may take
+constexpr int kList = 1024;   // elements that may pass the bound
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;  // log2(e) to 2^-50
+constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;  // ln 2 to 2^-50
+constexpr double kLog2eDouble = 1.4426950408889634, kLn2Double = 0.6931471805599453;
 
+// Sum of 2^((x - top) log2(e) + c) over a piece, as hi + lo.
 struct PieceSum {
-  double sum;   // of exp(x - top)
-  float top;    // largest logit, -inf if none
-  int32_t next; // the join's place in the piece's list
+  float hi, lo;
+  float top;    // largest logit
+  float pad;
 };
 static_assert(sizeof(PieceSum) == 16, "workspace layout");
+
+// hi + lo += x, the rounding of the first kept in the second (Knuth's two-sum).
+__device__ __forceinline__ void add_carried(float& hi, float& lo, float x, float xlo) {
+  const float s = hi + x, t = s - hi;
+  lo += xlo + ((hi - (s - t)) + (x - t));
+  hi = s;
+}
+__device__ __forceinline__ void warp_sum_carried(float& hi, float& lo) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
+    add_carried(hi, lo, x, y);
+  }
+}
+
+// Natural logarithm of hi + lo, normal and positive, as hi + lo, to 2^-32 and a
+// few 2^-46 of it: with m in [0.7, 1.4) and s = (m - 1) / (m + 1), log m =
+// 2 (s + s^3 / 3 + s^5 / 5 + ...), |s| < 0.172; only s itself needs two floats.
+__device__ __forceinline__ void log_carried(float& hi, float& lo) {
+  int e = ((__float_as_int(hi) >> 23) & 255) - 127;
+  float m = __int_as_float((__float_as_int(hi) & 0x7fffff) | 0x3f800000);
+  if (m > 1.41421354f) {
+    m *= 0.5f;
+    ++e;
+  }
+  const float ml = lo * __int_as_float((127 - max(e, -126)) << 23);
+  const float num = m - 1.f, den = m + 1.f, dl = (1.f - (den - m)) + ml;
+  const float q = num / den;
+  const float ql = (fmaf(-q, den, num) + ml - q * dl) / den;
+  const float z = q * q;
+  float tail = 1.f / 13.f;
+  tail = fmaf(tail, z, 1.f / 11.f);
+  tail = fmaf(tail, z, 1.f / 9.f);
+  tail = fmaf(tail, z, 1.f / 7.f);
+  tail = fmaf(tail, z, 1.f / 5.f);
+  tail = fmaf(tail, z, 1.f / 3.f);
+  const float fe = (float)e, p = fe * kLn2;
+  hi = p;
+  lo = fmaf(fe, kLn2, -p) + fe * kLn2Low;
+  add_carried(hi, lo, 2.f * q, 2.f * (ql + q * z * tail));
+}
+
+// c = top log2(e) - r to float32, for the integer r next above top log2(e).
+constexpr float kNear = 1048576.f;  // float32 holds r exactly, with room for c
+__device__ __forceinline__ float fraction(float top) {
+  const float p = top * kLog2e;
+  if (fabsf(p) < kNear) return (p - ceilf(p)) + fmaf(top, kLog2eLow, fmaf(top, kLog2e, -p));
+  const double x = top * kLog2eDouble;
+  return (float)(x - ceil(x));
+}
+// r of `own` minus r of `top`, at most 0 for own <= top; below -1000 it is -1000.
+__device__ __forceinline__ int reference_shift(float own, float top) {
+  const float p = own * kLog2e, q = top * kLog2e;
+  if (fabsf(p) < kNear && fabsf(q) < kNear) return (int)fmaxf(ceilf(p) - ceilf(q), -1000.f);
+  return (int)fmax(ceil(own * kLog2eDouble) - ceil(top * kLog2eDouble), -1000.0);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Order of the values as unsigned integers; -0 counts as +0.
 __device__ __forceinline__ uint32_t sortable(float x) {
@@ -38,11 +115,36 @@ __device__ __forceinline__ uint32_t sortable(float x) {
 __device__ __forceinline__ float unsortable(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
-constexpr uint32_t kNoKey = 0x007fffffu;  // of -inf: never a candidate
 
-// A candidate: larger is better, ties to the lower index.
-__device__ __forceinline__ uint64_t candidate(uint32_t key, int index) {
-  return ((uint64_t)key << 32) | (uint32_t)~index;
+// A logit and its place: larger is better, ties to the lower index.  0 is none.
+__device__ __forceinline__ uint64_t candidate(float x, int index) {
+  return ((uint64_t)sortable(x) << 32) | (uint32_t)~index;
+}
+
+// Workspace: the pieces' sums, then their M best (0 past the last), best first.
+struct Lists {
+  PieceSum* sum;
+  uint64_t* best;
+  __device__ __forceinline__ Lists(const BeamArgs& a, int splits) {
+    sum = reinterpret_cast<PieceSum*>(a.work);
+    best = reinterpret_cast<uint64_t*>(a.work + (int64_t)a.N * a.B * splits * 4);
+  }
+};
+
+// Least maximum of `groups` (8 .. 64, a power of two) groups of the block's
+// threads, per warp: groups / 8 of them lie in each warp.
+template <typename K>
+__device__ __forceinline__ K least_group_max(K mine, int groups) {
+  const int size = 32 * kWarps / groups;
+  for (int o = 1; o < size; o <<= 1) {
+    const K x = __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = x > mine ? x : mine;
+  }
+  for (int o = size; o < 32; o <<= 1) {
+    const K x = __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = x < mine ? x : mine;
+  }
+  return mine;
 }
 
 __device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
@@ -51,323 +153,443 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-// A live beam reads its logits: its score is finite and it is not finished.
-__device__ __forceinline__ bool reads_logits(const BeamArgs& a, int64_t beam) {
-  return isfinite(__ldg(a.scores + beam)) && (a.finished == nullptr || __ldg(a.finished + beam) == 0);
-}
-
-struct Lists {
-  PieceSum* sum;
-  float* value;
-  int32_t* index;
-  __device__ __forceinline__ Lists(const BeamArgs& a, int splits) {
-    const int64_t pieces = (int64_t)a.N * a.B * splits;
-    sum = reinterpret_cast<PieceSum*>(a.work);
-    value = a.work + pieces * 4;
-    index = reinterpret_cast<int32_t*>(value + pieces * a.M);
+template <typename T>
+struct Raw;  // 16 bytes of logits as loaded
+template <>
+struct Raw<float> {
+  static constexpr int VEC = 4;
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void set(int i, const float* p) {
+    const float x = p != nullptr ? __ldg(p) : -INFINITY;
+    (i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w))) = x;
   }
+  __device__ __forceinline__ float2 pair(int i) const { return i == 0 ? make_float2(v.x, v.y) : make_float2(v.z, v.w); }
+  __device__ __forceinline__ float top() const { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  static constexpr int VEC = 8;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  }
+  __device__ __forceinline__ void set(int i, const __nv_bfloat16* p) {
+    const uint32_t x = p != nullptr ? __ldg(reinterpret_cast<const unsigned short*>(p)) : 0xff80u;
+    w[i / 2] = i % 2 == 0 ? (w[i / 2] & 0xffff0000u) | x : (w[i / 2] & 0xffffu) | (x << 16);
+  }
+  __device__ __forceinline__ float2 pair(int i) const { return make_float2(bf_lo(w[i]), bf_hi(w[i])); }
+  __device__ __forceinline__ float top() const {
+    __nv_bfloat162 m = __hmax2(__hmax2(h(0), h(1)), __hmax2(h(2), h(3)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  __device__ __forceinline__ __nv_bfloat162 h(int i) const { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); }
 };
 
-template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) kda_beam_scan_kernel(const BeamArgs a, int splits) {
-  constexpr int VEC = 16 / sizeof(T), LOADS = E / VEC;
-  static_assert(LOADS * VEC == E && LOADS >= 1, "bad shape");
-  __shared__ float s_top[kThreads / 32];
-  __shared__ double s_sum[kThreads / 32];
-  __shared__ uint32_t s_key[kThreads];
+// Groups of threads for the bound.
+__device__ __forceinline__ int bound_groups(int M) {
+  int g = kWarps;
+  while (g < M) g *= 2;
+  return g;
+}
+
+// Thread's sum of 2^(x log2(e) - r) for one batch of loads, r at least every exponent.
+template <typename T, int LOADS>
+__device__ __forceinline__ float batch_sum(const Raw<T> (&x)[LOADS], float r) {
+  const float2 hi2 = dup2(kLog2e), lo2 = dup2(kLog2eLow), r2 = dup2(-r);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j)
+#pragma unroll
+    for (int i = 0; i < Raw<T>::VEC / 2; ++i) {
+      const float2 v = x[j].pair(i);
+      const float2 e = fma2(v, lo2, fma2(v, hi2, r2));
+      sum = add2(sum, make_float2(ex2(e.x), ex2(e.y)));
+    }
+  return sum.x + sum.y;
+}
+
+template <typename T, int LOADS>
+__global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamArgs a, int splits, int batches) {
+  constexpr int VEC = Raw<T>::VEC, BATCH = LOADS * kThreads * VEC;
+  __shared__ uint32_t s_top[kWarps], s_bound[kWarps];
+  __shared__ float s_hi[kThreads], s_tops[kBatches][kThreads];
   __shared__ uint64_t s_list[kList];
-  __shared__ uint32_t s_bound;
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int split = blockIdx.x % splits;
-  const int64_t beam = blockIdx.x / splits;
+  const uint32_t beam = blockIdx.x / (uint32_t)splits;
+  const int split = blockIdx.x - beam * splits;
+  if (tid == 0) s_count = 0;
+
+  // The vectors lie on 16-byte boundaries; the row may start and end inside one.
+  const uint32_t n = beam / (uint32_t)a.B;
+  const T* row = static_cast<const T*>(a.logits) + n * a.ns + (beam - n * a.B) * a.bs;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int first = split * batches * BATCH - lead;  // of the piece
+  const int i0 = first + tid * VEC;                  // of this thread's first vector
+  const auto load = [&](int batch, Raw<T>(&x)[LOADS]) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int i = i0 + batch * BATCH + j * kThreads * VEC;
+      if (i >= 0 && i + VEC <= a.V) {
+        x[j].load(row + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[j].set(e, nullptr);
+        if (i + VEC > 0 && i < a.V) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (i + e >= 0 && i + e < a.V) x[j].set(e, row + i + e);
+        }
+      }
+    }
+  };
   pdl_wait();
   pdl_launch_dependents();
-  if (!reads_logits(a, beam)) return;
+  // A live beam reads its logits: its score is finite and it is not finished.
+  const int done = a.finished != nullptr ? __ldg(a.finished + beam) : 0;
+  if (!isfinite(__ldg(a.scores + beam)) || done != 0) return;
 
-  // The piece's vectors lie on 16-byte boundaries; the row may start and end inside one.
-  const T* row = static_cast<const T*>(a.logits) + beam / a.B * a.ns + beam % a.B * a.bs;
-  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-  float x[E];
+  // One batch is summed while the next is on its way.  The thread's reference
+  // r moves in whole steps, so rescaling its sum is exact.
+  float top = -INFINITY, r = -kNear, sum = 0.f;
+  Raw<T> x[LOADS], ahead[LOADS];
+  load(0, ahead);
+#pragma unroll 1
+  for (int k = 0; k < batches; ++k) {
 #pragma unroll
-  for (int j = 0; j < LOADS; ++j) {
-    const int64_t i0 = ((int64_t)(split * LOADS + j) * kThreads + tid) * VEC - lead;
-    if (i0 >= 0 && i0 + VEC <= a.V) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 r = __ldcs(reinterpret_cast<const float4*>(row + i0));
-        x[j * VEC] = r.x; x[j * VEC + 1] = r.y; x[j * VEC + 2] = r.z; x[j * VEC + 3] = r.w;
-      } else {
-        const uint4 r = __ldcs(reinterpret_cast<const uint4*>(row + i0));
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    for (int j = 0; j < LOADS; ++j) x[j] = ahead[j];
+    if (k + 1 < batches) load(k + 1, ahead);
+    float t = x[0].top();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[j * VEC + 2 * i] = bf_lo(w[i]);
-          x[j * VEC + 2 * i + 1] = bf_hi(w[i]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int64_t at = i0 + i;
-        x[j * VEC + i] = -INFINITY;
-        if (at >= 0 && at < a.V) {
-          if constexpr (sizeof(T) == 4) x[j * VEC + i] = __ldg(row + at);
-          else x[j * VEC + i] = __bfloat162float(__ldg(row + at));
-        }
-      }
+    for (int j = 1; j < LOADS; ++j) t = fmaxf(t, x[j].top());
+    s_tops[k][tid] = t;
+    top = fmaxf(top, t);
+    const float up = ceilf(t * kLog2e);
+    if (up > r) {
+      sum *= __int_as_float(max((int)fmaxf(r - up, -126.f) + 127, 0) << 23);
+      r = up;
     }
+    sum += batch_sum<T, LOADS>(x, r);
   }
 
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < E; ++i) top = fmaxf(top, x[i]);
-  s_key[tid] = sortable(top);
-  float wtop = top;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
-  if (lane == 0) s_top[warp] = wtop;
-  if (tid == 0) s_count = 0;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) wtop = fmaxf(wtop, s_top[w]);
-  const float ref = wtop == -INFINITY ? 0.f : wtop;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) sum += expf(x[i] - ref);
-  double total = sum;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) s_sum[warp] = total;
-
-  if (warp == 0) {  // the M-th largest of the threads' maxima
-    uint32_t k[kThreads / 32];
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) k[w] = s_key[w * 32 + lane];
-    uint32_t bound = 0;
-    for (int m = 0; m < a.M; ++m) {
-      uint32_t mine = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) mine = max(mine, k[w]);
-      bound = __reduce_max_sync(0xffffffffu, mine);
-      const int owner = __ffs(__ballot_sync(0xffffffffu, mine == bound)) - 1;
-      bool gone = lane != owner;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w)
-        if (!gone && k[w] == bound) { k[w] = 0; gone = true; }
-    }
-    if (lane == 0) s_bound = max(bound, kNoKey + 1);
+  const int groups = bound_groups(a.M);
+  const uint32_t key = sortable(top), wkey = __reduce_max_sync(0xffffffffu, key);
+  const uint32_t least = groups == kWarps ? wkey : least_group_max(key, groups);
+  if (lane == 0) {
+    s_top[warp] = wkey;
+    s_bound[warp] = least;
   }
   __syncthreads();
-  const uint32_t bound = s_bound;
-  const Lists lists(a, splits);
-  const int64_t piece = beam * splits + split;
-  if (tid == 0) {
-    double all = 0.0;
+  uint32_t lowest = s_bound[0], highest = s_top[0];
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += s_sum[w];
-    lists.sum[piece].sum = all;
-    lists.sum[piece].top = wtop;
+  for (int w = 1; w < kWarps; ++w) {
+    lowest = min(lowest, s_bound[w]);
+    highest = max(highest, s_top[w]);
   }
-  if (sortable(top) >= bound) {
+  const float bound = unsortable(lowest), all = unsortable(highest);
+  const int end = (int)min((int64_t)a.V, (int64_t)first + (int64_t)batches * BATCH);
+
+  // The few vectors that hold a candidate are read again.
+  if (top >= bound) {
+#pragma unroll 1
+    for (int k = 0; k < batches; ++k) {
+      if (!(s_tops[k][tid] >= bound)) continue;
+      load(k, x);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const uint32_t key = sortable(x[i]);
-      if (key >= bound) {
-        const int at = atomicAdd(&s_count, 1);
-        const int64_t index = ((int64_t)(split * LOADS + i / VEC) * kThreads + tid) * VEC - lead + i % VEC;
-        if (at < kList) s_list[at] = candidate(key, (int)index);
+      for (int j = 0; j < LOADS; ++j) {
+        if (!(x[j].top() >= bound)) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 p = x[j].pair(e / 2);
+          const float v = e % 2 == 0 ? p.x : p.y;
+          if (v >= bound && v > -INFINITY) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kList) s_list[at] = candidate(v, i0 + k * BATCH + j * kThreads * VEC + e);
+          }
+        }
       }
     }
   }
+  float hi, lo = 0.f;
+  if (fabsf(all) < kNear / kLog2e) {
+    const int shift = (int)fmaxf(r - ceilf(all * kLog2e), -127.f);  // r is at most the block's
+    hi = sum * __int_as_float((shift + 127) << 23);
+  } else {
+    // Logits of 10^6 and more (or none above -inf, or infinite): once more, by their distance from the largest.
+    const float base = all > -INFINITY ? all : 0.f, c = fraction(base);
+    hi = 0.f;
+    for (int i = max(first, 0) + tid; i < end; i += kThreads)
+      hi += ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c));
+  }
+  s_hi[tid] = hi;
   __syncthreads();
   const int count = s_count;
-  float* value = lists.value + piece * a.M;
-  int32_t* index = lists.index + piece * a.M;
+  const Lists lists(a, splits);
+  const int64_t piece = blockIdx.x;
+  uint64_t* best = lists.best + piece * a.M;
+  if (warp == kWarps - 1) {  // the last to have a candidate to place
+    hi = s_hi[lane];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) add_carried(hi, lo, s_hi[w * 32 + lane], 0.f);
+    warp_sum_carried(hi, lo);
+    if (lane == 0) {
+      PieceSum p;
+      p.hi = hi; p.lo = lo; p.top = all; p.pad = 0.f;
+      lists.sum[piece] = p;
+    }
+  }
   if (count <= kList) {
-    if (warp != 0) return;
-    uint64_t last = ~0ull;
-    for (int m = 0; m < a.M; ++m) {
-      uint64_t best = 0;
-      for (int i = lane; i < count; i += 32)
-        if (s_list[i] < last && s_list[i] > best) best = s_list[i];
-      last = best = warp_max64(best);
-      if (lane == 0) {
-        value[m] = best == 0 ? -INFINITY : unsortable((uint32_t)(best >> 32));
-        index[m] = best == 0 ? -1 : (int)~(uint32_t)best;
+    for (int i = tid; i < max(count, a.M); i += kThreads) {
+      if (i < count) {
+        const uint64_t mine = s_list[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) rank += s_list[j] > mine ? 1 : 0;
+        if (rank < a.M) best[rank] = mine;
+      } else {
+        best[i] = 0;
       }
     }
     return;
   }
-  // Too many equal values at the bound: take the best below the last one, M times, from the registers.
-  __shared__ uint64_t s_best[kThreads / 32];
+  // Too many equal values at the bound: M times the best below the last one, from memory again.
   uint64_t last = ~0ull;
   for (int m = 0; m < a.M; ++m) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const uint32_t key = sortable(x[i]);
-      const int64_t at = ((int64_t)(split * LOADS + i / VEC) * kThreads + tid) * VEC - lead + i % VEC;
-      const uint64_t c = candidate(key, (int)at);
-      if (key >= bound && c < last && c > best) best = c;
+    uint64_t mine = 0;
+    for (int i = max(first, 0) + tid; i < end; i += kThreads) {
+      const float v = static_cast<float>(row[i]);
+      const uint64_t at = candidate(v, i);
+      if (v >= bound && v > -INFINITY && at < last && at > mine) mine = at;
     }
-    best = warp_max64(best);
-    if (lane == 0) s_best[warp] = best;
+    mine = warp_max64(mine);
+    __syncthreads();  // the list's last readers
+    if (lane == 0) s_list[warp] = mine;
     __syncthreads();
-    best = 0;
+    mine = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) best = max(best, s_best[w]);
-    last = best;
-    if (tid == 0) {
-      value[m] = best == 0 ? -INFINITY : unsortable((uint32_t)(best >> 32));
-      index[m] = best == 0 ? -1 : (int)~(uint32_t)best;
-    }
-    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) mine = max(mine, s_list[w]);
+    last = mine;
+    if (tid == 0) best[m] = mine;
   }
 }
 
-// One request: the beams' offsets score - log sum exp, then the merge of the
-// pieces' sorted lists, one best candidate of the block a round.
+// (x - top) + (hi + lo) to about 48 bits.
+__device__ __forceinline__ uint64_t value_key(float x, float top, float hi, float lo) {
+  float s = x, rest = 0.f;
+  add_carried(s, rest, -top, 0.f);
+  add_carried(s, rest, hi, lo);
+  if (!(s >= -FLT_MAX)) return 1;  // beyond float32: the last of all
+  const float value = s + rest;
+  return ((uint64_t)sortable(value) << 32) | sortable(rest - (value - s));
+}
+
+// A continuation of any beam: larger value, then lower flat index.
+struct __align__(16) Choice {
+  uint64_t key;  // sortable(hi) and sortable(lo) of the value hi + lo, hi its float32 rounding; 0: none
+  int32_t flat;  // beam * V + token
+};
+__device__ __forceinline__ bool before(const Choice& a, const Choice& b) {
+  return (a.key > b.key) | ((a.key == b.key) & (a.flat < b.flat));
+}
+
+// One request.  Candidate i of all beams' pieces: the pieces' best ones first,
+// beams fastest; a finished beam has one, in the place of its first.  They are
+// dealt to the warps in turn, so that every group of threads sees all beams'
+// best.  The first kHeld a thread are on their way while the sums are joined.
+constexpr int kHeld = 2;
 __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs a, int splits) {
-  // A candidate is worth (x - top) + offset, offset = score - log sum exp(x - top): near the best, no large numbers cancel.
-  __shared__ double s_offset[kBeamMax];
+  // A candidate is worth (x - top) + offset, offset = score - log sum exp(x - top): no large numbers cancel.
+  __shared__ float s_hi[kBeamMax], s_lo[kBeamMax];  // the sum, then the offset
   __shared__ float s_top[kBeamMax];
-  __shared__ int s_kind[kBeamMax];  // 0: nothing, 1: lists, 2: finished
-  __shared__ double s_value[kThreads / 32];
-  __shared__ int64_t s_flat[kThreads / 32];
+  __shared__ int s_kind[kBeamMax];                  // 0: nothing, 1: lists, 2: finished
+  __shared__ uint64_t s_bound[kWarps];
+  __shared__ Choice s_list[kList];
+  __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = blockIdx.x;
+  if (tid == 0) s_count = 0;
   pdl_wait();
   pdl_launch_dependents();
   const Lists lists(a, splits);
+  const int pieces = a.B * splits, count = pieces * a.M;
+  const uint64_t* best = lists.best + n * count;
+  const auto mine_at = [&](int k) { return k * kThreads + lane * kWarps + warp; };
+  const auto fetch = [&](int i) {
+    const int m = i / pieces, l = i - m * pieces, s = l / a.B, b = l - s * a.B;
+    return best[(b * splits + s) * a.M + m];  // without meaning for a beam whose logits were not read
+  };
+  uint64_t held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = mine_at(k) < count ? fetch(mine_at(k)) : 0;
 
-  for (int b = warp; b < a.B; b += kThreads / 32) {
+  for (int b = warp; b < a.B; b += kWarps) {
     const int64_t beam = n * a.B + b;
     const float score = __ldg(a.scores + beam);
-    int kind = 0;
-    double offset = 0.0;
-    float top = -INFINITY;
-    if (isfinite(score)) {
-      if (a.finished != nullptr && __ldg(a.finished + beam) != 0) {
-        kind = 2;
-        offset = score;
-      } else {
-        const PieceSum* p = lists.sum + beam * splits;
-        for (int s = lane; s < splits; s += 32) top = fmaxf(top, p[s].top);
+    const bool done = a.finished != nullptr && __ldg(a.finished + beam) != 0;
+    float hi = 0.f, lo = 0.f, top = -INFINITY;
+    if (isfinite(score) && !done) {
+      const PieceSum* p = lists.sum + beam * splits;
+      for (int s = lane; s < splits; s += 32) top = fmaxf(top, p[s].top);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        double sum = 0.0;
-        for (int s = lane; s < splits; s += 32) {
-          const double part = p[s].sum;  // NaN if the piece holds one
-          sum += part == 0.0 ? 0.0 : part * exp((double)p[s].top - (double)top);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        offset = (double)score - log(sum);
-        kind = isfinite(offset) && isfinite(top) ? 1 : 0;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int s = lane; s < splits; s += 32) {
+        // Times 2^(r_s - r), exact; below 2^-126 it adds nothing.  A NaN in the piece is in hi.
+        const PieceSum q = p[s];
+        const int shift = q.top > -INFINITY ? reference_shift(q.top, top) : 0;
+        const float scale = shift < -126 ? 0.f : __int_as_float((127 + min(shift, 0)) << 23);
+        add_carried(hi, lo, q.hi * scale, q.lo * scale);
       }
+      warp_sum_carried(hi, lo);
     }
     if (lane == 0) {
-      s_offset[b] = offset;
+      s_hi[b] = hi;
+      s_lo[b] = lo;
       s_top[b] = top;
-      s_kind[b] = kind;
+      s_kind[b] = !isfinite(score) ? 0 : (done ? 2 : (isfinite(top) ? 1 : 0));
     }
   }
   __syncthreads();
+  if (tid < a.B && s_kind[tid] != 0) {
+    const float score = __ldg(a.scores + n * a.B + tid);
+    float hi = score, lo = 0.f;
+    if (s_kind[tid] == 1) {
+      const float top = s_top[tid], sum = s_hi[tid], up = ceilf(top * kLog2e);
+      if (fabsf(top * kLog2e) < kNear) {  // score - log(sum) - (r ln 2 - top)
+        float ln = sum, lnl = s_lo[tid];
+        log_carried(ln, lnl);
+        const float p = up * kLn2;
+        add_carried(hi, lo, top, 0.f);
+        add_carried(hi, lo, -p, -fmaf(up, kLn2, -p) - up * kLn2Low);
+        add_carried(hi, lo, -ln, -lnl);
+        if (!(sum > 0.f && isfinite(sum))) hi = NAN;
+      } else {
+        const double offset = (double)score - (log((double)sum + (double)s_lo[tid]) - (double)fraction(top) * kLn2Double);
+        hi = (float)offset;
+        lo = (float)(offset - (double)hi);
+      }
+      if (!isfinite(hi)) s_kind[tid] = 0;
+    }
+    s_hi[tid] = hi;
+    s_lo[tid] = lo;
+  }
+  __syncthreads();
 
-  // Thread t owns the lists t, t + kThreads, ...: it alone moves their `next`
-  // forward.  `head` is the best candidate its lists still hold.
-  const int count = a.B * splits;
-  PieceSum* piece = lists.sum + n * count;
-  for (int l = tid; l < count; l += kThreads) piece[l].next = 0;
-  double head = -INFINITY;
-  int64_t head_flat = INT64_MAX;
-  int head_list = -1;
-  bool stale = true;
+  const auto choice = [&](int i, uint64_t x) {
+    Choice c;
+    c.key = 0;
+    c.flat = INT32_MAX;
+    const int l = i % pieces, b = l % a.B, kind = s_kind[b];
+    if (kind == 1) {
+      if (x != 0) {
+        c.flat = b * a.V + (int)~(uint32_t)x;
+        c.key = value_key(unsortable((uint32_t)(x >> 32)), s_top[b], s_hi[b], s_lo[b]);
+      }
+    } else if (kind == 2 && i == b) {
+      c.flat = b * a.V + a.eos;
+      c.key = value_key(0.f, 0.f, s_hi[b], 0.f);
+    }
+    return c;
+  };
+  uint64_t mine = 0;
+  Choice own[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = mine_at(k);
+    own[k].key = 0;
+    if (i < count) own[k] = choice(i, held[k]);
+    mine = max(mine, own[k].key);
+  }
+  for (int k = kHeld; k * kThreads < count; ++k)
+    if (mine_at(k) < count) mine = max(mine, choice(mine_at(k), fetch(mine_at(k))).key);
+  const uint64_t least = least_group_max(mine, bound_groups(a.M));
+  if (lane == 0) s_bound[warp] = least;
+  __syncthreads();
+  uint64_t bound = s_bound[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) bound = min(bound, s_bound[w]);
+  bound = max(bound, (uint64_t)1);
+  const auto push = [&](const Choice& c) {
+    if (c.key < bound) return;
+    const int at = atomicAdd(&s_count, 1);
+    if (at < kList) s_list[at] = c;
+  };
+  if (mine >= bound) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) push(own[k]);
+    for (int k = kHeld; k * kThreads < count; ++k)
+      if (mine_at(k) < count) push(choice(mine_at(k), fetch(mine_at(k))));
+  }
+  __syncthreads();
+  const int found = s_count;
+  const auto put = [&](int m, const Choice& c) {
+    const int64_t at = n * a.M + m;
+    a.out_scores[at] = c.key <= 1 ? -INFINITY : unsortable((uint32_t)(c.key >> 32));
+    a.out_parents[at] = c.key == 0 ? -1 : c.flat / a.V;
+    a.out_tokens[at] = c.key == 0 ? -1 : c.flat % a.V;
+  };
+  if (found <= kList) {
+    for (int i = tid; i < max(found, a.M); i += kThreads) {
+      Choice c{0, 0};
+      int rank = i;
+      if (i < found) {
+        c = s_list[i];
+        rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < found; ++j) rank += before(s_list[j], c) ? 1 : 0;
+      }
+      if (rank < a.M) put(rank, c);
+    }
+    return;
+  }
+  // Too many equal values at the bound: M times the best after the last one.
+  Choice last{~0ull, -1};
   for (int m = 0; m < a.M; ++m) {
-    if (stale) {
-      head = -INFINITY;
-      head_flat = INT64_MAX;
-      for (int l = tid; l < count; l += kThreads) {
-        const int b = l / splits, next = piece[l].next;
-        if (s_kind[b] == 0 || next == a.M) continue;
-        int token = -1;
-        double v = s_offset[b];
-        if (s_kind[b] == 1) {
-          token = lists.index[(n * count + l) * a.M + next];
-          v += (double)lists.value[(n * count + l) * a.M + next] - (double)s_top[b];
-        } else if (l == b * splits && next == 0) {
-          token = a.eos;  // the one continuation of a finished beam
-        }
-        const int64_t flat = (int64_t)b * a.V + token;
-        if (token >= 0 && (v > head || (v == head && flat < head_flat))) {
-          head = v;
-          head_flat = flat;
-          head_list = l;
-        }
-      }
-      stale = false;
+    Choice c{0, INT32_MAX};
+    for (int i = tid; i < count; i += kThreads) {
+      const Choice x = choice(i, fetch(i));
+      if (x.key >= bound && before(last, x) && before(x, c)) c = x;
     }
-    double best = head;
-    int64_t flat = head_flat;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v = __shfl_xor_sync(0xffffffffu, best, o);
-      const int64_t f = __shfl_xor_sync(0xffffffffu, flat, o);
-      if (v > best || (v == best && f < flat)) {
-        best = v;
-        flat = f;
-      }
-    }
-    if (lane == 0) {
-      s_value[warp] = best;
-      s_flat[warp] = flat;
-    }
+    const uint64_t key = warp_max64(c.key);
+    const int32_t flat = (int32_t)__reduce_min_sync(0xffffffffu, c.key == key ? (unsigned)c.flat : 0xffffffffu);
     __syncthreads();
-    best = s_value[0];
-    flat = s_flat[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w)
-      if (s_value[w] > best || (s_value[w] == best && s_flat[w] < flat)) {
-        best = s_value[w];
-        flat = s_flat[w];
-      }
-    const bool none = flat == INT64_MAX;
-    if (tid == 0) {
-      const int64_t at = n * a.M + m;
-      a.out_scores[at] = none ? -INFINITY : (float)best;
-      a.out_parents[at] = none ? -1 : (int)(flat / a.V);
-      a.out_tokens[at] = none ? -1 : (int)(flat % a.V);
-    }
-    if (!none && flat == head_flat) {
-      ++piece[head_list].next;
-      stale = true;
-    }
+    if (lane == 0) s_list[warp] = Choice{key, flat};
     __syncthreads();
+    c = s_list[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w)
+      if (before(s_list[w], c)) c = s_list[w];
+    last = c;
+    if (tid == 0) put(m, c);
   }
 }
 
 template <typename T>
 cudaError_t launch_scan(const BeamArgs& a, const BeamPlan& p, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.N * a.B * p.splits)), threads(kThreads);
-  switch (p.per_thread) {
-    case 8: return launch_pdl(kda_beam_scan_kernel<T, 8>, grid, threads, 0, s, 1, a, p.splits);
-    case 16: return launch_pdl(kda_beam_scan_kernel<T, 16>, grid, threads, 0, s, 1, a, p.splits);
-    default: return launch_pdl(kda_beam_scan_kernel<T, 32>, grid, threads, 0, s, 1, a, p.splits);
-  }
+  if (p.loads == 1) return launch_pdl(kda_beam_scan_kernel<T, 1>, grid, threads, 0, s, 1, a, p.splits, p.batches);
+  return launch_pdl(kda_beam_scan_kernel<T, 4>, grid, threads, 0, s, 1, a, p.splits, p.batches);
 }
 
 }  // namespace
 
-// Logits per thread: as many as still give every SM two blocks.
-BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, int32_t sms) {
+// The longest pieces (8 batches of 4 loads a thread) that still give every SM
+// two blocks, down to one load a thread.  A row whose start is not on a 16-byte
+// boundary reaches up to vec - 1 elements further.
+BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms) {
   BeamPlan p;
-  p.per_thread = 32;
-  const int vec = dtype == KDA_DT_F32 ? 4 : 8;
-  // A row that starts inside a vector reaches up to vec - 1 elements further.
-  const auto splits = [&](int e) { return (int32_t)((V + vec - 1 + kThreads * (int64_t)e - 1) / (kThreads * (int64_t)e)); };
-  while (p.per_thread > 8 && N * B * splits(p.per_thread) < 2 * sms) p.per_thread /= 2;
-  p.splits = splits(p.per_thread);
-  p.floats = N * B * p.splits * (4 + 2 * (int64_t)M);
+  const int64_t vec = dtype == KDA_DT_F32 ? 4 : 8;
+  const auto splits = [&](int vectors, bool whole) {
+    const int64_t per = kThreads * vec * vectors;
+    return (int32_t)((V + (whole ? 0 : vec - 1) + per - 1) / per);
+  };
+  int vectors = 4 * kBatches;
+  while (vectors > 1 && N * B * splits(vectors, true) < 2 * sms) vectors /= 2;
+  p.loads = vectors >= 4 ? 4 : 1;
+  p.batches = vectors / p.loads;
+  p.splits = splits(vectors, aligned);
+  p.floats = N * B * splits(vectors, false) * (4 + 2 * (int64_t)M);
   return p;
 }
 

@@ -90,12 +90,13 @@ struct BeamArgs {
   float* work;
   int32_t N, B, V, M, eos, dtype;
 };
-// A block scans `elements` logits of one beam; `splits` blocks a beam.
+// A block scans `batches` times 256 * `loads` vectors of 16 bytes of one beam; `splits` blocks a beam.
 struct BeamPlan {
-  int32_t per_thread, splits;
+  int32_t loads, batches, splits;
   int64_t floats;
 };
-BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, int32_t sms);
+// `aligned`: every row starts on a 16-byte boundary (fewer splits; `floats` serves both).
+BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms);
 cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& p, cudaStream_t s);
 
 }  // namespace kda

@@ -391,7 +391,7 @@ kda_status kda_beam_select_workspace(int64_t requests, int32_t beams, int64_t vo
   KDA_TRY(check_beam_sizes(requests, beams, vocab, num_out));
   KDA_CHECK(dtype == KDA_F32 || dtype == KDA_BF16, KDA_ERR_INVALID_ARG, "dtype %s not accepted", dtname(dtype));
   KDA_CHECK(sm_count >= 1 && sm_count <= 4096, KDA_ERR_INVALID_ARG, "sm_count %d out of range", sm_count);
-  *floats = requests == 0 ? 0 : kda::beam_plan(requests, beams, (int32_t)vocab, num_out, dtype, sm_count).floats;
+  *floats = requests == 0 ? 0 : kda::beam_plan(requests, beams, (int32_t)vocab, num_out, dtype, false, sm_count).floats;
   return KDA_OK;
 }
 
@@ -441,7 +441,8 @@ kda_status kda_beam_select(const kda_tensor* logits, const kda_tensor* scores, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeviceInfo dev;
   KDA_TRY(current_device(st, &dev));
-  const kda::BeamPlan plan = kda::beam_plan(N, (int32_t)B, (int32_t)V, (int32_t)M, X.dtype, dev.sms);
+  const kda::BeamPlan plan =
+      kda::beam_plan(N, (int32_t)B, (int32_t)V, (int32_t)M, X.dtype, vectors_aligned(X, 16), dev.sms);
   KDA_TRY(check_grid(N * B * plan.splits));
   KDA_CHECK(W.shape[0] >= plan.floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
             (long long)W.shape[0], (long long)plan.floats);
