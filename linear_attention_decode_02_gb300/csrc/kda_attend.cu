@@ -11,6 +11,8 @@
 // registers; KB * HG partial dot products are reduced by halving exchanges
 // (NV - 1 shuffles for NV values), which leaves each lane one score to
 // exponentiate.
+#include <algorithm>
+
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -312,9 +314,7 @@ int heads_class(int G, int D) {
 template <typename T, int D, int HG>
 cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t s) {
   constexpr int KB = 32 / HG < 8 ? 32 / HG : (D == 256 ? 4 : 8);
-  cudaError_t e = launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), 0, s, 1, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kda_attend_join_kernel<D, HG>, dim3(ctas, HG), dim3(128), 0, s, 1, a, ctas);
+  return launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), 0, s, 1, a);
 }
 
 template <typename T>
@@ -335,20 +335,42 @@ cudaError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream
   }
 }
 
-}  // namespace
+template <int D>
+cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  const dim3 grid(p.ctas, p.heads), threads(128);
+  switch (p.heads) {
+    case 1: return launch_pdl(kda_attend_join_kernel<D, 1>, grid, threads, 0, s, 1, a, p.ctas);
+    case 2: return launch_pdl(kda_attend_join_kernel<D, 2>, grid, threads, 0, s, 1, a, p.ctas);
+    case 4: return launch_pdl(kda_attend_join_kernel<D, 4>, grid, threads, 0, s, 1, a, p.ctas);
+    case 8: return launch_pdl(kda_attend_join_kernel<D, 8>, grid, threads, 0, s, 1, a, p.ctas);
+    default: return launch_pdl(kda_attend_join_kernel<D, 16>, grid, threads, 0, s, 1, a, p.ctas);
+  }
+}
 
-AttendPlan attend_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
-  (void)dtype;
+AttendPlan plan_of(int32_t G, int32_t D, int32_t sms, bool tensor) {
+  if (tensor) return attend_mma_plan(G, D, sms);
   AttendPlan p;
   p.ctas = 2 * sms;
-  p.heads = heads_class(Hq / Hkv, D);
+  p.heads = heads_class(G, D);
   p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
   return p;
 }
 
+}  // namespace
+
+int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
+  const int64_t floats = plan_of(Hq / Hkv, D, sms, false).floats;
+  return dtype == KDA_DT_F32 ? floats : std::max(floats, plan_of(Hq / Hkv, D, sms, true).floats);
+}
+
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s) {
-  const AttendPlan p = attend_plan(a.Hq, a.Hkv, a.D, a.dtype, sms);
-  return a.dtype == KDA_DT_F32 ? launch_attend_d<float>(a, p, s) : launch_attend_d<__nv_bfloat16>(a, p, s);
+  const bool tensor = a.dtype == KDA_DT_BF16 && a.vec16;
+  const AttendPlan p = plan_of(a.Hq / a.Hkv, a.D, sms, tensor);
+  const cudaError_t e = tensor ? launch_attend_mma(a, p, s)
+                               : (a.dtype == KDA_DT_F32 ? launch_attend_d<float>(a, p, s)
+                                                        : launch_attend_d<__nv_bfloat16>(a, p, s));
+  if (e != cudaSuccess) return e;
+  return a.D == 64 ? launch_join<64>(a, p, s) : (a.D == 128 ? launch_join<128>(a, p, s) : launch_join<256>(a, p, s));
 }
 
 }  // namespace kda

@@ -17,6 +17,10 @@ namespace kda {
 
 constexpr int kTile = 64;  // positions of a tile
 
+// The tensor-core kernel (kda_attend_mma.cu), for bfloat16 whose vectors start on 16-byte boundaries.
+AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms);
+cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+
 // First tile of piece c.
 __device__ __forceinline__ int64_t piece_start(int64_t c, int64_t T, int C) { return c * T / C; }
 // Piece that owns tile t.

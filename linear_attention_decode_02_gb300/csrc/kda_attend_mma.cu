@@ -1,0 +1,423 @@
+// Attention of one new token per sequence over a paged bfloat16 cache, on the
+// tensor cores' warp instructions.
+//
+// Bound by memory: a key or value byte is used for at most 16 query heads, far
+// below what any of the tensor paths needs, so the kernel is built around its
+// loads.  Each warp is a pipeline of its own: it copies 16 positions a stage
+// (their page looked up one stage earlier) into shared memory, several stages
+// ahead, and meets the block's other warps only at the end of a unit.  Nothing
+// between two units waits: the copies run on into the next sequence.
+//
+// S = Q K^T with query heads as rows (16 of them) and positions as columns, so
+// that a score's lane already is the one the second product wants its weight
+// in; keys come by ldmatrix, values by its transposing form, both from rows
+// whose 16-byte chunks are XORed with the row so that no two banks meet.
+//
+// The weights p enter the second product as two bfloat16 pieces, p = hi + lo
+// to 2^-17 (hi alone would put 2^-9 of rounding into the output, as much as
+// its own type has).  With up to 8 heads hi takes rows 0..7 and lo rows 8..15,
+// which would be empty, at no cost; with 16 heads lo is a second product.
+#include "kda_attend.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kKeys = 16;  // positions of a stage
+static_assert(kWarps * kKeys == kTile, "a tile is one stage of every warp");
+
+template <int D>
+struct Shape {
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int CTAS = D == 256 ? 1 : 2;        // a SM
+  static constexpr int ROW = D * 2;                    // bytes
+  static constexpr int TENSOR = kKeys * ROW;           // bytes of a stage's keys or values
+  static constexpr int RING = kWarps * STAGES * 2 * TENSOR;
+};
+template <int D, int HG>
+constexpr int smem_bytes() {
+  return Shape<D>::RING + (kWarps - 1) * HG * D * 4;
+}
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes, or zeros where live is false (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Where a walk over the piece's tiles stands.
+struct Walk {
+  int64_t tile, unit_start, unit_end;
+  int n, group;
+  Span sp;
+  __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
+    tile = p.start;
+    n = p.n;
+    sp = span_of(a, n);
+    group = (int)((tile - p.before) / sp.tiles);
+    unit_start = p.before + (int64_t)group * sp.tiles;
+    unit_end = unit_start + sp.tiles;
+  }
+  __device__ __forceinline__ void next_unit(const AttendArgs& a, int units) {
+    unit_start = unit_end;
+    if (++group == units) {
+      group = 0;
+      if (++n < a.N) sp = span_of(a, n);
+    }
+    unit_end = unit_start + sp.tiles;
+  }
+};
+
+template <int D, int HG>
+__global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
+  using S = Shape<D>;
+  constexpr int STAGES = S::STAGES, ROW = S::ROW, TENSOR = S::TENSOR;
+  constexpr int CHUNKS = D / 8, PASS_ROWS = 32 / CHUNKS, PASSES = kKeys / PASS_ROWS;  // of a stage's copy
+  constexpr int KSTEPS = D / 16, NT = D / 8;
+  constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
+  static_assert(HG == 8 || HG == 16, "16 rows of queries");
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int64_t s_offset[kWarps][2 * kKeys];  // elements; -1: not attended to
+  __shared__ uint32_t s_live[kWarps][STAGES];
+  __shared__ float s_m[2][kWarps][HG], s_l[2][kWarps][HG];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
+  const int C = gridDim.x, c = blockIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Place place = find_place<kThreads>(a, units, c, C);
+  const Workspace ws(a.work, C, HG, D);
+  if (place.start == place.stop) {
+    if (threadIdx.x == 0) ws.note[c].n = -1;
+    return;
+  }
+
+  // ---- the warp's copies ------------------------------------------------------------------
+  char* ring = smem + warp * (STAGES * 2 * TENSOR);
+  const uint32_t ring_at = shared_address(ring);
+  const PageView& mine = lane < kKeys ? a.kp : a.vp;  // lanes 0..15 place keys, 16..31 values
+  const int64_t my_page = mine.page, my_token = mine.token, my_head = mine.head;
+  Walk load;
+  load.start(a, place);
+  int page = 0, at = 0;  // of this lane's position in the next stage to copy; page 0: none
+  const auto look_up = [&]() {
+    page = 0;
+    if (load.tile < place.stop) {
+      const int t = (load.sp.tile0 + (int)(load.tile - load.unit_start)) * kTile + warp * kKeys + (lane & (kKeys - 1));
+      if (t >= load.sp.first && t < load.sp.end) {
+        const int col = t / a.page_size;
+        at = t - col * a.page_size;
+        page = __ldg(a.table + (int64_t)load.n * a.table_rs + col);
+      }
+    }
+  };
+  const auto copy = [&](int stage) {
+    if (load.tile < place.stop) {
+      const bool live = page > 0 && page < a.num_pages;
+      const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
+      __syncwarp();
+      s_offset[warp][lane] = live ? page * my_page + at * my_token + (load.group / groups) * my_head : -1;
+      if (lane == 0) s_live[warp][stage] = mask;
+      __syncwarp();
+      const int chunk = lane % CHUNKS, row0 = lane / CHUNKS;
+      const uint32_t base = ring_at + stage * 2 * TENSOR;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const char* data = static_cast<const char*>(kv == 0 ? a.kp.data : a.vp.data);
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const int row = row0 + i * PASS_ROWS;
+          const int64_t offset = s_offset[warp][kv * kKeys + row];
+          copy16(base + kv * TENSOR + row * ROW + ((chunk ^ (row & 7)) << 4),
+                 data + (offset < 0 ? 0 : (offset + chunk * 8) * 2), offset >= 0);
+        }
+      }
+      if (++load.tile == load.unit_end) load.next_unit(a, units);
+      look_up();
+    }
+    copy_commit();
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < STAGES - 1; ++s) copy(s);
+
+  // ---- the units --------------------------------------------------------------------------
+  Walk walk;
+  walk.start(a, place);
+  int stage = 0, parity = 0;
+  while (walk.tile < place.stop) {
+    const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
+    const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + walk.n * a.q_rs + (hk * G + g0) * a.q_hs;
+    uint32_t q[KSTEPS][PAIR ? 2 : 4];
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int col = k * 16 + half * 8 + 2 * t4;
+        const auto word = [&](int h) {
+          return h < heads ? __ldg(reinterpret_cast<const uint32_t*>(qh + h * a.q_hs + col)) : 0u;
+        };
+        if constexpr (PAIR) {
+          q[k][half] = word(g);
+        } else {
+          q[k][2 * half] = word(g);
+          q[k][2 * half + 1] = word(g + 8);
+        }
+      }
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    constexpr int RS = PAIR ? 1 : 2;  // rows of heads per lane
+    float m[RS], l[RS];
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+
+    const int64_t stop = min(walk.unit_end, place.stop);
+#pragma unroll 1
+    for (; walk.tile < stop; ++walk.tile) {
+      copy_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
+      const uint32_t live = s_live[warp][stage];
+      copy(stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t keys = ring_at + stage * 2 * TENSOR, values = keys + TENSOR;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+
+      float s[2][2][4] = {};  // [even / odd step][positions 0..7 / 8..15]
+      {
+        const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        const uint32_t base = keys + row * ROW;
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) {
+          uint32_t b[4];
+          ldmatrix4(b, base + (((k * 2 + half) ^ (row & 7)) << 4));
+          if constexpr (PAIR) {
+            mma(s[k & 1][0], q[k][0], 0u, q[k][1], 0u, b[0], b[1]);
+            mma(s[k & 1][1], q[k][0], 0u, q[k][1], 0u, b[2], b[3]);
+          } else {
+            mma(s[k & 1][0], q[k][0], q[k][1], q[k][2], q[k][3], b[0], b[1]);
+            mma(s[k & 1][1], q[k][0], q[k][1], q[k][2], q[k][3], b[2], b[3]);
+          }
+        }
+      }
+      float p[RS][4];  // this lane's positions 2 t4, + 1, + 8, + 9
+      bool rises = false;
+      float ref[RS], fall[RS];
+#pragma unroll
+      for (int r = 0; r < RS; ++r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[r][j] = (s[0][j >> 1][2 * r + (j & 1)] + s[1][j >> 1][2 * r + (j & 1)]) * a.scale_log2;
+        if (live != 0xffffu) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!(live >> ((j >> 1) * 8 + 2 * t4 + (j & 1)) & 1)) p[r][j] = -INFINITY;
+        }
+        float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = fmaxf(top, m[r]);
+        ref[r] = top == -INFINITY ? 0.f : top;
+        fall[r] = ex2(m[r] - ref[r]);
+        rises = rises || top > m[r];
+        m[r] = top;
+      }
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int r = 0; r < RS; ++r) l[r] *= fall[r];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          o[i][0] *= fall[0];
+          o[i][1] *= fall[0];
+          o[i][2] *= fall[RS - 1];
+          o[i][3] *= fall[RS - 1];
+        }
+      }
+      uint32_t hi[RS][2], lo[RS][2];
+#pragma unroll
+      for (int r = 0; r < RS; ++r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[r][j] = ex2(p[r][j] - ref[r]);
+        l[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          hi[r][j] = pack_bf2(p[r][2 * j], p[r][2 * j + 1]);
+          lo[r][j] = pack_bf2(p[r][2 * j] - bf_lo(hi[r][j]), p[r][2 * j + 1] - bf_hi(hi[r][j]));
+        }
+      }
+      {
+        const int row = lane & 15, half = lane >> 4;
+        const uint32_t base = values + row * ROW;
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, base + (((k * 2 + half) ^ (row & 7)) << 4));
+          if constexpr (PAIR) {
+            mma(o[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[0], b[1]);
+            mma(o[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2], b[3]);
+          } else {
+            mma(o[2 * k], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[0], b[1]);
+            mma(o[2 * k + 1], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[2], b[3]);
+            mma(o[2 * k], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[0], b[1]);
+            mma(o[2 * k + 1], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[2], b[3]);
+          }
+        }
+      }
+    }
+
+    // ---- the unit's end in this piece: join the warps -----------------------------------------
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t4 == 0) {
+        s_m[parity][warp][g + 8 * r] = m[r];
+        s_l[parity][warp][g + 8 * r] = l[r];
+      }
+    }
+    __syncthreads();  // warp 0 has left the last unit's outputs too
+    float M[RS], f[RS];
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      M[r] = s_m[parity][0][g + 8 * r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[parity][w][g + 8 * r]);
+      f[r] = ex2(m[r] - (M[r] == -INFINITY ? 0.f : M[r]));
+    }
+    float* shared_o = reinterpret_cast<float*>(smem + S::RING);
+    if (warp != 0) {
+      float* dst = shared_o + (warp - 1) * HG * D;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int d = i * 8 + 2 * t4;
+        if constexpr (PAIR) {
+          *reinterpret_cast<float2*>(dst + g * D + d) = make_float2((o[i][0] + o[i][2]) * f[0], (o[i][1] + o[i][3]) * f[0]);
+        } else {
+          *reinterpret_cast<float2*>(dst + g * D + d) = make_float2(o[i][0] * f[0], o[i][1] * f[0]);
+          *reinterpret_cast<float2*>(dst + (g + 8) * D + d) = make_float2(o[i][2] * f[RS - 1], o[i][3] * f[RS - 1]);
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
+    const bool at_start = walk.unit_start <= place.start;
+    if (warp == 0) {
+      const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
+#pragma unroll
+      for (int r = 0; r < RS; ++r) {
+        const int h = g + 8 * r;
+        const float ref = M[r] == -INFINITY ? 0.f : M[r];
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) L = fmaf(ex2(s_m[parity][w][h] - ref), s_l[parity][w][h], L);
+        if (h < heads) {
+          const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
+          const float scale = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int d = i * 8 + 2 * t4;
+            float x = PAIR ? (o[i][0] + o[i][2]) * f[0] : o[i][2 * r] * f[r];
+            float y = PAIR ? (o[i][1] + o[i][3]) * f[0] : o[i][2 * r + 1] * f[r];
+#pragma unroll
+            for (int w = 0; w < kWarps - 1; ++w) {
+              const float2 v = *reinterpret_cast<const float2*>(shared_o + (w * HG + h) * D + d);
+              x += v.x;
+              y += v.y;
+            }
+            if (whole) {
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
+            } else {
+              *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
+            }
+          }
+          if (t4 == 0) {
+            if (!whole) {
+              ws.ml_of(slot, h)[0] = M[r];
+              ws.ml_of(slot, h)[1] = L;
+            } else if (a.lse != nullptr) {
+              a.lse[head] = log_sum(ref, L);
+            }
+          }
+        }
+      }
+      if (lane == 0 && at_start) {
+        PieceNote note;
+        note.unit_start = walk.unit_start; note.unit_end = walk.unit_end; note.tiles = place.T;
+        note.n = walk.unit_start < place.start ? walk.n : -1;
+        note.group = walk.group;
+        ws.note[c] = note;
+      }
+    }
+    parity ^= 1;
+    if (walk.tile == walk.unit_end) walk.next_unit(a, units);
+  }
+  copy_wait<0>();
+}
+
+template <int D, int HG>
+cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  constexpr int bytes = smem_bytes<D, HG>();
+  const cudaError_t e = cudaFuncSetAttribute(kda_attend_mma_kernel<D, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kda_attend_mma_kernel<D, HG>, dim3(p.ctas), dim3(kThreads), bytes, s, 1, a);
+}
+
+}  // namespace
+
+AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms) {
+  AttendPlan p;
+  p.ctas = (D == 256 ? Shape<256>::CTAS : Shape<128>::CTAS) * sms;
+  // 16 heads of 256 channels would not leave the registers for their outputs.
+  p.heads = G <= 8 || D == 256 ? 8 : 16;
+  p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
+  return p;
+}
+
+cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  switch (a.D * 16 + p.heads - 1) {
+    case 64 * 16 + 7: return launch<64, 8>(a, p, s);
+    case 64 * 16 + 15: return launch<64, 16>(a, p, s);
+    case 128 * 16 + 7: return launch<128, 8>(a, p, s);
+    case 128 * 16 + 15: return launch<128, 16>(a, p, s);
+    case 256 * 16 + 7: return launch<256, 8>(a, p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kda

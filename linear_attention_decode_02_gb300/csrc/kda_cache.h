@@ -63,7 +63,7 @@ struct AttendArgs {
   const int32_t* lens;                    // [N]
   void* out;                              // bf16 [N, Hq, D] contiguous
   float* lse;                             // [N, Hq] contiguous, or null
-  float* work;                            // attend_plan().floats
+  float* work;                            // attend_floats()
   int32_t N, Hq, Hkv, D, dtype;
   int32_t window;                         // 0: all
   float scale_log2;                       // scale * log2(e)
@@ -76,7 +76,8 @@ struct AttendPlan {
   int32_t ctas, heads;
   int64_t floats;
 };
-AttendPlan attend_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
+// Floats of workspace for either kernel that may serve the dtype.
+int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
 
 // Beam selection over beams x vocabulary.

@@ -314,7 +314,7 @@ kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int3
   KDA_TRY(check_attention_heads(q_heads, kv_heads, head_dim));
   KDA_CHECK(dtype == KDA_F32 || dtype == KDA_BF16, KDA_ERR_INVALID_ARG, "dtype %s not accepted", dtname(dtype));
   KDA_CHECK(sm_count >= 1 && sm_count <= 4096, KDA_ERR_INVALID_ARG, "sm_count %d out of range", sm_count);
-  *floats = kda::attend_plan(q_heads, kv_heads, head_dim, dtype, sm_count).floats;
+  *floats = kda::attend_floats(q_heads, kv_heads, head_dim, dtype, sm_count);
   return KDA_OK;
 }
 
@@ -366,9 +366,9 @@ kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_p
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeviceInfo dev;
   KDA_TRY(current_device(st, &dev));
-  const kda::AttendPlan plan = kda::attend_plan((int32_t)Hq, (int32_t)Hkv, (int32_t)D, KP.dtype, dev.sms);
-  KDA_CHECK(W.shape[0] >= plan.floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
-            (long long)W.shape[0], (long long)plan.floats);
+  const int64_t floats = kda::attend_floats((int32_t)Hq, (int32_t)Hkv, (int32_t)D, KP.dtype, dev.sms);
+  KDA_CHECK(W.shape[0] >= floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
+            (long long)W.shape[0], (long long)floats);
   kda::AttendArgs a{};
   a.q = Q.data; a.q_rs = Q.stride[0]; a.q_hs = Q.stride[1];
   a.kp = page_view(KP); a.vp = page_view(VP);
