@@ -7,10 +7,15 @@
 // scale * log2(e).
 //
 // A warp takes KB positions at a time.  Its lanes hold D/32 channels each, so
-// a key or value vector is one coalesced load, reused by HG query heads from
+// a key or value vector is one coalesced access, reused by HG query heads from
 // registers; KB * HG partial dot products are reduced by halving exchanges
 // (NV - 1 shuffles for NV values), which leaves each lane one score to
 // exponentiate.
+//
+// float32: each warp copies its positions into a ring of shared-memory stages
+// ahead of their use, as the tensor-core kernel does; bound by memory.
+// bfloat16 comes here only with vectors off the 16-byte boundaries those
+// copies need, and is loaded straight to registers.
 #include <algorithm>
 
 #include "kda_attend.cuh"
@@ -49,6 +54,20 @@ __device__ __forceinline__ void load_lane(const T* p, float (&x)[VEC]) {
   }
 }
 
+template <int VEC>
+__device__ __forceinline__ void read_lane(const float* p, float (&x)[VEC]) {
+  if constexpr (VEC == 2) {
+    const float2 r = *reinterpret_cast<const float2*>(p);
+    x[0] = r.x; x[1] = r.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 r = *reinterpret_cast<const float4*>(p + i);
+      x[i] = r.x; x[i + 1] = r.y; x[i + 2] = r.z; x[i + 3] = r.w;
+    }
+  }
+}
+
 // Sums NV values over the warp; lane l returns value l / (32 / NV).
 template <int NV>
 __device__ __forceinline__ float reduce_scatter(float (&x)[NV], int lane) {
@@ -69,13 +88,30 @@ __device__ __forceinline__ float reduce_scatter(float (&x)[NV], int lane) {
   return r;
 }
 
+// Blocks a SM: two, where their rings and the joining of their warps fit in shared memory.
+constexpr int blocks_per_sm(bool ring, int D, int heads) { return ring && (D > 64 || heads == 8) ? 1 : 2; }
+
+template <typename T, int D, int HG>
+struct Stage {
+  static constexpr bool RING = sizeof(T) == 4;
+  static constexpr int KEYS = RING && D == 256 ? 4 : kWarpKeys;  // positions of a stage
+  static constexpr int CTAS = blocks_per_sm(RING, D, HG);
+  static constexpr int STAGES = CTAS == 1 && D == 64 ? 6 : 3;    // 192 KB a SM
+  using Copies = PageCopies<T, D, KEYS, STAGES, kWarps, false>;
+  static constexpr int BYTES = RING ? kWarps * Copies::RING : 0;
+};
+
 template <typename T, int D, int HG, int KB>
-__global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, Stage<T, D, HG>::CTAS) kda_attend_kernel(const __grid_constant__ AttendArgs a) {
+  using St = Stage<T, D, HG>;
+  using Copies = typename St::Copies;
   constexpr int VEC = D / 32, NV = HG * KB, REP = 32 / NV;
-  static_assert(NV <= 32 && kWarpKeys % KB == 0, "bad shape");
+  static_assert(NV <= 32 && St::KEYS % KB == 0, "bad shape");
+  extern __shared__ __align__(128) char smem[];
   __shared__ float s_p[kWarps][32];
   __shared__ float s_m[kWarps][HG], s_l[kWarps][HG];
   __shared__ float s_o[kWarps][HG * D];
+  __shared__ typename Copies::Notes s_notes[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
   const int C = gridDim.x, c = blockIdx.x;
@@ -87,15 +123,19 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_co
     if (threadIdx.x == 0) ws.note[c].n = -1;
     return;
   }
-  int n = place.n;
-  Span sp = span_of(a, n);
-  int64_t unit_start = place.before + (place.start - place.before) / sp.tiles * sp.tiles;
-  int group = (int)((unit_start - place.before) / sp.tiles);
+  char* ring = smem + warp * Copies::RING;
+  Copies copies(a, place, s_notes[warp], ring, units, groups, warp, lane);
+  if constexpr (St::RING) {
+#pragma unroll 1
+    for (int s = 0; s < St::STAGES - 1; ++s) copies.copy(s);
+  }
+  Walk walk;
+  walk.start(a, place);
+  int stage = 0;
 
-  for (int64_t tile = place.start; tile < place.stop;) {
-    const int hk = group / groups, g0 = (group - hk * groups) * HG, heads = min(HG, G - g0);
-    const int64_t unit_end = unit_start + sp.tiles;
-    const int64_t stop = min(unit_end, place.stop);
+  while (walk.tile < place.stop) {
+    const int n = walk.n, hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
+    const int64_t stop = min(walk.unit_end, place.stop);
     float q[HG][VEC], o[HG][VEC];
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
@@ -108,79 +148,104 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_co
       }
     }
     float m = -INFINITY, l = 0.f;  // of this lane's head (lane / REP) % HG
-    const int32_t* row = a.table + (int64_t)n * a.table_rs;
-    for (; tile < stop; ++tile) {
-      // Lanes 0 .. kWarpKeys-1 look up one position each.
-      const int t0 = (sp.tile0 + (int)(tile - unit_start)) * kTile + warp * kWarpKeys;
-      int64_t ko = -1, vo = 0;
-      if (lane < kWarpKeys) {
-        const int t = t0 + lane;
-        if (t >= sp.first && t < sp.end) {
-          const int col = t / a.page_size, at = t - col * a.page_size;
-          const int page = __ldg(row + col);
-          if (page > 0 && page < a.num_pages) {
-            ko = page * a.kp.page + at * a.kp.token + hk * a.kp.head;
-            vo = page * a.vp.page + at * a.vp.token + hk * a.vp.head;
-          }
+
+    // KB positions whose keys and values `fetch(j, k, v)` gives, those in `live` attended to.
+    const auto attend = [&](uint32_t live, const auto& fetch) {
+      float k[KB][VEC], v[KB][VEC], s[NV];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) fetch(j, k[j], v[j]);
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          float d = 0.f;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) d = fmaf(q[h][i], k[j][i], d);
+          s[j * HG + h] = d;
+        }
+      float score = reduce_scatter<NV>(s, lane);
+      if (!(live >> (lane / REP / HG) & 1)) score = -INFINITY;
+      float top = fmaxf(m, score);
+#pragma unroll
+      for (int x = HG * REP; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float p = exp2f(score - ref);
+      if (__any_sync(0xffffffffu, top > m)) {
+        const float fall = exp2f(m - ref);
+        l *= fall;
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float f = __shfl_sync(0xffffffffu, fall, h * REP);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o[h][i] *= f;
+        }
+        m = top;
+      }
+      l += p;
+      if (lane % REP == 0) s_p[warp][lane / REP] = p;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float w = s_p[warp][j * HG + h];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o[h][i] = fmaf(w, v[j][i], o[h][i]);
+        }
+      __syncwarp();
+    };
+
+    if constexpr (St::RING) {
+#pragma unroll 1
+      for (; walk.tile < stop; ++walk.tile) {
+#pragma unroll 1
+        for (int sub = 0; sub < Copies::SUBS; ++sub) {
+          copy_wait<St::STAGES - 2>();
+          __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
+          const uint32_t live = s_notes[warp].live[stage];
+          copies.copy(stage == 0 ? St::STAGES - 1 : stage - 1);
+          const T* keys = reinterpret_cast<const T*>(ring + stage * Copies::STAGE) + lane * VEC;
+          const T* values = keys + Copies::TENSOR / sizeof(T);
+          stage = stage + 1 == St::STAGES ? 0 : stage + 1;
+#pragma unroll
+          for (int b = 0; b < St::KEYS; b += KB)
+            attend(live >> b, [&](int j, float(&k)[VEC], float(&v)[VEC]) {
+              read_lane<VEC>(keys + (b + j) * D, k);
+              read_lane<VEC>(values + (b + j) * D, v);
+            });
         }
       }
-#pragma unroll
-      for (int b = 0; b < kWarpKeys; b += KB) {
-        float k[KB][VEC], v[KB][VEC], s[NV];
-        bool live[KB];
-#pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          const int64_t kj = __shfl_sync(0xffffffffu, ko, b + j), vj = __shfl_sync(0xffffffffu, vo, b + j);
-          live[j] = kj >= 0;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) k[j][i] = v[j][i] = 0.f;
-          if (live[j]) {
-            load_lane<T, VEC>(static_cast<const T*>(a.kp.data) + kj + lane * VEC, k[j]);
-            load_lane<T, VEC>(static_cast<const T*>(a.vp.data) + vj + lane * VEC, v[j]);
+    } else {
+#pragma unroll 1
+      for (; walk.tile < stop; ++walk.tile) {
+        // Lanes 0 .. kWarpKeys-1 look up one position each.
+        const int t0 = (walk.sp.tile0 + (int)(walk.tile - walk.unit_start)) * kTile + warp * kWarpKeys;
+        int64_t ko = 0, vo = 0;
+        bool found = false;
+        if (lane < kWarpKeys) {
+          const int t = t0 + lane;
+          if (t >= walk.sp.first && t < walk.sp.end) {
+            const int col = t / a.page_size, at = t - col * a.page_size;
+            const int page = __ldg(a.table + (int64_t)n * a.table_rs + col);
+            if (page > 0 && page < a.num_pages) {
+              ko = page * a.kp.page + at * a.kp.token + hk * a.kp.head;
+              vo = page * a.vp.page + at * a.vp.token + hk * a.vp.head;
+              found = true;
+            }
           }
         }
+        const uint32_t live = __ballot_sync(0xffffffffu, found);
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
+        for (int b = 0; b < kWarpKeys; b += KB)
+          attend(live >> b, [&](int j, float(&k)[VEC], float(&v)[VEC]) {
+            const int64_t kj = __shfl_sync(0xffffffffu, ko, b + j), vj = __shfl_sync(0xffffffffu, vo, b + j);
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            float d = 0.f;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) d = fmaf(q[h][i], k[j][i], d);
-            s[j * HG + h] = d;
-          }
-        float score = reduce_scatter<NV>(s, lane);
-        const int mine = lane / REP / HG;  // this lane's position in the batch
-#pragma unroll
-        for (int j = 0; j < KB; ++j)
-          if (mine == j && !live[j]) score = -INFINITY;
-        float top = fmaxf(m, score);
-#pragma unroll
-        for (int x = HG * REP; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float p = exp2f(score - ref);
-        if (__any_sync(0xffffffffu, top > m)) {
-          const float fall = exp2f(m - ref);
-          l *= fall;
-#pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const float f = __shfl_sync(0xffffffffu, fall, h * REP);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[h][i] *= f;
-          }
-          m = top;
-        }
-        l += p;
-        if (lane % REP == 0) s_p[warp][lane / REP] = p;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < KB; ++j)
-#pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const float w = s_p[warp][j * HG + h];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[h][i] = fmaf(w, v[j][i], o[h][i]);
-          }
-        __syncwarp();
+            for (int i = 0; i < VEC; ++i) k[i] = v[i] = 0.f;
+            if (live >> (b + j) & 1) {
+              load_lane<T, VEC>(static_cast<const T*>(a.kp.data) + kj + lane * VEC, k);
+              load_lane<T, VEC>(static_cast<const T*>(a.vp.data) + vj + lane * VEC, v);
+            }
+          });
       }
     }
 #pragma unroll
@@ -195,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_co
       for (int i = 0; i < VEC; ++i) s_o[warp][h * D + lane * VEC + i] = o[h][i];
     __syncthreads();
 
-    const bool whole = unit_start >= place.start && unit_end <= place.stop;
-    const bool at_start = unit_start <= place.start;
+    const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
+    const bool at_start = walk.unit_start <= place.start;
     const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
       const int h = i / D, d = i - h * D;
@@ -222,22 +287,11 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attend_kernel(const __grid_co
         }
       }
     }
-    if (threadIdx.x == 0 && at_start) {
-      PieceNote note;
-      note.unit_start = unit_start; note.unit_end = unit_end; note.tiles = place.T;
-      note.n = unit_start < place.start ? n : -1;
-      note.group = group;
-      ws.note[c] = note;
-    }
+    if (threadIdx.x == 0 && at_start) ws.note[c] = note_of(walk, place);
     __syncthreads();
-    if (tile == unit_end) {
-      unit_start = unit_end;
-      if (++group == units) {
-        group = 0;
-        if (++n < a.N) sp = span_of(a, n);
-      }
-    }
+    if (walk.tile == walk.unit_end) walk.next_unit(a, units);
   }
+  copy_wait<0>();
 }
 
 // Joins the partials of one query head of the unit that the cut before piece
@@ -314,7 +368,11 @@ int heads_class(int G, int D) {
 template <typename T, int D, int HG>
 cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t s) {
   constexpr int KB = 32 / HG < 8 ? 32 / HG : (D == 256 ? 4 : 8);
-  return launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), 0, s, 1, a);
+  constexpr int bytes = Stage<T, D, HG>::BYTES;
+  static std::atomic<bool> set[64];
+  const cudaError_t e = ensure_smem(kda_attend_kernel<T, D, HG, KB>, bytes, set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), bytes, s, 1, a);
 }
 
 template <typename T>
@@ -347,11 +405,11 @@ cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, cudaStream_t s
   }
 }
 
-AttendPlan plan_of(int32_t G, int32_t D, int32_t sms, bool tensor) {
+AttendPlan plan_of(int32_t G, int32_t D, int32_t dtype, int32_t sms, bool tensor) {
   if (tensor) return attend_mma_plan(G, D, sms);
   AttendPlan p;
-  p.ctas = 2 * sms;
   p.heads = heads_class(G, D);
+  p.ctas = blocks_per_sm(dtype == KDA_DT_F32, D, p.heads) * sms;
   p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
   return p;
 }
@@ -359,13 +417,13 @@ AttendPlan plan_of(int32_t G, int32_t D, int32_t sms, bool tensor) {
 }  // namespace
 
 int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
-  const int64_t floats = plan_of(Hq / Hkv, D, sms, false).floats;
-  return dtype == KDA_DT_F32 ? floats : std::max(floats, plan_of(Hq / Hkv, D, sms, true).floats);
+  const int64_t floats = plan_of(Hq / Hkv, D, dtype, sms, false).floats;
+  return dtype == KDA_DT_F32 ? floats : std::max(floats, plan_of(Hq / Hkv, D, dtype, sms, true).floats);
 }
 
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s) {
   const bool tensor = a.dtype == KDA_DT_BF16 && a.vec16;
-  const AttendPlan p = plan_of(a.Hq / a.Hkv, a.D, sms, tensor);
+  const AttendPlan p = plan_of(a.Hq / a.Hkv, a.D, a.dtype, sms, tensor);
   const cudaError_t e = tensor ? launch_attend_mma(a, p, s)
                                : (a.dtype == KDA_DT_F32 ? launch_attend_d<float>(a, p, s)
                                                         : launch_attend_d<__nv_bfloat16>(a, p, s));

@@ -122,4 +122,127 @@ __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// Where a walk over the piece's tiles stands.
+struct Walk {
+  int64_t tile, unit_start, unit_end;
+  int n, group;
+  Span sp;
+  __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
+    tile = p.start;
+    n = p.n;
+    sp = span_of(a, n);
+    group = (int)((tile - p.before) / sp.tiles);
+    unit_start = p.before + (int64_t)group * sp.tiles;
+    unit_end = unit_start + sp.tiles;
+  }
+  __device__ __forceinline__ void next_unit(const AttendArgs& a, int units) {
+    unit_start = unit_end;
+    if (++group == units) {
+      group = 0;
+      if (++n < a.N) sp = span_of(a, n);
+    }
+    unit_end = unit_start + sp.tiles;
+  }
+};
+
+__device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
+  PieceNote note;
+  note.unit_start = w.unit_start; note.unit_end = w.unit_end; note.tiles = p.T;
+  note.n = w.unit_start < p.start ? w.n : -1;
+  note.group = w.group;
+  return note;
+}
+
+// 16 bytes to shared memory, or zeros where live is false (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One warp's copies of keys and values into its ring of stages, KEYS positions
+// each.  A block of WARPS warps shares a tile; a warp's part of it is SUBS
+// stages.  The pages of a stage are looked up while the stage before it is
+// issued, so the table's latency is not in the way.  Positions not attended to
+// become zeros.  SWIZZLE puts 16-byte chunk c of row r at c ^ (r & 7).
+template <typename T, int D, int KEYS, int STAGES, int WARPS, bool SWIZZLE>
+struct PageCopies {
+  static constexpr int SUBS = kTile / WARPS / KEYS;
+  static constexpr int ROW = D * (int)sizeof(T);
+  static constexpr int TENSOR = KEYS * ROW;
+  static constexpr int STAGE = 2 * TENSOR;
+  static constexpr int RING = STAGES * STAGE;  // bytes of a warp
+  static constexpr int CHUNKS = ROW / 16;
+  static_assert(SUBS >= 1 && SUBS * KEYS * WARPS == kTile && 2 * KEYS <= 32 && KEYS * CHUNKS % 32 == 0, "bad shape");
+  struct Notes {
+    int64_t offset[2 * KEYS];  // elements; -1: not attended to
+    uint32_t live[STAGES];
+  };
+
+  const AttendArgs& a;
+  const Place& place;
+  Notes& notes;
+  uint32_t ring;
+  int units, groups, warp, lane;
+  int64_t page_stride, token_stride, head_stride;  // of keys for the first KEYS lanes, of values for the next
+  Walk at;
+  int sub, page, token;  // page 0: none
+
+  __device__ __forceinline__ PageCopies(const AttendArgs& a_, const Place& p, Notes& n, const void* ring_, int units_,
+                                        int groups_, int warp_, int lane_)
+      : a(a_), place(p), notes(n), ring(static_cast<uint32_t>(__cvta_generic_to_shared(ring_))), units(units_),
+        groups(groups_), warp(warp_), lane(lane_), sub(0), page(0), token(0) {
+    const PageView& mine = lane < KEYS ? a.kp : a.vp;
+    page_stride = mine.page;
+    token_stride = mine.token;
+    head_stride = mine.head;
+    at.start(a, place);
+    look_up();
+  }
+  __device__ __forceinline__ void look_up() {
+    page = 0;
+    if (at.tile < place.stop && lane < 2 * KEYS) {
+      const int t = (at.sp.tile0 + (int)(at.tile - at.unit_start)) * kTile + (warp * SUBS + sub) * KEYS + lane % KEYS;
+      if (t >= at.sp.first && t < at.sp.end) {
+        const int col = t / a.page_size;
+        token = t - col * a.page_size;
+        page = __ldg(a.table + (int64_t)at.n * a.table_rs + col);
+      }
+    }
+  }
+  // Copies the next stage's positions to `stage` and closes a copy group, empty at the end of the piece.
+  __device__ __forceinline__ void copy(int stage) {
+    if (at.tile < place.stop) {
+      const bool live = page > 0 && page < a.num_pages;
+      const uint32_t mask = __ballot_sync(0xffffffffu, live) & ((1u << KEYS) - 1);
+      __syncwarp();
+      if (lane < 2 * KEYS)
+        notes.offset[lane] =
+            live ? page * page_stride + token * token_stride + (at.group / groups) * head_stride : -1;
+      if (lane == 0) notes.live[stage] = mask;
+      __syncwarp();
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const char* data = static_cast<const char*>(kv == 0 ? a.kp.data : a.vp.data);
+#pragma unroll
+        for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
+          const int row = (i * 32 + lane) / CHUNKS, chunk = (i * 32 + lane) % CHUNKS;
+          const int64_t offset = notes.offset[kv * KEYS + row];
+          copy16(ring + stage * STAGE + kv * TENSOR + row * ROW + ((SWIZZLE ? chunk ^ (row & 7) : chunk) << 4),
+                 data + (offset < 0 ? 0 : offset * (int)sizeof(T) + chunk * 16), offset >= 0);
+        }
+      }
+      if (++sub == SUBS) {
+        sub = 0;
+        if (++at.tile == at.unit_end) at.next_unit(a, units);
+      }
+      look_up();
+    }
+    copy_commit();
+  }
+};
+
 }  // namespace kda

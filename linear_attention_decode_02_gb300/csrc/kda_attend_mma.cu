@@ -29,28 +29,14 @@ static_assert(kWarps * kKeys == kTile, "a tile is one stage of every warp");
 template <int D>
 struct Shape {
   static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int CTAS = D == 256 ? 1 : 2;        // a SM
-  static constexpr int ROW = D * 2;                    // bytes
-  static constexpr int TENSOR = kKeys * ROW;           // bytes of a stage's keys or values
-  static constexpr int RING = kWarps * STAGES * 2 * TENSOR;
+  static constexpr int CTAS = D == 256 ? 1 : 2;  // a SM
+  using Copies = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true>;
 };
 template <int D, int HG>
 constexpr int smem_bytes() {
-  return Shape<D>::RING + (kWarps - 1) * HG * D * 4;
+  return kWarps * Shape<D>::Copies::RING + (kWarps - 1) * HG * D * 4;
 }
 
-__device__ __forceinline__ uint32_t shared_address(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes, or zeros where live is false (src is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -77,40 +63,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Where a walk over the piece's tiles stands.
-struct Walk {
-  int64_t tile, unit_start, unit_end;
-  int n, group;
-  Span sp;
-  __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
-    tile = p.start;
-    n = p.n;
-    sp = span_of(a, n);
-    group = (int)((tile - p.before) / sp.tiles);
-    unit_start = p.before + (int64_t)group * sp.tiles;
-    unit_end = unit_start + sp.tiles;
-  }
-  __device__ __forceinline__ void next_unit(const AttendArgs& a, int units) {
-    unit_start = unit_end;
-    if (++group == units) {
-      group = 0;
-      if (++n < a.N) sp = span_of(a, n);
-    }
-    unit_end = unit_start + sp.tiles;
-  }
-};
-
 template <int D, int HG>
 __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
-  using S = Shape<D>;
-  constexpr int STAGES = S::STAGES, ROW = S::ROW, TENSOR = S::TENSOR;
-  constexpr int CHUNKS = D / 8, PASS_ROWS = 32 / CHUNKS, PASSES = kKeys / PASS_ROWS;  // of a stage's copy
+  using Copies = typename Shape<D>::Copies;
+  constexpr int STAGES = Shape<D>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 16, NT = D / 8;
   constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
   static_assert(HG == 8 || HG == 16, "16 rows of queries");
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t s_offset[kWarps][2 * kKeys];  // elements; -1: not attended to
-  __shared__ uint32_t s_live[kWarps][STAGES];
+  __shared__ typename Copies::Notes s_notes[kWarps];
   __shared__ float s_m[2][kWarps][HG], s_l[2][kWarps][HG];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -125,56 +86,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
     return;
   }
 
-  // ---- the warp's copies ------------------------------------------------------------------
-  char* ring = smem + warp * (STAGES * 2 * TENSOR);
-  const uint32_t ring_at = shared_address(ring);
-  const PageView& mine = lane < kKeys ? a.kp : a.vp;  // lanes 0..15 place keys, 16..31 values
-  const int64_t my_page = mine.page, my_token = mine.token, my_head = mine.head;
-  Walk load;
-  load.start(a, place);
-  int page = 0, at = 0;  // of this lane's position in the next stage to copy; page 0: none
-  const auto look_up = [&]() {
-    page = 0;
-    if (load.tile < place.stop) {
-      const int t = (load.sp.tile0 + (int)(load.tile - load.unit_start)) * kTile + warp * kKeys + (lane & (kKeys - 1));
-      if (t >= load.sp.first && t < load.sp.end) {
-        const int col = t / a.page_size;
-        at = t - col * a.page_size;
-        page = __ldg(a.table + (int64_t)load.n * a.table_rs + col);
-      }
-    }
-  };
-  const auto copy = [&](int stage) {
-    if (load.tile < place.stop) {
-      const bool live = page > 0 && page < a.num_pages;
-      const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
-      __syncwarp();
-      s_offset[warp][lane] = live ? page * my_page + at * my_token + (load.group / groups) * my_head : -1;
-      if (lane == 0) s_live[warp][stage] = mask;
-      __syncwarp();
-      const int chunk = lane % CHUNKS, row0 = lane / CHUNKS;
-      const uint32_t base = ring_at + stage * 2 * TENSOR;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const char* data = static_cast<const char*>(kv == 0 ? a.kp.data : a.vp.data);
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-          const int row = row0 + i * PASS_ROWS;
-          const int64_t offset = s_offset[warp][kv * kKeys + row];
-          copy16(base + kv * TENSOR + row * ROW + ((chunk ^ (row & 7)) << 4),
-                 data + (offset < 0 ? 0 : (offset + chunk * 8) * 2), offset >= 0);
-        }
-      }
-      if (++load.tile == load.unit_end) load.next_unit(a, units);
-      look_up();
-    }
-    copy_commit();
-  };
-  look_up();
+  Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
 #pragma unroll 1
-  for (int s = 0; s < STAGES - 1; ++s) copy(s);
+  for (int s = 0; s < STAGES - 1; ++s) copies.copy(s);
 
-  // ---- the units --------------------------------------------------------------------------
   Walk walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
@@ -215,9 +130,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
     for (; walk.tile < stop; ++walk.tile) {
       copy_wait<STAGES - 2>();
       __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
-      const uint32_t live = s_live[warp][stage];
-      copy(stage == 0 ? STAGES - 1 : stage - 1);
-      const uint32_t keys = ring_at + stage * 2 * TENSOR, values = keys + TENSOR;
+      const uint32_t live = s_notes[warp].live[stage];
+      copies.copy(stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t keys = copies.ring + stage * Copies::STAGE, values = keys + Copies::TENSOR;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
 
       float s[2][2][4] = {};  // [even / odd step][positions 0..7 / 8..15]
@@ -320,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
       for (int w = 1; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[parity][w][g + 8 * r]);
       f[r] = ex2(m[r] - (M[r] == -INFINITY ? 0.f : M[r]));
     }
-    float* shared_o = reinterpret_cast<float*>(smem + S::RING);
+    float* shared_o = reinterpret_cast<float*>(smem + kWarps * Copies::RING);
     if (warp != 0) {
       float* dst = shared_o + (warp - 1) * HG * D;
 #pragma unroll
@@ -376,13 +291,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
           }
         }
       }
-      if (lane == 0 && at_start) {
-        PieceNote note;
-        note.unit_start = walk.unit_start; note.unit_end = walk.unit_end; note.tiles = place.T;
-        note.n = walk.unit_start < place.start ? walk.n : -1;
-        note.group = walk.group;
-        ws.note[c] = note;
-      }
+      if (lane == 0 && at_start) ws.note[c] = note_of(walk, place);
     }
     parity ^= 1;
     if (walk.tile == walk.unit_end) walk.next_unit(a, units);
@@ -393,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
 template <int D, int HG>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D, HG>();
-  const cudaError_t e = cudaFuncSetAttribute(kda_attend_mma_kernel<D, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<bool> set[64];
+  const cudaError_t e = ensure_smem(kda_attend_mma_kernel<D, HG>, bytes, set);
   if (e != cudaSuccess) return e;
   return launch_pdl(kda_attend_mma_kernel<D, HG>, dim3(p.ctas), dim3(kThreads), bytes, s, 1, a);
 }
