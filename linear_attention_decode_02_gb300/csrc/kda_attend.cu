@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Stage<T, D, HG>::CTAS) kda_attend_ke
 // the unit's pieces, each lane D/32 channels.
 template <int D, int HG>
 __global__ void __launch_bounds__(128) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
-  constexpr int VEC = D / 32, WARPS = 4;
+  constexpr int VEC = D / 32, WARPS = 4, AHEAD = 4;
   __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS][D];
   const int c = blockIdx.x, h = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -312,27 +312,46 @@ __global__ void __launch_bounds__(128) kda_attend_join_kernel(const __grid_const
   const int hk = note.group / groups, g0 = (note.group - hk * groups) * HG;
   if (h >= min(HG, G - g0)) return;
   const int64_t T = note.tiles;
-  const int64_t start = piece_start(c, T, C);
-  const int64_t first = piece_of(start - 1, T, C);
-  if (piece_start(first, T, C) > note.unit_start) return;  // an earlier cut crosses this unit too
-  const int64_t last = piece_of(note.unit_end - 1, T, C);
+  const int pieces = pieces_of(T, C);
+  const int first = (int)piece_of(piece_start(c, T, pieces) - 1, T, pieces);
+  const int64_t first_start = piece_start(first, T, pieces);
+  if (first_start > note.unit_start) return;  // an earlier cut crosses this unit too
+  const int last = (int)piece_of(note.unit_end - 1, T, pieces);
 
+  // The first piece may hold another unit before this one.
+  const auto slot_of = [&](int i) { return 2 * (int64_t)i + (i == first && first_start < note.unit_start ? 1 : 0); };
   float m = -INFINITY, l = 0.f, o[VEC] = {};
-  for (int64_t i = first + warp; i <= last; i += WARPS) {
-    const int64_t begin = piece_start(i, T, C);
-    if (begin == piece_start(i + 1, T, C)) continue;  // an empty piece
-    const int64_t slot = 2 * i + (begin < note.unit_start ? 1 : 0);  // the first piece may hold another unit before
-    const float pm = ws.ml_of(slot, h)[0], pl = ws.ml_of(slot, h)[1];
-    float po[VEC];
-    const float* src = ws.o_of(slot, h) + lane * VEC;
+#pragma unroll 1
+  for (int i = first + warp; i <= last; i += WARPS * AHEAD) {
+    float pm[AHEAD], pl[AHEAD], po[AHEAD][VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) po[j] = src[j];
-    const float top = fmaxf(m, pm);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - ref), w = exp2f(pm - ref);
-    l = l * f + pl * w;
+    for (int k = 0; k < AHEAD; ++k) {
+      pm[k] = -INFINITY;
+      pl[k] = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = o[j] * f + po[j] * w;
+      for (int j = 0; j < VEC; ++j) po[k][j] = 0.f;
+      if (i + k * WARPS <= last) {
+        const int64_t slot = slot_of(i + k * WARPS);
+        const float2 ml = *reinterpret_cast<const float2*>(ws.ml_of(slot, h));
+        pm[k] = ml.x;
+        pl[k] = ml.y;
+        read_lane<VEC>(ws.o_of(slot, h) + lane * VEC, po[k]);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) top = fmaxf(top, pm[k]);
+    const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] *= f;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float w = exp2f(pm[k] - ref);
+      l = fmaf(pl[k], w, l);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = fmaf(po[k][j], w, o[j]);
+    }
     m = top;
   }
   if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }

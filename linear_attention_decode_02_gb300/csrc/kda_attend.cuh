@@ -2,8 +2,8 @@
 //
 // A unit is one sequence, one key head and one group of at most HG of its
 // query heads; its work is a row of tiles of kTile positions, at least one.
-// All units' tiles form one line, cut into `ctas` equal pieces whatever the
-// sequences' lengths, so ragged batches and a few very long sequences load
+// All units' tiles form one line, cut into equal pieces, one for each block of
+// the grid but at least a tile, whatever the sequences' lengths, so ragged batches and a few very long sequences load
 // the SMs alike, and the host needs no lengths.  A unit inside one piece is
 // finished there; one that crosses a cut leaves an unnormalised partial
 // (maximum, sum, output) per piece, which a second kernel joins.  A piece
@@ -21,10 +21,17 @@ constexpr int kTile = 64;  // positions of a tile
 AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms);
 cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 
-// First tile of piece c.
-__device__ __forceinline__ int64_t piece_start(int64_t c, int64_t T, int C) { return c * T / C; }
-// Piece that owns tile t.
-__device__ __forceinline__ int64_t piece_of(int64_t t, int64_t T, int C) { return ((t + 1) * C + T - 1) / T - 1; }
+// a / b, neither negative; 32-bit where they fit (a 64-bit division is a long call).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+// Pieces of T tiles, their first tiles, and the piece that owns a tile.
+__device__ __forceinline__ int pieces_of(int64_t T, int ctas) { return T < ctas ? (int)T : ctas; }
+__device__ __forceinline__ int64_t piece_start(int64_t c, int64_t T, int pieces) { return quotient(c * T, pieces); }
+__device__ __forceinline__ int64_t piece_of(int64_t t, int64_t T, int pieces) {
+  return quotient((t + 1) * pieces + T - 1, T) - 1;
+}
 
 // What a piece tells the join about the unit at its first tile.
 struct PieceNote {
@@ -63,8 +70,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
   return s;
 }
 
-// Finds, with the whole block, the number of tiles per (key head, group) of
-// all sequences and the sequence where tile `c * T / C` lies.
+// Finds, with the whole block, the tiles of all sequences and where piece c lies
+// in them; start == stop where there is no such piece.
 struct Place {
   int64_t T;       // all tiles
   int64_t start, stop;
@@ -72,7 +79,7 @@ struct Place {
   int64_t before;  // tiles before sequence n
 };
 template <int THREADS>
-__device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int c, int C) {
+__device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int c, int ctas) {
   __shared__ int64_t s_warp[THREADS / 32];
   __shared__ int s_n;
   __shared__ int64_t s_before;
@@ -97,8 +104,13 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   }
   Place p;
   p.T = total * units;
-  p.start = piece_start(c, p.T, C);
-  p.stop = piece_start(c + 1, p.T, C);
+  const int pieces = pieces_of(p.T, ctas);
+  p.start = p.stop = 0;
+  p.n = 0;
+  p.before = 0;
+  if (c >= pieces) return p;  // the whole block
+  p.start = piece_start(c, p.T, pieces);
+  p.stop = piece_start(c + 1, p.T, pieces);
   int64_t at = (prior + scan - mine) * units;  // tiles before sequence n0
   if (n0 < n1 && p.start >= at && p.start < at + mine * units) {
     int n = n0;
@@ -131,7 +143,7 @@ struct Walk {
     tile = p.start;
     n = p.n;
     sp = span_of(a, n);
-    group = (int)((tile - p.before) / sp.tiles);
+    group = (int)quotient(tile - p.before, sp.tiles);
     unit_start = p.before + (int64_t)group * sp.tiles;
     unit_end = unit_start + sp.tiles;
   }
