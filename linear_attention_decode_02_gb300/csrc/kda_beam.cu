@@ -216,11 +216,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   __shared__ uint32_t s_top[kWarps], s_bound[kWarps];
   __shared__ float s_hi[kThreads], s_tops[kBatches][kThreads];
   __shared__ uint64_t s_list[kList];
-  __shared__ int s_count;
+  __shared__ uint16_t s_hot[kBatches * kThreads];
+  __shared__ int s_count, s_hots;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t beam = blockIdx.x / (uint32_t)splits;
   const int split = blockIdx.x - beam * splits;
-  if (tid == 0) s_count = 0;
+  if (tid == 0) s_count = s_hots = 0;
 
   // The vectors lie on 16-byte boundaries; the row may start and end inside one.
   const uint32_t n = beam / (uint32_t)a.B;
@@ -228,34 +229,34 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
   const int first = split * batches * BATCH - lead;  // of the piece
   const int i0 = first + tid * VEC;                  // of this thread's first vector
-  const auto load = [&](int batch, Raw<T>(&x)[LOADS]) {
+  const auto load_vector = [&](int i, Raw<T>& v) {
+    if (i >= 0 && i + VEC <= a.V) {
+      v.load(row + i);
+    } else {
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int i = i0 + batch * BATCH + j * kThreads * VEC;
-      if (i >= 0 && i + VEC <= a.V) {
-        x[j].load(row + i);
-      } else {
+      for (int e = 0; e < VEC; ++e) v.set(e, nullptr);
+      if (i + VEC > 0 && i < a.V) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[j].set(e, nullptr);
-        if (i + VEC > 0 && i < a.V) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (i + e >= 0 && i + e < a.V) x[j].set(e, row + i + e);
-        }
+        for (int e = 0; e < VEC; ++e)
+          if (i + e >= 0 && i + e < a.V) v.set(e, row + i + e);
       }
     }
   };
+  const auto load = [&](int batch, Raw<T>(&x)[LOADS]) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) load_vector(i0 + batch * BATCH + j * kThreads * VEC, x[j]);
+  };
   pdl_wait();
   pdl_launch_dependents();
-  // A live beam reads its logits: its score is finite and it is not finished.
+  Raw<T> x[LOADS], ahead[LOADS];
+  load(0, ahead);
+  // A live beam's score is finite and it is not finished; of others the first batch is read for nothing.
   const int done = a.finished != nullptr ? __ldg(a.finished + beam) : 0;
   if (!isfinite(__ldg(a.scores + beam)) || done != 0) return;
 
   // One batch is summed while the next is on its way.  The thread's reference
   // r moves in whole steps, so rescaling its sum is exact.
   float top = -INFINITY, r = -kNear, sum = 0.f;
-  Raw<T> x[LOADS], ahead[LOADS];
-  load(0, ahead);
 #pragma unroll 1
   for (int k = 0; k < batches; ++k) {
 #pragma unroll
@@ -291,26 +292,28 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   const float bound = unsortable(lowest), all = unsortable(highest);
   const int end = (int)min((int64_t)a.V, (int64_t)first + (int64_t)batches * BATCH);
 
-  // The few vectors that hold a candidate are read again.
-  if (top >= bound) {
-#pragma unroll 1
-    for (int k = 0; k < batches; ++k) {
-      if (!(s_tops[k][tid] >= bound)) continue;
-      load(k, x);
+  // Elements at or above the bound go to the list.  One batch is still in
+  // registers; of several, the threads' batches that hold one are noted first
+  // and read again, a vector a thread, so that one memory latency serves all.
+  const auto push = [&](const Raw<T>& v, int i) {
+    if (!(v.top() >= bound)) return;
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        if (!(x[j].top() >= bound)) continue;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float2 p = x[j].pair(e / 2);
-          const float v = e % 2 == 0 ? p.x : p.y;
-          if (v >= bound && v > -INFINITY) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kList) s_list[at] = candidate(v, i0 + k * BATCH + j * kThreads * VEC + e);
-          }
-        }
+    for (int e = 0; e < VEC; ++e) {
+      const float2 p = v.pair(e / 2);
+      const float w = e % 2 == 0 ? p.x : p.y;
+      if (w >= bound && w > -INFINITY) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kList) s_list[at] = candidate(w, i + e);
       }
     }
+  };
+  if (batches == 1) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) push(x[j], i0 + j * kThreads * VEC);
+  } else if (top >= bound) {
+#pragma unroll 1
+    for (int k = 0; k < batches; ++k)
+      if (s_tops[k][tid] >= bound) s_hot[atomicAdd(&s_hots, 1)] = (uint16_t)(k * kThreads + tid);
   }
   float hi, lo = 0.f;
   if (fabsf(all) < kNear / kLog2e) {
@@ -325,6 +328,17 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   }
   s_hi[tid] = hi;
   __syncthreads();
+  if (batches > 1) {
+    const int hot = s_hots * LOADS;
+    for (int h = tid; h < hot; h += kThreads) {
+      const int entry = s_hot[h / LOADS], j = h % LOADS;
+      const int i = first + (entry / kThreads) * BATCH + (j * kThreads + entry % kThreads) * VEC;
+      Raw<T> v;
+      load_vector(i, v);
+      push(v, i);
+    }
+    __syncthreads();
+  }
   const int count = s_count;
   const Lists lists(a, splits);
   const int64_t piece = blockIdx.x;
