@@ -4,7 +4,8 @@ Each function has the name of its C entry point, turns torch tensors into
 ``kda_tensor`` descriptors, passes the current CUDA stream, and raises
 ``KdaError`` on any non-OK status.  All arithmetic runs in the library's
 CUDA kernels; there is no fallback path: if ``libkda.so`` is missing the
-first call raises.
+first call raises.  The cache and beam calls are marshalled by a small CPython
+module (``csrc/kda_python.c``) instead of ctypes, for their host time.
 """
 
 from __future__ import annotations
@@ -12,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import threading
@@ -19,6 +21,7 @@ import threading
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
+_MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kda_python.so")
 _lock = threading.Lock()
 _lib = None
 
@@ -163,9 +166,13 @@ def _stream(t):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
+# The current device without the lazy-initialisation check, which a CUDA tensor's existence has passed.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on(dev):
     """Device guard for the call, entered only when `dev` is not already current."""
-    if dev.type == "cuda" and dev.index == torch.cuda.current_device():
+    if dev.type == "cuda" and dev.index == _current_device():
         return _SAME_DEVICE
     return torch.cuda.device(dev)
 
@@ -270,18 +277,52 @@ def kda_spec_verify_decode(q, k, v, g, beta, cu_seqlens, state_indices, state, t
     return out
 
 
+_module = None
+
+
+def _native():
+    """The CPython marshalling module, loaded once and given the library's addresses."""
+    global _module
+    if _module is None:
+        lib = library()
+        with _lock:
+            if _module is None:
+                if not os.path.exists(_MODULE_PATH):
+                    raise RuntimeError(f"_kda_python.so is not built ({_MODULE_PATH}); run "
+                                       "`python -m linear_attention_decode_02_gb300.build`")
+                spec = importlib.util.spec_from_file_location("_kda_python", _MODULE_PATH)
+                m = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(m)
+                m.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.kda_rope_append, lib.kda_paged_attention_decode, lib.kda_beam_select,
+                                       lib.kda_pool_move)),
+                       (torch.float32, torch.bfloat16, torch.int32))
+                _module = m
+    return _module
+
+
+def _handle(dev):
+    """Raw handle of the device's current stream."""
+    if _raw_stream is not None and dev.type == "cuda":
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _raise(status):
+    raise KdaError(status, library().kda_last_error_message().decode())
+
+
 def kda_rope_append(q, k, v, phase_steps, seq_lens, page_table, k_pages, v_pages, cu_seqlens=None,
                     interleaved=False, amplitude=1.0, q_out=None):
     """Rotates q and k, writes k and v into the pages in place, returns the rotated q in the pages' dtype."""
-    lib = library()
+    dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=k_pages.dtype, device=q.device)
-    with _on(q.device):
-        st = lib.kda_rope_append(_ref(q), _ref(k), _ref(v), _ref(phase_steps),
-                                 _ref(cu_seqlens) if cu_seqlens is not None else None, _ref(seq_lens),
-                                 _ref(page_table), _ref(k_pages), _ref(v_pages), _ref(q_out),
-                                 int(bool(interleaved)), float(amplitude), _stream(q))
-    _check(lib, st)
+        q_out = torch.empty_like(q, dtype=k_pages.dtype, memory_format=torch.contiguous_format)
+    with _on(dev):
+        st = (_module or _native()).rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages,
+                                                q_out, 1 if interleaved else 0, amplitude, _handle(dev))
+    if st:
+        _raise(st)
     return q_out
 
 
@@ -317,20 +358,19 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
     Without `workspace` each call takes one from torch's allocator, which keeps
     concurrent streams and captured graphs apart.
     """
-    lib = library()
+    dev = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.size(0), q.size(1), dtype=torch.float32, device=dev)
     if workspace is None:
-        floats = _attention_floats(q.shape[1], k_pages.shape[2], q.shape[2], q.dtype, q.device)
-        workspace = torch.empty(floats, dtype=torch.float32, device=q.device)
-    with _on(q.device):
-        st = lib.kda_paged_attention_decode(_ref(q), _ref(k_pages), _ref(v_pages), _ref(page_table), _ref(seq_lens),
-                                            _ref(workspace), int(window),
-                                            float(scale if scale is not None else q.shape[2] ** -0.5), _ref(out),
-                                            _ref(lse) if lse is not None else None, _stream(q))
-    _check(lib, st)
+        floats = _attention_floats(q.size(1), k_pages.size(2), q.size(2), q.dtype, dev)
+        workspace = torch.empty(floats, dtype=torch.float32, device=dev)
+    with _on(dev):
+        st = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, window,
+                                              q.size(2) ** -0.5 if scale is None else scale, _handle(dev))
+    if st:
+        _raise(st)
     return (out, lse) if return_lse else out
 
 
@@ -355,40 +395,29 @@ def kda_beam_select(logits, scores, num_out, finished=None, eos_token=0, out=Non
     `out` may give the three tensors; the workspace is as in
     kda_paged_attention_decode.
     """
-    lib = library()
-    n, dev = logits.shape[0], logits.device
+    n, dev = logits.size(0), logits.device
     if out is None:
-        out = (torch.empty((n, num_out), dtype=torch.float32, device=dev),
-               torch.empty((n, num_out), dtype=torch.int32, device=dev),
-               torch.empty((n, num_out), dtype=torch.int32, device=dev))
+        out = (torch.empty(n, num_out, dtype=torch.float32, device=dev),
+               torch.empty(n, num_out, dtype=torch.int32, device=dev),
+               torch.empty(n, num_out, dtype=torch.int32, device=dev))
     if workspace is None:
-        floats = _beam_floats(n, logits.shape[1], logits.shape[2], int(num_out), logits.dtype, dev)
+        floats = _beam_floats(n, logits.size(1), logits.size(2), num_out, logits.dtype, dev)
         workspace = torch.empty(floats, dtype=torch.float32, device=dev)
     with _on(dev):
-        st = lib.kda_beam_select(_ref(logits), _ref(scores), _ref(finished) if finished is not None else None,
-                                 int(eos_token), _ref(workspace), _ref(out[0]), _ref(out[1]), _ref(out[2]),
-                                 _stream(logits))
-    _check(lib, st)
+        st = (_module or _native()).beam(logits, scores, finished, workspace, out[0], out[1], out[2], eos_token,
+                                         _handle(dev))
+    if st:
+        _raise(st)
     return out
 
 
 def kda_pool_move(pools, src_slots, dst_slots, parents=None):
     """Copies slots of every tensor of `pools` in place; returns None."""
-    lib = library()
     dev = src_slots.device
     with _on(dev):
-        st = lib.kda_pool_move(_pool_array(pools), len(pools), _ref(src_slots), _ref(dst_slots),
-                               _ref(parents) if parents is not None else None, _stream(src_slots))
-    _check(lib, st)
-
-
-def _pool_array(pools):
-    """Array of descriptor pointers; the descriptors stay referenced by the array's keep list."""
-    array = (ctypes.POINTER(KdaTensor) * max(1, len(pools)))()
-    array._keep = [desc(p) for p in pools]
-    for i, d in enumerate(array._keep):
-        array[i] = ctypes.pointer(d)
-    return array
+        st = (_module or _native()).move(pools, src_slots, dst_slots, parents, _handle(dev))
+    if st:
+        _raise(st)
 
 
 def kda_plan_split(op, units, state_dtype, t_max, sm_count):

@@ -1,10 +1,11 @@
-"""Build libkda.so in-tree with nvcc for sm_103a (GB300).
+"""Build libkda.so in-tree with nvcc for sm_103a (GB300), and with the C compiler
+the small CPython module that marshals the binding's calls.
 
     python -m linear_attention_decode_02_gb300.build [--force] [--verbose]
 
 Compiles each CUDA translation unit in parallel, then links one shared
 library next to this file.  Rebuilds only when a source or header is newer
-than the library.
+than the libraries.
 """
 
 from __future__ import annotations
@@ -15,12 +16,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+PYSRC = os.path.join(CSRC, "kda_python.c")
+PYLIB = os.path.join(PKG, "_kda_python.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
               "-I", os.path.join(ROOT, "include")]
@@ -42,13 +46,13 @@ def _sources():
 
 def _inputs():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+        glob.glob(os.path.join(ROOT, "include", "*.h")) + [PYSRC, os.path.abspath(__file__)]
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(PYLIB)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYLIB))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -63,6 +67,19 @@ def _compile(nvcc, src, verbose):
     return obj, r.stderr
 
 
+def _python_module():
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler found for the binding's CPython module")
+    tmp = PYLIB + ".tmp"
+    cmd = [cc, "-std=c11", "-O2", "-Wall", "-Wextra", "-Wno-missing-field-initializers", "-fPIC", "-shared",
+           "-I", sysconfig.get_paths()["include"], PYSRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for {PYSRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYLIB)
+
+
 def build(force=False, verbose=False):
     """Compile and link libkda.so; returns its path."""
     if not force and up_to_date():
@@ -70,7 +87,8 @@ def build(force=False, verbose=False):
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        module = ex.submit(_python_module)
         results = list(ex.map(lambda s: _compile(nvcc, s, verbose), srcs))
     if verbose:
         for _, log in results:
@@ -81,6 +99,7 @@ def build(force=False, verbose=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    module.result()
     return LIB
 
 

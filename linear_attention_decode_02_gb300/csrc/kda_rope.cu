@@ -9,9 +9,11 @@
 // rotation is float32 and each output is rounded once.
 //
 // Bound by memory: every input is read once and every output written once.
-// One CTA per token row: its rot/2 sines and cosines are computed once into
-// shared memory and reused by the row's Hq + Hkv heads, then the threads walk
-// the row's vectors.
+// A block takes ROWS token rows.  Their sines and cosines are computed once
+// into shared memory and reused by the rows' Hq + Hkv heads; then each thread
+// walks the vectors of a row and moves each for all the rows at once, so that
+// 2 * ROWS loads are in flight and the way from the row to its position and
+// page (three dependent loads) is paid once for them.
 #include "kda_cache.h"
 #include "kda_device.cuh"
 
@@ -19,6 +21,10 @@ namespace kda {
 namespace {
 
 constexpr int kMaxPairs = 256;  // head_dim <= 512
+// Rows from which a block takes four of them.  Measured with 48 heads of 128
+// bf16 channels: 23119 rows 97 us (5.9 TB/s; 1 row a block 121 us, 2 rows 98 to
+// 104 us by occupancy), while few rows want a block each (384 rows: 4 us).
+constexpr int kManyRows = 2048;
 
 // Index of the sequence owning `row`: the number of entries of cu[1..N] that
 // are <= row, by a 32-way search of the whole warp (N <= 32: one load).
@@ -35,154 +41,195 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int row, 
   return lo;
 }
 
-// VEC elements of type T as floats, and back (round to nearest even).
+// VEC elements as loaded, as floats, and rounded to nearest even for the store.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 r = __ldcs(reinterpret_cast<const float4*>(p + i));
-      x[i] = r.x; x[i + 1] = r.y; x[i + 2] = r.z; x[i + 3] = r.w;
-    }
-  } else if constexpr (VEC == 8) {
-    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
-    x[0] = bf_lo(r.x); x[1] = bf_hi(r.x); x[2] = bf_lo(r.y); x[3] = bf_hi(r.y);
-    x[4] = bf_lo(r.z); x[5] = bf_hi(r.z); x[6] = bf_lo(r.w); x[7] = bf_hi(r.w);
-  } else {
-    const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p));
-    x[0] = bf_lo(r.x); x[1] = bf_hi(r.x); x[2] = bf_lo(r.y); x[3] = bf_hi(r.y);
+struct Vec;
+template <>
+struct Vec<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
+  __device__ __forceinline__ static void store(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  } else if constexpr (VEC == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]),
-                                              pack_bf2(x[6], x[7]));
-  } else {
+};
+template <>
+struct Vec<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&x)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
   }
-}
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+    x[4] = bf_lo(v.z); x[5] = bf_hi(v.z); x[6] = bf_lo(v.w); x[7] = bf_hi(v.w);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]),
+                                              pack_bf2(x[6], x[7]));
+  }
+};
 
-template <typename In, typename Out, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) kda_rope_append_kernel(const RopeArgs a) {
-  __shared__ float2 s_cs[kMaxPairs];
-  __shared__ int s_pos;
-  __shared__ int64_t s_k, s_v;
-  __shared__ int s_write;
-  const int row = blockIdx.x;
+// A thread's place among heads x tasks, moved on by the block without dividing.
+struct Slot {
+  int h, t, dh, dt, tasks;
+  __device__ __forceinline__ explicit Slot(int tasks_) : tasks(tasks_) {
+    h = threadIdx.x / tasks;
+    t = threadIdx.x - h * tasks;
+    dh = blockDim.x / tasks;
+    dt = blockDim.x - dh * tasks;
+  }
+  __device__ __forceinline__ void next() {
+    h += dh;
+    t += dt;
+    if (t >= tasks) {
+      t -= tasks;
+      ++h;
+    }
+  }
+};
+
+template <typename In, typename Out, int VEC, bool INTERLEAVED, int ROWS>
+__global__ void __launch_bounds__(256, 4) kda_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float2 s_cs[ROWS][kMaxPairs];
+  __shared__ int s_pos[ROWS];           // -1: zero output
+  __shared__ int64_t s_k[ROWS], s_v[ROWS];  // element offsets of the row's place in its page, or -1
+  const int row0 = blockIdx.x * ROWS;
   pdl_wait();
   pdl_launch_dependents();
 
-  if (threadIdx.x < 32) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < ROWS) {
+    const int row = row0 + warp;
     int n = row, end = row + 1;
-    bool live = true;
+    bool live = row < a.R;
     if (a.cu != nullptr) {
-      n = find_sequence(a.cu, a.N, row, threadIdx.x);
-      live = n < a.N && row >= __ldg(a.cu + n);
+      n = find_sequence(a.cu, a.N, row, lane);
+      live = live && n < a.N && row >= __ldg(a.cu + n);
       end = live ? min(__ldg(a.cu + n + 1), a.R) : 0;
     }
-    if (threadIdx.x == 0) {
-      int64_t pos = live ? (int64_t)__ldg(a.lens + n) - end + row : -1;
-      int write = 0;
+    if (lane == 0) {
+      const int64_t pos = live ? (int64_t)__ldg(a.lens + n) - end + row : -1;
+      int64_t ko = -1, vo = -1;
       if (pos >= 0) {
         const int64_t col = pos / a.page_size;
         if (col < a.table_cols) {
           const int page = __ldg(a.table + (int64_t)n * a.table_rs + col);
           if (page > 0 && page < a.num_pages) {
             const int64_t t = pos - col * a.page_size;
-            s_k = page * a.kp.page + t * a.kp.token;
-            s_v = page * a.vp.page + t * a.vp.token;
-            write = 1;
+            ko = page * a.kp.page + t * a.kp.token;
+            vo = page * a.vp.page + t * a.vp.token;
           }
         }
       }
-      s_pos = pos < 0 ? -1 : (int)pos;
-      s_write = write;
+      s_pos[warp] = pos < 0 ? -1 : (int)pos;
+      s_k[warp] = ko;
+      s_v[warp] = vo;
     }
   }
   __syncthreads();
-  const int pos = s_pos;
-  const bool write = s_write != 0;
-  for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) {
-    const uint64_t phase = (uint64_t)(uint32_t)max(pos, 0) * __ldg(a.steps + i);
+  // Tasks of a rotated head: its pair vectors, then its unrotated tail.  The
+  // half layout's pair vectors hold VEC elements of either half.  Pair j of
+  // task t lies at j * pair_tasks + t, so that neighbouring tasks meet no bank.
+  constexpr int PAIRS = INTERLEAVED ? VEC / 2 : VEC;
+  const int pair_tasks = a.rot / (2 * PAIRS);
+  for (int i = threadIdx.x; i < ROWS * (a.rot / 2); i += blockDim.x) {
+    const int r = i / (a.rot / 2), pair = i - r * (a.rot / 2);
+    const uint64_t phase = (uint64_t)(uint32_t)max(s_pos[r], 0) * __ldg(a.steps + pair);
     float sn, cs;
     sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
-    s_cs[i] = make_float2(cs * a.amplitude, sn * a.amplitude);
+    s_cs[r][(pair % PAIRS) * pair_tasks + pair / PAIRS] = make_float2(cs * a.amplitude, sn * a.amplitude);
   }
   __syncthreads();
 
-  // Tasks of a rotated head: its pair vectors, then its unrotated tail.  The
-  // half layout's pair vectors hold VEC elements of either half.
-  const int pair_tasks = INTERLEAVED ? a.rot / VEC : a.rot / (2 * VEC);
-  const int tasks = pair_tasks + (a.D - a.rot) / VEC;
-  const int rotated = a.Hq + a.Hkv;
-  for (int i = threadIdx.x; i < rotated * tasks; i += blockDim.x) {
-    const int h = i / tasks, t = i - h * tasks;
-    const bool is_q = h < a.Hq;
-    if (!is_q && !write) break;  // only keys follow
-    const In* src = is_q ? static_cast<const In*>(a.q) + row * a.q_rs + h * a.q_hs
-                         : static_cast<const In*>(a.k) + row * a.k_rs + (h - a.Hq) * a.k_hs;
-    Out* dst = is_q ? static_cast<Out*>(a.q_out) + row * a.o_rs + h * a.o_hs
-                    : static_cast<Out*>(a.kp.data) + s_k + (h - a.Hq) * a.kp.head;
-    if (pos < 0) {  // padding row or null sequence (queries only)
-      float z[VEC] = {};
-      if (t < pair_tasks) {
-        store_vec<Out, VEC>(dst + t * VEC, z);
-        if (!INTERLEAVED) store_vec<Out, VEC>(dst + a.rot / 2 + t * VEC, z);
-      } else {
-        store_vec<Out, VEC>(dst + a.rot + (t - pair_tasks) * VEC, z);
+  Slot s(pair_tasks + (a.D - a.rot) / VEC);
+  for (; s.h < a.Hq + a.Hkv; s.next()) {
+    const bool is_q = s.h < a.Hq;
+    const int h = is_q ? s.h : s.h - a.Hq;
+    const In* src = is_q ? static_cast<const In*>(a.q) + h * a.q_hs : static_cast<const In*>(a.k) + h * a.k_hs;
+    const int64_t src_rs = is_q ? a.q_rs : a.k_rs;
+    const bool turns = s.t < pair_tasks;
+    const bool two = turns && !INTERLEAVED;
+    const int c = turns ? s.t * VEC : a.rot + (s.t - pair_tasks) * VEC;
+    Vec<In, VEC> vx[ROWS], vy[ROWS];
+    bool go[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      go[r] = row0 + r < a.R && (is_q || s_k[r] >= 0);
+      if (go[r]) {
+        const In* p = src + (row0 + r) * src_rs + c;
+        vx[r].load(p);
+        if (two) vy[r].load(p + a.rot / 2);
       }
-      continue;
     }
-    float x[VEC];
-    if (t >= pair_tasks) {
-      const int c = a.rot + (t - pair_tasks) * VEC;
-      load_vec<In, VEC>(src + c, x);
-      store_vec<Out, VEC>(dst + c, x);
-    } else if (INTERLEAVED) {
-      load_vec<In, VEC>(src + t * VEC, x);
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        const float2 cs = s_cs[(t * VEC + j) / 2];
-        const float p = x[j], r = x[j + 1];
-        x[j] = p * cs.x - r * cs.y;
-        x[j + 1] = p * cs.y + r * cs.x;
-      }
-      store_vec<Out, VEC>(dst + t * VEC, x);
-    } else {
-      float y[VEC];
-      load_vec<In, VEC>(src + t * VEC, x);
-      load_vec<In, VEC>(src + a.rot / 2 + t * VEC, y);
+    for (int r = 0; r < ROWS; ++r) {
+      if (!go[r]) continue;
+      Out* dst = (is_q ? static_cast<Out*>(a.q_out) + (row0 + r) * a.o_rs + h * a.o_hs
+                       : static_cast<Out*>(a.kp.data) + s_k[r] + h * a.kp.head) + c;
+      float x[VEC], y[VEC];
+      vx[r].get(x);
+      if (two) {
+        vy[r].get(y);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float2 cs = s_cs[t * VEC + j];
-        const float p = x[j], r = y[j];
-        x[j] = p * cs.x - r * cs.y;
-        y[j] = p * cs.y + r * cs.x;
+        for (int j = 0; j < VEC; ++j) {
+          const float2 cs = s_cs[r][j * pair_tasks + s.t];
+          const float u = x[j], w = y[j];
+          x[j] = u * cs.x - w * cs.y;
+          y[j] = u * cs.y + w * cs.x;
+        }
+      } else if (turns) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 cs = s_cs[r][j / 2 * pair_tasks + s.t];
+          const float u = x[j], w = x[j + 1];
+          x[j] = u * cs.x - w * cs.y;
+          x[j + 1] = u * cs.y + w * cs.x;
+        }
       }
-      store_vec<Out, VEC>(dst + t * VEC, x);
-      store_vec<Out, VEC>(dst + a.rot / 2 + t * VEC, y);
+      if (s_pos[r] < 0) {  // padding row or null sequence (queries only)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = y[j] = 0.f;
+      }
+      Vec<Out, VEC>::store(dst, x);
+      if (two) Vec<Out, VEC>::store(dst + a.rot / 2, y);
     }
   }
-  if (!write) return;
-  const int vt = a.D / VEC;
-  for (int i = threadIdx.x; i < a.Hkv * vt; i += blockDim.x) {
-    const int h = i / vt, c = (i - h * vt) * VEC;
-    float x[VEC];
-    load_vec<In, VEC>(static_cast<const In*>(a.v) + row * a.v_rs + h * a.v_hs + c, x);
-    store_vec<Out, VEC>(static_cast<Out*>(a.vp.data) + s_v + h * a.vp.head + c, x);
+  for (Slot s(a.D / VEC); s.h < a.Hkv; s.next()) {
+    const int c = s.t * VEC;
+    const In* src = static_cast<const In*>(a.v) + s.h * a.v_hs + c;
+    Vec<In, VEC> vx[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+      if (s_v[r] >= 0) vx[r].load(src + (row0 + r) * a.v_rs);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (s_v[r] < 0) continue;
+      float x[VEC];
+      vx[r].get(x);
+      Vec<Out, VEC>::store(static_cast<Out*>(a.vp.data) + s_v[r] + s.h * a.vp.head + c, x);
+    }
   }
+}
+
+template <typename In, typename Out, int VEC, int ROWS>
+cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
+  auto kernel = a.interleaved ? kda_rope_append_kernel<In, Out, VEC, true, ROWS>
+                              : kda_rope_append_kernel<In, Out, VEC, false, ROWS>;
+  return launch_pdl(kernel, dim3((unsigned)((a.R + (int64_t)ROWS - 1) / ROWS)), dim3(256), 0, s, 1, a);
 }
 
 template <typename In, typename Out, int VEC>
 cudaError_t launch_rope_variant(const RopeArgs& a, cudaStream_t s) {
-  auto kernel = a.interleaved ? kda_rope_append_kernel<In, Out, VEC, true> : kda_rope_append_kernel<In, Out, VEC, false>;
-  return launch_pdl(kernel, dim3((unsigned)a.R), dim3(256), 0, s, 1, a);
+  return a.R >= kManyRows ? launch_rope_rows<In, Out, VEC, 4>(a, s) : launch_rope_rows<In, Out, VEC, 1>(a, s);
 }
 
 }  // namespace
