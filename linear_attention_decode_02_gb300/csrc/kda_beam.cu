@@ -33,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatches = 8;   // batches of loads a block may take
 constexpr int kList = 1024;   // elements that may pass the bound
+constexpr int kJoin = 4096;
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;  // log2(e) to 2^-50
 constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;  // ln 2 to 2^-50
 constexpr double kLog2eDouble = 1.4426950408889634, kLn2Double = 0.6931471805599453;
@@ -131,22 +132,23 @@ struct Lists {
   }
 };
 
-// Least maximum of `groups` (8 .. 64, a power of two) groups of the block's
-// threads, per warp: groups / 8 of them lie in each warp.
-template <typename K>
-__device__ __forceinline__ K least_group_max(K mine, int groups) {
-  const int size = 32 * kWarps / groups;
-  for (int o = 1; o < size; o <<= 1) {
-    const K x = __shfl_xor_sync(0xffffffffu, mine, o);
-    mine = x > mine ? x : mine;
+// Every warp alone, from the threads' maxima: the largest, and the least maximum
+// of `groups` (8 .. 64, a power of two) groups of threads, thread t in group
+// t % groups, so that a few threads with data already fill all groups.
+__device__ __forceinline__ void block_bound(const uint32_t (&keys)[kThreads], int groups, int lane, uint32_t& highest,
+                                            uint32_t& lowest) {
+  uint32_t even = keys[lane], odd = keys[32 + lane];
+#pragma unroll
+  for (int w = 2; w < kWarps; w += 2) {
+    even = max(even, keys[w * 32 + lane]);
+    odd = max(odd, keys[(w + 1) * 32 + lane]);
   }
-  for (int o = size; o < 32; o <<= 1) {
-    const K x = __shfl_xor_sync(0xffffffffu, mine, o);
-    mine = x < mine ? x : mine;
-  }
-  return mine;
+  uint32_t m = max(even, odd);
+  highest = __reduce_max_sync(0xffffffffu, m);
+  if (groups == 64) m = min(even, odd);
+  for (int o = groups; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  lowest = __reduce_min_sync(0xffffffffu, m);
 }
-
 __device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32) == hi ? (uint32_t)x : 0u);
@@ -213,7 +215,7 @@ __device__ __forceinline__ float batch_sum(const Raw<T> (&x)[LOADS], float r) {
 template <typename T, int LOADS>
 __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamArgs a, int splits, int batches) {
   constexpr int VEC = Raw<T>::VEC, BATCH = LOADS * kThreads * VEC;
-  __shared__ uint32_t s_top[kWarps], s_bound[kWarps];
+  __shared__ uint32_t s_key[kThreads];
   __shared__ float s_hi[kThreads], s_tops[kBatches][kThreads];
   __shared__ uint64_t s_list[kList];
   __shared__ uint16_t s_hot[kBatches * kThreads];
@@ -275,20 +277,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     sum += batch_sum<T, LOADS>(x, r);
   }
 
-  const int groups = bound_groups(a.M);
-  const uint32_t key = sortable(top), wkey = __reduce_max_sync(0xffffffffu, key);
-  const uint32_t least = groups == kWarps ? wkey : least_group_max(key, groups);
-  if (lane == 0) {
-    s_top[warp] = wkey;
-    s_bound[warp] = least;
-  }
+  s_key[tid] = sortable(top);
   __syncthreads();
-  uint32_t lowest = s_bound[0], highest = s_top[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    lowest = min(lowest, s_bound[w]);
-    highest = max(highest, s_top[w]);
-  }
+  uint32_t lowest, highest;
+  block_bound(s_key, bound_groups(a.M), lane, highest, lowest);
   const float bound = unsortable(lowest), all = unsortable(highest);
   const int end = (int)min((int64_t)a.V, (int64_t)first + (int64_t)batches * BATCH);
 
@@ -368,7 +360,68 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     }
     return;
   }
-  // Too many equal values at the bound: M times the best below the last one, from memory again.
+  // Too many at the bound.  On masked or constant logits they equal it; of
+  // those only the first in the row matter.  The larger ones are counted again.
+  __syncthreads();
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  const int vectors = (end - first + VEC - 1) / VEC;
+  for (int h = tid; h < vectors; h += kThreads) {
+    Raw<T> v;
+    load_vector(first + h * VEC, v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float2 p = v.pair(e / 2);
+      const float w = e % 2 == 0 ? p.x : p.y;
+      if (w > bound) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kList) s_list[at] = candidate(w, first + h * VEC + e);
+      }
+    }
+  }
+  __syncthreads();
+  const int larger = s_count;
+  if (larger <= kList) {
+    for (int i = tid; i < larger; i += kThreads) {
+      const uint64_t mine = s_list[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < larger; ++j) rank += s_list[j] > mine ? 1 : 0;
+      if (rank < a.M) best[rank] = mine;
+    }
+    int place = larger;  // of the next equal one
+    for (int h0 = 0; h0 < vectors && place < a.M && bound > -INFINITY; h0 += kThreads) {
+      Raw<T> v;
+      load_vector(first + (h0 + tid) * VEC, v);
+      int equal = 0;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float2 p = v.pair(e / 2);
+        equal |= (e % 2 == 0 ? p.x : p.y) == bound ? 1 << e : 0;
+      }
+      if (h0 + tid >= vectors) equal = 0;
+      int scan = __popc(equal);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += up;
+      }
+      __syncthreads();  // the last step's readers
+      if (lane == 31) s_key[warp] = scan;
+      __syncthreads();
+      int at = place + scan - __popc(equal);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) at += s_key[w];
+        place += s_key[w];
+      }
+      for (int left = equal; left != 0 && at < a.M; left &= left - 1, ++at)
+        best[at] = candidate(bound, first + (h0 + tid) * VEC + __ffs(left) - 1);
+    }
+    for (int i = place + tid; i < a.M; i += kThreads) best[i] = 0;
+    return;
+  }
+  // Neither: M times the best below the last one, from memory.
   uint64_t last = ~0ull;
   for (int m = 0; m < a.M; ++m) {
     uint64_t mine = 0;
@@ -408,35 +461,38 @@ __device__ __forceinline__ bool before(const Choice& a, const Choice& b) {
   return (a.key > b.key) | ((a.key == b.key) & (a.flat < b.flat));
 }
 
-// One request.  Candidate i of all beams' pieces: the pieces' best ones first,
-// beams fastest; a finished beam has one, in the place of its first.  They are
-// dealt to the warps in turn, so that every group of threads sees all beams'
-// best.  The first kHeld a thread are on their way while the sums are joined.
+// One request.  List l is the one of piece l % splits of beam l / splits; a
+// finished beam has one candidate, in its first list.  The bound comes from the
+// first entries of the lists, kJoin in all, dealt to its groups by a hash: the
+// best may all be of one beam, and of the first places of a few lists.  The
+// lists are sorted, so each is then followed only as far as the bound lets it.
+constexpr int kStep = 8;  // entries of a list that one thread follows
 constexpr int kHeld = 2;
 __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs a, int splits) {
   // A candidate is worth (x - top) + offset, offset = score - log sum exp(x - top): no large numbers cancel.
   __shared__ float s_hi[kBeamMax], s_lo[kBeamMax];  // the sum, then the offset
   __shared__ float s_top[kBeamMax];
   __shared__ int s_kind[kBeamMax];                  // 0: nothing, 1: lists, 2: finished
-  __shared__ uint64_t s_bound[kWarps];
+  __shared__ uint32_t s_group[64];
   __shared__ Choice s_list[kList];
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = blockIdx.x;
   if (tid == 0) s_count = 0;
+  if (tid < 64) s_group[tid] = 0;
   pdl_wait();
   pdl_launch_dependents();
   const Lists lists(a, splits);
-  const int pieces = a.B * splits, count = pieces * a.M;
-  const uint64_t* best = lists.best + n * count;
-  const auto mine_at = [&](int k) { return k * kThreads + lane * kWarps + warp; };
-  const auto fetch = [&](int i) {
-    const int m = i / pieces, l = i - m * pieces, s = l / a.B, b = l - s * a.B;
-    return best[(b * splits + s) * a.M + m];  // without meaning for a beam whose logits were not read
-  };
-  uint64_t held[kHeld];
+  const int pieces = a.B * splits;
+  const uint64_t* best = lists.best + n * pieces * a.M;
+  const auto fetch = [&](int l, int m) { return best[(int64_t)l * a.M + m]; };
+  const int heads = min(a.M, max(1, kJoin / pieces)), count = heads * pieces;
+  uint64_t held[kHeld];  // on their way while the sums are joined; without meaning for a beam whose logits were not read
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) held[k] = mine_at(k) < count ? fetch(mine_at(k)) : 0;
+  for (int k = 0; k < kHeld; ++k) {
+    const int e = tid + k * kThreads;
+    held[k] = e < count ? fetch(e / heads, e % heads) : 0;
+  }
 
   for (int b = warp; b < a.B; b += kWarps) {
     const int64_t beam = n * a.B + b;
@@ -490,50 +546,48 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
   }
   __syncthreads();
 
-  const auto choice = [&](int i, uint64_t x) {
+  const auto choice = [&](int l, int m, uint64_t x) {
     Choice c;
     c.key = 0;
     c.flat = INT32_MAX;
-    const int l = i % pieces, b = l % a.B, kind = s_kind[b];
+    const int b = l / splits, kind = s_kind[b];
     if (kind == 1) {
       if (x != 0) {
         c.flat = b * a.V + (int)~(uint32_t)x;
         c.key = value_key(unsortable((uint32_t)(x >> 32)), s_top[b], s_hi[b], s_lo[b]);
       }
-    } else if (kind == 2 && i == b) {
+    } else if (kind == 2 && l == b * splits && m == 0) {
       c.flat = b * a.V + a.eos;
       c.key = value_key(0.f, 0.f, s_hi[b], 0.f);
     }
     return c;
   };
-  uint64_t mine = 0;
-  Choice own[kHeld];
+  const int groups = bound_groups(a.M);
+  const auto enter = [&](int e, uint64_t x) {
+    const uint32_t key = (uint32_t)(choice(e / heads, e % heads, x).key >> 32);
+    atomicMax(&s_group[((uint32_t)e * 2654435761u >> 26) & (groups - 1)], key);
+  };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int i = mine_at(k);
-    own[k].key = 0;
-    if (i < count) own[k] = choice(i, held[k]);
-    mine = max(mine, own[k].key);
-  }
-  for (int k = kHeld; k * kThreads < count; ++k)
-    if (mine_at(k) < count) mine = max(mine, choice(mine_at(k), fetch(mine_at(k))).key);
-  const uint64_t least = least_group_max(mine, bound_groups(a.M));
-  if (lane == 0) s_bound[warp] = least;
+  for (int k = 0; k < kHeld; ++k)
+    if (tid + k * kThreads < count) enter(tid + k * kThreads, held[k]);
+#pragma unroll 4
+  for (int e = tid + kHeld * kThreads; e < count; e += kThreads) enter(e, fetch(e / heads, e % heads));
   __syncthreads();
-  uint64_t bound = s_bound[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) bound = min(bound, s_bound[w]);
-  bound = max(bound, (uint64_t)1);
+  uint32_t least = min(s_group[lane & (groups - 1)], s_group[(lane + 32) & (groups - 1)]);
+  least = __reduce_min_sync(0xffffffffu, least);
+  const uint64_t bound = max((uint64_t)least << 32, (uint64_t)1);
   const auto push = [&](const Choice& c) {
-    if (c.key < bound) return;
     const int at = atomicAdd(&s_count, 1);
     if (at < kList) s_list[at] = c;
   };
-  if (mine >= bound) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) push(own[k]);
-    for (int k = kHeld; k * kThreads < count; ++k)
-      if (mine_at(k) < count) push(choice(mine_at(k), fetch(mine_at(k))));
+  const int steps = (a.M + kStep - 1) / kStep;
+  for (int u = tid; u < pieces * steps; u += kThreads) {
+    const int l = u / steps, step = u - l * steps;
+    for (int m = step * kStep; m < min(a.M, (step + 1) * kStep); ++m) {
+      const Choice c = choice(l, m, fetch(l, m));
+      if (c.key < bound) break;
+      push(c);
+    }
   }
   __syncthreads();
   const int found = s_count;
@@ -561,8 +615,8 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
   Choice last{~0ull, -1};
   for (int m = 0; m < a.M; ++m) {
     Choice c{0, INT32_MAX};
-    for (int i = tid; i < count; i += kThreads) {
-      const Choice x = choice(i, fetch(i));
+    for (int i = tid; i < pieces * a.M; i += kThreads) {
+      const Choice x = choice(i / a.M, i % a.M, fetch(i / a.M, i % a.M));
       if (x.key >= bound && before(last, x) && before(x, c)) c = x;
     }
     const uint64_t key = warp_max64(c.key);
@@ -589,7 +643,8 @@ cudaError_t launch_scan(const BeamArgs& a, const BeamPlan& p, cudaStream_t s) {
 }  // namespace
 
 // The longest pieces (8 batches of 4 loads a thread) that still give every SM
-// two blocks, down to one load a thread.  A row whose start is not on a 16-byte
+// two blocks, down to one load a thread, and not so short that the join, one
+// block a request, would have more than kJoin candidates to look at.  A row whose start is not on a 16-byte
 // boundary reaches up to vec - 1 elements further.
 BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms) {
   BeamPlan p;
@@ -599,7 +654,8 @@ BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bo
     return (int32_t)((V + (whole ? 0 : vec - 1) + per - 1) / per);
   };
   int vectors = 4 * kBatches;
-  while (vectors > 1 && N * B * splits(vectors, true) < 2 * sms) vectors /= 2;
+  while (vectors > 1 && N * B * splits(vectors, true) < 2 * sms && (int64_t)B * splits(vectors / 2, true) * M <= kJoin)
+    vectors /= 2;
   p.loads = vectors >= 4 ? 4 : 1;
   p.batches = vectors / p.loads;
   p.splits = splits(vectors, aligned);

@@ -181,3 +181,41 @@ def test_empty_batch():
     x, s = make(2, 3, 10)
     got = binding.kda_beam_select(x[:0], s[:0], 4)
     assert [tuple(t.shape) for t in got] == [(0, 4)] * 3
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [3000, 70000, 200001])
+@pytest.mark.parametrize("allowed", [1, 5, 40, 3000])
+def test_constrained_vocabularies_masked_by_a_finite_value(dtype, V, allowed):
+    # all but a few tokens at one low value: far more ties than any list holds
+    x, s = make(2, 3, V, dtype=dtype, seed=allowed)
+    g = torch.Generator().manual_seed(V)
+    keep = torch.zeros(V, dtype=torch.bool)
+    keep[torch.randperm(V, generator=g)[:min(allowed, V)]] = True
+    x = torch.where(keep.cuda(), x, torch.tensor(-1e9, device="cuda").to(dtype))
+    check(x, s, 16)
+    check(x, torch.where(torch.arange(3, device="cuda") == 1, s, s - 1e10), 33)  # one beam's masked tokens outrank others'
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_two_values_in_blocks(dtype):
+    # the larger value fills whole stretches, so that some groups of threads hold only the smaller one
+    x = torch.zeros(1, 2, 90000, dtype=dtype, device="cuda")
+    x[0, 0].view(-1, 8)[::32] = 1.0
+    x[0, 1, 40000:60000] = 2.0
+    check(x, torch.zeros(1, 2, device="cuda"), 64)
+    check(x, torch.tensor([[0.0, -5.0]], device="cuda"), 8)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("N,B,V,M", [(1, 16, 150000, 32), (2, 32, 30011, 64), (3, 1, 140000, 64), (40, 16, 999, 32),
+                                     (1, 1, 500, 1), (64, 2, 5000, 4)])
+def test_many_candidates_and_short_vocabularies(dtype, N, B, V, M):
+    check(*make(N, B, V, dtype=dtype, seed=M), M)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_sorted_logits(dtype):
+    x = torch.linspace(-9, 9, 100003).expand(2, 2, -1).to(dtype).contiguous().cuda()
+    x[1] = x[1].flip(-1)
+    check(x, torch.tensor([[0.0, -0.1], [-0.3, 0.0]], device="cuda"), 20)
