@@ -155,6 +155,23 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
   return ((uint64_t)hi << 32) | lo;
 }
 
+// Calls put(rank, list[i]) for the i below `count` whose rank, the number of
+// larger entries, is below M.  Four lanes share an entry's comparisons.
+template <typename E, typename Larger, typename Put>
+__device__ __forceinline__ void place(const E* list, int count, int M, const Larger& larger, const Put& put) {
+  const int part = threadIdx.x & 3;
+  for (int base = 0; base < count; base += kThreads / 4) {
+    const int i = base + (threadIdx.x >> 2);
+    const E mine = list[min(i, count - 1)];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = part; j < count; j += 4) rank += larger(list[j], mine) ? 1 : 0;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (i < count && part == 0 && rank < M) put(rank, mine);
+  }
+}
+
 template <typename T>
 struct Raw;  // 16 bytes of logits as loaded
 template <>
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
 
   // Elements at or above the bound go to the list.  One batch is still in
   // registers; of several, the threads' batches that hold one are noted first
-  // and read again, a vector a thread, so that one memory latency serves all.
+  // and read again, one a thread, so that one memory latency serves all.
   const auto push = [&](const Raw<T>& v, int i) {
     if (!(v.top() >= bound)) return;
 #pragma unroll
@@ -321,13 +338,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   s_hi[tid] = hi;
   __syncthreads();
   if (batches > 1) {
-    const int hot = s_hots * LOADS;
-    for (int h = tid; h < hot; h += kThreads) {
-      const int entry = s_hot[h / LOADS], j = h % LOADS;
-      const int i = first + (entry / kThreads) * BATCH + (j * kThreads + entry % kThreads) * VEC;
-      Raw<T> v;
-      load_vector(i, v);
-      push(v, i);
+    for (int h = tid; h < s_hots; h += kThreads) {
+      const int entry = s_hot[h], at = first + (entry / kThreads) * BATCH + entry % kThreads * VEC;
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) load_vector(at + j * kThreads * VEC, x[j]);
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) push(x[j], at + j * kThreads * VEC);
     }
     __syncthreads();
   }
@@ -346,18 +362,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
       lists.sum[piece] = p;
     }
   }
+  const auto above = [](uint64_t x, uint64_t y) { return x > y; };
+  const auto keep = [&](int rank, uint64_t x) { best[rank] = x; };
   if (count <= kList) {
-    for (int i = tid; i < max(count, a.M); i += kThreads) {
-      if (i < count) {
-        const uint64_t mine = s_list[i];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < count; ++j) rank += s_list[j] > mine ? 1 : 0;
-        if (rank < a.M) best[rank] = mine;
-      } else {
-        best[i] = 0;
-      }
-    }
+    place(s_list, count, a.M, above, keep);
+    for (int i = count + tid; i < a.M; i += kThreads) best[i] = 0;
     return;
   }
   // Too many at the bound.  On masked or constant logits they equal it; of
@@ -382,15 +391,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   __syncthreads();
   const int larger = s_count;
   if (larger <= kList) {
-    for (int i = tid; i < larger; i += kThreads) {
-      const uint64_t mine = s_list[i];
-      int rank = 0;
-#pragma unroll 8
-      for (int j = 0; j < larger; ++j) rank += s_list[j] > mine ? 1 : 0;
-      if (rank < a.M) best[rank] = mine;
-    }
-    int place = larger;  // of the next equal one
-    for (int h0 = 0; h0 < vectors && place < a.M && bound > -INFINITY; h0 += kThreads) {
+    place(s_list, larger, a.M, above, keep);
+    int next = larger;  // place of the next equal one
+    for (int h0 = 0; h0 < vectors && next < a.M && bound > -INFINITY; h0 += kThreads) {
       Raw<T> v;
       load_vector(first + (h0 + tid) * VEC, v);
       int equal = 0;
@@ -409,16 +412,16 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
       __syncthreads();  // the last step's readers
       if (lane == 31) s_key[warp] = scan;
       __syncthreads();
-      int at = place + scan - __popc(equal);
+      int at = next + scan - __popc(equal);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) at += s_key[w];
-        place += s_key[w];
+        next += s_key[w];
       }
       for (int left = equal; left != 0 && at < a.M; left &= left - 1, ++at)
         best[at] = candidate(bound, first + (h0 + tid) * VEC + __ffs(left) - 1);
     }
-    for (int i = place + tid; i < a.M; i += kThreads) best[i] = 0;
+    for (int i = next + tid; i < a.M; i += kThreads) best[i] = 0;
     return;
   }
   // Neither: M times the best below the last one, from memory.
@@ -467,7 +470,7 @@ __device__ __forceinline__ bool before(const Choice& a, const Choice& b) {
 // best may all be of one beam, and of the first places of a few lists.  The
 // lists are sorted, so each is then followed only as far as the bound lets it.
 constexpr int kStep = 8;  // entries of a list that one thread follows
-constexpr int kHeld = 2;
+constexpr int kHeld = 4;  // entries a thread keeps from the bound to the list
 __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs a, int splits) {
   // A candidate is worth (x - top) + offset, offset = score - log sum exp(x - top): no large numbers cancel.
   __shared__ float s_hi[kBeamMax], s_lo[kBeamMax];  // the sum, then the offset
@@ -494,19 +497,39 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     held[k] = e < count ? fetch(e / heads, e % heads) : 0;
   }
 
-  for (int b = warp; b < a.B; b += kWarps) {
-    const int64_t beam = n * a.B + b;
-    const float score = __ldg(a.scores + beam);
-    const bool done = a.finished != nullptr && __ldg(a.finished + beam) != 0;
+  // Warp w joins the sums of the beams w, w + kWarps, ...; all of its loads are on their way at once.
+  constexpr int BEAMS = kBeamMax / kWarps;
+  float scores[BEAMS];
+  int done[BEAMS];
+  PieceSum part[BEAMS];
+#pragma unroll
+  for (int k = 0; k < BEAMS; ++k) {
+    const int b = warp + k * kWarps;
+    scores[k] = 0.f;
+    done[k] = 0;
+    part[k].hi = part[k].lo = 0.f;
+    part[k].top = -INFINITY;
+    if (b < a.B) {
+      scores[k] = __ldg(a.scores + n * a.B + b);
+      if (a.finished != nullptr) done[k] = __ldg(a.finished + n * a.B + b);
+      if (lane < splits) part[k] = lists.sum[n * pieces + b * splits + lane];  // of a beam not read: not used
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < BEAMS; ++k) {
+    const int b = warp + k * kWarps;
+    if (b >= a.B) break;
+    const bool reads = isfinite(scores[k]) && done[k] == 0;
     float hi = 0.f, lo = 0.f, top = -INFINITY;
-    if (isfinite(score) && !done) {
-      const PieceSum* p = lists.sum + beam * splits;
-      for (int s = lane; s < splits; s += 32) top = fmaxf(top, p[s].top);
+    if (reads) {
+      const PieceSum* p = lists.sum + n * pieces + b * splits;
+      top = part[k].top;
+      for (int s = lane + 32; s < splits; s += 32) top = fmaxf(top, p[s].top);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       for (int s = lane; s < splits; s += 32) {
         // Times 2^(r_s - r), exact; below 2^-126 it adds nothing.  A NaN in the piece is in hi.
-        const PieceSum q = p[s];
+        const PieceSum q = s == lane ? part[k] : p[s];
         const int shift = q.top > -INFINITY ? reference_shift(q.top, top) : 0;
         const float scale = shift < -126 ? 0.f : __int_as_float((127 + min(shift, 0)) << 23);
         add_carried(hi, lo, q.hi * scale, q.lo * scale);
@@ -517,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
       s_hi[b] = hi;
       s_lo[b] = lo;
       s_top[b] = top;
-      s_kind[b] = !isfinite(score) ? 0 : (done ? 2 : (isfinite(top) ? 1 : 0));
+      s_kind[b] = reads ? (isfinite(top) ? 1 : 0) : (isfinite(scores[k]) ? 2 : 0);
     }
   }
   __syncthreads();
@@ -563,15 +586,20 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     return c;
   };
   const int groups = bound_groups(a.M);
-  const auto enter = [&](int e, uint64_t x) {
-    const uint32_t key = (uint32_t)(choice(e / heads, e % heads, x).key >> 32);
-    atomicMax(&s_group[((uint32_t)e * 2654435761u >> 26) & (groups - 1)], key);
+  const auto enter = [&](int e, const Choice& c) {
+    atomicMax(&s_group[((uint32_t)e * 2654435761u >> 26) & (groups - 1)], (uint32_t)(c.key >> 32));
   };
+  Choice own[kHeld];
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (tid + k * kThreads < count) enter(tid + k * kThreads, held[k]);
-#pragma unroll 4
-  for (int e = tid + kHeld * kThreads; e < count; e += kThreads) enter(e, fetch(e / heads, e % heads));
+  for (int k = 0; k < kHeld; ++k) {
+    const int e = tid + k * kThreads;
+    own[k].key = 0;
+    if (e < count) {
+      own[k] = choice(e / heads, e % heads, held[k]);
+      enter(e, own[k]);
+    }
+  }
+  for (int e = tid + kHeld * kThreads; e < count; e += kThreads) enter(e, choice(e / heads, e % heads, fetch(e / heads, e % heads)));
   __syncthreads();
   uint32_t least = min(s_group[lane & (groups - 1)], s_group[(lane + 32) & (groups - 1)]);
   least = __reduce_min_sync(0xffffffffu, least);
@@ -580,7 +608,12 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     const int at = atomicAdd(&s_count, 1);
     if (at < kList) s_list[at] = c;
   };
-  const int steps = (a.M + kStep - 1) / kStep;
+  if (heads == a.M && count <= kHeld * kThreads) {  // all of them are at hand
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (own[k].key >= bound) push(own[k]);
+  }
+  const int steps = heads == a.M && count <= kHeld * kThreads ? 0 : (a.M + kStep - 1) / kStep;
   for (int u = tid; u < pieces * steps; u += kThreads) {
     const int l = u / steps, step = u - l * steps;
     for (int m = step * kStep; m < min(a.M, (step + 1) * kStep); ++m) {
@@ -598,17 +631,8 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     a.out_tokens[at] = c.key == 0 ? -1 : c.flat % a.V;
   };
   if (found <= kList) {
-    for (int i = tid; i < max(found, a.M); i += kThreads) {
-      Choice c{0, 0};
-      int rank = i;
-      if (i < found) {
-        c = s_list[i];
-        rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < found; ++j) rank += before(s_list[j], c) ? 1 : 0;
-      }
-      if (rank < a.M) put(rank, c);
-    }
+    place(s_list, found, a.M, before, put);
+    for (int i = found + tid; i < a.M; i += kThreads) put(i, Choice{0, 0});
     return;
   }
   // Too many equal values at the bound: M times the best after the last one.
@@ -654,11 +678,13 @@ BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bo
     return (int32_t)((V + (whole ? 0 : vec - 1) + per - 1) / per);
   };
   int vectors = 4 * kBatches;
-  while (vectors > 1 && N * B * splits(vectors, true) < 2 * sms && (int64_t)B * splits(vectors / 2, true) * M <= kJoin)
+  while (vectors > 1 && (splits(vectors / 2, true) == 1 || (N * B * splits(vectors, true) < 2 * sms &&
+                                                           (int64_t)B * splits(vectors / 2, true) * M <= kJoin)))
     vectors /= 2;
   p.loads = vectors >= 4 ? 4 : 1;
-  p.batches = vectors / p.loads;
   p.splits = splits(vectors, aligned);
+  const int64_t batch = kThreads * vec * p.loads * (int64_t)p.splits;  // the splits share the row evenly
+  p.batches = (int32_t)((V + (aligned ? 0 : vec - 1) + batch - 1) / batch);
   p.floats = N * B * splits(vectors, false) * (4 + 2 * (int64_t)M);
   return p;
 }
