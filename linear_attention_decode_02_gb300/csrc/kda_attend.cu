@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, Stage<T, D, HG>::CTAS) kda_attend_ke
 // Joins the partials of one query head of the unit that the cut before piece
 // blockIdx.x crosses, if it is the unit's first cut.  The block's warps share
 // the unit's pieces, each lane D/32 channels.
-template <int D, int HG>
-__global__ void __launch_bounds__(128) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
-  constexpr int VEC = D / 32, WARPS = 4, AHEAD = 4;
+template <int D, int HG, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
+  constexpr int VEC = D / 32, AHEAD = 4;
   __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS][D];
   const int c = blockIdx.x, h = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(128) kda_attend_join_kernel(const __grid_const
 #pragma unroll
   for (int j = 0; j < VEC; ++j) s_o[warp][lane * VEC + j] = o[j];
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 128) {
+  for (int d = threadIdx.x; d < D; d += 32 * WARPS) {
     float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
@@ -412,15 +412,23 @@ cudaError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream
   }
 }
 
+template <int D, int HG>
+cudaError_t launch_join_heads(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  // Few units are cut into many pieces each: more warps share them.
+  const int64_t units = (int64_t)a.N * a.Hkv * ((a.Hq / a.Hkv + HG - 1) / HG);
+  const dim3 grid(p.ctas, HG);
+  if (p.ctas > 32 * units) return launch_pdl(kda_attend_join_kernel<D, HG, 16>, grid, dim3(512), 0, s, 1, a, p.ctas);
+  return launch_pdl(kda_attend_join_kernel<D, HG, 4>, grid, dim3(128), 0, s, 1, a, p.ctas);
+}
+
 template <int D>
 cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  const dim3 grid(p.ctas, p.heads), threads(128);
   switch (p.heads) {
-    case 1: return launch_pdl(kda_attend_join_kernel<D, 1>, grid, threads, 0, s, 1, a, p.ctas);
-    case 2: return launch_pdl(kda_attend_join_kernel<D, 2>, grid, threads, 0, s, 1, a, p.ctas);
-    case 4: return launch_pdl(kda_attend_join_kernel<D, 4>, grid, threads, 0, s, 1, a, p.ctas);
-    case 8: return launch_pdl(kda_attend_join_kernel<D, 8>, grid, threads, 0, s, 1, a, p.ctas);
-    default: return launch_pdl(kda_attend_join_kernel<D, 16>, grid, threads, 0, s, 1, a, p.ctas);
+    case 1: return launch_join_heads<D, 1>(a, p, s);
+    case 2: return launch_join_heads<D, 2>(a, p, s);
+    case 4: return launch_join_heads<D, 4>(a, p, s);
+    case 8: return launch_join_heads<D, 8>(a, p, s);
+    default: return launch_join_heads<D, 16>(a, p, s);
   }
 }
 

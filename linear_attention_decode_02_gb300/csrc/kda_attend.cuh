@@ -165,7 +165,10 @@ __device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
   return note;
 }
 
-// 16 bytes to shared memory, or zeros where live is false (src is then not read).
+// 16 bytes to shared memory; zeros where live is false (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -188,9 +191,11 @@ struct PageCopies {
   static constexpr int STAGE = 2 * TENSOR;
   static constexpr int RING = STAGES * STAGE;  // bytes of a warp
   static constexpr int CHUNKS = ROW / 16;
-  static_assert(SUBS >= 1 && SUBS * KEYS * WARPS == kTile && 2 * KEYS <= 32 && KEYS * CHUNKS % 32 == 0, "bad shape");
+  // One pass of the warp copies 32 chunks: part of a row, or PASS_ROWS rows.
+  static constexpr int PASSES = KEYS * CHUNKS / 32;
+  static_assert(SUBS >= 1 && SUBS * KEYS * WARPS == kTile && 2 * KEYS <= 32 && PASSES * 32 == KEYS * CHUNKS, "bad shape");
   struct Notes {
-    int64_t offset[2 * KEYS];  // elements; -1: not attended to
+    const char* row[2 * KEYS];  // keys, then values; of a position not attended to: the first page
     uint32_t live[STAGES];
   };
 
@@ -199,7 +204,8 @@ struct PageCopies {
   Notes& notes;
   uint32_t ring;
   int units, groups, warp, lane;
-  int64_t page_stride, token_stride, head_stride;  // of keys for the first KEYS lanes, of values for the next
+  const char* data;                                // of keys for the first KEYS lanes, of values for the next
+  int64_t page_stride, token_stride, head_stride;  // elements
   Walk at;
   int sub, page, token;  // page 0: none
 
@@ -208,6 +214,7 @@ struct PageCopies {
       : a(a_), place(p), notes(n), ring(static_cast<uint32_t>(__cvta_generic_to_shared(ring_))), units(units_),
         groups(groups_), warp(warp_), lane(lane_), sub(0), page(0), token(0) {
     const PageView& mine = lane < KEYS ? a.kp : a.vp;
+    data = static_cast<const char*>(mine.data);
     page_stride = mine.page;
     token_stride = mine.token;
     head_stride = mine.head;
@@ -225,27 +232,32 @@ struct PageCopies {
       }
     }
   }
+  // Pass i: its row among keys and values, its chunk of the row, and where that goes in a stage.
+  __device__ __forceinline__ int row_of(int i) const { return (i * 32 + lane) / CHUNKS; }
+  __device__ __forceinline__ int chunk_of(int i) const { return (i * 32 + lane) % CHUNKS; }
+  __device__ __forceinline__ uint32_t target(int i) const {
+    return row_of(i) * ROW + ((SWIZZLE ? chunk_of(i) ^ (row_of(i) & 7) : chunk_of(i)) << 4);
+  }
   // Copies the next stage's positions to `stage` and closes a copy group, empty at the end of the piece.
   __device__ __forceinline__ void copy(int stage) {
     if (at.tile < place.stop) {
       const bool live = page > 0 && page < a.num_pages;
       const uint32_t mask = __ballot_sync(0xffffffffu, live) & ((1u << KEYS) - 1);
       __syncwarp();
-      if (lane < 2 * KEYS)
-        notes.offset[lane] =
-            live ? page * page_stride + token * token_stride + (at.group / groups) * head_stride : -1;
+      if (lane < 2 * KEYS) {
+        const int64_t offset = page * page_stride + token * token_stride + (at.group / groups) * head_stride;
+        notes.row[lane] = data + (live ? offset * (int)sizeof(T) : 0);
+      }
       if (lane == 0) notes.live[stage] = mask;
       __syncwarp();
+      const uint32_t base = ring + stage * STAGE;
+      if (mask == (1u << KEYS) - 1) {
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const char* data = static_cast<const char*>(kv == 0 ? a.kp.data : a.vp.data);
+        for (int i = 0; i < 2 * PASSES; ++i) copy16(base + target(i), notes.row[row_of(i)] + chunk_of(i) * 16);
+      } else {
 #pragma unroll
-        for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
-          const int row = (i * 32 + lane) / CHUNKS, chunk = (i * 32 + lane) % CHUNKS;
-          const int64_t offset = notes.offset[kv * KEYS + row];
-          copy16(ring + stage * STAGE + kv * TENSOR + row * ROW + ((SWIZZLE ? chunk ^ (row & 7) : chunk) << 4),
-                 data + (offset < 0 ? 0 : offset * (int)sizeof(T) + chunk * 16), offset >= 0);
-        }
+        for (int i = 0; i < 2 * PASSES; ++i)
+          copy16(base + target(i), notes.row[row_of(i)] + chunk_of(i) * 16, mask >> (row_of(i) % KEYS) & 1);
       }
       if (++sub == SUBS) {
         sub = 0;

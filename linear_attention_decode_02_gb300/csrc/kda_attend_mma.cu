@@ -26,15 +26,18 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kKeys = 16;  // positions of a stage
 static_assert(kWarps * kKeys == kTile, "a tile is one stage of every warp");
 
-template <int D>
+// Blocks a SM and stages a warp: about 192 KB of rings a SM in any case, and
+// as many warps as leave a stage something to do.
+constexpr int blocks_per_sm(int D) { return D == 64 ? 4 : (D == 128 ? 2 : 1); }
+template <int D, int HG>
 struct Shape {
-  static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int CTAS = D == 256 ? 1 : 2;  // a SM
+  static constexpr int CTAS = blocks_per_sm(D);
+  static constexpr int STAGES = 3;
   using Copies = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true>;
 };
 template <int D, int HG>
 constexpr int smem_bytes() {
-  return kWarps * Shape<D>::Copies::RING + (kWarps - 1) * HG * D * 4;
+  return kWarps * Shape<D, HG>::Copies::RING + (kWarps - 1) * 8 * D * 4;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -64,9 +67,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 template <int D, int HG>
-__global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
-  using Copies = typename Shape<D>::Copies;
-  constexpr int STAGES = Shape<D>::STAGES, ROW = Copies::ROW;
+__global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
+  using Copies = typename Shape<D, HG>::Copies;
+  constexpr int STAGES = Shape<D, HG>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 16, NT = D / 8;
   constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
   static_assert(HG == 8 || HG == 16, "16 rows of queries");
@@ -87,16 +90,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
   }
 
   Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
+  // This lane's address for step k within keys, or values: offset[k % 4] + k / 4 * 128.
+  uint32_t key_at[4], value_at[4];
+  {
+    const int krow = ((lane >> 4) << 3) + (lane & 7), khalf = (lane >> 3) & 1, vrow = lane & 15, vhalf = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      key_at[k] = krow * ROW + (((2 * k + khalf) ^ (krow & 7)) << 4);
+      value_at[k] = Copies::TENSOR + vrow * ROW + (((2 * k + vhalf) ^ (vrow & 7)) << 4);
+    }
+  }
 #pragma unroll 1
   for (int s = 0; s < STAGES - 1; ++s) copies.copy(s);
 
   Walk walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
-  while (walk.tile < place.stop) {
-    const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
-    const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + walk.n * a.q_rs + (hk * G + g0) * a.q_hs;
-    uint32_t q[KSTEPS][PAIR ? 2 : 4];
+  uint32_t q_next[KSTEPS][PAIR ? 2 : 4];  // of the next unit, on their way while this one is worked on
+  const auto load_q = [&](const Walk& w) {
+    const int hk = w.group / groups, g0 = (w.group - hk * groups) * HG, heads = min(HG, G - g0);
+    const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + w.n * a.q_rs + (hk * G + g0) * a.q_hs;
 #pragma unroll
     for (int k = 0; k < KSTEPS; ++k)
 #pragma unroll
@@ -106,12 +119,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
           return h < heads ? __ldg(reinterpret_cast<const uint32_t*>(qh + h * a.q_hs + col)) : 0u;
         };
         if constexpr (PAIR) {
-          q[k][half] = word(g);
+          q_next[k][half] = word(g);
         } else {
-          q[k][2 * half] = word(g);
-          q[k][2 * half + 1] = word(g + 8);
+          q_next[k][2 * half] = word(g);
+          q_next[k][2 * half + 1] = word(g + 8);
         }
       }
+  };
+  load_q(walk);
+  while (walk.tile < place.stop) {
+    const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
+    uint32_t q[KSTEPS][PAIR ? 2 : 4];
+#pragma unroll
+    for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < (PAIR ? 2 : 4); ++i) q[k][i] = q_next[k][i];
+    Walk after = walk;
+    if (walk.unit_end < place.stop) {
+      after.next_unit(a, units);
+      if constexpr (D < 256) load_q(after);
+    }
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -132,17 +159,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
       __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
       const uint32_t live = s_notes[warp].live[stage];
       copies.copy(stage == 0 ? STAGES - 1 : stage - 1);
-      const uint32_t keys = copies.ring + stage * Copies::STAGE, values = keys + Copies::TENSOR;
+      const uint32_t base = copies.ring + stage * Copies::STAGE;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
 
       float s[2][2][4] = {};  // [even / odd step][positions 0..7 / 8..15]
       {
-        const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-        const uint32_t base = keys + row * ROW;
 #pragma unroll
         for (int k = 0; k < KSTEPS; ++k) {
           uint32_t b[4];
-          ldmatrix4(b, base + (((k * 2 + half) ^ (row & 7)) << 4));
+          ldmatrix4(b, base + key_at[k % 4] + k / 4 * 128);
           if constexpr (PAIR) {
             mma(s[k & 1][0], q[k][0], 0u, q[k][1], 0u, b[0], b[1]);
             mma(s[k & 1][1], q[k][0], 0u, q[k][1], 0u, b[2], b[3]);
@@ -197,12 +222,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
         }
       }
       {
-        const int row = lane & 15, half = lane >> 4;
-        const uint32_t base = values + row * ROW;
 #pragma unroll
         for (int k = 0; k < KSTEPS; ++k) {
           uint32_t b[4];
-          ldmatrix4_trans(b, base + (((k * 2 + half) ^ (row & 7)) << 4));
+          ldmatrix4_trans(b, base + value_at[k % 4] + k / 4 * 128);
           if constexpr (PAIR) {
             mma(o[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[0], b[1]);
             mma(o[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2], b[3]);
@@ -226,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
         s_l[parity][warp][g + 8 * r] = l[r];
       }
     }
-    __syncthreads();  // warp 0 has left the last unit's outputs too
+    __syncthreads();  // all have left the last unit's outputs too
     float M[RS], f[RS];
 #pragma unroll
     for (int r = 0; r < RS; ++r) {
@@ -235,66 +258,72 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::CTAS) kda_attend_mma_kerne
       for (int w = 1; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[parity][w][g + 8 * r]);
       f[r] = ex2(m[r] - (M[r] == -INFINITY ? 0.f : M[r]));
     }
+    // Warp w finishes the w-th quarter of the channels: it keeps its own part
+    // of that and hands over the rest, to place (its warp, as the owner counts),
+    // 8 heads at a time.
+    constexpr int QUARTER = NT / kWarps, QD = D / kWarps;
     float* shared_o = reinterpret_cast<float*>(smem + kWarps * Copies::RING);
-    if (warp != 0) {
-      float* dst = shared_o + (warp - 1) * HG * D;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int d = i * 8 + 2 * t4;
-        if constexpr (PAIR) {
-          *reinterpret_cast<float2*>(dst + g * D + d) = make_float2((o[i][0] + o[i][2]) * f[0], (o[i][1] + o[i][3]) * f[0]);
-        } else {
-          *reinterpret_cast<float2*>(dst + g * D + d) = make_float2(o[i][0] * f[0], o[i][1] * f[0]);
-          *reinterpret_cast<float2*>(dst + (g + 8) * D + d) = make_float2(o[i][2] * f[RS - 1], o[i][3] * f[RS - 1]);
-        }
-      }
-    }
-    __syncthreads();
+    const auto part = [&](int owner, int from) {
+      return shared_o + (owner * (kWarps - 1) + (from - owner - 1 + kWarps) % kWarps) * 8 * QD;
+    };
     const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
     const bool at_start = walk.unit_start <= place.start;
-    if (warp == 0) {
-      const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
+    const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
 #pragma unroll
-      for (int r = 0; r < RS; ++r) {
-        const int h = g + 8 * r;
-        const float ref = M[r] == -INFINITY ? 0.f : M[r];
-        float L = 0.f;
+    for (int r = 0; r < RS; ++r) {
+      if (r > 0) __syncthreads();  // all have taken the first heads
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) L = fmaf(ex2(s_m[parity][w][h] - ref), s_l[parity][w][h], L);
-        if (h < heads) {
-          const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
-          const float scale = L == 0.f ? 0.f : 1.f / L;
+      for (int i = 0; i < NT; ++i) {
+        const int owner = i / QUARTER;
+        o[i][2 * r] = (PAIR ? o[i][0] + o[i][2] : o[i][2 * r]) * f[r];
+        o[i][2 * r + 1] = (PAIR ? o[i][1] + o[i][3] : o[i][2 * r + 1]) * f[r];
+        if (owner != warp)
+          *reinterpret_cast<float2*>(part(owner, warp) + g * QD + (i % QUARTER) * 8 + 2 * t4) =
+              make_float2(o[i][2 * r], o[i][2 * r + 1]);
+      }
+      __syncthreads();
+      const int h = g + 8 * r;
+      if (h >= heads) continue;
+      const float ref = M[r] == -INFINITY ? 0.f : M[r];
+      float L = 0.f;
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const int d = i * 8 + 2 * t4;
-            float x = PAIR ? (o[i][0] + o[i][2]) * f[0] : o[i][2 * r] * f[r];
-            float y = PAIR ? (o[i][1] + o[i][3]) * f[0] : o[i][2 * r + 1] * f[r];
+      for (int w = 0; w < kWarps; ++w) L = fmaf(ex2(s_m[parity][w][h] - ref), s_l[parity][w][h], L);
+      const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
+      const float scale = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-            for (int w = 0; w < kWarps - 1; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(shared_o + (w * HG + h) * D + d);
-              x += v.x;
-              y += v.y;
-            }
-            if (whole) {
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
-            } else {
-              *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
-            }
-          }
-          if (t4 == 0) {
-            if (!whole) {
-              ws.ml_of(slot, h)[0] = M[r];
-              ws.ml_of(slot, h)[1] = L;
-            } else if (a.lse != nullptr) {
-              a.lse[head] = log_sum(ref, L);
-            }
-          }
+      for (int i = 0; i < NT; ++i) {
+        if (i / QUARTER != warp) continue;
+        const int d = i * 8 + 2 * t4;
+        float x = o[i][2 * r], y = o[i][2 * r + 1];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(shared_o + (warp * (kWarps - 1) + w - 1) * 8 * QD + g * QD +
+                                                            (i % QUARTER) * 8 + 2 * t4);
+          x += v.x;
+          y += v.y;
+        }
+        if (whole) {
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
+        } else {
+          *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
         }
       }
-      if (lane == 0 && at_start) ws.note[c] = note_of(walk, place);
+      if (t4 == 0 && warp == 0) {
+        if (!whole) {
+          ws.ml_of(slot, h)[0] = M[r];
+          ws.ml_of(slot, h)[1] = L;
+        } else if (a.lse != nullptr) {
+          a.lse[head] = log_sum(ref, L);
+        }
+      }
     }
+    if (threadIdx.x == 0 && at_start) ws.note[c] = note_of(walk, place);
     parity ^= 1;
-    if (walk.tile == walk.unit_end) walk.next_unit(a, units);
+    if constexpr (D == 256) {
+      if (walk.unit_end < place.stop) load_q(after);  // no registers for them any sooner
+    }
+    after.tile = walk.tile;
+    walk = after;
   }
   copy_wait<0>();
 }
@@ -312,9 +341,9 @@ cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
 
 AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms) {
   AttendPlan p;
-  p.ctas = (D == 256 ? Shape<256>::CTAS : Shape<128>::CTAS) * sms;
   // 16 heads of 256 channels would not leave the registers for their outputs.
   p.heads = G <= 8 || D == 256 ? 8 : 16;
+  p.ctas = blocks_per_sm(D) * sms;
   p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
   return p;
 }
