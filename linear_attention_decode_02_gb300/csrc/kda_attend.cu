@@ -389,7 +389,7 @@ cudaError_t launch_attend(const AttendArgs& a, int ctas, cudaStream_t s) {
   constexpr int KB = 32 / HG < 8 ? 32 / HG : (D == 256 ? 4 : 8);
   constexpr int bytes = Stage<T, D, HG>::BYTES;
   static std::atomic<bool> set[64];
-  const cudaError_t e = ensure_smem(kda_attend_kernel<T, D, HG, KB>, bytes, set);
+  const cudaError_t e = allow_shared(kda_attend_kernel<T, D, HG, KB>, bytes, set);
   if (e != cudaSuccess) return e;
   return launch_pdl(kda_attend_kernel<T, D, HG, KB>, dim3(ctas), dim3(kThreads), bytes, s, 1, a);
 }

@@ -10,10 +10,27 @@
 // cuts at most two units, so the workspace is fixed by the grid.
 #pragma once
 
+#include <atomic>
+
 #include "kda_cache.h"
 #include "kda_device.cuh"
 
 namespace kda {
+
+// Lets `k` use `bytes` of dynamic shared memory on the current device; `set`
+// (one flag a device) remembers where that was done.
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel k, int bytes, std::atomic<bool> (&set)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  // idempotent, so two host threads that both get here set the same value
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 constexpr int kTile = 64;  // positions of a tile
 

@@ -332,7 +332,7 @@ template <int D, int HG>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D, HG>();
   static std::atomic<bool> set[64];
-  const cudaError_t e = ensure_smem(kda_attend_mma_kernel<D, HG>, bytes, set);
+  const cudaError_t e = allow_shared(kda_attend_mma_kernel<D, HG>, bytes, set);
   if (e != cudaSuccess) return e;
   return launch_pdl(kda_attend_mma_kernel<D, HG>, dim3(p.ctas), dim3(kThreads), bytes, s, 1, a);
 }

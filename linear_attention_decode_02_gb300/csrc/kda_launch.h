@@ -6,8 +6,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace kda {
 
 enum : int { KDA_DT_F32 = 0, KDA_DT_BF16 = 1 };
@@ -97,22 +95,6 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-}
-
-// Lets `k` use `bytes` of dynamic shared memory on the current device; set_flags
-// (64 of them, one a device) remember where that was done.
-template <typename Kernel>
-inline cudaError_t ensure_smem(Kernel k, size_t bytes, std::atomic<bool>* set_flags) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && !set_flags[dev].load(std::memory_order_acquire)) {
-    // idempotent, so two host threads that both get here set the same value
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    set_flags[dev].store(true, std::memory_order_release);
-  }
-  return cudaSuccess;
 }
 
 // Launchers: return the launch error (cudaSuccess on success).

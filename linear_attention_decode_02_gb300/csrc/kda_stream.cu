@@ -678,6 +678,20 @@ __global__ void kda_selftest_wait_kernel() {
 
 namespace {
 
+template <typename Kernel>
+cudaError_t ensure_smem(Kernel k, size_t bytes, std::atomic<bool>* set_flags) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && !set_flags[dev].load(std::memory_order_acquire)) {
+    // idempotent, so two host threads that both get here set the same value
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    set_flags[dev].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
 template <typename StateT, int PARTS>
 cudaError_t launch_t1_stream_typed(const T1Args& a, int sm_count, cudaStream_t s) {
   CUtensorMap map;
