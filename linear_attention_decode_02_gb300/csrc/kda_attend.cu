@@ -294,29 +294,55 @@ __global__ void __launch_bounds__(kThreads, Stage<T, D, HG>::CTAS) kda_attend_ke
   copy_wait<0>();
 }
 
-// Joins the partials of one query head of the unit that the cut before piece
-// blockIdx.x crosses, if it is the unit's first cut.  The block's warps share
-// the unit's pieces, each lane D/32 channels.
-template <int D, int HG, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
-  constexpr int VEC = D / 32, AHEAD = 4;
+// Joins the partials of one query head of a unit that lies in several pieces.
+// BY_CUT: block (c, h) of 4 warps looks at the cut before piece c and works if
+// it is the first that crosses its unit, which any number of units allows.
+// Otherwise block (u, h) of 16 warps finds unit u itself: for few units, cut
+// into many pieces each.  The block's warps share the pieces, each lane D/32
+// channels.
+template <int D, int HG, bool BY_CUT>
+__global__ void __launch_bounds__(BY_CUT ? 128 : 512) kda_attend_join_kernel(const __grid_constant__ AttendArgs a, int C) {
+  constexpr int VEC = D / 32, AHEAD = 4, WARPS = BY_CUT ? 4 : 16;
   __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS][D];
-  const int c = blockIdx.x, h = blockIdx.y;
+  const int h = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
   const Workspace ws(a.work, C, HG, D);
-  const PieceNote note = ws.note[c];
-  if (note.n < 0) return;
   const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG;
+  PieceNote note;
+  if constexpr (BY_CUT) {
+    note = ws.note[blockIdx.x];
+    if (note.n < 0) return;
+  } else {
+    const int units = a.Hkv * groups;
+    note.n = blockIdx.x / units;
+    note.group = blockIdx.x - note.n * units;
+    int64_t before = 0, all = 0;
+    for (int n = lane; n < a.N; n += 32) {
+      const int tiles = span_of(a, n).tiles;
+      all += tiles;
+      before += n < note.n ? tiles : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    const int tiles = span_of(a, note.n).tiles;
+    note.tiles = all * units;
+    note.unit_start = before * units + (int64_t)note.group * tiles;
+    note.unit_end = note.unit_start + tiles;
+  }
   const int hk = note.group / groups, g0 = (note.group - hk * groups) * HG;
   if (h >= min(HG, G - g0)) return;
   const int64_t T = note.tiles;
   const int pieces = pieces_of(T, C);
-  const int first = (int)piece_of(piece_start(c, T, pieces) - 1, T, pieces);
+  const int first = (int)piece_of(BY_CUT ? piece_start(blockIdx.x, T, pieces) - 1 : note.unit_start, T, pieces);
   const int64_t first_start = piece_start(first, T, pieces);
-  if (first_start > note.unit_start) return;  // an earlier cut crosses this unit too
+  if (BY_CUT && first_start > note.unit_start) return;  // an earlier cut crosses this unit too
   const int last = (int)piece_of(note.unit_end - 1, T, pieces);
+  if (!BY_CUT && first == last) return;  // finished by its piece
 
   // The first piece may hold another unit before this one.
   const auto slot_of = [&](int i) { return 2 * (int64_t)i + (i == first && first_start < note.unit_start ? 1 : 0); };
@@ -414,11 +440,10 @@ cudaError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream
 
 template <int D, int HG>
 cudaError_t launch_join_heads(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  // Few units are cut into many pieces each: more warps share them.
   const int64_t units = (int64_t)a.N * a.Hkv * ((a.Hq / a.Hkv + HG - 1) / HG);
-  const dim3 grid(p.ctas, HG);
-  if (p.ctas > 32 * units) return launch_pdl(kda_attend_join_kernel<D, HG, 16>, grid, dim3(512), 0, s, 1, a, p.ctas);
-  return launch_pdl(kda_attend_join_kernel<D, HG, 4>, grid, dim3(128), 0, s, 1, a, p.ctas);
+  if (8 * units <= p.ctas)
+    return launch_pdl(kda_attend_join_kernel<D, HG, false>, dim3((unsigned)units, HG), dim3(512), 0, s, 1, a, p.ctas);
+  return launch_pdl(kda_attend_join_kernel<D, HG, true>, dim3(p.ctas, HG), dim3(128), 0, s, 1, a, p.ctas);
 }
 
 template <int D>

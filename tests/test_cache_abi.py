@@ -252,8 +252,9 @@ def test_attention_refuses_bad_scalars_and_tables(lib):
 
 
 def test_attention_workspace_query(lib):
-    small = binding.kda_paged_attention_workspace(8, 8, 64, BF16, 152)
-    assert 0 < small < binding.kda_paged_attention_workspace(64, 8, 128, BF16, 152) < 1 << 24
+    for shape in ((8, 8, 64), (64, 8, 128), (40, 2, 256)):
+        for dtype in (BF16, torch.float32):
+            assert 0 < binding.kda_paged_attention_workspace(*shape, dtype, 152) < 1 << 24
     for args in ((8, 3, 64, BF16, 152), (8, 0, 64, BF16, 152), (8, 8, 80, BF16, 152), (8, 8, 64, torch.int32, 152),
                  (8, 8, 64, BF16, 0)):
         with pytest.raises(binding.KdaError):
@@ -311,3 +312,29 @@ def test_beam_refuses_tokens_outside_the_vocabulary(lib):
         assert _call_beam(lib, _beam(), eos=eos) == INVALID and "eos_token" in _msg(lib)
     with pytest.raises(binding.KdaError):
         binding.kda_beam_select_workspace(1, 0, 10, 1, BF16, 152)
+
+
+def test_kept_workspaces_are_per_thread_stream_and_size(monkeypatch):
+    import threading
+    made = []
+    monkeypatch.setattr(binding, "_capturing", lambda: bool(made and made[-1] == "capture"))
+    monkeypatch.setattr(binding, "_WORK", threading.local())
+    dev = torch.device("cpu", 0)
+    a = binding._workspace(100, dev, 7)
+    assert binding._workspace(60, dev, 7) is a and a.numel() == 100
+    assert binding._workspace(100, dev, 8) is not a                      # another stream
+    assert binding._workspace(100, torch.device("cpu", 1), 7) is not a   # another device
+    b = binding._workspace(101, dev, 7)
+    assert b is not a and binding._workspace(1, dev, 7) is b             # grown
+    other = []
+    t = threading.Thread(target=lambda: other.append(binding._workspace(1, dev, 7)))
+    t.start()
+    t.join()
+    assert other[0] is not b                                             # another thread
+    made.append("capture")
+    c = binding._workspace(1, dev, 7)
+    assert c is not b and binding._workspace(1, dev, 7) is not c         # a captured call has its own
+    made.append("eager")
+    for s in range(100):
+        binding._workspace(1, dev, 100 + s)
+    assert len(binding._WORK.kept) <= binding._WORK_MAX
