@@ -87,20 +87,45 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
   return s;
 }
 
-// Finds, with the whole block, the tiles of all sequences and where piece c lies
-// in them; start == stop where there is no such piece.
+// The tiles of all sequences and where piece c lies in them, found by the whole
+// block; start == stop where there is no such piece.
 struct Place {
   int64_t T;       // all tiles
   int64_t start, stop;
   int n;           // sequence of tile `start`
   int64_t before;  // tiles before sequence n
+  // False where there is no piece c.
+  __device__ __forceinline__ bool cut(int64_t tiles, int c, int ctas) {
+    T = tiles;
+    const int pieces = pieces_of(T, ctas);
+    start = stop = before = 0;
+    n = 0;
+    if (c >= pieces) return false;
+    start = piece_start(c, T, pieces);
+    stop = piece_start(c + 1, T, pieces);
+    return true;
+  }
 };
 template <int THREADS>
 __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int c, int ctas) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place p;
+  if (a.N <= 32) {  // a sequence a lane, every warp alone
+    const int64_t mine = lane < a.N ? (int64_t)span_of(a, lane).tiles * units : 0;
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += up;
+    }
+    if (!p.cut(__shfl_sync(0xffffffffu, scan, 31), c, ctas)) return p;
+    p.n = __popc(__ballot_sync(0xffffffffu, scan <= p.start));
+    p.before = __shfl_sync(0xffffffffu, scan - mine, p.n);
+    return p;
+  }
   __shared__ int64_t s_warp[THREADS / 32];
   __shared__ int s_n;
   __shared__ int64_t s_before;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.N + THREADS - 1) / THREADS;
   const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
   int64_t mine = 0;
@@ -119,16 +144,8 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
     if (w < warp) prior += s_warp[w];
     total += s_warp[w];
   }
-  Place p;
-  p.T = total * units;
-  const int pieces = pieces_of(p.T, ctas);
-  p.start = p.stop = 0;
-  p.n = 0;
-  p.before = 0;
-  if (c >= pieces) return p;  // the whole block
-  p.start = piece_start(c, p.T, pieces);
-  p.stop = piece_start(c + 1, p.T, pieces);
-  int64_t at = (prior + scan - mine) * units;  // tiles before sequence n0
+  if (!p.cut(total * units, c, ctas)) return p;  // the whole block
+  int64_t at = (prior + scan - mine) * units;    // tiles before sequence n0
   if (n0 < n1 && p.start >= at && p.start < at + mine * units) {
     int n = n0;
     for (; n < n1 - 1; ++n) {
@@ -197,8 +214,8 @@ __device__ __forceinline__ void copy_wait() {
 
 // One warp's copies of keys and values into its ring of stages, KEYS positions
 // each.  A block of WARPS warps shares a tile; a warp's part of it is SUBS
-// stages.  The pages of a stage are looked up while the stage before it is
-// issued, so the table's latency is not in the way.  Positions not attended to
+// stages.  The pages of a stage are looked up two stages before it is issued,
+// so that the table's latency is not in the way.  Positions not attended to
 // become zeros.  SWIZZLE puts 16-byte chunk c of row r at c ^ (r & 7).
 template <typename T, int D, int KEYS, int STAGES, int WARPS, bool SWIZZLE>
 struct PageCopies {
@@ -223,31 +240,42 @@ struct PageCopies {
   int units, groups, warp, lane;
   const char* data;                                // of keys for the first KEYS lanes, of values for the next
   int64_t page_stride, token_stride, head_stride;  // elements
-  Walk at;
-  int sub, page, token;  // page 0: none
+  struct Look {
+    int page, token, head;  // of this lane's position (page 0: none) and of the stage; head -1: no stage
+  };
+  Look next, second;
+  Walk at;  // of the next look-up
+  int sub;
 
   __device__ __forceinline__ PageCopies(const AttendArgs& a_, const Place& p, Notes& n, const void* ring_, int units_,
                                         int groups_, int warp_, int lane_)
       : a(a_), place(p), notes(n), ring(static_cast<uint32_t>(__cvta_generic_to_shared(ring_))), units(units_),
-        groups(groups_), warp(warp_), lane(lane_), sub(0), page(0), token(0) {
+        groups(groups_), warp(warp_), lane(lane_), sub(0) {
     const PageView& mine = lane < KEYS ? a.kp : a.vp;
     data = static_cast<const char*>(mine.data);
     page_stride = mine.page;
     token_stride = mine.token;
     head_stride = mine.head;
     at.start(a, place);
-    look_up();
+    next = look_up();
+    second = look_up();
   }
-  __device__ __forceinline__ void look_up() {
-    page = 0;
-    if (at.tile < place.stop && lane < 2 * KEYS) {
+  __device__ __forceinline__ Look look_up() {
+    Look l{0, 0, -1};
+    if (at.tile < place.stop) {
+      l.head = groups == 1 ? at.group : at.group / groups;
       const int t = (at.sp.tile0 + (int)(at.tile - at.unit_start)) * kTile + (warp * SUBS + sub) * KEYS + lane % KEYS;
-      if (t >= at.sp.first && t < at.sp.end) {
+      if (lane < 2 * KEYS && t >= at.sp.first && t < at.sp.end) {
         const int col = t / a.page_size;
-        token = t - col * a.page_size;
-        page = __ldg(a.table + (int64_t)at.n * a.table_rs + col);
+        l.token = t - col * a.page_size;
+        l.page = __ldg(a.table + (int64_t)at.n * a.table_rs + col);
+      }
+      if (++sub == SUBS) {
+        sub = 0;
+        if (++at.tile == at.unit_end) at.next_unit(a, units);
       }
     }
+    return l;
   }
   // Pass i: its row among keys and values, its chunk of the row, and where that goes in a stage.
   __device__ __forceinline__ int row_of(int i) const { return (i * 32 + lane) / CHUNKS; }
@@ -257,12 +285,12 @@ struct PageCopies {
   }
   // Copies the next stage's positions to `stage` and closes a copy group, empty at the end of the piece.
   __device__ __forceinline__ void copy(int stage) {
-    if (at.tile < place.stop) {
-      const bool live = page > 0 && page < a.num_pages;
+    if (next.head >= 0) {
+      const bool live = next.page > 0 && next.page < a.num_pages;
       const uint32_t mask = __ballot_sync(0xffffffffu, live) & ((1u << KEYS) - 1);
       __syncwarp();
       if (lane < 2 * KEYS) {
-        const int64_t offset = page * page_stride + token * token_stride + (at.group / groups) * head_stride;
+        const int64_t offset = next.page * page_stride + next.token * token_stride + next.head * head_stride;
         notes.row[lane] = data + (live ? offset * (int)sizeof(T) : 0);
       }
       if (lane == 0) notes.live[stage] = mask;
@@ -276,11 +304,8 @@ struct PageCopies {
         for (int i = 0; i < 2 * PASSES; ++i)
           copy16(base + target(i), notes.row[row_of(i)] + chunk_of(i) * 16, mask >> (row_of(i) % KEYS) & 1);
       }
-      if (++sub == SUBS) {
-        sub = 0;
-        if (++at.tile == at.unit_end) at.next_unit(a, units);
-      }
-      look_up();
+      next = second;
+      second = look_up();
     }
     copy_commit();
   }

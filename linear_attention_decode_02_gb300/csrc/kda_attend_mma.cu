@@ -89,20 +89,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     return;
   }
 
-  Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
-  // This lane's address for step k within keys, or values: offset[k % 4] + k / 4 * 128.
-  uint32_t key_at[4], value_at[4];
-  {
-    const int krow = ((lane >> 4) << 3) + (lane & 7), khalf = (lane >> 3) & 1, vrow = lane & 15, vhalf = lane >> 4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      key_at[k] = krow * ROW + (((2 * k + khalf) ^ (krow & 7)) << 4);
-      value_at[k] = Copies::TENSOR + vrow * ROW + (((2 * k + vhalf) ^ (vrow & 7)) << 4);
-    }
-  }
-#pragma unroll 1
-  for (int s = 0; s < STAGES - 1; ++s) copies.copy(s);
-
   Walk walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
@@ -127,6 +113,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
       }
   };
   load_q(walk);
+  Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
+  // This lane's address for step k within keys, or values: offset[k % 4] + k / 4 * 128.
+  uint32_t key_at[4], value_at[4];
+  {
+    const int krow = ((lane >> 4) << 3) + (lane & 7), khalf = (lane >> 3) & 1, vrow = lane & 15, vhalf = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      key_at[k] = krow * ROW + (((2 * k + khalf) ^ (krow & 7)) << 4);
+      value_at[k] = Copies::TENSOR + vrow * ROW + (((2 * k + vhalf) ^ (vrow & 7)) << 4);
+    }
+  }
+#pragma unroll 1
+  for (int s = 0; s < STAGES - 1; ++s) copies.copy(s);
+
   while (walk.tile < place.stop) {
     const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
     uint32_t q[KSTEPS][PAIR ? 2 : 4];
