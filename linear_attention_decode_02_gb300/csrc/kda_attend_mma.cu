@@ -26,13 +26,15 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kKeys = 16;  // positions of a stage
 static_assert(kWarps * kKeys == kTile, "a tile is one stage of every warp");
 
-// Blocks a SM and stages a warp: about 192 KB of rings a SM in any case, and
-// as many warps as leave a stage something to do.
-constexpr int blocks_per_sm(int D) { return D == 64 ? 4 : (D == 128 ? 2 : 1); }
+// Blocks a SM and stages a warp: about 192 KB of rings a SM in any case.  For
+// D = 64, 48 x 6000 positions x 8 key heads (0.39 GB) took 74 us with 2 blocks of 6
+// stages, 82 us with 3 of 4 and 80 us with 4 of 3, and 16 query heads a key head
+// 83, 82 and 113 us.
+constexpr int blocks_per_sm(int D) { return D == 256 ? 1 : 2; }
 template <int D, int HG>
 struct Shape {
   static constexpr int CTAS = blocks_per_sm(D);
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D == 64 ? 6 : 3;
   using Copies = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true>;
 };
 template <int D, int HG>
