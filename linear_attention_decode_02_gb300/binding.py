@@ -343,7 +343,7 @@ def kda_rope_append(q, k, v, phase_steps, seq_lens, page_table, k_pages, v_pages
         q_out = torch.empty_like(q, dtype=k_pages.dtype, memory_format=torch.contiguous_format)
     with _on(dev):
         st = (_module or _native()).rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages,
-                                                q_out, 1 if interleaved else 0, amplitude, _handle(dev))
+                                                q_out, 1 if interleaved else 0, amplitude, _handle(dev), dev.index)
     if st:
         _raise(st)
     return q_out
@@ -391,7 +391,7 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
         if workspace is None:
             workspace = _workspace(_attention_floats(q.size(1), k_pages.size(2), q.size(2), q.dtype, dev.index), dev, stream)
         st = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, window,
-                                              q.size(2) ** -0.5 if scale is None else scale, stream)
+                                              q.size(2) ** -0.5 if scale is None else scale, stream, dev.index)
     if st:
         _raise(st)
     return (out, lse) if return_lse else out
@@ -428,7 +428,8 @@ def kda_beam_select(logits, scores, num_out, finished=None, eos_token=0, out=Non
         if workspace is None:
             floats = _beam_floats(n, logits.size(1), logits.size(2), num_out, logits.dtype, dev.index)
             workspace = _workspace(floats, dev, stream)
-        st = (_module or _native()).beam(logits, scores, finished, workspace, out[0], out[1], out[2], eos_token, stream)
+        st = (_module or _native()).beam(logits, scores, finished, workspace, out[0], out[1], out[2], eos_token, stream,
+                                         dev.index)
     if st:
         _raise(st)
     return out
@@ -438,7 +439,7 @@ def kda_pool_move(pools, src_slots, dst_slots, parents=None):
     """Copies slots of every tensor of `pools` in place; returns None."""
     dev = src_slots.device
     with _on(dev):
-        st = (_module or _native()).move(pools, src_slots, dst_slots, parents, _handle(dev))
+        st = (_module or _native()).move(pools, src_slots, dst_slots, parents, _handle(dev), dev.index)
     if st:
         _raise(st)
 

@@ -67,6 +67,20 @@ bool vectors_aligned(const View& v, int64_t bytes) {
   return true;
 }
 
+// No two elements of a view that is written share an address: every stride
+// spans the axes of smaller strides.
+kda_status need_distinct(const View& v) {
+  for (int i = 0; i < v.ndim; ++i) {
+    if (v.shape[i] <= 1) continue;
+    int64_t inner = 1;
+    for (int j = 0; j < v.ndim; ++j)
+      if (j != i && v.shape[j] > 1 && (v.stride[j] < v.stride[i] || (v.stride[j] == v.stride[i] && j < i)))
+        inner += (v.shape[j] - 1) * v.stride[j];
+    KDA_CHECK(v.stride[i] >= inner, KDA_ERR_INVALID_ARG, "%s: elements overlap along axis %d", v.name, i);
+  }
+  return KDA_OK;
+}
+
 // Key and value pages [num_pages, page_size, Hkv, D] of one dtype and shape.
 kda_status need_pages(const View& K, const View& V, int64_t Hkv, int64_t D) {
   KDA_TRY(need_dtype(K, KDA_F32, KDA_BF16));
@@ -199,6 +213,7 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
   KDA_TRY(need_vec_layout(O));
   KDA_CHECK(is_interleaved == 0 || is_interleaved == 1, KDA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
   KDA_CHECK(std::isfinite(amplitude), KDA_ERR_INVALID_ARG, "amplitude must be finite");
+  for (const View* w : {&O, &KP, &VP}) KDA_TRY(need_distinct(*w));
   if (!same_view(O, Q)) KDA_TRY(no_shared_bytes(O, {&Q}));
   KDA_TRY(no_shared_bytes(O, {&K, &V, &P, &CU, &L, &T, &KP, &VP}));
   KDA_TRY(no_shared_bytes(KP, {&Q, &K, &V, &P, &CU, &L, &T, &VP}));
@@ -254,6 +269,7 @@ kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const 
   KDA_CHECK(n_pools <= kMaxPools, KDA_ERR_UNSUPPORTED, "pools: %d pools, at most %d a call", n_pools, kMaxPools);
   View V[kMaxPools];
   kda::MovePool M[kMaxPools];
+  uintptr_t lo[kMaxPools], hi[kMaxPools];
   for (int32_t i = 0; i < n_pools; ++i) {
     View& v = V[i];
     KDA_TRY(raw_view(pools[i], "pool", &v));
@@ -276,9 +292,10 @@ kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const 
               (long long)v.stride[0]);
     M[i] = {v.data, v.shape[0] <= 1 ? 0 : v.stride[0] * esize(v.dtype), size * esize(v.dtype), 0};
     KDA_TRY(no_alias(v, {&S, &D, &P}));
+    v.range(&lo[i], &hi[i]);
     for (int32_t j = 0; j < i; ++j)
-      KDA_CHECK(!overlap(v, V[j]) || interleaved(v, V[j]) || interleaved(V[j], v), KDA_ERR_ALIAS,
-                "pool %d overlaps pool %d", i, j);
+      KDA_CHECK(hi[i] <= lo[j] || hi[j] <= lo[i] || !overlap(v, V[j]) || interleaved(v, V[j]) || interleaved(V[j], v),
+                KDA_ERR_ALIAS, "pool %d overlaps pool %d", i, j);
   }
   if (N == 0 || K == 0) return KDA_OK;
 

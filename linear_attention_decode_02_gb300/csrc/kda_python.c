@@ -15,7 +15,7 @@
 
 #include "../../include/kda.h"
 
-static PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr;
+static PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_get_device;
 static PyObject* dtypes[3]; /* torch.float32, torch.bfloat16, torch.int32, in kda_dtype order */
 
 static int64_t as_int(PyObject* o, int* bad) {
@@ -24,12 +24,26 @@ static int64_t as_int(PyObject* o, int* bad) {
   return (int64_t)v;
 }
 
-/* Fills *d from tensor t; 0, or -1 with an exception set. */
-static int describe(PyObject* t, kda_tensor* d) {
+/* Fills *d from tensor t of CUDA device `device`; 0, or -1 with an exception set.  A tensor of the host or of another
+ * device is refused: its address would mean something else, or nothing, to the kernels. */
+static int describe(PyObject* t, kda_tensor* d, long device) {
   int bad = 0, i;
+  long where;
   Py_ssize_t n;
-  PyObject *dtype, *shape = NULL, *stride = NULL, *ptr = NULL;
+  PyObject *dtype, *shape = NULL, *stride = NULL, *ptr = NULL, *at;
   memset(d, 0, sizeof(*d));
+  at = PyObject_CallMethodNoArgs(t, s_get_device);
+  if (at == NULL) return -1;
+  where = PyLong_AsLong(at);
+  Py_DECREF(at);
+  if (where == -1 && PyErr_Occurred()) return -1;
+  if (where != device) {
+    if (where < 0)
+      PyErr_Format(PyExc_ValueError, "expected every tensor on cuda:%ld, got one of the host", device);
+    else
+      PyErr_Format(PyExc_ValueError, "expected every tensor on cuda:%ld, got one on cuda:%ld", device, where);
+    return -1;
+  }
   dtype = PyObject_GetAttr(t, s_dtype);
   if (dtype == NULL) return -1;
   d->dtype = -1;
@@ -72,12 +86,12 @@ static int describe(PyObject* t, kda_tensor* d) {
 }
 
 /* Describes the first n arguments into d; p[i] is NULL for None. */
-static int describe_all(PyObject* const* args, Py_ssize_t n, kda_tensor* d, const kda_tensor** p) {
+static int describe_all(PyObject* const* args, Py_ssize_t n, kda_tensor* d, const kda_tensor** p, long device) {
   Py_ssize_t i;
   for (i = 0; i < n; ++i) {
     p[i] = NULL;
     if (args[i] == Py_None) continue;
-    if (describe(args[i], &d[i]) != 0) return -1;
+    if (describe(args[i], &d[i], device) != 0) return -1;
     p[i] = &d[i];
   }
   return 0;
@@ -102,6 +116,11 @@ static int float_of(PyObject* o, float* out) {
   return 0;
 }
 
+static int device_of(PyObject* o, long* out) {
+  *out = PyLong_AsLong(o);
+  return *out == -1 && PyErr_Occurred() ? -1 : 0;
+}
+
 static int stream_of(PyObject* o, void** out) {
   *out = PyLong_AsVoidPtr(o); /* 0: the legacy default stream */
   return *out == NULL && PyErr_Occurred() ? -1 : 0;
@@ -124,16 +143,18 @@ static struct {
   kda_status (*move)(const kda_tensor* const*, int32_t, const kda_tensor*, const kda_tensor*, const kda_tensor*, void*);
 } fn;
 
-/* rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages, q_out, interleaved, amplitude, stream) */
+/* rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages, q_out, interleaved, amplitude, stream, device) */
 static PyObject* rope_append(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   kda_tensor d[10];
   const kda_tensor* p[10];
   int32_t interleaved;
   float amplitude;
+  long device;
   void* stream;
   kda_status st;
   (void)self;
-  if (arity("rope_append", n, 13) != 0 || describe_all(args, 10, d, p) != 0 || int32_of(args[10], &interleaved) != 0 ||
+  if (arity("rope_append", n, 14) != 0 || device_of(args[13], &device) != 0 || describe_all(args, 10, d, p, device) != 0 ||
+      int32_of(args[10], &interleaved) != 0 ||
       float_of(args[11], &amplitude) != 0 || stream_of(args[12], &stream) != 0)
     return NULL;
   Py_BEGIN_ALLOW_THREADS
@@ -142,16 +163,18 @@ static PyObject* rope_append(PyObject* self, PyObject* const* args, Py_ssize_t n
   return PyLong_FromLong((long)st);
 }
 
-/* attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, window, scale, stream) */
+/* attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, window, scale, stream, device) */
 static PyObject* attention(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   kda_tensor d[8];
   const kda_tensor* p[8];
   int32_t window;
   float scale;
+  long device;
   void* stream;
   kda_status st;
   (void)self;
-  if (arity("attention", n, 11) != 0 || describe_all(args, 8, d, p) != 0 || int32_of(args[8], &window) != 0 ||
+  if (arity("attention", n, 12) != 0 || device_of(args[11], &device) != 0 || describe_all(args, 8, d, p, device) != 0 ||
+      int32_of(args[8], &window) != 0 ||
       float_of(args[9], &scale) != 0 || stream_of(args[10], &stream) != 0)
     return NULL;
   Py_BEGIN_ALLOW_THREADS
@@ -160,15 +183,17 @@ static PyObject* attention(PyObject* self, PyObject* const* args, Py_ssize_t n) 
   return PyLong_FromLong((long)st);
 }
 
-/* beam(logits, scores, finished, workspace, out_scores, out_parents, out_tokens, eos_token, stream) */
+/* beam(logits, scores, finished, workspace, out_scores, out_parents, out_tokens, eos_token, stream, device) */
 static PyObject* beam(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   kda_tensor d[7];
   const kda_tensor* p[7];
   int32_t eos;
+  long device;
   void* stream;
   kda_status st;
   (void)self;
-  if (arity("beam", n, 9) != 0 || describe_all(args, 7, d, p) != 0 || int32_of(args[7], &eos) != 0 ||
+  if (arity("beam", n, 10) != 0 || device_of(args[9], &device) != 0 || describe_all(args, 7, d, p, device) != 0 ||
+      int32_of(args[7], &eos) != 0 ||
       stream_of(args[8], &stream) != 0)
     return NULL;
   Py_BEGIN_ALLOW_THREADS
@@ -177,7 +202,7 @@ static PyObject* beam(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   return PyLong_FromLong((long)st);
 }
 
-/* move(pools, src_slots, dst_slots, parents, stream); pools a list or tuple of at most 256 tensors (more are refused
+/* move(pools, src_slots, dst_slots, parents, stream, device); pools a list or tuple of at most 256 tensors (more are refused
  * by the library, from the count alone) */
 static PyObject* move(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   enum { MOST = 256 };
@@ -185,22 +210,22 @@ static PyObject* move(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   const kda_tensor *p[3], *pools[MOST];
   PyObject* list;
   Py_ssize_t count, i;
+  long device;
   void* stream;
   kda_status st;
   (void)self;
-  if (arity("move", n, 5) != 0) return NULL;
-  list = PySequence_Fast(args[0], "pools must be a sequence of tensors");
-  if (list == NULL) return NULL;
+  if (arity("move", n, 6) != 0 || device_of(args[5], &device) != 0) return NULL;
+  list = args[0];
+  if (!PyList_Check(list) && !PyTuple_Check(list)) { /* a tensor would pass for the sequence of its rows */
+    PyErr_SetString(PyExc_TypeError, "pools must be a list or tuple of tensors");
+    return NULL;
+  }
   count = PySequence_Fast_GET_SIZE(list);
   for (i = 0; i < count && i < MOST; ++i) {
-    if (describe(PySequence_Fast_GET_ITEM(list, i), &pool[i]) != 0) {
-      Py_DECREF(list);
-      return NULL;
-    }
+    if (describe(PySequence_Fast_GET_ITEM(list, i), &pool[i], device) != 0) return NULL;
     pools[i] = &pool[i];
   }
-  Py_DECREF(list);
-  if (describe_all(args + 1, 3, d, p) != 0 || stream_of(args[4], &stream) != 0) return NULL;
+  if (describe_all(args + 1, 3, d, p, device) != 0 || stream_of(args[4], &stream) != 0) return NULL;
   Py_BEGIN_ALLOW_THREADS
   st = fn.move(pools, count > MOST ? MOST + 1 : (int32_t)count, p[0], p[1], p[2], stream);
   Py_END_ALLOW_THREADS
@@ -246,6 +271,7 @@ PyMODINIT_FUNC PyInit__kda_python(void) {
   s_stride = PyUnicode_InternFromString("stride");
   s_dtype = PyUnicode_InternFromString("dtype");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  if (s_shape == NULL || s_stride == NULL || s_dtype == NULL || s_data_ptr == NULL) return NULL;
+  s_get_device = PyUnicode_InternFromString("get_device");
+  if (s_shape == NULL || s_stride == NULL || s_dtype == NULL || s_data_ptr == NULL || s_get_device == NULL) return NULL;
   return PyModule_Create(&module);
 }

@@ -338,3 +338,50 @@ def test_kept_workspaces_are_per_thread_stream_and_size(monkeypatch):
     for s in range(100):
         binding._workspace(1, dev, 100 + s)
     assert len(binding._WORK.kept) <= binding._WORK_MAX
+
+
+# ---- the marshalling module ----------------------------------------------------------------
+
+
+def test_module_refuses_host_tensors_and_wrong_arguments(lib):
+    m = binding._native()
+    t = torch.zeros(2, 2)
+    with pytest.raises(ValueError, match="host"):
+        m.beam(t, t, None, t, t, t, t, 0, 0, 0)
+    with pytest.raises(TypeError, match="10 arguments"):
+        m.beam(t)
+    with pytest.raises(TypeError, match="list or tuple"):
+        m.move(t, t, t, None, 0, 0)  # not the rows of a tensor
+    with pytest.raises(AttributeError):
+        m.move([None], t, t, None, 0, 0)
+    with pytest.raises(TypeError):
+        m.rope_append(*[None] * 10, 0, 1.0, 0, "cuda")
+    with pytest.raises(OverflowError):
+        m.attention(*[None] * 8, 2 ** 40, 1.0, 0, 0)
+
+
+def test_module_passes_descriptors_as_they_are(lib):
+    # device -1 is the host's, so descriptors of host memory come as far as the library's own refusals
+    m = binding._native()
+    x, s = torch.zeros(2, 3, 100, dtype=BF16), torch.zeros(2, 3)
+    o = [torch.zeros(2, 4), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 5, dtype=torch.int32)]
+    assert m.beam(x, s, None, torch.zeros(4096), *o, 0, 0, -1) == INVALID and "out_tokens: axis 1" in _msg(lib)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        m.beam(x.to(torch.float64), s, None, s, *o, 0, 0, -1)
+    with pytest.raises(ValueError, match="rank 5"):
+        m.beam(x.view(1, 1, 2, 3, 100), s, None, s, *o, 0, 0, -1)
+    assert m.beam(x, s, None, None, *o, 0, 0, -1) == INVALID and "workspace: null" in _msg(lib)
+    many = [torch.zeros(2, 2) for _ in range(300)]
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    assert m.move(many, i, i, None, 0, -1) == UNSUPPORTED and "at most 256" in _msg(lib)
+    assert m.move([], i, i, None, 0, -1) == INVALID
+    assert m.move((many[0], many[0]), i, i, None, 0, -1) == ALIAS
+
+
+def test_rope_refuses_written_views_whose_elements_overlap(lib):
+    t = _rope()
+    t["k_pages"] = torch.as_strided(torch.zeros(4 * 8 * 2 * 64, dtype=BF16), (4, 8, 2, 64), (512, 128, 32, 1))
+    assert _call_rope(lib, t) == INVALID and "k_pages: elements overlap" in _msg(lib)
+    t = _rope()
+    t["q_out"] = torch.as_strided(torch.zeros(3 * 4 * 64, dtype=BF16), (3, 4, 64), (64, 64, 1))
+    assert _call_rope(lib, t) == INVALID and "q_out: elements overlap" in _msg(lib)

@@ -211,3 +211,30 @@ def test_empty_call_and_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert_rounded(out, ref[0], slack(c, 1.0), "q_out of a replay")
+
+
+def test_pages_past_4_gib():
+    pages, page = 20000, 64
+    pool = torch.zeros(pages, 2, page, 8, 128, dtype=BF16, device="cuda")  # 5 GB
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(3, 24, 128, device="cuda", generator=g).to(BF16)
+    q, k, v = x[:, :8], x[:, 8:16], x[:, 16:]
+    steps = binding.kda_rope_phase_steps(128)
+    lens = torch.tensor([1, 70, 130], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[pages - 1, 0, 0], [0, pages - 2, 0], [0, 0, pages - 9]], dtype=torch.int32, device="cuda")
+    small = torch.zeros(4, 2, page, 8, 128, dtype=BF16, device="cuda")
+    near = torch.tensor([[1, 0, 0], [0, 2, 0], [0, 0, 3]], dtype=torch.int32, device="cuda")
+    a = binding.kda_rope_append(q, k, v, steps, lens, table, pool[:, 0], pool[:, 1])
+    b = binding.kda_rope_append(q, k, v, steps, lens, near, small[:, 0], small[:, 1])
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    for n, p in enumerate((pages - 1, pages - 2, pages - 9)):
+        assert torch.equal(pool[p], small[n + 1]) and torch.count_nonzero(pool[p]) > 0
+    assert torch.count_nonzero(pool[:pages - 9]) == 0
+
+
+def test_host_tensors_are_refused():
+    c = make([3, 4])
+    with pytest.raises(ValueError, match="host"):
+        binding.kda_rope_append(c["q"], c["k"], c["v"], binding.kda_rope_phase_steps(64, device="cpu"), c["lens"],
+                                c["table"], c["k_pages"], c["v_pages"])
