@@ -21,9 +21,12 @@ namespace kda {
 namespace {
 
 constexpr int kMaxPairs = 256;  // head_dim <= 512
-// Rows from which a block takes four of them.  Measured with 48 heads of 128
-// bf16 channels: 23119 rows 97 us (5.9 TB/s; 1 row a block 121 us, 2 rows 98 to
-// 104 us by occupancy), while few rows want a block each (384 rows: 4 us).
+// Small blocks, so that some load while others wait for positions: 23119 rows
+// of 48 heads of 128 bf16 channels take 86 us (6.6 TB/s) with 128 threads, 97 us
+// with 256 and 112 us with 512.
+constexpr int kThreads = 128;
+// Rows from which a block takes four of them: the same 23119 rows take 99 us at
+// one row a block and 88 us at two.  Few rows want a block each (384 rows: 4 us).
 constexpr int kManyRows = 2048;
 
 // Index of the sequence owning `row`: the number of entries of cu[1..N] that
@@ -98,7 +101,7 @@ struct Slot {
 };
 
 template <typename In, typename Out, int VEC, bool INTERLEAVED, int ROWS>
-__global__ void __launch_bounds__(256, 4) kda_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 s_cs[ROWS][kMaxPairs];
   __shared__ int s_pos[ROWS];           // -1: zero output
   __shared__ int64_t s_k[ROWS], s_v[ROWS];  // element offsets of the row's place in its page, or -1
@@ -224,7 +227,7 @@ template <typename In, typename Out, int VEC, int ROWS>
 cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
   auto kernel = a.interleaved ? kda_rope_append_kernel<In, Out, VEC, true, ROWS>
                               : kda_rope_append_kernel<In, Out, VEC, false, ROWS>;
-  return launch_pdl(kernel, dim3((unsigned)((a.R + (int64_t)ROWS - 1) / ROWS)), dim3(256), 0, s, 1, a);
+  return launch_pdl(kernel, dim3((unsigned)((a.R + (int64_t)ROWS - 1) / ROWS)), dim3(kThreads), 0, s, 1, a);
 }
 
 template <typename In, typename Out, int VEC>
