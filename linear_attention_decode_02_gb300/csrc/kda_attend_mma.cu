@@ -35,11 +35,12 @@ template <int D, int HG>
 struct Shape {
   static constexpr int CTAS = blocks_per_sm(D);
   static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr bool QS = D == 256;  // no registers are left for the queries: they lie in shared memory
   using Copies = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true>;
 };
 template <int D, int HG>
 constexpr int smem_bytes() {
-  return kWarps * Shape<D, HG>::Copies::RING + (kWarps - 1) * 8 * D * 4;
+  return kWarps * Shape<D, HG>::Copies::RING + (kWarps - 1) * 8 * D * 4 + (Shape<D, HG>::QS ? HG * D * 2 : 0);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -47,6 +48,9 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ void ldmatrix2(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -94,36 +98,62 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   Walk walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
-  uint32_t q_next[KSTEPS][PAIR ? 2 : 4];  // of the next unit, on their way while this one is worked on
+  // Queries of the next unit, on their way while this one is worked on: the
+  // first product's operand itself, or (QS) the thread's share of HG rows of
+  // 16-byte chunks for shared memory, swizzled like the keys.
+  constexpr bool QS = Shape<D, HG>::QS;
+  constexpr int QN = PAIR ? 2 : 4, SHARE = HG * D / 8 / kThreads;
+  uint32_t q_next[QS ? 1 : KSTEPS][QN];
+  uint4 q_share[QS ? SHARE : 1];
   const auto load_q = [&](const Walk& w) {
     const int hk = w.group / groups, g0 = (w.group - hk * groups) * HG, heads = min(HG, G - g0);
     const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + w.n * a.q_rs + (hk * G + g0) * a.q_hs;
+    if constexpr (QS) {
 #pragma unroll
-    for (int k = 0; k < KSTEPS; ++k)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int col = k * 16 + half * 8 + 2 * t4;
-        const auto word = [&](int h) {
-          return h < heads ? __ldg(reinterpret_cast<const uint32_t*>(qh + h * a.q_hs + col)) : 0u;
-        };
-        if constexpr (PAIR) {
-          q_next[k][half] = word(g);
-        } else {
-          q_next[k][2 * half] = word(g);
-          q_next[k][2 * half + 1] = word(g + 8);
-        }
+      for (int i = 0; i < SHARE; ++i) {
+        const int row = (i * kThreads + threadIdx.x) / (D / 8), chunk = (i * kThreads + threadIdx.x) % (D / 8);
+        q_share[i] = row < heads ? __ldg(reinterpret_cast<const uint4*>(qh + row * a.q_hs) + chunk) : make_uint4(0, 0, 0, 0);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int col = k * 16 + half * 8 + 2 * t4;
+          const auto word = [&](int h) {
+            return h < heads ? __ldg(reinterpret_cast<const uint32_t*>(qh + h * a.q_hs + col)) : 0u;
+          };
+          if constexpr (PAIR) {
+            q_next[k][half] = word(g);
+          } else {
+            q_next[k][2 * half] = word(g);
+            q_next[k][2 * half + 1] = word(g + 8);
+          }
+        }
+    }
+  };
+  char* shared_q = smem + kWarps * Copies::RING + (kWarps - 1) * 8 * D * 4;
+  const auto place_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < SHARE; ++i) {
+      const int row = (i * kThreads + threadIdx.x) / (D / 8), chunk = (i * kThreads + threadIdx.x) % (D / 8);
+      *reinterpret_cast<uint4*>(shared_q + row * ROW + ((chunk ^ (row & 7)) << 4)) = q_share[i];
+    }
+    __syncthreads();
   };
   load_q(walk);
   Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
   // This lane's address for step k within keys, or values: offset[k % 4] + k / 4 * 128.
-  uint32_t key_at[4], value_at[4];
+  uint32_t key_at[4], value_at[4], query_at[4];
   {
+    const int qrow = PAIR ? lane & 7 : lane & 15, qhalf = PAIR ? (lane >> 3) & 1 : lane >> 4;
     const int krow = ((lane >> 4) << 3) + (lane & 7), khalf = (lane >> 3) & 1, vrow = lane & 15, vhalf = lane >> 4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       key_at[k] = krow * ROW + (((2 * k + khalf) ^ (krow & 7)) << 4);
       value_at[k] = Copies::TENSOR + vrow * ROW + (((2 * k + vhalf) ^ (vrow & 7)) << 4);
+      query_at[k] = static_cast<uint32_t>(__cvta_generic_to_shared(shared_q)) + qrow * ROW +
+                    (((2 * k + qhalf) ^ (qrow & 7)) << 4);
     }
   }
 #pragma unroll 1
@@ -131,15 +161,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
 
   while (walk.tile < place.stop) {
     const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
-    uint32_t q[KSTEPS][PAIR ? 2 : 4];
+    uint32_t q[QS ? 1 : KSTEPS][QN];
+    if constexpr (QS) {
+      place_q();
+    } else {
 #pragma unroll
-    for (int k = 0; k < KSTEPS; ++k)
+      for (int k = 0; k < KSTEPS; ++k)
 #pragma unroll
-      for (int i = 0; i < (PAIR ? 2 : 4); ++i) q[k][i] = q_next[k][i];
+        for (int i = 0; i < QN; ++i) q[k][i] = q_next[k][i];
+    }
     Walk after = walk;
     if (walk.unit_end < place.stop) {
       after.next_unit(a, units);
-      if constexpr (D < 256) load_q(after);
+      load_q(after);
     }
     float o[NT][4];
 #pragma unroll
@@ -170,12 +204,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
         for (int k = 0; k < KSTEPS; ++k) {
           uint32_t b[4];
           ldmatrix4(b, base + key_at[k % 4] + k / 4 * 128);
+          uint32_t x[4];
+          if constexpr (QS && PAIR) ldmatrix2(x[0], x[1], query_at[k % 4] + k / 4 * 128);
+          if constexpr (QS && !PAIR) ldmatrix4(x, query_at[k % 4] + k / 4 * 128);
+          if constexpr (!QS) {
+#pragma unroll
+            for (int i = 0; i < QN; ++i) x[i] = q[k][i];
+          }
           if constexpr (PAIR) {
-            mma(s[k & 1][0], q[k][0], 0u, q[k][1], 0u, b[0], b[1]);
-            mma(s[k & 1][1], q[k][0], 0u, q[k][1], 0u, b[2], b[3]);
+            mma(s[k & 1][0], x[0], 0u, x[1], 0u, b[0], b[1]);
+            mma(s[k & 1][1], x[0], 0u, x[1], 0u, b[2], b[3]);
           } else {
-            mma(s[k & 1][0], q[k][0], q[k][1], q[k][2], q[k][3], b[0], b[1]);
-            mma(s[k & 1][1], q[k][0], q[k][1], q[k][2], q[k][3], b[2], b[3]);
+            mma(s[k & 1][0], x[0], x[1], x[2], x[3], b[0], b[1]);
+            mma(s[k & 1][1], x[0], x[1], x[2], x[3], b[2], b[3]);
           }
         }
       }
@@ -321,9 +362,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     }
     if (threadIdx.x == 0 && at_start) ws.note[c] = note_of(walk, place);
     parity ^= 1;
-    if constexpr (D == 256) {
-      if (walk.unit_end < place.stop) load_q(after);  // no registers for them any sooner
-    }
     after.tile = walk.tile;
     walk = after;
   }
@@ -343,8 +381,7 @@ cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
 
 AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms) {
   AttendPlan p;
-  // 16 heads of 256 channels would not leave the registers for their outputs.
-  p.heads = G <= 8 || D == 256 ? 8 : 16;
+  p.heads = G <= 8 ? 8 : 16;
   p.ctas = blocks_per_sm(D) * sms;
   p.floats = (int64_t)p.ctas * kNoteFloats + 2LL * p.ctas * p.heads * (2 + D);
   return p;
@@ -357,6 +394,7 @@ cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStre
     case 128 * 16 + 7: return launch<128, 8>(a, p, s);
     case 128 * 16 + 15: return launch<128, 16>(a, p, s);
     case 256 * 16 + 7: return launch<256, 8>(a, p, s);
+    case 256 * 16 + 15: return launch<256, 16>(a, p, s);
     default: return cudaErrorInvalidValue;
   }
 }
