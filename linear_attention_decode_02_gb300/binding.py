@@ -5,14 +5,13 @@ Each function has the name of its C entry point, turns torch tensors into
 ``KdaError`` on any non-OK status.  All arithmetic runs in the library's
 CUDA kernels; there is no fallback path: if ``libkda.so`` is missing the
 first call raises.  The cache and beam calls are marshalled by a small CPython
-module (``csrc/kda_python.c``) instead of ctypes, for their host time.
+module (``csrc/kda_python.cpp``) instead of ctypes, for their host time.
 """
 
 from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import importlib.util
 import math
 import os
@@ -166,13 +165,9 @@ def _stream(t):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
-# The current device without the lazy-initialisation check, which a CUDA tensor's existence has passed.
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
 def _on(dev):
     """Device guard for the call, entered only when `dev` is not already current."""
-    if dev.type == "cuda" and dev.index == _current_device():
+    if dev.type == "cuda" and dev.index == torch.cuda.current_device():
         return _SAME_DEVICE
     return torch.cuda.device(dev)
 
@@ -293,42 +288,12 @@ def _native():
                 spec = importlib.util.spec_from_file_location("_kda_python", _MODULE_PATH)
                 m = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(m)
-                m.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.kda_rope_append, lib.kda_paged_attention_decode, lib.kda_beam_select,
-                                       lib.kda_pool_move)),
-                       (torch.float32, torch.bfloat16, torch.int32))
+                m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                         for f in (lib.kda_rope_append, lib.kda_paged_attention_decode,
+                                   lib.kda_paged_attention_workspace, lib.kda_beam_select,
+                                   lib.kda_beam_select_workspace, lib.kda_pool_move)))
                 _module = m
     return _module
-
-
-def _handle(dev):
-    """Raw handle of the device's current stream."""
-    if _raw_stream is not None and dev.type == "cuda":
-        return _raw_stream(dev.index)
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-# Workspaces of the calls that are given none.  One is kept for each host thread,
-# device and stream (allocating one anew takes 2.5 us a call): calls of one
-# thread on one stream follow one another, and no other call sees it.  A call
-# that is being captured gets its own from the graph's pool, so graphs share
-# theirs neither with each other nor with eager calls.
-_WORK = threading.local()
-_WORK_MAX = 16
-_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
-
-
-def _workspace(floats, dev, stream):
-    """At least `floats` floats for a call on `stream`, the current stream of the current device `dev`."""
-    if _capturing():
-        return torch.empty(floats, dtype=torch.float32, device=dev)
-    kept = _WORK.__dict__.setdefault("kept", {})
-    work = kept.get((dev.index, stream))
-    if work is None or work.numel() < floats:
-        if len(kept) >= _WORK_MAX:
-            kept.clear()
-        work = kept[(dev.index, stream)] = torch.empty(floats, dtype=torch.float32, device=dev)
-    return work
 
 
 def _raise(status):
@@ -338,15 +303,11 @@ def _raise(status):
 def kda_rope_append(q, k, v, phase_steps, seq_lens, page_table, k_pages, v_pages, cu_seqlens=None,
                     interleaved=False, amplitude=1.0, q_out=None):
     """Rotates q and k, writes k and v into the pages in place, returns the rotated q in the pages' dtype."""
-    dev = q.device
-    if q_out is None:
-        q_out = torch.empty_like(q, dtype=k_pages.dtype, memory_format=torch.contiguous_format)
-    with _on(dev):
-        st = (_module or _native()).rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages,
-                                                q_out, 1 if interleaved else 0, amplitude, _handle(dev), dev.index)
-    if st:
-        _raise(st)
-    return q_out
+    r = (_module or _native()).rope_append(q, k, v, phase_steps, cu_seqlens, seq_lens, page_table, k_pages, v_pages,
+                                           q_out, interleaved, amplitude)
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def kda_rope_phase_steps(rot_dim, base=10000.0, factor=1.0, original_len=0.0, low=1.0, high=32.0, device="cuda"):
@@ -368,12 +329,6 @@ def kda_paged_attention_workspace(q_heads, kv_heads, head_dim, dtype, sm_count):
     return floats.value
 
 
-@functools.lru_cache(maxsize=None)
-def _attention_floats(q_heads, kv_heads, head_dim, dtype, device):
-    sms = torch.cuda.get_device_properties(device).multi_processor_count
-    return kda_paged_attention_workspace(q_heads, kv_heads, head_dim, dtype, sms)
-
-
 def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window=0, scale=None, out=None, lse=None,
                                return_lse=False, workspace=None):
     """One new token per sequence over its pages; returns bf16 out [N, Hq, D], or (out, lse) with return_lse.
@@ -381,20 +336,11 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
     Without `workspace` the binding keeps one for each thread and stream, and
     takes one from the graph's pool for a captured call.
     """
-    dev = q.device
-    if out is None:
-        out = torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
-    if lse is None and return_lse:
-        lse = torch.empty(q.size(0), q.size(1), dtype=torch.float32, device=dev)
-    with _on(dev):
-        stream = _handle(dev)
-        if workspace is None:
-            workspace = _workspace(_attention_floats(q.size(1), k_pages.size(2), q.size(2), q.dtype, dev.index), dev, stream)
-        st = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, window,
-                                              q.size(2) ** -0.5 if scale is None else scale, stream, dev.index)
-    if st:
-        _raise(st)
-    return (out, lse) if return_lse else out
+    r = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, return_lse,
+                                         window, scale)
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sm_count):
@@ -406,42 +352,24 @@ def kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sm_count):
     return floats.value
 
 
-@functools.lru_cache(maxsize=256)
-def _beam_floats(requests, beams, vocab, num_out, dtype, device):
-    sms = torch.cuda.get_device_properties(device).multi_processor_count
-    return kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sms)
-
-
 def kda_beam_select(logits, scores, num_out, finished=None, eos_token=0, out=None, workspace=None):
     """The num_out best continuations of each request: (scores, parents, tokens), each [N, num_out].
 
     `out` may give the three tensors; the workspace is as in
     kda_paged_attention_decode.
     """
-    n, dev = logits.size(0), logits.device
-    if out is None:
-        out = (torch.empty(n, num_out, dtype=torch.float32, device=dev),
-               torch.empty(n, num_out, dtype=torch.int32, device=dev),
-               torch.empty(n, num_out, dtype=torch.int32, device=dev))
-    with _on(dev):
-        stream = _handle(dev)
-        if workspace is None:
-            floats = _beam_floats(n, logits.size(1), logits.size(2), num_out, logits.dtype, dev.index)
-            workspace = _workspace(floats, dev, stream)
-        st = (_module or _native()).beam(logits, scores, finished, workspace, out[0], out[1], out[2], eos_token, stream,
-                                         dev.index)
-    if st:
-        _raise(st)
-    return out
+    r = (_module or _native()).beam(logits, scores, finished, workspace, None if out is None else tuple(out), num_out,
+                                    eos_token)
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def kda_pool_move(pools, src_slots, dst_slots, parents=None):
     """Copies slots of every tensor of `pools` in place; returns None."""
-    dev = src_slots.device
-    with _on(dev):
-        st = (_module or _native()).move(pools, src_slots, dst_slots, parents, _handle(dev), dev.index)
-    if st:
-        _raise(st)
+    r = (_module or _native()).move(pools, src_slots, dst_slots, parents)
+    if type(r) is int:
+        _raise(r)
 
 
 def kda_plan_split(op, units, state_dtype, t_max, sm_count):

@@ -1,4 +1,4 @@
-"""Build libkda.so in-tree with nvcc for sm_103a (GB300), and with the C compiler
+"""Build libkda.so in-tree with nvcc for sm_103a (GB300), and with the C++ compiler
 the small CPython module that marshals the binding's calls.
 
     python -m linear_attention_decode_02_gb300.build [--force] [--verbose]
@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,7 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
-PYSRC = os.path.join(CSRC, "kda_python.c")
+PYSRC = os.path.join(CSRC, "kda_python.cpp")
 PYLIB = os.path.join(PKG, "_kda_python.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -68,15 +69,19 @@ def _compile(nvcc, src, verbose):
 
 
 def _python_module():
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        raise RuntimeError("no C compiler found for the binding's CPython module")
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found for the binding's CPython module")
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     tmp = PYLIB + ".tmp"
-    cmd = [cc, "-std=c11", "-O2", "-Wall", "-Wextra", "-Wno-missing-field-initializers", "-fPIC", "-shared",
-           "-I", sysconfig.get_paths()["include"], PYSRC, "-o", tmp]
+    cmd = [cxx, "-std=c++17", "-O2", "-Wall", "-Wno-unknown-pragmas", "-fPIC", "-shared",
+           "-isystem", os.path.join(torch, "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           PYSRC, "-o", tmp, "-L", os.path.join(torch, "lib"), "-Wl,--no-as-needed", "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed for {PYSRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cxx} failed for {PYSRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYLIB)
 
 

@@ -314,68 +314,36 @@ def test_beam_refuses_tokens_outside_the_vocabulary(lib):
         binding.kda_beam_select_workspace(1, 0, 10, 1, BF16, 152)
 
 
-def test_kept_workspaces_are_per_thread_stream_and_size(monkeypatch):
-    import threading
-    made = []
-    monkeypatch.setattr(binding, "_capturing", lambda: bool(made and made[-1] == "capture"))
-    monkeypatch.setattr(binding, "_WORK", threading.local())
-    dev = torch.device("cpu", 0)
-    a = binding._workspace(100, dev, 7)
-    assert binding._workspace(60, dev, 7) is a and a.numel() == 100
-    assert binding._workspace(100, dev, 8) is not a                      # another stream
-    assert binding._workspace(100, torch.device("cpu", 1), 7) is not a   # another device
-    b = binding._workspace(101, dev, 7)
-    assert b is not a and binding._workspace(1, dev, 7) is b             # grown
-    other = []
-    t = threading.Thread(target=lambda: other.append(binding._workspace(1, dev, 7)))
-    t.start()
-    t.join()
-    assert other[0] is not b                                             # another thread
-    made.append("capture")
-    c = binding._workspace(1, dev, 7)
-    assert c is not b and binding._workspace(1, dev, 7) is not c         # a captured call has its own
-    made.append("eager")
-    for s in range(100):
-        binding._workspace(1, dev, 100 + s)
-    assert len(binding._WORK.kept) <= binding._WORK_MAX
-
-
 # ---- the marshalling module ----------------------------------------------------------------
 
 
 def test_module_refuses_host_tensors_and_wrong_arguments(lib):
     m = binding._native()
     t = torch.zeros(2, 2)
-    with pytest.raises(ValueError, match="host"):
-        m.beam(t, t, None, t, t, t, t, 0, 0, 0)
-    with pytest.raises(TypeError, match="10 arguments"):
+    for call in (lambda: m.beam(t, t, None, None, None, 2, 0), lambda: m.move([t], t, t, None),
+                 lambda: m.rope_append(*[t] * 10, False, 1.0), lambda: m.attention(*[t] * 5, None, None, None, False, 0, None)):
+        with pytest.raises(ValueError, match="host"):
+            call()
+    with pytest.raises(TypeError, match="7 arguments"):
         m.beam(t)
     with pytest.raises(TypeError, match="list or tuple"):
-        m.move(t, t, t, None, 0, 0)  # not the rows of a tensor
-    with pytest.raises(AttributeError):
-        m.move([None], t, t, None, 0, 0)
-    with pytest.raises(TypeError):
-        m.rope_append(*[None] * 10, 0, 1.0, 0, "cuda")
-    with pytest.raises(OverflowError):
-        m.attention(*[None] * 8, 2 ** 40, 1.0, 0, 0)
+        m.move(t, t, t, None)  # not the rows of a tensor
+    with pytest.raises(TypeError, match="expected a tensor, got NoneType"):
+        m.move([t], None, t, None)
+    with pytest.raises(TypeError, match="expected a tensor, got int"):
+        m.attention(*[7] * 11)
 
 
-def test_module_passes_descriptors_as_they_are(lib):
-    # device -1 is the host's, so descriptors of host memory come as far as the library's own refusals
+def test_module_describes_tensors_as_ctypes_does(lib):
     m = binding._native()
-    x, s = torch.zeros(2, 3, 100, dtype=BF16), torch.zeros(2, 3)
-    o = [torch.zeros(2, 4), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 5, dtype=torch.int32)]
-    assert m.beam(x, s, None, torch.zeros(4096), *o, 0, 0, -1) == INVALID and "out_tokens: axis 1" in _msg(lib)
-    with pytest.raises(TypeError, match="unsupported dtype"):
-        m.beam(x.to(torch.float64), s, None, s, *o, 0, 0, -1)
-    with pytest.raises(ValueError, match="rank 5"):
-        m.beam(x.view(1, 1, 2, 3, 100), s, None, s, *o, 0, 0, -1)
-    assert m.beam(x, s, None, None, *o, 0, 0, -1) == INVALID and "workspace: null" in _msg(lib)
-    many = [torch.zeros(2, 2) for _ in range(300)]
-    i = torch.zeros(1, 1, dtype=torch.int32)
-    assert m.move(many, i, i, None, 0, -1) == UNSUPPORTED and "at most 256" in _msg(lib)
-    assert m.move([], i, i, None, 0, -1) == INVALID
-    assert m.move((many[0], many[0]), i, i, None, 0, -1) == ALIAS
+    base = torch.zeros(6, 4, 128, dtype=BF16)
+    for t in [base, base[1:], base[:, ::2], base.transpose(0, 1), torch.zeros(3, dtype=torch.int32),
+              torch.zeros(2, 3, 128, 128), torch.zeros(0, 4), base.as_strided((2, 2), (0, 5))]:
+        assert m.describe(t) == bytes(desc(t))
+    for t, kind, text in [(base.double(), TypeError, "unsupported dtype"), (base[None, None], ValueError, "rank 5"),
+                          (torch.tensor(1.0), ValueError, "rank 0"), (base.to_sparse(), TypeError, "strided")]:
+        with pytest.raises(kind, match=text):
+            m.describe(t)
 
 
 def test_rope_refuses_written_views_whose_elements_overlap(lib):

@@ -178,3 +178,53 @@ def test_a_step_of_the_search_replays_from_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert same_bits(a, b)
+
+
+def test_kept_workspaces_are_per_thread_stream_and_capture():
+    import threading
+    q = torch.randn(2, 8, 64, device="cuda").to(BF16)
+    pages = torch.randn(9, 16, 2, 64, device="cuda").to(BF16)
+    table = torch.arange(1, 9, dtype=torch.int32, device="cuda").view(2, 4)
+    lens = torch.tensor([60, 33], dtype=torch.int32, device="cuda")
+    want = binding.kda_paged_attention_decode(q, pages, pages, table, lens)
+    torch.cuda.synchronize()
+
+    def grown(f):  # bytes that f leaves allocated
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        f()
+        torch.cuda.synchronize()
+        return torch.cuda.memory_allocated() - before
+
+    call = lambda: binding.kda_paged_attention_decode(q, pages, pages, table, lens)  # noqa: E731
+    floats = binding.kda_paged_attention_workspace(8, 2, 64, BF16, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert grown(call) == 0                       # this thread's workspace on this stream is there already
+    stream = torch.cuda.Stream()
+
+    def on_stream():
+        with torch.cuda.stream(stream):
+            assert torch.equal(call(), want)
+    assert grown(on_stream) >= 4 * floats         # another stream has its own
+    assert grown(on_stream) == 0
+    kept = []
+
+    def in_thread():
+        t = threading.Thread(target=lambda: kept.append(grown(call)))
+        t.start()
+        t.join()
+    assert grown(in_thread) < 4 * floats and kept[0] >= 4 * floats  # another thread too, and it goes with the thread
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    graph.replay()
+    assert torch.equal(call(), want) and torch.equal(out, want)
+
+
+def test_calls_refuse_host_tensors():
+    i = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="host"):
+        binding.kda_pool_move([torch.zeros(2, 2)], i, i)
+    with pytest.raises(ValueError, match="host"):
+        binding.kda_beam_select(torch.zeros(1, 2, 9, device="cuda"), torch.zeros(1, 2), 2)
+    with pytest.raises(TypeError, match="list or tuple"):
+        binding.kda_pool_move(torch.zeros(2, 2, device="cuda"), i, i)
