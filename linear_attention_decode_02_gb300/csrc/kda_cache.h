@@ -30,6 +30,7 @@ struct RopeArgs {
   float amplitude;
   int32_t in_dtype, page_dtype;
   int32_t vec;                 // elements per access: 8 (bf16 -> bf16, 16-byte aligned rows) or 4
+  int32_t sms;                 // SMs of the device
 };
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);

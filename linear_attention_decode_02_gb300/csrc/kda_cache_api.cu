@@ -238,7 +238,7 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
   a.R = (int32_t)R; a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.rot = (int32_t)rot;
   a.interleaved = is_interleaved; a.amplitude = amplitude;
   a.in_dtype = Q.dtype; a.page_dtype = KP.dtype;
-  a.vec = 4;
+  a.vec = 4; a.sms = dev.sms;
   if (Q.dtype == KDA_BF16 && KP.dtype == KDA_BF16 && D % 8 == 0 && (is_interleaved || rot % 16 == 0)) {
     bool wide = true;
     for (const View* t : {&Q, &K, &V, &KP, &VP, &O}) wide = wide && vectors_aligned(*t, 16);

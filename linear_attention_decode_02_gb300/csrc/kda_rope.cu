@@ -9,11 +9,14 @@
 // rotation is float32 and each output is rounded once.
 //
 // Bound by memory: every input is read once and every output written once.
-// A block takes ROWS token rows.  Their sines and cosines are computed once
-// into shared memory and reused by the rows' Hq + Hkv heads; then each thread
-// walks the vectors of a row and moves each for all the rows at once, so that
-// 2 * ROWS loads are in flight and the way from the row to its position and
-// page (three dependent loads) is paid once for them.
+// A block takes ROWS token rows, or where they are few a part of their heads.
+// Sines and cosines are computed once into shared memory and reused by the
+// rows' heads; then each thread walks the vectors of a row and moves each for
+// all the rows at once, so that 2 * ROWS loads are in flight and the way from
+// the row to its position and page (three dependent loads) is paid once for
+// them.
+#include <algorithm>
+
 #include "kda_cache.h"
 #include "kda_device.cuh"
 
@@ -25,9 +28,11 @@ constexpr int kMaxPairs = 256;  // head_dim <= 512
 // of 48 heads of 128 bf16 channels take 86 us (6.6 TB/s) with 128 threads, 97 us
 // with 256 and 112 us with 512.
 constexpr int kThreads = 128;
-// Rows from which a block takes four of them: the same 23119 rows take 99 us at
-// one row a block and 88 us at two.  Few rows want a block each (384 rows: 4 us).
-constexpr int kManyRows = 2048;
+// Rows from which a block takes four of them.  Measured at four rows and at one
+// (40 heads, 128 bf16 / 256 float32 channels): 128 rows 4.0 and 3.3 / 4.9 and 5.5
+// us, 256 rows 4.3 and 4.0 / 7.0 and 7.9, 384 rows 4.2 and 4.5 / 7.2 and 10.5,
+// 1536 rows 8.4 and 9.9 / 26.6 and 40.2, 23119 rows 86 and 99 us.
+constexpr int kManyRows = 320;
 
 // Index of the sequence owning `row`: the number of entries of cu[1..N] that
 // are <= row, by a 32-way search of the whole warp (N <= 32: one load).
@@ -81,14 +86,15 @@ struct Vec<__nv_bfloat16, 8> {
   }
 };
 
-// A thread's place among heads x tasks, moved on by the block without dividing.
+// A thread's place among heads x tasks, moved on by the row's blocks without dividing.
 struct Slot {
   int h, t, dh, dt, tasks;
   __device__ __forceinline__ explicit Slot(int tasks_) : tasks(tasks_) {
-    h = threadIdx.x / tasks;
-    t = threadIdx.x - h * tasks;
-    dh = blockDim.x / tasks;
-    dt = blockDim.x - dh * tasks;
+    const int at = blockIdx.y * kThreads + threadIdx.x, step = gridDim.y * kThreads;
+    h = at / tasks;
+    t = at - h * tasks;
+    dh = step / tasks;
+    dt = step - dh * tasks;
   }
   __device__ __forceinline__ void next() {
     h += dh;
@@ -227,7 +233,12 @@ template <typename In, typename Out, int VEC, int ROWS>
 cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
   auto kernel = a.interleaved ? kda_rope_append_kernel<In, Out, VEC, true, ROWS>
                               : kda_rope_append_kernel<In, Out, VEC, false, ROWS>;
-  return launch_pdl(kernel, dim3((unsigned)((a.R + (int64_t)ROWS - 1) / ROWS)), dim3(kThreads), 0, s, 1, a);
+  // Few rows: several blocks share each, down to one vector a thread, until every SM has its six.
+  const int64_t blocks = (a.R + (int64_t)ROWS - 1) / ROWS;
+  const int pairs = a.interleaved ? a.rot / VEC : a.rot / (2 * VEC);
+  const int64_t tasks = (int64_t)(a.Hq + a.Hkv) * (pairs + (a.D - a.rot) / VEC);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((tasks + kThreads - 1) / kThreads, 6 * a.sms / blocks));
+  return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)parts), dim3(kThreads), 0, s, 1, a);
 }
 
 template <typename In, typename Out, int VEC>

@@ -238,3 +238,18 @@ def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="host"):
         binding.kda_rope_append(c["q"], c["k"], c["v"], binding.kda_rope_phase_steps(64, device="cpu"), c["lens"],
                                 c["table"], c["k_pages"], c["v_pages"])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,pdtype", [(BF16, BF16), (FP32, FP32), (BF16, FP32)])
+@pytest.mark.parametrize("D,rot", [(128, 128), (72, 24), (256, 64)])
+def test_many_rows(interleaved, dtype, pdtype, D, rot):
+    # several rows a block: counts that do not divide, null rows and padding among them
+    rng = np.random.default_rng(D)
+    lens = [int(x) for x in rng.integers(0, 40, 331)]
+    check(make(lens, D=D, rot=rot, dtype=dtype, pdtype=pdtype, page=7), interleaved=interleaved)
+    new = [int(x) for x in rng.integers(0, 30, 80)]
+    lens = [t + int(x) for t, x in zip(new, rng.integers(0, 9, 80))]
+    lens[3], lens[50] = 0, max(0, new[50] - 2)
+    out = check(make(lens, new=new, pad=5, D=D, rot=rot, dtype=dtype, pdtype=pdtype, page=16), interleaved=interleaved)
+    assert out.shape[0] >= 320 and torch.count_nonzero(out[sum(new):]) == 0
