@@ -330,8 +330,9 @@ kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, dou
  *               logarithm of the sum of exp(scale q.k) over the row's positions.
  * Positions past the length, outside the window or on null pages are never
  * read into the result, whatever their bytes hold.  A row without positions
- * gives zero and an lse of minus infinity.  A non-finite key or value at an
- * attended position makes its row's result non-finite.
+ * gives zero and an lse of minus infinity.  At an attended position a NaN, a
+ * score of +infinity and an infinite value make the row's result non-finite; a
+ * score of -infinity weighs nothing.
  */
 kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
                                       const kda_tensor* page_table, const kda_tensor* seq_lens,
@@ -357,8 +358,11 @@ kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int3
  *               (written), 1 <= M <= 64.
  * Continuation (b, t) is worth scores[b] + logits[b, t] - log sum exp(logits[b]);
  * the M largest of a request's B * V are returned in falling order, equal ones
- * by rising b, then t.  The comparison is in float64, the returned score
- * rounded to float32.  A logit of minus infinity is no continuation, and a beam
+ * by rising b, then t.  Candidates are compared as unrounded sums of two
+ * float32, the returned score is rounded to float32.  A beam's log-sum is off
+ * by the error of a float32 exponential, 2.4e-7 at most for few tokens, far less
+ * over a vocabulary, so beams whose candidates are closer than that may be
+ * taken in either order.  A logit of minus infinity is no continuation, and a beam
  * whose score or log-sum is not finite (a dead beam; a NaN or +infinity among
  * its logits) has none.  Places without one get -infinity, -1 and -1.
  */

@@ -3,11 +3,12 @@
 // A unit is one sequence, one key head and one group of at most HG of its
 // query heads; its work is a row of tiles of kTile positions, at least one.
 // All units' tiles form one line, cut into equal pieces, one for each block of
-// the grid but at least a tile, whatever the sequences' lengths, so ragged batches and a few very long sequences load
-// the SMs alike, and the host needs no lengths.  A unit inside one piece is
-// finished there; one that crosses a cut leaves an unnormalised partial
-// (maximum, sum, output) per piece, which a second kernel joins.  A piece
-// cuts at most two units, so the workspace is fixed by the grid.
+// the grid but at least a tile, whatever the sequences' lengths, so ragged
+// batches and a few very long sequences load the SMs alike, and the host needs
+// no lengths.  A unit inside one piece is finished there; one that crosses a
+// cut leaves an unnormalised partial (maximum, sum, output) per piece, which a
+// second kernel joins.  A piece cuts at most two units, so the workspace is
+// fixed by the grid.
 #pragma once
 
 #include <atomic>

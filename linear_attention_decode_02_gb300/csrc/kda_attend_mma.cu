@@ -12,15 +12,16 @@
 // sequence.
 //
 // Measured (32 query / 8 key heads of 128, pages of 64): 64 sequences of up to
-// 8192 positions, 1.27 GB, 190 to 197 us; 2 of 131072 and 66 thousand, 1.0 GB,
-// 150 to 155 us: 97 to 100 % of the copy bandwidth.  0.4 GB of 256-channel heads
-// 85 us (73 %), of 64-channel ones 74 us (79 %), 12 query heads a key head of
-// 128 75 us (77 %).  One sequence of 1000 positions 9 us with the join, of which
-// four dependent loads (length, page, keys, partials) and two launches are most.
+// 8192 positions, 1.27 GB, 189 to 199 us; 2 of up to 131072, 1.0 GB, 150 to 156
+// us: 95 to 100 % of the copy bandwidth.  0.4 GB of 256-channel heads 85 us (73 %),
+// of 64-channel ones 75 us (79 %), of 128-channel ones 70 us (85 %), with 12 query
+// heads a key head 75 us (77 %).  One sequence of 1000 positions 9 us with the
+// join: two launches and four dependent loads (length, page, keys, partials).
 //
-// A warp as a worker of its own, its units never shared with others, was slower
-// (the batch 210 us, 64 sequences of 100 positions 22 against 15 us): it leaves
-// four times as many partial results.
+// Every warp with a piece of its own, instead of four that share a tile: 64
+// sequences of up to 8192 199 -> 210 us, 32 of 2000 39 -> 44, 64 of 100 15 -> 22,
+// since it leaves more partial results to join; 512 of 64 47 -> 45 and, float32
+// with 256 channels, 100 of 50 46 -> 27 were better for it.
 //
 // S = Q K^T with query heads as rows (16 of them) and positions as columns, so
 // that a score's lane already is the one the second product wants its weight

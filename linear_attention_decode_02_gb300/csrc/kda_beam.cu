@@ -20,12 +20,13 @@
 // logarithm in it alone took 1.8 us).  What is left are the exponentials' own errors, which
 // are random and average out over the vocabulary.
 //
-// Every logit is read once, 64 to 128 bytes a thread in flight.  67 MB of
-// logits (32 requests of 8 beams over 131072 tokens, bf16) take 17 us and the join 5
-// to 7, 3 TB/s over both: about 10 us are the reading, the rest the start of
-// the two kernels and, after the last logit, the bound, the list and the order,
-// which all pieces reach at the same time.  Pieces half as long (1024 blocks
-// instead of 512) take 22 us, a quarter 28.  4 beams over 32000 tokens take 6 us.
+// Every logit is read once, 64 bytes a thread on their way while 64 are summed.
+// 32 requests of 8 beams, a tenth of them finished, over 131072 tokens in bf16,
+// 61 MB, which a copy would read in 9 us, take 22 us a call.  Alone the scan takes 17 to 20 us and the join 8,
+// which starts under the scan's end.  The scan uses 39 % of the DRAM's peak: after
+// the last logit come the bound, the list and the order, behind barriers, and
+// all pieces reach them at the same time.  Shorter pieces make more of that:
+// 1024 blocks instead of 512 take 22 to 25 us, 2048 26 to 28, beside 19 to 21.
 #include <float.h>
 
 #include "kda_cache.h"
@@ -673,8 +674,8 @@ cudaError_t launch_scan(const BeamArgs& a, const BeamPlan& p, cudaStream_t s) {
 
 // The longest pieces (8 batches of 4 loads a thread) that still give every SM
 // two blocks, down to one load a thread, and not so short that the join, one
-// block a request, would have more than kJoin candidates to look at.  A row whose start is not on a 16-byte
-// boundary reaches up to vec - 1 elements further.
+// block a request, would have more than kJoin candidates to look at.  A row
+// whose start is not on a 16-byte boundary reaches up to vec - 1 elements further.
 BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms) {
   BeamPlan p;
   const int64_t vec = dtype == KDA_DT_F32 ? 4 : 8;
