@@ -16,8 +16,8 @@
 // ahead of their use, as the tensor-core kernel does (loads straight to
 // registers took 165 us in the first case below).  Bound by memory up to 4 query
 // heads a key head: 48 sequences, window 2048, 16 heads of 64, 0.79 GB, 122 to 127
-// us, 93 to 97 % of the copy bandwidth; 32 / 8 heads of 128 83 %.  From 8 on by
-// the exchanges and products themselves: 12 / 1 heads of 128 165 us for 0.37 GB.
+// us, 93 to 97 % of the copy bandwidth; 32 / 8 heads of 128 83 %.  With 12 and 16
+// by the exchanges and products themselves: 12 / 1 heads of 128 165 us for 0.37 GB.
 // bfloat16 comes here only with vectors off the 16-byte boundaries those
 // copies need, and is loaded straight to registers.
 #include <algorithm>
@@ -442,12 +442,21 @@ cudaError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, cudaStream
   }
 }
 
+// Who finds the units to join.  Measured by cut and by unit, us a call with its
+// attention, bf16: 16 heads of a unit, 128 channels, units x positions 1 x 500 9.9
+// and 9.3, 1 x 16000 21.0 and 14.6, 16 x 2000 15.7 and 13.8, 32 x 500 11.9 and 12.7,
+// 64 x 2000 21.2 and 25.5; 256 channels, half the blocks, 8 x 2000 15.9 and 13.2,
+// 16 x 2000 20.1 and 20.5; 4 heads, 8 x 500 8.2 and 9.0, 8 x 16000 17.8 and 16.9,
+// 32 x 2000 13.0 and 13.4.  So by unit where a unit has 16 heads and there is at
+// most one unit for 16 blocks.
 template <int D, int HG>
 cudaError_t launch_join_heads(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  const int64_t units = (int64_t)a.N * a.Hkv * ((a.Hq / a.Hkv + HG - 1) / HG);
-  if (8 * units <= p.ctas)
-    return launch_pdl(kda_attend_join_kernel<D, HG, false>, dim3((unsigned)units, HG), dim3(512), 0, s, 1, a, p.ctas);
-  return launch_pdl(kda_attend_join_kernel<D, HG, true>, dim3(p.ctas, HG), dim3(128), 0, s, 1, a, p.ctas);
+  const int G = a.Hq / a.Hkv, heads = std::min(G, HG);
+  const int64_t units = (int64_t)a.N * a.Hkv * ((G + HG - 1) / HG);
+  if constexpr (HG == 16)
+    if (16 * units <= p.ctas)
+      return launch_pdl(kda_attend_join_kernel<D, HG, false>, dim3((unsigned)units, heads), dim3(512), 0, s, 1, a, p.ctas);
+  return launch_pdl(kda_attend_join_kernel<D, HG, true>, dim3(p.ctas, heads), dim3(128), 0, s, 1, a, p.ctas);
 }
 
 template <int D>

@@ -179,6 +179,41 @@ def test_splits_of_long_and_many_sequences(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[30000], [5000, 1, 0, 9000], [900] * 20, [100] * 330])
+def test_splits_of_units_of_many_heads(dtype, D, lens):
+    check(make(lens, Hq=12, Hkv=1, D=D, page=64, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("Hq", [2, 16])
+def test_infinite_scores(dtype, Hq):
+    # Head 0 scores -infinity at position 5 and loses it, head 1 scores +infinity; a lone -infinity leaves nothing.
+    c = make([70, 1], Hq=Hq, Hkv=1, D=64, page=16, dtype=dtype, garbage=False)
+    c["q"][:, 0::2, 0], c["q"][:, 1::2, 0] = 1.0, -1.0
+    c["k"][c["table"][0, 0], 5, 0, 0] = -float("inf")
+    c["k"][c["table"][1, 0], 0, 0, 0] = -float("inf")
+    out, lse = run(c)
+    torch.cuda.synchronize()
+    k, v = to_np(c["k"]), to_np(c["v"])
+    k = np.where(np.isinf(k), 0.0, k)
+    at = [t for t in range(70) if t != 5]
+    table = c["table"].cpu().numpy()
+    rows = [(table[0, t // 16], t % 16) for t in at]
+    keys, values = (np.stack([x[p, i, 0] for p, i in rows]) for x in (k, v))
+    plain = dict(q=c["q"], k=torch.from_numpy(k).float(), v=c["v"], lens=c["lens"])
+    t_out, t_lse = tolerances(plain, 0.125)
+    for h in range(0, Hq, 2):
+        s = to_np(c["q"])[0, h] @ keys.T * 0.125
+        w = np.exp(s - s.max())
+        assert_rounded(out[0, h].cpu(), w @ values / w.sum(), t_out, "out")
+        assert_rounded(lse[0, h].cpu(), np.log(w.sum()) + s.max(), t_lse, "lse")
+        assert not torch.isfinite(out[0, h + 1]).any()
+        assert torch.count_nonzero(out[1, h]) == 0 and lse[1, h] == -float("inf")
+        assert not torch.isfinite(out[1, h + 1]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("q_scale", [0.0, 40.0])
 def test_flat_and_peaked_scores(dtype, q_scale):
     check(make([300, 65, 2000], D=128, q_scale=q_scale, dtype=dtype), scale=0.3)
