@@ -314,12 +314,10 @@ PyObject* beam(PyObject*, PyObject* const* args, Py_ssize_t n) {
         raise(PyExc_TypeError, "out must be a tuple of three tensors");
       for (int i = 0; i < 3; ++i) given[i] = PyTuple_GET_ITEM(args[4], i);
     }
-    int64_t floats = 0;
-    if (args[3] == Py_None) {
-      const kda_status s = lib.beam_workspace(x.size(0), static_cast<int32_t>(std::min<int64_t>(x.size(1), INT32_MAX)),
-                                              x.size(2), num_out, dtype_of(x), call.sms(), &floats);
-      if (s != KDA_OK) return PyLong_FromLong(s);
-    }
+    int64_t floats = 0;  // refuses sizes before anything of them is allocated
+    const kda_status sizes = lib.beam_workspace(x.size(0), static_cast<int32_t>(std::min<int64_t>(x.size(1), INT32_MAX)),
+                                                x.size(2), num_out, dtype_of(x), call.sms(), &floats);
+    if (sizes != KDA_OK) return PyLong_FromLong(sizes);
     const at::Tensor work = workspace(call, args[3], floats);
     t.add(call, work);
     at::Tensor made[3];

@@ -219,3 +219,12 @@ def test_sorted_logits(dtype):
     x = torch.linspace(-9, 9, 100003).expand(2, 2, -1).to(dtype).contiguous().cuda()
     x[1] = x[1].flip(-1)
     check(x, torch.tensor([[0.0, -0.1], [-0.3, 0.0]], device="cuda"), 20)
+
+
+@pytest.mark.parametrize("num_out", [-1, 0, 65, 2 ** 31 - 1])
+def test_a_count_out_of_range_is_refused_before_it_is_allocated(num_out):
+    x, s = make(1, 2, 100)
+    work = torch.empty(1 << 16, device="cuda")
+    for w in (None, work):
+        with pytest.raises(binding.KdaError, match="candidates"):
+            binding.kda_beam_select(x, s, num_out, workspace=w)
