@@ -15,9 +15,10 @@
 // float32: each warp copies its positions into a ring of shared-memory stages
 // ahead of their use, as the tensor-core kernel does (loads straight to
 // registers took 165 us in the first case below).  Bound by memory up to 4 query
-// heads a key head: 48 sequences, window 2048, 16 heads of 64, 0.79 GB, 122 to 127
-// us, 93 to 97 % of the copy bandwidth; 32 / 8 heads of 128 83 %.  With 12 and 16
-// by the exchanges and products themselves: 12 / 1 heads of 128 165 us for 0.37 GB.
+// heads a key head: 48 sequences, window 2048, 16 heads of 64, 0.79 GB, 122 to 130
+// us, 91 to 97 % of the copy bandwidth; 32 / 8 heads of 128 83 %.  With more by the
+// exchanges and products themselves, 12 / 1 heads of 128 165 us for 0.37 GB, so
+// those come here only where there is little to attend to (kda_attend_tf32.cu).
 // bfloat16 comes here only with vectors off the 16-byte boundaries those
 // copies need, and is loaded straight to registers.
 #include <algorithm>
@@ -470,8 +471,26 @@ cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, cudaStream_t s
   }
 }
 
+// Float32 in matrix instructions: from five query heads a key head, where the
+// positions that the call may attend to, over sequences and key heads, are 256 a
+// channel or more.  The host knows only how many the table or the window allows;
+// short sequences in a roomy table are slower for it, by 2 us at 64 and 128
+// channels, 8 us at 256.  Measured in matrix instructions and on CUDA cores, us:
+//   64 channels   12 heads, 8000 positions 10 and 11, 32000 17 and 23, 1.2 million 112 and 226; 8 heads 97 and 118
+//   128 channels  12 heads, 8000 13 and 13, 16000 18 and 17, 32000 21 and 22, 0.6 million 102 and 165; 8 heads 78 and 85
+//   256 channels  12 heads, 16000 28 and 21, 64000 57 and 58, 0.3 million 167 and 193; 16 heads 175 and 272
+// With four heads or fewer CUDA cores are faster: 32 / 8 heads of 64 71 and 100 us.
+constexpr int kTensorHeads = 5;
+constexpr int64_t kTensorPositions = 256;
+bool tensor_path(const AttendArgs& a) {
+  if (a.dtype != KDA_DT_F32) return a.vec16;
+  int64_t most = (int64_t)a.table_cols * a.page_size;
+  if (a.window > 0) most = std::min<int64_t>(most, a.window);
+  return a.Hq / a.Hkv >= kTensorHeads && (double)a.N * a.Hkv * most >= (double)kTensorPositions * a.D;
+}
+
 AttendPlan plan_of(int32_t G, int32_t D, int32_t dtype, int32_t sms, bool tensor) {
-  if (tensor) return attend_mma_plan(G, D, sms);
+  if (tensor) return dtype == KDA_DT_F32 ? attend_tf32_plan(G, D, sms) : attend_mma_plan(G, D, sms);
   AttendPlan p;
   p.heads = heads_class(G, D);
   p.ctas = blocks_per_sm(dtype == KDA_DT_F32, D, p.heads) * sms;
@@ -482,16 +501,14 @@ AttendPlan plan_of(int32_t G, int32_t D, int32_t dtype, int32_t sms, bool tensor
 }  // namespace
 
 int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
-  const int64_t floats = plan_of(Hq / Hkv, D, dtype, sms, false).floats;
-  return dtype == KDA_DT_F32 ? floats : std::max(floats, plan_of(Hq / Hkv, D, dtype, sms, true).floats);
+  return std::max(plan_of(Hq / Hkv, D, dtype, sms, false).floats, plan_of(Hq / Hkv, D, dtype, sms, true).floats);
 }
 
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s) {
-  const bool tensor = a.dtype == KDA_DT_BF16 && a.vec16;
+  const bool tensor = tensor_path(a);
   const AttendPlan p = plan_of(a.Hq / a.Hkv, a.D, a.dtype, sms, tensor);
-  const cudaError_t e = tensor ? launch_attend_mma(a, p, s)
-                               : (a.dtype == KDA_DT_F32 ? launch_attend_d<float>(a, p, s)
-                                                        : launch_attend_d<__nv_bfloat16>(a, p, s));
+  const cudaError_t e = a.dtype == KDA_DT_F32 ? (tensor ? launch_attend_tf32(a, p, s) : launch_attend_d<float>(a, p, s))
+                                              : (tensor ? launch_attend_mma(a, p, s) : launch_attend_d<__nv_bfloat16>(a, p, s));
   if (e != cudaSuccess) return e;
   return a.D == 64 ? launch_join<64>(a, p, s) : (a.D == 128 ? launch_join<128>(a, p, s) : launch_join<256>(a, p, s));
 }

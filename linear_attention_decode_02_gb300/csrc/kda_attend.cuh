@@ -38,6 +38,9 @@ constexpr int kTile = 64;  // positions of a tile
 // The tensor-core kernel (kda_attend_mma.cu), for bfloat16 whose vectors start on 16-byte boundaries.
 AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms);
 cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+// Float32 in matrix instructions (kda_attend_tf32.cu), for many query heads a key head.
+AttendPlan attend_tf32_plan(int32_t G, int32_t D, int32_t sms);
+cudaError_t launch_attend_tf32(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 
 // a / b, neither negative; 32-bit where they fit (a 64-bit division is a long call).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {

@@ -32,7 +32,7 @@
 // to 2^-17 (hi alone would put 2^-9 of rounding into the output, as much as
 // its own type has).  With up to 8 heads hi takes rows 0..7 and lo rows 8..15,
 // which would be empty, at no cost; with 16 heads lo is a second product.
-#include "kda_attend.cuh"
+#include "kda_attend_rows.cuh"
 
 namespace kda {
 namespace {
@@ -81,12 +81,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int D, int HG>
 __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
   using Copies = typename Shape<D, HG>::Copies;
@@ -175,7 +169,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   for (int s = 0; s < STAGES - 1; ++s) copies.copy(s);
 
   while (walk.tile < place.stop) {
-    const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
     uint32_t q[QS ? 1 : KSTEPS][QN];
     if constexpr (QS) {
       place_q();
@@ -297,85 +290,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
       }
     }
 
-    // ---- the unit's end in this piece: join the warps -----------------------------------------
-#pragma unroll
-    for (int r = 0; r < RS; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t4 == 0) {
-        s_m[parity][warp][g + 8 * r] = m[r];
-        s_l[parity][warp][g + 8 * r] = l[r];
-      }
-    }
-    __syncthreads();  // all have left the last unit's outputs too
-    float M[RS], f[RS];
-#pragma unroll
-    for (int r = 0; r < RS; ++r) {
-      M[r] = s_m[parity][0][g + 8 * r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[parity][w][g + 8 * r]);
-      f[r] = ex2(m[r] - (M[r] == -INFINITY ? 0.f : M[r]));
-    }
-    // Warp w finishes the w-th quarter of the channels: it keeps its own part
-    // of that and hands over the rest, to place (its warp, as the owner counts),
-    // 8 heads at a time.
-    constexpr int QUARTER = NT / kWarps, QD = D / kWarps;
-    float* shared_o = reinterpret_cast<float*>(smem + kWarps * Copies::RING);
-    const auto part = [&](int owner, int from) {
-      return shared_o + (owner * (kWarps - 1) + (from - owner - 1 + kWarps) % kWarps) * 8 * QD;
-    };
-    const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
-    const bool at_start = walk.unit_start <= place.start;
-    const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
-#pragma unroll
-    for (int r = 0; r < RS; ++r) {
-      if (r > 0) __syncthreads();  // all have taken the first heads
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int owner = i / QUARTER;
-        o[i][2 * r] = (PAIR ? o[i][0] + o[i][2] : o[i][2 * r]) * f[r];
-        o[i][2 * r + 1] = (PAIR ? o[i][1] + o[i][3] : o[i][2 * r + 1]) * f[r];
-        if (owner != warp)
-          *reinterpret_cast<float2*>(part(owner, warp) + g * QD + (i % QUARTER) * 8 + 2 * t4) =
-              make_float2(o[i][2 * r], o[i][2 * r + 1]);
-      }
-      __syncthreads();
-      const int h = g + 8 * r;
-      if (h >= heads) continue;
-      const float ref = M[r] == -INFINITY ? 0.f : M[r];
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) L = fmaf(ex2(s_m[parity][w][h] - ref), s_l[parity][w][h], L);
-      const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
-      const float scale = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (i / QUARTER != warp) continue;
-        const int d = i * 8 + 2 * t4;
-        float x = o[i][2 * r], y = o[i][2 * r + 1];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(shared_o + (warp * (kWarps - 1) + w - 1) * 8 * QD + g * QD +
-                                                            (i % QUARTER) * 8 + 2 * t4);
-          x += v.x;
-          y += v.y;
-        }
-        if (whole) {
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
-        } else {
-          *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
-        }
-      }
-      if (t4 == 0 && warp == 0) {
-        if (!whole) {
-          ws.ml_of(slot, h)[0] = M[r];
-          ws.ml_of(slot, h)[1] = L;
-        } else if (a.lse != nullptr) {
-          a.lse[head] = log_sum(ref, L);
-        }
-      }
-    }
-    if (threadIdx.x == 0 && at_start) ws.note[c] = note_of(walk, place);
+    finish_unit<D, HG, kWarps, RS>(a, walk, place, ws, reinterpret_cast<float*>(smem + kWarps * Copies::RING),
+                                   s_m[parity], s_l[parity], o, m, l, groups, warp, g, t4, c);
     parity ^= 1;
     after.tile = walk.tile;
     walk = after;

@@ -185,11 +185,43 @@ def test_splits_of_units_of_many_heads(dtype, D, lens):
     check(make(lens, Hq=12, Hkv=1, D=D, page=64, dtype=dtype))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(5, 1), (8, 1), (9, 1), (12, 1), (16, 1), (24, 1), (32, 2)])
+@pytest.mark.parametrize("width", [63, 4500])
+def test_many_heads_in_narrow_and_wide_tables(D, Hq, Hkv, width):
+    # float32 with many query heads: the kernel is chosen by what the table could hold
+    c = make(LENGTHS, Hq=Hq, Hkv=Hkv, D=D, dtype=FP32, width=width)
+    check(c)
+    check(c, window=70)
+    check(c, window=5000)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["query", "value"])
+def test_many_heads_with_a_bad_query_or_value(where, bad):
+    c = make([300, 70], Hq=12, Hkv=1, D=128, dtype=FP32, width=4500, garbage=False)
+    good, _ = run(c)
+    if where == "query":
+        c["q"][0, 3, 17] = bad
+    else:
+        c["v"][c["table"][0, 2], 5, 0, 9] = bad
+    out, _ = run(c)
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    if where == "query":
+        hit[0, 3] = True
+    else:
+        hit[0, :, 9] = True
+    assert not torch.isfinite(out[hit]).any()
+    assert same(out[~hit], good[~hit])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("Hq", [2, 16])
-def test_infinite_scores(dtype, Hq):
+@pytest.mark.parametrize("width", [5, 600])
+def test_infinite_scores(dtype, Hq, width):
     # Head 0 scores -infinity at position 5 and loses it, head 1 scores +infinity; a lone -infinity leaves nothing.
-    c = make([70, 1], Hq=Hq, Hkv=1, D=64, page=16, dtype=dtype, garbage=False)
+    c = make([70, 1], Hq=Hq, Hkv=1, D=64, page=16, dtype=dtype, garbage=False, width=width)
     c["q"][:, 0::2, 0], c["q"][:, 1::2, 0] = 1.0, -1.0
     c["k"][c["table"][0, 0], 5, 0, 0] = -float("inf")
     c["k"][c["table"][1, 0], 0, 0, 0] = -float("inf")
