@@ -22,11 +22,14 @@
 //
 // Every logit is read once, 64 bytes a thread on their way while 64 are summed.
 // 32 requests of 8 beams, a tenth of them finished, over 131072 tokens in bf16,
-// 61 MB, which a copy would read in 9 us, take 22 us a call.  Alone the scan takes 17 to 20 us and the join 8,
-// which starts under the scan's end.  The scan uses 39 % of the DRAM's peak: after
-// the last logit come the bound, the list and the order, behind barriers, and
-// all pieces reach them at the same time.  Shorter pieces make more of that:
-// 1024 blocks instead of 512 take 22 to 25 us, 2048 26 to 28, beside 19 to 21.
+// 61 MB, which a copy would read in 9 us, take 19 to 20 us a call.  Alone the scan
+// takes 17 to 18 us and the join 6, which starts under the scan's end.  The scan
+// uses 42 % of the DRAM's peak: after the last logit come the bound, the list
+// and the order, behind barriers, and all pieces reach them at the same time.
+// Shorter pieces made more of that: 1024 blocks instead of 512 took 22 to 25 us,
+// 2048 26 to 28, beside 19 to 21 then.  Both kernels run their code once a block, so
+// what is unrolled counts: one thread that read a marked batch again, all four
+// vectors of it, and a join unrolled over 32 beams made 21 us of the 19.
 #include <float.h>
 
 #include "kda_cache.h"
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
 
   // Elements at or above the bound go to the list.  One batch is still in
   // registers; of several, the threads' batches that hold one are noted first
-  // and read again, one a thread, so that one memory latency serves all.
+  // and read again, a vector a thread, so that one memory latency serves all.
   const auto push = [&](const Raw<T>& v, int i) {
     if (!(v.top() >= bound)) return;
 #pragma unroll
@@ -344,12 +347,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   s_hi[tid] = hi;
   __syncthreads();
   if (batches > 1) {
-    for (int h = tid; h < s_hots; h += kThreads) {
-      const int entry = s_hot[h], at = first + (entry / kThreads) * BATCH + entry % kThreads * VEC;
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) load_vector(at + j * kThreads * VEC, x[j]);
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) push(x[j], at + j * kThreads * VEC);
+    for (int h = tid; h < s_hots * LOADS; h += kThreads) {
+      const int entry = s_hot[h / LOADS];
+      const int at = first + (entry / kThreads) * BATCH + (h % LOADS * kThreads + entry % kThreads) * VEC;
+      Raw<T> v;
+      load_vector(at, v);
+      push(v, at);
     }
     __syncthreads();
   }
@@ -503,39 +506,42 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     held[k] = e < count ? fetch(e / heads, e % heads) : 0;
   }
 
-  // Warp w joins the sums of the beams w, w + kWarps, ...; all of its loads are on their way at once.
-  constexpr int BEAMS = kBeamMax / kWarps;
-  float scores[BEAMS];
-  int done[BEAMS];
-  PieceSum part[BEAMS];
-#pragma unroll
-  for (int k = 0; k < BEAMS; ++k) {
-    const int b = warp + k * kWarps;
-    scores[k] = 0.f;
-    done[k] = 0;
-    part[k].hi = part[k].lo = 0.f;
-    part[k].top = -INFINITY;
+  // Warp w joins the sums of the beams w, w + kWarps, ..., the next one's loads on their way.
+  struct Loads {
+    float score;
+    int done;
+    PieceSum part;
+  };
+  const auto load_beam = [&](int b) {
+    Loads x;
+    x.score = 0.f;
+    x.done = 0;
+    x.part.hi = x.part.lo = 0.f;
+    x.part.top = -INFINITY;
     if (b < a.B) {
-      scores[k] = __ldg(a.scores + n * a.B + b);
-      if (a.finished != nullptr) done[k] = __ldg(a.finished + n * a.B + b);
-      if (lane < splits) part[k] = lists.sum[n * pieces + b * splits + lane];  // of a beam not read: not used
+      x.score = __ldg(a.scores + n * a.B + b);
+      if (a.finished != nullptr) x.done = __ldg(a.finished + n * a.B + b);
+      if (lane < splits) x.part = lists.sum[n * pieces + b * splits + lane];  // of a beam not read: not used
     }
-  }
-#pragma unroll
-  for (int k = 0; k < BEAMS; ++k) {
-    const int b = warp + k * kWarps;
-    if (b >= a.B) break;
-    const bool reads = isfinite(scores[k]) && done[k] == 0;
+    return x;
+  };
+  Loads next = load_beam(warp);
+#pragma unroll 1
+  for (int b = warp; b < a.B; b += kWarps) {
+    const Loads x = next;
+    next = load_beam(b + kWarps);
+    const bool reads = isfinite(x.score) && x.done == 0;
     float hi = 0.f, lo = 0.f, top = -INFINITY;
     if (reads) {
       const PieceSum* p = lists.sum + n * pieces + b * splits;
-      top = part[k].top;
+      top = x.part.top;
       for (int s = lane + 32; s < splits; s += 32) top = fmaxf(top, p[s].top);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 1
       for (int s = lane; s < splits; s += 32) {
         // Times 2^(r_s - r), exact; below 2^-126 it adds nothing.  A NaN in the piece is in hi.
-        const PieceSum q = s == lane ? part[k] : p[s];
+        const PieceSum q = s == lane ? x.part : p[s];
         const int shift = q.top > -INFINITY ? reference_shift(q.top, top) : 0;
         const float scale = shift < -126 ? 0.f : __int_as_float((127 + min(shift, 0)) << 23);
         add_carried(hi, lo, q.hi * scale, q.lo * scale);
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
       s_hi[b] = hi;
       s_lo[b] = lo;
       s_top[b] = top;
-      s_kind[b] = reads ? (isfinite(top) ? 1 : 0) : (isfinite(scores[k]) ? 2 : 0);
+      s_kind[b] = reads ? (isfinite(top) ? 1 : 0) : (isfinite(x.score) ? 2 : 0);
     }
   }
   __syncthreads();
