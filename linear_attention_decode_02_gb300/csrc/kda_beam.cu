@@ -29,7 +29,7 @@
 // Shorter pieces made more of that: 1024 blocks instead of 512 took 22 to 25 us,
 // 2048 26 to 28, beside 19 to 21 then.  Both kernels run their code once a block, so
 // what is unrolled counts: one thread that read a marked batch again, all four
-// vectors of it, and a join unrolled over 32 beams made 21 us of the 19.
+// vectors of it, and a join unrolled over 32 beams took 21 us instead of 19.
 #include <float.h>
 
 #include "kda_cache.h"
@@ -173,7 +173,7 @@ __device__ __forceinline__ void place(const E* list, int count, int M, const Lar
     const int i = base + (threadIdx.x >> 2);
     const E mine = list[min(i, count - 1)];
     int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = part; j < count; j += 4) rank += larger(list[j], mine) ? 1 : 0;
     rank += __shfl_xor_sync(0xffffffffu, rank, 1);
     rank += __shfl_xor_sync(0xffffffffu, rank, 2);
