@@ -7,20 +7,22 @@
 // as in the bfloat16 kernel, and the copies are the same rings.
 //
 // The instructions take 11 significant bits of an operand.  Each is split in
-// two, x = hi + lo to 2^-21 or better, and the products hi hi, lo hi and hi lo
-// are added in float32; lo lo is below 2^-22.  So scores and outputs carry the
-// error of a few float32 roundings.  With up to 8 heads hi takes rows 0..7 and lo
+// two, x = hi + lo to 2^-20 (queries 2^-22), and the products hi hi, lo hi and hi
+// lo are added in float32; lo lo is below 2^-21 of a score's product, 2^-20 of an
+// output's.  Together that is below 28 and 48 half steps of float32, where a
+// float32 sum of that many products may be off by more.  With up to 8 heads hi takes rows 0..7 and lo
 // rows 8..15, one instruction for two products.  A split loses infinities (inf -
 // inf in lo), so scores that come out as NaN are computed once more without it;
 // an infinite value makes its row non-finite either way.
 //
 // Bound by the latency of each warp's steps: 0.37 GB of 12 / 1 heads of 128 take
-// 102 us, 55 % of the copy bandwidth (CUDA cores 165), of 64 112 (226), 32 / 2 heads of
-// 256 175 (272).  At 102 us the issue slots are 37 % used, the tensor pipe 29 %
-// and shared memory 45 %, with two warps a scheduler and all registers taken.
-// Sums kept apart for every kind of product, four outputs in turn, a rolled
-// first product and queries laid out without bank conflicts changed that by 2 %
-// or made it slower.
+// 96 us, 58 % of the copy bandwidth (CUDA cores 165), of 64 106 (226), 32 / 2 heads of
+// 256 159 (272).  With parts rounded by conversion instructions, which took 102,
+// 112 and 175 us, the issue slots were 37 % used, the tensor pipe 29 % and shared
+// memory 45 %, with two warps a scheduler and all registers taken.  Sums kept
+// apart for every kind of product, four outputs in turn, a rolled first product
+// and queries laid out without bank conflicts changed that by 2 % or made it
+// slower.
 //
 // Keys and values are read from shared memory a word a lane: rows are XORed
 // into the 16-byte chunks, and the second product takes its positions in the
@@ -57,9 +59,9 @@ __device__ __forceinline__ uint32_t round_tf32(float x) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
   return r;
 }
-// x = hi + lo: hi to nearest, lo cut to 11 bits of what is left.
+// x = hi + lo, both cut to 11 bits: rounded up, either could take a finite x past the largest float.
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = round_tf32(x);
+  hi = __float_as_uint(x) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -196,6 +196,18 @@ def test_many_heads_in_narrow_and_wide_tables(D, Hq, Hkv, width):
     check(c, window=5000)
 
 
+@pytest.mark.parametrize("Hq", [2, 8, 12])
+@pytest.mark.parametrize("width", [5, 4500])
+def test_values_near_the_largest_float(Hq, width):
+    # Equal weights of the largest float and of nothing: half of it, which bfloat16 holds as 2^127.
+    c = make([2, 70], Hq=Hq, Hkv=1, D=128, page=16, dtype=FP32, width=width, garbage=False)
+    page = c["table"][0, 0]
+    c["k"][page, 0] = c["k"][page, 1]
+    c["v"][page, 0], c["v"][page, 1] = torch.finfo(FP32).max, 0.0
+    out, _ = run(c)
+    assert torch.all(out[0].float() == 2.0 ** 127) and torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("where", ["query", "value"])
 def test_many_heads_with_a_bad_query_or_value(where, bad):
