@@ -332,7 +332,8 @@ kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, dou
  * read into the result, whatever their bytes hold.  A row without positions
  * gives zero and an lse of minus infinity.  At an attended position a NaN, a
  * score of +infinity and an infinite value make the row's result non-finite; a
- * score of -infinity weighs nothing.
+ * score of -infinity weighs nothing.  Values are summed before they are divided
+ * by the weights' sum, so finite ones whose weighted sum passes float32 overflow.
  */
 kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
                                       const kda_tensor* page_table, const kda_tensor* seq_lens,

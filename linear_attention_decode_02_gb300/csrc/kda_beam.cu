@@ -22,7 +22,7 @@
 //
 // Every logit is read once, 64 bytes a thread on their way while 64 are summed.
 // 32 requests of 8 beams, a tenth of them finished, over 131072 tokens in bf16,
-// 61 MB, which a copy would read in 9 us, take 19 to 20 us a call.  Alone the scan
+// 61 MB, which a copy would read in 9 us, take 19 to 21 us a call.  Alone the scan
 // takes 17 to 18 us and the join 6, which starts under the scan's end.  The scan
 // uses 42 % of the DRAM's peak: after the last logit come the bound, the list
 // and the order, behind barriers, and all pieces reach them at the same time.
