@@ -96,19 +96,25 @@ __device__ __forceinline__ void log_carried(float& hi, float& lo) {
   add_carried(hi, lo, 2.f * q, 2.f * (ql + q * z * tail));
 }
 
-// c = top log2(e) - r to float32, for the integer r next above top log2(e).
+// A piece with the largest logit `top` is summed relative to 2^r, r the integer
+// next above top log2(e).  Its float32 product rounds to 2^-4 before kNear, so r
+// can be one off there; all that counts is that a piece's r, and the scaling of
+// its sum, follow from its own top alone: in float32 where near() holds,
+// in float64 beyond.
 constexpr float kNear = 1048576.f;  // float32 holds r exactly, with room for c
-__device__ __forceinline__ float fraction(float top) {
-  const float p = top * kLog2e;
-  if (fabsf(p) < kNear) return (p - ceilf(p)) + fmaf(top, kLog2eLow, fmaf(top, kLog2e, -p));
+__device__ __forceinline__ bool near(float top) { return fabsf(top * kLog2e) < kNear; }
+__device__ __forceinline__ double reference(float top) {
+  return near(top) ? (double)ceilf(top * kLog2e) : ceil(top * kLog2eDouble);
+}
+// c = top log2(e) - r of a top that is not near, to float32.
+__device__ __forceinline__ float far_fraction(float top) {
   const double x = top * kLog2eDouble;
   return (float)(x - ceil(x));
 }
 // r of `own` minus r of `top`, at most 0 for own <= top; below -1000 it is -1000.
 __device__ __forceinline__ int reference_shift(float own, float top) {
-  const float p = own * kLog2e, q = top * kLog2e;
-  if (fabsf(p) < kNear && fabsf(q) < kNear) return (int)fmaxf(ceilf(p) - ceilf(q), -1000.f);
-  return (int)fmax(ceil(own * kLog2eDouble) - ceil(top * kLog2eDouble), -1000.0);
+  if (near(own) && near(top)) return (int)fmaxf(ceilf(own * kLog2e) - ceilf(top * kLog2e), -1000.f);
+  return (int)fmax(reference(own) - reference(top), -1000.0);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -334,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
       if (s_tops[k][tid] >= bound) s_hot[atomicAdd(&s_hots, 1)] = (uint16_t)(k * kThreads + tid);
   }
   float hi, lo = 0.f;
-  if (fabsf(all) < kNear / kLog2e) {
+  if (near(all)) {
     const int shift = (int)fmaxf(r - ceilf(all * kLog2e), -127.f);  // r is at most the block's
     hi = sum * __int_as_float((shift + 127) << 23);
   } else {
     // Logits of 10^6 and more (or none above -inf, or infinite): once more, by their distance from the largest.
-    const float base = all > -INFINITY ? all : 0.f, c = fraction(base);
+    const float base = all > -INFINITY ? all : 0.f, c = all > -INFINITY ? far_fraction(base) : 0.f;
     hi = 0.f;
     for (int i = max(first, 0) + tid; i < end; i += kThreads)
       hi += ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c));
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     float hi = score, lo = 0.f;
     if (s_kind[tid] == 1) {
       const float top = s_top[tid], sum = s_hi[tid], up = ceilf(top * kLog2e);
-      if (fabsf(top * kLog2e) < kNear) {  // score - log(sum) - (r ln 2 - top)
+      if (near(top)) {  // score - log(sum) - (r ln 2 - top)
         float ln = sum, lnl = s_lo[tid];
         log_carried(ln, lnl);
         const float p = up * kLn2;
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
         add_carried(hi, lo, -ln, -lnl);
         if (!(sum > 0.f && isfinite(sum))) hi = NAN;
       } else {
-        const double offset = (double)score - (log((double)sum + (double)s_lo[tid]) - (double)fraction(top) * kLn2Double);
+        const double offset = (double)score - (log((double)sum + (double)s_lo[tid]) - (double)far_fraction(top) * kLn2Double);
         hi = (float)offset;
         lo = (float)(offset - (double)hi);
       }
