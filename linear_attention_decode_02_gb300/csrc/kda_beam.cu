@@ -45,7 +45,7 @@ constexpr int kList = 1024;   // elements that may pass the bound
 constexpr int kJoin = 4096;
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;  // log2(e) to 2^-50
 constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;  // ln 2 to 2^-50
-constexpr double kLog2eDouble = 1.4426950408889634, kLn2Double = 0.6931471805599453;
+constexpr double kLog2eDouble = 1.4426950408889634;
 
 // Sum of 2^((x - top) log2(e) + c) over a piece, as hi + lo.
 struct PieceSum {
@@ -566,20 +566,25 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
     const float score = __ldg(a.scores + n * a.B + tid);
     float hi = score, lo = 0.f;
     if (s_kind[tid] == 1) {
-      const float top = s_top[tid], sum = s_hi[tid], up = ceilf(top * kLog2e);
-      if (near(top)) {  // score - log(sum) - (r ln 2 - top)
-        float ln = sum, lnl = s_lo[tid];
-        log_carried(ln, lnl);
-        const float p = up * kLn2;
-        add_carried(hi, lo, top, 0.f);
-        add_carried(hi, lo, -p, -fmaf(up, kLn2, -p) - up * kLn2Low);
-        add_carried(hi, lo, -ln, -lnl);
-        if (!(sum > 0.f && isfinite(sum))) hi = NAN;
-      } else {
-        const double offset = (double)score - (log((double)sum + (double)s_lo[tid]) - (double)far_fraction(top) * kLn2Double);
-        hi = (float)offset;
-        lo = (float)(offset - (double)hi);
-      }
+      // log sum exp(x - top) = log(1 + (S - E) / 2^c), with S the pieces' sum, c = top log2(e) - r, and E = 2^c as the
+      // scan rounded it: E's own error, `off` relative to it, is not in the result, which is 0 where nothing but
+      // the largest logit weighs anything, so that a beam's only token is worth its score to the bit.
+      const float top = s_top[tid], all = s_hi[tid], up = ceilf(top * kLog2e);
+      const float c = near(top) ? fmaf(top, kLog2eLow, fmaf(top, kLog2e, -up)) : far_fraction(top), e = ex2(c);
+      float base = e, basel = 0.f;
+      log_carried(base, basel);
+      const float of = near(top) ? -up : c, p = of * kLn2;  // c ln 2 as two floats
+      float exact = near(top) ? top : 0.f, exactl = 0.f;
+      add_carried(exact, exactl, p, fmaf(of, kLn2, -p) + of * kLn2Low);
+      add_carried(exact, exactl, -base, -basel);
+      const float off = exact + exactl;
+      float ln = all, lnl = s_lo[tid], rest = ln, restl = lnl;
+      add_carried(rest, restl, -e, 0.f);
+      add_carried(ln, lnl, -(rest + restl) * off, 0.f);
+      log_carried(ln, lnl);
+      add_carried(base, basel, -ln, -lnl);
+      add_carried(hi, lo, base, basel);
+      if (!(all > 0.f && isfinite(all))) hi = NAN;
       if (!isfinite(hi)) s_kind[tid] = 0;
     }
     s_hi[tid] = hi;

@@ -51,3 +51,31 @@ def test_full_rows_around_the_limit():
     x = LIMIT + torch.randint(-160, 33, (4, 3, 50257), generator=g).double() / 16
     check(x.float().cuda(), torch.randn(4, 3, generator=g).cuda(), 8)
     check((-x).float().cuda(), torch.randn(4, 3, generator=g).cuda(), 8)
+
+
+@pytest.mark.parametrize("top", [1e6, 1e20, 3e38, -1e6, -1e20, -3e38])
+def test_pieces_far_past_the_limit(top):
+    x = torch.full((2, 2, 30000), top)
+    x[0, 0, 100], x[0, 1, 29000] = 5.0, -7.0   # above or far below the rest
+    scores = torch.zeros(2, 2, device="cuda")
+    if top > -1e16:
+        check(x.cuda(), scores, 6)
+        return
+    # Exactly: beams 0 and 1 are certain of tokens 100 and 29000, and their other tokens are worth top - 5 and top + 7.
+    # float64, which the oracle computes in, holds neither apart from top; the sums of two float32 do.
+    got = binding.kda_beam_select(x.cuda(), scores, 6)
+    assert got[1].tolist() == [[0, 1, 1, 1, 1, 1], [0] * 6]
+    assert got[2].tolist() == [[100, 29000, 0, 1, 2, 3], list(range(6))]
+    assert torch.equal(got[0][0].cpu(), torch.tensor([0.0, 0.0] + [top] * 4))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_forced_token_leaves_the_score_as_it_is(dtype):
+    # one token allowed: its probability is 1, so equal scores tie to the lower beam and are returned to the bit
+    g = torch.Generator().manual_seed(4)
+    x = torch.full((64, 4, 5000), -float("inf"))
+    at = torch.randint(0, 5000, (64, 4, 1), generator=g)
+    x.scatter_(2, at, torch.randn(64, 4, 1, generator=g) * 30)
+    s = (torch.randn(64, 1, generator=g) - 10).expand(64, 4).contiguous()
+    got = check(x.to(dtype).cuda(), s.cuda(), 4)
+    assert torch.equal(got[0].cpu(), s) and torch.equal(got[1].cpu(), torch.arange(4, dtype=torch.int32).expand(64, 4))
