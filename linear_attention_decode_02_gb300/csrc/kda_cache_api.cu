@@ -426,7 +426,6 @@ kda_status kda_beam_select(const kda_tensor* logits, const kda_tensor* scores, c
   const int64_t N = X.shape[0], B = X.shape[1], V = X.shape[2], M = OS.shape[1];
   KDA_TRY(need_dtype(X, KDA_F32, KDA_BF16));
   KDA_CHECK(V <= 1 || X.stride[2] == 1, KDA_ERR_INVALID_ARG, "logits: vocabulary axis must have stride 1");
-  KDA_CHECK(reinterpret_cast<uintptr_t>(X.data) % esize(X.dtype) == 0, KDA_ERR_INVALID_ARG, "logits: misaligned data");
   KDA_TRY(check_beam_sizes(N, B, V, M));
   KDA_TRY(need_dtype(S, KDA_F32));
   KDA_TRY(need_shape(S, 0, N));

@@ -96,7 +96,10 @@ inline kda_status raw_view(const kda_tensor* t, const char* name, View* v) {
     v->shape[i] = t->shape[i];
     v->stride[i] = t->shape[i] <= 1 && t->stride[i] <= 0 ? 1 : t->stride[i];
   }
-  KDA_CHECK(v->data != nullptr || v->numel() == 0, KDA_ERR_INVALID_ARG, "%s: null data pointer", name);
+  if (v->numel() == 0) return KDA_OK;
+  KDA_CHECK(v->data != nullptr, KDA_ERR_INVALID_ARG, "%s: null data pointer", name);
+  KDA_CHECK(reinterpret_cast<uintptr_t>(v->data) % esize(v->dtype) == 0, KDA_ERR_INVALID_ARG,
+            "%s: data must be %lld-byte aligned", name, (long long)esize(v->dtype));
   return KDA_OK;
 }
 
