@@ -7,13 +7,14 @@
 // as in the bfloat16 kernel, and the copies are the same rings.
 //
 // The instructions take 11 significant bits of an operand.  Each is split in
-// two, x = hi + lo to 2^-20 (queries 2^-22), and the products hi hi, lo hi and hi
-// lo are added in float32; lo lo is below 2^-21 of a score's product, 2^-20 of an
-// output's.  Together that is below 28 and 48 half steps of float32, where a
-// float32 sum of that many products may be off by more.  With up to 8 heads hi takes rows 0..7 and lo
-// rows 8..15, one instruction for two products.  A split loses infinities (inf -
-// inf in lo), so scores that come out as NaN are computed once more without it;
-// an infinite value makes its row non-finite either way.
+// two, x = hi + lo to 2^-23 (queries and keys, hi rounded) or 2^-21 (weights and
+// values, hi cut), and the products hi hi, lo hi and hi lo are added in float32; lo
+// lo is below 2^-22 of a score's product, 2^-20 of an output's.  Together that is
+// below 7 and 28 half steps of float32, where a float32 sum of that many products
+// may be off by more.  With up to 8 heads hi takes rows 0..7 and lo rows 8..15, one
+// instruction for two products.  A split loses infinities (inf - inf in lo), so
+// scores that come out as NaN are computed once more without it; an infinite value
+// makes its row non-finite either way.
 //
 // Bound by the latency of each warp's steps: 0.37 GB of 12 / 1 heads of 128 take
 // 96 us, 58 % of the copy bandwidth (CUDA cores 165), of 64 106 (226), 32 / 2 heads of
@@ -59,7 +60,17 @@ __device__ __forceinline__ uint32_t round_tf32(float x) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
   return r;
 }
-// x = hi + lo, both cut to 11 bits: rounded up, either could take a finite x past the largest float.
+// x = hi + lo in 11 bits each, less up to 2^-23 of x.  Of keys hi is the nearest
+// one: what lo then cuts off is as often above as below, and leans to no side (cut
+// in both parts, scores came out 2^-24 too small on average).  It can pass the
+// largest float, where hi and lo become opposite infinities and the score NaN.
+__device__ __forceinline__ void split_nearest(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+}
+// The same with hi cut, for weights and values, whose products are not computed
+// again: a finite one stays finite, and the 2^-24 that it is short of on average
+// is far below a bfloat16 output's step.
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
         for (int k = 0; k < KSTEPS; ++k) {
           uint32_t kh[2], kl[2], qh[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) split(word(base + key_at[i][k % 4] + k / 4 * 128), kh[i], kl[i]);
+          for (int i = 0; i < 2; ++i) split_nearest(word(base + key_at[i][k % 4] + k / 4 * 128), kh[i], kl[i]);
           const uint4 x = *reinterpret_cast<const uint4*>(tail + (k * 32 + lane) * 16);
           qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
           mma(s[k & 1], qh, kh[0], kh[1]);
