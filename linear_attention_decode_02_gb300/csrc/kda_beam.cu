@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatches = 8;   // batches of loads a block may take
 constexpr int kList = 1024;   // elements that may pass the bound
 constexpr int kJoin = 4096;
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;  // log2(e) to 2^-50
@@ -221,12 +220,67 @@ struct Raw<__nv_bfloat16> {
   __device__ __forceinline__ __nv_bfloat162 h(int i) const { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); }
 };
 
+// A thread's vector of a batch on its way.  Rows that all start on 16-byte
+// boundaries: neighbouring elements in one load.  Others: elements kThreads apart,
+// loaded one by one, so that which of them a thread adds, and in what order, does
+// not depend on where a row starts: equal rows have equal log-sums, and tie.
+// (16-byte loads from each row's own boundary on, which group by address, are
+// faster for bfloat16: 32 x 8 rows of 131071 23.6 us instead of 26.4, 16 x 8 of 50257
+// 11.4 and 13.0; float32 12 x 6 of 50257 12.5 and 12.3.)  Elements past the row are
+// -infinity.
+template <typename T, bool ALIGNED>
+struct Ahead;
+template <typename T>
+struct Ahead<T, true> {
+  static constexpr int STEP = 1;
+  Raw<T> v;
+  __device__ __forceinline__ void load(const T* row, int i, int V) {
+    constexpr int VEC = Raw<T>::VEC;
+    if (i + VEC <= V) {
+      v.load(row + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v.set(e, i + e < V ? row + i + e : nullptr);
+    }
+  }
+  __device__ __forceinline__ Raw<T> get() const { return v; }
+};
+template <>
+struct Ahead<float, false> {
+  static constexpr int STEP = kThreads;
+  Raw<float> v;
+  __device__ __forceinline__ void load(const float* row, int i, int V) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.set(e, i + e * STEP < V ? row + i + e * STEP : nullptr);
+  }
+  __device__ __forceinline__ Raw<float> get() const { return v; }
+};
+template <>
+struct Ahead<__nv_bfloat16, false> {
+  static constexpr int STEP = kThreads;
+  unsigned short u[8];  // a register each until they are used
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int i, int V) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      u[e] = i + e * STEP < V ? __ldg(reinterpret_cast<const unsigned short*>(row) + i + e * STEP) : (unsigned short)0xff80;
+  }
+  __device__ __forceinline__ Raw<__nv_bfloat16> get() const {
+    Raw<__nv_bfloat16> v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.w[e] = u[2 * e] | (uint32_t)u[2 * e + 1] << 16;
+    return v;
+  }
+};
+
 // Groups of threads for the bound.
 __device__ __forceinline__ int bound_groups(int M) {
   int g = kWarps;
   while (g < M) g *= 2;
   return g;
 }
+
+// Batches that a block may take: pieces have up to 32 vectors a thread, 2 where a batch has one.
+__host__ __device__ constexpr int most_batches(int loads) { return loads == 1 ? 2 : 32 / loads; }
 
 // Thread's sum of 2^(x log2(e) - r) for one batch of loads, r at least every exponent.
 template <typename T, int LOADS>
@@ -244,45 +298,45 @@ __device__ __forceinline__ float batch_sum(const Raw<T> (&x)[LOADS], float r) {
   return sum.x + sum.y;
 }
 
-template <typename T, int LOADS>
+template <typename T, int LOADS, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamArgs a, int splits, int batches) {
-  constexpr int VEC = Raw<T>::VEC, BATCH = LOADS * kThreads * VEC;
+  using Vector = Ahead<T, ALIGNED>;
+  constexpr int VEC = Raw<T>::VEC, BATCH = LOADS * kThreads * VEC, STEP = Vector::STEP;
+  constexpr int MOST = most_batches(LOADS);
   __shared__ uint32_t s_key[kThreads];
-  __shared__ float s_hi[kThreads], s_tops[kBatches][kThreads];
+  __shared__ float s_hi[kThreads], s_tops[MOST][kThreads];
   __shared__ uint64_t s_list[kList];
-  __shared__ uint16_t s_hot[kBatches * kThreads];
+  __shared__ uint16_t s_hot[MOST * kThreads];
   __shared__ int s_count, s_hots;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t beam = blockIdx.x / (uint32_t)splits;
   const int split = blockIdx.x - beam * splits;
   if (tid == 0) s_count = s_hots = 0;
 
-  // The vectors lie on 16-byte boundaries; the row may start and end inside one.
   const uint32_t n = beam / (uint32_t)a.B;
   const T* row = static_cast<const T*>(a.logits) + n * a.ns + (beam - n * a.B) * a.bs;
-  const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-  const int first = split * batches * BATCH - lead;  // of the piece
-  const int i0 = first + tid * VEC;                  // of this thread's first vector
-  const auto load_vector = [&](int i, Raw<T>& v) {
-    if (i >= 0 && i + VEC <= a.V) {
+  const int first = split * batches * BATCH;  // of the piece
+  // Where vector j of thread t's batch starts; its elements are STEP apart.
+  const auto place_of = [&](int batch, int j, int t) {
+    return first + batch * BATCH + j * kThreads * VEC + (ALIGNED ? t * VEC : t);
+  };
+  const auto load = [&](int batch, Vector(&x)[LOADS]) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) x[j].load(row, place_of(batch, j, tid), a.V);
+  };
+  // VEC elements that follow one another, whatever their alignment.
+  const auto load_run = [&](int i, Raw<T>& v) {
+    if (ALIGNED && i + VEC <= a.V) {
       v.load(row + i);
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v.set(e, nullptr);
-      if (i + VEC > 0 && i < a.V) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (i + e >= 0 && i + e < a.V) v.set(e, row + i + e);
-      }
+      for (int e = 0; e < VEC; ++e) v.set(e, i + e < a.V ? row + i + e : nullptr);
     }
-  };
-  const auto load = [&](int batch, Raw<T>(&x)[LOADS]) {
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) load_vector(i0 + batch * BATCH + j * kThreads * VEC, x[j]);
   };
   pdl_wait();
   pdl_launch_dependents();
-  Raw<T> x[LOADS], ahead[LOADS];
+  Raw<T> x[LOADS];
+  Vector ahead[LOADS];
   load(0, ahead);
   // A live beam's score is finite and it is not finished; of others the first batch is read for nothing.
   const int done = a.finished != nullptr ? __ldg(a.finished + beam) : 0;
@@ -294,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
 #pragma unroll 1
   for (int k = 0; k < batches; ++k) {
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) x[j] = ahead[j];
+    for (int j = 0; j < LOADS; ++j) x[j] = ahead[j].get();
     if (k + 1 < batches) load(k + 1, ahead);
     float t = x[0].top();
 #pragma unroll
@@ -327,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
       const float w = e % 2 == 0 ? p.x : p.y;
       if (w >= bound && w > -INFINITY) {
         const int at = atomicAdd(&s_count, 1);
-        if (at < kList) s_list[at] = candidate(w, i + e);
+        if (at < kList) s_list[at] = candidate(w, i + e * STEP);
       }
     }
   };
   if (batches == 1) {
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) push(x[j], i0 + j * kThreads * VEC);
+    for (int j = 0; j < LOADS; ++j) push(x[j], place_of(0, j, tid));
   } else if (top >= bound) {
 #pragma unroll 1
     for (int k = 0; k < batches; ++k)
@@ -347,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     // Logits of 10^6 and more (or none above -inf, or infinite): once more, by their distance from the largest.
     const float base = all > -INFINITY ? all : 0.f, c = all > -INFINITY ? far_fraction(base) : 0.f;
     hi = 0.f;
-    for (int i = max(first, 0) + tid; i < end; i += kThreads)
+    for (int i = first + tid; i < end; i += kThreads)
       hi += ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c));
   }
   s_hi[tid] = hi;
@@ -355,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   if (batches > 1) {
     for (int h = tid; h < s_hots * LOADS; h += kThreads) {
       const int entry = s_hot[h / LOADS];
-      const int at = first + (entry / kThreads) * BATCH + (h % LOADS * kThreads + entry % kThreads) * VEC;
-      Raw<T> v;
-      load_vector(at, v);
-      push(v, at);
+      const int at = place_of(entry / kThreads, h % LOADS, entry % kThreads);
+      Vector v;
+      v.load(row, at, a.V);
+      push(v.get(), at);
     }
     __syncthreads();
   }
@@ -392,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   const int vectors = (end - first + VEC - 1) / VEC;
   for (int h = tid; h < vectors; h += kThreads) {
     Raw<T> v;
-    load_vector(first + h * VEC, v);
+    load_run(first + h * VEC, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float2 p = v.pair(e / 2);
@@ -410,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     int next = larger;  // place of the next equal one
     for (int h0 = 0; h0 < vectors && next < a.M && bound > -INFINITY; h0 += kThreads) {
       Raw<T> v;
-      load_vector(first + (h0 + tid) * VEC, v);
+      load_run(first + (h0 + tid) * VEC, v);
       int equal = 0;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -443,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   uint64_t last = ~0ull;
   for (int m = 0; m < a.M; ++m) {
     uint64_t mine = 0;
-    for (int i = max(first, 0) + tid; i < end; i += kThreads) {
+    for (int i = first + tid; i < end; i += kThreads) {
       const float v = static_cast<float>(row[i]);
       const uint64_t at = candidate(v, i);
       if (v >= bound && v > -INFINITY && at < last && at > mine) mine = at;
@@ -680,40 +734,51 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const BeamArgs 
   }
 }
 
-template <typename T>
+template <typename T, int LOADS, bool ALIGNED>
 cudaError_t launch_scan(const BeamArgs& a, const BeamPlan& p, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.N * a.B * p.splits)), threads(kThreads);
-  if (p.loads == 1) return launch_pdl(kda_beam_scan_kernel<T, 1>, grid, threads, 0, s, 1, a, p.splits, p.batches);
-  return launch_pdl(kda_beam_scan_kernel<T, 4>, grid, threads, 0, s, 1, a, p.splits, p.batches);
+  return launch_pdl(kda_beam_scan_kernel<T, LOADS, ALIGNED>, grid, threads, 0, s, 1, a, p.splits, p.batches);
+}
+
+// Vectors of a batch.  Elements loaded one by one take a register each, so
+// there bfloat16 has half as many on their way.
+int batch_loads(int vectors, int32_t dtype, bool aligned) {
+  if (vectors < 4) return 1;
+  return aligned || dtype == KDA_DT_F32 ? 4 : 2;
 }
 
 }  // namespace
 
-// The longest pieces (8 batches of 4 loads a thread) that still give every SM
-// two blocks, down to one load a thread, and not so short that the join, one
-// block a request, would have more than kJoin candidates to look at.  A row
-// whose start is not on a 16-byte boundary reaches up to vec - 1 elements further.
+// The longest pieces (32 vectors a thread) that still give every SM
+// two blocks, down to one vector, and not so short that the join, one
+// block a request, would have more than kJoin candidates to look at.
 BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms) {
   BeamPlan p;
   const int64_t vec = dtype == KDA_DT_F32 ? 4 : 8;
-  const auto splits = [&](int vectors, bool whole) {
-    const int64_t per = kThreads * vec * vectors;
-    return (int32_t)((V + (whole ? 0 : vec - 1) + per - 1) / per);
-  };
-  int vectors = 4 * kBatches;
-  while (vectors > 1 && (splits(vectors / 2, true) == 1 || (N * B * splits(vectors, true) < 2 * sms &&
-                                                           (int64_t)B * splits(vectors / 2, true) * M <= kJoin)))
+  const auto splits = [&](int vectors) { return (int32_t)((V + kThreads * vec * vectors - 1) / (kThreads * vec * vectors)); };
+  int vectors = 32;
+  while (vectors > 1 && (splits(vectors / 2) == 1 || (N * B * splits(vectors) < 2 * sms &&
+                                                      (int64_t)B * splits(vectors / 2) * M <= kJoin)))
     vectors /= 2;
-  p.loads = vectors >= 4 ? 4 : 1;
-  p.splits = splits(vectors, aligned);
+  p.aligned = aligned;
+  p.loads = batch_loads(vectors, dtype, aligned);
+  p.splits = splits(vectors);
   const int64_t batch = kThreads * vec * p.loads * (int64_t)p.splits;  // the splits share the row evenly
-  p.batches = (int32_t)((V + (aligned ? 0 : vec - 1) + batch - 1) / batch);
-  p.floats = N * B * splits(vectors, false) * (4 + 2 * (int64_t)M);
+  p.batches = (int32_t)((V + batch - 1) / batch);
+  p.floats = N * B * p.splits * (4 + 2 * (int64_t)M);
   return p;
 }
 
 cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& p, cudaStream_t s) {
-  const cudaError_t e = a.dtype == KDA_DT_F32 ? launch_scan<float>(a, p, s) : launch_scan<__nv_bfloat16>(a, p, s);
+  using bf16 = __nv_bfloat16;
+  cudaError_t e;
+  if (a.dtype == KDA_DT_F32) {
+    e = p.aligned ? (p.loads == 1 ? launch_scan<float, 1, true>(a, p, s) : launch_scan<float, 4, true>(a, p, s))
+                  : (p.loads == 1 ? launch_scan<float, 1, false>(a, p, s) : launch_scan<float, 4, false>(a, p, s));
+  } else {
+    e = p.aligned ? (p.loads == 1 ? launch_scan<bf16, 1, true>(a, p, s) : launch_scan<bf16, 4, true>(a, p, s))
+                  : (p.loads == 1 ? launch_scan<bf16, 1, false>(a, p, s) : launch_scan<bf16, 2, false>(a, p, s));
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(kda_beam_join_kernel, dim3((unsigned)a.N), dim3(kThreads), 0, s, 1, a, p.splits);
 }

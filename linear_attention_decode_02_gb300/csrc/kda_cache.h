@@ -95,9 +95,10 @@ struct BeamArgs {
 // A block scans `batches` times 256 * `loads` vectors of 16 bytes of one beam; `splits` blocks a beam.
 struct BeamPlan {
   int32_t loads, batches, splits;
+  bool aligned;  // every row starts on a 16-byte boundary
   int64_t floats;
 };
-// `aligned`: every row starts on a 16-byte boundary (fewer splits; `floats` serves both).
+// `splits` and `floats` are the same for either alignment.
 BeamPlan beam_plan(int64_t N, int32_t B, int32_t V, int32_t M, int32_t dtype, bool aligned, int32_t sms);
 cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& p, cudaStream_t s);
 

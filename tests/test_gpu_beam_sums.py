@@ -79,3 +79,30 @@ def test_a_forced_token_leaves_the_score_as_it_is(dtype):
     s = (torch.randn(64, 1, generator=g) - 10).expand(64, 4).contiguous()
     got = check(x.to(dtype).cuda(), s.cuda(), 4)
     assert torch.equal(got[0].cpu(), s) and torch.equal(got[1].cpu(), torch.arange(4, dtype=torch.int32).expand(64, 4))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("N,B,V,M", [(1, 4, 501, 4), (2, 3, 2049, 9), (3, 8, 4097, 16), (1, 32, 9001, 64), (4, 5, 50257, 5),
+                                     (1, 2, 131071, 2), (40, 4, 30522, 8), (64, 3, 100003, 6)])
+def test_equal_beams_tie_to_the_first_wherever_their_rows_start(dtype, N, B, V, M):
+    # odd vocabularies: no two of a request's rows start alike on 16-byte boundaries
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(N, 1, V, generator=g) * 2.5).to(dtype).expand(N, B, V).contiguous().cuda()
+    s = (torch.randn(N, 1, generator=g) - 10).expand(N, B).contiguous().cuda()
+    check(x, s, M)  # a bfloat16 row may hold its largest logit twice: both of the first beam, then the next one's
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [777, 20001, 140001])
+def test_rows_that_start_elsewhere_have_the_same_sums(dtype, V):
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(2, 3, V, generator=g) * 2.5).to(dtype).cuda()
+    s = torch.randn(2, 3, generator=g).cuda()
+    results = []
+    for start in range(1, 8):
+        wide = torch.zeros(2 * 3 * (V + 8), dtype=dtype, device="cuda")
+        rows = torch.as_strided(wide, (2, 3, V), (3 * (V + 8), V + 3, 1), start)
+        rows.copy_(x)
+        results.append(check(rows, s, 12))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
