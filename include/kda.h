@@ -361,9 +361,9 @@ kda_status kda_paged_attention_workspace(int32_t q_heads, int32_t kv_heads, int3
  * the M largest of a request's B * V are returned in falling order, equal ones
  * by rising b, then t.  Candidates are compared as unrounded sums of two
  * float32, the returned score is rounded to float32.  A beam's log-sum is off
- * by the error of a float32 exponential, 2.4e-7 at most for few tokens, far less
- * over a vocabulary, so beams whose candidates are closer than that may be
- * taken in either order; beams of equal logits and scores are equal, wherever
+ * by 1.1e-6 at most, 3.5e-7 where all logits are equal, far less over a
+ * vocabulary of unequal ones, so beams whose candidates are closer than that
+ * may be taken in either order; beams of equal logits and scores are equal, wherever
  * their rows start.  A logit of minus infinity is no continuation, and a beam
  * whose score or log-sum is not finite (a dead beam; a NaN or +infinity among
  * its logits) has none.  Places without one get -infinity, -1 and -1.

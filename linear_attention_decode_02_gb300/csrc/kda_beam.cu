@@ -14,11 +14,16 @@
 // Which beam wins decides the tokens, so the log-sums have to be better than
 // float32 gives: a piece's exponentials are 2^((x - top) log2(e) + c), with c
 // such that top log2(e) - c is an integer, so that pieces are rescaled by exact
-// powers of two; log2(e) enters in two parts; lanes and pieces are added with
-// the rounding carried along; and logarithms and candidates are unrounded sums
-// of two float32 (float64 runs at a hundredth of float32's rate here: a
-// logarithm in it alone took 1.8 us).  What is left are the exponentials' own errors, which
-// are random and average out over the vocabulary.
+// powers of two; log2(e) enters in two parts; batches, lanes and
+// pieces are added with the rounding carried along; and logarithms and
+// candidates are unrounded sums of two float32 (float64 runs at a hundredth of
+// float32's rate here: a logarithm in it alone took 1.8 us).  What is left,
+// relative to the sum: 2^-22 of the exponential's approximation; two roundings of
+// its argument, 4.4e-7 at worst, where a thread's 256 logits are all 8 ln 2 below
+// its largest; and six of a batch's additions, 3.6e-7.  Measured: 1.6e-7 on rows
+// of one or two values (3.1e-7 with a thread's terms added one after another, in
+// 0.5 us less for the large case below); on 65536 normal logits 5e-8, all but 5e-9 of
+// it common to all beams, since the approximation errs a little to one side.
 //
 // Every logit is read once, 64 bytes a thread on their way while 64 are summed.
 // 32 requests of 8 beams, a tenth of them finished, over 131072 tokens in bf16,
@@ -282,19 +287,29 @@ __device__ __forceinline__ int bound_groups(int M) {
 // Batches that a block may take: pieces have up to 32 vectors a thread, 2 where a batch has one.
 __host__ __device__ constexpr int most_batches(int loads) { return loads == 1 ? 2 : 32 / loads; }
 
-// Thread's sum of 2^(x log2(e) - r) for one batch of loads, r at least every exponent.
+// Thread's sum of 2^(x log2(e) - r) for one batch of loads, r at least every
+// exponent.  Added in a tree: at most six roundings in a row, and next to none
+// where all terms are equal.
 template <typename T, int LOADS>
 __device__ __forceinline__ float batch_sum(const Raw<T> (&x)[LOADS], float r) {
+  constexpr int PAIRS = Raw<T>::VEC / 2;
   const float2 hi2 = dup2(kLog2e), lo2 = dup2(kLog2eLow), r2 = dup2(-r);
-  float2 sum = make_float2(0.f, 0.f);
+  float2 sum;
 #pragma unroll
-  for (int j = 0; j < LOADS; ++j)
+  for (int j = 0; j < LOADS; ++j) {
+    float2 e[PAIRS];
 #pragma unroll
-    for (int i = 0; i < Raw<T>::VEC / 2; ++i) {
+    for (int i = 0; i < PAIRS; ++i) {
       const float2 v = x[j].pair(i);
-      const float2 e = fma2(v, lo2, fma2(v, hi2, r2));
-      sum = add2(sum, make_float2(ex2(e.x), ex2(e.y)));
+      e[i] = fma2(v, lo2, fma2(v, hi2, r2));
+      e[i] = make_float2(ex2(e[i].x), ex2(e[i].y));
     }
+#pragma unroll
+    for (int o = 1; o < PAIRS; o *= 2)
+#pragma unroll
+      for (int i = 0; i < PAIRS; i += 2 * o) e[i] = add2(e[i], e[i + o]);
+    sum = j == 0 ? e[0] : add2(sum, e[0]);
+  }
   return sum.x + sum.y;
 }
 
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   constexpr int VEC = Raw<T>::VEC, BATCH = LOADS * kThreads * VEC, STEP = Vector::STEP;
   constexpr int MOST = most_batches(LOADS);
   __shared__ uint32_t s_key[kThreads];
-  __shared__ float s_hi[kThreads], s_tops[MOST][kThreads];
+  __shared__ float s_hi[kThreads], s_lo[kThreads], s_tops[MOST][kThreads];
   __shared__ uint64_t s_list[kList];
   __shared__ uint16_t s_hot[MOST * kThreads];
   __shared__ int s_count, s_hots;
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
 
   // One batch is summed while the next is on its way.  The thread's reference
   // r moves in whole steps, so rescaling its sum is exact.
-  float top = -INFINITY, r = -kNear, sum = 0.f;
+  float top = -INFINITY, r = -kNear, sum = 0.f, rest = 0.f;
 #pragma unroll 1
   for (int k = 0; k < batches; ++k) {
 #pragma unroll
@@ -357,10 +372,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     top = fmaxf(top, t);
     const float up = ceilf(t * kLog2e);
     if (up > r) {
-      sum *= __int_as_float(max((int)fmaxf(r - up, -126.f) + 127, 0) << 23);
+      const float down = __int_as_float(max((int)fmaxf(r - up, -126.f) + 127, 0) << 23);
+      sum *= down;
+      rest *= down;
       r = up;
     }
-    sum += batch_sum<T, LOADS>(x, r);
+    add_carried(sum, rest, batch_sum<T, LOADS>(x, r), 0.f);
   }
 
   s_key[tid] = sortable(top);
@@ -396,15 +413,18 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   float hi, lo = 0.f;
   if (near(all)) {
     const int shift = (int)fmaxf(r - ceilf(all * kLog2e), -127.f);  // r is at most the block's
-    hi = sum * __int_as_float((shift + 127) << 23);
+    const float down = __int_as_float((shift + 127) << 23);
+    hi = sum * down;
+    lo = rest * down;
   } else {
     // Logits of 10^6 and more (or none above -inf, or infinite): once more, by their distance from the largest.
     const float base = all > -INFINITY ? all : 0.f, c = all > -INFINITY ? far_fraction(base) : 0.f;
     hi = 0.f;
     for (int i = first + tid; i < end; i += kThreads)
-      hi += ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c));
+      add_carried(hi, lo, ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c)), 0.f);
   }
   s_hi[tid] = hi;
+  s_lo[tid] = lo;
   __syncthreads();
   if (batches > 1) {
     for (int h = tid; h < s_hots * LOADS; h += kThreads) {
@@ -422,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
   uint64_t* best = lists.best + piece * a.M;
   if (warp == kWarps - 1) {  // the last to have a candidate to place
     hi = s_hi[lane];
+    lo = s_lo[lane];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) add_carried(hi, lo, s_hi[w * 32 + lane], 0.f);
+    for (int w = 1; w < kWarps; ++w) add_carried(hi, lo, s_hi[w * 32 + lane], s_lo[w * 32 + lane]);
     warp_sum_carried(hi, lo);
     if (lane == 0) {
       PieceSum p;

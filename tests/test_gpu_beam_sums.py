@@ -106,3 +106,56 @@ def test_rows_that_start_elsewhere_have_the_same_sums(dtype, V):
         results.append(check(rows, s, 12))
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+def log_sum_errors(x):
+    """Error of the log-sums of rows x [N, 1, V], from scores that put the results near 0, where float32 is fine."""
+    ref = torch.logsumexp(x.double(), -1) - x.double().amax(-1)
+    s = ref.float()
+    got = binding.kda_beam_select(x, s, 1)
+    torch.cuda.synchronize()
+    return got[0][:, 0].double() - (s.double() - ref)[:, 0]
+
+
+def log_sum_error(x):
+    return log_sum_errors(x).abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [65536, 131071])
+def test_log_sums_of_constant_rows(dtype, V):
+    # Every exponential has the same error, 2^-22 at most, and its argument, within 1 of 0, two roundings of 2^-25;
+    # equal terms add up in a tree with one rounding at most of three of them; the rest is carried along.
+    x = torch.linspace(-20, 20, 512).to(dtype).cuda().view(-1, 1, 1)
+    for rows in x.split(128):
+        assert log_sum_error(rows.expand(-1, 1, V).contiguous()) <= 2.0 ** -22 + 0.7 * 2.0 ** -24 + 2.0 ** -24 + 1e-9
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [65536, 131071])
+@pytest.mark.parametrize("below", [1.0, 4.0, 5.5, 5.59, 11.0])
+def test_log_sums_of_few_distinct_values(dtype, V, below):
+    # most logits `below` the largest one, one in 256 (a thread's share) the largest: 2^-22 of the exponential, 4.4e-7 of
+    # its argument's roundings (their worst, at 8 ln 2 = 5.55), six roundings of 2^-24
+    top = torch.linspace(-3, 3, 96).to(dtype)
+    x = (top - torch.tensor(below).to(dtype)).view(-1, 1, 1).expand(-1, 1, V).contiguous()
+    x[:, 0, ::256] = top[:, None]
+    assert log_sum_error(x.cuda()) <= 1.1e-6
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_log_sums_of_unequal_logits_average_out(dtype):
+    # Of 65537 terms: 2^-22 bounds what the exponentials have in common, 2^-21 / sqrt(the number that weighs, over 4096)
+    # the deviation of the rest, of which ten are allowed between the rows.
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(64, 1, 65537, generator=g).to(dtype).cuda()
+    errors = log_sum_errors(x)
+    assert errors.abs().max() <= 2.0 ** -22 + 10 * 2.0 ** -27 and errors.max() - errors.min() <= 10 * 2.0 ** -27
+
+
+def test_log_sums_past_the_limit():
+    # each term is found from its distance to the largest logit, and every addition carries its rounding
+    g = torch.Generator().manual_seed(7)
+    x = (LIMIT + 100 + torch.randint(0, 16, (16, 1, 70001), generator=g).double() / 16).float()
+    assert log_sum_error(x.cuda()) <= 1.1e-6
+    assert log_sum_error(torch.full((4, 1, 70001), 1e7, device="cuda")) <= 1.1e-6
