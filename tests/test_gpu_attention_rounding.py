@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from linear_attention_decode_02_gb300 import binding, build
+from tests.attention_error import assert_rms, softmax_moments
 from tests.rounding import F32, to_np
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,35 @@ def test_float32_keys_near_the_largest_float(Hq):
     torch.cuda.synchronize()
     # exact product (a power of two), the two constants and products of the test above: 4 half steps bound them
     assert np.abs(to_np(lse) / (to_np(key)[:, None] * 2.0 ** -126) - 1.0).max() <= 4.01 * F32
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 32, 8), (128, 32, 8), (256, 16, 4), (64, 24, 2), (128, 24, 2), (256, 24, 2)])
+@pytest.mark.parametrize("length,window", [(1000, 0), (70001, 0), (70001, 5000)])
+def test_outputs_are_off_by_their_rounding_alone(dtype, D, Hq, Hkv, length, window):
+    # six sequences that share their pages, of slightly different lengths
+    N, page = 6, 64
+    P = -(-length // page)
+    g = torch.Generator(device="cuda").manual_seed(D + Hq + length)
+    k, v = (torch.randn(P + 1, page, Hkv, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(N, Hq, D, device="cuda", generator=g).to(dtype)
+    table = (torch.randperm(P, device="cuda", generator=g) + 1).to(torch.int32).expand(N, P).contiguous()
+    lens = [length - 13 * n for n in range(N)]
+    out, lse = binding.kda_paged_attention_decode(q, k, v, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                                  window=window, return_lse=True)
+    keys, values = (to_np(x[table[0].long()].flatten(0, 1).transpose(0, 1)) for x in (k, v))
+    G, scale = Hq // Hkv, D ** -0.5
+    queries = to_np(q)
+    ref, ref_lse = np.zeros((N, Hq, D)), np.zeros((N, Hq))
+    weighted, spread = np.zeros((N, Hq, D)), np.zeros((N, Hq, D))
+    for h in range(Hkv):
+        for n in range(N):
+            first = max(0, lens[n] - window) if window else 0
+            heads = slice(h * G, (h + 1) * G)
+            ref[n, heads], ref_lse[n, heads], weighted[n, heads], spread[n, heads] = softmax_moments(
+                queries[n, heads], keys[h, first:lens[n]], values[h, first:lens[n]], scale)
+    # 64 roundings in a score's product; weights in two bfloat16 (2^-16), or in float32's two parts (2^-20)
+    score = 64 * F32 * np.linalg.norm(queries, axis=-1).max() * np.linalg.norm(keys, axis=-1).max() * scale
+    assert_rms(to_np(out), ref, weighted, spread, score, 2.0 ** -16 if dtype is BF16 else 2.0 ** -20, "out")
+    # a log-sum: the scores' errors average, 2^-22 of the exponential, 512 roundings of its sums, its own 2^-24
+    assert np.abs(to_np(lse) - ref_lse).max() <= score + 2.0 ** -22 + 512 * F32 + F32 * np.abs(ref_lse).max()
