@@ -355,7 +355,7 @@ def kda_beam_select_workspace(requests, beams, vocab, num_out, dtype, sm_count):
 def kda_beam_select(logits, scores, num_out, finished=None, eos_token=0, out=None, workspace=None):
     """The num_out best continuations of each request: (scores, parents, tokens), each [N, num_out].
 
-    `out` may give the three tensors; the workspace is as in
+    `out` may give the three tensors, of num_out columns; the workspace is as in
     kda_paged_attention_decode.
     """
     r = (_module or _native()).beam(logits, scores, finished, workspace, None if out is None else tuple(out), num_out,

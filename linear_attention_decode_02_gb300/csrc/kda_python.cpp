@@ -313,6 +313,12 @@ PyObject* beam(PyObject*, PyObject* const* args, Py_ssize_t n) {
       if (!PyTuple_Check(args[4]) || PyTuple_GET_SIZE(args[4]) != 3)
         raise(PyExc_TypeError, "out must be a tuple of three tensors");
       for (int i = 0; i < 3; ++i) given[i] = PyTuple_GET_ITEM(args[4], i);
+      // The library goes by the tensors; a workspace for num_out might be too small for them, or they for num_out.
+      for (PyObject* o : given) {
+        const at::Tensor& t = tensor_of(o);
+        if (t.dim() != 2 || t.size(1) != num_out)
+          raise(PyExc_ValueError, "out must be of [N, num_out] tensors, num_out is %d", static_cast<int>(num_out));
+      }
     }
     int64_t floats = 0;  // refuses sizes before anything of them is allocated
     const kda_status sizes = lib.beam_workspace(x.size(0), static_cast<int32_t>(std::min<int64_t>(x.size(1), INT32_MAX)),

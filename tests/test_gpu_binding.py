@@ -1,0 +1,35 @@
+"""What the Python binding of the cache and beam calls refuses by itself, and what it keeps."""
+
+import pytest
+import torch
+
+from linear_attention_decode_02_gb300 import binding, build
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.library()
+
+
+def outputs(N, M):
+    return (torch.zeros(N, M, device="cuda"), *(torch.zeros(N, M, dtype=torch.int32, device="cuda") for _ in range(2)))
+
+
+@pytest.mark.parametrize("columns", [3, 5, 64])
+def test_beam_outputs_of_another_count_are_refused(columns):
+    # whatever was called before: a larger call leaves a larger workspace
+    x, s = torch.randn(2, 4, 5000, device="cuda"), torch.zeros(2, 4, device="cuda")
+    for before in (4, 64):
+        binding.kda_beam_select(x, s, before)
+        out = outputs(2, columns)
+        with pytest.raises(ValueError, match="num_out is 4"):
+            binding.kda_beam_select(x, s, 4, out=out)
+        assert all(torch.count_nonzero(t) == 0 for t in out)
+    with pytest.raises(ValueError, match="num_out is 4"):
+        binding.kda_beam_select(x, s, 4, out=tuple(t.flatten() for t in outputs(2, 4)))
+    got = binding.kda_beam_select(x, s, 4, out=outputs(2, 4))
+    assert all(torch.equal(a, b) for a, b in zip(got, binding.kda_beam_select(x, s, 4)))
