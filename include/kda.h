@@ -324,7 +324,7 @@ kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, dou
  *               stream may share one, concurrent calls may not.
  *   window      0: every position; w > 0: only the last w positions, t >=
  *               seq_lens[n] - w.
- *   scale       > 0, normally 1/sqrt(D).
+ *   scale       > 0 and at most 2.3e38, normally 1/sqrt(D).
  *   out         [N, Hq, D] bfloat16 contiguous (written).
  *   lse         [N, Hq] float32 contiguous (written), or NULL: the natural
  *               logarithm of the sum of exp(scale q.k) over the row's positions.

@@ -374,7 +374,8 @@ kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_p
   KDA_TRY(need_contiguous(W));
   KDA_CHECK(reinterpret_cast<uintptr_t>(W.data) % 16 == 0, KDA_ERR_INVALID_ARG, "workspace: data must be 16-byte aligned");
   KDA_CHECK(window >= 0, KDA_ERR_INVALID_ARG, "window must not be negative (0: all positions)");
-  KDA_CHECK(std::isfinite(scale) && scale > 0.f, KDA_ERR_INVALID_ARG, "scale must be finite and positive");
+  const float scale_log2 = scale * 1.4426950408889634f;  // scores are taken in units of log 2
+  KDA_CHECK(scale > 0.f && std::isfinite(scale_log2), KDA_ERR_INVALID_ARG, "scale must be positive and at most 2.3e38");
   KDA_TRY(no_shared_bytes(O, {&Q, &KP, &VP, &T, &L, &W, &E}));
   KDA_TRY(no_shared_bytes(W, {&Q, &KP, &VP, &T, &L, &E}));
   KDA_TRY(no_shared_bytes(E, {&Q, &KP, &VP, &T, &L}));
@@ -397,7 +398,7 @@ kda_status kda_paged_attention_decode(const kda_tensor* q, const kda_tensor* k_p
   a.work = reinterpret_cast<float*>(W.data);
   a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.dtype = KP.dtype;
   a.window = window;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.vec16 = vectors_aligned(Q, 16) && vectors_aligned(KP, 16) && vectors_aligned(VP, 16);
   return check_launch(kda::launch_paged_attention(a, dev.sms, st));
 }
