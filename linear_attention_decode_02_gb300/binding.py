@@ -15,12 +15,23 @@ import ctypes
 import importlib.util
 import math
 import os
+import platform
+import sys
 import threading
 
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
-_MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kda_python.so")
+
+
+def module_path(torch_version):
+    """The CPython module for this interpreter, machine and PyTorch, whose binary interfaces it is compiled to: one
+    built for others has another name, and is neither taken for up to date nor loaded."""
+    tag = f"{sys.implementation.cache_tag}-{platform.machine()}-torch-{torch_version}"
+    return os.path.join(os.path.dirname(os.path.abspath(__file__)), f"_kda_python.{tag}.so")
+
+
+_MODULE_PATH = module_path(torch.__version__)
 _lock = threading.Lock()
 _lib = None
 
@@ -283,7 +294,7 @@ def _native():
         with _lock:
             if _module is None:
                 if not os.path.exists(_MODULE_PATH):
-                    raise RuntimeError(f"_kda_python.so is not built ({_MODULE_PATH}); run "
+                    raise RuntimeError(f"the marshalling module is not built ({_MODULE_PATH}); run "
                                        "`python -m linear_attention_decode_02_gb300.build`")
                 spec = importlib.util.spec_from_file_location("_kda_python", _MODULE_PATH)
                 m = importlib.util.module_from_spec(spec)

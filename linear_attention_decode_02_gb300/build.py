@@ -12,12 +12,15 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
-import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+
+import torch
+
+from .binding import module_path
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 PYSRC = os.path.join(CSRC, "kda_python.cpp")
-PYLIB = os.path.join(PKG, "_kda_python.so")
+PYLIB = module_path(torch.__version__)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
               "-I", os.path.join(ROOT, "include")]
@@ -72,12 +75,12 @@ def _python_module():
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         raise RuntimeError("no C++ compiler found for the binding's CPython module")
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     tmp = PYLIB + ".tmp"
     cmd = [cxx, "-std=c++17", "-O2", "-Wall", "-Wno-unknown-pragmas", "-fPIC", "-shared",
-           "-isystem", os.path.join(torch, "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
-           PYSRC, "-o", tmp, "-L", os.path.join(torch, "lib"), "-Wl,--no-as-needed", "-ltorch_python", "-ltorch_cuda",
+           "-isystem", os.path.join(home, "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           PYSRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-Wl,--no-as-needed", "-ltorch_python", "-ltorch_cuda",
            "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
