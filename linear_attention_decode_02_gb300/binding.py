@@ -344,8 +344,8 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
                                return_lse=False, workspace=None):
     """One new token per sequence over its pages; returns bf16 out [N, Hq, D], or (out, lse) with return_lse.
 
-    Without `workspace` the binding keeps one for each thread and stream, and
-    takes one from the graph's pool for a captured call.
+    Without `workspace` the binding keeps one of up to 16 MB for each thread and
+    stream, and takes one from the graph's pool for a captured call.
     """
     r = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, return_lse,
                                          window, scale)

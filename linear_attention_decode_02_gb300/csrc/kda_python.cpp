@@ -172,13 +172,16 @@ kda_status without_gil(const F& f) {
 // thread (in its thread state's dictionary), device and stream: calls of one
 // thread on one stream follow one another, and no other call sees it.  A call
 // that is being captured gets its own from the graph's pool, so graphs share
-// theirs neither with each other nor with eager calls.
+// theirs neither with each other nor with eager calls.  One of more than 16 MB
+// (attention's never is, beams' only over tens of thousands of rows, whose call
+// takes far longer than allocating it) goes back to the allocator with the call.
 constexpr Py_ssize_t kKept = 16;
+constexpr int64_t kKeptFloats = 4 << 20;
 PyObject* s_workspaces;
 
 at::Tensor workspace(const Call& call, PyObject* given, int64_t floats) {
   if (given != Py_None) return tensor_of(given);
-  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+  if (floats > kKeptFloats || c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return call.empty({floats}, at::kFloat);
   PyObject* state = PyThreadState_GetDict();  // borrowed
   if (state == nullptr) return call.empty({floats}, at::kFloat);
