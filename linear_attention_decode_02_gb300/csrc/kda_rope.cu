@@ -4,9 +4,11 @@
 // Pair i of a head turns by the angle 2 pi pos s_i, with s_i turns per
 // position held as a 64-bit binary fraction.  The product pos * s_i modulo
 // 2^64 is exact in integers, so a far position loses no more of the angle
-// than position 1 does (a float32 product would lose 0.06 rad at 10^6); its
-// top 32 bits, taken as a signed fraction of a turn, go to sincospif.  The
-// rotation is float32 and each output is rounded once.
+// than position 1 does (a float32 product would lose 0.06 rad at 10^6).  Of its
+// top 32 bits the nearest quarter turn is taken off as an integer and the rest, at
+// most an eighth of a turn, goes to sincospif as a float32, whose rounding is then
+// within pi 2^-27 of the angle (pi 2^-25 for a half turn, more than a float32 cosine's
+// own).  The rotation is float32 and each output is rounded once.
 //
 // Bound by memory: every input is read once and every output written once.
 // A block takes ROWS token rows, or where they are few a part of their heads.
@@ -154,8 +156,15 @@ __global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __gr
     const int r = i / (a.rot / 2), pair = i - r * (a.rot / 2);
     const uint64_t phase = (uint64_t)(uint32_t)max(s_pos[r], 0) * __ldg(a.steps + pair);
     float sn, cs;
-    sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
-    s_cs[r][(pair % PAIRS) * pair_tasks + pair / PAIRS] = make_float2(cs * a.amplitude, sn * a.amplitude);
+    const uint32_t turn = (uint32_t)((phase + 0x80000000u) >> 32), quarter = (turn + 0x20000000u) >> 30;
+    sincospif((float)(int32_t)(turn - (quarter << 30)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
+    if (quarter & 1) {
+      const float x = cs;
+      cs = -sn;
+      sn = x;
+    }
+    const float amplitude = quarter & 2 ? -a.amplitude : a.amplitude;
+    s_cs[r][(pair % PAIRS) * pair_tasks + pair / PAIRS] = make_float2(cs * amplitude, sn * amplitude);
   }
   __syncthreads();
 
