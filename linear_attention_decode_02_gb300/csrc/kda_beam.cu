@@ -229,10 +229,15 @@ struct Raw<__nv_bfloat16> {
 // boundaries: neighbouring elements in one load.  Others: elements kThreads apart,
 // loaded one by one, so that which of them a thread adds, and in what order, does
 // not depend on where a row starts: equal rows have equal log-sums, and tie.
-// (16-byte loads from each row's own boundary on, which group by address, are
-// faster for bfloat16: 32 x 8 rows of 131071 23.6 us instead of 26.4, 16 x 8 of 50257
-// 11.4 and 13.0; float32 12 x 6 of 50257 12.5 and 12.3.)  Elements past the row are
-// -infinity.
+// Elements past the row are -infinity.
+//
+// Measured, kernels alone, against 16-byte loads from each row's own boundary on,
+// whose sums depend on it: bfloat16 32 x 8 rows of 131071 27.0 and 23.7 us, 64 x 4 of
+// 50257 17.0 and 14.6, 16 x 8 of 50257 13.1 and 12.0, 4 x 16 15.7 and 16.5; float32
+// 12 x 6 of 50257 12.8 and 12.4.  Others that do not depend on it: pairs of bfloat16
+// in one load where a row allows it 27.9, 18.0 and 14.5 us for the first three;
+// vectors put together from two lanes' 16 bytes 28.2 and 15.5 for the first and third;
+// four vectors instead of two on their way, at three blocks a SM, 27.1, 20.2 and 12.7.
 template <typename T, bool ALIGNED>
 struct Ahead;
 template <typename T>
@@ -339,15 +344,6 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) x[j].load(row, place_of(batch, j, tid), a.V);
   };
-  // VEC elements that follow one another, whatever their alignment.
-  const auto load_run = [&](int i, Raw<T>& v) {
-    if (ALIGNED && i + VEC <= a.V) {
-      v.load(row + i);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v.set(e, i + e < a.V ? row + i + e : nullptr);
-    }
-  };
   pdl_wait();
   pdl_launch_dependents();
   Raw<T> x[LOADS];
@@ -416,12 +412,14 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     const float down = __int_as_float((shift + 127) << 23);
     hi = sum * down;
     lo = rest * down;
-  } else {
-    // Logits of 10^6 and more (or none above -inf, or infinite): once more, by their distance from the largest.
-    const float base = all > -INFINITY ? all : 0.f, c = all > -INFINITY ? far_fraction(base) : 0.f;
+  } else if (all > -INFINITY) {
+    // Logits of 10^6 and more: once more, by their distance from the largest.
+    const float c = far_fraction(all);
     hi = 0.f;
     for (int i = first + tid; i < end; i += kThreads)
-      add_carried(hi, lo, ex2(fmaf(static_cast<float>(row[i]) - base, kLog2e, c)), 0.f);
+      add_carried(hi, lo, ex2(fmaf(static_cast<float>(row[i]) - all, kLog2e, c)), 0.f);
+  } else {
+    hi = sum;  // nothing above -infinity: 0, or NaN
   }
   s_hi[tid] = hi;
   s_lo[tid] = lo;
@@ -460,21 +458,32 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     return;
   }
   // Too many at the bound.  On masked or constant logits they equal it; of
-  // those only the first in the row matter.  The larger ones are counted again.
+  // those only the first in the row matter.  The larger ones are counted again,
+  // in the row's own order: 16 bytes at a time from the boundary before the piece,
+  // what is not the piece's left out.
+  const int from = first - (int)((reinterpret_cast<uintptr_t>(row + first) & 15) / sizeof(T));
+  const auto load_run = [&](int i, Raw<T>& v) {
+    if (i >= first && i + VEC <= end) {
+      v.load(row + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v.set(e, i + e >= first && i + e < end ? row + i + e : nullptr);
+    }
+  };
   __syncthreads();
   if (tid == 0) s_count = 0;
   __syncthreads();
-  const int vectors = (end - first + VEC - 1) / VEC;
+  const int vectors = (end - from + VEC - 1) / VEC;
   for (int h = tid; h < vectors; h += kThreads) {
     Raw<T> v;
-    load_run(first + h * VEC, v);
+    load_run(from + h * VEC, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float2 p = v.pair(e / 2);
       const float w = e % 2 == 0 ? p.x : p.y;
       if (w > bound) {
         const int at = atomicAdd(&s_count, 1);
-        if (at < kList) s_list[at] = candidate(w, first + h * VEC + e);
+        if (at < kList) s_list[at] = candidate(w, from + h * VEC + e);
       }
     }
   }
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
     int next = larger;  // place of the next equal one
     for (int h0 = 0; h0 < vectors && next < a.M && bound > -INFINITY; h0 += kThreads) {
       Raw<T> v;
-      load_run(first + (h0 + tid) * VEC, v);
+      load_run(from + (h0 + tid) * VEC, v);
       int equal = 0;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_scan_kernel(const BeamAr
         next += s_key[w];
       }
       for (int left = equal; left != 0 && at < a.M; left &= left - 1, ++at)
-        best[at] = candidate(bound, first + (h0 + tid) * VEC + __ffs(left) - 1);
+        best[at] = candidate(bound, from + (h0 + tid) * VEC + __ffs(left) - 1);
     }
     for (int i = next + tid; i < a.M; i += kThreads) best[i] = 0;
     return;
