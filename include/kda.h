@@ -316,8 +316,9 @@ kda_status kda_rope_phase_steps(int32_t rot_dim, double base, double factor, dou
  *               head strides that keep 4-element alignment.
  *   k_pages, v_pages, page_table: as above, of q's dtype; Hq a multiple of Hkv,
  *               query head h reads key head h / (Hq / Hkv).
- *   seq_lens    [N] int32, the new token included; clamped to the table's
- *               P * page_size positions, at most 2^30.
+ *   seq_lens    [N] int32, the new token included.  Positions past the table's
+ *               P * page_size, at most 2^30, are not there to be attended to; a
+ *               window counts from seq_lens[n] all the same.
  *   workspace   float32, contiguous, at least the floats that
  *               kda_paged_attention_workspace names for the device's SM count;
  *               its contents matter only during the call, so calls on one
@@ -381,7 +382,8 @@ kda_status kda_beam_select_workspace(int64_t requests, int32_t beams, int64_t vo
  * clears and, by parent beam, reorders recurrent states, conv caches and
  * pages alike.
  *
- *   pools       n_pools (1..256) descriptors, rank 1..4, any dtype: axis 0 is
+ *   pools       n_pools (1..256) descriptors, rank 1..4, of any kda_dtype (bytes
+ *               are copied, so other types move as views of one): axis 0 is
  *               the slot (the same number of slots in every pool), the other
  *               axes dense in any order (a conv cache's [slot_stride, 1, 3*H*128]
  *               and a head-major page are), slot stride as large or larger.

@@ -475,8 +475,8 @@ cudaError_t launch_join(const AttendArgs& a, const AttendPlan& p, cudaStream_t s
 // positions that the call may attend to, over sequences and key heads, are 256 a
 // channel or more.  The host knows only how many the table or the window allows;
 // short sequences in a roomy table are slower for it, by 2 us at 64 and 128
-// channels, 8 us at 256.  Measured in matrix instructions (a form 5 to 9 % slower
-// than the one there now) and on CUDA cores, us:
+// channels, 8 us at 256.  Measured in matrix instructions (a form up to 10 %
+// slower than the one there now) and on CUDA cores, us:
 //   64 channels   12 heads, 8000 positions 10 and 11, 32000 17 and 23, 1.2 million 112 and 226; 8 heads 97 and 118
 //   128 channels  12 heads, 8000 13 and 13, 16000 18 and 17, 32000 21 and 22, 0.6 million 102 and 165; 8 heads 78 and 85
 //   256 channels  12 heads, 16000 28 and 21, 64000 57 and 58, 0.3 million 167 and 193; 16 heads 175 and 272

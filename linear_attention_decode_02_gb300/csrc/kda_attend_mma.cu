@@ -15,7 +15,7 @@
 // 8192 positions, 1.27 GB, 189 to 199 us; 2 of up to 131072, 1.0 GB, 150 to 156
 // us: 95 to 100 % of the copy bandwidth.  0.4 GB of 256-channel heads 85 us (73 %),
 // of 64-channel ones 75 us (79 %), of 128-channel ones 70 us (85 %), with 12 query
-// heads a key head 75 us (77 %).  One sequence of 1000 positions 9 us with the
+// heads a key head 75 us (77 %).  One sequence of 1000 positions 9 to 11 us with the
 // join: two launches and four dependent loads (length, page, keys, partials).
 //
 // Every warp with a piece of its own, instead of four that share a tile: 64
@@ -29,9 +29,11 @@
 // whose 16-byte chunks are XORed with the row so that no two banks meet.
 //
 // The weights p enter the second product as two bfloat16 pieces, p = hi + lo
-// to 2^-17 (hi alone would put 2^-9 of rounding into the output, as much as
+// to 2^-17 (hi alone would put 2^-8 of rounding into the output, as much as
 // its own type has).  With up to 8 heads hi takes rows 0..7 and lo rows 8..15,
-// which would be empty, at no cost; with 16 heads lo is a second product.
+// which would be empty, at no cost; with 16 heads lo is a second product.  A third
+// piece left the outputs as far from 64 bits and from a float32 computation as they
+// are, and took 256 channels from 150 to 168 us, 12 heads from 46 to 48.
 #include "kda_attend_rows.cuh"
 
 namespace kda {

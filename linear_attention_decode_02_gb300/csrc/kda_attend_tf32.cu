@@ -17,10 +17,10 @@
 // makes its row non-finite either way.
 //
 // Bound by the latency of each warp's steps: 0.37 GB of 12 / 1 heads of 128 take
-// 96 us, 58 % of the copy bandwidth (CUDA cores 165), of 64 106 (226), 32 / 2 heads of
-// 256 159 (272).  With parts rounded by conversion instructions, which took 102,
-// 112 and 175 us, the issue slots were 37 % used, the tensor pipe 29 % and shared
-// memory 45 %, with two warps a scheduler and all registers taken.  Sums kept
+// 99 us, 57 % of the copy bandwidth (CUDA cores 165), of 64 111 (226), 32 / 2 heads of
+// 256 154 (272); keys cut instead of rounded took 98, 110 and 151.  The issue slots
+// are 31 % used, the tensor pipe 30 % and shared memory 46 %, with two warps a
+// scheduler and all registers taken.  Sums kept
 // apart for every kind of product, four outputs in turn, a rolled first product
 // and queries laid out without bank conflicts changed that by 2 % or made it
 // slower.
