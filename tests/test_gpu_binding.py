@@ -1,5 +1,7 @@
 """What the Python binding of the cache and beam calls refuses by itself, and what it keeps."""
 
+import gc
+
 import pytest
 import torch
 
@@ -43,6 +45,7 @@ def test_large_workspaces_are_not_kept():
     assert binding.kda_paged_attention_workspace(4096, 1, 256, BF16, sms) <= 4 << 20
     small = binding.kda_beam_select(x[:2], s[:2], 64)
     torch.cuda.synchronize()
+    gc.collect()  # nothing of another test's goes meanwhile
     before = torch.cuda.memory_allocated()
     first = binding.kda_beam_select(x, s, 64)
     again = binding.kda_beam_select(x, s, 64)
