@@ -1,0 +1,116 @@
+// Contract checks shared by the entry points over the paged cache: views that
+// interleave, element alignment, page and table shapes.  Host only.
+#pragma once
+
+#include "kda_cache.h"
+#include "kda_host.h"
+
+namespace kda {
+namespace host {
+
+// No byte is shared although the byte ranges cross: views that interleave
+// along one axis, as keys and values of one allocation do.  For a stride s of
+// `a` with every larger stride of both views a multiple of s, addresses modulo
+// s lie in [0, ea) and [r, r + eb), ea and eb the extents below that axis and
+// r the offset modulo s, which are disjoint where ea <= r and r + eb <= s.
+inline bool interleaved(const View& a, const View& b) {
+  const int64_t ba = esize(a.dtype), bb = esize(b.dtype);
+  for (int i = 0; i < a.ndim; ++i) {
+    if (a.shape[i] <= 1) continue;
+    const int64_t s = a.stride[i] * ba;
+    int64_t ext[2] = {0, 0};
+    bool nested = true;
+    for (int w = 0; w < 2; ++w) {
+      const View& v = w == 0 ? a : b;
+      const int64_t es = w == 0 ? ba : bb;
+      ext[w] = es;
+      for (int j = 0; j < v.ndim; ++j) {
+        if (v.shape[j] <= 1) continue;
+        const int64_t st = v.stride[j] * es;
+        if (st < s) ext[w] += (v.shape[j] - 1) * st;
+        else if (st % s != 0) nested = false;
+      }
+    }
+    if (!nested) continue;
+    const int64_t d = b.data - a.data;
+    const int64_t r = ((d % s) + s) % s;
+    if (ext[0] <= r && r + ext[1] <= s) return true;
+  }
+  return false;
+}
+
+inline kda_status no_shared_bytes(const View& w, std::initializer_list<const View*> others) {
+  for (const View* o : others)
+    KDA_CHECK(!overlap(w, *o) || interleaved(w, *o) || interleaved(*o, w), KDA_ERR_ALIAS, "%s overlaps %s", w.name,
+              o->name);
+  return KDA_OK;
+}
+
+inline bool same_view(const View& a, const View& b) {
+  if (a.data != b.data || a.dtype != b.dtype || a.ndim != b.ndim) return false;
+  for (int i = 0; i < a.ndim; ++i)
+    if (a.shape[i] != b.shape[i] || (a.shape[i] > 1 && a.stride[i] != b.stride[i])) return false;
+  return true;
+}
+
+// Every vector of the last axis starts on a `bytes` boundary.
+inline bool vectors_aligned(const View& v, int64_t bytes) {
+  if (reinterpret_cast<uintptr_t>(v.data) % bytes != 0) return false;
+  for (int i = 0; i < v.ndim - 1; ++i)
+    if (v.shape[i] > 1 && (v.stride[i] * esize(v.dtype)) % bytes != 0) return false;
+  return true;
+}
+
+// No two elements of a view that is written share an address: every stride
+// spans the axes of smaller strides.
+inline kda_status need_distinct(const View& v) {
+  for (int i = 0; i < v.ndim; ++i) {
+    if (v.shape[i] <= 1) continue;
+    int64_t inner = 1;
+    for (int j = 0; j < v.ndim; ++j)
+      if (j != i && v.shape[j] > 1 && (v.stride[j] < v.stride[i] || (v.stride[j] == v.stride[i] && j < i)))
+        inner += (v.shape[j] - 1) * v.stride[j];
+    KDA_CHECK(v.stride[i] >= inner, KDA_ERR_INVALID_ARG, "%s: elements overlap along axis %d", v.name, i);
+  }
+  return KDA_OK;
+}
+
+// Key and value pages [num_pages, page_size, Hkv, D] of one dtype and shape.
+inline kda_status need_pages(const View& K, const View& V, int64_t Hkv, int64_t D) {
+  KDA_TRY(need_dtype(K, KDA_F32, KDA_BF16));
+  KDA_CHECK(V.dtype == K.dtype, KDA_ERR_INVALID_ARG, "v_pages: dtype must match k_pages");
+  for (const View* p : {&K, &V}) {
+    KDA_CHECK(p->shape[0] >= 1 && p->shape[0] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: num_pages %lld out of range",
+              p->name, (long long)p->shape[0]);
+    KDA_CHECK(p->shape[1] >= 1 && p->shape[1] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: page size %lld out of range",
+              p->name, (long long)p->shape[1]);
+    KDA_TRY(need_shape(*p, 0, K.shape[0]));
+    KDA_TRY(need_shape(*p, 1, K.shape[1]));
+    KDA_TRY(need_shape(*p, 2, Hkv));
+    KDA_TRY(need_shape(*p, 3, D));
+    KDA_TRY(need_vec_layout(*p));
+  }
+  return KDA_OK;
+}
+
+inline kda_status need_table(const View& T, int64_t N) {
+  KDA_TRY(need_dtype(T, KDA_I32));
+  KDA_TRY(need_shape(T, 0, N));
+  KDA_CHECK(T.shape[1] <= INT32_MAX, KDA_ERR_INVALID_ARG, "%s: too many pages a sequence", T.name);
+  KDA_CHECK(T.shape[1] <= 1 || T.stride[1] == 1, KDA_ERR_INVALID_ARG, "%s: column stride must be 1", T.name);
+  return KDA_OK;
+}
+
+inline kda_status check_attention_heads(int64_t Hq, int64_t Hkv, int64_t D) {
+  KDA_CHECK(Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0, KDA_ERR_INVALID_ARG,
+            "%lld query heads cannot share %lld key heads evenly", (long long)Hq, (long long)Hkv);
+  KDA_CHECK(Hq <= 4096, KDA_ERR_UNSUPPORTED, "%lld query heads, at most 4096", (long long)Hq);
+  KDA_CHECK(D == 64 || D == 128 || D == 256, KDA_ERR_UNSUPPORTED, "head dimension %lld: 64, 128 and 256 are served",
+            (long long)D);
+  return KDA_OK;
+}
+
+inline kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
+
+}  // namespace host
+}  // namespace kda
