@@ -402,6 +402,70 @@ kda_status kda_beam_select_workspace(int64_t requests, int32_t beams, int64_t vo
 kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const kda_tensor* src_slots,
                          const kda_tensor* dst_slots, const kda_tensor* parents, void* stream);
 
+/*
+ * kda_page_assign: pages for the sequences of a step.  Grows and shrinks the
+ * sequences' rows of the page table to new lengths, from and into a ring of free
+ * pages, and names the slot of every new token row.
+ *
+ *   seq_lens    [N] int32, positions each sequence holds; its row of the table
+ *               lists their ceil(seq_lens / page_size) pages.  N <= 8192.
+ *   new_lens    [N] int32, positions it shall hold.  Below zero counts as zero.
+ *   shared_lens [N] int32 or NULL: the first shared_lens[n] / page_size (rounded
+ *               down) pages of a row are not its own and are never given back.
+ *   page_table  [N, P] int32, column stride 1 (written).
+ *   free_pages  [C] int32 contiguous (written), a ring that can hold every page:
+ *               pages are 1 .. C, (C + 1) * page_size < 2^31.
+ *   free_state  [2] int32: the place of the oldest free page, 0 .. C - 1, and how
+ *               many are free.  (Others count as an empty ring.)
+ *   lens_out    [N] int32 (written): the lengths after the call; may be seq_lens or
+ *               new_lens itself.
+ *   state_out   [2] int32 (written): free_state after the call; may be it itself.
+ *   cu_seqlens  [N+1] int32 (written): first new token row of each sequence, as
+ *               kda_rope_append takes it.
+ *   slots       [R] int32 contiguous (written): page * page_size + place of each
+ *               new row's position, as kda_rope_axes_append takes it; -1 for rows
+ *               past cu_seqlens[N] and where the table lists no page 1 .. C.
+ * A sequence that needs no further page gets its new length; one that does gets it
+ * where the pages that it and all sequences before it ask for are free, and else
+ * keeps the old one, as does one whose new length the table cannot hold (which
+ * counts as asking for none).  Pages are taken in order of sequences, the oldest
+ * free one first; those past a shorter length are given back behind the youngest,
+ * in order of sequences and columns, and can be taken from the next call on.
+ * Entries outside 1 .. C (pages that a window has left behind) are not given back.
+ * Entries past a row's pages mean nothing and are left as they are.  That a
+ * live page is in one place, one row's own part or the ring, is a caller contract.
+ */
+kda_status kda_page_assign(const kda_tensor* seq_lens, const kda_tensor* new_lens, const kda_tensor* shared_lens,
+                           const kda_tensor* page_table, const kda_tensor* free_pages, const kda_tensor* free_state,
+                           int32_t page_size, const kda_tensor* lens_out, const kda_tensor* state_out,
+                           const kda_tensor* cu_seqlens, const kda_tensor* slots, void* stream);
+
+/*
+ * kda_rope_axes_append: kda_rope_append for tokens with a position on each of
+ * several axes (time, height and width of pictures and clips), written to slots.
+ *
+ *   q, k, v, phase_steps, k_pages, v_pages, q_out, interleaved, amplitude: as there.
+ *   pair_axes   [rot/2] int32 contiguous: the axis whose position turns each pair
+ *               (kda_rope_pair_axes); one outside 0 .. A - 1 turns it not at all.
+ *   positions   [R, A] int32, any positive strides, A <= 4; negative ones turn
+ *               backwards.
+ *   slots       [R] int32 contiguous: page * page_size + place of each row's key
+ *               and value.  A slot of page 0 or below and one past the last page are
+ *               null: the row's q_out is zero and nothing is written.  Live slots
+ *               must be unique.
+ */
+kda_status kda_rope_axes_append(const kda_tensor* q, const kda_tensor* k, const kda_tensor* v,
+                                const kda_tensor* phase_steps, const kda_tensor* pair_axes, const kda_tensor* positions,
+                                const kda_tensor* slots, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                const kda_tensor* q_out, int32_t interleaved, float amplitude, void* stream);
+
+/*
+ * The axis of every pair for kda_rope_axes_append, on the host: sections[a] pairs
+ * of axis a.  cyclic = 0: one section after another; 1: the axes in turn, each
+ * until its section is used up.  Writes the sum of the sections, at most 256.
+ */
+kda_status kda_rope_pair_axes(const int32_t* sections, int32_t num_axes, int32_t cyclic, int32_t* pair_axes);
+
 /* ---- host-only queries (no CUDA calls) ---------------------------------- */
 
 /* Operation ids for kda_plan_split. */

@@ -50,6 +50,7 @@ EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda
            "kda_rope_append", "kda_rope_phase_steps", "kda_pool_move",
            "kda_paged_attention_decode", "kda_paged_attention_workspace",
            "kda_beam_select", "kda_beam_select_workspace",
+           "kda_page_assign", "kda_rope_axes_append", "kda_rope_pair_axes",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -86,6 +87,9 @@ def _declare(lib):
         "kda_beam_select_workspace": [ctypes.c_int64, i32, ctypes.c_int64, i32, i32, i32, vp],
         "kda_pool_move": [ctypes.POINTER(T), i32, T, T, T, vp],
         "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
+        "kda_page_assign": [T, T, T, T, T, T, i32, T, T, T, T, vp],
+        "kda_rope_axes_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
+        "kda_rope_pair_axes": [ctypes.POINTER(i32), i32, i32, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -302,7 +306,8 @@ def _native():
                 m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                          for f in (lib.kda_rope_append, lib.kda_paged_attention_decode,
                                    lib.kda_paged_attention_workspace, lib.kda_beam_select,
-                                   lib.kda_beam_select_workspace, lib.kda_pool_move)))
+                                   lib.kda_beam_select_workspace, lib.kda_pool_move, lib.kda_page_assign,
+                                   lib.kda_rope_axes_append)))
                 _module = m
     return _module
 
@@ -329,6 +334,41 @@ def kda_rope_phase_steps(rot_dim, base=10000.0, factor=1.0, original_len=0.0, lo
                                   float(high), steps.data_ptr() or None)
     _check(lib, st)
     return steps.to(device)
+
+
+def kda_rope_axes_append(q, k, v, phase_steps, pair_axes, positions, slots, k_pages, v_pages, interleaved=False,
+                         amplitude=1.0, q_out=None):
+    """Rotates q and k by positions [R, A] on several axes, writes k and v to their slots in the pages, returns the
+    rotated q in the pages' dtype."""
+    r = (_module or _native()).rope_axes_append(q, k, v, phase_steps, pair_axes, positions, slots, k_pages, v_pages,
+                                                q_out, interleaved, amplitude)
+    if type(r) is int:
+        _raise(r)
+    return r
+
+
+def kda_rope_pair_axes(sections, cyclic=False, device="cuda"):
+    """The axis of every pair for kda_rope_axes_append, from the pairs of each axis, as an int32 tensor on `device`."""
+    lib = library()
+    sections = [min(max(int(n), -1), 257) for n in sections]  # what lies outside is refused all the same
+    out = torch.empty(min(max(sum(sections), 0), 256), dtype=torch.int32)
+    _check(lib, lib.kda_rope_pair_axes((ctypes.c_int32 * len(sections))(*sections), len(sections), int(bool(cyclic)),
+                                       out.data_ptr() or None))
+    return out.to(device)
+
+
+def kda_page_assign(seq_lens, new_lens, page_table, free_pages, free_state, page_size, rows, shared_lens=None,
+                    lens_out=None, state_out=None, cu_seqlens=None, slots=None):
+    """Grows and shrinks the rows of `page_table` to new lengths; returns (lens, free state, cu_seqlens, slots [rows]).
+
+    The table and the ring of free pages are updated in place; the lengths and the ring's state too where
+    lens_out=seq_lens and state_out=free_state.
+    """
+    r = (_module or _native()).page_assign(seq_lens, new_lens, shared_lens, page_table, free_pages, free_state,
+                                           page_size, rows, lens_out, state_out, cu_seqlens, slots)
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def kda_paged_attention_workspace(q_heads, kv_heads, head_dim, dtype, sm_count):

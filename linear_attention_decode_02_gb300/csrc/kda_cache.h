@@ -31,7 +31,14 @@ struct RopeArgs {
   int32_t in_dtype, page_dtype;
   int32_t vec;                 // elements per access: 8 (bf16 -> bf16, 16-byte aligned rows) or 4
   int32_t sms;                 // SMs of the device
+  // Rows with a position on each of several axes and a slot each; cu, lens and table are not used then.
+  const int32_t* positions;    // [R, num_axes], or null
+  int64_t p_rs, p_as;
+  const int32_t* slots;        // [R]: page * page_size + place
+  const int32_t* pair_axes;    // [rot/2]
+  int32_t num_axes;
 };
+constexpr int kRopeAxes = 4;   // most axes
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
 
@@ -54,6 +61,21 @@ struct MoveArgs {
 // Sets the pools' first blocks and launches; the block count must stay below 2^31 (false: it does not).
 bool plan_pool_move(MoveArgs& a, int64_t* blocks);
 cudaError_t launch_pool_move(const MoveArgs& a, int64_t blocks, cudaStream_t s);
+
+// Pages of a step's sequences.
+constexpr int kPageSequences = 8192;  // most sequences of a call
+struct PagesArgs {
+  const int32_t* old_lens; const int32_t* new_lens;  // [N]
+  const int32_t* shared_lens;                        // [N], or null
+  int32_t* table; int64_t table_rs; int32_t table_cols;
+  int32_t* ring; int32_t capacity;                   // free pages
+  const int32_t* state;                              // {head, count}
+  int32_t* lens_out; int32_t* state_out;             // may be old_lens or new_lens, and state
+  int32_t* cu; int32_t* slots;                       // [N + 1], [R]
+  int32_t N, page_size;
+  int64_t R;
+};
+cudaError_t launch_page_assign(const PagesArgs& a, cudaStream_t s);
 
 // Attention of one new token per sequence over paged keys and values.
 struct AttendArgs {

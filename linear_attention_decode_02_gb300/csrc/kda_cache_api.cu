@@ -67,28 +67,9 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
   KDA_TRY(ranked_view(v_pages, "v_pages", 4, -1, &VP));
   KDA_TRY(ranked_view(q_out, "q_out", 3, -1, &O));
 
-  const int64_t R = Q.shape[0], Hq = Q.shape[1], D = Q.shape[2], Hkv = K.shape[1];
-  KDA_TRY(need_dtype(Q, KDA_F32, KDA_BF16));
-  KDA_CHECK(R <= INT32_MAX, KDA_ERR_INVALID_ARG, "q: too many token rows");
-  KDA_CHECK(Hq >= 1 && Hkv >= 1, KDA_ERR_INVALID_ARG, "q, k: need at least one head");
-  KDA_CHECK((Hq + 2 * Hkv) * D <= (1 << 24), KDA_ERR_UNSUPPORTED, "q, k: too many heads");
-  KDA_CHECK(D >= 4 && D % 4 == 0 && D <= 512, KDA_ERR_UNSUPPORTED, "q: head dimension %lld must be a multiple of 4 in 4..512",
-            (long long)D);
-  for (View* t : {&K, &V}) {
-    KDA_CHECK(t->dtype == Q.dtype, KDA_ERR_INVALID_ARG, "%s: dtype must match q", t->name);
-    KDA_TRY(need_shape(*t, 0, R));
-    KDA_TRY(need_shape(*t, 1, Hkv));
-    KDA_TRY(need_shape(*t, 2, D));
-  }
-  for (View* t : {&Q, &K, &V}) KDA_TRY(need_vec_layout(*t));
-  KDA_TRY(need_dtype(P, KDA_I32));
-  KDA_TRY(need_shape(P, 1, 2));
-  KDA_TRY(need_contiguous(P));
-  const int64_t rot = 2 * P.shape[0];
-  KDA_CHECK(rot <= D && rot % 8 == 0, KDA_ERR_INVALID_ARG,
-            "phase_steps: %lld pairs; the rotated part must be a multiple of 8 and at most the head dimension",
-            (long long)P.shape[0]);
-  KDA_CHECK(reinterpret_cast<uintptr_t>(P.data) % 8 == 0, KDA_ERR_INVALID_ARG, "phase_steps: data must be 8-byte aligned");
+  kda::RopeArgs a{};
+  KDA_TRY(check_rope(Q, K, V, P, KP, VP, O, is_interleaved, amplitude, &a));
+  const int64_t R = Q.shape[0];
   KDA_CHECK(L.ndim == 1, KDA_ERR_INVALID_ARG, "seq_lens: expected rank 1");
   const int64_t N = L.shape[0];
   KDA_CHECK(N <= INT32_MAX - 1, KDA_ERR_INVALID_ARG, "seq_lens: too many sequences");
@@ -100,16 +81,6 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
               (long long)N, (long long)R);
   }
   KDA_TRY(need_table(T, N));
-  KDA_TRY(need_pages(KP, VP, Hkv, D));
-  KDA_CHECK(O.dtype == KP.dtype, KDA_ERR_INVALID_ARG, "q_out: dtype must match the pages");
-  KDA_TRY(need_shape(O, 0, R));
-  KDA_TRY(need_shape(O, 1, Hq));
-  KDA_TRY(need_shape(O, 2, D));
-  KDA_TRY(need_vec_layout(O));
-  KDA_CHECK(is_interleaved == 0 || is_interleaved == 1, KDA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  KDA_CHECK(std::isfinite(amplitude), KDA_ERR_INVALID_ARG, "amplitude must be finite");
-  for (const View* w : {&O, &KP, &VP}) KDA_TRY(need_distinct(*w));
-  if (!same_view(O, Q)) KDA_TRY(no_shared_bytes(O, {&Q}));
   KDA_TRY(no_shared_bytes(O, {&K, &V, &P, &CU, &L, &T, &KP, &VP}));
   KDA_TRY(no_shared_bytes(KP, {&Q, &K, &V, &P, &CU, &L, &T, &VP}));
   KDA_TRY(no_shared_bytes(VP, {&Q, &K, &V, &P, &CU, &L, &T}));
@@ -118,27 +89,11 @@ kda_status kda_rope_append(const kda_tensor* q, const kda_tensor* k, const kda_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeviceInfo dev;
   KDA_TRY(current_device(st, &dev));
-  kda::RopeArgs a{};
-  a.q = Q.data; a.k = K.data; a.v = V.data;
-  a.q_rs = Q.stride[0]; a.q_hs = Q.stride[1];
-  a.k_rs = K.stride[0]; a.k_hs = K.stride[1];
-  a.v_rs = V.stride[0]; a.v_hs = V.stride[1];
-  a.steps = reinterpret_cast<const uint64_t*>(P.data);
+  a.sms = dev.sms;
   a.cu = cu_seqlens != nullptr ? reinterpret_cast<const int32_t*>(CU.data) : nullptr;
   a.lens = reinterpret_cast<const int32_t*>(L.data);
   a.table = reinterpret_cast<const int32_t*>(T.data); a.table_rs = T.stride[0]; a.table_cols = (int32_t)T.shape[1];
-  a.kp = page_view(KP); a.vp = page_view(VP);
-  a.num_pages = (int32_t)KP.shape[0]; a.page_size = (int32_t)KP.shape[1];
-  a.q_out = O.data; a.o_rs = O.stride[0]; a.o_hs = O.stride[1];
-  a.R = (int32_t)R; a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.rot = (int32_t)rot;
-  a.interleaved = is_interleaved; a.amplitude = amplitude;
-  a.in_dtype = Q.dtype; a.page_dtype = KP.dtype;
-  a.vec = 4; a.sms = dev.sms;
-  if (Q.dtype == KDA_BF16 && KP.dtype == KDA_BF16 && D % 8 == 0 && (is_interleaved || rot % 16 == 0)) {
-    bool wide = true;
-    for (const View* t : {&Q, &K, &V, &KP, &VP, &O}) wide = wide && vectors_aligned(*t, 16);
-    if (wide) a.vec = 8;
-  }
+  a.N = (int32_t)N;
   return check_launch(kda::launch_rope_append(a, st));
 }
 

@@ -2,6 +2,8 @@
 // interleave, element alignment, page and table shapes.  Host only.
 #pragma once
 
+#include <cmath>
+
 #include "kda_cache.h"
 #include "kda_host.h"
 
@@ -111,6 +113,61 @@ inline kda_status check_attention_heads(int64_t Hq, int64_t Hkv, int64_t D) {
 }
 
 inline kda::PageView page_view(const View& v) { return {v.data, v.stride[0], v.stride[1], v.stride[2]}; }
+
+// Rows, steps, pages and outputs of the rotary entry points: checked, and the arguments that they share filled in.
+inline kda_status check_rope(const View& Q, const View& K, const View& V, const View& P, const View& KP, const View& VP,
+                             const View& O, int32_t is_interleaved, float amplitude, kda::RopeArgs* a) {
+  const int64_t R = Q.shape[0], Hq = Q.shape[1], D = Q.shape[2], Hkv = K.shape[1];
+  KDA_TRY(need_dtype(Q, KDA_F32, KDA_BF16));
+  KDA_CHECK(R <= INT32_MAX, KDA_ERR_INVALID_ARG, "q: too many token rows");
+  KDA_CHECK(Hq >= 1 && Hkv >= 1, KDA_ERR_INVALID_ARG, "q, k: need at least one head");
+  KDA_CHECK((Hq + 2 * Hkv) * D <= (1 << 24), KDA_ERR_UNSUPPORTED, "q, k: too many heads");
+  KDA_CHECK(D >= 4 && D % 4 == 0 && D <= 512, KDA_ERR_UNSUPPORTED, "q: head dimension %lld must be a multiple of 4 in 4..512",
+            (long long)D);
+  for (const View* t : {&K, &V}) {
+    KDA_CHECK(t->dtype == Q.dtype, KDA_ERR_INVALID_ARG, "%s: dtype must match q", t->name);
+    KDA_TRY(need_shape(*t, 0, R));
+    KDA_TRY(need_shape(*t, 1, Hkv));
+    KDA_TRY(need_shape(*t, 2, D));
+  }
+  for (const View* t : {&Q, &K, &V}) KDA_TRY(need_vec_layout(*t));
+  KDA_TRY(need_dtype(P, KDA_I32));
+  KDA_TRY(need_shape(P, 1, 2));
+  KDA_TRY(need_contiguous(P));
+  const int64_t rot = 2 * P.shape[0];
+  KDA_CHECK(rot <= D && rot % 8 == 0, KDA_ERR_INVALID_ARG,
+            "phase_steps: %lld pairs; the rotated part must be a multiple of 8 and at most the head dimension",
+            (long long)P.shape[0]);
+  KDA_CHECK(reinterpret_cast<uintptr_t>(P.data) % 8 == 0, KDA_ERR_INVALID_ARG, "phase_steps: data must be 8-byte aligned");
+  KDA_TRY(need_pages(KP, VP, Hkv, D));
+  KDA_CHECK(O.dtype == KP.dtype, KDA_ERR_INVALID_ARG, "q_out: dtype must match the pages");
+  KDA_TRY(need_shape(O, 0, R));
+  KDA_TRY(need_shape(O, 1, Hq));
+  KDA_TRY(need_shape(O, 2, D));
+  KDA_TRY(need_vec_layout(O));
+  KDA_CHECK(is_interleaved == 0 || is_interleaved == 1, KDA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  KDA_CHECK(std::isfinite(amplitude), KDA_ERR_INVALID_ARG, "amplitude must be finite");
+  for (const View* w : {&O, &KP, &VP}) KDA_TRY(need_distinct(*w));
+  if (!same_view(O, Q)) KDA_TRY(no_shared_bytes(O, {&Q}));
+  a->q = Q.data; a->k = K.data; a->v = V.data;
+  a->q_rs = Q.stride[0]; a->q_hs = Q.stride[1];
+  a->k_rs = K.stride[0]; a->k_hs = K.stride[1];
+  a->v_rs = V.stride[0]; a->v_hs = V.stride[1];
+  a->steps = reinterpret_cast<const uint64_t*>(P.data);
+  a->kp = page_view(KP); a->vp = page_view(VP);
+  a->num_pages = (int32_t)KP.shape[0]; a->page_size = (int32_t)KP.shape[1];
+  a->q_out = O.data; a->o_rs = O.stride[0]; a->o_hs = O.stride[1];
+  a->R = (int32_t)R; a->Hq = (int32_t)Hq; a->Hkv = (int32_t)Hkv; a->D = (int32_t)D; a->rot = (int32_t)rot;
+  a->interleaved = is_interleaved; a->amplitude = amplitude;
+  a->in_dtype = Q.dtype; a->page_dtype = KP.dtype;
+  a->vec = 4;
+  if (Q.dtype == KDA_BF16 && KP.dtype == KDA_BF16 && D % 8 == 0 && (is_interleaved || rot % 16 == 0)) {
+    bool wide = true;
+    for (const View* t : {&Q, &K, &V, &KP, &VP, &O}) wide = wide && vectors_aligned(*t, 16);
+    if (wide) a->vec = 8;
+  }
+  return KDA_OK;
+}
 
 }  // namespace host
 }  // namespace kda

@@ -36,6 +36,8 @@ struct Library {
   decltype(&kda_beam_select) beam;
   decltype(&kda_beam_select_workspace) beam_workspace;
   decltype(&kda_pool_move) move;
+  decltype(&kda_page_assign) page_assign;
+  decltype(&kda_rope_axes_append) rope_axes;
 } lib;
 
 // A Python exception is set.
@@ -252,6 +254,74 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// rope_axes_append(q, k, v, phase_steps, pair_axes, positions, slots, k_pages, v_pages, q_out, interleaved, amplitude)
+PyObject* rope_axes_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_arity("rope_axes_append", n, 12);
+    const at::Tensor& q = tensor_of(args[0]);
+    const Call call(q);
+    Described<10> t;
+    for (int i = 0; i < 9; ++i) t.add(call, args[i]);
+    at::Tensor made;
+    if (args[9] == Py_None) {
+      made = call.empty(q.sizes(), tensor_of(args[7]).scalar_type());
+      t.add(call, made);
+    } else {
+      t.add(call, args[9]);
+    }
+    const int32_t interleaved = truth_of(args[10]) ? 1 : 0;
+    const float amplitude = float_of(args[11]);
+    const kda_status s = without_gil([&] {
+      return lib.rope_axes(t.p[0], t.p[1], t.p[2], t.p[3], t.p[4], t.p[5], t.p[6], t.p[7], t.p[8], t.p[9], interleaved,
+                           amplitude, call.stream);
+    });
+    return s != KDA_OK ? PyLong_FromLong(s) : result(args[9], made);
+  });
+}
+
+// page_assign(seq_lens, new_lens, shared_lens, page_table, free_pages, free_state, page_size, rows, lens_out, state_out,
+// cu_seqlens, slots): the last four as a tuple
+PyObject* page_assign(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_arity("page_assign", n, 12);
+    const at::Tensor& lens = tensor_of(args[0]);
+    const Call call(lens);
+    Described<10> t;
+    for (int i = 0; i < 6; ++i) t.add(call, args[i]);
+    const int32_t page_size = int32_of(args[6]), rows = int32_of(args[7]);
+    if (rows < 0) raise(PyExc_ValueError, "rows must not be negative");
+    const int64_t N = lens.size(0);  // rank 1 at least: the descriptor's check
+    const int64_t size[4] = {N, 2, N + 1, rows};
+    at::Tensor made[4];
+    for (int i = 0; i < 4; ++i) {
+      if (args[8 + i] == Py_None) {
+        made[i] = call.empty({size[i]}, at::kInt);
+        t.add(call, made[i]);
+      } else {
+        const at::Tensor& given = tensor_of(args[8 + i]);
+        if (i == 3 && (given.dim() != 1 || given.size(0) != rows))
+          raise(PyExc_ValueError, "slots must be of [rows], rows is %d", static_cast<int>(rows));
+        t.add(call, given);
+      }
+    }
+    const kda_status s = without_gil([&] {
+      return lib.page_assign(t.p[0], t.p[1], t.p[2], t.p[3], t.p[4], t.p[5], page_size, t.p[6], t.p[7], t.p[8], t.p[9],
+                             call.stream);
+    });
+    if (s != KDA_OK) return PyLong_FromLong(s);
+    PyObject* four = PyTuple_New(4);
+    for (int i = 0; i < 4 && four != nullptr; ++i) {
+      PyObject* o = result(args[8 + i], made[i]);
+      if (o == nullptr) {
+        Py_DECREF(four);
+        return nullptr;
+      }
+      PyTuple_SET_ITEM(four, i, o);
+    }
+    return four;
+  });
+}
+
 // attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, return_lse, window, scale or None)
 PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -398,12 +468,13 @@ PyObject* describe_bytes(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// bind(addresses of rope_append, attention, attention_workspace, beam, beam_workspace, move)
+// bind(addresses of rope_append, attention, attention_workspace, beam, beam_workspace, move, page_assign, rope_axes)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    need_arity("bind", n, 6);
-    void* address[6];
-    for (int i = 0; i < 6; ++i) {
+    constexpr Py_ssize_t COUNT = 8;
+    need_arity("bind", n, COUNT);
+    void* address[COUNT];
+    for (Py_ssize_t i = 0; i < COUNT; ++i) {
       address[i] = PyLong_AsVoidPtr(args[i]);
       if (address[i] == nullptr) {
         if (PyErr_Occurred()) throw Raised();
@@ -416,6 +487,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     lib.beam = reinterpret_cast<decltype(lib.beam)>(address[3]);
     lib.beam_workspace = reinterpret_cast<decltype(lib.beam_workspace)>(address[4]);
     lib.move = reinterpret_cast<decltype(lib.move)>(address[5]);
+    lib.page_assign = reinterpret_cast<decltype(lib.page_assign)>(address[6]);
+    lib.rope_axes = reinterpret_cast<decltype(lib.rope_axes)>(address[7]);
     Py_RETURN_NONE;
   });
 }
@@ -427,6 +500,8 @@ PyMethodDef methods[] = {{"rope_append", fast(rope_append), METH_FASTCALL, nullp
                          {"attention", fast(attention), METH_FASTCALL, nullptr},
                          {"beam", fast(beam), METH_FASTCALL, nullptr},
                          {"move", fast(move), METH_FASTCALL, nullptr},
+                         {"rope_axes_append", fast(rope_axes_append), METH_FASTCALL, nullptr},
+                         {"page_assign", fast(page_assign), METH_FASTCALL, nullptr},
                          {"describe", fast(describe_bytes), METH_FASTCALL, nullptr},
                          {"bind", fast(bind), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

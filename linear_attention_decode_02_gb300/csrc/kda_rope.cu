@@ -17,6 +17,11 @@
 // all the rows at once, so that 2 * ROWS loads are in flight and the way from
 // the row to its position and page (three dependent loads) is paid once for
 // them.
+//
+// With several axes a row has a position on each of them, and pair i turns by
+// its own axis' position; negative ones turn backwards, since the product modulo
+// 2^64 does.  The row's place is a slot that it is given, so two loads that do not
+// depend on each other take the place of the search and the table.
 #include <algorithm>
 
 #include "kda_cache.h"
@@ -108,9 +113,10 @@ struct Slot {
   }
 };
 
-template <typename In, typename Out, int VEC, bool INTERLEAVED, int ROWS>
+template <typename In, typename Out, int VEC, bool INTERLEAVED, int ROWS, bool AXES>
 __global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 s_cs[ROWS][kMaxPairs];
+  __shared__ int s_at[AXES ? ROWS : 1][kRopeAxes];  // positions of the axes
   __shared__ int s_pos[ROWS];           // -1: zero output
   __shared__ int64_t s_k[ROWS], s_v[ROWS];  // element offsets of the row's place in its page, or -1
   const int row0 = blockIdx.x * ROWS;
@@ -118,7 +124,21 @@ __global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __gr
   pdl_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < ROWS) {
+  if (AXES && warp < ROWS) {
+    const int row = row0 + warp;
+    if (lane < kRopeAxes)
+      s_at[warp][lane] = row < a.R && lane < a.num_axes ? __ldg(a.positions + row * a.p_rs + lane * a.p_as) : 0;
+    if (lane == 0) {
+      const int slot = row < a.R ? __ldg(a.slots + row) : -1;
+      const int page = slot < 0 ? 0 : slot / a.page_size;
+      const bool live = page > 0 && page < a.num_pages;
+      const int64_t t = slot - (int64_t)page * a.page_size;
+      s_pos[warp] = live ? 0 : -1;
+      s_k[warp] = live ? page * a.kp.page + t * a.kp.token : -1;
+      s_v[warp] = live ? page * a.vp.page + t * a.vp.token : -1;
+    }
+  }
+  if (!AXES && warp < ROWS) {
     const int row = row0 + warp;
     int n = row, end = row + 1;
     bool live = row < a.R;
@@ -154,7 +174,13 @@ __global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __gr
   const int pair_tasks = a.rot / (2 * PAIRS);
   for (int i = threadIdx.x; i < ROWS * (a.rot / 2); i += blockDim.x) {
     const int r = i / (a.rot / 2), pair = i - r * (a.rot / 2);
-    const uint64_t phase = (uint64_t)(uint32_t)max(s_pos[r], 0) * __ldg(a.steps + pair);
+    uint64_t phase;
+    if constexpr (AXES) {
+      const int axis = __ldg(a.pair_axes + pair);  // none of the call's: the pair is not turned
+      phase = axis >= 0 && axis < a.num_axes ? (uint64_t)(int64_t)s_at[r][axis] * __ldg(a.steps + pair) : 0;
+    } else {
+      phase = (uint64_t)(uint32_t)max(s_pos[r], 0) * __ldg(a.steps + pair);
+    }
     float sn, cs;
     const uint32_t turn = (uint32_t)((phase + 0x80000000u) >> 32), quarter = (turn + 0x20000000u) >> 30;
     sincospif((float)(int32_t)(turn - (quarter << 30)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
@@ -240,8 +266,11 @@ __global__ void __launch_bounds__(kThreads, 6) kda_rope_append_kernel(const __gr
 
 template <typename In, typename Out, int VEC, int ROWS>
 cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
-  auto kernel = a.interleaved ? kda_rope_append_kernel<In, Out, VEC, true, ROWS>
-                              : kda_rope_append_kernel<In, Out, VEC, false, ROWS>;
+  const bool axes = a.positions != nullptr;
+  auto kernel = a.interleaved ? (axes ? kda_rope_append_kernel<In, Out, VEC, true, ROWS, true>
+                                      : kda_rope_append_kernel<In, Out, VEC, true, ROWS, false>)
+                              : (axes ? kda_rope_append_kernel<In, Out, VEC, false, ROWS, true>
+                                      : kda_rope_append_kernel<In, Out, VEC, false, ROWS, false>);
   // Few rows: several blocks share each, down to one vector a thread, until every SM has its six.
   const int64_t blocks = (a.R + (int64_t)ROWS - 1) / ROWS;
   const int pairs = a.interleaved ? a.rot / VEC : a.rot / (2 * VEC);

@@ -60,6 +60,59 @@ def rope_append(q, k, v, freq, seq_lens, page_table, k_pages, v_pages, cu_seqlen
     return q_out, kp, vp
 
 
+def rope_axes_append(q, k, v, freq, pair_axes, positions, slots, k_pages, v_pages, interleaved=False, amplitude=1.0):
+    """(q_out, k_pages, v_pages) after the call; the inputs are not changed."""
+    q_out = np.zeros_like(q, dtype=np.float64)
+    kp, vp = np.array(k_pages, dtype=np.float64), np.array(v_pages, dtype=np.float64)
+    num_pages, page = kp.shape[:2]
+    for r in range(q.shape[0]):
+        p, t = divmod(int(slots[r]), page)
+        if not 0 < p < num_pages:
+            continue
+        at = np.array([float(positions[r, a]) if 0 <= a < positions.shape[1] else 0.0 for a in pair_axes])
+        q_out[r] = rotate(q[r], at, freq, interleaved, amplitude)
+        kp[p, t] = rotate(k[r], at, freq, interleaved, amplitude)
+        vp[p, t] = v[r]
+    return q_out, kp, vp
+
+
+def page_assign(seq_lens, new_lens, table, ring, state, page, rows, shared_lens=None):
+    """(lens, state, cu_seqlens, slots, table, ring) after the call, sequence by sequence; the inputs are not changed."""
+    table, ring = np.array(table), np.array(ring)
+    N, P = table.shape
+    C = len(ring)
+    head, count = int(state[0]), int(state[1])
+    if not (0 <= head < C and count >= 0):
+        head = count = 0
+    count = min(count, C)
+    lens, cu, slots, back = [], [0], [], []
+    taken = asked = 0
+    for n in range(N):
+        old, new = min(max(int(seq_lens[n]), 0), P * page), max(int(new_lens[n]), 0)
+        held, want = -(-old // page), -(-new // page)
+        if new > P * page:
+            new, want = old, held
+        asked += max(0, want - held)
+        if want > held and asked > count:
+            new, want = old, held
+        for col in range(held, want):
+            table[n, col] = ring[(head + taken) % C]
+            taken += 1
+        keep = 0 if shared_lens is None else max(int(shared_lens[n]), 0) // page
+        back += [int(p) for p in table[n, max(want, keep):held] if 1 <= p <= C]
+        for pos in range(old, new):
+            p = int(table[n, pos // page])
+            slots.append(p * page + pos % page if 1 <= p <= C else -1)
+        lens.append(new)
+        cu.append(cu[-1] + max(0, new - old))
+    back = back[:C - count]
+    for j, p in enumerate(back):
+        ring[(head + count + j) % C] = p
+    slots = (slots + [-1] * rows)[:rows]
+    return (np.array(lens, dtype=np.int64), np.array([(head + taken) % C, count - taken + len(back)]),
+            np.array(cu), np.array(slots, dtype=np.int64), table, ring)
+
+
 def paged_attention(q, k_pages, v_pages, page_table, seq_lens, window=0, scale=None):
     """(out [N, Hq, D], lse [N, Hq]); a row without live positions gives 0 and -inf."""
     N, Hq, D = q.shape
