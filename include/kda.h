@@ -466,6 +466,37 @@ kda_status kda_rope_axes_append(const kda_tensor* q, const kda_tensor* k, const 
  */
 kda_status kda_rope_pair_axes(const int32_t* sections, int32_t num_axes, int32_t cyclic, int32_t* pair_axes);
 
+/*
+ * kda_prefix_attention_decode: kda_paged_attention_decode for groups of sequences
+ * that begin alike (beams of one prompt, users of one system prompt): the common
+ * positions are read once a group for all of its query heads, each sequence's own
+ * positions once.  Launches three kernels.
+ *
+ *   q, k_pages, v_pages, page_table, seq_lens, window, scale, out, lse: as there.  A
+ *               sequence's row of the table lists all its pages, common ones too.
+ *   group_starts [G+1] int32, not falling: group g is sequences group_starts[g] ..
+ *               group_starts[g+1] - 1.  Sequences outside every group are on their own.
+ *   prefix_lens [G] int32: the first prefix_lens[g] positions of a group's sequences
+ *               are the same.  They are read through the row of its first sequence,
+ *               whatever that one's length.  The end may lie inside a page.
+ *   workspace   as there, of the floats that kda_prefix_attention_workspace names.
+ * The result is that of kda_paged_attention_decode but for rounding: weights may be
+ * up to 16 times those relative to the largest score before they are summed, so values
+ * within that factor of the largest float may overflow.  A sequence shorter than its
+ * group's prefix, or whose window leaves part of it out, is on its own too.  So is
+ * every sequence where the dtype is float32, where vectors are off 16-byte boundaries
+ * and where there are not fewer groups than sequences.
+ */
+kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                       const kda_tensor* page_table, const kda_tensor* seq_lens,
+                                       const kda_tensor* group_starts, const kda_tensor* prefix_lens,
+                                       const kda_tensor* workspace, int32_t window, float scale, const kda_tensor* out,
+                                       const kda_tensor* lse, void* stream);
+
+/* Floats of workspace of kda_prefix_attention_decode on a device of sm_count SMs (dtype: KDA_F32 / KDA_BF16). */
+kda_status kda_prefix_attention_workspace(int64_t sequences, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                          int32_t dtype, int32_t sm_count, int64_t* floats);
+
 /* ---- host-only queries (no CUDA calls) ---------------------------------- */
 
 /* Operation ids for kda_plan_split. */
@@ -541,10 +572,11 @@ int32_t kda_plan_schedule(int32_t op, int64_t units, int32_t state_dtype, int32_
 kda_status kda_set_schedule_override(int32_t schedule);
 
 /*
- * Device error word of the streaming kernels on the current device: bit 0 =
+ * Device error word of the streaming and tensor-core kernels on the current device: bit 0 =
  * a wait for a filled stage timed out (2 s), bit 1 = a wait for a free stage
  * timed out, bit 2 = the kda_selftest_wait_timeout wait gave up (expected),
- * bit 3 = a wait of the tensor-core (MMA) speculative kernel timed out.  A
+ * bit 3 = a wait of the tensor-core (MMA) speculative kernel timed out, bit 4 =
+ * a wait of the shared-prefix attention kernel timed out.  A
  * kernel that times out records the bit and returns early, its results for
  * the affected units are undefined.  Synchronises the device;
  * clears the word when `clear` is non-zero.

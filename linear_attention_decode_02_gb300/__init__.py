@@ -18,6 +18,7 @@ and the operators that the attention layers and beams around them need:
     kda_pool_move          copies, forks, clears and reorders slots of any pools
     kda_page_assign        page tables and slots of new tokens from the sequences' lengths
     kda_rope_axes_append   rotary positions on several axes, keys and values to slots of the cache
+    kda_prefix_attention_decode  the attention of sequences that share prefixes, each read once
 
 Build the library with ``python -m linear_attention_decode_02_gb300.build``.
 """
@@ -25,6 +26,7 @@ Build the library with ``python -m linear_attention_decode_02_gb300.build``.
 from .binding import (SCHED_AUTO, SCHED_SPLIT, SCHED_STREAM, KdaError, kda_beam_select,  # noqa: F401
                       kda_beam_select_workspace, kda_device_error, kda_fused_decode, kda_packed_decode,
                       kda_packed_fused_decode, kda_page_assign, kda_paged_attention_decode, kda_paged_attention_workspace,
-                      kda_plan_schedule, kda_plan_split, kda_pool_move, kda_recurrent_decode, kda_rope_append,
+                      kda_plan_schedule, kda_plan_split, kda_pool_move, kda_prefix_attention_decode,
+                      kda_prefix_attention_workspace, kda_recurrent_decode, kda_rope_append,
                       kda_rope_axes_append, kda_rope_pair_axes, kda_rope_phase_steps, kda_set_schedule_override, kda_set_split_override, kda_spec_decode,
                       kda_spec_verify_decode, kda_version, library)

@@ -51,6 +51,7 @@ EXPORTS = ("kda_recurrent_decode", "kda_packed_decode", "kda_fused_decode", "kda
            "kda_paged_attention_decode", "kda_paged_attention_workspace",
            "kda_beam_select", "kda_beam_select_workspace",
            "kda_page_assign", "kda_rope_axes_append", "kda_rope_pair_axes",
+           "kda_prefix_attention_decode", "kda_prefix_attention_workspace",
            "kda_plan_split", "kda_set_split_override", "kda_plan_schedule", "kda_set_schedule_override",
            "kda_device_error", "kda_selftest_wait_timeout", "kda_status_string", "kda_last_error_message",
            "kda_version")
@@ -89,6 +90,8 @@ def _declare(lib):
         "kda_rope_phase_steps": [i32, f64, f64, f64, f64, f64, vp],
         "kda_page_assign": [T, T, T, T, T, T, i32, T, T, T, T, vp],
         "kda_rope_axes_append": [T, T, T, T, T, T, T, T, T, T, i32, f32, vp],
+        "kda_prefix_attention_decode": [T, T, T, T, T, T, T, T, i32, f32, T, T, vp],
+        "kda_prefix_attention_workspace": [ctypes.c_int64, i32, i32, i32, i32, i32, vp],
         "kda_rope_pair_axes": [ctypes.POINTER(i32), i32, i32, vp],
     }
     for name, args in sigs.items():
@@ -307,7 +310,8 @@ def _native():
                          for f in (lib.kda_rope_append, lib.kda_paged_attention_decode,
                                    lib.kda_paged_attention_workspace, lib.kda_beam_select,
                                    lib.kda_beam_select_workspace, lib.kda_pool_move, lib.kda_page_assign,
-                                   lib.kda_rope_axes_append)))
+                                   lib.kda_rope_axes_append, lib.kda_prefix_attention_decode,
+                                   lib.kda_prefix_attention_workspace)))
                 _module = m
     return _module
 
@@ -389,6 +393,28 @@ def kda_paged_attention_decode(q, k_pages, v_pages, page_table, seq_lens, window
     """
     r = (_module or _native()).attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, return_lse,
                                          window, scale)
+    if type(r) is int:
+        _raise(r)
+    return r
+
+
+def kda_prefix_attention_workspace(sequences, q_heads, kv_heads, head_dim, dtype, sm_count):
+    """Floats of workspace a kda_prefix_attention_decode call needs (host-only query)."""
+    lib = library()
+    floats = ctypes.c_int64(0)
+    _check(lib, lib.kda_prefix_attention_workspace(int(sequences), int(q_heads), int(kv_heads), int(head_dim),
+                                                   _DTYPES.get(dtype, -1), int(sm_count), ctypes.addressof(floats)))
+    return floats.value
+
+
+def kda_prefix_attention_decode(q, k_pages, v_pages, page_table, seq_lens, group_starts, prefix_lens, window=0,
+                                scale=None, out=None, lse=None, return_lse=False, workspace=None):
+    """kda_paged_attention_decode for groups of sequences whose first prefix_lens [G] positions are the same.
+
+    Group g is sequences group_starts[g] .. group_starts[g + 1] - 1; the workspace is as in kda_paged_attention_decode.
+    """
+    r = (_module or _native()).prefix_attention(q, k_pages, v_pages, page_table, seq_lens, group_starts, prefix_lens,
+                                                workspace, out, lse, return_lse, window, scale)
     if type(r) is int:
         _raise(r)
     return r

@@ -618,11 +618,12 @@ kda_status kda_set_schedule_override(int32_t schedule) {
 
 kda_status kda_device_error(uint32_t* flags, int32_t clear) {
   KDA_CHECK(flags != nullptr, KDA_ERR_INVALID_ARG, "flags: null pointer");
-  unsigned int f = 0, fm = 0;
+  unsigned int f = 0, fm = 0, fp = 0;
   cudaError_t e = kda::read_device_error(&f, clear != 0);
   if (e == cudaSuccess) e = kda::read_mma_error(&fm, clear != 0);
+  if (e == cudaSuccess) e = kda::read_prefix_error(&fp, clear != 0);
   KDA_CHECK(e == cudaSuccess, KDA_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(e));
-  *flags = f | fm;
+  *flags = f | fm | fp;
   return KDA_OK;
 }
 

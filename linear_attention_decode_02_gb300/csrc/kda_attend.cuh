@@ -85,6 +85,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
   Span s;
   s.end = (int)min((int64_t)max(len, 0), cap);
   s.first = a.window > 0 && len > a.window ? len - a.window : 0;
+  if (a.skip != nullptr) s.first = max(s.first, __ldg(a.skip + n));
   if (s.first >= s.end) s.first = s.end = 0;
   s.tile0 = s.first / kTile;
   s.tiles = s.end == 0 ? 1 : (s.end - 1) / kTile - s.tile0 + 1;
@@ -201,6 +202,12 @@ __device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
   note.n = w.unit_start < p.start ? w.n : -1;
   note.group = w.group;
   return note;
+}
+
+// A result that another kernel joins: its row's maximum and sum, the piece that
+// made it and how many pieces after that one hold more of it, at row `row`.
+__device__ __forceinline__ float4 first_note(float m, float l, int piece, int more, int row) {
+  return make_float4(m, l, __int_as_float(piece), __int_as_float(more << 8 | row));
 }
 
 // 16 bytes to shared memory; zeros where live is false (src is then not read).

@@ -13,7 +13,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Joins the warps of a block at a unit's end in its piece and writes the
-// result, or the piece's partial.  Lane (g, t4) holds channels 8 i + 2 t4 and + 1
+// result, or the piece's partial; under a shared prefix its result, or first
+// piece, goes to another kernel's join.  Lane (g, t4) holds channels 8 i + 2 t4 and + 1
 // of rows g (o[i][0], o[i][1]) and g + 8 (o[i][2], o[i][3]): two heads with HG =
 // 16, two parts of one head to be added with HG = 8.  m and l are the warp's
 // row maxima and this lane's sums.  shared_o: (WARPS - 1) * 8 * D floats; stats:
@@ -55,6 +56,7 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
   const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
   const bool at_start = walk.unit_start <= place.start;
   const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
+  const bool first = a.first_o != nullptr && walk.unit_start >= place.start;
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
     if (r > 0) __syncthreads();  // all have taken the first heads
@@ -88,14 +90,19 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
         x += v.x;
         y += v.y;
       }
-      if (whole) {
+      if (first) {
+        *reinterpret_cast<float2*>(a.first_o + head * D + d) = make_float2(x, y);
+      } else if (whole) {
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
       } else {
         *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
       }
     }
     if (t4 == 0 && warp == 0) {
-      if (!whole) {
+      if (first) {
+        const int pieces = pieces_of(place.T, gridDim.x);
+        a.first_note[head] = first_note(M[r], L, c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
+      } else if (!whole) {
         ws.ml_of(slot, h)[0] = M[r];
         ws.ml_of(slot, h)[1] = L;
       } else if (a.lse != nullptr) {

@@ -91,6 +91,11 @@ struct AttendArgs {
   int32_t window;                         // 0: all
   float scale_log2;                       // scale * log2(e)
   int32_t vec16;                          // q rows, key and value vectors start on 16-byte boundaries
+  // Under a shared prefix: the first positions of each sequence that are attended to elsewhere, and where a unit's
+  // result (or its first piece's) goes instead of out and lse, [N, Hq, D] and [N, Hq].  Null otherwise.
+  const int32_t* skip;
+  float* first_o;
+  float4* first_note;
 };
 
 // Grid and workspace of the attention kernels: `ctas` workers that each may
@@ -102,6 +107,16 @@ struct AttendPlan {
 // Floats of workspace for either kernel that may serve the dtype.
 int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
+
+// Attention of sequences that share prefixes, group by group.
+struct PrefixArgs {
+  AttendArgs attend;
+  const int32_t* starts;                  // [G + 1]: group g is sequences starts[g] .. starts[g + 1] - 1
+  const int32_t* prefix_lens;             // [G]
+  int32_t G;
+};
+int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
+cudaError_t launch_prefix_attention(const PrefixArgs& a, int32_t sms, cudaStream_t s);
 
 // Beam selection over beams x vocabulary.
 constexpr int kBeamMax = 32;      // beams of a request

@@ -169,5 +169,70 @@ inline kda_status check_rope(const View& Q, const View& K, const View& V, const 
   return KDA_OK;
 }
 
+// Tensors of the attention entry points: checked, and the launch arguments that they share filled in.
+struct AttentionViews {
+  View Q, KP, VP, T, L, W, O, E;
+};
+inline kda_status check_attention(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                  const kda_tensor* page_table, const kda_tensor* seq_lens, const kda_tensor* workspace,
+                                  int32_t window, float scale, const kda_tensor* out, const kda_tensor* lse,
+                                  AttentionViews* views, kda::AttendArgs* args) {
+  View &Q = views->Q, &KP = views->KP, &VP = views->VP, &T = views->T, &L = views->L, &W = views->W, &O = views->O,
+       &E = views->E;
+  KDA_TRY(ranked_view(q, "q", 3, -1, &Q));
+  KDA_TRY(ranked_view(k_pages, "k_pages", 4, -1, &KP));
+  KDA_TRY(ranked_view(v_pages, "v_pages", 4, -1, &VP));
+  KDA_TRY(ranked_view(page_table, "page_table", 2, -1, &T));
+  KDA_TRY(raw_view(seq_lens, "seq_lens", &L));
+  KDA_TRY(ranked_view(workspace, "workspace", 1, -1, &W));
+  KDA_TRY(ranked_view(out, "out", 3, -1, &O));
+  const int64_t N = Q.shape[0], Hq = Q.shape[1], D = Q.shape[2], Hkv = KP.shape[2];
+  KDA_TRY(need_dtype(Q, KDA_F32, KDA_BF16));
+  KDA_CHECK(N <= INT32_MAX, KDA_ERR_INVALID_ARG, "q: too many sequences");
+  KDA_TRY(check_attention_heads(Hq, Hkv, D));
+  KDA_TRY(need_vec_layout(Q));
+  KDA_TRY(need_pages(KP, VP, Hkv, D));
+  KDA_CHECK(KP.dtype == Q.dtype, KDA_ERR_INVALID_ARG, "k_pages: dtype must match q");
+  KDA_TRY(need_table(T, N));
+  KDA_CHECK(T.shape[1] <= (1 << 30) / KP.shape[1], KDA_ERR_UNSUPPORTED,
+            "page_table: %lld pages of %lld positions, more than 2^30 positions a sequence", (long long)T.shape[1],
+            (long long)KP.shape[1]);
+  KDA_TRY(need_indices(L, N));
+  KDA_TRY(need_out(O));
+  KDA_TRY(need_shape(O, 0, N));
+  KDA_TRY(need_shape(O, 1, Hq));
+  KDA_TRY(need_shape(O, 2, D));
+  if (lse != nullptr) {
+    KDA_TRY(ranked_view(lse, "lse", 2, -1, &E));
+    KDA_TRY(need_dtype(E, KDA_F32));
+    KDA_TRY(need_shape(E, 0, N));
+    KDA_TRY(need_shape(E, 1, Hq));
+    KDA_TRY(need_contiguous(E));
+  }
+  KDA_TRY(need_dtype(W, KDA_F32));
+  KDA_TRY(need_contiguous(W));
+  KDA_CHECK(reinterpret_cast<uintptr_t>(W.data) % 16 == 0, KDA_ERR_INVALID_ARG, "workspace: data must be 16-byte aligned");
+  KDA_CHECK(window >= 0, KDA_ERR_INVALID_ARG, "window must not be negative (0: all positions)");
+  const float scale_log2 = scale * 1.4426950408889634f;  // scores are taken in units of log 2
+  KDA_CHECK(scale > 0.f && std::isfinite(scale_log2), KDA_ERR_INVALID_ARG, "scale must be positive and at most 2.3e38");
+  KDA_TRY(no_shared_bytes(O, {&Q, &KP, &VP, &T, &L, &W, &E}));
+  KDA_TRY(no_shared_bytes(W, {&Q, &KP, &VP, &T, &L, &E}));
+  KDA_TRY(no_shared_bytes(E, {&Q, &KP, &VP, &T, &L}));
+  kda::AttendArgs& a = *args;
+  a.q = Q.data; a.q_rs = Q.stride[0]; a.q_hs = Q.stride[1];
+  a.kp = page_view(KP); a.vp = page_view(VP);
+  a.num_pages = (int32_t)KP.shape[0]; a.page_size = (int32_t)KP.shape[1];
+  a.table = reinterpret_cast<const int32_t*>(T.data); a.table_rs = T.stride[0]; a.table_cols = (int32_t)T.shape[1];
+  a.lens = reinterpret_cast<const int32_t*>(L.data);
+  a.out = O.data;
+  a.lse = lse != nullptr ? reinterpret_cast<float*>(E.data) : nullptr;
+  a.work = reinterpret_cast<float*>(W.data);
+  a.N = (int32_t)N; a.Hq = (int32_t)Hq; a.Hkv = (int32_t)Hkv; a.D = (int32_t)D; a.dtype = KP.dtype;
+  a.window = window;
+  a.scale_log2 = scale_log2;
+  a.vec16 = vectors_aligned(Q, 16) && vectors_aligned(KP, 16) && vectors_aligned(VP, 16);
+  return KDA_OK;
+}
+
 }  // namespace host
 }  // namespace kda

@@ -135,6 +135,21 @@ __device__ __forceinline__ float f4get(const float4& v, int j) {
   return j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w));
 }
 
+// Index of the sequence owning `row`: the number of entries of cu[1..N] that
+// are <= row, by a 32-way search of the whole warp (N <= 32: one load).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int row, int lane) {
+  int lo = 0, hi = N;
+  while (hi > lo) {
+    const int step = (hi - lo + 31) / 32;
+    const int64_t p = lo + (int64_t)(lane + 1) * step - 1;
+    const bool le = p < hi && __ldg(cu + 1 + p) <= row;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    lo += c * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 // ---- reductions -----------------------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float x) {

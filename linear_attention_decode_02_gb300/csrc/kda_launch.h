@@ -119,6 +119,9 @@ cudaError_t launch_spec_mma(const SpecArgs& a, bool verify, int sm_count, cudaSt
 // speculative kernel: bit 3 = one of its waits timed out.
 cudaError_t read_mma_error(unsigned int* flags, bool clear);
 
+// The same of the shared-prefix attention kernel: bit 4.
+cudaError_t read_prefix_error(unsigned int* flags, bool clear);
+
 // One warp waiting on a barrier nothing completes (bounded-wait self-test).
 cudaError_t launch_selftest_wait(cudaStream_t s);
 

@@ -11,6 +11,15 @@
 
 using namespace kda::host;
 
+namespace {
+
+kda_status check_prefix_sequences(int64_t N) {
+  KDA_CHECK(N >= 0 && N < (1 << 24), KDA_ERR_UNSUPPORTED, "%lld sequences, fewer than 2^24 are served", (long long)N);
+  return KDA_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 kda_status kda_page_assign(const kda_tensor* seq_lens, const kda_tensor* new_lens, const kda_tensor* shared_lens,
@@ -135,6 +144,52 @@ kda_status kda_rope_axes_append(const kda_tensor* q, const kda_tensor* k, const 
   a.pair_axes = reinterpret_cast<const int32_t*>(A.data);
   a.num_axes = (int32_t)X.shape[1];
   return check_launch(kda::launch_rope_append(a, st));
+}
+
+kda_status kda_prefix_attention_workspace(int64_t sequences, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                          int32_t dtype, int32_t sm_count, int64_t* floats) {
+  KDA_CHECK(floats != nullptr, KDA_ERR_INVALID_ARG, "floats: null pointer");
+  KDA_TRY(check_attention_heads(q_heads, kv_heads, head_dim));
+  KDA_TRY(check_prefix_sequences(sequences));
+  KDA_CHECK(dtype == KDA_F32 || dtype == KDA_BF16, KDA_ERR_INVALID_ARG, "dtype %s not accepted", dtname(dtype));
+  KDA_CHECK(sm_count >= 1 && sm_count <= 4096, KDA_ERR_INVALID_ARG, "sm_count %d out of range", sm_count);
+  *floats = kda::prefix_floats(sequences, q_heads, kv_heads, head_dim, dtype, sm_count);
+  return KDA_OK;
+}
+
+kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
+                                       const kda_tensor* page_table, const kda_tensor* seq_lens,
+                                       const kda_tensor* group_starts, const kda_tensor* prefix_lens,
+                                       const kda_tensor* workspace, int32_t window, float scale, const kda_tensor* out,
+                                       const kda_tensor* lse, void* stream) {
+  AttentionViews v;
+  View S, P;
+  kda::PrefixArgs a{};
+  KDA_TRY(check_attention(q, k_pages, v_pages, page_table, seq_lens, workspace, window, scale, out, lse, &v, &a.attend));
+  KDA_TRY(check_prefix_sequences(v.Q.shape[0]));
+  KDA_TRY(raw_view(group_starts, "group_starts", &S));
+  KDA_TRY(raw_view(prefix_lens, "prefix_lens", &P));
+  KDA_CHECK(P.ndim == 1, KDA_ERR_INVALID_ARG, "prefix_lens: expected rank 1");
+  const int64_t G = P.shape[0];
+  KDA_CHECK(G <= INT32_MAX - 1, KDA_ERR_INVALID_ARG, "prefix_lens: too many groups");
+  KDA_TRY(need_indices(P, G));
+  KDA_TRY(need_indices(S, G + 1));
+  KDA_TRY(no_shared_bytes(v.O, {&S, &P}));
+  KDA_TRY(no_shared_bytes(v.W, {&S, &P}));
+  KDA_TRY(no_shared_bytes(v.E, {&S, &P}));
+  if (a.attend.N == 0) return KDA_OK;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DeviceInfo dev;
+  KDA_TRY(current_device(st, &dev));
+  const kda::AttendArgs& t = a.attend;
+  const int64_t floats = kda::prefix_floats(t.N, t.Hq, t.Hkv, t.D, t.dtype, dev.sms);
+  KDA_CHECK(v.W.shape[0] >= floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
+            (long long)v.W.shape[0], (long long)floats);
+  a.starts = reinterpret_cast<const int32_t*>(S.data);
+  a.prefix_lens = reinterpret_cast<const int32_t*>(P.data);
+  a.G = (int32_t)G;
+  return check_launch(kda::launch_prefix_attention(a, dev.sms, st));
 }
 
 }  // extern "C"

@@ -38,6 +38,8 @@ struct Library {
   decltype(&kda_pool_move) move;
   decltype(&kda_page_assign) page_assign;
   decltype(&kda_rope_axes_append) rope_axes;
+  decltype(&kda_prefix_attention_decode) prefix;
+  decltype(&kda_prefix_attention_workspace) prefix_workspace;
 } lib;
 
 // A Python exception is set.
@@ -322,52 +324,74 @@ PyObject* page_assign(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// The attention calls; `starts` and `prefixes` null without shared prefixes.
+PyObject* attend(PyObject* const* five, PyObject* starts, PyObject* prefixes, PyObject* given_work, PyObject* given_out,
+                 PyObject* given_lse, bool both, int32_t window, PyObject* given_scale) {
+  const at::Tensor &q = tensor_of(five[0]), &k = tensor_of(five[1]);
+  const Call call(q);
+  const bool shared = starts != nullptr;
+  Described<10> t;
+  for (int i = 0; i < 5; ++i) t.add(call, five[i]);
+  if (shared) {
+    t.add(call, starts);
+    t.add(call, prefixes);
+  }
+  if (q.dim() != 3 || k.dim() != 4) raise(PyExc_ValueError, "q must be [N, Hq, D] and the pages of rank 4");
+  int64_t floats = 0;
+  if (given_work == Py_None) {
+    const auto small = [](int64_t x) { return static_cast<int32_t>(std::min<int64_t>(x, INT32_MAX)); };
+    const int32_t hq = small(q.size(1)), hkv = small(k.size(2)), d = small(q.size(2)), dtype = dtype_of(q);
+    const kda_status s = shared ? lib.prefix_workspace(q.size(0), hq, hkv, d, dtype, call.sms(), &floats)
+                                : lib.attention_workspace(hq, hkv, d, dtype, call.sms(), &floats);
+    if (s != KDA_OK) return PyLong_FromLong(s);
+  }
+  const at::Tensor work = workspace(call, given_work, floats);
+  t.add(call, work);
+  at::Tensor out, lse;
+  if (given_out == Py_None) {
+    out = call.empty(q.sizes(), at::kBFloat16);
+    t.add(call, out);
+  } else {
+    t.add(call, given_out);
+  }
+  if (given_lse == Py_None && both) {
+    lse = call.empty({q.size(0), q.size(1)}, at::kFloat);
+    t.add(call, lse);
+  } else {
+    t.add(call, given_lse);
+  }
+  const float scale = given_scale == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(q.size(2))))
+                                             : float_of(given_scale);
+  const kda_status s = without_gil([&] {
+    return shared ? lib.prefix(t.p[0], t.p[1], t.p[2], t.p[3], t.p[4], t.p[5], t.p[6], t.p[7], window, scale, t.p[8],
+                               t.p[9], call.stream)
+                  : lib.attention(t.p[0], t.p[1], t.p[2], t.p[3], t.p[4], t.p[5], window, scale, t.p[6], t.p[7],
+                                  call.stream);
+  });
+  if (s != KDA_OK) return PyLong_FromLong(s);
+  PyObject* o = result(given_out, out);
+  if (!both || o == nullptr) return o;
+  PyObject* e = result(given_lse, lse);
+  PyObject* pair = e != nullptr ? PyTuple_Pack(2, o, e) : nullptr;
+  Py_DECREF(o);
+  Py_XDECREF(e);
+  return pair;
+}
+
 // attention(q, k_pages, v_pages, page_table, seq_lens, workspace, out, lse, return_lse, window, scale or None)
 PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     need_arity("attention", n, 11);
-    const at::Tensor &q = tensor_of(args[0]), &k = tensor_of(args[1]);
-    const Call call(q);
-    Described<8> t;
-    for (int i = 0; i < 5; ++i) t.add(call, args[i]);
-    if (q.dim() != 3 || k.dim() != 4) raise(PyExc_ValueError, "q must be [N, Hq, D] and the pages of rank 4");
-    int64_t floats = 0;
-    if (args[5] == Py_None) {
-      const auto small = [](int64_t x) { return static_cast<int32_t>(std::min<int64_t>(x, INT32_MAX)); };
-      const kda_status s = lib.attention_workspace(small(q.size(1)), small(k.size(2)), small(q.size(2)), dtype_of(q),
-                                                   call.sms(), &floats);
-      if (s != KDA_OK) return PyLong_FromLong(s);
-    }
-    const at::Tensor work = workspace(call, args[5], floats);
-    t.add(call, work);
-    at::Tensor out, lse;
-    if (args[6] == Py_None) {
-      out = call.empty(q.sizes(), at::kBFloat16);
-      t.add(call, out);
-    } else {
-      t.add(call, args[6]);
-    }
-    const bool both = truth_of(args[8]);
-    if (args[7] == Py_None && both) {
-      lse = call.empty({q.size(0), q.size(1)}, at::kFloat);
-      t.add(call, lse);
-    } else {
-      t.add(call, args[7]);
-    }
-    const int32_t window = int32_of(args[9]);
-    const float scale = args[10] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(q.size(2))))
-                                            : float_of(args[10]);
-    const kda_status s = without_gil([&] {
-      return lib.attention(t.p[0], t.p[1], t.p[2], t.p[3], t.p[4], t.p[5], window, scale, t.p[6], t.p[7], call.stream);
-    });
-    if (s != KDA_OK) return PyLong_FromLong(s);
-    PyObject* o = result(args[6], out);
-    if (!both || o == nullptr) return o;
-    PyObject* e = result(args[7], lse);
-    PyObject* pair = e != nullptr ? PyTuple_Pack(2, o, e) : nullptr;
-    Py_DECREF(o);
-    Py_XDECREF(e);
-    return pair;
+    return attend(args, nullptr, nullptr, args[5], args[6], args[7], truth_of(args[8]), int32_of(args[9]), args[10]);
+  });
+}
+
+// prefix_attention(q, k_pages, v_pages, page_table, seq_lens, group_starts, prefix_lens, workspace, out, lse, return_lse,
+// window, scale or None)
+PyObject* prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need_arity("prefix_attention", n, 13);
+    return attend(args, args[5], args[6], args[7], args[8], args[9], truth_of(args[10]), int32_of(args[11]), args[12]);
   });
 }
 
@@ -468,10 +492,11 @@ PyObject* describe_bytes(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// bind(addresses of rope_append, attention, attention_workspace, beam, beam_workspace, move, page_assign, rope_axes)
+// bind(addresses of rope_append, attention, attention_workspace, beam, beam_workspace, move, page_assign, rope_axes,
+// prefix, prefix_workspace)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    constexpr Py_ssize_t COUNT = 8;
+    constexpr Py_ssize_t COUNT = 10;
     need_arity("bind", n, COUNT);
     void* address[COUNT];
     for (Py_ssize_t i = 0; i < COUNT; ++i) {
@@ -489,6 +514,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     lib.move = reinterpret_cast<decltype(lib.move)>(address[5]);
     lib.page_assign = reinterpret_cast<decltype(lib.page_assign)>(address[6]);
     lib.rope_axes = reinterpret_cast<decltype(lib.rope_axes)>(address[7]);
+    lib.prefix = reinterpret_cast<decltype(lib.prefix)>(address[8]);
+    lib.prefix_workspace = reinterpret_cast<decltype(lib.prefix_workspace)>(address[9]);
     Py_RETURN_NONE;
   });
 }
@@ -502,6 +529,7 @@ PyMethodDef methods[] = {{"rope_append", fast(rope_append), METH_FASTCALL, nullp
                          {"move", fast(move), METH_FASTCALL, nullptr},
                          {"rope_axes_append", fast(rope_axes_append), METH_FASTCALL, nullptr},
                          {"page_assign", fast(page_assign), METH_FASTCALL, nullptr},
+                         {"prefix_attention", fast(prefix_attention), METH_FASTCALL, nullptr},
                          {"describe", fast(describe_bytes), METH_FASTCALL, nullptr},
                          {"bind", fast(bind), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -41,21 +41,6 @@ constexpr int kThreads = 128;
 // 1536 rows 8.4 and 9.9 / 26.6 and 40.2, 23119 rows 86 and 99 us.
 constexpr int kManyRows = 320;
 
-// Index of the sequence owning `row`: the number of entries of cu[1..N] that
-// are <= row, by a 32-way search of the whole warp (N <= 32: one load).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int row, int lane) {
-  int lo = 0, hi = N;
-  while (hi > lo) {
-    const int step = (hi - lo + 31) / 32;
-    const int64_t p = lo + (int64_t)(lane + 1) * step - 1;
-    const bool le = p < hi && __ldg(cu + 1 + p) <= row;
-    const int c = __popc(__ballot_sync(0xffffffffu, le));
-    lo += c * step;
-    hi = min(hi, lo + step - 1);
-  }
-  return lo;
-}
-
 // VEC elements as loaded, as floats, and rounded to nearest even for the store.
 template <typename T, int VEC>
 struct Vec;

@@ -113,26 +113,6 @@ constexpr uint32_t IDS = tc::idesc_bf16(128, 128, false, true);
 
 __device__ __forceinline__ void record_mma_error() { atomicOr(&g_kda_mma_error, 8u); }
 
-// Waits for the phase of `bar` with the given parity.  Each try may suspend
-// the thread for up to 0.2 ms (it wakes as soon as the phase completes), so
-// waiting warps take no issue slots from the working ones; false after
-// kWaitNs in total.
-__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_ns();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(200000u)
-        : "memory");
-    if (done) return true;
-    if (global_ns() - t0 > kWaitNs) return false;
-  }
-}
-
 // Shared -> global TMA tensor store (bulk-group completion).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
