@@ -59,23 +59,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// The same, but each try may suspend the thread for up to 0.2 ms (it wakes as
-// soon as the phase completes), so waiting warps take no issue slots from the
-// working ones; false after kWaitNs in total.
+// A try that may suspend the thread for up to 0.2 ms (it wakes as soon as the
+// phase completes), so that waiting warps take no issue slots from working ones.
+__device__ __forceinline__ bool mbar_sleep_try(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(200000u)
+      : "memory");
+  return done != 0;
+}
+
+// Waits by such tries; false after kWaitNs.  The clock is read only where the
+// first try gave up: reading it takes longer than most waits.
 __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_sleep_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(200000u)
-        : "memory");
-    if (done) return true;
+  while (!mbar_sleep_try(bar, parity)) {
     if (global_ns() - t0 > kWaitNs) return false;
   }
+  return true;
 }
 
 // Global -> shared bulk copy completing `bytes` of transaction on `bar`.
@@ -103,6 +109,11 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 
 // Waits until the committed bulk stores are complete.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Arrives on `bar`, of this thread's share of its count, when the thread's cp.async copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 
 // Orders earlier shared-memory accesses of this thread before later async-proxy operations.
 __device__ __forceinline__ void fence_proxy_async_smem() {

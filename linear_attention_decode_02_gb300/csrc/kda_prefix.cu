@@ -16,21 +16,24 @@
 // to the row's own place, later parts to a place of their piece.
 //
 // Roles of a CTA:
-//   warps 0 .. 4 RT - 1   softmax: thread = row of its 128-row tile
+//   warps 0 .. 4 W - 1    softmax, a group of four for each of W lanes: thread = row
 //   the next warp         allocates tensor memory, issues the matrix products
 //   the last four         copy queries, keys and values into shared memory
-// S = Q K^T (128 rows x KT positions, float32, tensor memory) is read by the row's
-// thread, which puts the weights back over it as the next product's left operand,
-// in two bfloat16 pieces, p = hi + lo to 2^-17, for 32 positions at a time 16
-// columns of hi and 16 of lo.  O += P V accumulates in tensor memory; it is rescaled
-// only when a row's maximum rises by more than 2^kSlack, so weights may pass 1.
-// One row tile has two buffers of S, so that the product of the next tile runs
-// under this one's softmax; two row tiles share every key and value, and each
-// one's softmax runs under the other's products.
+// A lane is a buffer of scores S (128 rows x KT positions, float32), an output O
+// and the warps between them.  With two row tiles each lane is one of them and both
+// use every tile of keys and values; with one they take the tiles in turn, each to
+// an output and statistics of its own, which are joined at the unit's end.  Either
+// way one lane's softmax runs under the other's products.  256 channels leave room
+// for one output: its softmax takes both buffers in turn.
+// The row's thread puts the weights back over S as the next product's left operand,
+// in two bfloat16 pieces, p = hi + lo to 2^-16, for 16 positions at a time 8 columns
+// of hi and 8 of lo.  It reads S twice, for the row's maximum and for the weights,
+// which are taken relative to a reference that follows the maximum only when that
+// has passed it by 2^kSlack: O, which lies in tensor memory, is seldom rescaled.
 //
 // A barrier's parity tells two phases apart, so each is waited for, or known to be
-// over, before the next: with one row tile S of tile j is issued behind the
-// product of tile j - 2, and tile j's barriers are those of its buffer.
+// over, before the next: S of a buffer is issued behind the product of the weights
+// that were in it, so a lane's O is at rest while its warps work on new scores.
 //
 // Every mbarrier wait is bounded in time: a role whose wait runs out records a bit
 // in the error word, raises the CTA's abort flag and leaves its loop; all meet at
@@ -60,13 +63,14 @@ struct PrefixShape {
   static constexpr int QSLOTS = RT == 1 && D < 256 ? 2 : 1;
   static constexpr int HALF = BLOCKS * KT * 128;   // keys or values of a tile
   static constexpr int SLOTS = D == 64 ? 12 : 5;
-  static constexpr int LAG = D == 64 ? 4 : 2;      // halves in flight behind the one being issued
   static constexpr int BYTES = QSLOTS * RT * Q_TILE + SLOTS * HALF + 1024;
-  static constexpr int THREADS = (4 * RT + 1) * 32 + kLoaders;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * KT;   // two buffers of S, then O of each row tile
+  static constexpr int LANES = D == 256 ? 1 : 2;
+  static constexpr bool SPLIT = RT < LANES;        // lanes take tiles in turn
+  static constexpr int THREADS = (4 * LANES + 1) * 32 + kLoaders;
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * KT;   // two buffers of S, then O of each lane
   static constexpr uint32_t COLS = 512;
-  static_assert(O_COL + RT * D <= COLS, "tensor memory");
-  static_assert(LAG < SLOTS && SLOTS / 2 + 4 <= kLiveDepth, "ring");
+  static_assert(O_COL + LANES * D <= COLS && RT <= LANES, "tensor memory");
+  static_assert(SLOTS / 2 + 4 <= kLiveDepth, "ring");
 };
 
 struct PrefixWork {
@@ -137,11 +141,23 @@ struct PrefixWalk {
   __device__ __forceinline__ int rows_left() const { return group.rows - row_tile * ROWS; }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Scores of 32 positions, those not attended to set to minus infinity.
+__device__ __forceinline__ void masked(uint32_t (&x)[32], uint32_t live) {
+  if (live == 0xffffffffu) return;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = live >> i & 1 ? x[i] : 0xff800000u;
+}
+
 template <int D, int RT>
 __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     kda_prefix_kernel(const __grid_constant__ PrefixArgs a, const PrefixWork ws) {
   using P = PrefixShape<D, RT>;
-  constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, WARPS = P::THREADS / 32;
+  constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, LANES = P::LANES, WARPS = P::THREADS / 32;
   using Walker = PrefixWalk<KT, ROWS>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -149,7 +165,8 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   unsigned char* const s_q = sm;
   unsigned char* const s_ring = sm + P::QSLOTS * RT * P::Q_TILE;
   __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], o_done[2], q_empty[P::QSLOTS], live_full[kLiveDepth],
-      drained;
+      x_full, x_empty, drained;
+  __shared__ float2 s_ml[P::SPLIT ? kRows : 1];
   __shared__ uint32_t s_live[kLiveDepth][KT / 32];
   __shared__ uint32_t s_taddr;
   __shared__ volatile int s_abort;
@@ -166,16 +183,18 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kRows);
+      mbar_init(&p_full[i], kRows / 32);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < P::QSLOTS; ++i) mbar_init(&q_empty[i], 1);
     for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live_full[i], kLoaders / 32);
+    mbar_init(&x_full, kRows);
+    mbar_init(&x_empty, kRows);
     mbar_init(&drained, 1);
     s_abort = 0;
     mbar_fence_init();
   }
-  if (warp == 4 * RT) tc::alloc(&s_taddr, P::COLS);
+  if (warp == 4 * LANES) tc::alloc(&s_taddr, P::COLS);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -222,7 +241,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   }
   __syncthreads();
 
+  // Nearly every wait ends with its first try, which looks at nothing else.
   auto wait_or_abort = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_sleep_try(bar, parity))) return true;
     const bool stopped = s_abort;  // by another role
     const bool ok = !stopped && mbar_sleep_wait(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
@@ -236,9 +257,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   Walker walk;
   if (any) walk.start(a, start, s_g, s_before);
 
-  if (warp < 4 * RT) {
+  if (warp < 4 * LANES) {
     // ---------------- which sequences take part, and softmax ----------------
-    for (int n = c * 4 * RT + warp; n < at.N; n += C * 4 * RT) {
+    for (int n = c * 4 * LANES + warp; n < at.N; n += C * 4 * LANES) {
       const int g = find_sequence(a.starts, a.G, n, lane);
       bool part = false;
       int prefix = 0;
@@ -250,200 +271,250 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       if (!part)
         for (int h = lane; h < at.Hq; h += 32) ws.note[(int64_t)n * at.Hq + h] = first_note(-INFINITY, 0.f, 0, 0, 0);
     }
-    const int r = RT == 1 ? 0 : warp >> 2;   // row tile
-    const int row = (warp & 3) * 32 + lane;  // of the tile, and tensor-memory lane
+    const int me = LANES == 1 ? 0 : warp >> 2;   // lane of the CTA
+    const int row_tile = RT == 1 ? 0 : me;
+    const int row = (warp & 3) * 32 + lane;      // of the row tile, and tensor-memory lane
     const uint32_t tl = taddr + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t o_addr = tl + P::O_COL + r * D;
-    int job = 0;  // tiles so far
+    const uint32_t o_addr = tl + P::O_COL + me * D;
+    int tile = 0, job = 0, unit = 0;  // tiles of the piece, this lane's tiles and units so far
     bool run = any;
     while (run && walk.tile < stop) {
-      const int valid = walk.rows_left() - r * kRows;    // rows of this tile that exist
-      const bool idle = valid <= (warp & 3) * 32;        // none of this warp's
+      const int valid = walk.rows_left() - row_tile * kRows;  // rows of this tile that exist
+      const bool idle = valid <= (warp & 3) * 32;             // none of this warp's
       float m = -INFINITY, l = 0.f;
       const int64_t end = min(walk.unit_end, stop);
+      const int count = (int)(end - walk.tile);
       const bool begins = walk.unit_start >= start;
-      for (bool first = true; walk.tile < end; ++walk.tile, ++job, first = false) {
-        const int b = RT == 1 ? job & 1 : r;
-        const uint32_t phase = RT == 1 ? (job >> 1) & 1 : job & 1;
-        if (!wait_or_abort(&s_full[b], phase) ||
-            !wait_or_abort(&live_full[job % kLiveDepth], (job / kLiveDepth) & 1)) { run = false; break; }
+      for (int j = P::SPLIT ? me : 0; j < count; j += P::SPLIT ? 2 : 1, ++job) {
+        const int b = LANES == 1 ? job & 1 : me, at_mask = (tile + j) % kLiveDepth;
+        const uint32_t phase = LANES == 1 ? (job >> 1) & 1 : job & 1;
+        const bool first = j < (P::SPLIT ? 2 : 1);  // O holds nothing yet
+        if (!wait_or_abort(&s_full[b], phase) || !wait_or_abort(&live_full[at_mask], ((tile + j) / kLiveDepth) & 1)) {
+          run = false;
+          break;
+        }
         tc::fence_after_sync();
         if (!idle) {
           const uint32_t s_addr = tl + P::S_COL + b * KT;
-          const uint32_t* live = s_live[job % kLiveDepth];
-          float top = -INFINITY;
-#pragma unroll 1
+          // The maximum first, for all positions: 128 columns of S pass through 64 registers.
+          uint32_t s[2][32];
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tc::ld32_async(s_addr, s[0]);
+#pragma unroll
           for (int k = 0; k < KT / 32; ++k) {
-            float s[32];
-            tc::ld32(s_addr + 32 * k, s);
-            const uint32_t word = live[k];
-            if (word == 0xffffffffu) {
+            tc::ld_wait(s[k & 1]);
+            tc::ld32_async(s_addr + (k + 1 < KT / 32 ? 32 * (k + 1) : 0), s[(k + 1) & 1]);  // the first again at the end
+            masked(s[k & 1], s_live[at_mask][k]);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
-            } else {
+            for (int i = 0; i < 32; i += 8)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, word >> i & 1 ? s[i] : -INFINITY);
-            }
+              for (int e = 0; e < 4; ++e)
+                top[e] = max3(top[e], __uint_as_float(s[k & 1][i + 2 * e]), __uint_as_float(s[k & 1][i + 2 * e + 1]));
           }
-          top *= at.scale_log2;
-          const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
+          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * at.scale_log2;
+          const bool rises = most > m + kSlack || (m == -INFINITY && most > m);
           if (__any_sync(0xffffffffu, rises)) {
-            const float to = rises ? top : m;
-            const float fall = m == -INFINITY ? 0.f : ex2(m - to);
-            m = to;
+            const float fall = rises ? (m == -INFINITY ? 0.f : ex2(m - most)) : 1.f;
+            if (rises) m = most;
             l *= fall;
             if (!first) {
-              // with one row tile the last tile's product may still run (with two it came before this S)
-              if (RT == 1 && !wait_or_abort(&o_done[(job - 1) & 1], ((job - 1) >> 1) & 1)) { run = false; break; }
+              // with one lane the last tile's product may still run
+              if (LANES == 1 && !wait_or_abort(&o_done[(job - 1) & 1], ((job - 1) >> 1) & 1)) { run = false; break; }
               tc::fence_after_sync();
 #pragma unroll 1
-              for (int k = 0; k < D / 32; ++k) {
-                float o[32];
-                tc::ld32(o_addr + 32 * k, o);
+              for (int i = 0; i < D; i += 16) {
+                float o[16];
+                tc::ld16(o_addr + i, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = fall == 0.f ? 0.f : o[i] * fall;
-                tc::st32(o_addr + 32 * k, o);
+                for (int e = 0; e < 16; ++e) o[e] = fall == 0.f ? 0.f : o[e] * fall;
+                tc::st16(o_addr + i, o);
               }
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
+          const float2 scale2 = dup2(at.scale_log2), ref2 = dup2(-ref), minus2 = dup2(-1.f);
+          float2 sum[4] = {dup2(0.f), dup2(0.f), dup2(0.f), dup2(0.f)};
+#pragma unroll
           for (int k = 0; k < KT / 32; ++k) {
-            float s[32];
-            tc::ld32(s_addr + 32 * k, s);
-            const uint32_t word = live[k];
+            uint32_t(&x)[32] = s[(k + KT / 32) & 1];
+            tc::ld_wait(x);
+            if (k + 1 < KT / 32) tc::ld32_async(s_addr + 32 * (k + 1), s[(k + 1 + KT / 32) & 1]);
+            masked(x, s_live[at_mask][k]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = ex2(fmaf(s[i], at.scale_log2, -ref));
-            if (word != 0xffffffffu) {
+            for (int h = 0; h < 32; h += 16) {
+              uint32_t w[16];  // 8 columns of hi, 8 of lo
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = word >> i & 1 ? s[i] : 0.f;
+              for (int i = 0; i < 8; ++i) {
+                const float2 y =
+                    fma2(make_float2(__uint_as_float(x[h + 2 * i]), __uint_as_float(x[h + 2 * i + 1])), scale2, ref2);
+                const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                // hi is the upper half of the float32, cut off; lo what is left, rounded
+                const uint32_t u = __float_as_uint(p.x), v = __float_as_uint(p.y);
+                w[i] = __byte_perm(u, v, 0x7632);
+                const float2 rest =
+                    fma2(make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), minus2, p);
+                w[8 + i] = pack_bf2(rest.x, rest.y);
+              }
+              tc::st16_async(s_addr + 32 * k + h, w);
             }
-            float w[32];  // 16 columns of hi, 16 of lo
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              sum[i & 3] += s[2 * i] + s[2 * i + 1];
-              const uint32_t hi = pack_bf2(s[2 * i], s[2 * i + 1]);
-              w[i] = __uint_as_float(hi);
-              w[16 + i] = __uint_as_float(pack_bf2(s[2 * i] - bf_lo(hi), s[2 * i + 1] - bf_hi(hi)));
-            }
-            tc::st32(s_addr + 32 * k, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::st_wait();
+          const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          l += all.x + all.y;
         }
+        // The other lane's warps have read this one's last output.
+        if (P::SPLIT && me == 1 && j < 2 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
         tc::fence_before_sync();
-        mbar_arrive(&p_full[b]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
       }
       if (!run) break;
       // The unit's end in this piece: its rows' statistics and outputs.
-      if (!wait_or_abort(&o_done[RT == 1 ? (job - 1) & 1 : r], RT == 1 ? ((job - 1) >> 1) & 1 : (job - 1) & 1)) {
+      const int last = job - 1;
+      if ((!P::SPLIT || me < count) &&
+          !wait_or_abort(&o_done[LANES == 1 ? last & 1 : me], LANES == 1 ? (last >> 1) & 1 : last & 1)) {
         run = false;
         break;
       }
       tc::fence_after_sync();
-      if (!idle) {
-        const int i = walk.row_tile * ROWS + r * kRows + row;  // query row
-        const int n = walk.group.first + i / G;
-        const bool mine = row < valid && takes_part(at, n, walk.group.prefix);
-        float* dst = nullptr;
-        if (mine) {
-          const int64_t head = (int64_t)n * at.Hq + walk.head * G + i % G;
-          if (begins) {
-            ws.note[head] = first_note(m, l, c, (int)piece_of(walk.unit_end - 1, T, pieces) - c, r * kRows + row);
-            dst = ws.o + head * D;
-          } else {
-            const int64_t at_piece = (int64_t)c * ROWS + r * kRows + row;
-            ws.ml[at_piece] = make_float2(m, l);
-            dst = ws.more + at_piece * D;
-          }
+      if (P::SPLIT && me == 1) {
+        if (count < 2 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
+        s_ml[row] = make_float2(m, l);
+        tc::fence_before_sync();
+        mbar_arrive(&x_full);
+      } else {
+        float other_scale = 0.f, scale = 1.f;
+        if constexpr (P::SPLIT) {
+          if (!wait_or_abort(&x_full, unit & 1)) { run = false; break; }
+          tc::fence_after_sync();
+          const float2 other = s_ml[row];
+          const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+          scale = exp2f(m - ref);
+          other_scale = exp2f(other.x - ref);
+          l = fmaf(l, scale, other.y == 0.f ? 0.f : other.y * other_scale);
+          m = top;
         }
-#pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-          tc::ld32(o_addr + 32 * k, o);
+        if (!idle) {
+          const int i = walk.row_tile * ROWS + row_tile * kRows + row;  // query row
+          const int n = walk.group.first + i / G;
+          const bool mine = row < valid && takes_part(at, n, walk.group.prefix);
+          float* dst = nullptr;
           if (mine) {
+            const int64_t head = (int64_t)n * at.Hq + walk.head * G + i % G;
+            if (begins) {
+              ws.note[head] =
+                  first_note(m, l, c, (int)piece_of(walk.unit_end - 1, T, pieces) - c, row_tile * kRows + row);
+              dst = ws.o + head * D;
+            } else {
+              const int64_t at_piece = (int64_t)c * ROWS + row_tile * kRows + row;
+              ws.ml[at_piece] = make_float2(m, l);
+              dst = ws.more + at_piece * D;
+            }
+          }
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            float o[32];
+            tc::ld32(o_addr + 32 * k, o);
+            if constexpr (P::SPLIT) {
+              if (count > 1) {
+                float x[32];
+                tc::ld32(o_addr + D + 32 * k, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              reinterpret_cast<float4*>(dst + 32 * k)[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                for (int e = 0; e < 32; ++e) o[e] = fmaf(o[e], scale, x[e] * other_scale);
+              }
+            }
+            if (mine) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                reinterpret_cast<float4*>(dst + 32 * k)[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
           }
         }
+        tc::fence_before_sync();
+        if (P::SPLIT) mbar_arrive(&x_empty);
       }
-      tc::fence_before_sync();
+      tile += count;
+      ++unit;
+      walk.tile = end;
       walk.next_unit(a);
     }
-  } else if (warp == 4 * RT) {
+  } else if (warp == 4 * LANES) {
     // ---------------- matrix products ----------------
     constexpr uint32_t ID_S = tc::idesc_bf16(kRows, KT, false, false), ID_O = tc::idesc_bf16(kRows, D, false, true);
     const uint32_t q_addr = smem_addr(s_q), ring = smem_addr(s_ring);
-    int half = 0;  // of the next K; its V is the one after it
-    int job = 0, unit = 0;
+    int half = 0;           // of the next K; its V is the one after it
+    int unit = 0;
+    uint32_t weighed = 0;  // parity of the outputs issued from each buffer
     bool run = any;
-    const auto slot_wait = [&](int h) { return wait_or_abort(&full[h % SLOTS], (h / SLOTS) & 1); };
-    const auto scores = [&](int q_slot, int r, int b, int h) {  // S of row tile r into buffer b from the keys in half h
-      if (lane == 0) {
-        tc::fence_after_sync();
-        const uint32_t q = q_addr + (q_slot * RT + r) * P::Q_TILE, k = ring + (h % SLOTS) * P::HALF;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16(taddr + P::S_COL + b * KT, tc::desc_sw128(q + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024),
-                       tc::desc_sw128(k + (ks >> 2) * (KT * 128) + (ks & 3) * 32, 16, 1024), ID_S, ks > 0);
-        tc::commit(&s_full[b]);
-      }
+    // A half that has landed; the tensor cores read it through another proxy than the copies wrote it.
+    const auto slot_wait = [&](int h) {
+      const bool ok = wait_or_abort(&full[h % SLOTS], (h / SLOTS) & 1);
+      fence_proxy_async_smem();
+      return ok;
     };
-    const auto outputs = [&](int r, int b, int h, bool first) {  // O of row tile r += weights in buffer b times half h
-      if (lane == 0) {
-        tc::fence_after_sync();
-        const uint32_t v = ring + (h % SLOTS) * P::HALF, p = taddr + P::S_COL + b * KT;
+    const uint32_t issue = tc::elect();
+    const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    // S of row tile r into buffer b from the keys in half h.
+    const auto scores = [&](int q_slot, int r, int b, int h) {
+      tc::fence_after_sync();
+      const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + r) * P::Q_TILE, 16, 1024);
+      const uint64_t k = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, 16, 1024);
+      const int buffer = uniform(b);
 #pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
+      for (int ks = 0; ks < D / 16; ++ks)  // descriptors count in 16 bytes
+        tc::mma_bf16_by(issue, taddr + P::S_COL + buffer * KT, q + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
+                        k + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, ID_S, ks > 0);
+      tc::commit_by(issue, &s_full[buffer]);
+    };
+    // Waits for the weights in buffer b; the output of lane o += them times the values in half h.
+    const auto outputs = [&](int o, int b, int h, bool first) -> bool {
+      const int buffer = uniform(b);
+      if (!wait_or_abort(&p_full[buffer], weighed >> buffer & 1)) return false;
+      weighed ^= 1u << buffer;
+      tc::fence_after_sync();
+      const uint64_t v = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, KT * 128, 1024);
+      const uint32_t p = taddr + P::S_COL + buffer * KT, d = taddr + P::O_COL + uniform(o) * D;
+      const bool onto = uniform(!first);
 #pragma unroll
-          for (int piece = 0; piece < 2; ++piece)
-            tc::mma_bf16_ta(taddr + P::O_COL + r * D, p + (ks >> 1) * 32 + piece * 16 + (ks & 1) * 8,
-                            tc::desc_sw128(v + ks * 2048, KT * 128, 1024), ID_O, !(first && ks == 0 && piece == 0));
-        tc::commit(&o_done[b]);
-      }
+      for (int ks = 0; ks < KT / 16; ++ks)
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece)
+          tc::mma_bf16_ta_by(issue, d, p + ks * 16 + piece * 8, v + ks * 2048 / 16, ID_O, onto || ks > 0 || piece > 0);
+      tc::commit_by(issue, &o_done[buffer]);
+      return true;
     };
-    const auto release = [&](uint64_t* bar) {
-      if (lane == 0) tc::commit(bar);
-      __syncwarp();
-    };
+    const auto release = [&](uint64_t* bar) { tc::commit_by(issue, bar); };
+    int job = 0;
     while (run && walk.tile < stop) {
       const int count = (int)(min(walk.unit_end, stop) - walk.tile);
       const int q_slot = unit % P::QSLOTS;
-      if constexpr (RT == 1) {
-        for (int j = 0; j <= count; ++j) {  // the products of tile j with its keys, of tile j - 1 with its values
+      // the products of tile j with its keys, of tile j - 1 with its values
+      for (int j = 0; j <= count && run; ++j) {
+        const int hk = half + 2 * j, hv = hk - 1;
+        if (j < count && !slot_wait(hk)) { run = false; break; }
+        if constexpr (RT == 1) {
+          const int b = P::SPLIT ? j & 1 : (job + j) & 1;
           if (j < count) {
-            const int h = half + 2 * j;
-            if (!slot_wait(h)) { run = false; break; }
-            scores(q_slot, 0, (job + j) & 1, h);
-            release(&empty[h % SLOTS]);
-            if (j == count - 1) release(&q_empty[q_slot]);
+            scores(q_slot, 0, b, hk);
+            release(&empty[uniform(hk % SLOTS)]);
           }
           if (j > 0) {
-            const int h = half + 2 * j - 1, b = (job + j - 1) & 1;
-            if (!slot_wait(h) || !wait_or_abort(&p_full[b], ((job + j - 1) >> 1) & 1)) { run = false; break; }
-            outputs(0, b, h, j == 1);
-            release(&empty[h % SLOTS]);
+            if (!slot_wait(hv) || !outputs(P::SPLIT ? b ^ 1 : 0, b ^ 1, hv, j <= (P::SPLIT ? 2 : 1))) { run = false; break; }
+            release(&empty[uniform(hv % SLOTS)]);
           }
-        }
-      } else {
-        for (int j = 0; j <= count; ++j) {
-          const int hk = half + 2 * j, hv = hk - 1;
-          if (j < count && !slot_wait(hk)) { run = false; break; }
+        } else {
           if (j > 0 && !slot_wait(hv)) { run = false; break; }
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            if (j > 0) {
-              if (!wait_or_abort(&p_full[r], (job + j - 1) & 1)) { run = false; break; }
-              outputs(r, r, hv, j == 1);
-            }
-            if (j < count) scores(q_slot, r, r, hk);
+            if (j > 0 && run && !outputs(r, r, hv, j == 1)) run = false;
+            if (r == RT - 1 && j > 0 && run) release(&empty[uniform(hv % SLOTS)]);
+            if (j < count && run) scores(q_slot, r, r, hk);
           }
           if (!run) break;
-          if (j > 0) release(&empty[hv % SLOTS]);
-          if (j < count) release(&empty[hk % SLOTS]);
-          if (j == count - 1) release(&q_empty[q_slot]);
+          if (j < count) release(&empty[uniform(hk % SLOTS)]);
         }
+        if (j == count - 1) release(&q_empty[uniform(q_slot)]);
       }
       half += 2 * count;
       job += count;
@@ -459,7 +530,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     constexpr int WARP_ROWS = KT / 4;                // keys of a warp
     constexpr int STEP_ROWS = 32 / CHUNKS;           // keys of one instruction
     static_assert(CHUNKS <= 32 && WARP_ROWS <= 32, "a row or more an instruction, a key or less a lane");
-    const int lw = warp - (4 * RT + 1);
+    const int lw = warp - (4 * LANES + 1);
     const int chunk = lane % CHUNKS, sub = lane / CHUNKS;
     const uint32_t ring = smem_addr(s_ring), q_addr = smem_addr(s_q);
     const auto place = [](int row, int ch, int rows) {  // of a 16-byte piece in an operand of `rows` rows
@@ -468,32 +539,24 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     // This lane's key of a tile: found a tile ahead of its copy.
     Walker ahead = walk;
     struct Look {
-      int64_t k, v;  // element offsets
-      bool live;
+      int page, token, head;  // page 0: none
     };
     const auto look_up = [&]() {
-      Look l{0, 0, false};
+      Look l{0, 0, 0};
       if (ahead.tile < stop) {
         const int t = (int)(ahead.tile - ahead.unit_start) * KT + lw * WARP_ROWS + lane;
         if (lane < WARP_ROWS && t < ahead.group.prefix) {
-          const int col = t / at.page_size, token = t - col * at.page_size;
-          const int page = __ldg(at.table + (int64_t)ahead.group.first * at.table_rs + col);
-          if (page > 0 && page < at.num_pages) {
-            l.k = page * at.kp.page + token * at.kp.token + ahead.head * at.kp.head;
-            l.v = page * at.vp.page + token * at.vp.token + ahead.head * at.vp.head;
-            l.live = true;
-          }
+          const int col = t / at.page_size;
+          l.token = t - col * at.page_size;
+          l.page = __ldg(at.table + (int64_t)ahead.group.first * at.table_rs + col);
         }
+        l.head = ahead.head;
         if (++ahead.tile == ahead.unit_end) ahead.next_unit(a);
       }
       return l;
     };
-    int half = 0, done = 0, tile = 0, unit = 0;
+    int half = 0, tile = 0, unit = 0;
     bool run = any;
-    const auto signal = [&](int upto) {  // halves before `upto` have arrived, as far as this thread copied them
-      fence_proxy_async_smem();
-      for (; done < upto; ++done) mbar_arrive(&full[done % SLOTS]);
-    };
     const auto copy_half = [&](const void* data, int64_t offset, uint32_t mask) {
       const uint32_t base = ring + (half % SLOTS) * P::HALF;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(data);
@@ -503,30 +566,19 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         const int64_t from = __shfl_sync(0xffffffffu, offset, k);
         copy16(base + place(lw * WARP_ROWS + k, chunk, KT), src + from + chunk * 8, mask >> k & 1);
       }
-      copy_commit();
+      copy_arrive(&full[half % SLOTS]);
       ++half;
-      if (half > P::LAG) {
-        copy_wait<P::LAG>();
-        signal(half - P::LAG);
-      }
     };
-    Look look = any ? look_up() : Look{0, 0, false};
+    Look look = any ? look_up() : Look{0, 0, 0};
     while (run && walk.tile < stop) {
       const int64_t end = min(walk.unit_end, stop);
       const int q_slot = unit % P::QSLOTS;
       if (unit >= P::QSLOTS) {
-        // An earlier unit's last scores free the slot, and they may wait for halves not signalled yet.
-        const uint32_t parity = (unit / P::QSLOTS - 1) & 1;
-        if (!mbar_try_wait(&q_empty[q_slot], parity)) {
-          copy_wait<0>();
-          signal(half);
-        }
-        __syncwarp();
-        if (!wait_or_abort(&q_empty[q_slot], parity)) { run = false; break; }
+        if (!wait_or_abort(&q_empty[q_slot], (unit / P::QSLOTS - 1) & 1)) { run = false; break; }
       }
       {
         const int left = min(walk.rows_left(), ROWS), rows = (left + 31) & ~31;
-        for (int i = tid - (4 * RT + 1) * 32; i < rows * CHUNKS; i += kLoaders) {
+        for (int i = tid - (4 * LANES + 1) * 32; i < rows * CHUNKS; i += kLoaders) {
           const int row = i / CHUNKS, ch = i % CHUNKS;
           const int q = walk.row_tile * ROWS + row;
           const bool real = row < left;
@@ -538,7 +590,11 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       }
       for (; walk.tile < end; ++walk.tile, ++tile) {
         const Look next = look_up();
-        const uint32_t mask = __ballot_sync(0xffffffffu, look.live);
+        const bool live = look.page > 0 && look.page < at.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, live);
+        const auto offset = [&](const PageView& p) {
+          return live ? look.page * p.page + look.token * p.token + look.head * p.head : 0;
+        };
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
         if (WARP_ROWS == 32) {
           if (lane == 0) s_live[tile % kLiveDepth][lw] = mask;
@@ -546,22 +602,21 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           reinterpret_cast<uint16_t*>(s_live[tile % kLiveDepth])[lw] = (uint16_t)mask;
         }
         if (lane == 0) mbar_arrive(&live_full[tile % kLiveDepth]);
-        copy_half(at.kp.data, look.k, mask);
+        copy_half(at.kp.data, offset(at.kp), mask);
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
-        copy_half(at.vp.data, look.v, mask);
+        copy_half(at.vp.data, offset(at.vp), mask);
         look = next;
       }
       if (!run) break;
       ++unit;
       walk.next_unit(a);
     }
-    copy_wait<0>();
-    if (run) signal(half);
+    asm volatile("cp.async.wait_all;" ::: "memory");  // none lands when the CTA is gone
   }
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 4 * RT) {
+  if (warp == 4 * LANES) {
     tc::fence_after_sync();
     tc::dealloc(taddr, P::COLS);
   }

@@ -281,7 +281,7 @@ def test_infinite_scores():
     assert_rounded(lse[:, 0], ref_lse[:, 0], t_lse, "lse")
 
 
-@pytest.mark.parametrize("D,beams", [(64, 8), (128, 8), (128, 40), (256, 8)])
+@pytest.mark.parametrize("D,beams", [(64, 16), (128, 8), (128, 40), (256, 8)])
 def test_rounding_by_root_mean_square(D, beams):
     """As the paged kernel: a low part of the weights that is missing would double the mean square."""
     c = make([(3000, [50] * beams)], Hq=8, Hkv=1, D=D, page=64, seed=3)
