@@ -204,11 +204,9 @@ __device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
   return note;
 }
 
-// A result that another kernel joins: its row's maximum and sum, the piece that
-// made it and how many pieces after that one hold more of it, at row `row`.
-__device__ __forceinline__ float4 first_note(float m, float l, int piece, int more, int row) {
-  return make_float4(m, l, __int_as_float(piece), __int_as_float(more << 8 | row));
-}
+// What another kernel that joins a result needs: the piece that began it and how
+// many after that hold more of it, at row `row`.
+__device__ __forceinline__ int2 part_note(int piece, int more, int row) { return make_int2(piece, more << 8 | row); }
 
 // 16 bytes to shared memory; zeros where live is false (src is then not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {

@@ -39,7 +39,7 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = kAttendWarps, kThreads = 32 * kWarps;
 constexpr int kKeys = 16;  // positions of a stage
 static_assert(kWarps * kKeys == kTile, "a tile is one stage of every warp");
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <int D, int HG>
+template <int D, int HG, bool PARTS>
 __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
   using Copies = typename Shape<D, HG>::Copies;
   constexpr int STAGES = Shape<D, HG>::STAGES, ROW = Copies::ROW;
@@ -292,8 +292,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
       }
     }
 
-    finish_unit<D, HG, kWarps, RS>(a, walk, place, ws, reinterpret_cast<float*>(smem + kWarps * Copies::RING),
-                                   s_m[parity], s_l[parity], o, m, l, groups, warp, g, t4, c);
+    if constexpr (PARTS) {
+      leave_parts<D, HG, kWarps, RS>(a, walk, place, o, m, l, groups, warp, g, t4, c);
+    } else {
+      finish_unit<D, HG, kWarps, RS>(a, walk, place, ws, reinterpret_cast<float*>(smem + kWarps * Copies::RING),
+                                     s_m[parity], s_l[parity], o, m, l, groups, warp, g, t4, c);
+    }
     parity ^= 1;
     after.tile = walk.tile;
     walk = after;
@@ -301,13 +305,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   copy_wait<0>();
 }
 
-template <int D, int HG>
-cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+template <int D, int HG, bool PARTS>
+cudaError_t launch_parts(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D, HG>();
   static std::atomic<bool> set[64];
-  const cudaError_t e = allow_shared(kda_attend_mma_kernel<D, HG>, bytes, set);
+  const cudaError_t e = allow_shared(kda_attend_mma_kernel<D, HG, PARTS>, bytes, set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kda_attend_mma_kernel<D, HG>, dim3(p.ctas), dim3(kThreads), bytes, s, 1, a);
+  return launch_pdl(kda_attend_mma_kernel<D, HG, PARTS>, dim3(p.ctas), dim3(kThreads), bytes, s, 1, a);
+}
+template <int D, int HG>
+cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  return a.first_o != nullptr ? launch_parts<D, HG, true>(a, p, s) : launch_parts<D, HG, false>(a, p, s);
 }
 
 }  // namespace

@@ -13,8 +13,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Joins the warps of a block at a unit's end in its piece and writes the
-// result, or the piece's partial; under a shared prefix its result, or first
-// piece, goes to another kernel's join.  Lane (g, t4) holds channels 8 i + 2 t4 and + 1
+// result, or the piece's partial.  Lane (g, t4) holds channels 8 i + 2 t4 and + 1
 // of rows g (o[i][0], o[i][1]) and g + 8 (o[i][2], o[i][3]): two heads with HG =
 // 16, two parts of one head to be added with HG = 8.  m and l are the warp's
 // row maxima and this lane's sums.  shared_o: (WARPS - 1) * 8 * D floats; stats:
@@ -56,7 +55,6 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
   const bool whole = walk.unit_start >= place.start && walk.unit_end <= place.stop;
   const bool at_start = walk.unit_start <= place.start;
   const int64_t slot = 2 * (int64_t)c + (at_start ? 0 : 1);
-  const bool first = a.first_o != nullptr && walk.unit_start >= place.start;
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
     if (r > 0) __syncthreads();  // all have taken the first heads
@@ -90,19 +88,14 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
         x += v.x;
         y += v.y;
       }
-      if (first) {
-        *reinterpret_cast<float2*>(a.first_o + head * D + d) = make_float2(x, y);
-      } else if (whole) {
+      if (whole) {
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + d) = pack_bf2(x * scale, y * scale);
       } else {
         *reinterpret_cast<float2*>(ws.o_of(slot, h) + d) = make_float2(x, y);
       }
     }
     if (t4 == 0 && warp == 0) {
-      if (first) {
-        const int pieces = pieces_of(place.T, gridDim.x);
-        a.first_note[head] = first_note(M[r], L, c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
-      } else if (!whole) {
+      if (!whole) {
         ws.ml_of(slot, h)[0] = M[r];
         ws.ml_of(slot, h)[1] = L;
       } else if (a.lse != nullptr) {
@@ -111,6 +104,42 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
     }
   }
   if (threadIdx.x == 0 && at_start) ws.note[c] = note_of(walk, place);
+}
+
+// Leaves each warp's own part of a unit, and goes on, where another kernel joins
+// all parts: sequences' own positions are often few, and for the block to meet at the
+// end of each took as long as 150 of them.  Arguments as of finish_unit.
+template <int D, int HG, int WARPS, int RS>
+__device__ __forceinline__ void leave_parts(const AttendArgs& a, const Walk& walk, const Place& place,
+                                            float (&o)[D / 8][4], float (&m)[RS], float (&l)[RS], int groups, int warp,
+                                            int g, int t4, int c) {
+  constexpr bool PAIR = HG == 8;
+  const int G = a.Hq / a.Hkv, hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
+  const bool first = walk.unit_start >= place.start;
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    const int h = g + 8 * r;
+    if (h >= heads) continue;
+    const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
+    const int64_t at = first ? (int64_t)warp * a.N * a.Hq + head : ((int64_t)c * WARPS + warp) * HG + h;
+    float* to = (first ? a.first_o : a.more_o) + at * D + 2 * t4;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      *reinterpret_cast<float2*>(to + 8 * i) =
+          PAIR ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]) : make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    if (t4 == 0) {
+      (first ? a.first_ml : a.more_ml)[at] = make_float2(m[r], l[r]);
+      if (first && warp == 0) {
+        const int pieces = pieces_of(place.T, gridDim.x);
+        a.first_note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
+      }
+    }
+  }
 }
 
 }  // namespace kda

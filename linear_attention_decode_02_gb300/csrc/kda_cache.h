@@ -91,12 +91,14 @@ struct AttendArgs {
   int32_t window;                         // 0: all
   float scale_log2;                       // scale * log2(e)
   int32_t vec16;                          // q rows, key and value vectors start on 16-byte boundaries
-  // Under a shared prefix: the first positions of each sequence that are attended to elsewhere, and where a unit's
-  // result (or its first piece's) goes instead of out and lse, [N, Hq, D] and [N, Hq].  Null otherwise.
+  // Under a shared prefix: the first positions of each sequence that are attended to elsewhere, and where each warp's
+  // part of a unit goes instead of out and lse: of the piece that begins it, [kAttendWarps, N, Hq(, D)] with that piece
+  // and how many follow, [N, Hq]; of those that follow, [ctas, kAttendWarps, heads(, D)].  Null otherwise.
   const int32_t* skip;
-  float* first_o;
-  float4* first_note;
+  float* first_o; float2* first_ml; int2* first_note;
+  float* more_o; float2* more_ml;
 };
+constexpr int kAttendWarps = 4;  // of a block of the tensor-core kernel
 
 // Grid and workspace of the attention kernels: `ctas` workers that each may
 // leave two partial results of `heads` query heads.

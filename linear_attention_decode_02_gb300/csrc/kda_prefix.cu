@@ -17,7 +17,8 @@
 //
 // Roles of a CTA:
 //   warps 0 .. 4 W - 1    softmax, a group of four for each of W lanes: thread = row
-//   the next warp         allocates tensor memory, issues the matrix products
+//   the next W warps      issue a lane's matrix products each (one warp for both was
+//                         at work on issuing them for longer than they took)
 //   the last four         copy queries, keys and values into shared memory
 // A lane is a buffer of scores S (128 rows x KT positions, float32), an output O
 // and the warps between them.  With two row tiles each lane is one of them and both
@@ -27,9 +28,10 @@
 // for one output: its softmax takes both buffers in turn.
 // The row's thread puts the weights back over S as the next product's left operand,
 // in two bfloat16 pieces, p = hi + lo to 2^-16, for 16 positions at a time 8 columns
-// of hi and 8 of lo.  It reads S twice, for the row's maximum and for the weights,
-// which are taken relative to a reference that follows the maximum only when that
-// has passed it by 2^kSlack: O, which lies in tensor memory, is seldom rescaled.
+// of hi and 8 of lo.  It reads S once: weights are taken relative to a reference that
+// follows the row's maximum only where that has passed it by 2^kSlack, and then in
+// whole steps, so that weights of the tile that are written already move to it
+// exactly; O, which lies in tensor memory, is seldom rescaled.
 //
 // A barrier's parity tells two phases apart, so each is waited for, or known to be
 // over, before the next: S of a buffer is issued behind the product of the weights
@@ -41,6 +43,7 @@
 #include <algorithm>
 
 #include "kda_attend_rows.cuh"
+#include "kda_stream_common.cuh"
 #include "kda_tcgen05.cuh"
 
 namespace kda {
@@ -66,7 +69,8 @@ struct PrefixShape {
   static constexpr int BYTES = QSLOTS * RT * Q_TILE + SLOTS * HALF + 1024;
   static constexpr int LANES = D == 256 ? 1 : 2;
   static constexpr bool SPLIT = RT < LANES;        // lanes take tiles in turn
-  static constexpr int THREADS = (4 * LANES + 1) * 32 + kLoaders;
+  static constexpr int THREADS = LANES == 1 ? 9 * 32 : 16 * 32;
+  static constexpr int LOADER0 = LANES == 1 ? 5 : 8, PRODUCT0 = LANES == 1 ? 4 : 12;  // first warps of the roles
   static constexpr uint32_t S_COL = 0, O_COL = 2 * KT;   // two buffers of S, then O of each lane
   static constexpr uint32_t COLS = 512;
   static_assert(O_COL + LANES * D <= COLS && RT <= LANES, "tensor memory");
@@ -74,7 +78,8 @@ struct PrefixShape {
 };
 
 struct PrefixWork {
-  float4* note;   // [N * Hq]
+  int2* note;     // [N * Hq]
+  float2* first;  // [N * Hq]
   float* o;       // [N * Hq][D]
   float2* ml;     // [ctas][RT * 128]: continued units
   float* more;    // [ctas][RT * 128][D]
@@ -141,21 +146,30 @@ struct PrefixWalk {
   __device__ __forceinline__ int rows_left() const { return group.rows - row_tile * ROWS; }
 };
 
+// Registers of the four warps of a group: up to N, down to -N, 0: as they are.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  if constexpr (N > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(-N));
+}
+// A box of rows x 64 channels to shared memory, its 16-byte pieces swizzled over 128-byte rows.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_addr(bar))
+      : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Scores of 32 positions, those not attended to set to minus infinity.
-__device__ __forceinline__ void masked(uint32_t (&x)[32], uint32_t live) {
-  if (live == 0xffffffffu) return;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = live >> i & 1 ? x[i] : 0xff800000u;
-}
-
 template <int D, int RT>
 __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
-    kda_prefix_kernel(const __grid_constant__ PrefixArgs a, const PrefixWork ws) {
+    kda_prefix_kernel(const __grid_constant__ PrefixArgs a, const PrefixWork ws, int box,
+                      const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using P = PrefixShape<D, RT>;
   constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, LANES = P::LANES, WARPS = P::THREADS / 32;
   using Walker = PrefixWalk<KT, ROWS>;
@@ -165,9 +179,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   unsigned char* const s_q = sm;
   unsigned char* const s_ring = sm + P::QSLOTS * RT * P::Q_TILE;
   __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], o_done[2], q_empty[P::QSLOTS], live_full[kLiveDepth],
-      x_full, x_empty, drained;
+      x_full, x_empty, turn[2], drained[LANES];
   __shared__ float2 s_ml[P::SPLIT ? kRows : 1];
-  __shared__ uint32_t s_live[kLiveDepth][KT / 32];
+  __shared__ __align__(8) uint32_t s_live[kLiveDepth][KT / 32];
   __shared__ uint32_t s_taddr;
   __shared__ volatile int s_abort;
   __shared__ int64_t s_warp[WARPS], s_before;
@@ -179,22 +193,24 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], kLoaders);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], RT);  // the lanes that use a half
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kRows / 32);
       mbar_init(&o_done[i], 1);
     }
-    for (int i = 0; i < P::QSLOTS; ++i) mbar_init(&q_empty[i], 1);
+    for (int i = 0; i < P::QSLOTS; ++i) mbar_init(&q_empty[i], LANES);
     for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live_full[i], kLoaders / 32);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
     mbar_init(&x_full, kRows);
     mbar_init(&x_empty, kRows);
-    mbar_init(&drained, 1);
+    for (int i = 0; i < LANES; ++i) mbar_init(&drained[i], 1);
     s_abort = 0;
     mbar_fence_init();
   }
-  if (warp == 4 * LANES) tc::alloc(&s_taddr, P::COLS);
+  if (warp == P::PRODUCT0) tc::alloc(&s_taddr, P::COLS);
   pdl_wait();
   pdl_launch_dependents();
 
@@ -258,6 +274,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   if (any) walk.start(a, start, s_g, s_before);
 
   if (warp < 4 * LANES) {
+    more_registers<LANES == 1 ? 0 : 144>();
     // ---------------- which sequences take part, and softmax ----------------
     for (int n = c * 4 * LANES + warp; n < at.N; n += C * 4 * LANES) {
       const int g = find_sequence(a.starts, a.G, n, lane);
@@ -269,14 +286,17 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       }
       if (lane == 0) ws.skip[n] = part ? prefix : 0;
       if (!part)
-        for (int h = lane; h < at.Hq; h += 32) ws.note[(int64_t)n * at.Hq + h] = first_note(-INFINITY, 0.f, 0, 0, 0);
+        for (int h = lane; h < at.Hq; h += 32) {
+          ws.note[(int64_t)n * at.Hq + h] = part_note(0, 0, 0);
+          ws.first[(int64_t)n * at.Hq + h] = make_float2(-INFINITY, 0.f);
+        }
     }
     const int me = LANES == 1 ? 0 : warp >> 2;   // lane of the CTA
     const int row_tile = RT == 1 ? 0 : me;
     const int row = (warp & 3) * 32 + lane;      // of the row tile, and tensor-memory lane
     const uint32_t tl = taddr + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_addr = tl + P::O_COL + me * D;
-    int tile = 0, job = 0, unit = 0;  // tiles of the piece, this lane's tiles and units so far
+    int tile = 0, job = 0, unit = 0, ends = 0;  // tiles of the piece, this lane's tiles, units and its own of them so far
     bool run = any;
     while (run && walk.tile < stop) {
       const int valid = walk.rows_left() - row_tile * kRows;  // rows of this tile that exist
@@ -296,52 +316,74 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         tc::fence_after_sync();
         if (!idle) {
           const uint32_t s_addr = tl + P::S_COL + b * KT;
-          // The maximum first, for all positions: 128 columns of S pass through 64 registers.
-          uint32_t s[2][32];
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tc::ld32_async(s_addr, s[0]);
+          const float2 scale2 = dup2(at.scale_log2), minus2 = dup2(-1.f);
+          float2 sum[4] = {dup2(0.f), dup2(0.f), dup2(0.f), dup2(0.f)};
+          // 64 positions from k on.
+          const auto weigh = [&](int k) -> bool {
+            uint32_t x[64];
+            tc::ld64_async(s_addr + k, x);
+            const uint2 word = *reinterpret_cast<const uint2*>(&s_live[at_mask][k / 32]);
+            tc::ld_wait(x);
+            if ((word.x & word.y) != 0xffffffffu) {
 #pragma unroll
-          for (int k = 0; k < KT / 32; ++k) {
-            tc::ld_wait(s[k & 1]);
-            tc::ld32_async(s_addr + (k + 1 < KT / 32 ? 32 * (k + 1) : 0), s[(k + 1) & 1]);  // the first again at the end
-            masked(s[k & 1], s_live[at_mask][k]);
+              for (int i = 0; i < 64; ++i) x[i] = (i < 32 ? word.x : word.y) >> (i & 31) & 1 ? x[i] : 0xff800000u;  // -infinity
+            }
+            float tops[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
+            for (int e = 0; e < 4; ++e) {
+              tops[e] = __uint_as_float(x[e]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                top[e] = max3(top[e], __uint_as_float(s[k & 1][i + 2 * e]), __uint_as_float(s[k & 1][i + 2 * e + 1]));
-          }
-          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * at.scale_log2;
-          const bool rises = most > m + kSlack || (m == -INFINITY && most > m);
-          if (__any_sync(0xffffffffu, rises)) {
-            const float fall = rises ? (m == -INFINITY ? 0.f : ex2(m - most)) : 1.f;
-            if (rises) m = most;
-            l *= fall;
-            if (!first) {
-              // with one lane the last tile's product may still run
-              if (LANES == 1 && !wait_or_abort(&o_done[(job - 1) & 1], ((job - 1) >> 1) & 1)) { run = false; break; }
-              tc::fence_after_sync();
+              for (int i = 4; i < 60; i += 8)
+                tops[e] = max3(tops[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
+              tops[e] = fmaxf(tops[e], __uint_as_float(x[60 + e]));
+            }
+            const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * at.scale_log2;
+            const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, rises)) {
+              // The reference rises by whole steps, so what is weighted already moves exactly.
+              float fall = 1.f;
+              if (rises && m == -INFINITY) {
+                m = top;
+                fall = 0.f;
+              } else if (rises) {
+                const float steps = ceilf(top - m);
+                m += steps;
+                fall = steps < 127.f ? __int_as_float((127 - (int)steps) << 23) : 0.f;
+              }
+              l *= fall;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], dup2(fall));
+              if (k > 0) {
+                tc::st_wait();
 #pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                float o[16];
-                tc::ld16(o_addr + i, o);
+                for (int i = 0; i < k; i += 16) {
+                  float w[16];
+                  tc::ld16(s_addr + i, w);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = fall == 0.f ? 0.f : o[e] * fall;
-                tc::st16(o_addr + i, o);
+                  for (int e = 0; e < 16; ++e) {
+                    const uint32_t u = __float_as_uint(w[e]);
+                    w[e] = __uint_as_float(pack_bf2(bf_lo(u) * fall, bf_hi(u) * fall));
+                  }
+                  tc::st16(s_addr + i, w);
+                }
+              }
+              if (!first) {
+                // with one lane the last tile's product may still run
+                if (LANES == 1 && !wait_or_abort(&o_done[(job - 1) & 1], ((job - 1) >> 1) & 1)) return false;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int i = 0; i < D; i += 16) {
+                  float o[16];
+                  tc::ld16(o_addr + i, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = fall == 0.f ? 0.f : o[e] * fall;
+                  tc::st16(o_addr + i, o);
+                }
               }
             }
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
-          const float2 scale2 = dup2(at.scale_log2), ref2 = dup2(-ref), minus2 = dup2(-1.f);
-          float2 sum[4] = {dup2(0.f), dup2(0.f), dup2(0.f), dup2(0.f)};
+            const float2 ref2 = dup2(m == -INFINITY ? 0.f : -m);
 #pragma unroll
-          for (int k = 0; k < KT / 32; ++k) {
-            uint32_t(&x)[32] = s[(k + KT / 32) & 1];
-            tc::ld_wait(x);
-            if (k + 1 < KT / 32) tc::ld32_async(s_addr + 32 * (k + 1), s[(k + 1 + KT / 32) & 1]);
-            masked(x, s_live[at_mask][k]);
-#pragma unroll
-            for (int h = 0; h < 32; h += 16) {
+            for (int h = 0; h < 64; h += 16) {
               uint32_t w[16];  // 8 columns of hi, 8 of lo
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -356,9 +398,13 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
                     fma2(make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), minus2, p);
                 w[8 + i] = pack_bf2(rest.x, rest.y);
               }
-              tc::st16_async(s_addr + 32 * k + h, w);
+              tc::st16_async(s_addr + k + h, w);
             }
-          }
+            return true;
+          };
+#pragma unroll 1
+          for (int k = 0; k < KT && run; k += 64) run = weigh(k);
+          if (!run) break;
           tc::st_wait();
           const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l += all.x + all.y;
@@ -371,11 +417,12 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       }
       if (!run) break;
       // The unit's end in this piece: its rows' statistics and outputs.
-      const int last = job - 1;
-      if ((!P::SPLIT || me < count) &&
-          !wait_or_abort(&o_done[LANES == 1 ? last & 1 : me], LANES == 1 ? (last >> 1) & 1 : last & 1)) {
-        run = false;
-        break;
+      if (!P::SPLIT || me < count) {
+        const int last = job - 1;
+        if (!wait_or_abort(&o_done[LANES == 1 ? last & 1 : me], LANES == 1 ? (last >> 1) & 1 : ends++ & 1)) {
+          run = false;
+          break;
+        }
       }
       tc::fence_after_sync();
       if (P::SPLIT && me == 1) {
@@ -403,8 +450,8 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           if (mine) {
             const int64_t head = (int64_t)n * at.Hq + walk.head * G + i % G;
             if (begins) {
-              ws.note[head] =
-                  first_note(m, l, c, (int)piece_of(walk.unit_end - 1, T, pieces) - c, row_tile * kRows + row);
+              ws.note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, T, pieces) - c, row_tile * kRows + row);
+              ws.first[head] = make_float2(m, l);
               dst = ws.o + head * D;
             } else {
               const int64_t at_piece = (int64_t)c * ROWS + row_tile * kRows + row;
@@ -439,98 +486,129 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       walk.tile = end;
       walk.next_unit(a);
     }
-  } else if (warp == 4 * LANES) {
-    // ---------------- matrix products ----------------
+  } else if (warp >= P::PRODUCT0 && warp < P::PRODUCT0 + LANES) {
+    more_registers<LANES == 1 ? 0 : -112>();
+    // ---------------- matrix products, a warp for each lane ----------------
     constexpr uint32_t ID_S = tc::idesc_bf16(kRows, KT, false, false), ID_O = tc::idesc_bf16(kRows, D, false, true);
     const uint32_t q_addr = smem_addr(s_q), ring = smem_addr(s_ring);
-    int half = 0;           // of the next K; its V is the one after it
-    int unit = 0;
-    uint32_t weighed = 0;  // parity of the outputs issued from each buffer
-    bool run = any;
-    // A half that has landed; the tensor cores read it through another proxy than the copies wrote it.
-    const auto slot_wait = [&](int h) {
-      const bool ok = wait_or_abort(&full[h % SLOTS], (h / SLOTS) & 1);
-      fence_proxy_async_smem();
-      return ok;
-    };
     const uint32_t issue = tc::elect();
     const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    // S of row tile r into buffer b from the keys in half h.
-    const auto scores = [&](int q_slot, int r, int b, int h) {
-      tc::fence_after_sync();
-      const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + r) * P::Q_TILE, 16, 1024);
+    const int me = uniform(warp - P::PRODUCT0), row_tile = RT == 1 ? 0 : me;
+    int half = 0, tile = 0, unit = 0;  // of the next K, whose V is the one after it; tiles and units so far
+    uint32_t weighed = 0;              // parity of the outputs issued from each buffer
+    bool run = any, threads = true;
+    const auto release = [&](uint64_t* bar) { tc::commit_by(issue, bar); };
+    // A half that has landed.  What threads copied the tensor cores read through another proxy.
+    const auto slot_wait = [&](int h) {
+      if (!wait_or_abort(&full[h % SLOTS], (h / SLOTS) & 1)) return false;
+      if (threads) fence_proxy_async_smem();
+      return true;
+    };
+    // The keys of the unit's tile j.
+    const auto keys_wait = [&](int j) -> bool {
+      const int at_mask = (tile + j) % kLiveDepth;
+      if (!wait_or_abort(&live_full[at_mask], ((tile + j) / kLiveDepth) & 1)) return false;
+      threads = box == 0 || j < (P::SPLIT ? 2 : 1);  // the queries are always copied by threads
+#pragma unroll
+      for (int i = 0; i < KT / 32; ++i) threads = threads || s_live[at_mask][i] != 0xffffffffu;
+      return slot_wait(half + 2 * j);
+    };
+    // S of the unit's tile j into buffer b.
+    const auto scores = [&](int q_slot, int b, int j) {
+      const int h = half + 2 * j;
+      const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + row_tile) * P::Q_TILE, 16, 1024);
       const uint64_t k = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, 16, 1024);
-      const int buffer = uniform(b);
+      const uint32_t to = taddr + P::S_COL + uniform(b) * KT;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)  // descriptors count in 16 bytes
-        tc::mma_bf16_by(issue, taddr + P::S_COL + buffer * KT, q + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
+        tc::mma_bf16_by(issue, to, q + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
                         k + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, ID_S, ks > 0);
-      tc::commit_by(issue, &s_full[buffer]);
+      release(&s_full[uniform(b)]);
+      release(&empty[uniform(h % SLOTS)]);
     };
-    // Waits for the weights in buffer b; the output of lane o += them times the values in half h.
-    const auto outputs = [&](int o, int b, int h, bool first) -> bool {
-      const int buffer = uniform(b);
-      if (!wait_or_abort(&p_full[buffer], weighed >> buffer & 1)) return false;
-      weighed ^= 1u << buffer;
-      tc::fence_after_sync();
+    // The values of tile j and its weights in buffer b.
+    const auto weights_wait = [&](int b, int j) -> bool {
+      if (!slot_wait(half + 2 * j + 1) || !wait_or_abort(&p_full[uniform(b)], weighed >> b & 1)) return false;
+      weighed ^= 1u << b;
+      return true;
+    };
+    // The output += the weights in buffer b times the values of tile j.
+    const auto outputs = [&](int b, int j, bool first, bool last) {
+      const int h = half + 2 * j + 1;
       const uint64_t v = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, KT * 128, 1024);
-      const uint32_t p = taddr + P::S_COL + buffer * KT, d = taddr + P::O_COL + uniform(o) * D;
+      const uint32_t p = taddr + P::S_COL + uniform(b) * KT, d = taddr + P::O_COL + me * D;
       const bool onto = uniform(!first);
 #pragma unroll
       for (int ks = 0; ks < KT / 16; ++ks)
 #pragma unroll
         for (int piece = 0; piece < 2; ++piece)
           tc::mma_bf16_ta_by(issue, d, p + ks * 16 + piece * 8, v + ks * 2048 / 16, ID_O, onto || ks > 0 || piece > 0);
-      tc::commit_by(issue, &o_done[buffer]);
-      return true;
+      if (LANES == 1 || last) release(&o_done[uniform(b)]);
+      release(&empty[uniform(h % SLOTS)]);
     };
-    const auto release = [&](uint64_t* bar) { tc::commit_by(issue, bar); };
-    int job = 0;
+    int turns = 0;
     while (run && walk.tile < stop) {
       const int count = (int)(min(walk.unit_end, stop) - walk.tile);
       const int q_slot = unit % P::QSLOTS;
-      // the products of tile j with its keys, of tile j - 1 with its values
-      for (int j = 0; j <= count && run; ++j) {
-        const int hk = half + 2 * j, hv = hk - 1;
-        if (j < count && !slot_wait(hk)) { run = false; break; }
-        if constexpr (RT == 1) {
-          const int b = P::SPLIT ? j & 1 : (job + j) & 1;
+      if constexpr (LANES == 1) {  // the next tile's scores before this one's outputs
+        for (int j = 0; j <= count && run; ++j) {
+          const int b = (tile + j) & 1;
           if (j < count) {
-            scores(q_slot, 0, b, hk);
-            release(&empty[uniform(hk % SLOTS)]);
+            if (!keys_wait(j)) { run = false; break; }
+            tc::fence_after_sync();
+            scores(q_slot, b, j);
           }
           if (j > 0) {
-            if (!slot_wait(hv) || !outputs(P::SPLIT ? b ^ 1 : 0, b ^ 1, hv, j <= (P::SPLIT ? 2 : 1))) { run = false; break; }
-            release(&empty[uniform(hv % SLOTS)]);
+            if (!weights_wait(b ^ 1, j - 1)) { run = false; break; }
+            tc::fence_after_sync();
+            outputs(b ^ 1, j - 1, j == 1, true);
           }
-        } else {
-          if (j > 0 && !slot_wait(hv)) { run = false; break; }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if (j > 0 && run && !outputs(r, r, hv, j == 1)) run = false;
-            if (r == RT - 1 && j > 0 && run) release(&empty[uniform(hv % SLOTS)]);
-            if (j < count && run) scores(q_slot, r, r, hk);
-          }
-          if (!run) break;
-          if (j < count) release(&empty[uniform(hk % SLOTS)]);
         }
-        if (j == count - 1) release(&q_empty[uniform(q_slot)]);
+      } else if constexpr (P::SPLIT) {
+        for (int j = me; j < count; j += 2) {
+          if (!keys_wait(j)) { run = false; break; }
+          tc::fence_after_sync();
+          scores(q_slot, me, j);
+          if (!weights_wait(me, j)) { run = false; break; }
+          tc::fence_after_sync();
+          outputs(me, j, j < 2, j + 2 >= count);
+        }
+      } else {
+        // Outputs of a tile and scores of the next in one go, the lanes in turn: left to themselves their softmaxes fall
+        // into step, and the tensor cores wait for both.
+        for (int j = 0; j <= count; ++j, ++turns) {
+          const bool behind = threads;
+          if (j < count && !keys_wait(j)) { run = false; break; }
+          const bool now = threads;
+          threads = behind;
+          if (j > 0 && !weights_wait(me, j - 1)) { run = false; break; }
+          threads = now;
+          if ((me > 0 || turns > 0) && !wait_or_abort(&turn[me], (turns - 1 + me) & 1)) { run = false; break; }
+          tc::fence_after_sync();
+          if (j > 0) outputs(me, j - 1, j == 1, j == count);
+          if (j < count) scores(q_slot, me, j);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&turn[me ^ 1]);
+        }
       }
+      if (!run) break;
+      release(&q_empty[uniform(q_slot)]);
       half += 2 * count;
-      job += count;
+      tile += count;
       ++unit;
       walk.tile += count;
       if (walk.tile < stop) walk.next_unit(a);
     }
-    release(&drained);  // every product issued has completed before the columns are freed
-    mbar_sleep_wait(&drained, 0);
-  } else {
+    release(&drained[me]);  // every product issued has completed before the columns are freed
+    mbar_sleep_wait(&drained[me], 0);
+  } else if (warp >= P::LOADER0 && warp < P::LOADER0 + kLoaders / 32) {
+    more_registers<LANES == 1 ? 0 : -112>();
     // ---------------- copies ----------------
     constexpr int CHUNKS = D / 8;                    // 16-byte pieces of a row
     constexpr int WARP_ROWS = KT / 4;                // keys of a warp
     constexpr int STEP_ROWS = 32 / CHUNKS;           // keys of one instruction
     static_assert(CHUNKS <= 32 && WARP_ROWS <= 32, "a row or more an instruction, a key or less a lane");
-    const int lw = warp - (4 * LANES + 1);
+    const int lw = warp - P::LOADER0;
     const int chunk = lane % CHUNKS, sub = lane / CHUNKS;
     const uint32_t ring = smem_addr(s_ring), q_addr = smem_addr(s_q);
     const auto place = [](int row, int ch, int rows) {  // of a 16-byte piece in an operand of `rows` rows
@@ -557,16 +635,34 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     };
     int half = 0, tile = 0, unit = 0;
     bool run = any;
-    const auto copy_half = [&](const void* data, int64_t offset, uint32_t mask) {
+    // This warp's keys or values of a tile: by TMA where all are there and pages hold whole boxes, by threads, which put
+    // zeros in the place of what is not attended to, otherwise.
+    const auto copy_half = [&](const PageView& view, const CUtensorMap* map, const Look& look, uint32_t mask) {
       const uint32_t base = ring + (half % SLOTS) * P::HALF;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(data);
+      uint64_t* const bar = &full[half % SLOTS];
+      if (box > 0 && mask == (WARP_ROWS == 32 ? 0xffffffffu : (1u << WARP_ROWS) - 1)) {
+        if (lane == 0) mbar_expect_tx(bar, WARP_ROWS * D * 2);
+        __syncwarp();
+        if (lane < WARP_ROWS && lane % box == 0) {
+#pragma unroll
+          for (int b = 0; b < P::BLOCKS; ++b)
+            tma_load_4d(base + (b * KT + lw * WARP_ROWS + lane) * 128, map, 64 * b, look.token, look.head, look.page, bar);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_many(bar, 32);
+        ++half;
+        return;
+      }
+      const int64_t offset =
+          mask >> lane & 1 ? look.page * view.page + look.token * view.token + look.head * view.head : 0;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(view.data);
 #pragma unroll 4
       for (int i = 0; i < WARP_ROWS / STEP_ROWS; ++i) {
         const int k = i * STEP_ROWS + sub;
         const int64_t from = __shfl_sync(0xffffffffu, offset, k);
         copy16(base + place(lw * WARP_ROWS + k, chunk, KT), src + from + chunk * 8, mask >> k & 1);
       }
-      copy_arrive(&full[half % SLOTS]);
+      copy_arrive(bar);
       ++half;
     };
     Look look = any ? look_up() : Look{0, 0, 0};
@@ -578,7 +674,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       }
       {
         const int left = min(walk.rows_left(), ROWS), rows = (left + 31) & ~31;
-        for (int i = tid - (4 * LANES + 1) * 32; i < rows * CHUNKS; i += kLoaders) {
+        for (int i = tid - P::LOADER0 * 32; i < rows * CHUNKS; i += kLoaders) {
           const int row = i / CHUNKS, ch = i % CHUNKS;
           const int q = walk.row_tile * ROWS + row;
           const bool real = row < left;
@@ -592,9 +688,6 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         const Look next = look_up();
         const bool live = look.page > 0 && look.page < at.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, live);
-        const auto offset = [&](const PageView& p) {
-          return live ? look.page * p.page + look.token * p.token + look.head * p.head : 0;
-        };
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
         if (WARP_ROWS == 32) {
           if (lane == 0) s_live[tile % kLiveDepth][lw] = mask;
@@ -602,86 +695,88 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           reinterpret_cast<uint16_t*>(s_live[tile % kLiveDepth])[lw] = (uint16_t)mask;
         }
         if (lane == 0) mbar_arrive(&live_full[tile % kLiveDepth]);
-        copy_half(at.kp.data, offset(at.kp), mask);
+        copy_half(at.kp, &k_map, look, mask);
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
-        copy_half(at.vp.data, offset(at.vp), mask);
+        copy_half(at.vp, &v_map, look, mask);
         look = next;
       }
       if (!run) break;
       ++unit;
       walk.next_unit(a);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // none lands when the CTA is gone
+    // No copy lands when the CTA is gone; all have been waited for but where a role gave up.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int h = max(0, half - SLOTS); h < half; ++h) mbar_sleep_wait(&full[h % SLOTS], (h / SLOTS) & 1);
+  } else {
+    more_registers<LANES == 1 ? 0 : -112>();
   }
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 4 * LANES) {
+  if (warp == P::PRODUCT0) {
     tc::fence_after_sync();
     tc::dealloc(taddr, P::COLS);
   }
 }
 
-// Joins the parts of one query head of a sequence: of the common positions and of
-// its own, each a first part and those of later pieces.  WARPS warps share the
-// parts; a block of four warps joins one head or four.
+// Joins the parts of one query head of a sequence: of the common positions a first
+// one and those of later pieces, of its own the same from each warp.  WARPS warps
+// share the parts; a block of four warps joins one head or four.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_constant__ AttendArgs a, const PrefixWork pre,
-                                                              int ctas, int own_rows, int pre_ctas,
-                                                              int pre_rows) {
+                                                              int ctas, int own_rows, int pre_ctas, int pre_rows) {
   constexpr int VEC = D / 32, AHEAD = 4;
   __shared__ float s_m[4], s_l[4], s_o[WARPS > 1 ? 4 : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t head = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
-  if (head >= (int64_t)a.N * a.Hq) return;
-  const Workspace own(a.work, ctas, own_rows, D);
-  const float4 notes[2] = {pre.note[head], a.first_note[head]};
+  const int64_t heads = (int64_t)a.N * a.Hq, head = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
+  if (head >= heads) return;
+  const int2 notes[2] = {pre.note[head], a.first_note[head]};
   // A kernel that gave up a wait has left notes that say anything: no part outside the workspace is read for them.
   int piece[2], row[2], more[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int packed = __float_as_int(notes[w].w), last = (w == 0 ? pre_ctas : ctas) - 1;
-    piece[w] = __float_as_int(notes[w].z);
-    row[w] = packed & 255;
-    more[w] = packed >> 8;
+    const int last = (w == 0 ? pre_ctas : ctas) - 1;
+    piece[w] = notes[w].x;
+    row[w] = notes[w].y & 255;
+    more[w] = notes[w].y >> 8;
     if (piece[w] < 0 || more[w] < 0 || piece[w] > last || more[w] > last - piece[w] ||
         row[w] >= (w == 0 ? pre_rows : own_rows))
       more[w] = 0;
   }
-  const int parts0 = 1 + more[0], parts = parts0 + 1 + more[1];
+  const int parts0 = 1 + more[0], parts = parts0 + kAttendWarps * (1 + more[1]);
   float m = -INFINITY, l = 0.f, o[VEC] = {};
 #pragma unroll 1
   for (int i = WARPS == 1 ? 0 : warp; i < parts; i += WARPS * AHEAD) {
     float pm[AHEAD], pl[AHEAD], po[AHEAD][VEC];
+    const float* from[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int p = i + k * WARPS;
       pm[k] = -INFINITY;
       pl[k] = 0.f;
-      const float* from = nullptr;
+      from[k] = nullptr;
       if (p < parts) {
         const bool w = p >= parts0;
-        const int j = w ? p - parts0 : p;
-        if (j == 0) {
-          pm[k] = w ? notes[1].x : notes[0].x;
-          pl[k] = w ? notes[1].y : notes[0].y;
-          from = (w ? a.first_o : pre.o) + head * D;
-        } else {
-          const int64_t place = w ? 2 * (int64_t)(piece[1] + j) * own_rows + row[1] : (int64_t)(piece[0] + j) * pre_rows + row[0];
-          const float2 ml = w ? *reinterpret_cast<const float2*>(own.ml + 2 * place) : pre.ml[place];
-          pm[k] = ml.x;
-          pl[k] = ml.y;
-          from = (w ? own.o : pre.more) + place * D;
-        }
+        const int q = w ? p - parts0 : p, j = w ? q / kAttendWarps : q, by = w ? q % kAttendWarps : 0;
+        const int64_t place = j == 0 ? by * heads + head
+                                     : (w ? ((int64_t)(piece[1] + j) * kAttendWarps + by) * own_rows + row[1]
+                                          : (int64_t)(piece[0] + j) * pre_rows + row[0]);
+        const float2 ml = (w ? (j == 0 ? a.first_ml : a.more_ml) : (j == 0 ? pre.first : pre.ml))[place];
+        pm[k] = ml.x;
+        pl[k] = ml.y;
+        from[k] = (w ? (j == 0 ? a.first_o : a.more_o) : (j == 0 ? pre.o : pre.more)) + place * D;
       }
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
 #pragma unroll
       for (int v = 0; v < VEC; ++v) po[k][v] = 0.f;
       if (pl[k] != 0.f) {  // a part of no positions may have left no output
 #pragma unroll
         for (int v = 0; v < VEC; v += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(from + lane * VEC + v);
+          const float2 x = *reinterpret_cast<const float2*>(from[k] + lane * VEC + v);
           po[k][v] = x.x;
           po[k][v + 1] = x.y;
         }
@@ -738,24 +833,28 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
 }
 
 // Places of the workspace, in floats: the paged kernel's own, then both kernels'
-// first parts, the prefix kernel's later ones and the sequences' skips.
+// first parts and later ones, and the sequences' skips.
 struct PrefixPlan {
   AttendPlan own;
-  int64_t own_note, own_o, note, o, ml, more, skip, floats;
+  int64_t own_note, own_ml, own_o, own_more_ml, own_more, note, first, o, ml, more, skip, floats;
 };
 PrefixPlan prefix_plan(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t sms) {
   PrefixPlan p;
   p.own = attend_mma_plan(Hq / Hkv, D, sms);
-  const int64_t heads = N * Hq, rows = (int64_t)sms * 2 * kRows;
-  int64_t at = (p.own.floats + 3) & ~int64_t{3};
+  const int64_t heads = N * Hq, rows = (int64_t)sms * 2 * kRows, own = (int64_t)kAttendWarps * p.own.ctas * p.own.heads;
+  int64_t at = p.own.ctas * (int64_t)kNoteFloats;  // the notes that the paged kernel leaves all the same
   const auto take = [&](int64_t floats) {
     const int64_t r = at;
     at += (floats + 3) & ~int64_t{3};
     return r;
   };
-  p.own_note = take(4 * heads);
-  p.own_o = take(heads * D);
-  p.note = take(4 * heads);
+  p.own_note = take(2 * heads);
+  p.own_ml = take(2 * kAttendWarps * heads);
+  p.own_o = take(kAttendWarps * heads * D);
+  p.own_more_ml = take(2 * own);
+  p.own_more = take(own * D);
+  p.note = take(2 * heads);
+  p.first = take(2 * heads);
   p.o = take(heads * D);
   p.ml = take(2 * rows);
   p.more = take(rows * D);
@@ -764,13 +863,34 @@ PrefixPlan prefix_plan(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t sm
   return p;
 }
 
+// The pages as [num_pages][Hkv][page_size][D], boxes of `rows` positions and 64 channels.
+bool encode_pages(CUtensorMap* map, const PageView& p, const AttendArgs& a, int rows) {
+  EncodeTiledFn encode = encode_tiled();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  // an axis of one element may have any stride, which the map need not accept
+  const auto bytes = [&](int64_t stride, int64_t extent) { return (cuuint64_t)(extent > 1 ? stride : a.D) * 2; };
+  const cuuint64_t strides[3] = {bytes(p.token, a.page_size), bytes(p.head, a.Hkv), bytes(p.page, a.num_pages)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.data, dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int RT>
 cudaError_t launch_prefix(const PrefixArgs& a, const PrefixWork& ws, int sms, cudaStream_t s) {
   using P = PrefixShape<D, RT>;
   static std::atomic<bool> set[64];
   const cudaError_t e = allow_shared(kda_prefix_kernel<D, RT>, P::BYTES, set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kda_prefix_kernel<D, RT>, dim3(sms), dim3(P::THREADS), P::BYTES, s, 1, a, ws);
+  // A warp's positions of a tile are whole boxes, of whole eights as the swizzle repeats, and a page whole boxes too.
+  CUtensorMap k_map = {}, v_map = {};
+  const AttendArgs& t = a.attend;
+  int box = P::KT / 4;
+  if (t.page_size < box) box = t.page_size >= 8 && box % t.page_size == 0 ? t.page_size : 0;
+  if (box > 0 && t.page_size % box != 0) box = 0;
+  if (box > 0 && !(encode_pages(&k_map, t.kp, t, box) && encode_pages(&v_map, t.vp, t, box))) box = 0;
+  return launch_pdl(kda_prefix_kernel<D, RT>, dim3(sms), dim3(P::THREADS), P::BYTES, s, 1, a, ws, box, k_map, v_map);
 }
 
 template <int D>
@@ -797,7 +917,8 @@ cudaError_t launch_prefix_attention(const PrefixArgs& given, int32_t sms, cudaSt
   if (t.dtype == KDA_DT_F32 || !t.vec16 || a.G >= t.N) return launch_paged_attention(t, sms, s);
   const PrefixPlan p = prefix_plan(t.N, t.Hq, t.Hkv, t.D, sms);
   PrefixWork ws;
-  ws.note = reinterpret_cast<float4*>(t.work + p.note);
+  ws.note = reinterpret_cast<int2*>(t.work + p.note);
+  ws.first = reinterpret_cast<float2*>(t.work + p.first);
   ws.o = t.work + p.o;
   ws.ml = reinterpret_cast<float2*>(t.work + p.ml);
   ws.more = t.work + p.more;
@@ -811,8 +932,11 @@ cudaError_t launch_prefix_attention(const PrefixArgs& given, int32_t sms, cudaSt
   }
   if (e != cudaSuccess) return e;
   t.skip = ws.skip;
-  t.first_note = reinterpret_cast<float4*>(t.work + p.own_note);
+  t.first_note = reinterpret_cast<int2*>(t.work + p.own_note);
+  t.first_ml = reinterpret_cast<float2*>(t.work + p.own_ml);
   t.first_o = t.work + p.own_o;
+  t.more_ml = reinterpret_cast<float2*>(t.work + p.own_more_ml);
+  t.more_o = t.work + p.own_more;
   e = launch_attend_mma(t, p.own, s);
   if (e != cudaSuccess) return e;
   const int rows = two ? 2 * kRows : kRows;
