@@ -906,6 +906,16 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixWork& ws, const 
 
 }  // namespace
 
+// Bytes of keys and values from which sharing is worth its two launches more, by
+// what it could save at the table's width (the host knows no lengths): below, every
+// sequence is on its own.  Measured shared and alone, us (groups x sequences x common
+// positions, 64 own ones; the bytes that sharing saves):
+//   32 / 8 heads of 128   1 x 2 x 1024 (4 MB) 18 and 10, 1 x 16 x 1024 (63 MB) 22 and 19, 16 x 4 x 256 (50 MB) 28 and 23,
+//                         4 x 16 x 256 (63 MB) 26 and 23, 1 x 16 x 4032 (248 MB) 25 and 42, 16 x 4 x 1024 (201 MB) 38 and 47
+//   64 channels           1 x 4 x 16000 (98 MB) 26 and 27, 16 x 4 x 1024 (101 MB) 29 and 31, 4 x 2 x 16000 (131 MB) 52 and 46
+//   256 channels          1 x 4 x 4032 (99 MB) 25 and 34, 12 / 1 heads 1 x 16 x 16000 (246 MB) 48 and 66, 4 x 16 x 1024 (63 MB) 32 and 28
+constexpr int64_t kSharedBytes = 96 << 20;
+
 int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
   const int64_t paged = attend_floats(Hq, Hkv, D, dtype, sms);
   return dtype == KDA_DT_F32 ? paged : std::max(paged, prefix_plan(N, Hq, Hkv, D, sms).floats);
@@ -914,7 +924,9 @@ int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dty
 cudaError_t launch_prefix_attention(const PrefixArgs& given, int32_t sms, cudaStream_t s) {
   PrefixArgs a = given;
   AttendArgs& t = a.attend;
-  if (t.dtype == KDA_DT_F32 || !t.vec16 || a.G >= t.N) return launch_paged_attention(t, sms, s);
+  const double most = (double)t.table_cols * t.page_size;
+  if (t.dtype == KDA_DT_F32 || !t.vec16 || (t.N - (double)a.G) * most * t.Hkv * t.D * 4 < kSharedBytes)
+    return launch_paged_attention(t, sms, s);
   const PrefixPlan p = prefix_plan(t.N, t.Hq, t.Hkv, t.D, sms);
   PrefixWork ws;
   ws.note = reinterpret_cast<int2*>(t.work + p.note);

@@ -14,6 +14,7 @@ from tests.test_gpu_paged_attention import same, tolerances
 
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
+SHARED = 96 << 20  # bytes that sharing has to save at the table's width
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -26,11 +27,14 @@ def make(groups, Hq=8, Hkv=2, D=128, page=16, dtype=BF16, seed=0, layout="token"
          width=None):
     """groups: (prefix, [own positions of each sequence]); a sequence's length is their sum.  `before` and `after`
     sequences of 37 positions belong to no group.  Whole pages of a prefix are shared; what is dead holds NaN and
-    infinities."""
+    infinities.  The table is as wide as it takes for the call to share, unless `width` is given."""
     g = torch.Generator().manual_seed(seed)
     seqs = [(None, 0, 37)] * before + [(i, p, t) for i, (p, tails) in enumerate(groups) for t in tails] + [(None, 0, 37)] * after
     lens = [max(0, p + t) for _, p, t in seqs]
-    P = width or max([1] + [-(-n // page) for n in lens])
+    P = max([1] + [-(-n // page) for n in lens])
+    if width is None:
+        P = max(P, -(-SHARED // (max(1, len(seqs) - len(groups)) * Hkv * D * 4 * page)))
+    P = width or P
     total = sum(-(-n // page) for n in lens) + sum(-(-p // page) for p, _ in groups)
     pages = total + 1 + spare
     order = (torch.randperm(pages - 1, generator=g) + 1).tolist()
@@ -89,14 +93,18 @@ def expected(c, window=0, scale=None):
     one that shares) through the first sequence's row."""
     k, v, table, lens = to_np(c["k"]), to_np(c["v"]), c["table"].cpu().numpy().astype(np.int64), c["lens"].cpu().numpy()
     pages, page = k.shape[:2]
+    cap = table.shape[1] * page  # the table is mostly empty: what no sequence reaches is left out
+    reached = min(cap, max([0, *lens.tolist(), *c["prefix"].tolist()]))
+    table = table[:, :max(1, -(-reached // page))]
     places = np.where((table > 0) & (table < pages), table, 0)[:, :, None] * page + np.arange(page)
     places = np.where(places < page, 0, places).reshape(len(lens), -1)
+    shares = (len(lens) - len(c["prefix"])) * cap * k.shape[2] * k.shape[3] * 4 >= SHARED
     starts, prefixes = c["starts"].tolist(), c["prefix"].tolist()
-    if c["q"].dtype == BF16:
+    if c["q"].dtype == BF16 and shares:
         for first, end, p in zip(starts, starts[1:], prefixes):
-            p = min(max(p, 0), places.shape[1])
+            p = min(max(p, 0), cap)
             for n in range(first, end):
-                if min(lens[n], places.shape[1]) >= p and (window == 0 or lens[n] <= window):
+                if min(lens[n], cap) >= p and (window == 0 or lens[n] <= window):
                     places[n, :p] = places[first, :p]
     return co.paged_attention(to_np(c["q"]), k.reshape(-1, 1, *k.shape[2:]), v.reshape(-1, 1, *v.shape[2:]), places, lens,
                               window=window, scale=scale)
@@ -185,6 +193,18 @@ def test_lengths_and_prefixes_past_the_table():
     c["lens"][:] = torch.tensor([64, 2 ** 31 - 1, 70], dtype=torch.int32)
     check(c)
     c["prefix"][0] = -3
+    check(c)
+
+
+def test_a_prefix_of_the_whole_table():
+    c = make([(300, [40, 60, 5])])
+    c["prefix"][0] = 2 ** 31 - 1  # as much as the table holds, mostly null pages
+    c["lens"][:2] = torch.tensor([2 ** 31 - 1, 10 ** 9], dtype=torch.int32)
+    c["table"][0, -3:] = c["table"][0, :3].clone()
+    c["table"][1] = c["table"][0].clone()
+    for n in range(2):  # pages listed past the old lengths hold garbage
+        for x in set(c["table"][n].tolist()):
+            c["k"][x].nan_to_num_(0.5, 0.25, -0.25), c["v"][x].nan_to_num_(0.5, 0.25, -0.25)
     check(c)
 
 
@@ -329,6 +349,15 @@ def test_out_lse_and_workspace_of_the_caller():
     assert torch.isnan(work[floats:]).all()
     with pytest.raises(binding.KdaError, match="workspace"):
         run(c, workspace=work[:floats - 1])
+
+
+@pytest.mark.parametrize("groups", [[(128, [1, 2])], [(1000, [5] * 20), (60, [4, 4])]])
+def test_narrow_tables_whose_sequences_are_on_their_own(groups):
+    check(make(groups, width=90))
+
+
+def test_groups_of_one_sequence():
+    check(make([(100, [5]), (64, [1]), (700, [30])], width=5000))
 
 
 def test_empty_batch():
