@@ -74,6 +74,7 @@ struct PagesArgs {
   int32_t* cu; int32_t* slots;                       // [N + 1], [R]
   int32_t N, page_size;
   int64_t R;
+  int32_t run;                                       // rows a thread takes at once (set by the launcher)
 };
 cudaError_t launch_page_assign(const PagesArgs& a, cudaStream_t s);
 

@@ -13,7 +13,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/CUDAContextLight.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -138,7 +138,7 @@ struct Call {
             static_cast<int>(t.device().index()));
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);  // at::empty without its dispatch
   }
   int sms() const { return at::cuda::getDeviceProperties(device.index())->multiProcessorCount; }
 };

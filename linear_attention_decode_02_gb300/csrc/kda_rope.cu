@@ -256,11 +256,12 @@ cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
                                       : kda_rope_append_kernel<In, Out, VEC, true, ROWS, false>)
                               : (axes ? kda_rope_append_kernel<In, Out, VEC, false, ROWS, true>
                                       : kda_rope_append_kernel<In, Out, VEC, false, ROWS, false>);
-  // Few rows: several blocks share each, down to one vector a thread, until every SM has its six.
+  // Few rows: several blocks share each, down to one vector a thread, until every SM has its six, or nearest to it: 1900
+  // rows in fours, 475 blocks, take 9.2 us shared by two and 11.3 us by one.
   const int64_t blocks = (a.R + (int64_t)ROWS - 1) / ROWS;
   const int pairs = a.interleaved ? a.rot / VEC : a.rot / (2 * VEC);
   const int64_t tasks = (int64_t)(a.Hq + a.Hkv) * (pairs + (a.D - a.rot) / VEC);
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((tasks + kThreads - 1) / kThreads, 6 * a.sms / blocks));
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((tasks + kThreads - 1) / kThreads, (6 * a.sms + blocks / 2) / blocks));
   return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)parts), dim3(kThreads), 0, s, 1, a);
 }
 
