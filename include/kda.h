@@ -484,9 +484,8 @@ kda_status kda_rope_pair_axes(const int32_t* sections, int32_t num_axes, int32_t
  * up to 16 times those relative to the largest score before they are summed, so values
  * within that factor of the largest float may overflow.  A sequence shorter than its
  * group's prefix, or whose window leaves part of it out, is on its own too.  So is
- * every sequence where the dtype is float32, where vectors are off 16-byte boundaries,
- * and where the keys and values that sharing could save, (N - G) * P * page_size
- * positions, come to less than 96 MB.
+ * every sequence where vectors are off 16-byte boundaries, and where the keys and values
+ * that sharing could save, (N - G) * P * page_size positions, come to less than 96 MB.
  */
 kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,
                                        const kda_tensor* page_table, const kda_tensor* seq_lens,

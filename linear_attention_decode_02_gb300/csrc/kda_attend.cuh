@@ -40,7 +40,10 @@ AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms);
 cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 // Float32 in matrix instructions (kda_attend_tf32.cu), for many query heads a key head.
 AttendPlan attend_tf32_plan(int32_t G, int32_t D, int32_t sms);
+int attend_tf32_warps(int32_t D);  // of a block
 cudaError_t launch_attend_tf32(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
+// The same over the groups' common positions, units of p.heads query rows.
+cudaError_t launch_attend_tf32_groups(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 
 // a / b, neither negative; 32-bit where they fit (a 64-bit division is a long call).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -74,6 +77,10 @@ struct Workspace {
   __device__ __forceinline__ float* ml_of(int64_t slot, int h) const { return ml + (slot * heads + h) * 2; }
   __device__ __forceinline__ float* o_of(int64_t slot, int h) const { return o + (slot * heads + h) * D; }
 };
+
+// Where a result's later parts are: the piece that began it, how many after that
+// hold more of it, and its place in them (below 256).
+__device__ __forceinline__ int2 part_note(int piece, int more, int row) { return make_int2(piece, more << 8 | row); }
 
 // Positions a sequence attends to: [first, end), and its tiles [tile0, tile0 + tiles).
 struct Span {
@@ -167,6 +174,146 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   return p;
 }
 
+// ---- groups of sequences that share a prefix -------------------------------------
+
+// A group's sequences and what its unit, a key head and ROWS query rows, has of
+// tiles of KT positions.  Query row i of a key head is its query head i % G (G to a
+// key head) in sequence i / G of the group.
+struct Group {
+  int first, rows, prefix, tiles, row_tiles;  // first sequence; query rows of a key head; common positions
+};
+template <int KT, int ROWS>
+__device__ __forceinline__ Group group_of(const AttendArgs& a, int g) {
+  Group r;
+  r.first = min(max(__ldg(a.starts + g), 0), a.N);
+  const int end = min(max(__ldg(a.starts + g + 1), r.first), a.N);
+  const int64_t cap = (int64_t)a.table_cols * a.page_size;
+  r.prefix = (int)min((int64_t)max(__ldg(a.prefix_lens + g), 0), cap);
+  r.rows = (end - r.first) * (a.Hq / a.Hkv);
+  r.tiles = (r.prefix + KT - 1) / KT;
+  r.row_tiles = r.tiles > 0 ? (r.rows + ROWS - 1) / ROWS : 0;
+  return r;
+}
+
+// A sequence takes part in its group's common positions where it attends to all of them.
+__device__ __forceinline__ bool takes_part(const AttendArgs& a, int n, int prefix) {
+  const int64_t cap = (int64_t)a.table_cols * a.page_size;
+  const int len = __ldg(a.lens + n);
+  return prefix > 0 && min((int64_t)max(len, 0), cap) >= prefix && (a.window == 0 || len <= a.window);
+}
+
+// Warp w of `warps`: notes which sequences take part, and empty parts for those that do not.
+__device__ __forceinline__ void mark_sequences(const AttendArgs& a, int w, int warps, int lane) {
+  const int64_t heads = (int64_t)a.N * a.Hq;
+  for (int n = w; n < a.N; n += warps) {
+    const int g = find_sequence(a.starts, a.num_groups, n, lane);
+    bool part = false;
+    int prefix = 0;
+    if (g < a.num_groups && n >= __ldg(a.starts + g)) {
+      prefix = group_of<1, 1>(a, g).prefix;
+      part = takes_part(a, n, prefix);
+    }
+    if (lane == 0) a.mark[n] = part ? prefix : 0;
+    if (part) continue;
+    for (int h = lane; h < a.Hq; h += 32) {
+      const int64_t head = (int64_t)n * a.Hq + h;
+      a.parts.first_note[head] = part_note(0, 0, 0);
+      for (int i = 0; i < a.parts.warps; ++i) a.parts.first_ml[i * heads + head] = make_float2(-INFINITY, 0.f);
+    }
+  }
+}
+
+// Where a walk over the tiles of groups' units stands; the key head's row tiles lie together.
+template <int KT, int ROWS>
+struct GroupWalk {
+  int64_t tile, unit_start, unit_end;
+  int g, n, group, row_tile;  // n: the sequence whose pages are read; group: the key head
+  Span sp;
+  Group of;
+  __device__ __forceinline__ void enter(const AttendArgs& a) {
+    of = group_of<KT, ROWS>(a, g);
+    n = of.first;
+    sp = Span{0, of.prefix, 0, of.tiles};
+  }
+  __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
+    tile = p.start;
+    g = p.n;
+    enter(a);
+    const int64_t u = quotient(tile - p.before, of.tiles);
+    group = (int)quotient(u, of.row_tiles);
+    row_tile = (int)(u - (int64_t)group * of.row_tiles);
+    unit_start = p.before + u * of.tiles;
+    unit_end = unit_start + of.tiles;
+  }
+  __device__ __forceinline__ void next_unit(const AttendArgs& a, int = 0) {
+    unit_start = unit_end;
+    if (++row_tile == of.row_tiles) {
+      row_tile = 0;
+      if (++group == a.Hkv) {
+        group = 0;
+        do {
+          if (++g >= a.num_groups) return;
+          enter(a);
+        } while (of.row_tiles == 0);
+      }
+    }
+    unit_end = unit_start + of.tiles;
+  }
+  __device__ __forceinline__ int rows_left() const { return of.rows - row_tile * ROWS; }
+  // Sequence and query head of row r of the unit.
+  __device__ __forceinline__ int2 row(const AttendArgs& a, int r) const {
+    const int G = a.Hq / a.Hkv, i = row_tile * ROWS + r;
+    return make_int2(of.first + i / G, group * G + i % G);
+  }
+};
+
+// The tiles of all groups' units and where piece c lies in them (p.n: the group), found by the whole block.
+template <int THREADS, int KT, int ROWS>
+__device__ __forceinline__ Place find_group_place(const AttendArgs& a, int c, int ctas) {
+  __shared__ int64_t s_warp[THREADS / 32], s_before;
+  __shared__ int s_g;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.num_groups + THREADS - 1) / THREADS;
+  const int g0 = min(a.num_groups, tid * per), g1 = min(a.num_groups, g0 + per);
+  const auto tiles_of = [&](int g) {
+    const Group r = group_of<KT, ROWS>(a, g);
+    return (int64_t)r.row_tiles * a.Hkv * r.tiles;
+  };
+  int64_t mine = 0;
+  for (int g = g0; g < g1; ++g) mine += tiles_of(g);
+  int64_t scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += up;
+  }
+  if (lane == 31) s_warp[warp] = scan;
+  __syncthreads();
+  int64_t prior = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) prior += s_warp[w];
+    total += s_warp[w];
+  }
+  Place p;
+  if (!p.cut(total, c, ctas)) return p;  // the whole block
+  int64_t before = prior + scan - mine;
+  if (p.start < p.stop && p.start >= before && p.start < before + mine) {
+    int g = g0;
+    for (; g < g1 - 1; ++g) {
+      const int64_t t = tiles_of(g);
+      if (p.start < before + t) break;
+      before += t;
+    }
+    s_g = g;
+    s_before = before;
+  }
+  __syncthreads();
+  p.n = s_g;
+  p.before = s_before;
+  return p;
+}
+
 // out[h][d] of a finished head from its sum of weights and unnormalised output.
 __device__ __forceinline__ float finished(float o, float l) { return l == 0.f ? 0.f : o / l; }
 __device__ __forceinline__ float log_sum(float m, float l) {
@@ -204,10 +351,6 @@ __device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
   return note;
 }
 
-// What another kernel that joins a result needs: the piece that began it and how
-// many after that hold more of it, at row `row`.
-__device__ __forceinline__ int2 part_note(int piece, int more, int row) { return make_int2(piece, more << 8 | row); }
-
 // 16 bytes to shared memory; zeros where live is false (src is then not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -226,7 +369,7 @@ __device__ __forceinline__ void copy_wait() {
 // stages.  The pages of a stage are looked up two stages before it is issued,
 // so that the table's latency is not in the way.  Positions not attended to
 // become zeros.  SWIZZLE puts 16-byte chunk c of row r at c ^ (r & 7).
-template <typename T, int D, int KEYS, int STAGES, int WARPS, bool SWIZZLE>
+template <typename T, int D, int KEYS, int STAGES, int WARPS, bool SWIZZLE, typename W = Walk>
 struct PageCopies {
   static constexpr int SUBS = kTile / WARPS / KEYS;
   static constexpr int ROW = D * (int)sizeof(T);
@@ -253,7 +396,7 @@ struct PageCopies {
     int page, token, head;  // of this lane's position (page 0: none) and of the stage; head -1: no stage
   };
   Look next, second;
-  Walk at;  // of the next look-up
+  W at;  // of the next look-up
   int sub;
 
   __device__ __forceinline__ PageCopies(const AttendArgs& a_, const Place& p, Notes& n, const void* ring_, int units_,

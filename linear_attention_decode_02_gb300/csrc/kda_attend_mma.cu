@@ -293,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     }
 
     if constexpr (PARTS) {
-      leave_parts<D, HG, kWarps, RS>(a, walk, place, o, m, l, groups, warp, g, t4, c);
+      const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG;
+      leave_parts<D, HG, kWarps, RS>(a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; },
+                                     min(HG, G - g0), o, m, l, warp, g, t4, c);
     } else {
       finish_unit<D, HG, kWarps, RS>(a, walk, place, ws, reinterpret_cast<float*>(smem + kWarps * Copies::RING),
                                      s_m[parity], s_l[parity], o, m, l, groups, warp, g, t4, c);
@@ -315,7 +317,7 @@ cudaError_t launch_parts(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
 }
 template <int D, int HG>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  return a.first_o != nullptr ? launch_parts<D, HG, true>(a, p, s) : launch_parts<D, HG, false>(a, p, s);
+  return a.skip != nullptr ? launch_parts<D, HG, true>(a, p, s) : launch_parts<D, HG, false>(a, p, s);
 }
 
 }  // namespace

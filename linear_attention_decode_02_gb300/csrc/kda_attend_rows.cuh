@@ -108,13 +108,13 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
 
 // Leaves each warp's own part of a unit, and goes on, where another kernel joins
 // all parts: sequences' own positions are often few, and for the block to meet at the
-// end of each took as long as 150 of them.  Arguments as of finish_unit.
-template <int D, int HG, int WARPS, int RS>
-__device__ __forceinline__ void leave_parts(const AttendArgs& a, const Walk& walk, const Place& place,
-                                            float (&o)[D / 8][4], float (&m)[RS], float (&l)[RS], int groups, int warp,
-                                            int g, int t4, int c) {
+// end of each took as long as 150 of them.  head_of(h) is row h's place among the
+// N * Hq, below 0 for rows that take no part; the other arguments as of finish_unit.
+template <int D, int HG, int WARPS, int RS, typename W, typename HeadOf>
+__device__ __forceinline__ void leave_parts(const AttendArgs& a, const W& walk, const Place& place, const HeadOf& head_of,
+                                            int rows, float (&o)[D / 8][4], float (&m)[RS], float (&l)[RS], int warp, int g,
+                                            int t4, int c) {
   constexpr bool PAIR = HG == 8;
-  const int G = a.Hq / a.Hkv, hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG, heads = min(HG, G - g0);
   const bool first = walk.unit_start >= place.start;
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
@@ -124,19 +124,20 @@ __device__ __forceinline__ void leave_parts(const AttendArgs& a, const Walk& wal
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
     const int h = g + 8 * r;
-    if (h >= heads) continue;
-    const int64_t head = (int64_t)walk.n * a.Hq + hk * G + g0 + h;
+    if (h >= rows) continue;
+    const int64_t head = head_of(h);
+    if (head < 0) continue;
     const int64_t at = first ? (int64_t)warp * a.N * a.Hq + head : ((int64_t)c * WARPS + warp) * HG + h;
-    float* to = (first ? a.first_o : a.more_o) + at * D + 2 * t4;
+    float* to = (first ? a.parts.first_o : a.parts.more_o) + at * D + 2 * t4;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
       *reinterpret_cast<float2*>(to + 8 * i) =
           PAIR ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]) : make_float2(o[i][2 * r], o[i][2 * r + 1]);
     if (t4 == 0) {
-      (first ? a.first_ml : a.more_ml)[at] = make_float2(m[r], l[r]);
+      (first ? a.parts.first_ml : a.parts.more_ml)[at] = make_float2(m[r], l[r]);
       if (first && warp == 0) {
         const int pieces = pieces_of(place.T, gridDim.x);
-        a.first_note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
+        a.parts.first_note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
       }
     }
   }

@@ -29,6 +29,8 @@
 // into the 16-byte chunks, and the second product takes its positions in the
 // order in which the first leaves the weights (2 t, 2 t + 1 for lane t of four).
 // Both meet every bank once.
+#include <type_traits>
+
 #include "kda_attend_rows.cuh"
 
 namespace kda {
@@ -42,7 +44,9 @@ template <int D>
 struct Shape {
   static constexpr int WARPS = D == 256 ? 4 : 8, THREADS = 32 * WARPS;
   static constexpr int STAGES = D == 64 ? 6 : 3;
-  using Copies = PageCopies<float, D, kKeys, STAGES, WARPS, true>;
+  template <typename W>
+  using CopiesOver = PageCopies<float, D, kKeys, STAGES, WARPS, true, W>;
+  using Copies = CopiesOver<Walk>;
 };
 // Queries of a unit (both parts), then, when they are done with, the outputs that its warps exchange.
 template <int D, int HG>
@@ -83,9 +87,16 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int HG>
+// Whose positions a launch is over, and where results go: sequences', to out or the
+// join of pieces; sequences' own under a shared prefix, or groups' common ones, as
+// parts of another kernel's join.
+enum class Over { kSequences, kOwn, kGroups };
+
+template <int D, int HG, Over OVER>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(const __grid_constant__ AttendArgs a) {
-  using Copies = typename Shape<D>::Copies;
+  constexpr bool GROUPS = OVER == Over::kGroups;
+  using W = std::conditional_t<GROUPS, GroupWalk<kTile, HG>, Walk>;
+  using Copies = typename Shape<D>::template CopiesOver<W>;
   constexpr int WARPS = Shape<D>::WARPS, THREADS = Shape<D>::THREADS, STAGES = Shape<D>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 8, NT = D / 8;
   constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
@@ -96,18 +107,22 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   __shared__ float s_m[2][WARPS][HG], s_l[2][WARPS][HG];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
+  // Of a sequence, `groups` units a key head; of a group, the walk counts row tiles by itself.
+  const int G = a.Hq / a.Hkv, groups = GROUPS ? 1 : (G + HG - 1) / HG, units = a.Hkv * groups;
   const int C = gridDim.x, c = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
-  const Place place = find_place<THREADS>(a, units, c, C);
+  if constexpr (GROUPS) mark_sequences(a, c * WARPS + warp, C * WARPS, lane);
+  Place place;
+  if constexpr (GROUPS) place = find_group_place<THREADS, kTile, HG>(a, c, C);
+  else place = find_place<THREADS>(a, units, c, C);
   const Workspace ws(a.work, C, HG, D);
   if (place.start == place.stop) {
-    if (threadIdx.x == 0) ws.note[c].n = -1;
+    if (OVER == Over::kSequences && threadIdx.x == 0) ws.note[c].n = -1;
     return;
   }
 
-  Walk walk;
+  W walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
   // Queries of the next unit, on their way while this one is worked on; in
@@ -117,18 +132,26 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   constexpr int SHARE = (HG * D / 4 + THREADS - 1) / THREADS;
   float4 q_next[SHARE];
   char* const tail = smem + WARPS * Copies::RING;
-  const auto q_row = [&](const Walk& w) {
-    const int hk = w.group / groups;
-    return static_cast<const float*>(a.q) + w.n * a.q_rs + (hk * G + (w.group - hk * groups) * HG) * a.q_hs;
+  // Row h of a unit, and how many rows it has.
+  const auto q_row = [&](const W& w, int h) {
+    if constexpr (GROUPS) {
+      const int2 at = w.row(a, h);
+      return static_cast<const float*>(a.q) + at.x * a.q_rs + at.y * a.q_hs;
+    } else {
+      const int hk = w.group / groups;
+      return static_cast<const float*>(a.q) + w.n * a.q_rs + (hk * G + (w.group - hk * groups) * HG + h) * a.q_hs;
+    }
   };
-  const auto heads_of = [&](const Walk& w) { return min(HG, G - w.group % groups * HG); };
-  const auto load_q = [&](const Walk& w) {
-    const float* q = q_row(w);
-    const int heads = heads_of(w);
+  const auto rows_of = [&](const W& w) {
+    if constexpr (GROUPS) return min(HG, w.rows_left());
+    else return min(HG, G - w.group % groups * HG);
+  };
+  const auto load_q = [&](const W& w) {
+    const int rows = rows_of(w);
 #pragma unroll
     for (int i = 0; i < SHARE; ++i) {
       const int h = (i * THREADS + threadIdx.x) / (D / 4), chunk = (i * THREADS + threadIdx.x) % (D / 4);
-      q_next[i] = h < heads ? __ldg(reinterpret_cast<const float4*>(q + h * a.q_hs) + chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
+      q_next[i] = h < rows ? __ldg(reinterpret_cast<const float4*>(q_row(w, h)) + chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   const auto place_q = [&]() {
@@ -172,7 +195,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   while (walk.tile < place.stop) {
     __syncthreads();  // all have taken the last unit's outputs
     place_q();
-    Walk after = walk;
+    W after = walk;
     if (walk.unit_end < place.stop) {
       after.next_unit(a, units);
       load_q(after);
@@ -229,7 +252,6 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
             lost = lost || p[r][j] != p[r][j];
           }
         if (__any_sync(0xffffffffu, lost)) {
-          const float* q = q_row(walk);
 #pragma unroll
           for (int r = 0; r < RS; ++r)
 #pragma unroll 1
@@ -237,10 +259,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
               float sum = 0.f;
               const float had = j == 0 ? p[r][0] : p[r][1];
               if (had == had) continue;  // other heads and positions keep their bits
-              if (g + 8 * r < heads_of(walk)) {
+              if (g + 8 * r < rows_of(walk)) {
+                const float* q = q_row(walk, g + 8 * r);
 #pragma unroll 1
                 for (int d = 0; d < D; ++d)
-                  sum = fmaf(__ldg(q + (g + 8 * r) * a.q_hs + d),
+                  sum = fmaf(__ldg(q + d),
                              word(base + (2 * t4 + j) * ROW + (((d >> 2) ^ (2 * t4 + j)) << 4) + (d & 3) * 4), sum);
               }
               (j == 0 ? p[r][0] : p[r][1]) = sum;
@@ -304,8 +327,22 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
         }
       }
     }
-    finish_unit<D, HG, WARPS, RS>(a, walk, place, ws, reinterpret_cast<float*>(tail), s_m[parity], s_l[parity], o, m, l,
-                                  groups, warp, g, t4, c);
+    if constexpr (GROUPS) {
+      leave_parts<D, HG, WARPS, RS>(
+          a, walk, place,
+          [&](int h) -> int64_t {
+            const int2 at = walk.row(a, h);
+            return takes_part(a, at.x, walk.of.prefix) ? (int64_t)at.x * a.Hq + at.y : -1;
+          },
+          rows_of(walk), o, m, l, warp, g, t4, c);
+    } else if constexpr (OVER == Over::kOwn) {
+      const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG;
+      leave_parts<D, HG, WARPS, RS>(a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; },
+                                    min(HG, G - g0), o, m, l, warp, g, t4, c);
+    } else {
+      finish_unit<D, HG, WARPS, RS>(a, walk, place, ws, reinterpret_cast<float*>(tail), s_m[parity], s_l[parity], o, m, l,
+                                    groups, warp, g, t4, c);
+    }
     parity ^= 1;
     after.tile = walk.tile;
     walk = after;
@@ -313,13 +350,25 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   copy_wait<0>();
 }
 
-template <int D, int HG>
+template <int D, int HG, Over OVER>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   constexpr int bytes = smem_bytes<D, HG>();
   static std::atomic<bool> set[64];
-  const cudaError_t e = allow_shared(kda_attend_tf32_kernel<D, HG>, bytes, set);
+  const cudaError_t e = allow_shared(kda_attend_tf32_kernel<D, HG, OVER>, bytes, set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kda_attend_tf32_kernel<D, HG>, dim3(p.ctas), dim3(Shape<D>::THREADS), bytes, s, 1, a);
+  return launch_pdl(kda_attend_tf32_kernel<D, HG, OVER>, dim3(p.ctas), dim3(Shape<D>::THREADS), bytes, s, 1, a);
+}
+template <Over OVER>
+cudaError_t launch_over(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  switch (a.D * 16 + p.heads - 1) {
+    case 64 * 16 + 7: return launch<64, 8, OVER>(a, p, s);
+    case 64 * 16 + 15: return launch<64, 16, OVER>(a, p, s);
+    case 128 * 16 + 7: return launch<128, 8, OVER>(a, p, s);
+    case 128 * 16 + 15: return launch<128, 16, OVER>(a, p, s);
+    case 256 * 16 + 7: return launch<256, 8, OVER>(a, p, s);
+    case 256 * 16 + 15: return launch<256, 16, OVER>(a, p, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
@@ -332,16 +381,13 @@ AttendPlan attend_tf32_plan(int32_t G, int32_t D, int32_t sms) {
   return p;
 }
 
+int attend_tf32_warps(int32_t D) { return D == 256 ? Shape<256>::WARPS : Shape<128>::WARPS; }
+
 cudaError_t launch_attend_tf32(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  switch (a.D * 16 + p.heads - 1) {
-    case 64 * 16 + 7: return launch<64, 8>(a, p, s);
-    case 64 * 16 + 15: return launch<64, 16>(a, p, s);
-    case 128 * 16 + 7: return launch<128, 8>(a, p, s);
-    case 128 * 16 + 15: return launch<128, 16>(a, p, s);
-    case 256 * 16 + 7: return launch<256, 8>(a, p, s);
-    case 256 * 16 + 15: return launch<256, 16>(a, p, s);
-    default: return cudaErrorInvalidValue;
-  }
+  return a.skip != nullptr ? launch_over<Over::kOwn>(a, p, s) : launch_over<Over::kSequences>(a, p, s);
+}
+cudaError_t launch_attend_tf32_groups(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  return launch_over<Over::kGroups>(a, p, s);
 }
 
 }  // namespace kda

@@ -78,6 +78,17 @@ struct PagesArgs {
 };
 cudaError_t launch_page_assign(const PagesArgs& a, cudaStream_t s);
 
+// Parts of results that another kernel joins: unnormalised outputs with their
+// row's maximum (units of log 2) and sum.  The piece that begins a unit leaves
+// part [warp][row of the batch's N * Hq] with a note of that piece, how many more
+// follow and the row's place in the unit (part_note); piece c of those that follow
+// leaves part [c][warp][place].
+struct Parts {
+  float* first_o; float2* first_ml; int2* first_note;
+  float* more_o; float2* more_ml;
+  int32_t ctas, warps, rows;  // pieces, parts a piece and places a unit
+};
+
 // Attention of one new token per sequence over paged keys and values.
 struct AttendArgs {
   const void* q; int64_t q_rs, q_hs;      // [N, Hq, D]
@@ -92,12 +103,13 @@ struct AttendArgs {
   int32_t window;                         // 0: all
   float scale_log2;                       // scale * log2(e)
   int32_t vec16;                          // q rows, key and value vectors start on 16-byte boundaries
-  // Under a shared prefix: the first positions of each sequence that are attended to elsewhere, and where each warp's
-  // part of a unit goes instead of out and lse: of the piece that begins it, [kAttendWarps, N, Hq(, D)] with that piece
-  // and how many follow, [N, Hq]; of those that follow, [ctas, kAttendWarps, heads(, D)].  Null otherwise.
+  // Under shared prefixes (null otherwise).  Group g is sequences starts[g] .. starts[g + 1] - 1, whose first
+  // prefix_lens[g] positions are attended to by one kernel, which notes in `mark` how many those are for each sequence;
+  // the other leaves out the first `skip` positions of each.  Both leave parts.
+  const int32_t* starts; const int32_t* prefix_lens; int32_t num_groups;
+  int32_t* mark;
   const int32_t* skip;
-  float* first_o; float2* first_ml; int2* first_note;
-  float* more_o; float2* more_ml;
+  Parts parts;
 };
 constexpr int kAttendWarps = 4;  // of a block of the tensor-core kernel
 
@@ -111,15 +123,9 @@ struct AttendPlan {
 int64_t attend_floats(int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
 cudaError_t launch_paged_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
 
-// Attention of sequences that share prefixes, group by group.
-struct PrefixArgs {
-  AttendArgs attend;
-  const int32_t* starts;                  // [G + 1]: group g is sequences starts[g] .. starts[g + 1] - 1
-  const int32_t* prefix_lens;             // [G]
-  int32_t G;
-};
+// Attention of sequences that share prefixes, group by group (starts, prefix_lens and num_groups set).
 int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms);
-cudaError_t launch_prefix_attention(const PrefixArgs& a, int32_t sms, cudaStream_t s);
+cudaError_t launch_prefix_attention(const AttendArgs& a, int32_t sms, cudaStream_t s);
 
 // Beam selection over beams x vocabulary.
 constexpr int kBeamMax = 32;      // beams of a request

@@ -164,8 +164,8 @@ kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_
                                        const kda_tensor* lse, void* stream) {
   AttentionViews v;
   View S, P;
-  kda::PrefixArgs a{};
-  KDA_TRY(check_attention(q, k_pages, v_pages, page_table, seq_lens, workspace, window, scale, out, lse, &v, &a.attend));
+  kda::AttendArgs a{};
+  KDA_TRY(check_attention(q, k_pages, v_pages, page_table, seq_lens, workspace, window, scale, out, lse, &v, &a));
   KDA_TRY(check_prefix_sequences(v.Q.shape[0]));
   KDA_TRY(raw_view(group_starts, "group_starts", &S));
   KDA_TRY(raw_view(prefix_lens, "prefix_lens", &P));
@@ -177,18 +177,17 @@ kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_
   KDA_TRY(no_shared_bytes(v.O, {&S, &P}));
   KDA_TRY(no_shared_bytes(v.W, {&S, &P}));
   KDA_TRY(no_shared_bytes(v.E, {&S, &P}));
-  if (a.attend.N == 0) return KDA_OK;
+  if (a.N == 0) return KDA_OK;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DeviceInfo dev;
   KDA_TRY(current_device(st, &dev));
-  const kda::AttendArgs& t = a.attend;
-  const int64_t floats = kda::prefix_floats(t.N, t.Hq, t.Hkv, t.D, t.dtype, dev.sms);
+  const int64_t floats = kda::prefix_floats(a.N, a.Hq, a.Hkv, a.D, a.dtype, dev.sms);
   KDA_CHECK(v.W.shape[0] >= floats, KDA_ERR_INVALID_ARG, "workspace: %lld floats, this call needs %lld",
             (long long)v.W.shape[0], (long long)floats);
   a.starts = reinterpret_cast<const int32_t*>(S.data);
   a.prefix_lens = reinterpret_cast<const int32_t*>(P.data);
-  a.G = (int32_t)G;
+  a.num_groups = (int32_t)G;
   return check_launch(kda::launch_prefix_attention(a, dev.sms, st));
 }
 

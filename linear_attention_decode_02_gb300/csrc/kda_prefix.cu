@@ -77,75 +77,6 @@ struct PrefixShape {
   static_assert(SLOTS / 2 + 4 <= kLiveDepth, "ring");
 };
 
-struct PrefixWork {
-  int2* note;     // [N * Hq]
-  float2* first;  // [N * Hq]
-  float* o;       // [N * Hq][D]
-  float2* ml;     // [ctas][RT * 128]: continued units
-  float* more;    // [ctas][RT * 128][D]
-  int32_t* skip;  // [N]
-};
-
-// Groups' sequences and tiles.
-struct Group {
-  int first, rows, prefix, tiles, row_tiles;  // sequences first .. ; query rows of a key head; positions
-  __device__ __forceinline__ int64_t units(int Hkv) const { return (int64_t)row_tiles * Hkv; }
-};
-template <int KT, int ROWS>
-__device__ __forceinline__ Group group_of(const PrefixArgs& a, int g) {
-  const AttendArgs& at = a.attend;
-  Group r;
-  r.first = min(max(__ldg(a.starts + g), 0), at.N);
-  const int end = min(max(__ldg(a.starts + g + 1), r.first), at.N);
-  const int64_t cap = (int64_t)at.table_cols * at.page_size;
-  r.prefix = (int)min((int64_t)max(__ldg(a.prefix_lens + g), 0), cap);
-  r.rows = (end - r.first) * (at.Hq / at.Hkv);
-  r.tiles = (r.prefix + KT - 1) / KT;
-  r.row_tiles = r.tiles > 0 ? (r.rows + ROWS - 1) / ROWS : 0;
-  return r;
-}
-
-// A sequence takes part in its group's common positions where it attends to all of them.
-__device__ __forceinline__ bool takes_part(const AttendArgs& a, int n, int prefix) {
-  const int64_t cap = (int64_t)a.table_cols * a.page_size;
-  const int len = __ldg(a.lens + n);
-  return prefix > 0 && min((int64_t)max(len, 0), cap) >= prefix && (a.window == 0 || len <= a.window);
-}
-
-// Where a walk over the piece's tiles stands.
-template <int KT, int ROWS>
-struct PrefixWalk {
-  int64_t tile, unit_start, unit_end;
-  int g, head, row_tile;
-  Group group;
-  __device__ __forceinline__ void start(const PrefixArgs& a, int64_t tile_, int g_, int64_t before) {
-    tile = tile_;
-    g = g_;
-    group = group_of<KT, ROWS>(a, g);
-    const int64_t u = quotient(tile - before, group.tiles);
-    head = (int)quotient(u, group.row_tiles);
-    row_tile = (int)(u - (int64_t)head * group.row_tiles);
-    unit_start = before + u * group.tiles;
-    unit_end = unit_start + group.tiles;
-  }
-  // False behind the last unit.
-  __device__ __forceinline__ void next_unit(const PrefixArgs& a) {
-    unit_start = unit_end;
-    if (++row_tile == group.row_tiles) {
-      row_tile = 0;
-      if (++head == a.attend.Hkv) {
-        head = 0;
-        do {
-          if (++g >= a.G) return;
-          group = group_of<KT, ROWS>(a, g);
-        } while (group.row_tiles == 0);
-      }
-    }
-    unit_end = unit_start + group.tiles;
-  }
-  __device__ __forceinline__ int rows_left() const { return group.rows - row_tile * ROWS; }
-};
-
 // Registers of the four warps of a group: up to N, down to -N, 0: as they are.
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -168,11 +99,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 template <int D, int RT>
 __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
-    kda_prefix_kernel(const __grid_constant__ PrefixArgs a, const PrefixWork ws, int box,
+    kda_prefix_kernel(const __grid_constant__ AttendArgs a, int box,
                       const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using P = PrefixShape<D, RT>;
   constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, LANES = P::LANES, WARPS = P::THREADS / 32;
-  using Walker = PrefixWalk<KT, ROWS>;
+  using Walker = GroupWalk<KT, ROWS>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                        ~static_cast<uintptr_t>(1023));
@@ -184,11 +115,8 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   __shared__ __align__(8) uint32_t s_live[kLiveDepth][KT / 32];
   __shared__ uint32_t s_taddr;
   __shared__ volatile int s_abort;
-  __shared__ int64_t s_warp[WARPS], s_before;
-  __shared__ int s_g;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const AttendArgs& at = a.attend;
-  const int C = gridDim.x, c = blockIdx.x, G = at.Hq / at.Hkv;
+  const int C = gridDim.x, c = blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
@@ -214,48 +142,11 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // The piece: groups' tiles summed by the whole block.
-  const int per = (a.G + P::THREADS - 1) / P::THREADS;
-  const int g0 = min(a.G, tid * per), g1 = min(a.G, g0 + per);
-  const auto tiles_of = [&](int g) {
-    const Group r = group_of<KT, ROWS>(a, g);
-    return r.units(at.Hkv) * r.tiles;
-  };
-  int64_t mine = 0;
-  for (int g = g0; g < g1; ++g) mine += tiles_of(g);
-  int64_t scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += up;
-  }
-  if (lane == 31) s_warp[warp] = scan;
   tc::fence_before_sync();
-  __syncthreads();
+  const Place piece = find_group_place<P::THREADS, KT, ROWS>(a, c, C);  // every thread passes a barrier in it
   tc::fence_after_sync();
   const uint32_t taddr = s_taddr;
-  int64_t prior = 0, T = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) prior += s_warp[w];
-    T += s_warp[w];
-  }
-  const int pieces = pieces_of(T, C);
-  const int64_t start = c < pieces ? piece_start(c, T, pieces) : 0, stop = c < pieces ? piece_start(c + 1, T, pieces) : 0;
-  {
-    int64_t before = prior + scan - mine;
-    if (start < stop && start >= before && start < before + mine) {
-      int g = g0;
-      for (; g < g1 - 1; ++g) {
-        const int64_t t = tiles_of(g);
-        if (start < before + t) break;
-        before += t;
-      }
-      s_g = g;
-      s_before = before;
-    }
-  }
-  __syncthreads();
+  const int64_t start = piece.start, stop = piece.stop;
 
   // Nearly every wait ends with its first try, which looks at nothing else.
   auto wait_or_abort = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -271,26 +162,12 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   };
   const bool any = start < stop;
   Walker walk;
-  if (any) walk.start(a, start, s_g, s_before);
+  if (any) walk.start(a, piece);
 
   if (warp < 4 * LANES) {
     more_registers<LANES == 1 ? 0 : 144>();
     // ---------------- which sequences take part, and softmax ----------------
-    for (int n = c * 4 * LANES + warp; n < at.N; n += C * 4 * LANES) {
-      const int g = find_sequence(a.starts, a.G, n, lane);
-      bool part = false;
-      int prefix = 0;
-      if (g < a.G && n >= __ldg(a.starts + g)) {
-        prefix = group_of<KT, ROWS>(a, g).prefix;
-        part = takes_part(at, n, prefix);
-      }
-      if (lane == 0) ws.skip[n] = part ? prefix : 0;
-      if (!part)
-        for (int h = lane; h < at.Hq; h += 32) {
-          ws.note[(int64_t)n * at.Hq + h] = part_note(0, 0, 0);
-          ws.first[(int64_t)n * at.Hq + h] = make_float2(-INFINITY, 0.f);
-        }
-    }
+    mark_sequences(a, c * 4 * LANES + warp, C * 4 * LANES, lane);
     const int me = LANES == 1 ? 0 : warp >> 2;   // lane of the CTA
     const int row_tile = RT == 1 ? 0 : me;
     const int row = (warp & 3) * 32 + lane;      // of the row tile, and tensor-memory lane
@@ -316,7 +193,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         tc::fence_after_sync();
         if (!idle) {
           const uint32_t s_addr = tl + P::S_COL + b * KT;
-          const float2 scale2 = dup2(at.scale_log2), minus2 = dup2(-1.f);
+          const float2 scale2 = dup2(a.scale_log2), minus2 = dup2(-1.f);
           float2 sum[4] = {dup2(0.f), dup2(0.f), dup2(0.f), dup2(0.f)};
           // 64 positions from k on.
           const auto weigh = [&](int k) -> bool {
@@ -337,7 +214,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
                 tops[e] = max3(tops[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
               tops[e] = fmaxf(tops[e], __uint_as_float(x[60 + e]));
             }
-            const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * at.scale_log2;
+            const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale_log2;
             const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, rises)) {
               // The reference rises by whole steps, so what is weighted already moves exactly.
@@ -443,21 +320,18 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           m = top;
         }
         if (!idle) {
-          const int i = walk.row_tile * ROWS + row_tile * kRows + row;  // query row
-          const int n = walk.group.first + i / G;
-          const bool mine = row < valid && takes_part(at, n, walk.group.prefix);
+          const int r = row_tile * kRows + row;  // of the unit
+          const int2 of = walk.row(a, r);
+          const bool mine = row < valid && takes_part(a, of.x, walk.of.prefix);
           float* dst = nullptr;
           if (mine) {
-            const int64_t head = (int64_t)n * at.Hq + walk.head * G + i % G;
+            const int64_t head = (int64_t)of.x * a.Hq + of.y, later = (int64_t)c * ROWS + r;
             if (begins) {
-              ws.note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, T, pieces) - c, row_tile * kRows + row);
-              ws.first[head] = make_float2(m, l);
-              dst = ws.o + head * D;
-            } else {
-              const int64_t at_piece = (int64_t)c * ROWS + row_tile * kRows + row;
-              ws.ml[at_piece] = make_float2(m, l);
-              dst = ws.more + at_piece * D;
+              const int pieces = pieces_of(piece.T, C);
+              a.parts.first_note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, piece.T, pieces) - c, r);
             }
+            (begins ? a.parts.first_ml[head] : a.parts.more_ml[later]) = make_float2(m, l);
+            dst = begins ? a.parts.first_o + head * D : a.parts.more_o + later * D;
           }
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
@@ -623,12 +497,12 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       Look l{0, 0, 0};
       if (ahead.tile < stop) {
         const int t = (int)(ahead.tile - ahead.unit_start) * KT + lw * WARP_ROWS + lane;
-        if (lane < WARP_ROWS && t < ahead.group.prefix) {
-          const int col = t / at.page_size;
-          l.token = t - col * at.page_size;
-          l.page = __ldg(at.table + (int64_t)ahead.group.first * at.table_rs + col);
+        if (lane < WARP_ROWS && t < ahead.of.prefix) {
+          const int col = t / a.page_size;
+          l.token = t - col * a.page_size;
+          l.page = __ldg(a.table + (int64_t)ahead.of.first * a.table_rs + col);
         }
-        l.head = ahead.head;
+        l.head = ahead.group;
         if (++ahead.tile == ahead.unit_end) ahead.next_unit(a);
       }
       return l;
@@ -676,17 +550,18 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         const int left = min(walk.rows_left(), ROWS), rows = (left + 31) & ~31;
         for (int i = tid - P::LOADER0 * 32; i < rows * CHUNKS; i += kLoaders) {
           const int row = i / CHUNKS, ch = i % CHUNKS;
-          const int q = walk.row_tile * ROWS + row;
           const bool real = row < left;
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(at.q);
-          if (real)
-            src += (int64_t)(walk.group.first + q / G) * at.q_rs + (int64_t)(walk.head * G + q % G) * at.q_hs + ch * 8;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
+          if (real) {
+            const int2 of = walk.row(a, row);
+            src += of.x * a.q_rs + of.y * a.q_hs + ch * 8;
+          }
           copy16(q_addr + (q_slot * RT + row / kRows) * P::Q_TILE + place(row % kRows, ch, kRows), src, real);
         }
       }
       for (; walk.tile < end; ++walk.tile, ++tile) {
         const Look next = look_up();
-        const bool live = look.page > 0 && look.page < at.num_pages;
+        const bool live = look.page > 0 && look.page < a.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, live);
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
         if (WARP_ROWS == 32) {
@@ -695,9 +570,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           reinterpret_cast<uint16_t*>(s_live[tile % kLiveDepth])[lw] = (uint16_t)mask;
         }
         if (lane == 0) mbar_arrive(&live_full[tile % kLiveDepth]);
-        copy_half(at.kp, &k_map, look, mask);
+        copy_half(a.kp, &k_map, look, mask);
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
-        copy_half(at.vp, &v_map, look, mask);
+        copy_half(a.vp, &v_map, look, mask);
         look = next;
       }
       if (!run) break;
@@ -719,12 +594,12 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   }
 }
 
-// Joins the parts of one query head of a sequence: of the common positions a first
-// one and those of later pieces, of its own the same from each warp.  WARPS warps
-// share the parts; a block of four warps joins one head or four.
+// Joins the parts of one query head of a sequence, `pre` of the common positions
+// and `own` of its own.  WARPS warps share the parts; a block of four warps joins one
+// head or four.
 template <int D, int WARPS>
-__global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_constant__ AttendArgs a, const PrefixWork pre,
-                                                              int ctas, int own_rows, int pre_ctas, int pre_rows) {
+__global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_constant__ AttendArgs a, const Parts pre,
+                                                              const Parts own) {
   constexpr int VEC = D / 32, AHEAD = 4;
   __shared__ float s_m[4], s_l[4], s_o[WARPS > 1 ? 4 : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -732,20 +607,18 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
   pdl_launch_dependents();
   const int64_t heads = (int64_t)a.N * a.Hq, head = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
   if (head >= heads) return;
-  const int2 notes[2] = {pre.note[head], a.first_note[head]};
+  const int2 notes[2] = {pre.first_note[head], own.first_note[head]};
   // A kernel that gave up a wait has left notes that say anything: no part outside the workspace is read for them.
   int piece[2], row[2], more[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int last = (w == 0 ? pre_ctas : ctas) - 1;
+    const Parts& p = w == 0 ? pre : own;
     piece[w] = notes[w].x;
     row[w] = notes[w].y & 255;
     more[w] = notes[w].y >> 8;
-    if (piece[w] < 0 || more[w] < 0 || piece[w] > last || more[w] > last - piece[w] ||
-        row[w] >= (w == 0 ? pre_rows : own_rows))
-      more[w] = 0;
+    if (piece[w] < 0 || more[w] < 0 || piece[w] >= p.ctas || more[w] >= p.ctas - piece[w] || row[w] >= p.rows) more[w] = 0;
   }
-  const int parts0 = 1 + more[0], parts = parts0 + kAttendWarps * (1 + more[1]);
+  const int parts0 = pre.warps * (1 + more[0]), parts = parts0 + own.warps * (1 + more[1]);
   float m = -INFINITY, l = 0.f, o[VEC] = {};
 #pragma unroll 1
   for (int i = WARPS == 1 ? 0 : warp; i < parts; i += WARPS * AHEAD) {
@@ -753,20 +626,20 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
     const float* from[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
-      const int p = i + k * WARPS;
+      const int q = i + k * WARPS;
       pm[k] = -INFINITY;
       pl[k] = 0.f;
       from[k] = nullptr;
-      if (p < parts) {
-        const bool w = p >= parts0;
-        const int q = w ? p - parts0 : p, j = w ? q / kAttendWarps : q, by = w ? q % kAttendWarps : 0;
-        const int64_t place = j == 0 ? by * heads + head
-                                     : (w ? ((int64_t)(piece[1] + j) * kAttendWarps + by) * own_rows + row[1]
-                                          : (int64_t)(piece[0] + j) * pre_rows + row[0]);
-        const float2 ml = (w ? (j == 0 ? a.first_ml : a.more_ml) : (j == 0 ? pre.first : pre.ml))[place];
+      if (q < parts) {
+        const bool w = q >= parts0;
+        const Parts& p = w ? own : pre;
+        const int at = w ? q - parts0 : q, j = at / p.warps, by = at - j * p.warps;
+        const int64_t place =
+            j == 0 ? by * heads + head : ((int64_t)((w ? piece[1] : piece[0]) + j) * p.warps + by) * p.rows + (w ? row[1] : row[0]);
+        const float2 ml = (j == 0 ? p.first_ml : p.more_ml)[place];
         pm[k] = ml.x;
         pl[k] = ml.y;
-        from[k] = (w ? (j == 0 ? a.first_o : a.more_o) : (j == 0 ? pre.o : pre.more)) + place * D;
+        from[k] = (j == 0 ? p.first_o : p.more_o) + place * D;
       }
     }
 #pragma unroll
@@ -832,33 +705,54 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
   }
 }
 
-// Places of the workspace, in floats: the paged kernel's own, then both kernels'
-// first parts and later ones, and the sequences' skips.
+// The paged kernel's grid for sequences' own positions, the kernel over the groups' common ones, both kernels' parts
+// and the sequences' marks in the workspace, and its size.
 struct PrefixPlan {
-  AttendPlan own;
-  int64_t own_note, own_ml, own_o, own_more_ml, own_more, note, first, o, ml, more, skip, floats;
+  AttendPlan own, pre;
+  Parts own_parts, pre_parts;
+  int32_t* mark;
+  int64_t floats;
 };
-PrefixPlan prefix_plan(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t sms) {
+PrefixPlan prefix_plan(float* work, int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms, int64_t groups) {
   PrefixPlan p;
-  p.own = attend_mma_plan(Hq / Hkv, D, sms);
-  const int64_t heads = N * Hq, rows = (int64_t)sms * 2 * kRows, own = (int64_t)kAttendWarps * p.own.ctas * p.own.heads;
-  int64_t at = p.own.ctas * (int64_t)kNoteFloats;  // the notes that the paged kernel leaves all the same
+  int64_t at = 0;
   const auto take = [&](int64_t floats) {
-    const int64_t r = at;
+    float* r = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(work) + 4 * at);  // work may be null, for the size
     at += (floats + 3) & ~int64_t{3};
     return r;
   };
-  p.own_note = take(2 * heads);
-  p.own_ml = take(2 * kAttendWarps * heads);
-  p.own_o = take(kAttendWarps * heads * D);
-  p.own_more_ml = take(2 * own);
-  p.own_more = take(own * D);
-  p.note = take(2 * heads);
-  p.first = take(2 * heads);
-  p.o = take(heads * D);
-  p.ml = take(2 * rows);
-  p.more = take(rows * D);
-  p.skip = take(N);
+  const int64_t heads = N * Hq;
+  const auto parts = [&](int ctas, int warps, int rows, int most_rows) {
+    Parts r;
+    const int64_t later = (int64_t)ctas * warps * most_rows;
+    r.first_note = reinterpret_cast<int2*>(take(2 * heads));
+    r.first_ml = reinterpret_cast<float2*>(take(2 * warps * heads));
+    r.first_o = take(warps * heads * D);
+    r.more_ml = reinterpret_cast<float2*>(take(2 * later));
+    r.more_o = take(later * D);
+    r.ctas = ctas;
+    r.warps = warps;
+    r.rows = rows;
+    return r;
+  };
+  const int32_t G = Hq / Hkv;
+  // Query rows that a group has a key head, on average, decide how many a unit takes.
+  const double rows = groups > 0 ? (double)N * G / groups : 0;
+  if (dtype == KDA_DT_F32) {
+    p.own = attend_tf32_plan(G, D, sms);
+    p.pre = attend_tf32_plan(rows <= 8 ? 8 : 16, D, sms);
+    take(p.own.ctas * (int64_t)kNoteFloats);
+    p.own_parts = parts(p.own.ctas, attend_tf32_warps(D), p.own.heads, p.own.heads);
+    p.pre_parts = parts(p.pre.ctas, attend_tf32_warps(D), p.pre.heads, 16);
+  } else {
+    p.own = attend_mma_plan(G, D, sms);
+    p.pre.ctas = sms;
+    p.pre.heads = D < 256 && rows > kRows ? 2 * kRows : kRows;
+    take(p.own.ctas * (int64_t)kNoteFloats);  // the notes that the paged kernel leaves all the same
+    p.own_parts = parts(p.own.ctas, kAttendWarps, p.own.heads, p.own.heads);
+    p.pre_parts = parts(p.pre.ctas, 1, p.pre.heads, 2 * kRows);
+  }
+  p.mark = reinterpret_cast<int32_t*>(take(N));
   p.floats = at;
   return p;
 }
@@ -878,30 +772,27 @@ bool encode_pages(CUtensorMap* map, const PageView& p, const AttendArgs& a, int 
 }
 
 template <int D, int RT>
-cudaError_t launch_prefix(const PrefixArgs& a, const PrefixWork& ws, int sms, cudaStream_t s) {
+cudaError_t launch_prefix(const AttendArgs& a, int sms, cudaStream_t s) {
   using P = PrefixShape<D, RT>;
   static std::atomic<bool> set[64];
   const cudaError_t e = allow_shared(kda_prefix_kernel<D, RT>, P::BYTES, set);
   if (e != cudaSuccess) return e;
   // A warp's positions of a tile are whole boxes, of whole eights as the swizzle repeats, and a page whole boxes too.
   CUtensorMap k_map = {}, v_map = {};
-  const AttendArgs& t = a.attend;
   int box = P::KT / 4;
-  if (t.page_size < box) box = t.page_size >= 8 && box % t.page_size == 0 ? t.page_size : 0;
-  if (box > 0 && t.page_size % box != 0) box = 0;
-  if (box > 0 && !(encode_pages(&k_map, t.kp, t, box) && encode_pages(&v_map, t.vp, t, box))) box = 0;
-  return launch_pdl(kda_prefix_kernel<D, RT>, dim3(sms), dim3(P::THREADS), P::BYTES, s, 1, a, ws, box, k_map, v_map);
+  if (a.page_size < box) box = a.page_size >= 8 && box % a.page_size == 0 ? a.page_size : 0;
+  if (box > 0 && a.page_size % box != 0) box = 0;
+  if (box > 0 && !(encode_pages(&k_map, a.kp, a, box) && encode_pages(&v_map, a.vp, a, box))) box = 0;
+  return launch_pdl(kda_prefix_kernel<D, RT>, dim3(sms), dim3(P::THREADS), P::BYTES, s, 1, a, box, k_map, v_map);
 }
 
 template <int D>
-cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixWork& ws, const AttendPlan& own, int rows, int sms,
-                               cudaStream_t s) {
+cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms, cudaStream_t s) {
   const int64_t heads = (int64_t)a.N * a.Hq;
   if (heads >= 16LL * sms)
-    return launch_pdl(kda_prefix_join_kernel<D, 1>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, s, 1, a, ws, own.ctas,
-                      own.heads, sms, rows);
-  return launch_pdl(kda_prefix_join_kernel<D, 4>, dim3((unsigned)heads), dim3(128), 0, s, 1, a, ws, own.ctas,
-                      own.heads, sms, rows);
+    return launch_pdl(kda_prefix_join_kernel<D, 1>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, s, 1, a, p.pre_parts,
+                      p.own_parts);
+  return launch_pdl(kda_prefix_join_kernel<D, 4>, dim3((unsigned)heads), dim3(128), 0, s, 1, a, p.pre_parts, p.own_parts);
 }
 
 }  // namespace
@@ -917,44 +808,31 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixWork& ws, const 
 constexpr int64_t kSharedBytes = 96 << 20;
 
 int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
-  const int64_t paged = attend_floats(Hq, Hkv, D, dtype, sms);
-  return dtype == KDA_DT_F32 ? paged : std::max(paged, prefix_plan(N, Hq, Hkv, D, sms).floats);
+  return std::max(attend_floats(Hq, Hkv, D, dtype, sms), prefix_plan(nullptr, N, Hq, Hkv, D, dtype, sms, 0).floats);
 }
 
-cudaError_t launch_prefix_attention(const PrefixArgs& given, int32_t sms, cudaStream_t s) {
-  PrefixArgs a = given;
-  AttendArgs& t = a.attend;
-  const double most = (double)t.table_cols * t.page_size;
-  if (t.dtype == KDA_DT_F32 || !t.vec16 || (t.N - (double)a.G) * most * t.Hkv * t.D * 4 < kSharedBytes)
-    return launch_paged_attention(t, sms, s);
-  const PrefixPlan p = prefix_plan(t.N, t.Hq, t.Hkv, t.D, sms);
-  PrefixWork ws;
-  ws.note = reinterpret_cast<int2*>(t.work + p.note);
-  ws.first = reinterpret_cast<float2*>(t.work + p.first);
-  ws.o = t.work + p.o;
-  ws.ml = reinterpret_cast<float2*>(t.work + p.ml);
-  ws.more = t.work + p.more;
-  ws.skip = reinterpret_cast<int32_t*>(t.work + p.skip);
-  const bool two = t.D < 256 && (int64_t)t.N * (t.Hq / t.Hkv) > (int64_t)kRows * a.G;
+cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaStream_t s) {
+  AttendArgs a = given;
+  const bool f32 = a.dtype == KDA_DT_F32;
+  const double saved = (a.N - (double)a.num_groups) * a.table_cols * a.page_size * a.Hkv * a.D * (f32 ? 8 : 4);
+  if (!a.vec16 || saved < kSharedBytes) return launch_paged_attention(a, sms, s);
+  const PrefixPlan p = prefix_plan(a.work, a.N, a.Hq, a.Hkv, a.D, a.dtype, sms, a.num_groups);
+  a.parts = p.pre_parts;
+  a.mark = p.mark;
+  const bool two = p.pre.heads > kRows;
   cudaError_t e = cudaErrorInvalidValue;
-  switch (t.D) {
-    case 64: e = two ? launch_prefix<64, 2>(a, ws, sms, s) : launch_prefix<64, 1>(a, ws, sms, s); break;
-    case 128: e = two ? launch_prefix<128, 2>(a, ws, sms, s) : launch_prefix<128, 1>(a, ws, sms, s); break;
-    case 256: e = launch_prefix<256, 1>(a, ws, sms, s); break;
-  }
+  if (f32) e = launch_attend_tf32_groups(a, p.pre, s);
+  else if (a.D == 64) e = two ? launch_prefix<64, 2>(a, sms, s) : launch_prefix<64, 1>(a, sms, s);
+  else if (a.D == 128) e = two ? launch_prefix<128, 2>(a, sms, s) : launch_prefix<128, 1>(a, sms, s);
+  else if (a.D == 256) e = launch_prefix<256, 1>(a, sms, s);
   if (e != cudaSuccess) return e;
-  t.skip = ws.skip;
-  t.first_note = reinterpret_cast<int2*>(t.work + p.own_note);
-  t.first_ml = reinterpret_cast<float2*>(t.work + p.own_ml);
-  t.first_o = t.work + p.own_o;
-  t.more_ml = reinterpret_cast<float2*>(t.work + p.own_more_ml);
-  t.more_o = t.work + p.own_more;
-  e = launch_attend_mma(t, p.own, s);
+  a.parts = p.own_parts;
+  a.skip = p.mark;
+  e = f32 ? launch_attend_tf32(a, p.own, s) : launch_attend_mma(a, p.own, s);
   if (e != cudaSuccess) return e;
-  const int rows = two ? 2 * kRows : kRows;
-  if (t.D == 64) return launch_prefix_join<64>(t, ws, p.own, rows, sms, s);
-  if (t.D == 128) return launch_prefix_join<128>(t, ws, p.own, rows, sms, s);
-  return launch_prefix_join<256>(t, ws, p.own, rows, sms, s);
+  if (a.D == 64) return launch_prefix_join<64>(a, p, sms, s);
+  if (a.D == 128) return launch_prefix_join<128>(a, p, sms, s);
+  return launch_prefix_join<256>(a, p, sms, s);
 }
 
 cudaError_t read_prefix_error(unsigned int* flags, bool clear) {

@@ -98,9 +98,9 @@ def expected(c, window=0, scale=None):
     table = table[:, :max(1, -(-reached // page))]
     places = np.where((table > 0) & (table < pages), table, 0)[:, :, None] * page + np.arange(page)
     places = np.where(places < page, 0, places).reshape(len(lens), -1)
-    shares = (len(lens) - len(c["prefix"])) * cap * k.shape[2] * k.shape[3] * 4 >= SHARED
+    shares = (len(lens) - len(c["prefix"])) * cap * k.shape[2] * k.shape[3] * 2 * c["q"].element_size() >= SHARED
     starts, prefixes = c["starts"].tolist(), c["prefix"].tolist()
-    if c["q"].dtype == BF16 and shares:
+    if shares:
         for first, end, p in zip(starts, starts[1:], prefixes):
             p = min(max(p, 0), cap)
             for n in range(first, end):
@@ -125,52 +125,61 @@ def check(c, window=0, scale=None):
     return out, lse
 
 
-def test_one_small_group():
-    check(make([(128, [1, 2])], Hq=1, Hkv=1))
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_small_group(dtype):
+    check(make([(128, [1, 2])], Hq=1, Hkv=1, dtype=dtype))
 
 
-def test_one_tile_and_a_bit():
-    check(make([(130, [1, 20, 64])], Hq=4, Hkv=2))
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_tile_and_a_bit(dtype):
+    check(make([(130, [1, 20, 64])], Hq=4, Hkv=2, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 2), (6, 2), (8, 1), (12, 1), (20, 1), (3, 3)])
-def test_head_groups(D, Hq, Hkv):
-    check(make([(200, [1, 5, 70]), (33, [4, 4]), (517, [9])], Hq=Hq, Hkv=Hkv, D=D))
+def test_head_groups(dtype, D, Hq, Hkv):
+    check(make([(200, [1, 5, 70]), (33, [4, 4]), (517, [9])], Hq=Hq, Hkv=Hkv, D=D, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("beams", [2, 15, 16, 17, 33, 64, 65, 100])
-def test_group_sizes(D, beams):
+def test_group_sizes(dtype, D, beams):
     # 4 query heads a key head: row tiles from partly filled ones to several
-    check(make([(300, [1 + i % 7 for i in range(beams)])], Hq=8, Hkv=2, D=D, page=64))
+    check(make([(300, [1 + i % 7 for i in range(beams)])], Hq=8, Hkv=2, D=D, page=64, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("prefix", [1, 15, 16, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000, 5000])
-def test_prefix_lengths(D, prefix):
-    check(make([(prefix, [1, 30, 200])], Hq=4, Hkv=1, D=D))
+def test_prefix_lengths(dtype, D, prefix):
+    check(make([(prefix, [1, 30, 200])], Hq=4, Hkv=1, D=D, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("page", [1, 3, 7, 24, 64, 100, 256])
-def test_page_sizes(page):
-    check(make([(333, [1, 7, 40]), (64, [64, 1])], page=page))
+def test_page_sizes(dtype, page):
+    check(make([(333, [1, 7, 40]), (64, [64, 1])], page=page, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_many_groups(D):
+def test_many_groups(dtype, D):
     sizes = [(i * 37 % 150 + 1, [1 + (i + j) % 9 for j in range(1 + i % 4)]) for i in range(90)]
-    check(make(sizes, Hq=4, Hkv=2, D=D))
+    check(make(sizes, Hq=4, Hkv=2, D=D, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("groups", [[(20000, [3] * 3)], [(9000, [1] * 40), (1, [5]), (4000, [100, 1])]])
-def test_prefixes_in_many_pieces(D, groups):
-    check(make(groups, Hq=8, Hkv=1, D=D, page=64))
+def test_prefixes_in_many_pieces(dtype, D, groups):
+    check(make(groups, Hq=8, Hkv=1, D=D, page=64, dtype=dtype))
 
 
-def test_groups_without_prefix_or_sequences_and_sequences_without_group():
-    c = make([(0, [5, 9]), (100, [3, 4]), (50, []), (0, []), (200, [1])], before=3, after=2)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_groups_without_prefix_or_sequences_and_sequences_without_group(dtype):
+    c = make([(0, [5, 9]), (100, [3, 4]), (50, []), (0, []), (200, [1])], before=3, after=2, dtype=dtype)
     check(c)
     c["starts"][:] = 0  # no group has a sequence
     check(c)
@@ -178,9 +187,10 @@ def test_groups_without_prefix_or_sequences_and_sequences_without_group():
     check(c)
 
 
-def test_sequences_that_take_no_part():
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_sequences_that_take_no_part(dtype):
     # shorter than the prefix, of no length, of negative length, ending with it
-    c = make([(150, [1, -30, -150, 0, 9]), (40, [-39, 2])], page=8)
+    c = make([(150, [1, -30, -150, 0, 9]), (40, [-39, 2])], page=8, dtype=dtype)
     check(c)
     c["lens"][2] = -5
     check(c)
@@ -196,8 +206,9 @@ def test_lengths_and_prefixes_past_the_table():
     check(c)
 
 
-def test_a_prefix_of_the_whole_table():
-    c = make([(300, [40, 60, 5])])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_prefix_of_the_whole_table(dtype):
+    c = make([(300, [40, 60, 5])], dtype=dtype)
     c["prefix"][0] = 2 ** 31 - 1  # as much as the table holds, mostly null pages
     c["lens"][:2] = torch.tensor([2 ** 31 - 1, 10 ** 9], dtype=torch.int32)
     c["table"][0, -3:] = c["table"][0, :3].clone()
@@ -208,14 +219,16 @@ def test_a_prefix_of_the_whole_table():
     check(c)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("window", [1, 64, 150, 163, 170, 10 ** 6])
-def test_windows(window):
+def test_windows(dtype, window):
     # those that reach behind the prefix's start share it, the others do not
-    check(make([(150, [1, 12, 13, 20, 64]), (5, [200, 1])]), window=window)
+    check(make([(150, [1, 12, 13, 20, 64]), (5, [200, 1])], dtype=dtype), window=window)
 
 
-def test_null_pages():
-    c = make([(200, [30, 1, 64]), (64, [5, 6])], page=16)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_null_pages(dtype):
+    c = make([(200, [30, 1, 64]), (64, [5, 6])], page=16, dtype=dtype)
     c["table"][0:3, 2] = 0
     c["table"][0:3, 7] = torch.tensor([-5, -5, -5], dtype=torch.int32)
     c["table"][3:5, :4] = 2 ** 31 - 1  # nothing left of the prefix
@@ -239,30 +252,33 @@ def test_four_element_alignment():
     check(c)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("q_scale", [0.0, 40.0])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_flat_and_peaked_scores(q_scale, D):
-    check(make([(900, [65, 3])], D=D, q_scale=q_scale), scale=0.3)
+def test_flat_and_peaked_scores(dtype, q_scale, D):
+    check(make([(900, [65, 3])], D=D, q_scale=q_scale, dtype=dtype), scale=0.3)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("beams", [2, 70])
 @pytest.mark.parametrize("step", [1 / 64, 1 / 8])
-def test_rising_scores(beams, step):
+def test_rising_scores(dtype, beams, step):
     # scores that rise by less and by more a tile than the reference of the weights lets pass
-    c = make([(1500, [2] * beams)], Hq=4, Hkv=1, D=64, page=4)
-    ramp = (torch.arange(1500, device="cuda") * step).to(BF16)
+    c = make([(1500, [2] * beams)], Hq=4, Hkv=1, D=64, page=4, dtype=dtype)
+    ramp = (torch.arange(1500, device="cuda") * step).to(BF16).to(dtype)
     flat = c["k"].view(-1, 1, 64)
     index = (c["table"][0, :375].long()[:, None] * 4 + torch.arange(4, device="cuda")).flatten()
     flat[index] = 0.0
     flat[index, 0, 0] = ramp
     c["q"].zero_()
-    c["q"][..., 0] = torch.linspace(-3, 3, c["q"].shape[0] * 4, device="cuda").to(BF16).view(-1, 4)
+    c["q"][..., 0] = torch.linspace(-3, 3, c["q"].shape[0] * 4, device="cuda").to(BF16).to(dtype).view(-1, 4)
     check(c, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_a_bad_query_spoils_its_head_alone(bad):
-    c = make([(300, [9, 20, 5])], Hq=12, Hkv=1)
+def test_a_bad_query_spoils_its_head_alone(dtype, bad):
+    c = make([(300, [9, 20, 5])], Hq=12, Hkv=1, dtype=dtype)
     good, _ = check(c)
     c["q"][1, 3, 17] = bad
     out, _ = run(c)
@@ -272,8 +288,9 @@ def test_a_bad_query_spoils_its_head_alone(bad):
     assert not torch.isfinite(out[hit]).any() and same(out[~hit], good[~hit])
 
 
-def test_a_bad_value_spoils_its_channel_alone():
-    c = make([(300, [9, 20])], Hq=12, Hkv=1)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_bad_value_spoils_its_channel_alone(dtype):
+    c = make([(300, [9, 20])], Hq=12, Hkv=1, dtype=dtype)
     good, _ = check(c)
     c["v"][c["table"][0, 2], 5, 0, 9] = float("nan")
     out, _ = run(c)
@@ -283,9 +300,10 @@ def test_a_bad_value_spoils_its_channel_alone():
     assert not torch.isfinite(out[hit]).any() and same(out[~hit], good[~hit])
 
 
-def test_infinite_scores():
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_infinite_scores(dtype):
     # Head 0 scores -infinity at position 5 and loses it, head 1 scores +infinity.
-    c = make([(140, [9, 20])], Hq=2, Hkv=1, D=64)
+    c = make([(140, [9, 20])], Hq=2, Hkv=1, D=64, dtype=dtype)
     c["q"][:, 0, 0], c["q"][:, 1, 0] = 1.0, -1.0
     lost = c["k"][c["table"][0, 0], 5, 0].clone()
     c["k"][c["table"][0, 0], 5, 0, 0] = -float("inf")
@@ -367,9 +385,10 @@ def test_empty_batch():
     assert run(c)[0].shape == (0, 8, 128)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("beams", [3, 60])
-def test_repeats_streams_and_graphs_give_the_same_bits(beams):
-    c = make([(5000, [7] * beams), (700, [80, 1])], Hq=8, Hkv=2)
+def test_repeats_streams_and_graphs_give_the_same_bits(dtype, beams):
+    c = make([(5000, [7] * beams), (700, [80, 1])], Hq=8, Hkv=2, dtype=dtype)
     out, lse = check(c)
     for _ in range(3):
         again, sums = run(c)
