@@ -40,9 +40,11 @@ AttendPlan attend_mma_plan(int32_t G, int32_t D, int32_t sms);
 cudaError_t launch_attend_mma(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 // Float32 in matrix instructions (kda_attend_tf32.cu), for many query heads a key head.
 AttendPlan attend_tf32_plan(int32_t G, int32_t D, int32_t sms);
-int attend_tf32_warps(int32_t D);  // of a block
 cudaError_t launch_attend_tf32(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
-// The same over the groups' common positions, units of p.heads query rows.
+// The same under shared prefixes, for 64 and 128 channels: sequences' own positions, up to 8 heads a key head, and the
+// groups' common ones, in units of p.heads query rows.  Both leave parts of as many warps.
+constexpr int kTf32PartWarps = 8;
+cudaError_t launch_attend_tf32_own(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 cudaError_t launch_attend_tf32_groups(const AttendArgs& a, const AttendPlan& p, cudaStream_t s);
 
 // a / b, neither negative; 32-bit where they fit (a 64-bit division is a long call).

@@ -358,18 +358,6 @@ cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_pdl(kda_attend_tf32_kernel<D, HG, OVER>, dim3(p.ctas), dim3(Shape<D>::THREADS), bytes, s, 1, a);
 }
-template <Over OVER>
-cudaError_t launch_over(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  switch (a.D * 16 + p.heads - 1) {
-    case 64 * 16 + 7: return launch<64, 8, OVER>(a, p, s);
-    case 64 * 16 + 15: return launch<64, 16, OVER>(a, p, s);
-    case 128 * 16 + 7: return launch<128, 8, OVER>(a, p, s);
-    case 128 * 16 + 15: return launch<128, 16, OVER>(a, p, s);
-    case 256 * 16 + 7: return launch<256, 8, OVER>(a, p, s);
-    case 256 * 16 + 15: return launch<256, 16, OVER>(a, p, s);
-    default: return cudaErrorInvalidValue;
-  }
-}
 
 }  // namespace
 
@@ -381,13 +369,34 @@ AttendPlan attend_tf32_plan(int32_t G, int32_t D, int32_t sms) {
   return p;
 }
 
-int attend_tf32_warps(int32_t D) { return D == 256 ? Shape<256>::WARPS : Shape<128>::WARPS; }
+static_assert(Shape<64>::WARPS == kTf32PartWarps && Shape<128>::WARPS == kTf32PartWarps, "parts a piece leaves");
 
 cudaError_t launch_attend_tf32(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  return a.skip != nullptr ? launch_over<Over::kOwn>(a, p, s) : launch_over<Over::kSequences>(a, p, s);
+  switch (a.D * 16 + p.heads - 1) {
+    case 64 * 16 + 7: return launch<64, 8, Over::kSequences>(a, p, s);
+    case 64 * 16 + 15: return launch<64, 16, Over::kSequences>(a, p, s);
+    case 128 * 16 + 7: return launch<128, 8, Over::kSequences>(a, p, s);
+    case 128 * 16 + 15: return launch<128, 16, Over::kSequences>(a, p, s);
+    case 256 * 16 + 7: return launch<256, 8, Over::kSequences>(a, p, s);
+    case 256 * 16 + 15: return launch<256, 16, Over::kSequences>(a, p, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
+
+cudaError_t launch_attend_tf32_own(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  if (p.heads != 8) return cudaErrorInvalidValue;
+  return a.D == 64 ? launch<64, 8, Over::kOwn>(a, p, s)
+                   : (a.D == 128 ? launch<128, 8, Over::kOwn>(a, p, s) : cudaErrorInvalidValue);
+}
+
 cudaError_t launch_attend_tf32_groups(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  return launch_over<Over::kGroups>(a, p, s);
+  switch (a.D * 16 + p.heads - 1) {
+    case 64 * 16 + 7: return launch<64, 8, Over::kGroups>(a, p, s);
+    case 64 * 16 + 15: return launch<64, 16, Over::kGroups>(a, p, s);
+    case 128 * 16 + 7: return launch<128, 8, Over::kGroups>(a, p, s);
+    case 128 * 16 + 15: return launch<128, 16, Over::kGroups>(a, p, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace kda

@@ -600,7 +600,8 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
 template <int D, int WARPS>
 __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_constant__ AttendArgs a, const Parts pre,
                                                               const Parts own) {
-  constexpr int VEC = D / 32, AHEAD = 4;
+    // parts read at once: 34 parts of 64 channels (7 groups of 20, 12 heads) 37 -> 32 us a call for eight, 128 channels 97 -> 98
+  constexpr int VEC = D / 32, AHEAD = D == 64 ? 8 : 4;
   __shared__ float s_m[4], s_l[4], s_o[WARPS > 1 ? 4 : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
@@ -612,11 +613,13 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
   int piece[2], row[2], more[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const Parts& p = w == 0 ? pre : own;
+    const int ctas = w == 0 ? pre.ctas : own.ctas;
     piece[w] = notes[w].x;
     row[w] = notes[w].y & 255;
     more[w] = notes[w].y >> 8;
-    if (piece[w] < 0 || more[w] < 0 || piece[w] >= p.ctas || more[w] >= p.ctas - piece[w] || row[w] >= p.rows) more[w] = 0;
+    if (piece[w] < 0 || more[w] < 0 || piece[w] >= ctas || more[w] >= ctas - piece[w] ||
+        row[w] >= (w == 0 ? pre.rows : own.rows))
+      more[w] = 0;
   }
   const int parts0 = pre.warps * (1 + more[0]), parts = parts0 + own.warps * (1 + more[1]);
   float m = -INFINITY, l = 0.f, o[VEC] = {};
@@ -632,14 +635,15 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
       from[k] = nullptr;
       if (q < parts) {
         const bool w = q >= parts0;
-        const Parts& p = w ? own : pre;
-        const int at = w ? q - parts0 : q, j = at / p.warps, by = at - j * p.warps;
-        const int64_t place =
-            j == 0 ? by * heads + head : ((int64_t)((w ? piece[1] : piece[0]) + j) * p.warps + by) * p.rows + (w ? row[1] : row[0]);
-        const float2 ml = (j == 0 ? p.first_ml : p.more_ml)[place];
+        const int at = w ? q - parts0 : q, warps = w ? own.warps : pre.warps;
+        const bool first = at < warps;  // of the piece that begins the unit
+        const int64_t place = first ? at * heads + head
+                                    : ((int64_t)(w ? piece[1] : piece[0]) * warps + at) * (w ? own.rows : pre.rows) +
+                                          (w ? row[1] : row[0]);
+        const float2 ml = (w ? (first ? own.first_ml : own.more_ml) : (first ? pre.first_ml : pre.more_ml))[place];
         pm[k] = ml.x;
         pl[k] = ml.y;
-        from[k] = (j == 0 ? p.first_o : p.more_o) + place * D;
+        from[k] = (w ? (first ? own.first_o : own.more_o) : (first ? pre.first_o : pre.more_o)) + place * D;
       }
     }
 #pragma unroll
@@ -742,8 +746,8 @@ PrefixPlan prefix_plan(float* work, int64_t N, int32_t Hq, int32_t Hkv, int32_t 
     p.own = attend_tf32_plan(G, D, sms);
     p.pre = attend_tf32_plan(rows <= 8 ? 8 : 16, D, sms);
     take(p.own.ctas * (int64_t)kNoteFloats);
-    p.own_parts = parts(p.own.ctas, attend_tf32_warps(D), p.own.heads, p.own.heads);
-    p.pre_parts = parts(p.pre.ctas, attend_tf32_warps(D), p.pre.heads, 16);
+    p.own_parts = parts(p.own.ctas, kTf32PartWarps, p.own.heads, p.own.heads);
+    p.pre_parts = parts(p.pre.ctas, kTf32PartWarps, p.pre.heads, 16);
   } else {
     p.own = attend_mma_plan(G, D, sms);
     p.pre.ctas = sms;
@@ -789,13 +793,11 @@ cudaError_t launch_prefix(const AttendArgs& a, int sms, cudaStream_t s) {
 template <int D>
 cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms, cudaStream_t s) {
   const int64_t heads = (int64_t)a.N * a.Hq;
-  if (heads >= 16LL * sms)
+  if (heads >= 16LL * sms)  // 1404 heads of 34 parts, by one warp each, 37 -> 61 us
     return launch_pdl(kda_prefix_join_kernel<D, 1>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, s, 1, a, p.pre_parts,
                       p.own_parts);
   return launch_pdl(kda_prefix_join_kernel<D, 4>, dim3((unsigned)heads), dim3(128), 0, s, 1, a, p.pre_parts, p.own_parts);
 }
-
-}  // namespace
 
 // Bytes of keys and values from which sharing is worth its two launches more, by
 // what it could save at the table's width (the host knows no lengths): below, every
@@ -806,6 +808,24 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms
 //   64 channels           1 x 4 x 16000 (98 MB) 26 and 27, 16 x 4 x 1024 (101 MB) 29 and 31, 4 x 2 x 16000 (131 MB) 52 and 46
 //   256 channels          1 x 4 x 4032 (99 MB) 25 and 34, 12 / 1 heads 1 x 16 x 16000 (246 MB) 48 and 66, 4 x 16 x 1024 (63 MB) 32 and 28
 constexpr int64_t kSharedBytes = 96 << 20;
+// Float32 works on its rows as long as on its bytes: with more query heads a key
+// head, or 256 channels, the sequences alone already do, and sharing saves little.
+//   32 / 8 heads of 64    4 x 16 x 1024 (252 MB) 46 and 55, 16 x 2 x 4032 (264 MB) 78 and 92, 16 x 16 x 256 (252 MB) 88 and 71
+//   32 / 8 of 128         4 x 6 x 1024 (168 MB) 43 and 41, 1 x 16 x 4032 (496 MB) 57 and 87, 16 x 2 x 1024 (134 MB) 50 and 55
+//   16 / 16 of 128        1 x 6 x 4032 (330 MB) 44 and 53, 4 x 16 x 256 (252 MB) 49 and 52, 16 x 6 x 256 (168 MB) 68 and 75
+//   32 / 2 of 128         4 x 16 x 4032 (496 MB) 137 and 126, 16 x 16 x 1024 (503 MB) 183 and 145
+//   256 channels          32 / 8 4 x 6 x 1024 (336 MB) 94 and 79, 16 / 16 16 x 2 x 1024 (537 MB) 216 and 165
+constexpr int64_t kSharedBytesF32 = 256 << 20;
+constexpr int kSharedHeadsF32 = 4;
+
+bool shares(const AttendArgs& a) {
+  const double positions = (a.N - (double)a.num_groups) * a.table_cols * a.page_size;
+  if (a.dtype == KDA_DT_F32)
+    return a.Hq / a.Hkv <= kSharedHeadsF32 && a.D <= 128 && positions * a.Hkv * a.D * 8 >= kSharedBytesF32;
+  return a.vec16 && positions * a.Hkv * a.D * 4 >= kSharedBytes;
+}
+
+}  // namespace
 
 int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
   return std::max(attend_floats(Hq, Hkv, D, dtype, sms), prefix_plan(nullptr, N, Hq, Hkv, D, dtype, sms, 0).floats);
@@ -813,9 +833,8 @@ int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dty
 
 cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaStream_t s) {
   AttendArgs a = given;
+  if (!shares(a)) return launch_paged_attention(a, sms, s);
   const bool f32 = a.dtype == KDA_DT_F32;
-  const double saved = (a.N - (double)a.num_groups) * a.table_cols * a.page_size * a.Hkv * a.D * (f32 ? 8 : 4);
-  if (!a.vec16 || saved < kSharedBytes) return launch_paged_attention(a, sms, s);
   const PrefixPlan p = prefix_plan(a.work, a.N, a.Hq, a.Hkv, a.D, a.dtype, sms, a.num_groups);
   a.parts = p.pre_parts;
   a.mark = p.mark;
@@ -828,7 +847,7 @@ cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaSt
   if (e != cudaSuccess) return e;
   a.parts = p.own_parts;
   a.skip = p.mark;
-  e = f32 ? launch_attend_tf32(a, p.own, s) : launch_attend_mma(a, p.own, s);
+  e = f32 ? launch_attend_tf32_own(a, p.own, s) : launch_attend_mma(a, p.own, s);
   if (e != cudaSuccess) return e;
   if (a.D == 64) return launch_prefix_join<64>(a, p, sms, s);
   if (a.D == 128) return launch_prefix_join<128>(a, p, sms, s);
