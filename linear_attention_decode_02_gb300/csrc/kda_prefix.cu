@@ -20,22 +20,33 @@
 //   the next W warps      issue a lane's matrix products each (one warp for both was
 //                         at work on issuing them for longer than they took)
 //   the last four         copy queries, keys and values into shared memory
-// A lane is a buffer of scores S (128 rows x KT positions, float32), an output O
-// and the warps between them.  With two row tiles each lane is one of them and both
-// use every tile of keys and values; with one they take the tiles in turn, each to
-// an output and statistics of its own, which are joined at the unit's end.  Either
-// way one lane's softmax runs under the other's products.  256 channels leave room
-// for one output: its softmax takes both buffers in turn.
+// Work goes in steps of 64 positions.  A lane has two buffers of scores S (128 rows x
+// 64, float32), an output O and the warps between them: the scores of a step are
+// issued before the output of the last one, so they are there when its softmax ends.
+// With two row tiles each lane is one of them and both use every tile of keys and
+// values; with one they take the tiles in turn, each to an output and statistics of
+// its own, which are joined at the unit's end.  256 channels leave room for one
+// output, and one lane.
 // The row's thread puts the weights back over S as the next product's left operand,
 // in two bfloat16 pieces, p = hi + lo to 2^-16, for 16 positions at a time 8 columns
-// of hi and 8 of lo.  It reads S once: weights are taken relative to a reference that
-// follows the row's maximum only where that has passed it by 2^kSlack, and then in
-// whole steps, so that weights of the tile that are written already move to it
-// exactly; O, which lies in tensor memory, is seldom rescaled.
+// of hi and 8 of lo: one piece alone would cost each output 2^-9 of its weights'
+// largest.  Weights are relative to a reference that follows the row's maximum only
+// where that has passed it by 2^kSlack, so O, which lies in tensor memory, is seldom
+// rescaled.
 //
 // A barrier's parity tells two phases apart, so each is waited for, or known to be
 // over, before the next: S of a buffer is issued behind the product of the weights
-// that were in it, so a lane's O is at rest while its warps work on new scores.
+// that were in it, so a second phase of that product cannot pass unseen.
+//
+// What bounds it, at 32 / 8 heads of 128 (each of the three launches under a profiler,
+// in us):
+//   16 prompts of 8192 positions, four beams each (one row tile): 76, 392 MB at 65 % of DRAM's rate;
+//     the steps of a lane wait for one another, and a ring of five halves holds little
+//   256 users of one system prompt of 32768 (two row tiles): 155, tensor pipe 54 %;
+//     softmax of 64 positions takes 1340 cycles of a warp, the three products of a step 660
+// Tried: one warp that issues both lanes' products (246 -> 300 us a call), tiles of 64
+// positions (76 -> 104, 155 -> 171: twice the copies' bookkeeping, and values held
+// through two more tiles), scores first at a tile's end with one row tile (76 -> 88).
 //
 // Every mbarrier wait is bounded in time: a role whose wait runs out records a bit
 // in the error word, raises the CTA's abort flag and leaves its loop; all meet at
@@ -57,10 +68,12 @@ constexpr int kRows = 128;       // rows of a tile
 constexpr int kLoaders = 128;    // threads
 constexpr float kSlack = 4.f;    // in units of log 2
 constexpr int kLiveDepth = 16;   // tiles whose masks are kept
+constexpr int kStep = 64;        // positions that a softmax takes at once
 
 template <int D, int RT>
 struct PrefixShape {
   static constexpr int KT = D == 256 ? 64 : 128;   // positions of a tile
+  static constexpr int STEPS = KT / kStep;         // of a tile
   static constexpr int BLOCKS = D / 64;            // 128-byte wide column blocks of an operand
   static constexpr int Q_TILE = BLOCKS * kRows * 128;
   static constexpr int QSLOTS = RT == 1 && D < 256 ? 2 : 1;
@@ -71,7 +84,7 @@ struct PrefixShape {
   static constexpr bool SPLIT = RT < LANES;        // lanes take tiles in turn
   static constexpr int THREADS = LANES == 1 ? 9 * 32 : 16 * 32;
   static constexpr int LOADER0 = LANES == 1 ? 5 : 8, PRODUCT0 = LANES == 1 ? 4 : 12;  // first warps of the roles
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * KT;   // two buffers of S, then O of each lane
+  static constexpr uint32_t S_COL = 0, O_COL = LANES * 2 * kStep;   // two buffers of S for each lane, then its O
   static constexpr uint32_t COLS = 512;
   static_assert(O_COL + LANES * D <= COLS && RT <= LANES, "tensor memory");
   static_assert(SLOTS / 2 + 4 <= kLiveDepth, "ring");
@@ -102,15 +115,15 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     kda_prefix_kernel(const __grid_constant__ AttendArgs a, int box,
                       const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using P = PrefixShape<D, RT>;
-  constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, LANES = P::LANES, WARPS = P::THREADS / 32;
+  constexpr int KT = P::KT, ROWS = RT * kRows, SLOTS = P::SLOTS, LANES = P::LANES;
   using Walker = GroupWalk<KT, ROWS>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                        ~static_cast<uintptr_t>(1023));
   unsigned char* const s_q = sm;
   unsigned char* const s_ring = sm + P::QSLOTS * RT * P::Q_TILE;
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_full[2], o_done[2], q_empty[P::QSLOTS], live_full[kLiveDepth],
-      x_full, x_empty, turn[2], drained[LANES];
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2 * LANES], p_full[2 * LANES], o_done[2 * LANES],
+      q_full[P::QSLOTS], q_empty[P::QSLOTS], live_full[kLiveDepth], x_full, x_empty, drained[LANES];
   __shared__ float2 s_ml[P::SPLIT ? kRows : 1];
   __shared__ __align__(8) uint32_t s_live[kLiveDepth][KT / 32];
   __shared__ uint32_t s_taddr;
@@ -123,15 +136,16 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       mbar_init(&full[i], kLoaders);
       mbar_init(&empty[i], RT);  // the lanes that use a half
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * LANES; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kRows / 32);
       mbar_init(&o_done[i], 1);
     }
-    for (int i = 0; i < P::QSLOTS; ++i) mbar_init(&q_empty[i], LANES);
+    for (int i = 0; i < P::QSLOTS; ++i) {
+      mbar_init(&q_full[i], kLoaders);
+      mbar_init(&q_empty[i], LANES);
+    }
     for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live_full[i], kLoaders / 32);
-    mbar_init(&turn[0], 1);
-    mbar_init(&turn[1], 1);
     mbar_init(&x_full, kRows);
     mbar_init(&x_empty, kRows);
     for (int i = 0; i < LANES; ++i) mbar_init(&drained[i], 1);
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     const int row = (warp & 3) * 32 + lane;      // of the row tile, and tensor-memory lane
     const uint32_t tl = taddr + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_addr = tl + P::O_COL + me * D;
-    int tile = 0, job = 0, unit = 0, ends = 0;  // tiles of the piece, this lane's tiles, units and its own of them so far
+    int tile = 0, job = 0, unit = 0;  // tiles of the piece, this lane's steps and units so far
     bool run = any;
     while (run && walk.tile < stop) {
       const int valid = walk.rows_left() - row_tile * kRows;  // rows of this tile that exist
@@ -182,128 +196,89 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       const int64_t end = min(walk.unit_end, stop);
       const int count = (int)(end - walk.tile);
       const bool begins = walk.unit_start >= start;
-      for (int j = P::SPLIT ? me : 0; j < count; j += P::SPLIT ? 2 : 1, ++job) {
-        const int b = LANES == 1 ? job & 1 : me, at_mask = (tile + j) % kLiveDepth;
-        const uint32_t phase = LANES == 1 ? (job >> 1) & 1 : job & 1;
-        const bool first = j < (P::SPLIT ? 2 : 1);  // O holds nothing yet
-        if (!wait_or_abort(&s_full[b], phase) || !wait_or_abort(&live_full[at_mask], ((tile + j) / kLiveDepth) & 1)) {
+      const int steps = (P::SPLIT ? (count + 1 - me) / 2 : count) * P::STEPS;  // this lane's
+      for (int i = 0; i < steps; ++i, ++job) {
+        const int j = tile + i / P::STEPS * (P::SPLIT ? 2 : 1) + (P::SPLIT ? me : 0), at_mask = j % kLiveDepth;
+        const int b = 2 * me + (job & 1);
+        if (!wait_or_abort(&s_full[b], (job >> 1) & 1) ||
+            (i % P::STEPS == 0 && !wait_or_abort(&live_full[at_mask], (j / kLiveDepth) & 1))) {
           run = false;
           break;
         }
         tc::fence_after_sync();
         if (!idle) {
-          const uint32_t s_addr = tl + P::S_COL + b * KT;
-          const float2 scale2 = dup2(a.scale_log2), minus2 = dup2(-1.f);
+          const uint32_t s_addr = tl + P::S_COL + b * kStep;
+          uint32_t x[kStep];
+          tc::ld64_async(s_addr, x);
+          const uint2 word = *reinterpret_cast<const uint2*>(&s_live[at_mask][i % P::STEPS * 2]);
+          tc::ld_wait(x);
+          if ((word.x & word.y) != 0xffffffffu) {
+#pragma unroll
+            for (int e = 0; e < kStep; ++e) x[e] = (e < 32 ? word.x : word.y) >> (e & 31) & 1 ? x[e] : 0xff800000u;  // -infinity
+          }
+          float tops[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            tops[e] = __uint_as_float(x[e]);
+#pragma unroll
+            for (int k = 4; k < 60; k += 8) tops[e] = max3(tops[e], __uint_as_float(x[k + e]), __uint_as_float(x[k + e + 4]));
+            tops[e] = fmaxf(tops[e], __uint_as_float(x[60 + e]));
+          }
+          const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale_log2;
+          const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, rises)) {
+            const float fall = rises ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
+            if (rises) m = top;
+            l *= fall;
+            if (i > 0) {  // the last step's product may still run
+              if (!wait_or_abort(&o_done[2 * me + ((job - 1) & 1)], ((job - 1) >> 1) & 1)) { run = false; break; }
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int k = 0; k < D; k += 16) {
+                float o[16];
+                tc::ld16(o_addr + k, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = fall == 0.f ? 0.f : o[e] * fall;
+                tc::st16(o_addr + k, o);
+              }
+            }
+          }
+          const float2 scale2 = dup2(a.scale_log2), minus2 = dup2(-1.f), ref2 = dup2(m == -INFINITY ? 0.f : -m);
           float2 sum[4] = {dup2(0.f), dup2(0.f), dup2(0.f), dup2(0.f)};
-          // 64 positions from k on.
-          const auto weigh = [&](int k) -> bool {
-            uint32_t x[64];
-            tc::ld64_async(s_addr + k, x);
-            const uint2 word = *reinterpret_cast<const uint2*>(&s_live[at_mask][k / 32]);
-            tc::ld_wait(x);
-            if ((word.x & word.y) != 0xffffffffu) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) x[i] = (i < 32 ? word.x : word.y) >> (i & 31) & 1 ? x[i] : 0xff800000u;  // -infinity
+          for (int h = 0; h < kStep; h += 16) {
+            uint32_t w[16];  // 8 columns of hi, 8 of lo
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y =
+                  fma2(make_float2(__uint_as_float(x[h + 2 * e]), __uint_as_float(x[h + 2 * e + 1])), scale2, ref2);
+              const float2 p = make_float2(ex2(y.x), ex2(y.y));
+              sum[e & 3] = add2(sum[e & 3], p);
+              // hi is the upper half of the float32, cut off; lo what is left, rounded
+              const uint32_t u = __float_as_uint(p.x), v = __float_as_uint(p.y);
+              w[e] = __byte_perm(u, v, 0x7632);
+              const float2 rest =
+                  fma2(make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), minus2, p);
+              w[8 + e] = pack_bf2(rest.x, rest.y);
             }
-            float tops[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              tops[e] = __uint_as_float(x[e]);
-#pragma unroll
-              for (int i = 4; i < 60; i += 8)
-                tops[e] = max3(tops[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4]));
-              tops[e] = fmaxf(tops[e], __uint_as_float(x[60 + e]));
-            }
-            const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale_log2;
-            const bool rises = top > m + kSlack || (m == -INFINITY && top > m);
-            if (__any_sync(0xffffffffu, rises)) {
-              // The reference rises by whole steps, so what is weighted already moves exactly.
-              float fall = 1.f;
-              if (rises && m == -INFINITY) {
-                m = top;
-                fall = 0.f;
-              } else if (rises) {
-                const float steps = ceilf(top - m);
-                m += steps;
-                fall = steps < 127.f ? __int_as_float((127 - (int)steps) << 23) : 0.f;
-              }
-              l *= fall;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], dup2(fall));
-              if (k > 0) {
-                tc::st_wait();
-#pragma unroll 1
-                for (int i = 0; i < k; i += 16) {
-                  float w[16];
-                  tc::ld16(s_addr + i, w);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const uint32_t u = __float_as_uint(w[e]);
-                    w[e] = __uint_as_float(pack_bf2(bf_lo(u) * fall, bf_hi(u) * fall));
-                  }
-                  tc::st16(s_addr + i, w);
-                }
-              }
-              if (!first) {
-                // with one lane the last tile's product may still run
-                if (LANES == 1 && !wait_or_abort(&o_done[(job - 1) & 1], ((job - 1) >> 1) & 1)) return false;
-                tc::fence_after_sync();
-#pragma unroll 1
-                for (int i = 0; i < D; i += 16) {
-                  float o[16];
-                  tc::ld16(o_addr + i, o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = fall == 0.f ? 0.f : o[e] * fall;
-                  tc::st16(o_addr + i, o);
-                }
-              }
-            }
-            const float2 ref2 = dup2(m == -INFINITY ? 0.f : -m);
-#pragma unroll
-            for (int h = 0; h < 64; h += 16) {
-              uint32_t w[16];  // 8 columns of hi, 8 of lo
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 y =
-                    fma2(make_float2(__uint_as_float(x[h + 2 * i]), __uint_as_float(x[h + 2 * i + 1])), scale2, ref2);
-                const float2 p = make_float2(ex2(y.x), ex2(y.y));
-                sum[i & 3] = add2(sum[i & 3], p);
-                // hi is the upper half of the float32, cut off; lo what is left, rounded
-                const uint32_t u = __float_as_uint(p.x), v = __float_as_uint(p.y);
-                w[i] = __byte_perm(u, v, 0x7632);
-                const float2 rest =
-                    fma2(make_float2(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), minus2, p);
-                w[8 + i] = pack_bf2(rest.x, rest.y);
-              }
-              tc::st16_async(s_addr + k + h, w);
-            }
-            return true;
-          };
-#pragma unroll 1
-          for (int k = 0; k < KT && run; k += 64) run = weigh(k);
-          if (!run) break;
+            tc::st16_async(s_addr + h, w);
+          }
           tc::st_wait();
           const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l += all.x + all.y;
         }
         // The other lane's warps have read this one's last output.
-        if (P::SPLIT && me == 1 && j < 2 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
+        if (P::SPLIT && me == 1 && i == 0 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[b]);
       }
       if (!run) break;
       // The unit's end in this piece: its rows' statistics and outputs.
-      if (!P::SPLIT || me < count) {
-        const int last = job - 1;
-        if (!wait_or_abort(&o_done[LANES == 1 ? last & 1 : me], LANES == 1 ? (last >> 1) & 1 : ends++ & 1)) {
-          run = false;
-          break;
-        }
-      }
+      if (steps > 0 && !wait_or_abort(&o_done[2 * me + ((job - 1) & 1)], ((job - 1) >> 1) & 1)) { run = false; break; }
       tc::fence_after_sync();
       if (P::SPLIT && me == 1) {
-        if (count < 2 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
+        if (steps == 0 && unit > 0 && !wait_or_abort(&x_empty, (unit - 1) & 1)) { run = false; break; }
         s_ml[row] = make_float2(m, l);
         tc::fence_before_sync();
         mbar_arrive(&x_full);
@@ -363,112 +338,80 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   } else if (warp >= P::PRODUCT0 && warp < P::PRODUCT0 + LANES) {
     more_registers<LANES == 1 ? 0 : -112>();
     // ---------------- matrix products, a warp for each lane ----------------
-    constexpr uint32_t ID_S = tc::idesc_bf16(kRows, KT, false, false), ID_O = tc::idesc_bf16(kRows, D, false, true);
+    constexpr uint32_t ID_S = tc::idesc_bf16(kRows, kStep, false, false), ID_O = tc::idesc_bf16(kRows, D, false, true);
     const uint32_t q_addr = smem_addr(s_q), ring = smem_addr(s_ring);
     const uint32_t issue = tc::elect();
     const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     const int me = uniform(warp - P::PRODUCT0), row_tile = RT == 1 ? 0 : me;
-    int half = 0, tile = 0, unit = 0;  // of the next K, whose V is the one after it; tiles and units so far
-    uint32_t weighed = 0;              // parity of the outputs issued from each buffer
-    bool run = any, threads = true;
+    int half = 0, tile = 0, unit = 0, job = 0;  // of the next K, whose V is the one after it; tiles, units and steps so far
+    bool run = any;
     const auto release = [&](uint64_t* bar) { tc::commit_by(issue, bar); };
     // A half that has landed.  What threads copied the tensor cores read through another proxy.
-    const auto slot_wait = [&](int h) {
+    const auto slot_wait = [&](int h, bool threads) {
       if (!wait_or_abort(&full[h % SLOTS], (h / SLOTS) & 1)) return false;
       if (threads) fence_proxy_async_smem();
       return true;
     };
-    // The keys of the unit's tile j.
-    const auto keys_wait = [&](int j) -> bool {
-      const int at_mask = (tile + j) % kLiveDepth;
-      if (!wait_or_abort(&live_full[at_mask], ((tile + j) / kLiveDepth) & 1)) return false;
-      threads = box == 0 || j < (P::SPLIT ? 2 : 1);  // the queries are always copied by threads
-#pragma unroll
-      for (int i = 0; i < KT / 32; ++i) threads = threads || s_live[at_mask][i] != 0xffffffffu;
-      return slot_wait(half + 2 * j);
-    };
-    // S of the unit's tile j into buffer b.
-    const auto scores = [&](int q_slot, int b, int j) {
-      const int h = half + 2 * j;
-      const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + row_tile) * P::Q_TILE, 16, 1024);
-      const uint64_t k = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, 16, 1024);
-      const uint32_t to = taddr + P::S_COL + uniform(b) * KT;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)  // descriptors count in 16 bytes
-        tc::mma_bf16_by(issue, to, q + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
-                        k + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, ID_S, ks > 0);
-      release(&s_full[uniform(b)]);
-      release(&empty[uniform(h % SLOTS)]);
-    };
-    // The values of tile j and its weights in buffer b.
-    const auto weights_wait = [&](int b, int j) -> bool {
-      if (!slot_wait(half + 2 * j + 1) || !wait_or_abort(&p_full[uniform(b)], weighed >> b & 1)) return false;
-      weighed ^= 1u << b;
-      return true;
-    };
-    // The output += the weights in buffer b times the values of tile j.
-    const auto outputs = [&](int b, int j, bool first, bool last) {
-      const int h = half + 2 * j + 1;
-      const uint64_t v = tc::desc_sw128(ring + uniform(h % SLOTS) * P::HALF, KT * 128, 1024);
-      const uint32_t p = taddr + P::S_COL + uniform(b) * KT, d = taddr + P::O_COL + me * D;
-      const bool onto = uniform(!first);
-#pragma unroll
-      for (int ks = 0; ks < KT / 16; ++ks)
-#pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
-          tc::mma_bf16_ta_by(issue, d, p + ks * 16 + piece * 8, v + ks * 2048 / 16, ID_O, onto || ks > 0 || piece > 0);
-      if (LANES == 1 || last) release(&o_done[uniform(b)]);
-      release(&empty[uniform(h % SLOTS)]);
-    };
-    int turns = 0;
     while (run && walk.tile < stop) {
       const int count = (int)(min(walk.unit_end, stop) - walk.tile);
       const int q_slot = unit % P::QSLOTS;
-      if constexpr (LANES == 1) {  // the next tile's scores before this one's outputs
-        for (int j = 0; j <= count && run; ++j) {
-          const int b = (tile + j) & 1;
-          if (j < count) {
-            if (!keys_wait(j)) { run = false; break; }
-            tc::fence_after_sync();
-            scores(q_slot, b, j);
-          }
-          if (j > 0) {
-            if (!weights_wait(b ^ 1, j - 1)) { run = false; break; }
-            tc::fence_after_sync();
-            outputs(b ^ 1, j - 1, j == 1, true);
-          }
+      const int steps = (P::SPLIT ? (count + 1 - me) / 2 : count) * P::STEPS;
+      bool threads = true, behind = true;  // whether threads copied any of this step's tile, and of the last one's
+      const auto tile_of = [&](int i) { return i / P::STEPS * (P::SPLIT ? 2 : 1) + (P::SPLIT ? me : 0); };
+      const auto scores = [&](int i) {
+        const int j = tile_of(i), hk = half + 2 * j, sub = i % P::STEPS;
+        behind = threads;
+        if (i == 0 && !wait_or_abort(&q_full[q_slot], (unit / P::QSLOTS) & 1)) return false;
+        if (sub == 0) {
+          const int at_mask = (tile + j) % kLiveDepth;
+          if (!wait_or_abort(&live_full[at_mask], ((tile + j) / kLiveDepth) & 1)) return false;
+          threads = box == 0;
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k) threads = threads || s_live[at_mask][k] != 0xffffffffu;
+          if (!slot_wait(hk, threads || i == 0)) return false;  // the queries are always copied by threads
         }
-      } else if constexpr (P::SPLIT) {
-        for (int j = me; j < count; j += 2) {
-          if (!keys_wait(j)) { run = false; break; }
-          tc::fence_after_sync();
-          scores(q_slot, me, j);
-          if (!weights_wait(me, j)) { run = false; break; }
-          tc::fence_after_sync();
-          outputs(me, j, j < 2, j + 2 >= count);
-        }
-      } else {
-        // Outputs of a tile and scores of the next in one go, the lanes in turn: left to themselves their softmaxes fall
-        // into step, and the tensor cores wait for both.
-        for (int j = 0; j <= count; ++j, ++turns) {
-          const bool behind = threads;
-          if (j < count && !keys_wait(j)) { run = false; break; }
-          const bool now = threads;
-          threads = behind;
-          if (j > 0 && !weights_wait(me, j - 1)) { run = false; break; }
-          threads = now;
-          if ((me > 0 || turns > 0) && !wait_or_abort(&turn[me], (turns - 1 + me) & 1)) { run = false; break; }
-          tc::fence_after_sync();
-          if (j > 0) outputs(me, j - 1, j == 1, j == count);
-          if (j < count) scores(q_slot, me, j);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&turn[me ^ 1]);
-        }
+        tc::fence_after_sync();
+        const int b = uniform(2 * me + ((job + i) & 1));
+        const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + row_tile) * P::Q_TILE, 16, 1024);
+        const uint64_t k = tc::desc_sw128(ring + uniform(hk % SLOTS) * P::HALF + uniform(sub) * (kStep * 128), 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)  // descriptors count in 16 bytes
+          tc::mma_bf16_by(issue, taddr + P::S_COL + b * kStep, q + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
+                          k + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, ID_S, ks > 0);
+        release(&s_full[b]);
+        if (sub == P::STEPS - 1) release(&empty[uniform(hk % SLOTS)]);
+        return true;
+      };
+      const auto output = [&](int i, bool by_threads) {
+        const int hv = half + 2 * tile_of(i) + 1, sub = i % P::STEPS, b = uniform(2 * me + ((job + i) & 1));
+        if (sub == 0 && !slot_wait(hv, by_threads)) return false;
+        if (!wait_or_abort(&p_full[b], ((job + i) >> 1) & 1)) return false;
+        tc::fence_after_sync();
+        const uint64_t v = tc::desc_sw128(ring + uniform(hv % SLOTS) * P::HALF + uniform(sub) * (kStep * 128), KT * 128, 1024);
+        const uint32_t p = taddr + P::S_COL + b * kStep, d = taddr + P::O_COL + me * D;
+        const bool onto = uniform(i > 0);
+#pragma unroll
+        for (int ks = 0; ks < kStep / 16; ++ks)
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece)
+            tc::mma_bf16_ta_by(issue, d, p + ks * 16 + piece * 8, v + ks * 2048 / 16, ID_O, onto || ks > 0 || piece > 0);
+        release(&o_done[b]);
+        if (sub == P::STEPS - 1) release(&empty[uniform(hv % SLOTS)]);
+        return true;
+      };
+      // Scores of step i, then the output of step i - 1, whose softmax ran meanwhile.  Lanes that take tiles in turn run
+      // under each other, and would only hold the values while the next keys are on their way: output first between tiles.
+      for (int i = 0; run && i <= steps; ++i) {
+        const bool first = P::SPLIT && i % P::STEPS == 0;
+        if (first && i > 0) run = output(i - 1, threads);
+        if (run && i < steps) run = scores(i);
+        if (!first && run && i > 0) run = output(i - 1, behind);
       }
       if (!run) break;
       release(&q_empty[uniform(q_slot)]);
       half += 2 * count;
       tile += count;
+      job += steps;
       ++unit;
       walk.tile += count;
       if (walk.tile < stop) walk.next_unit(a);
@@ -558,6 +501,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           }
           copy16(q_addr + (q_slot * RT + row / kRows) * P::Q_TILE + place(row % kRows, ch, kRows), src, real);
         }
+        copy_arrive(&q_full[q_slot]);
       }
       for (; walk.tile < end; ++walk.tile, ++tile) {
         const Look next = look_up();
