@@ -19,7 +19,8 @@
 //   warps 0 .. 4 W - 1    softmax, a group of four for each of W lanes: thread = row
 //   the next W warps      issue a lane's matrix products each (one warp for both was
 //                         at work on issuing them for longer than they took)
-//   the last four         copy queries, keys and values into shared memory
+//   four more             copy keys and values into shared memory
+//   two more              copy queries
 // Work goes in steps of 64 positions.  A lane has two buffers of scores S (128 rows x
 // 64, float32), an output O and the warps between them: the scores of a step are
 // issued before the output of the last one, so they are there when its softmax ends.
@@ -40,13 +41,16 @@
 //
 // What bounds it, at 32 / 8 heads of 128 (each of the three launches under a profiler,
 // in us):
-//   16 prompts of 8192 positions, four beams each (one row tile): 76, 392 MB at 65 % of DRAM's rate;
+//   16 prompts of 8192 positions, four beams each (one row tile): 75, 392 MB at 65 % of DRAM's rate;
 //     the steps of a lane wait for one another, and a ring of five halves holds little
-//   256 users of one system prompt of 32768 (two row tiles): 155, tensor pipe 54 %;
+//   256 users of one system prompt of 32768 (two row tiles): 152, tensor pipe 54 %;
 //     softmax of 64 positions takes 1340 cycles of a warp, the three products of a step 660
 // Tried: one warp that issues both lanes' products (246 -> 300 us a call), tiles of 64
 // positions (76 -> 104, 155 -> 171: twice the copies' bookkeeping, and values held
-// through two more tiles), scores first at a tile's end with one row tile (76 -> 88).
+// through two more tiles), scores first at a tile's end with one row tile (76 -> 88),
+// parts laid out in planes of 8 channels, so that a warp's stores join (152 -> 153, and
+// the join 16 -> 18).  Of a piece's 270000 cycles 25000 pass before its first weights
+// (lengths and groups 9000, table, keys and queries 14000), 10000 with its last output.
 //
 // Every mbarrier wait is bounded in time: a role whose wait runs out records a bit
 // in the error word, raises the CTA's abort flag and leaves its loop; all meet at
@@ -66,6 +70,7 @@ namespace {
 
 constexpr int kRows = 128;       // rows of a tile
 constexpr int kLoaders = 128;    // threads
+constexpr int kQueryThreads = 64;
 constexpr float kSlack = 4.f;    // in units of log 2
 constexpr int kLiveDepth = 16;   // tiles whose masks are kept
 constexpr int kStep = 64;        // positions that a softmax takes at once
@@ -82,8 +87,9 @@ struct PrefixShape {
   static constexpr int BYTES = QSLOTS * RT * Q_TILE + SLOTS * HALF + 1024;
   static constexpr int LANES = D == 256 ? 1 : 2;
   static constexpr bool SPLIT = RT < LANES;        // lanes take tiles in turn
-  static constexpr int THREADS = LANES == 1 ? 9 * 32 : 16 * 32;
-  static constexpr int LOADER0 = LANES == 1 ? 5 : 8, PRODUCT0 = LANES == 1 ? 4 : 12;  // first warps of the roles
+  static constexpr int THREADS = LANES == 1 ? 11 * 32 : 16 * 32;
+  // first warps of the roles
+  static constexpr int LOADER0 = LANES == 1 ? 5 : 8, PRODUCT0 = LANES == 1 ? 4 : 12, QUERY0 = LANES == 1 ? 9 : 14;
   static constexpr uint32_t S_COL = 0, O_COL = LANES * 2 * kStep;   // two buffers of S for each lane, then its O
   static constexpr uint32_t COLS = 512;
   static_assert(O_COL + LANES * D <= COLS && RT <= LANES, "tensor memory");
@@ -104,6 +110,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_addr(bar))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < P::QSLOTS; ++i) {
-      mbar_init(&q_full[i], kLoaders);
+      mbar_init(&q_full[i], kQueryThreads);
       mbar_init(&q_empty[i], LANES);
     }
     for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live_full[i], kLoaders / 32);
@@ -151,6 +160,10 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     for (int i = 0; i < LANES; ++i) mbar_init(&drained[i], 1);
     s_abort = 0;
     mbar_fence_init();
+  }
+  if (tid == P::LOADER0 * 32 && box > 0) {
+    prefetch_map(&k_map);
+    prefetch_map(&v_map);
   }
   if (warp == P::PRODUCT0) tc::alloc(&s_taddr, P::COLS);
   pdl_wait();
@@ -173,6 +186,10 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       s_abort = 1;
     }
     return false;
+  };
+  constexpr int CHUNKS = D / 8;  // 16-byte pieces of a row
+  const auto place = [](int row, int ch, int rows) {  // of a 16-byte piece in an operand of `rows` rows
+    return (uint32_t)((ch >> 3) * rows * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
   };
   const bool any = start < stop;
   Walker walk;
@@ -421,16 +438,12 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   } else if (warp >= P::LOADER0 && warp < P::LOADER0 + kLoaders / 32) {
     more_registers<LANES == 1 ? 0 : -112>();
     // ---------------- copies ----------------
-    constexpr int CHUNKS = D / 8;                    // 16-byte pieces of a row
     constexpr int WARP_ROWS = KT / 4;                // keys of a warp
     constexpr int STEP_ROWS = 32 / CHUNKS;           // keys of one instruction
     static_assert(CHUNKS <= 32 && WARP_ROWS <= 32, "a row or more an instruction, a key or less a lane");
     const int lw = warp - P::LOADER0;
     const int chunk = lane % CHUNKS, sub = lane / CHUNKS;
-    const uint32_t ring = smem_addr(s_ring), q_addr = smem_addr(s_q);
-    const auto place = [](int row, int ch, int rows) {  // of a 16-byte piece in an operand of `rows` rows
-      return (uint32_t)((ch >> 3) * rows * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-    };
+    const uint32_t ring = smem_addr(s_ring);
     // This lane's key of a tile: found a tile ahead of its copy.
     Walker ahead = walk;
     struct Look {
@@ -450,7 +463,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       }
       return l;
     };
-    int half = 0, tile = 0, unit = 0;
+    int half = 0, tile = 0;
     bool run = any;
     // This warp's keys or values of a tile: by TMA where all are there and pages hold whole boxes, by threads, which put
     // zeros in the place of what is not attended to, otherwise.
@@ -485,24 +498,6 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     Look look = any ? look_up() : Look{0, 0, 0};
     while (run && walk.tile < stop) {
       const int64_t end = min(walk.unit_end, stop);
-      const int q_slot = unit % P::QSLOTS;
-      if (unit >= P::QSLOTS) {
-        if (!wait_or_abort(&q_empty[q_slot], (unit / P::QSLOTS - 1) & 1)) { run = false; break; }
-      }
-      {
-        const int left = min(walk.rows_left(), ROWS), rows = (left + 31) & ~31;
-        for (int i = tid - P::LOADER0 * 32; i < rows * CHUNKS; i += kLoaders) {
-          const int row = i / CHUNKS, ch = i % CHUNKS;
-          const bool real = row < left;
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
-          if (real) {
-            const int2 of = walk.row(a, row);
-            src += of.x * a.q_rs + of.y * a.q_hs + ch * 8;
-          }
-          copy16(q_addr + (q_slot * RT + row / kRows) * P::Q_TILE + place(row % kRows, ch, kRows), src, real);
-        }
-        copy_arrive(&q_full[q_slot]);
-      }
       for (; walk.tile < end; ++walk.tile, ++tile) {
         const Look next = look_up();
         const bool live = look.page > 0 && look.page < a.num_pages;
@@ -520,7 +515,6 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         look = next;
       }
       if (!run) break;
-      ++unit;
       walk.next_unit(a);
     }
     // No copy lands when the CTA is gone; all have been waited for but where a role gave up.
@@ -528,6 +522,37 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     for (int h = max(0, half - SLOTS); h < half; ++h) mbar_sleep_wait(&full[h % SLOTS], (h / SLOTS) & 1);
   } else {
     more_registers<LANES == 1 ? 0 : -112>();
+    // ---------------- queries of the units ----------------
+    // A thread's rows are STEP apart; addresses only step (with divisions and products for
+    // each row, on the loaders, a unit's queries took 10000 cycles).
+    constexpr int STEP = kQueryThreads / CHUNKS;
+    const int t = tid - P::QUERY0 * 32, chunk = t % CHUNKS, first_row = t / CHUNKS;
+    const int G = a.Hq / a.Hkv, over = STEP % G;
+    const int64_t step = STEP / G * a.q_rs + over * a.q_hs, wrap = a.q_rs - G * a.q_hs;
+    const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q) + chunk * 8;
+    for (int unit = 0; walk.tile < stop && any; ++unit) {
+      const int q_slot = unit % P::QSLOTS;
+      if (unit >= P::QSLOTS && !wait_or_abort(&q_empty[q_slot], (unit / P::QSLOTS - 1) & 1)) break;
+      const int left = min(walk.rows_left(), ROWS), rows = (left + 31) & ~31, i = walk.row_tile * ROWS + first_row;
+      int head = i % G;
+      const __nv_bfloat16* src = q + (walk.of.first + i / G) * a.q_rs + (walk.group * G + head) * a.q_hs;
+      const uint32_t dst = smem_addr(s_q) + q_slot * RT * P::Q_TILE + place(first_row, chunk, kRows);
+#pragma unroll 4
+      for (int row = first_row; row < rows; row += STEP) {
+        const int on = row - first_row, tile = RT == 1 ? 0 : row / kRows;
+        copy16((dst + on * 128 + tile * (P::Q_TILE - kRows * 128)) ^ ((on & 7) << 4), row < left ? src : q, row < left);
+        src += step;
+        head += over;
+        if (head >= G) {
+          head -= G;
+          src += wrap;
+        }
+      }
+      copy_arrive(&q_full[q_slot]);
+      walk.tile = min(walk.unit_end, stop);
+      if (walk.tile < stop) walk.next_unit(a);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   tc::fence_before_sync();
