@@ -29,6 +29,11 @@
 // into the 16-byte chunks, and the second product takes its positions in the
 // order in which the first leaves the weights (2 t, 2 t + 1 for lane t of four).
 // Both meet every bank once.
+//
+// Under shared prefixes (enum Over) the same loop runs over groups' common positions,
+// rows being the query heads of several sequences, and over sequences' own ones; both
+// leave parts of every warp.  6 groups of 6 sequences, 16 heads of 64, 5000 common
+// positions (0.18 GB) 47 us, bound as above; up to 100 own ones of each 15 us.
 #include <type_traits>
 
 #include "kda_attend_rows.cuh"
