@@ -88,18 +88,56 @@ __device__ __forceinline__ int2 part_note(int piece, int more, int row) { return
 struct Span {
   int first, end, tile0, tiles;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
+// `skip`: positions at the beginning that are left out.
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int n, int skip = 0) {
   const int64_t cap = (int64_t)a.table_cols * a.page_size;
   const int len = __ldg(a.lens + n);
   Span s;
   s.end = (int)min((int64_t)max(len, 0), cap);
   s.first = a.window > 0 && len > a.window ? len - a.window : 0;
-  if (a.skip != nullptr) s.first = max(s.first, __ldg(a.skip + n));
+  if (skip > 0) s.first = max(s.first, skip);
   if (s.first >= s.end) s.first = s.end = 0;
   s.tile0 = s.first / kTile;
   s.tiles = s.end == 0 ? 1 : (s.end - 1) / kTile - s.tile0 + 1;
   return s;
 }
+
+// A sequence takes part in its group's common positions where it attends to all of them.
+__device__ __forceinline__ bool takes_part(const AttendArgs& a, int n, int prefix) {
+  const int64_t cap = (int64_t)a.table_cols * a.page_size;
+  const int len = __ldg(a.lens + n);
+  return prefix > 0 && min((int64_t)max(len, 0), cap) >= prefix && (a.window == 0 || len <= a.window);
+}
+
+// Positions that a sequence leaves to its group's kernel, for sequences that go by in order: none, or found by their groups.
+struct Whole {
+  __device__ __forceinline__ int shared(const AttendArgs&, int) { return 0; }
+};
+struct Own {
+  int end = 0, prefix = 0;  // the sequences before `end` that are left have `prefix` positions in common
+  __device__ __forceinline__ int shared(const AttendArgs& a, int n) {
+    if (n >= end) {
+      int g = 0, hi = a.num_groups;
+      end = INT32_MAX;
+      while (g < hi) {  // the first group that ends behind n
+        const int mid = (int)(((unsigned)g + (unsigned)hi) >> 1), e = __ldg(a.starts + mid + 1);
+        if (e <= n) {
+          g = mid + 1;
+        } else {
+          hi = mid;
+          end = e;
+        }
+      }
+      prefix = 0;
+      if (g < a.num_groups) {
+        const int first = __ldg(a.starts + g), common = __ldg(a.prefix_lens + g);
+        if (n < first) end = first;
+        else prefix = (int)min((int64_t)max(common, 0), (int64_t)a.table_cols * a.page_size);
+      }
+    }
+    return takes_part(a, n, prefix) ? prefix : 0;
+  }
+};
 
 // The tiles of all sequences and where piece c lies in them, found by the whole
 // block; start == stop where there is no such piece.
@@ -120,12 +158,12 @@ struct Place {
     return true;
   }
 };
-template <int THREADS>
+template <int THREADS, typename Part = Whole>
 __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int c, int ctas) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place p;
   if (a.N <= 32) {  // a sequence a lane, every warp alone
-    const int64_t mine = lane < a.N ? (int64_t)span_of(a, lane).tiles * units : 0;
+    const int64_t mine = lane < a.N ? (int64_t)span_of(a, lane, Part().shared(a, lane)).tiles * units : 0;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,7 +181,8 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   const int per = (a.N + THREADS - 1) / THREADS;
   const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += span_of(a, n).tiles;
+  Part part;
+  for (int n = n0; n < n1; ++n) mine += span_of(a, n, part.shared(a, n)).tiles;
   int64_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -161,9 +200,10 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   if (!p.cut(total * units, c, ctas)) return p;  // the whole block
   int64_t at = (prior + scan - mine) * units;    // tiles before sequence n0
   if (n0 < n1 && p.start >= at && p.start < at + mine * units) {
+    Part again;
     int n = n0;
     for (; n < n1 - 1; ++n) {
-      const int64_t t = (int64_t)span_of(a, n).tiles * units;
+      const int64_t t = (int64_t)span_of(a, n, again.shared(a, n)).tiles * units;
       if (p.start < at + t) break;
       at += t;
     }
@@ -197,26 +237,12 @@ __device__ __forceinline__ Group group_of(const AttendArgs& a, int g) {
   return r;
 }
 
-// A sequence takes part in its group's common positions where it attends to all of them.
-__device__ __forceinline__ bool takes_part(const AttendArgs& a, int n, int prefix) {
-  const int64_t cap = (int64_t)a.table_cols * a.page_size;
-  const int len = __ldg(a.lens + n);
-  return prefix > 0 && min((int64_t)max(len, 0), cap) >= prefix && (a.window == 0 || len <= a.window);
-}
-
-// Warp w of `warps`: notes which sequences take part, and empty parts for those that do not.
-__device__ __forceinline__ void mark_sequences(const AttendArgs& a, int w, int warps, int lane) {
+// Warp w of `warps`: empty parts for the sequences that take no part in their groups' positions.
+__device__ __forceinline__ void leave_empty_parts(const AttendArgs& a, int w, int warps, int lane) {
   const int64_t heads = (int64_t)a.N * a.Hq;
   for (int n = w; n < a.N; n += warps) {
     const int g = find_sequence(a.starts, a.num_groups, n, lane);
-    bool part = false;
-    int prefix = 0;
-    if (g < a.num_groups && n >= __ldg(a.starts + g)) {
-      prefix = group_of<1, 1>(a, g).prefix;
-      part = takes_part(a, n, prefix);
-    }
-    if (lane == 0) a.mark[n] = part ? prefix : 0;
-    if (part) continue;
+    if (g < a.num_groups && n >= __ldg(a.starts + g) && takes_part(a, n, group_of<1, 1>(a, g).prefix)) continue;
     for (int h = lane; h < a.Hq; h += 32) {
       const int64_t head = (int64_t)n * a.Hq + h;
       a.parts.first_note[head] = part_note(0, 0, 0);
@@ -323,14 +349,16 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 }
 
 // Where a walk over the piece's tiles stands.
-struct Walk {
+template <typename Part>
+struct WalkOf {
   int64_t tile, unit_start, unit_end;
   int n, group;
   Span sp;
+  Part part;
   __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
     tile = p.start;
     n = p.n;
-    sp = span_of(a, n);
+    sp = span_of(a, n, part.shared(a, n));
     group = (int)quotient(tile - p.before, sp.tiles);
     unit_start = p.before + (int64_t)group * sp.tiles;
     unit_end = unit_start + sp.tiles;
@@ -339,11 +367,12 @@ struct Walk {
     unit_start = unit_end;
     if (++group == units) {
       group = 0;
-      if (++n < a.N) sp = span_of(a, n);
+      if (++n < a.N) sp = span_of(a, n, part.shared(a, n));
     }
     unit_end = unit_start + sp.tiles;
   }
 };
+using Walk = WalkOf<Whole>;
 
 __device__ __forceinline__ PieceNote note_of(const Walk& w, const Place& p) {
   PieceNote note;

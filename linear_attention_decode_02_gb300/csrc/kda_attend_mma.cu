@@ -37,8 +37,10 @@
 //
 // With PARTS sequences begin behind a prefix that they share, and each warp leaves
 // its own part of a unit to another kernel's join: 256 sequences of up to 600 such
-// positions, 0.32 GB, 72 us (66 % of the copy bandwidth; 94 us where a block's warps
+// positions, 0.32 GB, 74 us (64 % of the copy bandwidth; 94 us where a block's warps
 // joined theirs first).  What is left are the starts and ends of 2048 short units.
+#include <type_traits>
+
 #include "kda_attend_rows.cuh"
 
 namespace kda {
@@ -58,7 +60,9 @@ struct Shape {
   static constexpr int CTAS = blocks_per_sm(D);
   static constexpr int STAGES = D == 64 ? 6 : 3;
   static constexpr bool QS = D == 256;  // no registers are left for the queries: they lie in shared memory
-  using Copies = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true>;
+  template <typename W>
+  using CopiesOver = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true, W>;
+  using Copies = CopiesOver<Walk>;
 };
 template <int D, int HG>
 constexpr int smem_bytes() {
@@ -90,7 +94,8 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 template <int D, int HG, bool PARTS>
 __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
-  using Copies = typename Shape<D, HG>::Copies;
+  using Part = std::conditional_t<PARTS, Own, Whole>;
+  using Copies = typename Shape<D, HG>::template CopiesOver<WalkOf<Part>>;
   constexpr int STAGES = Shape<D, HG>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 16, NT = D / 8;
   constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
@@ -102,16 +107,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   const int g = lane >> 2, t4 = lane & 3;
   const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
   const int C = gridDim.x, c = blockIdx.x;
-  pdl_wait();
+  // Parts go where the kernel before writes nothing, and nothing that it writes is read: that kernel has waited for all
+  // before it when this one begins, and is waited for at the end.
+  if (!PARTS) pdl_wait();
   pdl_launch_dependents();
-  const Place place = find_place<kThreads>(a, units, c, C);
+  const Place place = find_place<kThreads, Part>(a, units, c, C);
   const Workspace ws(a.work, C, HG, D);
   if (place.start == place.stop) {
-    if (threadIdx.x == 0) ws.note[c].n = -1;
+    if (PARTS) pdl_wait();
+    else if (threadIdx.x == 0) ws.note[c].n = -1;
     return;
   }
 
-  Walk walk;
+  WalkOf<Part> walk;
   walk.start(a, place);
   int stage = 0, parity = 0;
   // Queries of the next unit, on their way while this one is worked on: the
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   constexpr int QN = PAIR ? 2 : 4, SHARE = HG * D / 8 / kThreads;
   uint32_t q_next[QS ? 1 : KSTEPS][QN];
   uint4 q_share[QS ? SHARE : 1];
-  const auto load_q = [&](const Walk& w) {
+  const auto load_q = [&](const WalkOf<Part>& w) {
     const int hk = w.group / groups, g0 = (w.group - hk * groups) * HG, heads = min(HG, G - g0);
     const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + w.n * a.q_rs + (hk * G + g0) * a.q_hs;
     if constexpr (QS) {
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
 #pragma unroll
         for (int i = 0; i < QN; ++i) q[k][i] = q_next[k][i];
     }
-    Walk after = walk;
+    WalkOf<Part> after = walk;
     if (walk.unit_end < place.stop) {
       after.next_unit(a, units);
       load_q(after);
@@ -310,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     walk = after;
   }
   copy_wait<0>();
+  if (PARTS) pdl_wait();
 }
 
 template <int D, int HG, bool PARTS>
@@ -322,7 +331,7 @@ cudaError_t launch_parts(const AttendArgs& a, const AttendPlan& p, cudaStream_t 
 }
 template <int D, int HG>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
-  return a.skip != nullptr ? launch_parts<D, HG, true>(a, p, s) : launch_parts<D, HG, false>(a, p, s);
+  return a.own != 0 ? launch_parts<D, HG, true>(a, p, s) : launch_parts<D, HG, false>(a, p, s);
 }
 
 }  // namespace

@@ -33,7 +33,7 @@
 // Under shared prefixes (enum Over) the same loop runs over groups' common positions,
 // rows being the query heads of several sequences, and over sequences' own ones; both
 // leave parts of every warp.  6 groups of 6 sequences, 16 heads of 64, 5000 common
-// positions (0.18 GB) 47 us, bound as above; up to 100 own ones of each 15 us.
+// positions (0.18 GB) 47 us, bound as above; up to 100 own ones of each 17 us.
 #include <type_traits>
 
 #include "kda_attend_rows.cuh"
@@ -100,7 +100,9 @@ enum class Over { kSequences, kOwn, kGroups };
 template <int D, int HG, Over OVER>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(const __grid_constant__ AttendArgs a) {
   constexpr bool GROUPS = OVER == Over::kGroups;
-  using W = std::conditional_t<GROUPS, GroupWalk<kTile, HG>, Walk>;
+  constexpr bool OWN = OVER == Over::kOwn;
+  using Part = std::conditional_t<OWN, Own, Whole>;
+  using W = std::conditional_t<GROUPS, GroupWalk<kTile, HG>, WalkOf<Part>>;
   using Copies = typename Shape<D>::template CopiesOver<W>;
   constexpr int WARPS = Shape<D>::WARPS, THREADS = Shape<D>::THREADS, STAGES = Shape<D>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 8, NT = D / 8;
@@ -115,15 +117,16 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   // Of a sequence, `groups` units a key head; of a group, the walk counts row tiles by itself.
   const int G = a.Hq / a.Hkv, groups = GROUPS ? 1 : (G + HG - 1) / HG, units = a.Hkv * groups;
   const int C = gridDim.x, c = blockIdx.x;
-  pdl_wait();
+  if (!OWN) pdl_wait();  // as in the bfloat16 kernel
   pdl_launch_dependents();
-  if constexpr (GROUPS) mark_sequences(a, c * WARPS + warp, C * WARPS, lane);
+  if constexpr (GROUPS) leave_empty_parts(a, c * WARPS + warp, C * WARPS, lane);
   Place place;
   if constexpr (GROUPS) place = find_group_place<THREADS, kTile, HG>(a, c, C);
-  else place = find_place<THREADS>(a, units, c, C);
+  else place = find_place<THREADS, Part>(a, units, c, C);
   const Workspace ws(a.work, C, HG, D);
   if (place.start == place.stop) {
     if (OVER == Over::kSequences && threadIdx.x == 0) ws.note[c].n = -1;
+    if (OWN) pdl_wait();
     return;
   }
 
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
             return takes_part(a, at.x, walk.of.prefix) ? (int64_t)at.x * a.Hq + at.y : -1;
           },
           rows_of(walk), o, m, l, warp, g, t4, c);
-    } else if constexpr (OVER == Over::kOwn) {
+    } else if constexpr (OWN) {
       const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG;
       leave_parts<D, HG, WARPS, RS>(a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; },
                                     min(HG, G - g0), o, m, l, warp, g, t4, c);
@@ -353,6 +356,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
     walk = after;
   }
   copy_wait<0>();
+  if (OWN) pdl_wait();
 }
 
 template <int D, int HG, Over OVER>

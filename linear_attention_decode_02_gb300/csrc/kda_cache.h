@@ -103,12 +103,11 @@ struct AttendArgs {
   int32_t window;                         // 0: all
   float scale_log2;                       // scale * log2(e)
   int32_t vec16;                          // q rows, key and value vectors start on 16-byte boundaries
-  // Under shared prefixes (null otherwise).  Group g is sequences starts[g] .. starts[g + 1] - 1, whose first
-  // prefix_lens[g] positions are attended to by one kernel, which notes in `mark` how many those are for each sequence;
-  // the other leaves out the first `skip` positions of each.  Both leave parts.
+  // Under shared prefixes (zero otherwise).  Group g is sequences starts[g] .. starts[g + 1] - 1, whose first
+  // prefix_lens[g] positions are attended to by one kernel and left out by the other, which is told so by `own`.
+  // Both leave parts.
   const int32_t* starts; const int32_t* prefix_lens; int32_t num_groups;
-  int32_t* mark;
-  const int32_t* skip;
+  int32_t own;
   Parts parts;
 };
 constexpr int kAttendWarps = 4;  // of a block of the tensor-core kernel

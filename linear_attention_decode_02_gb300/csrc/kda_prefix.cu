@@ -52,6 +52,11 @@
 // the join 16 -> 18).  Of a piece's 270000 cycles 25000 pass before its first weights
 // (lengths and groups 9000, table, keys and queries 14000), 10000 with its last output.
 //
+// The kernel of own positions reads nothing that this one writes and writes elsewhere.
+// So it begins as this one's blocks leave, all of which have waited for what came
+// before the call, and waits for this one at its own end: 101 -> 94 us for the 16
+// prompts, 243 -> 229 for the 256 users.
+//
 // Every mbarrier wait is bounded in time: a role whose wait runs out records a bit
 // in the error word, raises the CTA's abort flag and leaves its loop; all meet at
 // the end before tensor memory is freed.
@@ -197,8 +202,8 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
 
   if (warp < 4 * LANES) {
     more_registers<LANES == 1 ? 0 : 144>();
-    // ---------------- which sequences take part, and softmax ----------------
-    mark_sequences(a, c * 4 * LANES + warp, C * 4 * LANES, lane);
+    // ---------------- softmax ----------------
+    leave_empty_parts(a, c * 4 * LANES + warp, C * 4 * LANES, lane);
     const int me = LANES == 1 ? 0 : warp >> 2;   // lane of the CTA
     const int row_tile = RT == 1 ? 0 : me;
     const int row = (warp & 3) * 32 + lane;      // of the row tile, and tensor-memory lane
@@ -679,11 +684,10 @@ __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_const
 }
 
 // The paged kernel's grid for sequences' own positions, the kernel over the groups' common ones, both kernels' parts
-// and the sequences' marks in the workspace, and its size.
+// in the workspace, and its size.
 struct PrefixPlan {
   AttendPlan own, pre;
   Parts own_parts, pre_parts;
-  int32_t* mark;
   int64_t floats;
 };
 PrefixPlan prefix_plan(float* work, int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms, int64_t groups) {
@@ -714,18 +718,15 @@ PrefixPlan prefix_plan(float* work, int64_t N, int32_t Hq, int32_t Hkv, int32_t 
   if (dtype == KDA_DT_F32) {
     p.own = attend_tf32_plan(G, D, sms);
     p.pre = attend_tf32_plan(rows <= 8 ? 8 : 16, D, sms);
-    take(p.own.ctas * (int64_t)kNoteFloats);
     p.own_parts = parts(p.own.ctas, kTf32PartWarps, p.own.heads, p.own.heads);
     p.pre_parts = parts(p.pre.ctas, kTf32PartWarps, p.pre.heads, 16);
   } else {
     p.own = attend_mma_plan(G, D, sms);
     p.pre.ctas = sms;
     p.pre.heads = D < 256 && rows > kRows ? 2 * kRows : kRows;
-    take(p.own.ctas * (int64_t)kNoteFloats);  // the notes that the paged kernel leaves all the same
     p.own_parts = parts(p.own.ctas, kAttendWarps, p.own.heads, p.own.heads);
     p.pre_parts = parts(p.pre.ctas, 1, p.pre.heads, 2 * kRows);
   }
-  p.mark = reinterpret_cast<int32_t*>(take(N));
   p.floats = at;
   return p;
 }
@@ -806,7 +807,6 @@ cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaSt
   const bool f32 = a.dtype == KDA_DT_F32;
   const PrefixPlan p = prefix_plan(a.work, a.N, a.Hq, a.Hkv, a.D, a.dtype, sms, a.num_groups);
   a.parts = p.pre_parts;
-  a.mark = p.mark;
   const bool two = p.pre.heads > kRows;
   cudaError_t e = cudaErrorInvalidValue;
   if (f32) e = launch_attend_tf32_groups(a, p.pre, s);
@@ -815,7 +815,7 @@ cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaSt
   else if (a.D == 256) e = launch_prefix<256, 1>(a, sms, s);
   if (e != cudaSuccess) return e;
   a.parts = p.own_parts;
-  a.skip = p.mark;
+  a.own = 1;
   e = f32 ? launch_attend_tf32_own(a, p.own, s) : launch_attend_mma(a, p.own, s);
   if (e != cudaSuccess) return e;
   if (a.D == 64) return launch_prefix_join<64>(a, p, sms, s);

@@ -417,3 +417,24 @@ def test_repeats_streams_and_graphs_give_the_same_bits(dtype, beams):
     torch.cuda.synchronize()
     for o, e in outs:
         assert same(o, out) and same(e, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_inputs_written_just_before_the_call(dtype):
+    """Nothing is waited for on the host between the kernels that write a call's inputs, over those of the last call,
+    and the call: every one of its kernels reads the new ones."""
+    groups = [(700, [5, 9, 30, 200]), (300, [1, 2, 60, 400]), (40, [3, 3, 3, 3])]
+    cases = [make([groups[i] for i in order], Hq=16, Hkv=8, dtype=dtype, seed=seed, page=32)
+             for seed, order in enumerate([(0, 1, 2), (2, 0, 1), (1, 2, 0), (2, 1, 0)])]
+    wanted = [tuple(t.clone() for t in run(c)) for c in cases]
+    now = {key: torch.empty_like(t) for key, t in cases[0].items()}
+    out = []
+    for i in range(48):
+        for key, t in cases[i % 4 if i < 24 else (i * 7 // 3) % 4].items():
+            now[key].copy_(t)
+        out.append(tuple(t.clone() for t in run(now)))
+    torch.cuda.synchronize()
+    assert binding.kda_device_error() == 0
+    for i, got in enumerate(out):
+        for a, b in zip(got, wanted[i % 4 if i < 24 else (i * 7 // 3) % 4]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
