@@ -74,7 +74,8 @@ struct PagesArgs {
   int32_t* cu; int32_t* slots;                       // [N + 1], [R]
   int32_t N, page_size;
   int64_t R;
-  int32_t run;                                       // rows a thread takes at once (set by the launcher)
+  // A place / page_size is (place * page_factor) >> page_shift for places below 2^31 (set by the launcher).
+  uint32_t page_factor; int32_t page_shift;
 };
 cudaError_t launch_page_assign(const PagesArgs& a, cudaStream_t s);
 

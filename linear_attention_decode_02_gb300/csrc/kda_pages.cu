@@ -2,24 +2,32 @@
 // and shrunk into a ring of free pages, and the slot of every new token row.
 //
 // With held_n = ceil(old_n / page_size) and want_n = ceil(new_n / page_size) the
-// pages taken are sums over the sequences before n, so three prefix sums (pages
-// asked for, to decide who is served; then pages taken, rows and pages given
-// back) say where everything goes, and all writes are independent.  Free pages
-// are taken from the ring's head and given back behind its tail: no place of the
-// ring is both read and written in a call.
+// pages taken are sums over the sequences before n, so prefix sums (pages taken,
+// rows, pieces, pages given back) say where everything goes, and all writes are
+// independent.  They are made as if all were served; where that takes more pages than
+// are free, the first of them says who is, and they are made again.  Free pages are
+// taken from the ring's head and given back behind its tail: no place of the ring
+// is both read and written in a call.
+//
+// Slots come in pieces, the new rows of a sequence that lie on one page: a lane
+// searches a piece's sequence and loads its page once, then lanes write its rows.
 //
 // Bound by latency: the widest call moves a few MB.  So it is one launch of one
 // thread-block cluster: every CTA makes the sums for itself in shared memory,
 // only the count of the pages given back, which has to read the table, is shared
 // out and exchanged over distributed shared memory, and one cluster barrier
 // separates the last read of the lengths and the ring's state from the first
-// write, so both may be updated in place.  Small calls are one CTA.
+// write, so both may be updated in place.  Small calls are one CTA.  Every
+// instruction runs a few times at most, so that fewer of them count: sums in 32 bits
+// that saturate, by the warps that have sequences, and division by a factor.
 //
-// Measured, one call after another: 8 sequences of a step 5.6 us (7.1 with the host's
-// part, through the binding); 512 sequences, a few ended, 47,515 rows 12.4 us; 48
-// prompts of up to 16,384 tokens, 486,830 rows, 12.1 us.  With 8 CTAs 19.8 and 19.5
-// us, with 512 threads a CTA 17.1 and 13.1; rows taken 4 at a time 28.8 us for the
-// prompts (8 CTAs), 16 at a time 13.0, 32 at a time 12.1.
+// Measured in a graph, one call after another: 8 sequences of a step 3.8 us (6.6 to 7.1
+// with the host's part, through the binding; 5.7 with 64-bit sums and divisions); 512
+// sequences, a few ended, 47,515 rows 8.8 us (12.2); 48 prompts of up to 16,384
+// tokens, 486,830 rows, 8.4 us (12.0): half of that is writing 2 MB from 16 SMs, which
+// took as long with 15 pieces a warp, all warps at work, and longer with four or
+// eight rows a lane that searches for itself (10.9 us; 512 sequences 12.3).  With 8 CTAs
+// instead of 16, before these steps, 19.8 and 19.5 us, with 512 threads a CTA 17.1 and 13.1.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -34,38 +42,46 @@ namespace kda {
 namespace {
 
 constexpr int kMostThreads = 1024;
+constexpr int kPiece = 256;  // most rows of a piece
 constexpr int kCluster = 16, kPortableCluster = 8;  // CTAs; more than 8 a device need not grant
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+// a + b, or the largest int32 where that is less; so sums of what is not negative saturate in any order.
+__device__ __forceinline__ int saturated(int a, int b) {
+  return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)INT32_MAX);
+}
 
-// Exclusive prefix sums of V values a thread over the block; `total` their sums.
-// `scratch` holds [warps][V] and may be used again after the next __syncthreads.
+// Exclusive saturating prefix sums of V values a thread over the first `warps`
+// warps of the block; `total` their sums.  The other warps only pass the barrier.
 template <int V>
-__device__ __forceinline__ void block_scan(int64_t (&x)[V], int64_t (&total)[V], int64_t (*scratch)[V]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int64_t own[V];
+__device__ __forceinline__ void block_scan(int (&x)[V], int (&total)[V], int (*scratch)[V], int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < warps) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    own[v] = x[v];
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, x[v], o);
-      if (lane >= o) x[v] += up;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, x[v], o);
+        if (lane >= o) x[v] = saturated(x[v], up);
+      }
+      if (lane == 31) scratch[warp][v] = x[v];
+      const int before = __shfl_up_sync(0xffffffffu, x[v], 1);
+      x[v] = lane > 0 ? before : 0;
     }
-    if (lane == 31) scratch[warp][v] = x[v];
   }
   __syncthreads();
+  if (warp < warps) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int64_t w = lane < warps ? scratch[lane][v] : 0;
-    int64_t before = lane < warp ? w : 0, all = w;
+    for (int v = 0; v < V; ++v) {
+      int w = lane < warps ? scratch[lane][v] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-      all += __shfl_xor_sync(0xffffffffu, all, o);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w = saturated(w, up);
+      }
+      total[v] = __shfl_sync(0xffffffffu, w, 31);
+      const int before = __shfl_sync(0xffffffffu, w, max(warp, 1) - 1);
+      if (warp > 0) x[v] = saturated(x[v], before);
     }
-    x[v] += before - own[v];
-    total[v] = all;
   }
 }
 
@@ -82,13 +98,14 @@ __device__ __forceinline__ int owner_of(const int* first, int N, int i) {
 
 __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __grid_constant__ PagesArgs a) {
   extern __shared__ int smem[];
-  __shared__ int64_t s_asked[kMostThreads / 32][1], s_sums[kMostThreads / 32][3];
+  __shared__ int s_sums[kMostThreads / 32][4], s_takes, s_given, s_pieces;
   const int N = a.N, page_size = a.page_size, threads = blockDim.x, tid = threadIdx.x, lane = tid & 31;
   int* s_old = smem;            // [N] length before
   int* s_new = s_old + N;       // [N] length wanted, then the one given; -1: more than the table holds
   int* s_take = s_new + N;      // [N] first page taken, counted over the call
   int* s_rel = s_take + N;      // [N] pages given back, then the first of them
-  int* s_cu = s_rel + N;        // [N + 1] first row
+  int* s_piece = s_rel + N;     // [N] first piece
+  int* s_cu = s_piece + N;      // [N + 1] first row
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   if (ctas > 1) cluster.sync();  // every CTA runs, so its shared memory can be written
@@ -102,26 +119,30 @@ __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __g
   const int cap = (int)min((int64_t)a.table_cols * page_size, (int64_t)INT32_MAX);
   const int per = (N + threads - 1) / threads;
   const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
-  for (int n = n0; n < n1; ++n) {
-    s_old[n] = min(max(a.old_lens[n], 0), cap);
+  const auto page_of = [&](int place) { return (int)(((uint64_t)(uint32_t)place * a.page_factor) >> a.page_shift); };
+  const auto pages_of = [&](int places) { return places > 0 ? page_of(places - 1) + 1 : 0; };
+  const auto old_of = [&](int n) { return min(max(a.old_lens[n], 0), cap); };
+  const auto new_of = [&](int n) {  // -1: more than the table holds
     const int to = max(a.new_lens[n], 0);
-    s_new[n] = to > cap ? -1 : to;
+    return to > cap ? -1 : to;
+  };
+  for (int n = n0; n < n1; ++n) {
+    s_old[n] = old_of(n);
+    s_new[n] = new_of(n);
   }
-  __syncthreads();
 
   // Pages given back, a warp a sequence: those of the table's columns past the
   // new length that are real and not of the shared beginning.
   const int warps = threads >> 5;
-  const auto released = [&](int n, int& lo, int& hi) {
-    const int to = s_new[n];
-    hi = ceil_div(s_old[n], page_size);
-    lo = to < 0 ? hi : ceil_div(to, page_size);
-    if (lo < hi && a.shared_lens != nullptr) lo = max(lo, max(__ldg(a.shared_lens + n), 0) / page_size);
+  const auto released = [&](int n, int old, int to, int& lo, int& hi) {
+    hi = pages_of(old);
+    lo = to < 0 ? hi : pages_of(to);
+    if (lo < hi && a.shared_lens != nullptr) lo = max(lo, page_of(max(__ldg(a.shared_lens + n), 0)));
   };
   constexpr int AHEAD = 8;
   for (int n = rank * warps + (tid >> 5); n < N; n += ctas * warps) {
     int lo, hi, found = 0;
-    released(n, lo, hi);
+    released(n, old_of(n), new_of(n), lo, hi);  // not those in shared memory, which would be waited for
     for (int col = lo; col < hi; col += 32 * AHEAD) {
       int page[AHEAD];
 #pragma unroll
@@ -135,42 +156,58 @@ __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __g
   if (ctas > 1) cluster.sync();  // all counts are here, and every CTA has read the lengths and the state
   else __syncthreads();
 
+  // A sequence's new rows come in pieces: what lies on one page, or, of pages of more than kPiece, that many rows, which
+  // lie on two at most.
+  const int piece = min(page_size, kPiece);
+  const auto piece0 = [&](int old) { return page_size <= kPiece ? page_of(old) * page_size : old; };  // where the first would begin
   // Who is served: those that ask for no page, and those whose pages, counted
-  // with all asked for before them, are there.
-  int64_t asked[1] = {0}, all_asked[1];
-  for (int n = n0; n < n1; ++n)
-    if (s_new[n] >= 0) asked[0] += max(0, ceil_div(s_new[n], page_size) - ceil_div(s_old[n], page_size));
-  block_scan<1>(asked, all_asked, s_asked);
-  int64_t sums[3] = {0, 0, 0}, all[3];  // pages taken, rows, pages given back
-  for (int n = n0; n < n1; ++n) {
-    const int old = s_old[n];
-    int to = s_new[n], take = 0;
-    if (to >= 0) take = max(0, ceil_div(to, page_size) - ceil_div(old, page_size));
-    asked[0] += take;
-    if (to < 0 || (take > 0 && asked[0] > count)) {
-      to = old;
-      take = 0;
+  // with all asked for before them, are there.  Mostly that is everybody, and the
+  // sums for everybody are the ones wanted; else they are made once more.
+  const int scanning = N == 0 ? 0 : ((N + per - 1) / per + 31) / 32;  // warps that have sequences
+#pragma unroll 1
+  for (bool scarce = false;; scarce = true) {
+    int sums[4] = {0, 0, 0, 0}, all[4] = {0, 0, 0, 0};  // pages taken, rows, pieces, pages given back
+    for (int n = n0; n < n1; ++n) {
+      const int old = s_old[n];
+      int to = s_new[n], take = to < 0 ? 0 : max(0, pages_of(to) - pages_of(old));
+      if (to < 0 || (scarce && take > 0 && saturated(s_take[n], take) > count)) {
+        s_new[n] = to = old;
+        take = 0;
+      }
+      const int last = to - 1 - piece0(old);  // from where the first piece would begin to the last row
+      const int pieces = to <= old ? 0 : (page_size <= kPiece ? page_of(last) : last / kPiece) + 1;
+      s_take[n] = take;
+      s_piece[n] = pieces;
+      sums[0] = saturated(sums[0], take);
+      sums[1] = saturated(sums[1], max(0, to - old));
+      sums[2] = saturated(sums[2], pieces);
+      if (!scarce) sums[3] = saturated(sums[3], s_rel[n]);  // who grows gives none back
     }
-    s_new[n] = to;
-    s_take[n] = take;
-    sums[0] += take;
-    sums[1] += max(0, to - old);
-    sums[2] += s_rel[n];
+    block_scan<4>(sums, all, s_sums, scanning);
+    for (int n = n0; n < n1; ++n) {
+      const int take = s_take[n], pieces = s_piece[n], rel = s_rel[n];
+      s_take[n] = sums[0];
+      s_cu[n] = sums[1];
+      s_piece[n] = sums[2];
+      sums[0] = saturated(sums[0], take);
+      sums[1] = saturated(sums[1], max(0, s_new[n] - s_old[n]));
+      sums[2] = saturated(sums[2], pieces);
+      if (!scarce) {
+        s_rel[n] = sums[3];
+        sums[3] = saturated(sums[3], rel);
+      }
+    }
+    if (tid == 0) {
+      s_takes = all[0];
+      s_cu[N] = all[1];
+      s_pieces = all[2];
+      if (!scarce) s_given = all[3];
+    }
+    __syncthreads();
+    if (scarce || s_takes <= count) break;
   }
-  block_scan<3>(sums, all, s_sums);
-  for (int n = n0; n < n1; ++n) {
-    const int take = s_take[n], rel = s_rel[n];
-    s_take[n] = (int)sums[0];
-    s_rel[n] = (int)min(sums[2], (int64_t)INT32_MAX);
-    s_cu[n] = (int)min(sums[1], (int64_t)INT32_MAX);
-    sums[0] += take;
-    sums[1] += max(0, s_new[n] - s_old[n]);
-    sums[2] += rel;
-  }
-  if (tid == 0) s_cu[N] = (int)min(all[1], (int64_t)INT32_MAX);
-  __syncthreads();
 
-  const int takes = (int)all[0], rows = s_cu[N];
+  const int takes = s_takes, rows = s_cu[N];
   const auto ring = [&](uint32_t i) {  // place i <= C behind the head
     i += (uint32_t)head;
     return i >= C ? i - C : i;
@@ -183,16 +220,16 @@ __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __g
     if (tid == 0) {
       a.cu[N] = rows;
       a.state_out[0] = (int)ring((uint32_t)takes);
-      a.state_out[1] = (int)(count - takes + min(all[2], (int64_t)C - count));
+      a.state_out[1] = count - takes + min(s_given, (int)C - count);
     }
   }
   for (int64_t i = (int64_t)rank * threads + tid; i < takes; i += (int64_t)ctas * threads) {
     const int n = owner_of(s_take, N, (int)i);
-    a.table[n * a.table_rs + ceil_div(s_old[n], page_size) + ((int)i - s_take[n])] = a.ring[ring((uint32_t)i)];
+    a.table[n * a.table_rs + pages_of(s_old[n]) + ((int)i - s_take[n])] = a.ring[ring((uint32_t)i)];
   }
   for (int n = rank * warps + (tid >> 5); n < N; n += ctas * warps) {
     int lo, hi;
-    released(n, lo, hi);
+    released(n, s_old[n], s_new[n], lo, hi);
     int64_t at = s_rel[n];
     for (int col = lo; col < hi; col += 32 * AHEAD) {
       int page[AHEAD];
@@ -209,57 +246,68 @@ __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __g
     }
   }
 
-  // Slots.  A thread takes a.run rows, found by one search, one look-up a page.
-  const bool wide = reinterpret_cast<uintptr_t>(a.slots) % 16 == 0;
-  for (int64_t r0 = (int64_t)a.run * ((int64_t)rank * threads + tid); r0 < a.R; r0 += (int64_t)a.run * ctas * threads) {
-    int n = 0, stop = 0, col = 0, off = 0, held = 0, page = 0;
-    bool enter = true;  // a sequence's first row here
-    if (r0 < rows) {
-      n = owner_of(s_cu, N, (int)r0);
-      stop = s_cu[n + 1];
+  // Slots, 32 pieces a warp: a lane finds one, then all write each, or, where all are short, every lane its own.
+  const auto page_at = [&](int n, int held, int col) {
+    return col < held ? a.table[n * a.table_rs + col] : a.ring[ring((uint32_t)(s_take[n] + (col - held)))];
+  };
+  const auto slot_of = [&](int page, int off) { return page > 0 && (uint32_t)page <= C ? page * page_size + off : -1; };
+  const int pieces = s_pieces;
+  // Lanes that write a piece together.
+  const int share = piece <= 8 ? 8 : (piece <= 16 ? 16 : 32), x0 = lane & (share - 1);
+  for (int64_t i0 = 32LL * ((tid >> 5) * ctas + rank); i0 < pieces; i0 += 32LL * warps * ctas) {
+    int row = 0, len = 0, left = 0;   // the piece's first row, its rows, those on its first page
+    int first = -1, second = -1;  // slots of its first place and of the next page's
+    if (i0 + lane < pieces) {
+      const int n = owner_of(s_piece, N, (int)i0 + lane), old = s_old[n], held = pages_of(old);
+      const int64_t start = piece0(old) + (int64_t)((int)i0 + lane - s_piece[n]) * piece;
+      const int from = (int)max(start, (int64_t)old), to = (int)min(start + piece, (int64_t)s_new[n]);
+      const int col = page_of(from), off = from - col * page_size;
+      row = saturated(s_cu[n], from - old);
+      len = (int)min((int64_t)(to - from), a.R - row);
+      left = page_size - off;
+      if (len > 0) first = slot_of(page_at(n, held, col), off);
+      if (left < len) second = slot_of(page_at(n, held, col + 1), 0);
     }
-    for (int64_t r = r0; r < min(r0 + a.run, a.R); r += 4) {
-      int slot[4] = {-1, -1, -1, -1};
+    if (__shfl_sync(0xffffffffu, row, 0) >= a.R) break;  // nor are later ones wanted
+    if (__all_sync(0xffffffffu, len <= 4 && len <= left)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r + j >= rows) break;
-        if (r + j >= stop) {
-          do stop = s_cu[++n + 1];
-          while (r + j >= stop);
-          enter = true;
-        }
-        bool turn = enter;
-        if (enter) {
-          const int pos = s_old[n] + ((int)r + j - s_cu[n]);
-          col = pos / page_size;
-          off = pos - col * page_size;
-          held = ceil_div(s_old[n], page_size);
-          enter = false;
-        } else if (++off == page_size) {
-          ++col;
-          off = 0;
-          turn = true;
-        }
-        if (turn)
-          page = col < held ? a.table[n * a.table_rs + col] : a.ring[ring((uint32_t)(s_take[n] + (col - held)))];
-        if (page > 0 && (uint32_t)page <= C) slot[j] = page * page_size + off;
+      for (int x = 0; x < 4; ++x)
+        if (x < len) a.slots[row + x] = first < 0 ? -1 : first + x;
+    } else if (page_size <= kPiece) {  // one page each
+#pragma unroll 4
+      for (int k = 0; k < 32; k += 32 / share) {
+        const int from = k + lane / share;
+        const int n = __shfl_sync(0xffffffffu, len, from), at = __shfl_sync(0xffffffffu, first, from);
+        int32_t* const to = a.slots + __shfl_sync(0xffffffffu, row, from);
+        for (int x = x0; x < n; x += share) to[x] = at < 0 ? -1 : at + x;
       }
-      if (wide && r + 4 <= a.R) {
-        *reinterpret_cast<int4*>(a.slots + r) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (r + j < a.R) a.slots[r + j] = slot[j];
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < 32; ++k) {
+        const int n = __shfl_sync(0xffffffffu, len, k), here = __shfl_sync(0xffffffffu, left, k);
+        const int at = __shfl_sync(0xffffffffu, first, k), after = __shfl_sync(0xffffffffu, second, k);
+        int32_t* const to = a.slots + __shfl_sync(0xffffffffu, row, k);
+        for (int x = lane; x < n; x += 32) {
+          const int page = x < here ? at : after;
+          to[x] = page < 0 ? -1 : page + (x < here ? x : x - here);
+        }
       }
     }
   }
+  for (int64_t r = rows + (int64_t)rank * threads + tid; r < a.R; r += (int64_t)ctas * threads) a.slots[r] = -1;
 }
 
 }  // namespace
 
 cudaError_t launch_page_assign(const PagesArgs& given, cudaStream_t s) {
   PagesArgs a = given;
-  const int bytes = (5 * a.N + 1) * (int)sizeof(int), most_bytes = (5 * kPageSequences + 1) * (int)sizeof(int);
+  // Division by an invariant (Granlund and Montgomery, 1994): with 2^(k-1) < d <= 2^k and f = floor(2^(31+k) / d) + 1,
+  // f d - 2^(31+k) is 1 to d, at most 2^k, so that floor(n f / 2^(31+k)) = floor(n / d) for n < 2^31.
+  int k = 0;
+  while ((int64_t{1} << k) < a.page_size) ++k;
+  a.page_shift = 31 + k;
+  a.page_factor = (uint32_t)((uint64_t{1} << a.page_shift) / (uint32_t)a.page_size + 1);
+  const int bytes = (6 * a.N + 1) * (int)sizeof(int), most_bytes = (6 * kPageSequences + 1) * (int)sizeof(int);
   static std::atomic<bool> set[64];
   static std::atomic<int> granted[64];  // CTAs of a cluster, 0: not asked yet
   int dev = 0;
@@ -288,8 +336,6 @@ cudaError_t launch_page_assign(const PagesArgs& given, cudaStream_t s) {
     granted[dev].store(cluster, std::memory_order_release);
   }
   const int threads = cluster > 1 ? kMostThreads : 256;
-  const int64_t each = (a.R + 4LL * cluster * threads - 1) / (4LL * cluster * threads);
-  a.run = 4 * (int)std::max<int64_t>(1, std::min<int64_t>(each, 8));
   return launch_pdl(kda_page_assign_kernel, dim3(cluster), dim3(threads), bytes, s, cluster, a);
 }
 

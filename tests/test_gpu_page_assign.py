@@ -227,3 +227,28 @@ def test_streams_at_once():
     for x, o, ref in zip(inputs, outs, refs):
         for g, e in zip((*o, x[2], x[3]), ref):
             assert np.array_equal(g.cpu().numpy(), e)
+
+
+@pytest.mark.parametrize("page", [1, 2, 3, 7, 8, 9, 15, 16, 17, 24, 33, 255, 256, 257, 300, 1000])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_rows_that_begin_and_end_anywhere(page, seed):
+    """Slots are written by pieces of a page, or of 256 rows of a larger one: every beginning and end of a sequence's rows,
+    short ones among long ones, more rows than the slots hold and fewer."""
+    r = random.Random(100 * page + seed)
+    old = [r.choice([0, r.randint(0, 3 * page), r.randint(0, 700)]) for _ in range(90)]
+    new = [a + r.choice([0, 1, 2, 5, r.randint(0, 2 * page), r.randint(0, 900)]) for a in old]
+    rows = sum(max(0, b - a) for a, b in zip(old, new))
+    c = make(old, new, page=page, spare=4)
+    check(c, rows=rows // 2 + 1)
+    check(c, rows=rows + 300)
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 300])
+@pytest.mark.parametrize("share", [0.0, 0.3, 0.7, 0.99, 1.0])
+def test_scarce_pages_of_many_sequences(page, share):
+    r = random.Random(page)
+    old = [r.randint(0, 60) for _ in range(600)]
+    new = [r.choice([a, a + 1, a + r.randint(0, 400), r.randint(0, 60)]) for a in old]
+    c = make(old, new, page=page, spare=0)
+    c["state"][1] = int(c["state"][1] * share)
+    check(c)
