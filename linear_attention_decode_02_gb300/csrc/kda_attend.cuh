@@ -158,7 +158,8 @@ struct Place {
     return true;
   }
 };
-template <int THREADS, typename Part = Whole>
+// With EACH a block has a piece for every warp, c is the warp's own and ctas counts warps.
+template <int THREADS, typename Part = Whole, bool EACH = false>
 __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int c, int ctas) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place p;
@@ -176,8 +177,9 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
     return p;
   }
   __shared__ int64_t s_warp[THREADS / 32];
-  __shared__ int s_n;
-  __shared__ int64_t s_before;
+  constexpr int PIECES = EACH ? THREADS / 32 : 1;
+  __shared__ int s_n[PIECES];
+  __shared__ int64_t s_before[PIECES];
   const int per = (a.N + THREADS - 1) / THREADS;
   const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
   int64_t mine = 0;
@@ -197,22 +199,30 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
     if (w < warp) prior += s_warp[w];
     total += s_warp[w];
   }
-  if (!p.cut(total * units, c, ctas)) return p;  // the whole block
-  int64_t at = (prior + scan - mine) * units;    // tiles before sequence n0
-  if (n0 < n1 && p.start >= at && p.start < at + mine * units) {
-    Part again;
-    int n = n0;
-    for (; n < n1 - 1; ++n) {
-      const int64_t t = (int64_t)span_of(a, n, again.shared(a, n)).tiles * units;
-      if (p.start < at + t) break;
-      at += t;
+  if (!p.cut(total * units, c, ctas) && !EACH) return p;  // the whole block
+  const int64_t before = (prior + scan - mine) * units;   // tiles before sequence n0
+#pragma unroll
+  for (int w = 0; w < PIECES; ++w) {
+    Place q = p;
+    if (EACH && !q.cut(total * units, c - warp + w, ctas)) break;
+    if (n0 < n1 && q.start >= before && q.start < before + mine * units) {
+      int64_t at = before;
+      Part again;
+      int n = n0;
+      for (; n < n1 - 1; ++n) {
+        const int64_t t = (int64_t)span_of(a, n, again.shared(a, n)).tiles * units;
+        if (q.start < at + t) break;
+        at += t;
+      }
+      s_n[w] = n;
+      s_before[w] = at;
     }
-    s_n = n;
-    s_before = at;
   }
   __syncthreads();
-  p.n = s_n;
-  p.before = s_before;
+  if (p.start < p.stop) {
+    p.n = s_n[EACH ? warp : 0];
+    p.before = s_before[EACH ? warp : 0];
+  }
   return p;
 }
 

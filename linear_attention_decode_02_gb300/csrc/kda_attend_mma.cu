@@ -35,10 +35,13 @@
 // piece left the outputs as far from 64 bits and from a float32 computation as they
 // are, and took 256 channels from 150 to 168 us, 12 heads from 46 to 48.
 //
-// With PARTS sequences begin behind a prefix that they share, and each warp leaves
-// its own part of a unit to another kernel's join: 256 sequences of up to 600 such
-// positions, 0.32 GB, 74 us (64 % of the copy bandwidth; 94 us where a block's warps
-// joined theirs first).  What is left are the starts and ends of 2048 short units.
+// With PARTS sequences begin behind a prefix that they share, and results go as parts
+// to another kernel's join.  Up to 128 channels each warp has a piece of its own, so
+// that it ends a quarter of the units and leaves a quarter of the parts: 256 sequences
+// of up to 600 such positions, 0.32 GB, 71 us (67 % of the copy bandwidth), with the
+// join 83; 74 and 90 us where a block shared its units and each warp left its part, 94
+// where the block joined them first.  What is left are the starts and ends of 2048
+// short units.
 #include <type_traits>
 
 #include "kda_attend_rows.cuh"
@@ -60,9 +63,13 @@ struct Shape {
   static constexpr int CTAS = blocks_per_sm(D);
   static constexpr int STAGES = D == 64 ? 6 : 3;
   static constexpr bool QS = D == 256;  // no registers are left for the queries: they lie in shared memory
-  template <typename W>
-  using CopiesOver = PageCopies<__nv_bfloat16, D, kKeys, STAGES, kWarps, true, W>;
-  using Copies = CopiesOver<Walk>;
+  // Sequences' own positions are short units: a warp takes them alone, so that it ends a quarter of them.
+  static constexpr bool ALONE = own_warps_alone(D) > 1;
+  static_assert(ALONE != QS, "shared queries are the block's");
+  template <bool PARTS>
+  using CopiesOf = PageCopies<__nv_bfloat16, D, kKeys, STAGES, PARTS && ALONE ? 1 : kWarps, true,
+                              WalkOf<std::conditional_t<PARTS, Own, Whole>>>;
+  using Copies = CopiesOf<false>;
 };
 template <int D, int HG>
 constexpr int smem_bytes() {
@@ -95,7 +102,8 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 template <int D, int HG, bool PARTS>
 __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
   using Part = std::conditional_t<PARTS, Own, Whole>;
-  using Copies = typename Shape<D, HG>::template CopiesOver<WalkOf<Part>>;
+  using Copies = typename Shape<D, HG>::template CopiesOf<PARTS>;
+  constexpr bool ALONE = PARTS && Shape<D, HG>::ALONE;
   constexpr int STAGES = Shape<D, HG>::STAGES, ROW = Copies::ROW;
   constexpr int KSTEPS = D / 16, NT = D / 8;
   constexpr bool PAIR = HG == 8;  // rows 8..15 carry lo
@@ -106,12 +114,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int G = a.Hq / a.Hkv, groups = (G + HG - 1) / HG, units = a.Hkv * groups;
-  const int C = gridDim.x, c = blockIdx.x;
+  const int C = ALONE ? gridDim.x * kWarps : gridDim.x, c = ALONE ? blockIdx.x * kWarps + warp : blockIdx.x;
   // Parts go where the kernel before writes nothing, and nothing that it writes is read: that kernel has waited for all
   // before it when this one begins, and is waited for at the end.
   if (!PARTS) pdl_wait();
   pdl_launch_dependents();
-  const Place place = find_place<kThreads, Part>(a, units, c, C);
+  const Place place = find_place<kThreads, Part, ALONE>(a, units, c, C);
   const Workspace ws(a.work, C, HG, D);
   if (place.start == place.stop) {
     if (PARTS) pdl_wait();
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     __syncthreads();
   };
   load_q(walk);
-  Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, warp, lane);
+  Copies copies(a, place, s_notes[warp], smem + warp * Copies::RING, units, groups, ALONE ? 0 : warp, lane);
   // This lane's address for step k within keys, or values: offset[k % 4] + k / 4 * 128.
   uint32_t key_at[4], value_at[4], query_at[4];
   {
@@ -214,92 +222,96 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
     const int64_t stop = min(walk.unit_end, place.stop);
 #pragma unroll 1
     for (; walk.tile < stop; ++walk.tile) {
-      copy_wait<STAGES - 2>();
-      __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
-      const uint32_t live = s_notes[warp].live[stage];
-      copies.copy(stage == 0 ? STAGES - 1 : stage - 1);
-      const uint32_t base = copies.ring + stage * Copies::STAGE;
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
+#pragma unroll 1
+      for (int sub = 0; sub < Copies::SUBS; ++sub) {
+        copy_wait<STAGES - 2>();
+        __syncwarp();  // every lane's copies of this stage; and all are done with the stage copied to next
+        const uint32_t live = s_notes[warp].live[stage];
+        copies.copy(stage == 0 ? STAGES - 1 : stage - 1);
+        const uint32_t base = copies.ring + stage * Copies::STAGE;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        if (Copies::SUBS > 1 && live == 0) continue;
 
-      float s[2][2][4] = {};  // [even / odd step][positions 0..7 / 8..15]
-      {
+        float s[2][2][4] = {};  // [even / odd step][positions 0..7 / 8..15]
+        {
 #pragma unroll
-        for (int k = 0; k < KSTEPS; ++k) {
-          uint32_t b[4];
-          ldmatrix4(b, base + key_at[k % 4] + k / 4 * 128);
-          uint32_t x[4];
-          if constexpr (QS && PAIR) ldmatrix2(x[0], x[1], query_at[k % 4] + k / 4 * 128);
-          if constexpr (QS && !PAIR) ldmatrix4(x, query_at[k % 4] + k / 4 * 128);
-          if constexpr (!QS) {
+          for (int k = 0; k < KSTEPS; ++k) {
+            uint32_t b[4];
+            ldmatrix4(b, base + key_at[k % 4] + k / 4 * 128);
+            uint32_t x[4];
+            if constexpr (QS && PAIR) ldmatrix2(x[0], x[1], query_at[k % 4] + k / 4 * 128);
+            if constexpr (QS && !PAIR) ldmatrix4(x, query_at[k % 4] + k / 4 * 128);
+            if constexpr (!QS) {
 #pragma unroll
-            for (int i = 0; i < QN; ++i) x[i] = q[k][i];
+              for (int i = 0; i < QN; ++i) x[i] = q[k][i];
+            }
+            if constexpr (PAIR) {
+              mma(s[k & 1][0], x[0], 0u, x[1], 0u, b[0], b[1]);
+              mma(s[k & 1][1], x[0], 0u, x[1], 0u, b[2], b[3]);
+            } else {
+              mma(s[k & 1][0], x[0], x[1], x[2], x[3], b[0], b[1]);
+              mma(s[k & 1][1], x[0], x[1], x[2], x[3], b[2], b[3]);
+            }
           }
-          if constexpr (PAIR) {
-            mma(s[k & 1][0], x[0], 0u, x[1], 0u, b[0], b[1]);
-            mma(s[k & 1][1], x[0], 0u, x[1], 0u, b[2], b[3]);
-          } else {
-            mma(s[k & 1][0], x[0], x[1], x[2], x[3], b[0], b[1]);
-            mma(s[k & 1][1], x[0], x[1], x[2], x[3], b[2], b[3]);
+        }
+        float p[RS][4];  // this lane's positions 2 t4, + 1, + 8, + 9
+        bool rises = false;
+        float ref[RS], fall[RS];
+#pragma unroll
+        for (int r = 0; r < RS; ++r) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[r][j] = (s[0][j >> 1][2 * r + (j & 1)] + s[1][j >> 1][2 * r + (j & 1)]) * a.scale_log2;
+          if (live != 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!(live >> ((j >> 1) * 8 + 2 * t4 + (j & 1)) & 1)) p[r][j] = -INFINITY;
+          }
+          float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaxf(top, m[r]);
+          ref[r] = top == -INFINITY ? 0.f : top;
+          fall[r] = ex2(m[r] - ref[r]);
+          rises = rises || top > m[r];
+          m[r] = top;
+        }
+        if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+          for (int r = 0; r < RS; ++r) l[r] *= fall[r];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o[i][0] *= fall[0];
+            o[i][1] *= fall[0];
+            o[i][2] *= fall[RS - 1];
+            o[i][3] *= fall[RS - 1];
           }
         }
-      }
-      float p[RS][4];  // this lane's positions 2 t4, + 1, + 8, + 9
-      bool rises = false;
-      float ref[RS], fall[RS];
+        uint32_t hi[RS][2], lo[RS][2];
 #pragma unroll
-      for (int r = 0; r < RS; ++r) {
+        for (int r = 0; r < RS; ++r) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[r][j] = (s[0][j >> 1][2 * r + (j & 1)] + s[1][j >> 1][2 * r + (j & 1)]) * a.scale_log2;
-        if (live != 0xffffu) {
+          for (int j = 0; j < 4; ++j) p[r][j] = ex2(p[r][j] - ref[r]);
+          l[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!(live >> ((j >> 1) * 8 + 2 * t4 + (j & 1)) & 1)) p[r][j] = -INFINITY;
+          for (int j = 0; j < 2; ++j) {
+            hi[r][j] = pack_bf2(p[r][2 * j], p[r][2 * j + 1]);
+            lo[r][j] = pack_bf2(p[r][2 * j] - bf_lo(hi[r][j]), p[r][2 * j + 1] - bf_hi(hi[r][j]));
+          }
         }
-        float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = fmaxf(top, m[r]);
-        ref[r] = top == -INFINITY ? 0.f : top;
-        fall[r] = ex2(m[r] - ref[r]);
-        rises = rises || top > m[r];
-        m[r] = top;
-      }
-      if (__any_sync(0xffffffffu, rises)) {
+        {
 #pragma unroll
-        for (int r = 0; r < RS; ++r) l[r] *= fall[r];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= fall[0];
-          o[i][1] *= fall[0];
-          o[i][2] *= fall[RS - 1];
-          o[i][3] *= fall[RS - 1];
-        }
-      }
-      uint32_t hi[RS][2], lo[RS][2];
-#pragma unroll
-      for (int r = 0; r < RS; ++r) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[r][j] = ex2(p[r][j] - ref[r]);
-        l[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          hi[r][j] = pack_bf2(p[r][2 * j], p[r][2 * j + 1]);
-          lo[r][j] = pack_bf2(p[r][2 * j] - bf_lo(hi[r][j]), p[r][2 * j + 1] - bf_hi(hi[r][j]));
-        }
-      }
-      {
-#pragma unroll
-        for (int k = 0; k < KSTEPS; ++k) {
-          uint32_t b[4];
-          ldmatrix4_trans(b, base + value_at[k % 4] + k / 4 * 128);
-          if constexpr (PAIR) {
-            mma(o[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[0], b[1]);
-            mma(o[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2], b[3]);
-          } else {
-            mma(o[2 * k], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[0], b[1]);
-            mma(o[2 * k + 1], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[2], b[3]);
-            mma(o[2 * k], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[0], b[1]);
-            mma(o[2 * k + 1], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[2], b[3]);
+          for (int k = 0; k < KSTEPS; ++k) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, base + value_at[k % 4] + k / 4 * 128);
+            if constexpr (PAIR) {
+              mma(o[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[0], b[1]);
+              mma(o[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2], b[3]);
+            } else {
+              mma(o[2 * k], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[0], b[1]);
+              mma(o[2 * k + 1], hi[0][0], hi[RS - 1][0], hi[0][1], hi[RS - 1][1], b[2], b[3]);
+              mma(o[2 * k], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[0], b[1]);
+              mma(o[2 * k + 1], lo[0][0], lo[RS - 1][0], lo[0][1], lo[RS - 1][1], b[2], b[3]);
+            }
           }
         }
       }
@@ -307,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
 
     if constexpr (PARTS) {
       const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG;
-      leave_parts<D, HG, kWarps, RS>(a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; },
-                                     min(HG, G - g0), o, m, l, warp, g, t4, c);
+      leave_parts<D, HG, ALONE ? 1 : kWarps, RS>(
+          a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; }, min(HG, G - g0), o, m, l,
+          ALONE ? 0 : warp, g, t4, c, C);
     } else {
       finish_unit<D, HG, kWarps, RS>(a, walk, place, ws, reinterpret_cast<float*>(smem + kWarps * Copies::RING),
                                      s_m[parity], s_l[parity], o, m, l, groups, warp, g, t4, c);

@@ -107,13 +107,13 @@ __device__ __forceinline__ void finish_unit(const AttendArgs& a, const Walk& wal
 }
 
 // Leaves each warp's own part of a unit, and goes on, where another kernel joins
-// all parts: sequences' own positions are often few, and for the block to meet at the
+// all parts: sequences' own positions are often few, and for a block to meet at the
 // end of each took as long as 150 of them.  head_of(h) is row h's place among the
-// N * Hq, below 0 for rows that take no part; the other arguments as of finish_unit.
+// N * Hq, below 0 for rows that take no part; c of `most` pieces, WARPS warps each; the other arguments as of finish_unit.
 template <int D, int HG, int WARPS, int RS, typename W, typename HeadOf>
 __device__ __forceinline__ void leave_parts(const AttendArgs& a, const W& walk, const Place& place, const HeadOf& head_of,
                                             int rows, float (&o)[D / 8][4], float (&m)[RS], float (&l)[RS], int warp, int g,
-                                            int t4, int c) {
+                                            int t4, int c, int most) {
   constexpr bool PAIR = HG == 8;
   const bool first = walk.unit_start >= place.start;
 #pragma unroll
@@ -136,7 +136,7 @@ __device__ __forceinline__ void leave_parts(const AttendArgs& a, const W& walk, 
     if (t4 == 0) {
       (first ? a.parts.first_ml : a.parts.more_ml)[at] = make_float2(m[r], l[r]);
       if (first && warp == 0) {
-        const int pieces = pieces_of(place.T, gridDim.x);
+        const int pieces = pieces_of(place.T, most);
         a.parts.first_note[head] = part_note(c, (int)piece_of(walk.unit_end - 1, place.T, pieces) - c, h);
       }
     }

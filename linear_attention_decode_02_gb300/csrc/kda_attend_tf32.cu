@@ -342,11 +342,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
             const int2 at = walk.row(a, h);
             return takes_part(a, at.x, walk.of.prefix) ? (int64_t)at.x * a.Hq + at.y : -1;
           },
-          rows_of(walk), o, m, l, warp, g, t4, c);
+          rows_of(walk), o, m, l, warp, g, t4, c, C);
     } else if constexpr (OWN) {
       const int hk = walk.group / groups, g0 = (walk.group - hk * groups) * HG;
       leave_parts<D, HG, WARPS, RS>(a, walk, place, [&](int h) { return (int64_t)walk.n * a.Hq + hk * G + g0 + h; },
-                                    min(HG, G - g0), o, m, l, warp, g, t4, c);
+                                    min(HG, G - g0), o, m, l, warp, g, t4, c, C);
     } else {
       finish_unit<D, HG, WARPS, RS>(a, walk, place, ws, reinterpret_cast<float*>(tail), s_m[parity], s_l[parity], o, m, l,
                                     groups, warp, g, t4, c);

@@ -112,6 +112,8 @@ struct AttendArgs {
   Parts parts;
 };
 constexpr int kAttendWarps = 4;  // of a block of the tensor-core kernel
+// Of these, those that take a piece of sequences' own positions under a shared prefix each; else the block takes one.
+constexpr int own_warps_alone(int D) { return D < 256 ? kAttendWarps : 1; }
 
 // Grid and workspace of the attention kernels: `ctas` workers that each may
 // leave two partial results of `heads` query heads.

@@ -724,7 +724,8 @@ PrefixPlan prefix_plan(float* work, int64_t N, int32_t Hq, int32_t Hkv, int32_t 
     p.own = attend_mma_plan(G, D, sms);
     p.pre.ctas = sms;
     p.pre.heads = D < 256 && rows > kRows ? 2 * kRows : kRows;
-    p.own_parts = parts(p.own.ctas, kAttendWarps, p.own.heads, p.own.heads);
+    const int alone = own_warps_alone(D);
+    p.own_parts = parts(p.own.ctas * alone, kAttendWarps / alone, p.own.heads, p.own.heads);
     p.pre_parts = parts(p.pre.ctas, 1, p.pre.heads, 2 * kRows);
   }
   p.floats = at;
