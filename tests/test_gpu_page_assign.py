@@ -252,3 +252,11 @@ def test_scarce_pages_of_many_sequences(page, share):
     c = make(old, new, page=page, spare=0)
     c["state"][1] = int(c["state"][1] * share)
     check(c)
+
+
+@pytest.mark.parametrize("old, new", [
+    ([1990000000, 0], [1990000700, 5]), ([7, 1990000000 - 300], [9, 1990000000 + 2 ** 20]), ([1989148671, 3], [1989148673, 0]),
+])
+def test_positions_near_two_to_the_31(old, new):
+    c = make(old, new, page=2 ** 20, spare=2)
+    check(c, rows=1200)
