@@ -774,16 +774,16 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms
 // what it could save at the table's width (the host knows no lengths): below, every
 // sequence is on its own.  Measured shared and alone, us (groups x sequences x common
 // positions, 64 own ones; the bytes that sharing saves):
-//   32 / 8 heads of 128   1 x 2 x 1024 (4 MB) 18 and 10, 1 x 16 x 1024 (63 MB) 22 and 19, 16 x 4 x 256 (50 MB) 28 and 23,
-//                         4 x 16 x 256 (63 MB) 26 and 23, 1 x 16 x 4032 (248 MB) 25 and 42, 16 x 4 x 1024 (201 MB) 38 and 47
-//   64 channels           1 x 4 x 16000 (98 MB) 26 and 27, 16 x 4 x 1024 (101 MB) 29 and 31, 4 x 2 x 16000 (131 MB) 52 and 46
-//   256 channels          1 x 4 x 4032 (99 MB) 25 and 34, 12 / 1 heads 1 x 16 x 16000 (246 MB) 48 and 66, 4 x 16 x 1024 (63 MB) 32 and 28
+//   32 / 8 heads of 128   1 x 2 x 1024 (4 MB) 16 and 10, 1 x 16 x 1024 (63 MB) 19 and 19, 16 x 4 x 256 (50 MB) 28 and 23,
+//                         4 x 16 x 256 (63 MB) 19 and 23, 1 x 16 x 4032 (248 MB) 29 and 42, 16 x 4 x 1024 (201 MB) 41 and 47
+//   64 channels           1 x 4 x 16000 (98 MB) 27 and 27, 16 x 4 x 1024 (101 MB) 32 and 31, 4 x 2 x 16000 (131 MB) 61 and 46
+//   256 channels          1 x 4 x 4032 (99 MB) 23 and 34, 12 / 1 heads 1 x 16 x 16000 (246 MB) 38 and 65, 4 x 16 x 1024 (63 MB) 28 and 28
 constexpr int64_t kSharedBytes = 96 << 20;
 // Float32 works on its rows as long as on its bytes: with more query heads a key
 // head, or 256 channels, the sequences alone already do, and sharing saves little.
-//   32 / 8 heads of 64    4 x 16 x 1024 (252 MB) 46 and 55, 16 x 2 x 4032 (264 MB) 78 and 92, 16 x 16 x 256 (252 MB) 88 and 71
-//   32 / 8 of 128         4 x 6 x 1024 (168 MB) 43 and 41, 1 x 16 x 4032 (496 MB) 57 and 87, 16 x 2 x 1024 (134 MB) 50 and 55
-//   16 / 16 of 128        1 x 6 x 4032 (330 MB) 44 and 53, 4 x 16 x 256 (252 MB) 49 and 52, 16 x 6 x 256 (168 MB) 68 and 75
+//   32 / 8 heads of 64    4 x 16 x 1024 (252 MB) 46 and 55, 16 x 2 x 4032 (264 MB) 78 and 93, 16 x 16 x 256 (252 MB) 86 and 71
+//   32 / 8 of 128         4 x 6 x 1024 (168 MB) 43 and 40, 1 x 16 x 4032 (496 MB) 56 and 83, 16 x 2 x 1024 (134 MB) 50 and 53
+//   16 / 16 of 128        1 x 6 x 4032 (330 MB) 43 and 53, 4 x 16 x 256 (252 MB) 49 and 51, 16 x 6 x 256 (336 MB) 66 and 74
 //   32 / 2 of 128         4 x 16 x 4032 (496 MB) 137 and 126, 16 x 16 x 1024 (503 MB) 183 and 145
 //   256 channels          32 / 8 4 x 6 x 1024 (336 MB) 94 and 79, 16 / 16 16 x 2 x 1024 (537 MB) 216 and 165
 constexpr int64_t kSharedBytesF32 = 256 << 20;
