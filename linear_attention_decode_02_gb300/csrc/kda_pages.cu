@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(kMostThreads) kda_page_assign_kernel(const __g
   // Lanes that write a piece together.
   const int share = piece <= 8 ? 8 : (piece <= 16 ? 16 : 32), x0 = lane & (share - 1);
   for (int64_t i0 = 32LL * ((tid >> 5) * ctas + rank); i0 < pieces; i0 += 32LL * warps * ctas) {
-    int row = 0, len = 0, left = 0;   // the piece's first row, its rows, those on its first page
-    int first = -1, second = -1;  // slots of its first place and of the next page's
+    int row = 0, len = 0, left = 0;  // the piece's first row, its rows, those on its first page
+    int first = -1, second = -1;     // slots of its first place and of the next page's
     if (i0 + lane < pieces) {
       const int n = owner_of(s_piece, N, (int)i0 + lane), old = s_old[n], held = pages_of(old);
       const int64_t start = piece0(old) + (int64_t)((int)i0 + lane - s_piece[n]) * piece;

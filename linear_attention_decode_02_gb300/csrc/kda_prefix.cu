@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
 template <int D, int WARPS>
 __global__ void __launch_bounds__(128) kda_prefix_join_kernel(const __grid_constant__ AttendArgs a, const Parts pre,
                                                               const Parts own) {
-    // parts read at once: 34 parts of 64 channels (7 groups of 20, 12 heads) 37 -> 32 us a call for eight, 128 channels 97 -> 98
+  // Parts read at once: 34 parts of 64 channels (7 groups of 20, 12 heads) 37 -> 32 us a call for eight, 128 channels 97 -> 98
   constexpr int VEC = D / 32, AHEAD = D == 64 ? 8 : 4;
   __shared__ float s_m[4], s_l[4], s_o[WARPS > 1 ? 4 : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
