@@ -89,6 +89,7 @@ struct Span {
   int first, end, tile0, tiles;
 };
 // `skip`: positions at the beginning that are left out.
+template <int TILE = kTile>
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int n, int skip = 0) {
   const int64_t cap = (int64_t)a.table_cols * a.page_size;
   const int len = __ldg(a.lens + n);
@@ -97,8 +98,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int n, int skip = 0
   s.first = a.window > 0 && len > a.window ? len - a.window : 0;
   if (skip > 0) s.first = max(s.first, skip);
   if (s.first >= s.end) s.first = s.end = 0;
-  s.tile0 = s.first / kTile;
-  s.tiles = s.end == 0 ? 1 : (s.end - 1) / kTile - s.tile0 + 1;
+  s.tile0 = s.first / TILE;
+  s.tiles = s.end == 0 ? 1 : (s.end - 1) / TILE - s.tile0 + 1;
   return s;
 }
 
@@ -109,11 +110,15 @@ __device__ __forceinline__ bool takes_part(const AttendArgs& a, int n, int prefi
   return prefix > 0 && min((int64_t)max(len, 0), cap) >= prefix && (a.window == 0 || len <= a.window);
 }
 
-// Positions that a sequence leaves to its group's kernel, for sequences that go by in order: none, or found by their groups.
+// Positions that a sequence leaves to its group's kernel, for sequences that go by in order: none, or found by their groups;
+// and positions of a tile.
 struct Whole {
+  static constexpr int TILE = kTile;
   __device__ __forceinline__ int shared(const AttendArgs&, int) { return 0; }
 };
+template <int T>
 struct Own {
+  static constexpr int TILE = T;
   int end = 0, prefix = 0;  // the sequences before `end` that are left have `prefix` positions in common
   __device__ __forceinline__ int shared(const AttendArgs& a, int n) {
     if (n >= end) {
@@ -164,7 +169,7 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place p;
   if (a.N <= 32) {  // a sequence a lane, every warp alone
-    const int64_t mine = lane < a.N ? (int64_t)span_of(a, lane, Part().shared(a, lane)).tiles * units : 0;
+    const int64_t mine = lane < a.N ? (int64_t)span_of<Part::TILE>(a, lane, Part().shared(a, lane)).tiles * units : 0;
     int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +189,7 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
   const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
   int64_t mine = 0;
   Part part;
-  for (int n = n0; n < n1; ++n) mine += span_of(a, n, part.shared(a, n)).tiles;
+  for (int n = n0; n < n1; ++n) mine += span_of<Part::TILE>(a, n, part.shared(a, n)).tiles;
   int64_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -210,7 +215,7 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, int units, int 
       Part again;
       int n = n0;
       for (; n < n1 - 1; ++n) {
-        const int64_t t = (int64_t)span_of(a, n, again.shared(a, n)).tiles * units;
+        const int64_t t = (int64_t)span_of<Part::TILE>(a, n, again.shared(a, n)).tiles * units;
         if (q.start < at + t) break;
         at += t;
       }
@@ -264,6 +269,7 @@ __device__ __forceinline__ void leave_empty_parts(const AttendArgs& a, int w, in
 // Where a walk over the tiles of groups' units stands; the key head's row tiles lie together.
 template <int KT, int ROWS>
 struct GroupWalk {
+  static constexpr int TILE = KT;
   int64_t tile, unit_start, unit_end;
   int g, n, group, row_tile;  // n: the sequence whose pages are read; group: the key head
   Span sp;
@@ -361,6 +367,7 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // Where a walk over the piece's tiles stands.
 template <typename Part>
 struct WalkOf {
+  static constexpr int TILE = Part::TILE;
   int64_t tile, unit_start, unit_end;
   int n, group;
   Span sp;
@@ -368,7 +375,7 @@ struct WalkOf {
   __device__ __forceinline__ void start(const AttendArgs& a, const Place& p) {
     tile = p.start;
     n = p.n;
-    sp = span_of(a, n, part.shared(a, n));
+    sp = span_of<TILE>(a, n, part.shared(a, n));
     group = (int)quotient(tile - p.before, sp.tiles);
     unit_start = p.before + (int64_t)group * sp.tiles;
     unit_end = unit_start + sp.tiles;
@@ -377,7 +384,7 @@ struct WalkOf {
     unit_start = unit_end;
     if (++group == units) {
       group = 0;
-      if (++n < a.N) sp = span_of(a, n, part.shared(a, n));
+      if (++n < a.N) sp = span_of<TILE>(a, n, part.shared(a, n));
     }
     unit_end = unit_start + sp.tiles;
   }
@@ -412,7 +419,7 @@ __device__ __forceinline__ void copy_wait() {
 // become zeros.  SWIZZLE puts 16-byte chunk c of row r at c ^ (r & 7).
 template <typename T, int D, int KEYS, int STAGES, int WARPS, bool SWIZZLE, typename W = Walk>
 struct PageCopies {
-  static constexpr int SUBS = kTile / WARPS / KEYS;
+  static constexpr int SUBS = W::TILE / WARPS / KEYS;
   static constexpr int ROW = D * (int)sizeof(T);
   static constexpr int TENSOR = KEYS * ROW;
   static constexpr int STAGE = 2 * TENSOR;
@@ -420,7 +427,7 @@ struct PageCopies {
   static constexpr int CHUNKS = ROW / 16;
   // One pass of the warp copies 32 chunks: part of a row, or PASS_ROWS rows.
   static constexpr int PASSES = KEYS * CHUNKS / 32;
-  static_assert(SUBS >= 1 && SUBS * KEYS * WARPS == kTile && 2 * KEYS <= 32 && PASSES * 32 == KEYS * CHUNKS, "bad shape");
+  static_assert(SUBS >= 1 && SUBS * KEYS * WARPS == W::TILE && 2 * KEYS <= 32 && PASSES * 32 == KEYS * CHUNKS, "bad shape");
   struct Notes {
     const char* row[2 * KEYS];  // keys, then values; of a position not attended to: the first page
     uint32_t live[STAGES];
@@ -457,7 +464,7 @@ struct PageCopies {
     Look l{0, 0, -1};
     if (at.tile < place.stop) {
       l.head = groups == 1 ? at.group : at.group / groups;
-      const int t = (at.sp.tile0 + (int)(at.tile - at.unit_start)) * kTile + (warp * SUBS + sub) * KEYS + lane % KEYS;
+      const int t = (at.sp.tile0 + (int)(at.tile - at.unit_start)) * W::TILE + (warp * SUBS + sub) * KEYS + lane % KEYS;
       if (lane < 2 * KEYS && t >= at.sp.first && t < at.sp.end) {
         const int col = t / a.page_size;
         l.token = t - col * a.page_size;

@@ -38,8 +38,8 @@
 // With PARTS sequences begin behind a prefix that they share, and results go as parts
 // to another kernel's join.  Up to 128 channels each warp has a piece of its own, so
 // that it ends a quarter of the units and leaves a quarter of the parts: 256 sequences
-// of up to 600 such positions, 0.32 GB, 71 us (67 % of the copy bandwidth), with the
-// join 83; 74 and 90 us where a block shared its units and each warp left its part, 94
+// of up to 600 such positions, 0.32 GB, 65 us (73 % of the copy bandwidth), with the
+// join 77; 74 and 90 us where a block shared its units and each warp left its part, 94
 // where the block joined them first.  What is left are the starts and ends of 2048
 // short units.
 #include <type_traits>
@@ -66,9 +66,14 @@ struct Shape {
   // Sequences' own positions are short units: a warp takes them alone, so that it ends a quarter of them.
   static constexpr bool ALONE = own_warps_alone(D) > 1;
   static_assert(ALONE != QS, "shared queries are the block's");
+  // A lone warp's pieces are cut between stages, where 16 x 4 sequences of up to 300 positions take 16.5 us, by tiles of 64
+  // positions 20; but with 64 channels, whose rings hold a tile, by tiles: 7 x 20 of up to 500 31 us a call, with its join of
+  // fewer parts, 33 between stages.
+  static constexpr int CUT = ALONE && D == 128 ? kKeys : kTile;
   template <bool PARTS>
-  using CopiesOf = PageCopies<__nv_bfloat16, D, kKeys, STAGES, PARTS && ALONE ? 1 : kWarps, true,
-                              WalkOf<std::conditional_t<PARTS, Own, Whole>>>;
+  using PartOf = std::conditional_t<PARTS, Own<CUT>, Whole>;
+  template <bool PARTS>
+  using CopiesOf = PageCopies<__nv_bfloat16, D, kKeys, STAGES, PARTS && ALONE ? 1 : kWarps, true, WalkOf<PartOf<PARTS>>>;
   using Copies = CopiesOf<false>;
 };
 template <int D, int HG>
@@ -101,7 +106,7 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 template <int D, int HG, bool PARTS>
 __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_kernel(const __grid_constant__ AttendArgs a) {
-  using Part = std::conditional_t<PARTS, Own, Whole>;
+  using Part = typename Shape<D, HG>::template PartOf<PARTS>;
   using Copies = typename Shape<D, HG>::template CopiesOf<PARTS>;
   constexpr bool ALONE = PARTS && Shape<D, HG>::ALONE;
   constexpr int STAGES = Shape<D, HG>::STAGES, ROW = Copies::ROW;

@@ -101,7 +101,7 @@ template <int D, int HG, Over OVER>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(const __grid_constant__ AttendArgs a) {
   constexpr bool GROUPS = OVER == Over::kGroups;
   constexpr bool OWN = OVER == Over::kOwn;
-  using Part = std::conditional_t<OWN, Own, Whole>;
+  using Part = std::conditional_t<OWN, Own<kTile>, Whole>;
   using W = std::conditional_t<GROUPS, GroupWalk<kTile, HG>, WalkOf<Part>>;
   using Copies = typename Shape<D>::template CopiesOver<W>;
   constexpr int WARPS = Shape<D>::WARPS, THREADS = Shape<D>::THREADS, STAGES = Shape<D>::STAGES, ROW = Copies::ROW;
