@@ -429,6 +429,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         if (run && i < steps) run = scores(i);
         if (!first && run && i > 0) run = output(i - 1, behind);
       }
+      // A lane without a tile of the unit waits for its queries all the same: it would run ahead, and its arrivals for this
+      // unit and the next in the slot would pass for both lanes' of one.
+      if (steps == 0 && run) run = wait_or_abort(&q_full[q_slot], (unit / P::QSLOTS) & 1);
       if (!run) break;
       release(&q_empty[uniform(q_slot)]);
       half += 2 * count;

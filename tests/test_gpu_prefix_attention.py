@@ -2,6 +2,8 @@
 pages: group sizes and shapes, prefixes from nothing to many tiles, ends inside pages and tiles, sequences that take no
 part, windows, null pages, garbage in every place that is not attended to, layouts, and repeated use."""
 
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -438,3 +440,20 @@ def test_inputs_written_just_before_the_call(dtype):
     for i, got in enumerate(out):
         for a, b in zip(got, wanted[i % 4 if i < 24 else (i * 7 // 3) % 4]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("most", [60, 130, 300])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_units_of_few_tiles_a_block(D, most):
+    """More units than a block's slots of queries, of one tile, or one and two, or up to five: where one of two lanes that
+    take tiles in turn has none, the other's queries stay where they are."""
+    r = random.Random(most + D)
+    groups = [(r.randint(1, most), [r.randint(1, 20) for _ in range(r.randint(2, 4))]) for _ in range(56)]
+    check(make(groups, Hq=16, Hkv=16, D=D))
+
+
+@pytest.mark.parametrize("window", [0, 101])
+def test_many_groups_of_short_prefixes(window):
+    r = random.Random(window)
+    groups = [(r.choice([48, 64, 79]), [r.randint(1, 42) for _ in range(r.randint(4, 8))]) for _ in range(35)]
+    check(make(groups, Hq=16, Hkv=16, D=128), window=window)
