@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, HG>::CTAS) kda_attend_mma_k
   };
   char* shared_q = smem + kWarps * Copies::RING + (kWarps - 1) * 8 * D * 4;
   const auto place_q = [&]() {
+    if (PARTS) __syncthreads();  // no unit's end held the warps together: all are done with the last one's queries
 #pragma unroll
     for (int i = 0; i < SHARE; ++i) {
       const int row = (i * kThreads + threadIdx.x) / (D / 8), chunk = (i * kThreads + threadIdx.x) % (D / 8);

@@ -457,3 +457,15 @@ def test_many_groups_of_short_prefixes(window):
     r = random.Random(window)
     groups = [(r.choice([48, 64, 79]), [r.randint(1, 42) for _ in range(r.randint(4, 8))]) for _ in range(35)]
     check(make(groups, Hq=16, Hkv=16, D=128), window=window)
+
+
+@pytest.mark.parametrize("Hq, Hkv", [(4, 1), (24, 8), (16, 16)])
+def test_many_short_units_of_256_channels(Hq, Hkv):
+    """Own positions of 256 channels are worked on by blocks whose warps share queries and do not meet at a unit's end."""
+    r = random.Random(Hq)
+    groups = [(r.choice([1, 64, 100]), [r.randint(1, 150) for _ in range(r.randint(2, 12))]) for _ in range(60)]
+    c = make(groups, Hq=Hq, Hkv=Hkv, D=256)
+    out, lse = check(c)
+    for _ in range(20):
+        again, sums = run(c)
+        assert same(again, out) and same(sums, lse)
