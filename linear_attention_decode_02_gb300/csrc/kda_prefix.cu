@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         const bool first = P::SPLIT && i % P::STEPS == 0;
         if (first && i > 0) run = output(i - 1, threads);
         if (run && i < steps) run = scores(i);
-        if (!first && run && i > 0) run = output(i - 1, behind);
+        if (!first && run && i > 0) run = output(i - 1, i < steps ? behind : threads);
       }
       // A lane without a tile of the unit waits for its queries all the same: it would run ahead, and its arrivals for this
       // unit and the next in the slot would pass for both lanes' of one.

@@ -469,3 +469,10 @@ def test_many_short_units_of_256_channels(Hq, Hkv):
     for _ in range(20):
         again, sums = run(c)
         assert same(again, out) and same(sums, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_last_tile_alone_is_copied_by_threads(D):
+    """Whole pages of 64 come in boxes; a prefix that ends inside a page has its last tile from threads."""
+    groups = [(64 * k + e, [5, 9]) for k in (1, 2, 3, 7) for e in (1, 17, 40, 63)]
+    check(make(groups, Hq=16, Hkv=16, D=D, page=64))
