@@ -37,7 +37,11 @@
 //
 // A barrier's parity tells two phases apart, so each is waited for, or known to be
 // over, before the next: S of a buffer is issued behind the product of the weights
-// that were in it, so a second phase of that product cannot pass unseen.
+// that were in it, so a second phase of that product cannot pass unseen.  Lanes that
+// take tiles in turn do not wait for each other's halves of the ring: a tile's mask is
+// given when what was in both its slots has been used, and a lane waits for the mask
+// before it waits for either half (given with the keys' slot, the values' barrier could
+// still be in the phase before the last one, which looks like the one waited for).
 //
 // What bounds it, at 32 / 8 heads of 128 (each of the three launches under a profiler,
 // in us):
@@ -516,9 +520,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
         } else if (lane == 0) {  // two warps a word
           reinterpret_cast<uint16_t*>(s_live[tile % kLiveDepth])[lw] = (uint16_t)mask;
         }
-        if (lane == 0) mbar_arrive(&live_full[tile % kLiveDepth]);
         copy_half(a.kp, &k_map, look, mask);
         if (half >= SLOTS && !wait_or_abort(&empty[half % SLOTS], (half / SLOTS - 1) & 1)) { run = false; break; }
+        if (lane == 0) mbar_arrive(&live_full[tile % kLiveDepth]);  // both halves' slots are free
         copy_half(a.vp, &v_map, look, mask);
         look = next;
       }
