@@ -35,9 +35,13 @@
 // where that has passed it by 2^kSlack, so O, which lies in tensor memory, is seldom
 // rescaled.
 //
+// Products of one accumulator and shape complete in the order in which they are issued;
+// for others PTX promises none.  So scores that go where weights were wait for the
+// product that read those.
+//
 // A barrier's parity tells two phases apart, so each is waited for, or known to be
-// over, before the next: S of a buffer is issued behind the product of the weights
-// that were in it, so a second phase of that product cannot pass unseen.  Lanes that
+// over, before the next: the scores of a buffer wait for every product of the weights
+// that were in it, so no second phase of that product passes unseen.  Lanes that
 // take tiles in turn do not wait for each other's halves of the ring: a tile's mask is
 // given when what was in both its slots has been used, and a lane waits for the mask
 // before it waits for either half (given with the keys' slot, the values' barrier could
@@ -396,8 +400,9 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
           for (int k = 0; k < KT / 32; ++k) threads = threads || s_live[at_mask][k] != 0xffffffffu;
           if (!slot_wait(hk, threads || i == 0)) return false;  // the queries are always copied by threads
         }
+        const int g = job + i, b = uniform(2 * me + (g & 1));
+        if (g >= 2 && !wait_or_abort(&o_done[b], ((g >> 1) - 1) & 1)) return false;  // has read the weights that were in S
         tc::fence_after_sync();
-        const int b = uniform(2 * me + ((job + i) & 1));
         const uint64_t q = tc::desc_sw128(q_addr + uniform(q_slot * RT + row_tile) * P::Q_TILE, 16, 1024);
         const uint64_t k = tc::desc_sw128(ring + uniform(hk % SLOTS) * P::HALF + uniform(sub) * (kStep * 128), 16, 1024);
 #pragma unroll

@@ -1,6 +1,7 @@
 """A model of the barriers of the shared-prefix attention kernel: its roles step in random order, copies land in random
-order, and every read is checked to find what it is meant to find.  The order in which the copying warps take their steps
-is read from the kernel's source."""
+order, matrix products of different shapes complete in random order, and every read is checked to find what it is meant
+to find.  The order in which the copying warps take their steps, and whether scores wait for the weights in their place
+to be done with, is read from the kernel's source."""
 
 import os
 import random
@@ -26,6 +27,10 @@ def copy_steps():
     return [names[n] for n in found]
 
 
+def scores_wait():
+    return "wait_or_abort(&o_done" in section("const auto scores", "const auto output")
+
+
 class Barrier:
     """As an mbarrier: `count` arrivals end a phase; a wait for a parity passes when the current phase has the other one."""
 
@@ -44,18 +49,23 @@ class Barrier:
 
 
 class Pipe:
-    """A lane's tensor operations, in order; a commit's arrival follows all before it."""
+    """A lane's tensor operations: those of one kind complete in order; a commit's arrival follows all before it."""
 
     def __init__(self):
         self.queue = []
 
     def step(self, rng):
-        if self.queue:
-            self.queue.pop(0)[1]()
+        kinds = [kind for kind, _ in self.queue]
+        first = {kind: kinds.index(kind) for kind in kinds}
+        if first.get("commit") != 0:
+            first.pop("commit", None)
+        if first:
+            self.queue.pop(rng.choice(list(first.values())))[1]()
 
 
 class Model:
-    def __init__(self, counts, seed, RT, LANES, STEPS, SLOTS, QSLOTS, steps):
+    def __init__(self, counts, seed, RT, LANES, STEPS, SLOTS, QSLOTS, steps, wait):
+        self.scores_wait = wait
         self.rng, self.counts, self.shape, self.loader_steps = random.Random(seed), counts, (RT, LANES, STEPS, SLOTS, QSLOTS), steps
         self.split = RT < LANES
         bars = lambda n, count: [Barrier(count) for _ in range(n)]  # noqa: E731
@@ -133,6 +143,8 @@ class Model:
                 yield from self.wait(self.live[(tile + j) % 16], (tile + j) // 16)
                 self.need(self.mask[(tile + j) % 16], tile + j, "mask")
                 yield from self.wait(self.full[h % SLOTS], h // SLOTS)
+            if self.scores_wait and job + i >= 2:
+                yield from self.wait(self.o_done[b], (job + i) // 2 - 1)
 
             def run():
                 self.need(self.Q[q], unit, "queries")
@@ -247,14 +259,14 @@ SHAPES = {"one row tile": (1, 2, 2, 5, 2), "one row tile, 64 channels": (1, 2, 2
           "two row tiles, 64 channels": (2, 2, 2, 12, 1), "256 channels": (1, 1, 1, 5, 1)}
 
 
-def sweep(name, steps, runs=150):
+def sweep(name, steps, wait, runs=150):
     found = []
     for seed in range(runs):
         rng = random.Random(seed * 7 + 1)
         counts = [rng.choice([1, 1, 2, 3, 3, 5, rng.randint(1, 9)]) for _ in range(rng.randint(1, 9))]
         if seed % 5 == 0:
             counts = [1] * rng.randint(1, 9)
-        found += [(counts, w) for w in Model(counts, seed, *SHAPES[name], steps).run()[:1]]
+        found += [(counts, w) for w in Model(counts, seed, *SHAPES[name], steps, wait).run()[:1]]
     return found
 
 
@@ -264,9 +276,15 @@ def test_the_source_has_the_steps_of_the_model():
 
 @pytest.mark.parametrize("name", SHAPES)
 def test_every_read_finds_what_it_waits_for(name):
-    assert sweep(name, copy_steps()) == []
+    assert sweep(name, copy_steps(), scores_wait()) == []
 
 
 def test_a_mask_given_before_the_values_have_room_is_noticed():
-    found = sweep("one row tile", ["room", "mask", "keys", "room", "values"], 400)
+    found = sweep("one row tile", ["room", "mask", "keys", "room", "values"], True, 400)
     assert any("values" in w for _, w in found)
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_scores_that_go_where_weights_are_still_read_are_noticed(name):
+    found = sweep(name, copy_steps(), False)
+    assert any("weights" in w for _, w in found)
