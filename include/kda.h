@@ -485,7 +485,8 @@ kda_status kda_rope_pair_axes(const int32_t* sections, int32_t num_axes, int32_t
  * within that factor of the largest float may overflow.  A sequence shorter than its
  * group's prefix, or whose window leaves part of it out, is on its own too.  So is
  * every sequence where vectors are off 16-byte boundaries, and where the keys and values
- * that sharing could save, (N - G) * P * page_size positions, come to less than 96 MB;
+ * that sharing could save, those of (N - G) * min(P * page_size, window) positions (no
+ * window: P * page_size), come to less than 96 MB;
  * in float32 256 MB, and with more than four query heads a key head or 256 channels.
  */
 kda_status kda_prefix_attention_decode(const kda_tensor* q, const kda_tensor* k_pages, const kda_tensor* v_pages,

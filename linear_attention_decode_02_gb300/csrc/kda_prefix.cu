@@ -784,11 +784,13 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms
 }
 
 // Bytes of keys and values from which sharing is worth its two launches more, by
-// what it could save at the table's width (the host knows no lengths): below, every
-// sequence is on its own.  Measured shared and alone, us (groups x sequences x common
+// what it could save at the table's width, or the window's (the host knows no lengths;
+// a sequence that shares is no longer than the window): below, every sequence is on its own.  Measured shared and alone, us (groups x sequences x common
 // positions, 64 own ones; the bytes that sharing saves):
 //   32 / 8 heads of 128   1 x 2 x 1024 (4 MB) 16 and 10, 1 x 16 x 1024 (63 MB) 19 and 19, 16 x 4 x 256 (50 MB) 28 and 23,
 //                         4 x 16 x 256 (63 MB) 19 and 23, 1 x 16 x 4032 (248 MB) 29 and 42, 16 x 4 x 1024 (201 MB) 41 and 47
+//     windows: 4 x 2 x 1024 under 512 (17 MB) 28 and 11; 1 x 64 x 4096 + up to 300 under 8192 (all share) 44 and 141, under
+//     4200 (a third do; 1 GB) 132 and 140; 16 x 4 x 1024 + up to 300 under 1200 (half do; 236 MB) 65 and 50
 //   64 channels           1 x 4 x 16000 (98 MB) 27 and 27, 16 x 4 x 1024 (101 MB) 32 and 31, 4 x 2 x 16000 (131 MB) 61 and 46
 //   256 channels          1 x 4 x 4032 (99 MB) 23 and 34, 12 / 1 heads 1 x 16 x 16000 (246 MB) 38 and 65, 4 x 16 x 1024 (63 MB) 28 and 28
 constexpr int64_t kSharedBytes = 96 << 20;
@@ -803,7 +805,9 @@ constexpr int64_t kSharedBytesF32 = 256 << 20;
 constexpr int kSharedHeadsF32 = 4;
 
 bool shares(const AttendArgs& a) {
-  const double positions = (a.N - (double)a.num_groups) * a.table_cols * a.page_size;
+  int64_t most = (int64_t)a.table_cols * a.page_size;  // common positions that a sequence may have
+  if (a.window > 0) most = std::min<int64_t>(most, a.window);
+  const double positions = (a.N - (double)a.num_groups) * most;
   if (a.dtype == KDA_DT_F32)
     return a.Hq / a.Hkv <= kSharedHeadsF32 && a.D <= 128 && positions * a.Hkv * a.D * 8 >= kSharedBytesF32;
   return a.vec16 && positions * a.Hkv * a.D * 4 >= kSharedBytes;

@@ -6,9 +6,10 @@ import pytest
 import torch
 
 from linear_attention_decode_02_gb300 import binding, build
+from oracle import cache_oracle as co
 from tests.rounding import to_np
 from tests.test_gpu_paged_attention import same
-from tests.test_gpu_prefix_attention import check, make, run
+from tests.test_gpu_prefix_attention import BF16, FP32, SHARED, check, expected, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +18,12 @@ pytestmark = pytest.mark.gpu
 def lib():
     build.build()
     return binding.library()
+
+
+def alone_of(c, window=0):
+    """The outputs of every sequence by its own row."""
+    return co.paged_attention(to_np(c["q"]), to_np(c["k"]), to_np(c["v"]), c["table"].cpu().numpy()[:, :64],
+                              c["lens"].cpu().numpy(), window=window)[0]
 
 
 @pytest.mark.parametrize("page", [64, 24])
@@ -84,3 +91,40 @@ def test_weights_are_held_to_two_pieces_rounded_to_nearest(D):
         allowed.append(square)
     ratio = np.sqrt(np.square(error).mean() / np.mean(allowed))
     assert ratio < 1.2, ratio
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_the_window_counts_in_what_sharing_could_save(dtype):
+    """Whether a call shares shows in a second sequence whose row lists another page than the first one's for a common
+    position, which breaks the contract and is read by those alone that are on their own."""
+    c = make([(64, [10] * 60)], Hq=8, Hkv=8, dtype=dtype)
+    c["table"][30, 1] = c["table"][0, 2]
+    width = c["table"].shape[1] * 16
+    bytes_each = 8 * 128 * 2 * dtype.itemsize
+    assert 59 * width * bytes_each >= SHARED[dtype] > 59 * 100 * bytes_each
+    shared, alone = expected(c)[0][30], alone_of(c)[30]
+    assert np.abs(shared - alone).max() > 0.1
+    for window, wanted in ((0, shared), (width, shared), (100, alone), (75, alone)):
+        out, _ = run(c, window=window)
+        torch.cuda.synchronize()
+        assert np.abs(to_np(out)[30] - wanted).max() < 0.02, window
+    few = -(-SHARED[dtype] // (59 * bytes_each))  # positions from which the rule shares
+    for window, wanted in ((few - 1, alone), (few, shared)):
+        out, _ = run(c, window=window)
+        torch.cuda.synchronize()
+        assert np.abs(to_np(out)[30] - wanted).max() < 0.02, window
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_windows_of_calls_that_share(dtype, D):
+    """Groups that begin with more than the window (none of their sequences takes part), groups of which some do, and
+    groups of which all do."""
+    window = 250
+    tails = [1, 2, 60, 61, 4, 5, 9]
+    groups = [(window + over, tails) for over in (-60, -5, -1, 0, 1, 5)]
+    groups = (groups + [(700, [3, 1]), (40, tails * 4), (window - 61, [61, 62, 1]), (1, [300, 249, 250])]) * 2
+    c = make(groups, Hq=16, Hkv=16, D=D, dtype=dtype)
+    n = len(c["lens"])
+    assert (n - len(groups)) * window * 16 * D * 2 * dtype.itemsize >= SHARED[dtype]
+    check(c, window=window)
