@@ -804,19 +804,25 @@ constexpr int64_t kSharedBytes = 96 << 20;
 constexpr int64_t kSharedBytesF32 = 256 << 20;
 constexpr int kSharedHeadsF32 = 4;
 
+// Whether any call of such heads shares.
+bool may_share(int32_t G, int32_t D, int32_t dtype) {
+  return dtype != KDA_DT_F32 || (G <= kSharedHeadsF32 && D <= 128);
+}
+
 bool shares(const AttendArgs& a) {
   int64_t most = (int64_t)a.table_cols * a.page_size;  // common positions that a sequence may have
   if (a.window > 0) most = std::min<int64_t>(most, a.window);
-  const double positions = (a.N - (double)a.num_groups) * most;
-  if (a.dtype == KDA_DT_F32)
-    return a.Hq / a.Hkv <= kSharedHeadsF32 && a.D <= 128 && positions * a.Hkv * a.D * 8 >= kSharedBytesF32;
-  return a.vec16 && positions * a.Hkv * a.D * 4 >= kSharedBytes;
+  const bool f32 = a.dtype == KDA_DT_F32;
+  const double saved = (a.N - (double)a.num_groups) * most * a.Hkv * a.D * (f32 ? 8 : 4);
+  return may_share(a.Hq / a.Hkv, a.D, a.dtype) && a.vec16 && saved >= (f32 ? kSharedBytesF32 : kSharedBytes);
 }
 
 }  // namespace
 
 int64_t prefix_floats(int64_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int32_t sms) {
-  return std::max(attend_floats(Hq, Hkv, D, dtype, sms), prefix_plan(nullptr, N, Hq, Hkv, D, dtype, sms, 0).floats);
+  const int64_t alone = attend_floats(Hq, Hkv, D, dtype, sms);
+  if (!may_share(Hq / Hkv, D, dtype)) return alone;
+  return std::max(alone, prefix_plan(nullptr, N, Hq, Hkv, D, dtype, sms, 0).floats);
 }
 
 cudaError_t launch_prefix_attention(const AttendArgs& given, int32_t sms, cudaStream_t s) {
