@@ -156,10 +156,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) kda_attend_tf32_kernel(c
   };
   const auto load_q = [&](const W& w) {
     const int rows = rows_of(w);
+    const float* const first = q_row(w, 0);
 #pragma unroll
     for (int i = 0; i < SHARE; ++i) {
       const int h = (i * THREADS + threadIdx.x) / (D / 4), chunk = (i * THREADS + threadIdx.x) % (D / 4);
-      q_next[i] = h < rows ? __ldg(reinterpret_cast<const float4*>(q_row(w, h)) + chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* const q = GROUPS ? q_row(w, h) : first + h * a.q_hs;
+      q_next[i] = h < rows ? __ldg(reinterpret_cast<const float4*>(q) + chunk) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   const auto place_q = [&]() {
