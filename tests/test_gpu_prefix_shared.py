@@ -26,6 +26,15 @@ def alone_of(c, window=0):
                               c["lens"].cpu().numpy(), window=window)[0]
 
 
+def assert_shares(c, window=0):
+    """The rule, as the header has it."""
+    n, (_, page, heads, D), size = len(c["lens"]), c["k"].shape, c["k"].element_size()
+    most = c["table"].shape[1] * page
+    most = min(most, window) if window > 0 else most
+    assert (n - len(c["prefix"])) * most * heads * D * 2 * size >= SHARED[c["k"].dtype]
+    assert c["k"].dtype == BF16 or (c["q"].shape[1] // heads <= 4 and D <= 128)
+
+
 @pytest.mark.parametrize("page", [64, 24])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_units_of_an_odd_number_of_tiles(D, page):
@@ -125,8 +134,7 @@ def test_windows_of_calls_that_share(dtype, D):
     groups = [(window + over, tails) for over in (-60, -5, -1, 0, 1, 5)]
     groups = (groups + [(700, [3, 1]), (40, tails * 4), (window - 61, [61, 62, 1]), (1, [300, 249, 250])]) * 2
     c = make(groups, Hq=16, Hkv=16, D=D, dtype=dtype)
-    n = len(c["lens"])
-    assert (n - len(groups)) * window * 16 * D * 2 * dtype.itemsize >= SHARED[dtype]
+    assert_shares(c, window)
     check(c, window=window)
 
 
@@ -141,3 +149,60 @@ def test_float32_heads_that_never_share_take_the_paged_workspace(Hq, Hkv, D):
     assert same(out, alone) and same(lse, sums) and torch.isnan(work[floats:]).all()
     with pytest.raises(binding.KdaError, match="workspace"):
         run(c, workspace=work[:floats - 1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("page,D", [(64, 128), (24, 128), (64, 64), (16, 256)])
+def test_caches_past_4_gib_and_2_to_31_elements(dtype, page, D):
+    """Keys and values of one pool, far and near: the same bits, and those of the definition.  Pages of whole boxes and
+    not, a prefix that ends inside a page, own positions behind it."""
+    if dtype == FP32 and D == 256:
+        pytest.skip("never shared")
+    row = 2 * page * 8 * D * dtype.itemsize  # bytes of a page
+    pages = (5 << 30) // row
+    pool = torch.zeros(pages, 2, page, 8, D, dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    pool[-500:] = torch.randn(500, 2, page, 8, D, device="cuda", generator=g).to(dtype)
+    lens, prefix = [20 * page + 30, 20 * page + 5, 25 * page - 1, 300], 19 * page + page // 2
+    width = SHARED[dtype] // (3 * row) + 40
+    table = torch.zeros(4, width, dtype=torch.int32)
+    table[:, :25] = pages - 1 - torch.arange(100, dtype=torch.int32).reshape(4, 25)
+    table[1:3, :19] = table[0, :19]
+    for n in (1, 2):  # the rest of the prefix, on pages of their own
+        pool[table[n, 19], :, :page // 2] = pool[table[0, 19], :, :page // 2].clone()
+    q = torch.randn(4, 16, D, device="cuda", generator=g).to(dtype)
+    c = dict(q=q, k=pool[:, 0], v=pool[:, 1], table=table.cuda(), **{
+        name: torch.tensor(x, dtype=torch.int32, device="cuda") for name, x in (("lens", lens), ("starts", [0, 3]), ("prefix", [prefix]))})
+    assert_shares(c)
+    assert pool.numel() > 2 ** 31 or dtype == FP32
+    near = dict(c, k=pool[-500:, 0].contiguous(), v=pool[-500:, 1].contiguous(), table=(c["table"] - (pages - 500)).clamp(min=0))
+    out, lse = run(c)
+    again, sums = run(near)
+    torch.cuda.synchronize()
+    assert same(out, again) and same(lse, sums) and torch.count_nonzero(out) > 0
+    del pool, c
+    check(near)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_lengths_and_prefixes_past_the_table_and_below_zero_where_calls_share(dtype, D):
+    c = make([(60, [4] * 70), (100, [1, 2])], Hq=8, Hkv=8, D=D, page=8, dtype=dtype)
+    assert_shares(c)
+    c["prefix"][:] = torch.tensor([-3, -2 ** 31], dtype=torch.int32)  # as none: all are on their own
+    check(c)
+    c["lens"][5:8] = torch.tensor([-1, 0, -2 ** 31], dtype=torch.int32)
+    check(c)
+    c["prefix"][:] = torch.tensor([60, 100], dtype=torch.int32)
+    check(c)
+    # past the table, all of which is real for two sequences
+    c = make([(60, [4] * 70)], Hq=8, Hkv=8, D=D, page=64, dtype=dtype)
+    width = c["table"].shape[1]
+    assert_shares(c)
+    for x in ("k", "v"):
+        c[x][c["table"][0, 0].long()].nan_to_num_(0.5, 0.25, -0.25)
+    c["table"][:2] = c["table"][0, 0].clone()
+    c["lens"][:2] = torch.tensor([2 ** 31 - 1, 64 * width + 3], dtype=torch.int32)
+    for prefix in (2 ** 31 - 1, 64 * width, 64 * width + 1):
+        c["prefix"][0] = prefix
+        check(c)
