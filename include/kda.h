@@ -428,7 +428,9 @@ kda_status kda_pool_move(const kda_tensor* const* pools, int32_t n_pools, const 
  * A sequence that needs no further page gets its new length; one that does gets it
  * where the pages that it and all sequences before it ask for are free, and else
  * keeps the old one, as does one whose new length the table cannot hold (which
- * counts as asking for none).  Pages are taken in order of sequences, the oldest
+ * counts as asking for none).  One that is not served still counts as asking, so a
+ * prompt that asks for more than there is keeps all sequences after it from new
+ * pages until the caller withdraws it.  Pages are taken in order of sequences, the oldest
  * free one first; those past a shorter length are given back behind the youngest,
  * in order of sequences and columns, and can be taken from the next call on.
  * Entries outside 1 .. C (pages that a window has left behind) are not given back.
@@ -469,8 +471,9 @@ kda_status kda_rope_pair_axes(const int32_t* sections, int32_t num_axes, int32_t
 /*
  * kda_prefix_attention_decode: kda_paged_attention_decode for groups of sequences
  * that begin alike (beams of one prompt, users of one system prompt): the common
- * positions are read once a group for all of its query heads, each sequence's own
- * positions once.  Launches three kernels.
+ * positions are read once for every 256 query rows of a key head in the group (128
+ * where groups have no more than that on average, and with 256 channels; in float32
+ * 16, or 8), each sequence's own positions once.  Launches three kernels.
  *
  *   q, k_pages, v_pages, page_table, seq_lens, window, scale, out, lse: as there.  A
  *               sequence's row of the table lists all its pages, common ones too.

@@ -71,8 +71,12 @@ struct SpecArgs {
 // stream serialization: the grid may begin (launch, CTA placement, on-chip
 // set-up) while the previous kernel on the stream drains; every kernel of this
 // library executes pdl_wait() before its first global-memory access, so
-// nothing the previous kernel writes is read early.  `cluster` > 1 adds a
-// thread-block cluster of that many CTAs along x.
+// nothing the previous kernel writes is read early.  The one exception are the
+// attention kernels of sequences' own positions, which wait at their end: the
+// kernel of common positions is always launched right before them, lets them
+// begin only behind its own pdl_wait(), writes nothing that they read, and
+// reads and writes nothing that they write.  `cluster` > 1 adds a thread-block
+// cluster of that many CTAs along x.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                               int cluster, Args&&... args) {

@@ -1,6 +1,6 @@
 // Attention of one new token per sequence where groups of sequences begin with
-// the same positions: the common part is read once a group, by the tensor cores,
-// with all the group's queries of a key head as rows; each sequence's own part is
+// the same positions: the common part is read once for up to 256 rows, the queries of a
+// key head in all the group's sequences, by the tensor cores; each sequence's own part is
 // left to the paged kernel; a last kernel joins both.
 //
 // For a row with maximum m, sum l and unnormalised output o over a part of its
@@ -51,18 +51,18 @@
 // before it waits for either half (given with the keys' slot, the values' barrier could
 // still be in the phase before the last one, which looks like the one waited for).
 //
-// What bounds it, at 32 / 8 heads of 128 (each of the three launches under a profiler,
-// in us):
-//   16 prompts of 8192 positions, four beams each (one row tile): 75, 392 MB at 65 % of DRAM's rate;
+// What bounds it, at 32 / 8 heads of 128 (the launch alone under a profiler, in us):
+//   16 prompts of 8192 positions, four beams each (one row tile): 77, 392 MB at 64 % of DRAM's rate;
 //     the steps of a lane wait for one another, and a ring of five halves holds little
-//   256 users of one system prompt of 32768 (two row tiles): 152, tensor pipe 54 %;
-//     softmax of 64 positions takes 1340 cycles of a warp, the three products of a step 660
+//   256 users of one system prompt of 32768 (two row tiles): 158, tensor pipe 55 %; a step of 64 positions
+//     takes both lanes 2300 cycles, 1536 of them the tensor pipe's for its products, 1250 its softmax
 // Tried: one warp that issues both lanes' products (246 -> 300 us a call), tiles of 64
 // positions (76 -> 104, 155 -> 171: twice the copies' bookkeeping, and values held
 // through two more tiles), scores first at a tile's end with one row tile (76 -> 88),
 // parts laid out in planes of 8 channels, so that a warp's stores join (152 -> 153, and
-// the join 16 -> 18).  Of a piece's 270000 cycles 25000 pass before its first weights
-// (lengths and groups 9000, table, keys and queries 14000), 10000 with its last output.
+// the join 16 -> 18).  Of a piece's 283000 cycles 26000 pass before its first weights
+// (lengths and groups 6000, table, keys and queries 16000), 12000 with its last output.
+// Compiled for 128 registers a thread, 80 bytes of one spill (with 256 channels, 150 registers, none).
 //
 // The kernel of own positions reads nothing that this one writes and writes elsewhere.
 // So it begins as this one's blocks leave, all of which have waited for what came

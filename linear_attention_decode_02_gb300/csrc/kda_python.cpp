@@ -192,8 +192,9 @@ kda_status without_gil(const F& f) {
 // thread on one stream follow one another, and no other call sees it.  A call
 // that is being captured gets its own from the graph's pool, so graphs share
 // theirs neither with each other nor with eager calls.  One of more than 16 MB
-// (attention's never is, beams' only over tens of thousands of rows, whose call
-// takes far longer than allocating it) goes back to the allocator with the call.
+// (the paged attention's never is, beams' only over tens of thousands of rows, that of
+// attention under shared prefixes mostly; such calls take far longer than allocating it)
+// goes back to the allocator with the call.
 constexpr Py_ssize_t kKept = 16;
 constexpr int64_t kKeptFloats = 4 << 20;
 PyObject* s_workspaces;

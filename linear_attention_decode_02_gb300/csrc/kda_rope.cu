@@ -21,10 +21,10 @@
 // With several axes a row has a position on each of them, and pair i turns by
 // its own axis' position; negative ones turn backwards, since the product modulo
 // 2^64 does.  The row's place is a slot that it is given, so two loads that do not
-// depend on each other take the place of the search and the table.  34,800 rows of 24
+// depend on each other take the place of the search and the table.  20,934 rows of 24
 // / 8 heads of 128 bf16 channels, half of them turned (0.43 GB), take 72 us, 88 % of
-// the copy bandwidth; 1900 rows of 32 / 8 heads 9.2 us where the bytes need 6.9, a
-// single wave of blocks; 16 rows 3.5 us.
+// the copy bandwidth; 1900 rows of 32 / 8 heads 9.2 us where the bytes need 6.9, 950
+// blocks on 912 places; 16 rows 3.5 us.
 #include <algorithm>
 
 #include "kda_cache.h"
@@ -259,8 +259,10 @@ cudaError_t launch_rope_rows(const RopeArgs& a, cudaStream_t s) {
                                       : kda_rope_append_kernel<In, Out, VEC, true, ROWS, false>)
                               : (axes ? kda_rope_append_kernel<In, Out, VEC, false, ROWS, true>
                                       : kda_rope_append_kernel<In, Out, VEC, false, ROWS, false>);
-  // Few rows: several blocks share each, down to one vector a thread, until every SM has its six, or nearest to it: 1900
-  // rows in fours, 475 blocks, take 9.2 us shared by two and 11.3 us by one.
+  // Few rows: several blocks share each, down to one vector a thread, until every SM has its six, or nearest to it.  At
+  // five head shapes and 64 to 6000 rows, us of kda_rope_append (the call with axes alike) up to six / nearest: 1900 rows of
+  // 32 / 8 heads of 128 13.4 / 11.9, 960 of 24 / 8 7.9 / 6.6, 2400 14.0 / 13.6; slower are 400 of 32 / 8 4.75 / 4.90, 1900 of 16 / 16
+  // of 64 in float32 12.3 / 12.6 and 2400 of 12 / 1 of 256 11.3 / 11.7; most are alike.
   const int64_t blocks = (a.R + (int64_t)ROWS - 1) / ROWS;
   const int pairs = a.interleaved ? a.rot / VEC : a.rot / (2 * VEC);
   const int64_t tasks = (int64_t)(a.Hq + a.Hkv) * (pairs + (a.D - a.rot) / VEC);
