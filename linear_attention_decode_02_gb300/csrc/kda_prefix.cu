@@ -131,6 +131,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+// mbar_sleep_wait behind a try that gave up, with another before the clock is read: 256 users 232.4 us without, 231.2 with it.
+__device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity) {
+  return mbar_sleep_try(bar, parity) || mbar_sleep_wait(bar, parity);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
   auto wait_or_abort = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_sleep_try(bar, parity))) return true;
     const bool stopped = s_abort;  // by another role
-    const bool ok = !stopped && mbar_sleep_wait(bar, parity);
+    const bool ok = !stopped && wait_longer(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     if (lane == 0 && !stopped) {
       atomicOr(&g_kda_prefix_error, 16u);
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
       if (walk.tile < stop) walk.next_unit(a);
     }
     release(&drained[me]);  // every product issued has completed before the columns are freed
-    mbar_sleep_wait(&drained[me], 0);
+    wait_longer(&drained[me], 0);
   } else if (warp >= P::LOADER0 && warp < P::LOADER0 + kLoaders / 32) {
     more_registers<LANES == 1 ? 0 : -112>();
     // ---------------- copies ----------------
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(PrefixShape<D, RT>::THREADS, 1)
     }
     // No copy lands when the CTA is gone; all have been waited for but where a role gave up.
     asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int h = max(0, half - SLOTS); h < half; ++h) mbar_sleep_wait(&full[h % SLOTS], (h / SLOTS) & 1);
+    for (int h = max(0, half - SLOTS); h < half; ++h) wait_longer(&full[h % SLOTS], (h / SLOTS) & 1);
   } else {
     more_registers<LANES == 1 ? 0 : -112>();
     // ---------------- queries of the units ----------------
