@@ -228,7 +228,8 @@ at::Tensor workspace(const Call& call, PyObject* given, int64_t floats) {
     Py_DECREF(key);
     throw Raised();
   }
-  at::Tensor t = call.empty({floats}, at::kFloat);
+  // Past the dispatcher: what a mode gives instead, a tensor without memory say, is not for other calls.
+  at::Tensor t = at::detail::empty_cuda({floats}, at::kFloat, call.device, std::nullopt);
   if (held == nullptr && PyDict_Size(kept) >= kKept) PyDict_Clear(kept);
   PyObject* wrapped = THPVariable_Wrap(t);
   const int bad = wrapped == nullptr ? -1 : PyDict_SetItem(kept, key, wrapped);

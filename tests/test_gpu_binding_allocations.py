@@ -2,6 +2,7 @@
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 from torch.utils._python_dispatch import TorchDispatchMode
 
 from linear_attention_decode_02_gb300 import binding, build
@@ -47,7 +48,8 @@ def attention(shared):
     q = torch.zeros(3, 4, 64, dtype=BF16, device="cuda")
     more = (i32(2), i32(1)) if shared else ()
     call = binding.kda_prefix_attention_decode if shared else binding.kda_paged_attention_decode
-    return lambda: call(q, *cache(), i32(3, 2), i32(3), *more, return_lse=True)
+    args = (q, *cache(), i32(3, 2), i32(3), *more)
+    return lambda: call(*args, return_lse=True)
 
 
 CALLS = {"rope": (lambda: rope(False), [(3, 4, 64)]), "rope axes": (lambda: rope(True), [(3, 4, 64)]),
@@ -99,4 +101,20 @@ def test_calls_under_inference_mode_and_deterministic_fills():
         got = call()
     finally:
         torch.use_deterministic_algorithms(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, wanted))
+
+
+@pytest.mark.parametrize("name", ["attention", "beams"])
+def test_a_workspace_is_not_kept_from_a_mode_that_gives_no_memory(name):
+    x, s = torch.randn(2, 4, 500, device="cuda"), torch.zeros(2, 4, device="cuda")
+    call = attention(False) if name == "attention" else lambda: binding.kda_beam_select(x, s, 3)
+    wanted = call()
+    stream = torch.cuda.Stream()  # without a workspace of its own yet
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        with FakeTensorMode():
+            with pytest.raises(Exception):
+                call()
+        got = call()
+    torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, wanted))
