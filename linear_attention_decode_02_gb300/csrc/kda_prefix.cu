@@ -788,9 +788,10 @@ cudaError_t launch_prefix_join(const AttendArgs& a, const PrefixPlan& p, int sms
 }
 
 // Bytes of keys and values from which sharing is worth its two launches more, by
-// what it could save at the table's width, or the window's (the host knows no lengths;
-// a sequence that shares is no longer than the window): below, every sequence is on its own.  Measured shared and alone, us (groups x sequences x common
-// positions, 64 own ones; the bytes that sharing saves):
+// what it could save at the table's width, or the window's (the host knows no lengths; a
+// sequence that shares is no longer than the window): below, every sequence is on its
+// own.  Measured shared and alone, us (groups x sequences x common positions, 64 own
+// ones; the bytes that sharing saves):
 //   32 / 8 heads of 128   1 x 2 x 1024 (4 MB) 16 and 10, 1 x 16 x 1024 (63 MB) 19 and 19, 16 x 4 x 256 (50 MB) 28 and 23,
 //                         4 x 16 x 256 (63 MB) 19 and 23, 1 x 16 x 4032 (248 MB) 29 and 42, 16 x 4 x 1024 (201 MB) 41 and 47
 //     windows: 4 x 2 x 1024 under 512 (17 MB) 28 and 11; 1 x 64 x 4096 + up to 300 under 8192 (all share) 44 and 141, under
